@@ -21,7 +21,7 @@ FP8W = 2
 
 STATUS = {0: "ok", -1: "invalid argument", -2: "shape", -3: "block size", -4: "dtype",
           -5: "workspace", -6: "cuda", -7: "unsupported"}
-DEV_BAD_PAGE, DEV_BAD_TOKEN, DEV_WAIT_TIMEOUT, DEV_BAD_LENGTH = 0x1, 0x2, 0x4, 0x8
+DEV_BAD_PAGE, DEV_BAD_TOKEN, DEV_WAIT_TIMEOUT, DEV_BAD_LENGTH, DEV_EMPTY_ROW = 0x1, 0x2, 0x4, 0x8, 0x10
 
 
 class DFlash2Error(RuntimeError):
@@ -155,6 +155,17 @@ def lib():
         L.dflash2_verify_sampled.argtypes = [I, I, I, P, P, P, P, P, P, P, P, P, P, P, P]
         L.dflash2_verify_accept_ex.restype = I
         L.dflash2_verify_accept_ex.argtypes = [I, I, P, P, P, P, P, P, P, P, P, P]
+        I64 = ctypes.c_int64
+        L.dflash2_sample.restype = I
+        L.dflash2_sample.argtypes = [I, I, I, P, I64] + [P] * 9
+        L.dflash2_target_probs.restype = I
+        L.dflash2_target_probs.argtypes = [I, I, I, I, P, I64] + [P] * 7
+        L.dflash2_verify_logits_workspace.restype = S
+        L.dflash2_verify_logits_workspace.argtypes = [I, I]
+        L.dflash2_verify_logits.restype = I
+        L.dflash2_verify_logits.argtypes = [I, I, I, I, P, P, P, I64] + [P] * 13 + [S, P]
+        L.dflash2_linear_w4.restype = I
+        L.dflash2_linear_w4.argtypes = [P, P, I, I, I, P, I64, I, P, I64, I, I, P]
         L.dflash2_launch_count.restype = ctypes.c_int64
         L.dflash2_set_stage_events.restype = None
         L.dflash2_set_stage_events.argtypes = [P]
@@ -314,6 +325,139 @@ def dflash2_verify_sampled(batch, block_size, vocab, path, n_draft, target_prob,
         batch, block_size, vocab, _ptr(path), _ptr(n_draft), _ptr(target_prob), _ptr(u_accept), _ptr(u_sample),
         _ptr(accept_len), _ptr(out_tok), _ptr(n_out), _ptr(next_anchor), _ptr(seq_len), _ptr(counters),
         _stream(stream)))
+
+
+# The operators below read their sizes from the tensors, so they check them:
+# a tensor of another type, shape or layout, or on another device than the
+# current one, is refused before the call.
+
+def _refuse(fn, status, why):
+    raise DFlash2Error(fn, status, why)
+
+
+def _here(t):
+    return t is not None and t.get_device() >= 0 and t.get_device() == torch.cuda.current_device()
+
+
+def _need(fn, name, t, dtype, shape, null=False):
+    """A contiguous tensor of this type and shape on the current device (or
+    None where the call allows it)."""
+    if t is None and null:
+        return
+    if not _here(t):
+        _refuse(fn, -1, f"{name} must be on the current device")
+    if t.dtype is not dtype:
+        _refuse(fn, -4, f"{name} must be {dtype}")
+    if t.shape != shape or not t.is_contiguous():
+        _refuse(fn, -2, f"{name} must be contiguous, of shape {tuple(shape)}")
+
+
+_LOGIT_TYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _rows_of(fn, name, t, dims):
+    """Type code and the distance of the rows of a [..., n] tensor whose rows
+    are evenly spaced."""
+    if not _here(t):
+        _refuse(fn, -1, f"{name} must be on the current device")
+    code = _LOGIT_TYPES.get(t.dtype)
+    if code is None:
+        _refuse(fn, -4, f"{name} must be float32 or bfloat16")
+    st, sz = t.stride(), t.shape
+    if len(sz) != dims or (sz[-1] > 1 and st[-1] != 1):
+        _refuse(fn, -2, f"{name} must have {dims} dimensions, the last one contiguous")
+    if dims == 2:
+        return code, st[0] if sz[0] > 1 else sz[1]
+    row = st[1] if sz[1] > 1 else (st[0] if sz[0] > 1 else sz[2])
+    if sz[0] > 1 and sz[1] > 1 and st[0] != sz[1] * row:
+        _refuse(fn, -2, f"the rows of {name} must be evenly spaced")
+    return code, row
+
+
+def _check_settings(fn, n, temperature, top_k, top_p, min_p):
+    _need(fn, "temperature", temperature, torch.float32, (n,), True)
+    _need(fn, "top_k", top_k, torch.int32, (n,), True)
+    _need(fn, "top_p", top_p, torch.float32, (n,), True)
+    _need(fn, "min_p", min_p, torch.float32, (n,), True)
+
+
+def dflash2_sample(logits, temperature, top_k, top_p, min_p, u, token, prob=None, workspace=None, stream=None):
+    """logits: [rows, vocab] float32 or bfloat16, rows evenly spaced; the
+    settings: [rows] tensors or None; u, token, prob: [rows]."""
+    fn = "dflash2_sample"
+    code, stride = _rows_of(fn, "logits", logits, 2)
+    n, vocab = logits.shape
+    _check_settings(fn, n, temperature, top_k, top_p, min_p)
+    _need(fn, "u", u, torch.float32, (n,))
+    _need(fn, "token", token, torch.int32, (n,))
+    _need(fn, "prob", prob, torch.float32, (n,), True)
+    return _check(fn, lib().dflash2_sample(
+        code, n, vocab, _ptr(logits), stride, _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(u),
+        _ptr(token), _ptr(prob), _ptr(workspace), _stream(stream)))
+
+
+def dflash2_target_probs(logits, temperature, top_k, top_p, min_p, prob, workspace=None, stream=None):
+    """logits: [batch, rows, vocab] float32 or bfloat16, rows evenly spaced;
+    the settings: [batch] tensors or None; prob: [batch, rows, vocab] float32."""
+    fn = "dflash2_target_probs"
+    code, stride = _rows_of(fn, "logits", logits, 3)
+    batch, rows, vocab = logits.shape
+    _check_settings(fn, batch, temperature, top_k, top_p, min_p)
+    _need(fn, "prob", prob, torch.float32, logits.shape)
+    return _check(fn, lib().dflash2_target_probs(
+        code, batch, rows, vocab, _ptr(logits), stride, _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
+        _ptr(prob), _ptr(workspace), _stream(stream)))
+
+
+def dflash2_verify_logits_workspace(batch, block_size):
+    return lib().dflash2_verify_logits_workspace(batch, block_size)
+
+
+def dflash2_verify_logits(path, n_draft, logits, temperature, top_k, top_p, min_p, u_accept, u_sample, accept_len,
+                          out_tok, n_out, next_anchor, workspace, seq_len=None, counters=None, stream=None):
+    """logits: [batch, block_size, vocab] float32 or bfloat16, rows evenly
+    spaced; path, u_accept: [batch, block_size - 1]; the settings: [batch]
+    tensors or None."""
+    fn = "dflash2_verify_logits"
+    code, stride = _rows_of(fn, "logits", logits, 3)
+    batch, B, vocab = logits.shape
+    i32 = torch.int32
+    _check_settings(fn, batch, temperature, top_k, top_p, min_p)
+    _need(fn, "path", path, i32, (batch, B - 1))
+    _need(fn, "n_draft", n_draft, i32, (batch,), True)
+    _need(fn, "u_accept", u_accept, torch.float32, (batch, B - 1))
+    _need(fn, "u_sample", u_sample, torch.float32, (batch,))
+    for name, t in (("accept_len", accept_len), ("n_out", n_out), ("next_anchor", next_anchor)):
+        _need(fn, name, t, i32, (batch,))
+    _need(fn, "out_tok", out_tok, i32, (batch, B))
+    _need(fn, "seq_len", seq_len, i32, (batch,), True)
+    _need(fn, "counters", counters, torch.int64, (4 + 2 * B - 1,), True)
+    if not _here(workspace):
+        _refuse(fn, -5, "workspace must be on the current device")
+    return _check(fn, lib().dflash2_verify_logits(
+        code, batch, B, vocab, _ptr(path), _ptr(n_draft), _ptr(logits), stride, _ptr(temperature), _ptr(top_k),
+        _ptr(top_p), _ptr(min_p), _ptr(u_accept), _ptr(u_sample), _ptr(accept_len), _ptr(out_tok), _ptr(n_out),
+        _ptr(next_anchor), _ptr(seq_len), _ptr(counters), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def dflash2_linear_w4(codes, scale, group, x, out, accumulate=False, stream=None):
+    """codes: [out_features, in_features / 2] uint8; scale: [out_features,
+    in_features / group] bfloat16; x: [rows, in_features] bfloat16, out:
+    [rows, out_features] float32 or bfloat16, both with evenly spaced rows."""
+    fn = "dflash2_linear_w4"
+    xcode, xs = _rows_of(fn, "x", x, 2)
+    code, os_ = _rows_of(fn, "out", out, 2)
+    if xcode != BF16:
+        _refuse(fn, -4, "x must be bfloat16")
+    n, k = x.shape
+    m = out.shape[1]
+    if group not in (32, 64, 128) or k % group or out.shape[0] != n:
+        _refuse(fn, -2, "group must be 32, 64 or 128 and divide in_features, x and out have as many rows")
+    _need(fn, "codes", codes, torch.uint8, (m, k // 2))
+    _need(fn, "scale", scale, torch.bfloat16, (m, k // group))
+    return _check(fn, lib().dflash2_linear_w4(
+        _ptr(codes), _ptr(scale), group, m, k, _ptr(x), xs, n, _ptr(out), os_, code, int(accumulate), _stream(stream)))
 
 
 def dflash2_verify_accept_ex(batch, block_size, path, n_draft, target, accept_len, out_tok, n_out, next_anchor,

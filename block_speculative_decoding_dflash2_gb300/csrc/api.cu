@@ -110,6 +110,9 @@ int check_config(const dflash2_config* c) {
 // Most lm_head rows (batch * drafts) a draft step takes.
 constexpr int kMaxTopkRows = 32 * 256;
 
+// Most rows of logits a sampling call takes.
+constexpr int64_t kMaxSamplingRows = 1 << 20;
+
 struct Layout {
   size_t status, cnt, cnta, thr, f, Y, P, Ya, Pa, h, u, u2, ua, u2a, q, kb, vb, attn, O, act, hn, logits, lv, li, selx,
       rope, ropea, dsta, total;
@@ -870,6 +873,130 @@ int dflash2_verify_sampled(int batch, int block_size, int vocab, const int32_t* 
     return DFLASH2_ERR_INVALID_ARG;
   return launch_verify_sampled(batch, block_size, vocab, path, n_draft, target_prob, u_accept, u_sample, accept_len,
                                out_tok, n_out, next_anchor, seq_len, counters, static_cast<cudaStream_t>(stream));
+}
+
+int dflash2_linear_w4(const uint8_t* codes, const void* scale, int group, int out_features, int in_features,
+                      const void* x, int64_t x_stride, int rows, void* out, int64_t out_stride, int out_dtype,
+                      int accumulate, void* stream) {
+  if (group != 32 && group != 64 && group != 128) return DFLASH2_ERR_SHAPE;
+  if (out_features <= 0 || in_features <= 0 || in_features % group || rows < 0) return DFLASH2_ERR_SHAPE;
+  if (out_dtype != DFLASH2_F32 && out_dtype != DFLASH2_BF16) return DFLASH2_ERR_DTYPE;
+  if (rows == 0) return DFLASH2_OK;
+  if (!codes || !scale || !x || !out) return DFLASH2_ERR_INVALID_ARG;
+  if (rows > 1 && (x_stride < in_features || x_stride % 8 || out_stride < out_features)) return DFLASH2_ERR_SHAPE;
+  const uintptr_t os = out_dtype == DFLASH2_F32 ? 4 : 2;
+  if ((uintptr_t)codes % 16 || (uintptr_t)x % 16 || (uintptr_t)scale % 16 || (uintptr_t)out % os)
+    return DFLASH2_ERR_INVALID_ARG;
+  Ctx ctx;
+  TRY(device_ctx(&ctx, stream, nullptr));
+  return launch_linear_w4({codes, scale, group, out_features, in_features, x, rows > 1 ? x_stride : in_features, rows,
+                           out, rows > 1 ? out_stride : out_features, out_dtype == DFLASH2_BF16, accumulate != 0},
+                          ctx);
+}
+
+static int check_sampling(int dtype, int batch, int rows, int vocab, const void* logits, int64_t stride) {
+  if (dtype != DFLASH2_F32 && dtype != DFLASH2_BF16) return DFLASH2_ERR_DTYPE;
+  if (batch <= 0 || rows <= 0 || (int64_t)batch * rows > kMaxSamplingRows) return DFLASH2_ERR_SHAPE;
+  if (vocab < 1 || vocab > DFLASH2_SAMPLING_MAX_VOCAB) return DFLASH2_ERR_SHAPE;
+  if ((int64_t)batch * rows > 1 && stride < vocab) return DFLASH2_ERR_SHAPE;
+  if (!logits || (uintptr_t)logits % (dtype == DFLASH2_F32 ? 4 : 2)) return DFLASH2_ERR_INVALID_ARG;
+  return DFLASH2_OK;
+}
+
+int dflash2_sample(int dtype, int rows, int vocab, const void* logits, int64_t stride, const float* temperature,
+                   const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* token,
+                   float* prob, void* workspace, void* stream) {
+  TRY(check_sampling(dtype, rows, 1, vocab, logits, stride));
+  if (!u || !token) return DFLASH2_ERR_INVALID_ARG;
+  Ctx ctx;
+  TRY(device_ctx(&ctx, stream, workspace));
+  SamplingArgs a = {};
+  a.kind = SAMPLING_TOKEN;
+  a.batch = rows;
+  a.rows = 1;
+  a.vocab = vocab;
+  a.bf16_logits = dtype == DFLASH2_BF16;
+  a.logits = logits;
+  a.stride = stride;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.status = ctx.status;
+  a.u = u;
+  a.token = token;
+  a.prob = prob;
+  return launch_sampling(a, ctx);
+}
+
+int dflash2_target_probs(int dtype, int batch, int rows, int vocab, const void* logits, int64_t stride,
+                         const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                         float* prob, void* workspace, void* stream) {
+  TRY(check_sampling(dtype, batch, rows, vocab, logits, stride));
+  if (!prob) return DFLASH2_ERR_INVALID_ARG;
+  Ctx ctx;
+  TRY(device_ctx(&ctx, stream, workspace));
+  SamplingArgs a = {};
+  a.kind = SAMPLING_PROBS;
+  a.batch = batch;
+  a.rows = rows;
+  a.vocab = vocab;
+  a.bf16_logits = dtype == DFLASH2_BF16;
+  a.logits = logits;
+  a.stride = stride;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.status = ctx.status;
+  a.prob = prob;
+  return launch_sampling(a, ctx);
+}
+
+size_t dflash2_verify_logits_workspace(int batch, int block_size) {
+  if (batch <= 0 || block_size < 2 || block_size > 32) return 0;
+  return 256 + al((size_t)batch * block_size * sizeof(int2));
+}
+
+int dflash2_verify_logits(int dtype, int batch, int block_size, int vocab, const int32_t* path,
+                          const int32_t* n_draft, const void* logits, int64_t stride, const float* temperature,
+                          const int32_t* top_k, const float* top_p, const float* min_p, const float* u_accept,
+                          const float* u_sample, int32_t* accept_len, int32_t* out_tok, int32_t* n_out,
+                          int32_t* next_anchor, int32_t* seq_len, int64_t* counters, void* workspace,
+                          size_t ws_bytes, void* stream) {
+  if (block_size < 2 || block_size > 32) return DFLASH2_ERR_BLOCK_SIZE;
+  TRY(check_sampling(dtype, batch, block_size, vocab, logits, stride));
+  if (!path || !u_accept || !u_sample || !accept_len || !out_tok || !n_out || !next_anchor)
+    return DFLASH2_ERR_INVALID_ARG;
+  if (!workspace || (uintptr_t)workspace % 16 || ws_bytes < dflash2_verify_logits_workspace(batch, block_size))
+    return DFLASH2_ERR_WORKSPACE;
+  Ctx ctx;
+  TRY(device_ctx(&ctx, stream, workspace));
+  SamplingArgs a = {};
+  a.kind = SAMPLING_VERIFY;
+  a.batch = batch;
+  a.rows = block_size;
+  a.vocab = vocab;
+  a.bf16_logits = dtype == DFLASH2_BF16;
+  a.logits = logits;
+  a.stride = stride;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.status = ctx.status;
+  a.u = u_sample;
+  a.path = path;
+  a.n_draft = n_draft;
+  a.u_accept = u_accept;
+  a.rowout = at<int2>(workspace, 256);
+  a.accept_len = accept_len;
+  a.out_tok = out_tok;
+  a.n_out = n_out;
+  a.next_anchor = next_anchor;
+  a.seq_len = seq_len;
+  a.counters = counters;
+  return launch_sampling(a, ctx);
 }
 
 int dflash2_read_device_status(void* workspace, size_t ws_bytes, void* stream) {

@@ -270,4 +270,42 @@ int launch_verify(int batch, int B, const int32_t* path, const int32_t* n_draft,
                   int32_t* accept_len, int32_t* out_tok, int32_t* n_out, int32_t* next_anchor, int32_t* seq_len,
                   int64_t* counters, cudaStream_t st);
 
+// product with 4-bit weights (linear_w4.cu)
+struct W4Op {
+  const void* codes;  // [M, K / 2] bytes, 16-byte aligned
+  const void* scale;  // [M, K / group] bf16
+  int group;          // 32, 64 or 128; K % group == 0
+  int M, K;
+  const void* x;  // [N, K] bf16, row stride ldx elements, rows 16-byte aligned
+  long long ldx;
+  int N;
+  void* out;  // [N, M] fp32 or bf16, row stride ldo elements
+  long long ldo;
+  bool out_bf16, accumulate;
+};
+int launch_linear_w4(const W4Op& g, const Ctx& c);
+
+// logits to tokens (sampling.cu)
+enum { SAMPLING_TOKEN = 0, SAMPLING_PROBS = 1, SAMPLING_VERIFY = 2 };
+struct SamplingArgs {
+  int kind, batch, rows, vocab;  // rows of logits per sequence; settings are per sequence
+  bool bf16_logits;
+  const void* logits;  // [batch * rows, vocab], row stride `stride` elements
+  long long stride;
+  const float* temperature;  // settings: nullable [batch]
+  const int32_t* top_k;
+  const float *top_p, *min_p;
+  unsigned* status;
+  const float* u;  // [batch] draws (tokens and verification)
+  int32_t* token;  // tokens: [batch]
+  float* prob;     // tokens: nullable [batch]; probs: [batch * rows, vocab]
+  // verification
+  const int32_t *path, *n_draft;
+  const float* u_accept;
+  int2* rowout;  // workspace [batch * rows]: (draft passes, token emitted if it does not)
+  int32_t *accept_len, *out_tok, *n_out, *next_anchor, *seq_len;
+  int64_t* counters;
+};
+int launch_sampling(const SamplingArgs& a, const Ctx& c);
+
 }  // namespace df2

@@ -68,6 +68,7 @@ extern "C" {
 #define DFLASH2_DEV_BAD_TOKEN       0x2  /* token id outside [0, vocab) */
 #define DFLASH2_DEV_WAIT_TIMEOUT    0x4  /* a bounded pipeline wait gave up */
 #define DFLASH2_DEV_BAD_LENGTH      0x8  /* a context length beyond the block table */
+#define DFLASH2_DEV_EMPTY_ROW      0x10  /* a row of logits with no token above -inf */
 
 /* ---------------------------------------------------------------- types */
 #define DFLASH2_F32   0  /* float32 weights, activations and cache */
@@ -453,6 +454,105 @@ int dflash2_verify_sampled(int batch, int block_size, int vocab, const int32_t *
                            const float *target_prob, const float *u_accept, const float *u_sample,
                            int32_t *accept_len, int32_t *out_tok, int32_t *n_out, int32_t *next_anchor,
                            int32_t *seq_len, int64_t *counters, void *stream);
+
+/*
+ * From a target's logits to tokens.  The three calls below share one
+ * definition of a truncated distribution.  For a row of logits z with a
+ * temperature T > 0 the mass of token v is e_v = exp((z_v - max z) / T); the
+ * tokens are ordered by logit descending, equal logits by smaller id, and
+ *   top_k > 0   keeps the first top_k of the order;
+ *   top_p < 1   of these the shortest prefix that holds at least top_p of
+ *               their mass (never less than one token);
+ *   min_p > 0   of these the tokens with e_v >= min_p (at most 1);
+ * p_v is e_v over the kept mass, 0 for the others.  T <= 0 (or NaN) keeps the
+ * first token alone: greedy.  Tokens whose logit is -inf or NaN have no mass
+ * and are never kept; a row without any other token gives no token (-1) and
+ * zeros, and records DFLASH2_DEV_EMPTY_ROW when a workspace is given.
+ * Logits of +inf share the whole mass.
+ *   dtype        DFLASH2_F32 or DFLASH2_BF16, the type of the logits
+ *   vocab        1 .. DFLASH2_SAMPLING_MAX_VOCAB
+ *   logits       rows of vocab values, the rows `stride` elements apart
+ *                (stride >= vocab); only aligned to their elements
+ *   temperature, top_k, top_p, min_p
+ *                nullable device arrays, one entry per sequence (null: 1, 0,
+ *                1 and 0: no truncation)
+ * Random numbers are inputs in [0, 1), so a call is deterministic.  A draw
+ * with number u takes the first token, in id order, whose cumulative kept
+ * mass exceeds u times the total.  Cuts and draws are decided on 64-bit whole
+ * masses in units of 2^-42 of the largest one, each good to about 2^-37.
+ */
+#define DFLASH2_SAMPLING_MAX_VOCAB 1048576
+
+/*
+ * One token per row (the first anchor after a prompt, plain decoding).
+ * The settings have one entry per row.
+ *   u          [rows] float, the draws
+ *   token      [rows] int32 out
+ *   prob       nullable [rows] float out, the drawn token's probability
+ *   workspace  nullable: its status word only (the call needs no scratch)
+ */
+int dflash2_sample(int dtype, int rows, int vocab, const void *logits, int64_t stride,
+                   const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                   const float *u, int32_t *token, float *prob, void *workspace, void *stream);
+
+/*
+ * The truncated, renormalised distribution of every row, as
+ * dflash2_verify_sampled takes it (rows = block_size).  Row i of sequence s
+ * is row s * rows + i of `logits`; the settings have one entry per sequence.
+ *   prob       [batch, rows, vocab] float out
+ *   workspace  nullable: its status word only (the call needs no scratch)
+ */
+int dflash2_target_probs(int dtype, int batch, int rows, int vocab, const void *logits, int64_t stride,
+                         const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                         float *prob, void *workspace, void *stream);
+
+/*
+ * Sampled verification straight from the target's logits: the result of
+ * dflash2_target_probs followed by dflash2_verify_sampled (up to the
+ * rounding of the probabilities to fp32), without the distribution in
+ * between.  A sequence with temperature <= 0 is verified greedily: draft i
+ * passes when it is row i's largest logit.  Rows past n_draft[s] are not
+ * read.  A row without any token passes no draft and emits token -1.
+ *   logits     [batch * block_size, vocab]: row s * block_size + i follows
+ *              [anchor, path_1..path_i] of sequence s
+ *   n_draft    nullable [batch]: drafts kept per sequence (B-1 when null)
+ *   u_accept   [batch, B-1] float, the acceptance draws
+ *   u_sample   [batch] float, the draw of the emitted token
+ * Outputs, seq_len and counters as dflash2_verify_accept_ex.  The workspace
+ * needs dflash2_verify_logits_workspace bytes (0 for bad sizes; host only),
+ * 16-byte aligned, and serves one call at a time.
+ */
+size_t dflash2_verify_logits_workspace(int batch, int block_size);
+int dflash2_verify_logits(int dtype, int batch, int block_size, int vocab, const int32_t *path,
+                          const int32_t *n_draft, const void *logits, int64_t stride, const float *temperature,
+                          const int32_t *top_k, const float *top_p, const float *min_p, const float *u_accept,
+                          const float *u_sample, int32_t *accept_len, int32_t *out_tok, int32_t *n_out,
+                          int32_t *next_anchor, int32_t *seq_len, int64_t *counters, void *workspace,
+                          size_t ws_bytes, void *stream);
+
+/*
+ * Product with 4-bit weights and group scales:
+ *   out[n][m] (= or +=) sum_g scale[m][g] * sum_{k in g} (code[m][k] - 8) * x[n][k]
+ * `group` consecutive inputs share a scale.  Sums are fp32; a bf16
+ * output is rounded once (with accumulate: after the addition).
+ *   codes        [out_features, in_features / 2] bytes: byte j of a row holds
+ *                input 2j in its low and 2j + 1 in its high nibble, each the
+ *                weight's whole number -8..7 plus 8
+ *   scale        [out_features, in_features / group] bfloat16
+ *   group        32, 64 or 128; in_features must be a multiple of it
+ *   x            [rows, in_features] bfloat16, rows x_stride elements apart
+ *                (a multiple of 8, at least in_features)
+ *   rows         >= 0 (0: nothing is done)
+ *   out          [rows, out_features] of out_dtype (DFLASH2_F32 or
+ *                DFLASH2_BF16), rows out_stride elements apart
+ *                (>= out_features); must not overlap the inputs
+ *   accumulate   0: store, else add to out
+ * codes, scale and x are 16-byte aligned.  The call needs no workspace and
+ * gives the same bits for the same inputs.
+ */
+int dflash2_linear_w4(const uint8_t *codes, const void *scale, int group, int out_features, int in_features,
+                      const void *x, int64_t x_stride, int rows, void *out, int64_t out_stride, int out_dtype,
+                      int accumulate, void *stream);
 
 /*
  * Instrumentation.  Number of kernel launches the library has issued since
