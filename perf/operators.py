@@ -257,7 +257,7 @@ def _own(s):
         lib.dflash2_linear_w4(s["codes"], s["scale"], s["group"], s["x"], s["out"])
         return s["out"]
     if s["op"] == "sample":
-        lib.dflash2_sample(s["logits"], *s["settings"], s["u"], s["token"], s["prob"])
+        lib.dflash2_sample(s["logits"][:, 0], *s["settings"], s["u"], s["token"], s["prob"])
         return {"token": s["token"], "prob": s["prob"]}
     if s["op"] == "target_probs":
         lib.dflash2_target_probs(s["logits"], *s["settings"], s["prob"])
