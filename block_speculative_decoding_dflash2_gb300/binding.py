@@ -336,7 +336,10 @@ def _refuse(fn, status, why):
 
 
 def _here(t):
-    return t is not None and t.get_device() >= 0 and t.get_device() == torch.cuda.current_device()
+    if t is None:
+        return False
+    d = t.get_device()
+    return d >= 0 and d == torch.cuda.current_device()
 
 
 def _need(fn, name, t, dtype, shape, null=False):

@@ -5,9 +5,23 @@
 // q are nibbles (byte j of a row holds elements 2j and 2j + 1), scale and x
 // bf16, sums fp32, y fp32 or bf16 (rounded once).
 //
-// One warp per weight row and up to NB activation rows; the lanes stride over
-// the row's 16-byte pieces (32 weights, which lie in one group since a group
-// is a multiple of 32), and a butterfly joins the 32 partial sums.
+// The weights are read once and decide the time while there are few
+// activation rows, so they go from global memory straight into the registers
+// of mma.sync.m16n8k16 as operand A: within a group the order of k is free as
+// long as A and B agree, so each lane loads contiguous nibbles of its two rows
+// (16, 8 or 4 bytes for groups of 128, 64 or 32: the four lanes of a row then
+// always hold the same group) and the activations are stored in shared memory
+// in the matching order, one 16-byte read per lane for two products.  A
+// nibble becomes a bf16 whole number in -8..7 by two integer steps and one
+// subtraction, so every product is exact; a group's fp32 sums are then scaled
+// and added to the row's, which keeps the scale out of bf16.
+//
+// A CTA of 8 warps owns 128 weight rows at a time (16 a warp).  With few row
+// blocks the inputs are split over a cluster of up to 8 CTAs, whose partial
+// sums are added in rank order through distributed shared memory.
+#include <algorithm>
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -15,62 +29,301 @@ namespace df2 {
 
 namespace {
 
-constexpr int W4_WARPS = 8, NB = 4;
+constexpr int WARPS = 8, RB = WARPS * 16;  // weight rows of a CTA's block
+constexpr int CK = 128;                    // inputs of a chunk
+constexpr int XS_MAX = 96 * 1024;          // activation bytes of a CTA (two CTAs share an SM)
 
-template <typename OutT>
-__global__ void __launch_bounds__(W4_WARPS * 32)
-    linear_w4_kernel(const uint8_t* __restrict__ codes, const bf16* __restrict__ scale, int lg_group, int M, int K,
-                     const bf16* __restrict__ x, long long ldx, int N, OutT* __restrict__ out, long long ldo,
-                     int accumulate) {
+struct Args {
+  const uint8_t* codes;
+  const bf16* scale;
+  int M, K, chunks, slice;  // chunks of 128 inputs in all, and at most per CTA of a cluster
+  int window;               // chunks whose activations are in shared memory at a time
+  int blocks;               // row blocks
+  int split;                // CTAs of a cluster
+  const bf16* x;
+  long long ldx;
+  int N;
+  void* out;
+  long long ldo;
+  int accumulate;
+};
+
+// Nibbles e and e + 4 of a word as bf16x2 (128 + q) - 136 = q - 8, exactly.
+__device__ __forceinline__ uint32_t nib2(uint32_t w, int e) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(r) : "r"(w >> (4 * e)));
+  const __nv_bfloat162 d =
+      __hsub2(*reinterpret_cast<__nv_bfloat162*>(&r), __float2bfloat162_rn(136.f));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 ldw128(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ldw64(const uint8_t* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
+// First input of word i (8 nibbles) of lane-in-row t within a chunk.
+template <int G>
+__device__ __forceinline__ int word_k(int i, int t) {
+  return G == 128 ? t * 32 + i * 8 : G == 64 ? (i >> 1) * 64 + t * 16 + (i & 1) * 8 : i * 32 + t * 8;
+}
+
+constexpr int U = 4;  // chunks of weights in flight per warp
+
+// One lane's share of a chunk: 32 nibbles of two rows.
+struct Chunk {
+  uint32_t w[2][4];
+};
+
+// The group scales of four chunks of two rows: lane t of a row's four holds
+// chunk t's (a request of 2-byte loads costs as much as one of 16-byte loads,
+// so four chunks share it; the products fetch them by shuffles).
+template <int G>
+struct Scales {
+  float s[2][CK / G];
+};
+template <int G>
+__device__ __forceinline__ void load_scales(Scales<G>& c, const bf16* const (&srow)[2], int chunk, int K, int t) {
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int i = 0; i < CK / G; ++i) {
+      const int k = (chunk + t) * CK + i * G;
+      c.s[r][i] = k < K ? __bfloat162float(srow[r][k / G]) : 0.f;
+    }
+}
+
+template <int G>
+__device__ __forceinline__ void load_chunk(Chunk& c, const uint8_t* const (&row)[2], int chunk, int K, int t) {
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const uint8_t* p = row[r] + (size_t)chunk * (CK / 2);
+    if constexpr (G == 128) {
+      const uint4 v = ldw128(p + t * 16);
+      c.w[r][0] = v.x, c.w[r][1] = v.y, c.w[r][2] = v.z, c.w[r][3] = v.w;
+    } else if constexpr (G == 64) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint2 v = make_uint2(0x88888888u, 0x88888888u);  // weight 0 past the row's end
+        if (chunk * CK + h * 64 < K) v = ldw64(p + h * 32 + t * 8);
+        c.w[r][2 * h] = v.x, c.w[r][2 * h + 1] = v.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        c.w[r][i] = chunk * CK + i * 32 < K ? __ldg(reinterpret_cast<const uint32_t*>(p + i * 16 + t * 4)) : 0x88888888u;
+    }
+  }
+}
+
+template <int G, int NT, typename OutT>
+__global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 2 : 1) linear_w4_kernel(Args a) {
+  extern __shared__ uint4 xs[];  // [window][4 words][NT][32 lanes], then the partial sums [NT * 8][RB]
+  float* part = reinterpret_cast<float*>(xs + (size_t)a.window * 4 * NT * 32);
   pdl_launch_next();
   pdl_wait();
-  const int m = blockIdx.x * W4_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int n0 = blockIdx.y * NB;
-  if (m >= M) return;
-  const uint4* row = reinterpret_cast<const uint4*>(codes + (size_t)m * (K / 2));
-  const bf16* srow = scale + (size_t)m * (K >> lg_group);
-  float acc[NB];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int rank = blockIdx.x % a.split, n0 = blockIdx.y * (NT * 8);
+  const int c_begin = min(a.chunks, rank * a.slice), c_end = min(a.chunks, c_begin + a.slice);
+  const bool once = c_end - c_begin <= a.window;  // the activations stay for every row block
+
+  // activations of chunks [c0, c1) in the order of the products
+  auto stage = [&](int c0, int c1) {
+    for (int i = threadIdx.x; i < (c1 - c0) * (NT * 8) * 16; i += WARPS * 32) {
+      const int kb = i & 15, n = (i >> 4) % (NT * 8), c = (i >> 4) / (NT * 8);
+      const int word = kb >> 2, tt = kb & 3;
+      const int k = (c0 + c) * CK + word_k<G>(word, tt);
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (n0 + n < a.N && k < a.K) v = __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)(n0 + n) * a.ldx + k));
+      const uint4 o = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                                 __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+      xs[((c * 4 + word) * NT + (n >> 3)) * 32 + (n & 7) * 4 + tt] = o;
+    }
+  };
+  if (once) {
+    stage(c_begin, c_end);
+    __syncthreads();
+  }
+  for (int blk = blockIdx.x / a.split; blk < a.blocks; blk += gridDim.x / a.split) {
+    const int m0 = blk * RB + warp * 16 + g;
+    const uint8_t* row[2];
+    const bf16* srow[2];
 #pragma unroll
-  for (int j = 0; j < NB; ++j) acc[j] = 0.f;
-  for (int p = lane; p < K / 32; p += 32) {
-    const uint4 q4 = __ldg(row + p);
-    const uint32_t w[4] = {q4.x, q4.y, q4.z, q4.w};
-    const float s = __bfloat162float(srow[(p * 32) >> lg_group]);
+    for (int r = 0; r < 2; ++r) {  // rows past the end read the last one and are not stored
+      const size_t m = min(m0 + 8 * r, a.M - 1);
+      row[r] = a.codes + m * (a.K / 2);
+      srow[r] = a.scale + m * (a.K / G);
+    }
+    float acc[NT][4];
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      if (n0 + j >= N) break;
-      const bf16* xr = x + (size_t)(n0 + j) * ldx + p * 32;
-      float t = 0.f;
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        t = fmaf((float)((int)((w[i >> 3] >> (4 * (i & 7))) & 15u) - 8), __bfloat162float(xr[i]), t);
-      acc[j] = fmaf(s, t, acc[j]);
+      for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+
+    for (int w0 = c_begin; w0 < c_end; w0 += a.window) {
+      const int w1 = min(c_end, w0 + a.window);
+      if (!once) {
+        __syncthreads();
+        stage(w0, w1);
+        __syncthreads();
+      }
+      Chunk buf[U];
+      Scales<G> sc, sn;
+      load_scales<G>(sn, srow, w0, a.K, t);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (w0 + u < w1) load_chunk<G>(buf[u], row, w0 + u, a.K, t);
+      for (int c0 = w0; c0 < w1; c0 += U) {
+        sc = sn;
+        if (c0 + U < w1) load_scales<G>(sn, srow, c0 + U, a.K, t);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int c = c0 + u;
+          if (c >= w1) break;
+          float p[NT][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i % (G / 32) == 0) {
+#pragma unroll
+              for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p[j][e] = 0.f;
+            }
+            const uint32_t wl = buf[u].w[0][i], wh = buf[u].w[1][i];
+            const uint32_t a0 = nib2(wl, 0), a1 = nib2(wh, 0), a2 = nib2(wl, 1), a3 = nib2(wh, 1);
+            const uint32_t b0 = nib2(wl, 2), b1 = nib2(wh, 2), b2 = nib2(wl, 3), b3 = nib2(wh, 3);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              const uint4 xv = xs[(((c - w0) * 4 + i) * NT + j) * 32 + lane];
+              mma16816(p[j], a0, a1, a2, a3, xv.x, xv.y);
+              mma16816(p[j], b0, b1, b2, b3, xv.z, xv.w);
+            }
+            if (i % (G / 32) == G / 32 - 1) {
+              const float s0 = __shfl_sync(0xffffffffu, sc.s[0][i / (G / 32)], u, 4);
+              const float s1 = __shfl_sync(0xffffffffu, sc.s[1][i / (G / 32)], u, 4);
+#pragma unroll
+              for (int j = 0; j < NT; ++j) {
+                acc[j][0] = fmaf(s0, p[j][0], acc[j][0]);
+                acc[j][1] = fmaf(s0, p[j][1], acc[j][1]);
+                acc[j][2] = fmaf(s1, p[j][2], acc[j][2]);
+                acc[j][3] = fmaf(s1, p[j][3], acc[j][3]);
+              }
+            }
+          }
+          if (c + U < w1) load_chunk<G>(buf[u], row, c + U, a.K, t);
+        }
+      }
+    }
+    auto put = [&](int n, int m, float v) {
+      if (n < a.N && m < a.M) {
+        OutT* o = static_cast<OutT*>(a.out) + (size_t)n * a.ldo + m;
+        st(o, a.accumulate ? ld(o) + v : v);
+      }
+    };
+    if (a.split == 1) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) put(n0 + j * 8 + 2 * t + (e & 1), m0 + 8 * (e >> 1), acc[j][e]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) part[(j * 8 + 2 * t + (e & 1)) * RB + warp * 16 + g + 8 * (e >> 1)] = acc[j][e];
+      cluster_sync();
+      // CTA `rank` adds a share of the block's sums, in rank order
+      for (int i = rank * (WARPS * 32) + threadIdx.x; i < NT * 8 * RB / 4; i += a.split * WARPS * 32) {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r = 0; r < a.split; ++r) {
+          const float4 v = ld_dsmem4(dsmem_addr(part + i * 4, r));
+          s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+        const int n = n0 + i * 4 / RB, m = blk * RB + i * 4 % RB;
+        put(n, m, s.x), put(n, m + 1, s.y), put(n, m + 2, s.z), put(n, m + 3, s.w);
+      }
+      cluster_sync();  // every partial sum has been read
     }
   }
-#pragma unroll
-  for (int j = 0; j < NB; ++j) {
-    const float v = warp_sum(acc[j]);
-    if (lane == 0 && n0 + j < N) {
-      OutT* o = out + (size_t)(n0 + j) * ldo + m;
-      st(o, accumulate ? ld(o) + v : v);
-    }
+}
+
+template <int G, int NT, typename OutT>
+int launch(Args a, const Ctx& c) {
+  const int nb = (a.N + NT * 8 - 1) / (NT * 8);
+  a.blocks = (a.M + RB - 1) / RB;
+  // split the inputs until two CTAs an SM have work and the activations fit
+  const int per_chunk = NT * 8 * CK * 2, fit = XS_MAX / per_chunk;
+  a.split = 1;
+  while (a.split < 8 && a.chunks >= 2 * a.split * 2 &&
+         ((long long)a.blocks * nb * a.split < 2 * c.nsm || (a.chunks + a.split - 1) / a.split > fit))
+    a.split *= 2;
+  a.slice = (a.chunks + a.split - 1) / a.split;
+  a.window = std::min(a.slice, fit);
+  const size_t smem = (size_t)a.window * per_chunk + (size_t)NT * 8 * RB * 4;
+  int clusters = std::max(1, (NT <= 2 ? 2 : 1) * c.nsm / a.split);
+  clusters = std::min(clusters, a.blocks);
+  auto kern = linear_w4_kernel<G, NT, OutT>;
+  static std::atomic<unsigned long long> opted{0};  // devices whose kernel may use the largest size
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DFLASH2_ERR_CUDA;
+  if (!(opted.load(std::memory_order_relaxed) >> dev & 1)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, XS_MAX + NT * 8 * RB * 4) != cudaSuccess)
+      return DFLASH2_ERR_CUDA;
+    opted.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
+  return launch_kx(kern, dim3(clusters * a.split, nb), dim3(WARPS * 32), smem, c, a.split, a);
+}
+
+template <int G, typename OutT>
+int launch_n(const Args& a, const Ctx& c) {
+  if (a.N <= 8) return launch<G, 1, OutT>(a, c);
+  if (a.N <= 16) return launch<G, 2, OutT>(a, c);
+  if (a.N <= 32) return launch<G, 4, OutT>(a, c);
+  return launch<G, 8, OutT>(a, c);
+}
+
+template <typename OutT>
+int launch_g(int group, const Args& a, const Ctx& c) {
+  return group == 32 ? launch_n<32, OutT>(a, c) : group == 64 ? launch_n<64, OutT>(a, c) : launch_n<128, OutT>(a, c);
 }
 
 }  // namespace
 
 int launch_linear_w4(const W4Op& g, const Ctx& c) {
-  int lg = 0;
-  while ((1 << lg) < g.group) ++lg;
-  const dim3 grid((g.M + W4_WARPS - 1) / W4_WARPS, (g.N + NB - 1) / NB);
-  const uint8_t* codes = static_cast<const uint8_t*>(g.codes);
-  const bf16* scale = static_cast<const bf16*>(g.scale);
-  const bf16* x = static_cast<const bf16*>(g.x);
-  if (g.out_bf16)
-    return launch_k(linear_w4_kernel<bf16>, grid, dim3(W4_WARPS * 32), 0, c, codes, scale, lg, g.M, g.K, x, g.ldx, g.N,
-                    static_cast<bf16*>(g.out), g.ldo, (int)g.accumulate);
-  return launch_k(linear_w4_kernel<float>, grid, dim3(W4_WARPS * 32), 0, c, codes, scale, lg, g.M, g.K, x, g.ldx, g.N,
-                  static_cast<float*>(g.out), g.ldo, (int)g.accumulate);
+  const int most = 64 * 65535;  // rows of a launch (grid y)
+  for (int n = 0; n < g.N; n += most) {
+    Args a = {};
+    a.codes = static_cast<const uint8_t*>(g.codes);
+    a.scale = static_cast<const bf16*>(g.scale);
+    a.M = g.M;
+    a.K = g.K;
+    a.chunks = (g.K + CK - 1) / CK;
+    a.x = static_cast<const bf16*>(g.x) + (size_t)n * g.ldx;
+    a.ldx = g.ldx;
+    a.N = std::min(most, g.N - n);
+    a.out = static_cast<char*>(g.out) + (size_t)n * g.ldo * (g.out_bf16 ? 2 : 4);
+    a.ldo = g.ldo;
+    a.accumulate = g.accumulate;
+    const int rc = g.out_bf16 ? launch_g<bf16>(g.group, a, c) : launch_g<float>(g.group, a, c);
+    if (rc != DFLASH2_OK) return rc;
+  }
+  return DFLASH2_OK;
 }
 
 }  // namespace df2
