@@ -19,6 +19,8 @@
 // deterministic and sit within 2^-37 of the exact ones; in plain fp32 a cut
 // or a draw next to a border falls on the wrong side about once in a
 // thousand rows of a 150k vocabulary.
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -29,6 +31,10 @@ namespace {
 typedef unsigned long long u64;
 
 constexpr int NT = 512, NW = NT / 32;
+constexpr int NB = 1024;    // bins of a row's histogram
+constexpr int CAP = 2048;   // tokens of a sorted list
+constexpr int CMAX = 8;     // CTAs of a row's cluster
+constexpr int SLICE2 = 20480, SLICE1 = 50000;  // logits a CTA holds, two CTAs and one CTA an SM
 constexpr unsigned KEY_NINF = 0x007fffffu;  // order of -inf; NaN maps to 0
 
 // Order-preserving map of a logit (a larger one has a larger key; -0 equals 0).
@@ -131,24 +137,23 @@ __device__ __forceinline__ u64 warp_sum_u64(u64 v) {
   return v;
 }
 
-struct Smem {
-  unsigned cnt[256];
-  u64 mass[256];
-  u64 wsum[NW];
-  float wmax[NW];
-  unsigned sel_key;
-  u64 sel_before;
-  int pick;
-};
+// ------------------------------------------------------------------ clusters
 
-__device__ __forceinline__ u64 block_sum_u64(u64 v, Smem& sm) {
-  v = warp_sum_u64(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sm.wsum[threadIdx.x >> 5] = v;
-  __syncthreads();
-  u64 t = 0;
-  for (int i = 0; i < NW; ++i) t += sm.wsum[i];
-  return t;
+__device__ __forceinline__ void st_cl(uint32_t addr, unsigned v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_cl(uint32_t addr, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ unsigned ld_cl(uint32_t addr) {
+  unsigned v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ unsigned add_cl(uint32_t addr, unsigned v) {
+  unsigned o;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(o) : "r"(addr), "r"(v) : "memory");
+  return o;
 }
 
 // The kept prefix of a row's order: every token with (key, id) ahead of or
@@ -161,28 +166,158 @@ __device__ __forceinline__ bool kept(unsigned k, int id, const Cut& c) {
   return k > c.key || (k == c.key && id <= c.id);
 }
 
-// One step of a row's selection: among the tokens kept by `c`, the first one
-// of the order whose running sum of weights (1 each when by_count, else the
-// masses) reaches `target` (>= 1, at most the total).  Radix selection on the
-// key, 8 bits a level, then on the ids of equal keys.
+// What the cluster's first CTA decides for the others.
+enum { STEP_NONE = 0, STEP_LIST = 1, STEP_TOPK = 2, STEP_TOPP = 3, STEP_SLOW_K = 4, STEP_SLOW_P = 5 };
+struct Decision {
+  int step;
+  int lo, hi;       // bins to gather
+  unsigned before;  // tokens in bins ahead of lo
+  Cut cut;
+  unsigned total_lo, total_hi;  // mass of the cut, when known
+};
+constexpr int DW = sizeof(Decision) / 4;
+
+struct Smem {
+  u64 cand[CAP];  // first CTA: gathered tokens, (key, ~id)
+  unsigned hist[NB];
+  u64 radix[256];
+  u64 wsum[NW];
+  u64 xm[2][CMAX], xg[2][CMAX];  // exchanged masses, two turns
+  float xmax[CMAX], xmin[CMAX];
+  int xid[CMAX];
+  float fsum[NW];
+  Decision mk;      // first CTA: the next decision
+  Decision dec[2];  // the last one received, two turns
+  unsigned ncand;
+  unsigned sel_key;
+  u64 sel_before;
+  int pick, pick2;
+};
+
+__device__ __forceinline__ u64 block_sum_u64(u64 v, Smem& sm) {
+  v = warp_sum_u64(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sm.wsum[threadIdx.x >> 5] = v;
+  __syncthreads();
+  u64 t = 0;
+#pragma unroll
+  for (int i = 0; i < NW; ++i) t += sm.wsum[i];
+  return t;
+}
+
+// Sum over the threads before this one (and the block's total).
+__device__ __forceinline__ u64 block_scan_u64(u64 mine, u64* total, Smem& sm) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  u64 inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  __syncthreads();
+  if (lane == 31) sm.wsum[warp] = inc;
+  __syncthreads();
+  u64 before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < NW; ++i) {
+    if (i < warp) before += sm.wsum[i];
+    all += sm.wsum[i];
+  }
+  *total = all;
+  return before + inc - mine;
+}
+
+// Descending sort of the first n entries of `a` (n <= CAP, padded with zeros
+// to a power of two; every entry is above zero).
+__device__ void sort_desc(u64* a, int n) {
+  int p = 32;
+  while (p < n) p <<= 1;
+  for (int i = n + threadIdx.x; i < p; i += NT) a[i] = 0;
+  __syncthreads();
+  for (int k = 2; k <= p; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      for (int q = threadIdx.x; q < p / 2; q += NT) {
+        const int i = ((q & ~(j - 1)) << 1) | (q & (j - 1));
+        const u64 x = a[i], y = a[i + j];
+        if ((x < y) == ((i & k) == 0)) a[i] = y, a[i + j] = x;
+      }
+      __syncthreads();
+    }
+}
+
+// One CTA's slice of a row: ids [begin, begin + n).  Element i of the slice's
+// storage is id first + i; storage is cut in groups of four that lie on
+// 16-byte boundaries of the row for fp32 (8 bytes for bf16), and what it holds
+// outside the slice reads as -inf.
+template <typename T, bool RES>
+struct Slice {
+  const T* row;
+  float* zs;
+  int begin, end, first, groups;
+  __device__ __forceinline__ float4 get4(int i) const {
+    if constexpr (RES) return *reinterpret_cast<const float4*>(zs + 4 * i);
+    float4 v;
+    float* e = &v.x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int id = first + 4 * i + j;
+      e[j] = id >= begin && id < end ? ld(row + id) : -INFINITY;
+    }
+    return v;
+  }
+};
+
 template <typename T>
-__device__ Cut select_prefix(const T* row, int V, const Scale& s, Cut c, bool by_count, u64 target, Smem& sm) {
+__device__ __forceinline__ void unpack16(const uint4& v, float (&e)[16 / sizeof(T)]);
+template <>
+__device__ __forceinline__ void unpack16<float>(const uint4& v, float (&e)[4]) {
+  e[0] = __uint_as_float(v.x), e[1] = __uint_as_float(v.y), e[2] = __uint_as_float(v.z), e[3] = __uint_as_float(v.w);
+}
+template <>
+__device__ __forceinline__ void unpack16<bf16>(const uint4& v, float (&e)[8]) {
+  const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    e[2 * i] = __uint_as_float(w[i] << 16);
+    e[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// Calls f(z, id) on every element of the slice, each lane its own; every
+// thread makes the same number of calls (elements outside read as -inf).
+template <typename S, typename F>
+__device__ __forceinline__ void for_each(const S& s, F f) {
+  for (int i0 = 0; i0 < s.groups; i0 += NT) {
+    const int i = i0 + threadIdx.x;
+    const float4 v = i < s.groups ? s.get4(i) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    const int id = s.first + 4 * i;
+    f(v.x, id), f(v.y, id + 1), f(v.z, id + 2), f(v.w, id + 3);
+  }
+}
+
+// The first token of the order, among those kept by `c`, at which the running
+// sum of weights (1 each when by_count, else the masses) reaches `target`
+// (>= 1, at most the total): radix selection on the key, 8 bits a level, then
+// on the ids of equal keys.  By one CTA on the whole row: the way out for
+// rows with more equal or nearly equal tokens than a list holds.
+template <typename T>
+__device__ Cut select_slow(const T* row, int V, const Scale& s, Cut c, bool by_count, u64 target, Smem& sm) {
   unsigned prefix = 0, mask = 0;
   u64 before = 0;  // weight ahead of the keys that match the prefix
   for (int level = 3; level >= 0; --level) {
-    for (int i = threadIdx.x; i < 256; i += NT) sm.mass[i] = 0;
+    for (int i = threadIdx.x; i < 256; i += NT) sm.radix[i] = 0;
     __syncthreads();
     for (int v = threadIdx.x; v < V; v += NT) {
       const float z = ld(row + v);
       const unsigned k = okey(z);
       if ((k & mask) == prefix && kept(k, v, c))
-        atomicAdd(&sm.mass[(k >> (8 * level)) & 255u], by_count ? 1ull : mass_of(z, s));
+        atomicAdd(&sm.radix[(k >> (8 * level)) & 255u], by_count ? 1ull : mass_of(z, s));
     }
     __syncthreads();
     if (threadIdx.x == 0) {
       u64 b = before;
       int d = 255;
-      while (d > 0 && b + sm.mass[d] < target) b += sm.mass[d--];
+      while (d > 0 && b + sm.radix[d] < target) b += sm.radix[d--];
       sm.sel_key = prefix | ((unsigned)d << (8 * level));
       sm.sel_before = b;
     }
@@ -193,30 +328,17 @@ __device__ Cut select_prefix(const T* row, int V, const Scale& s, Cut c, bool by
     __syncthreads();
   }
   // equal keys: the need-th of them in id order (each has the same weight)
-  const float zs = okey_value(prefix);
-  const u64 w = by_count ? 1ull : mass_of(zs, s);
-  u64 need = w ? (target - before + w - 1) / w : 1;
-  if (need == 0) need = 1;
+  const u64 w = by_count ? 1ull : mass_of(okey_value(prefix), s);
+  const u64 need = w ? max(1ull, (target - before + w - 1) / w) : 1ull;
   const int per = (V + NT - 1) / NT;
   const int a = min(V, (int)threadIdx.x * per), b = min(V, a + per);
-  unsigned mine = 0;
+  u64 mine = 0, all;
   for (int v = a; v < b; ++v) {
     const unsigned k = okey(ld(row + v));
     mine += k == prefix && kept(k, v, c);
   }
-  unsigned inc = mine;
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned y = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += y;
-  }
-  __syncthreads();
-  if (lane == 31) sm.wsum[threadIdx.x >> 5] = inc;
   if (threadIdx.x == 0) sm.pick = c.key == prefix ? c.id : V - 1;
-  __syncthreads();
-  u64 ahead = inc - mine;
-  for (int i = 0; i < (int)(threadIdx.x >> 5); ++i) ahead += sm.wsum[i];
+  const u64 ahead = block_scan_u64(mine, &all, sm);
   if (ahead < need && ahead + mine >= need) {
     u64 left = need - ahead;
     for (int v = a; v < b; ++v) {
@@ -225,169 +347,600 @@ __device__ Cut select_prefix(const T* row, int V, const Scale& s, Cut c, bool by
     }
   }
   __syncthreads();
-  Cut out;
-  out.key = prefix;
-  out.id = sm.pick;
+  const Cut out = {prefix, sm.pick};
   __syncthreads();
   return out;
 }
 
-struct Row {
-  Scale s;
-  Cut cut;
-  u64 total;  // kept mass; 0: no token has any
-  bool greedy;
-};
-
-// Everything the outputs need of one row.
-template <typename T>
-__device__ Row row_cut(const T* row, int V, float temp, int top_k, float top_p, float min_p, Smem& sm) {
-  float mx = -INFINITY;
-  for (int v = threadIdx.x; v < V; v += NT) {
-    const float z = ld(row + v);
-    mx = z > mx ? z : mx;
-  }
-  mx = warp_max(mx);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sm.wmax[threadIdx.x >> 5] = mx;
-  __syncthreads();
-  for (int i = 0; i < NW; ++i) mx = fmaxf(mx, sm.wmax[i]);
-  Row r;
-  r.greedy = !(temp > 0.f);
-  r.s = make_scale(mx, r.greedy ? 1.f : temp);
-  r.cut.key = KEY_NINF + 1;  // everything above -inf
-  r.cut.id = V;
-  r.total = 0;
-  if (!(mx > -INFINITY)) return r;
-  if (r.greedy) top_k = 1;
-  if (top_k > 0 && top_k < V) {
-    u64 n = 0;
-    for (int v = threadIdx.x; v < V; v += NT) n += okey(ld(row + v)) > KEY_NINF;
-    n = block_sum_u64(n, sm);
-    if ((u64)top_k < n) r.cut = select_prefix(row, V, r.s, r.cut, true, (u64)top_k, sm);
-  }
-  auto sum = [&]() {
-    u64 t = 0;
-    for (int v = threadIdx.x; v < V; v += NT) {
-      const float z = ld(row + v);
-      const unsigned k = okey(z);
-      if (kept(k, v, r.cut)) t += mass_of(z, r.s);
-    }
-    return block_sum_u64(t, sm);
-  };
-  r.total = sum();
-  if (r.greedy) return r;
-  if (top_p < 1.f) {
-    const double want = (double)top_p * (double)r.total;
-    u64 target = want > 0.0 ? (u64)ceil(want) : 1ull;
-    if (target < 1) target = 1;
-    if (target > r.total) target = r.total;
-    r.cut = select_prefix(row, V, r.s, r.cut, false, target, sm);
-    r.total = sum();
-  }
-  if (min_p > 0.f) {
-    // z >= max z + T ln(min_p), as the smallest float that satisfies it
-    const double zt = (double)mx + (double)temp * log((double)min_p);
-    float zf = (float)zt;
-    if ((double)zf < zt) zf = nextafterf(zf, INFINITY);
-    zf = fminf(zf, mx);
-    const unsigned k = okey(zf);
-    if (k > r.cut.key) {
-      r.cut.key = k;
-      r.cut.id = V;
-      r.total = sum();
-    }
-  }
-  return r;
+// The smallest number of mass units that holds `p` of `total`.
+__device__ __forceinline__ u64 share_of(float p, u64 total) {
+  const double want = (double)p * (double)total;
+  const u64 t = want > 0.0 ? (u64)ceil(want) : 1ull;
+  return min(max(t, 1ull), total);
 }
 
-// First token in id order whose cumulative kept mass exceeds u times the
-// total, without token x.  -1 when no mass is left.
-template <typename T>
-__device__ int row_draw(const T* row, int V, const Row& r, int x, float u, Smem& sm) {
-  const int per = (V + NT - 1) / NT;
-  const int a = min(V, (int)threadIdx.x * per), b = min(V, a + per);
-  auto w = [&](int v) {
-    const float z = ld(row + v);
-    return v != x && kept(okey(z), v, r.cut) ? mass_of(z, r.s) : 0ull;
-  };
-  u64 mine = 0;
-  for (int v = a; v < b; ++v) mine += w(v);
-  const u64 total = block_sum_u64(mine, sm);
-  if (total == 0) return -1;
-  u64 inc = mine;
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += y;
-  }
-  __syncthreads();
-  if (lane == 31) sm.wsum[threadIdx.x >> 5] = inc;
-  __syncthreads();
-  u64 c = inc - mine;
-  for (int i = 0; i < (int)(threadIdx.x >> 5); ++i) c += sm.wsum[i];
-  const u64 t = (u64)((double)fminf(fmaxf(u, 0.f), 0.99999994f) * (double)total);
-  if (c <= t && t < c + mine)
-    for (int v = a; v < b; ++v) {
-      c += w(v);
-      if (t < c) {
-        sm.pick = v;
-        break;
-      }
-    }
-  __syncthreads();
-  return sm.pick;
+// The cut of min_p: max z + T ln(min_p), as the smallest float not below it.
+__device__ __forceinline__ unsigned min_p_key(float zmax, float temp, float min_p) {
+  const double zt = (double)zmax + (double)temp * log((double)min_p);
+  float zf = (float)zt;
+  if ((double)zf < zt) zf = nextafterf(zf, INFINITY);
+  return okey(fminf(zf, zmax));
 }
 
-template <typename T>
-__global__ void __launch_bounds__(NT) sample_kernel(SamplingArgs a) {
+template <typename T, bool RES>
+__global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice) {
+  extern __shared__ __align__(16) float zs_buf[];
   __shared__ Smem sm;
   pdl_launch_next();
   pdl_wait();
-  const int row = blockIdx.x, V = a.vocab;
-  const int s = row / a.rows, i = row - s * a.rows;  // sequence and its row
+  const int C = a.cluster, row = blockIdx.x / C, rank = blockIdx.x - row * C, V = a.vocab;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int seq = row / a.rows, i = row - seq * a.rows;  // sequence and its row
   int nd = a.rows - 1;
   if (a.kind == SAMPLING_VERIFY) {
-    if (a.n_draft) nd = min(max(a.n_draft[s], 0), nd);
-    if (i > nd) return;
+    if (a.n_draft) nd = min(max(a.n_draft[seq], 0), nd);
+    if (i > nd) return;  // the whole cluster
   }
-  const T* z = static_cast<const T*>(a.logits) + (size_t)row * a.stride;
-  const Row r = row_cut(z, V, a.temperature ? a.temperature[s] : 1.f, a.top_k ? a.top_k[s] : 0,
-                        a.top_p ? a.top_p[s] : 1.f, a.min_p ? a.min_p[s] : 0.f, sm);
-  if (r.total == 0 && threadIdx.x == 0) flag(a.status, DFLASH2_DEV_EMPTY_ROW);
+  const T* z_row = static_cast<const T*>(a.logits) + (size_t)row * a.stride;
+  const float temp = a.temperature ? a.temperature[seq] : 1.f;
+  const int top_k = a.top_k ? a.top_k[seq] : 0;
+  const float top_p = a.top_p ? a.top_p[seq] : 1.f, min_p = a.min_p ? a.min_p[seq] : 0.f;
+  const bool greedy = !(temp > 0.f);
+
+  // ---- 1. the slice into shared memory, its largest and smallest logit
+  Slice<T, RES> s;
+  s.row = z_row;
+  s.zs = zs_buf;
+  s.begin = min(V, rank * slice);
+  s.end = min(V, s.begin + slice);
+  constexpr int VEC = 16 / sizeof(T);
+  const int mis = (int)((reinterpret_cast<uintptr_t>(z_row + s.begin) / sizeof(T)) % VEC);
+  s.first = s.begin - mis;
+  s.groups = s.end > s.begin ? (s.end - s.first + VEC - 1) / VEC * (VEC / 4) : 0;
+  float mx = -INFINITY, mn = INFINITY;
+  auto see = [&](float z) {
+    if (z > -INFINITY) {  // (false for NaN)
+      mx = fmaxf(mx, z);
+      mn = fminf(mn, z);
+    }
+  };
+  if constexpr (RES) {
+    constexpr int U = 4;
+    const int nv = s.groups / (VEC / 4);
+    for (int v0 = tid; v0 < nv; v0 += U * NT) {
+      uint4 q[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int v = v0 + u * NT, id = s.first + v * VEC;
+        if (v < nv && id >= s.begin && id + VEC <= s.end) q[u] = __ldg(reinterpret_cast<const uint4*>(z_row + id));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int v = v0 + u * NT, id = s.first + v * VEC;
+        if (v >= nv) break;
+        float e[VEC];
+        if (id >= s.begin && id + VEC <= s.end) {
+          unpack16<T>(q[u], e);
+        } else {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) e[j] = id + j >= s.begin && id + j < s.end ? ld(z_row + id + j) : -INFINITY;
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) see(e[j]);
+#pragma unroll
+        for (int j = 0; j < VEC; j += 4)
+          *reinterpret_cast<float4*>(zs_buf + v * VEC + j) = make_float4(e[j], e[j + 1], e[j + 2], e[j + 3]);
+      }
+    }
+  } else {
+    for_each(s, [&](float z, int) { see(z); });
+  }
+  for (int b = tid; b < NB; b += NT) sm.hist[b] = 0;
+  if (tid == 0) {
+    sm.ncand = 0;
+    sm.pick = -1;
+    sm.pick2 = 0x7fffffff;
+  }
+  mx = warp_max(mx);
+  mn = -warp_max(-mn);
+  if (lane == 0) {
+    sm.fsum[warp] = mx;
+    reinterpret_cast<float*>(sm.wsum)[warp] = mn;
+  }
+  __syncthreads();
+  if (tid < C) {
+    float x = sm.fsum[0], y = reinterpret_cast<float*>(sm.wsum)[0];
+    for (int w = 1; w < NW; ++w) {
+      x = fmaxf(x, sm.fsum[w]);
+      y = fminf(y, reinterpret_cast<float*>(sm.wsum)[w]);
+    }
+    st_cl(dsmem_addr(&sm.xmax[rank], tid), __float_as_uint(x));
+    st_cl(dsmem_addr(&sm.xmin[rank], tid), __float_as_uint(y));
+  }
+  cluster_sync();
+  float zmin = INFINITY, zmax = -INFINITY;
+  for (int r = 0; r < C; ++r) {
+    zmax = fmaxf(zmax, sm.xmax[r]);
+    zmin = fminf(zmin, sm.xmin[r]);
+  }
+  const Scale sc = make_scale(zmax, greedy ? 1.f : temp);
+  const bool empty = !(zmax > -INFINITY);
+
+  Cut cut = {KEY_NINF + 1, V};  // everything above -inf
+  u64 total = 0;                // mass of the cut, when known
+  bool list = false;            // the kept tokens are the first `n_kept` of the first CTA's sorted list
+  int n_kept = 0;
+
+  // Broadcasts the first CTA's sm.mk.  (Two turns: a CTA that still reads one
+  // decision is at least a cluster barrier ahead of the next but one.)
+  int told = 0;
+  auto broadcast = [&]() -> const Decision& {
+    if (rank == 0) {
+      __syncthreads();
+      for (int w = tid; w < DW * C; w += NT)
+        st_cl(dsmem_addr(reinterpret_cast<unsigned*>(&sm.dec[told]) + w % DW, w / DW),
+              reinterpret_cast<const unsigned*>(&sm.mk)[w % DW]);
+    }
+    cluster_sync();
+    const Decision& d = sm.dec[told];
+    told ^= 1;
+    return d;
+  };
+  // Sums two masses over the cluster.
+  int turn = 0;
+  auto exchange = [&](u64& m, u64& g) {
+    m = block_sum_u64(m, sm);
+    g = block_sum_u64(g, sm);
+    if (tid < C) {
+      st_cl(dsmem_addr(&sm.xm[turn][rank], tid), m);
+      st_cl(dsmem_addr(&sm.xg[turn][rank], tid), g);
+    }
+    cluster_sync();
+    m = g = 0;
+    for (int r = 0; r < C; ++r) m += sm.xm[turn][r], g += sm.xg[turn][r];
+    turn ^= 1;
+  };
+  auto mass_kept = [&]() {
+    u64 m = 0, g = 0;
+    for_each(s, [&](float z, int id) {
+      if (kept(okey(z), id, cut)) m += mass_of(z, sc);
+    });
+    exchange(m, g);
+    return m;
+  };
+
+  if (!empty && greedy) {
+    int id0 = 0x7fffffff;
+    for_each(s, [&](float z, int id) {
+      if (z == zmax) id0 = min(id0, id);
+    });
+    id0 = __reduce_min_sync(0xffffffffu, id0);
+    if (lane == 0 && id0 != 0x7fffffff) atomicMin(&sm.pick2, id0);
+    __syncthreads();
+    if (tid < C) st_cl(dsmem_addr(&sm.xid[rank], tid), (unsigned)sm.pick2);
+    cluster_sync();
+    id0 = 0x7fffffff;
+    for (int r = 0; r < C; ++r) id0 = min(id0, sm.xid[r]);
+    cut = {okey(zmax), id0};
+    total = 1ull << 42;
+  }
+
+  // ---- 2. top-k and top-p: a histogram of the row's range finds the bins that
+  // hold a border; their tokens are gathered and sorted by the first CTA
+  const bool by_k = !empty && !greedy && top_k > 0 && top_k < V, by_p = !empty && !greedy && top_p < 1.f;
+  if (by_k || by_p) {
+    // bins of equal width over [zmax - 64, zmax] or the row's own range if that
+    // is smaller; what lies lower falls into the last bin
+    const float range = fminf(zmax - zmin, 64.f);
+    const float per = range > 0.f ? fminf((float)NB / range, 1e30f) : 1.f;
+    auto bin_of = [&](float z) { return z == zmax ? 0 : (int)fminf((zmax - z) * per, (float)(NB - 1)); };
+    for_each(s, [&](float z, int) {
+      if (z > -INFINITY) atomicAdd(&sm.hist[bin_of(z)], 1u);
+    });
+    cluster_sync();
+    unsigned c2[2] = {0, 0};  // the first CTA's threads: counts of bins 2 tid, 2 tid + 1, then of those before
+    u64 n_all = 0, n_before = 0;
+    if (rank == 0) {
+      for (int r = 0; r < C; ++r) {
+        c2[0] += ld_cl(dsmem_addr(&sm.hist[2 * tid], r));
+        c2[1] += ld_cl(dsmem_addr(&sm.hist[2 * tid + 1], r));
+      }
+      n_before = block_scan_u64(c2[0] + c2[1], &n_all, sm);
+      __syncthreads();
+      sm.hist[2 * tid] = c2[0];  // from here on the row's counts
+      sm.hist[2 * tid + 1] = c2[1];
+      if (tid == 0) sm.mk.step = STEP_NONE;
+      __syncthreads();
+      if (by_k && (u64)top_k < n_all) {
+        for (int h = 0; h < 2; ++h) {
+          const u64 b0 = n_before + (h ? c2[0] : 0);
+          if (b0 < (u64)top_k && (u64)top_k <= b0 + c2[h]) {  // one thread
+            const int b = 2 * tid + h;
+            sm.mk.lo = b;
+            sm.mk.hi = b;
+            sm.mk.before = (unsigned)b0;
+            if (b0 + c2[h] <= CAP) {
+              sm.mk.lo = 0;
+              sm.mk.before = 0;
+              sm.mk.step = STEP_LIST;
+            } else {
+              sm.mk.step = c2[h] <= CAP ? STEP_TOPK : STEP_SLOW_K;
+            }
+          }
+        }
+      }
+    }
+    Decision dec = broadcast();
+    // Gathers the tokens of the decision's bins into the first CTA's list.
+    auto gather = [&](int lo, int hi) {
+      const uint32_t counter = dsmem_addr(&sm.ncand, 0), base = dsmem_addr(sm.cand, 0);
+      for_each(s, [&](float z, int id) {
+        bool in = z > -INFINITY;
+        if (in) {
+          const int b = bin_of(z);
+          in = b >= lo && b <= hi;
+        }
+        const unsigned m = __ballot_sync(0xffffffffu, in);
+        if (m) {
+          unsigned at = 0;
+          if (lane == 0) at = add_cl(counter, __popc(m));
+          at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1));
+          if (in && at < CAP) st_cl(base + 8 * at, ((u64)okey(z) << 32) | (unsigned)~id);
+        }
+      });
+    };
+    auto cut_at = [&](int p) { return Cut{(unsigned)(sm.cand[p] >> 32), (int)~(unsigned)sm.cand[p]}; };
+    // masses of the list in order: this thread's four, and the mass before them
+    u64 lm[CAP / NT], lbefore = 0, lall = 0;
+    auto scan_list = [&](int n) {
+      u64 sum = 0;
+#pragma unroll
+      for (int j = 0; j < CAP / NT; ++j) {
+        const int p = tid * (CAP / NT) + j;
+        lm[j] = p < n ? mass_of(okey_value((unsigned)(sm.cand[p] >> 32)), sc) : 0ull;
+        sum += lm[j];
+      }
+      lbefore = block_scan_u64(sum, &lall, sm);
+    };
+    // first position of the list whose running mass, after `ahead`, reaches `want`
+    auto find_mass = [&](int n, u64 ahead, u64 want) {
+      if (tid == 0) sm.pick2 = n - 1;
+      __syncthreads();
+      u64 c = ahead + lbefore;
+#pragma unroll
+      for (int j = 0; j < CAP / NT; ++j) {
+        if (c < want && want <= c + lm[j]) sm.pick2 = tid * (CAP / NT) + j;
+        c += lm[j];
+      }
+      __syncthreads();
+      const int p = sm.pick2;
+      __syncthreads();
+      return p;
+    };
+    // mass of the list up to position p
+    auto mass_to = [&](int p) {
+      u64 c = lbefore;
+#pragma unroll
+      for (int j = 0; j < CAP / NT; ++j) {
+        c += lm[j];
+        if (tid * (CAP / NT) + j == p) sm.sel_before = c;
+      }
+      __syncthreads();
+      const u64 v = sm.sel_before;
+      __syncthreads();
+      return v;
+    };
+
+    if (dec.step == STEP_LIST) {
+      gather(0, dec.hi);
+      cluster_sync();
+      list = true;
+      if (rank == 0) {
+        const int n = (int)sm.ncand;
+        sort_desc(sm.cand, n);
+        scan_list(n);
+        n_kept = min(top_k, n);
+        total = mass_to(n_kept - 1);
+        if (by_p) {
+          n_kept = min(n_kept, find_mass(n, 0, share_of(top_p, total)) + 1);
+          total = mass_to(n_kept - 1);
+        }
+      }
+    } else {
+      if (dec.step == STEP_TOPK) {
+        gather(dec.lo, dec.hi);
+        cluster_sync();
+        if (rank == 0) {
+          const int n = (int)sm.ncand;
+          sort_desc(sm.cand, n);
+          if (tid == 0) {
+            sm.mk.cut = cut_at(top_k - (int)dec.before - 1);
+            sm.ncand = 0;
+          }
+        }
+        cut = broadcast().cut;
+      } else if (dec.step == STEP_SLOW_K) {
+        if (rank == 0) {
+          const Cut c = select_slow(z_row, V, sc, cut, true, (u64)top_k, sm);
+          if (tid == 0) sm.mk.cut = c;
+        }
+        cut = broadcast().cut;
+      }
+      if (by_p) {
+        // the border's bin by the counts and each bin's middle: an estimate
+        // that only decides which bins are gathered; the exact masses decide
+        if (rank == 0) {
+          const int last = dec.step == STEP_NONE ? NB - 1 : dec.lo;
+          __syncthreads();
+          float w2[2], f = 0.f;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int b = 2 * tid + h;
+            w2[h] = b <= last ? (float)c2[h] * exp2f(-((float)b + 0.5f) / per * sc.hi) : 0.f;
+            f += w2[h];
+          }
+          float inc = f;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const float y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+          }
+          if (lane == 31) sm.fsum[warp] = inc;
+          if (tid == 0) sm.pick2 = 0;
+          __syncthreads();
+          float before = inc - f, all = 0.f;
+          for (int w = 0; w < NW; ++w) {
+            if (w < warp) before += sm.fsum[w];
+            all += sm.fsum[w];
+          }
+          const float want = top_p * all;
+          if (w2[0] > 0.f && before < want) atomicMax(&sm.pick2, 2 * tid);
+          if (w2[1] > 0.f && before + w2[0] < want) atomicMax(&sm.pick2, 2 * tid + 1);
+          __syncthreads();
+          if (tid == 0) {
+            int lo = sm.pick2, hi = lo;
+            unsigned n = sm.hist[lo];
+            for (int d = 0; d < 32; ++d) {  // widen by turns, down to the top and to 16 bins a side
+              const bool up = d & 1;
+              if (up ? lo == 0 : hi == last) continue;
+              const unsigned m = sm.hist[up ? lo - 1 : hi + 1];
+              if (n + m > CAP / 2) continue;
+              n += m;
+              if (up) --lo; else ++hi;
+            }
+            sm.mk.lo = lo;
+            sm.mk.hi = hi;
+            sm.mk.step = n <= CAP ? STEP_TOPP : STEP_SLOW_P;
+          }
+        }
+        dec = broadcast();
+        const int lo = dec.lo, hi = dec.hi;
+        u64 m = 0, g = 0;  // kept mass, and what of it lies ahead of the gathered bins
+        for_each(s, [&](float z, int id) {
+          if (kept(okey(z), id, cut)) {
+            const u64 e = mass_of(z, sc);
+            m += e;
+            if (bin_of(z) < lo) g += e;
+          }
+        });
+        if (dec.step == STEP_TOPP) gather(lo, hi);
+        exchange(m, g);
+        const u64 want = share_of(top_p, m);
+        if (rank == 0) {
+          bool found = false;
+          if (dec.step == STEP_TOPP) {
+            const int n = (int)sm.ncand;
+            sort_desc(sm.cand, n);
+            scan_list(n);
+            // (tokens of the last bin past the top-k cut stay behind the border:
+            // the mass up to the cut is m, and want <= m)
+            if (g < want && want <= g + lall) {
+              found = true;
+              const int p = find_mass(n, g, want);
+              total = g + mass_to(p);
+              if (tid == 0) sm.mk.cut = cut_at(p);
+              n_kept = p + 1;
+            }
+          }
+          if (!found) {
+            const Cut c = select_slow(z_row, V, sc, cut, false, want, sm);
+            if (tid == 0) sm.mk.cut = c;
+            total = 0;
+          }
+          if (tid == 0) {
+            sm.mk.step = found && lo == 0 ? STEP_LIST : STEP_NONE;
+            sm.mk.total_lo = (unsigned)total;
+            sm.mk.total_hi = (unsigned)(total >> 32);
+          }
+        }
+        dec = broadcast();
+        cut = dec.cut;
+        total = ((u64)dec.total_hi << 32) | dec.total_lo;
+        list = dec.step == STEP_LIST;
+      }
+    }
+    if (list && rank == 0) {
+      if (min_p > 0.f) {
+        const unsigned mk = min_p_key(zmax, temp, min_p);
+        if (tid == 0) sm.pick2 = 0;
+        __syncthreads();
+        for (int p = tid; p < n_kept; p += NT)
+          if ((unsigned)(sm.cand[p] >> 32) >= mk) atomicMax(&sm.pick2, p);
+        __syncthreads();
+        n_kept = sm.pick2 + 1;
+        __syncthreads();
+        total = mass_to(n_kept - 1);
+      }
+      cut = cut_at(n_kept - 1);
+      __syncthreads();  // the list is reordered below
+    }
+  }
+  if (!list && !empty && !greedy && min_p > 0.f) {
+    const unsigned mk = min_p_key(zmax, temp, min_p);
+    if (mk > cut.key) {
+      cut = {mk, V};
+      total = 0;
+    }
+  }
+
+  // ---- 3. the outputs
+  if (empty && rank == 0 && tid == 0) flag(a.status, DFLASH2_DEV_EMPTY_ROW);
   if (a.kind == SAMPLING_PROBS) {
+    if (list) {  // the others need the first CTA's cut
+      if (rank == 0 && tid == 0) {
+        sm.mk.cut = cut;
+        sm.mk.total_lo = (unsigned)total;
+        sm.mk.total_hi = (unsigned)(total >> 32);
+      }
+      const Decision dec = broadcast();
+      cut = dec.cut;
+      total = ((u64)dec.total_hi << 32) | dec.total_lo;
+    } else if (!empty && total == 0) {
+      total = mass_kept();
+    }
     float* p = a.prob + (size_t)row * V;
-    const float inv = r.total ? (float)(4398046511104.0 / (double)r.total) : 0.f;
-    for (int v = threadIdx.x; v < V; v += NT) {
-      const float zv = ld(z + v);
-      p[v] = r.total && kept(okey(zv), v, r.cut) ? mass_f32(zv, r.s) * inv : 0.f;
+    const float inv = empty ? 0.f : (float)(4398046511104.0 / (double)total);
+    for (int q = tid; q < 4 * s.groups; q += NT) {
+      const int id = s.first + q;
+      if (id < s.begin || id >= s.end) continue;
+      const float z = RES ? zs_buf[q] : ld(z_row + id);
+      p[id] = !empty && kept(okey(z), id, cut) ? mass_f32(z, sc) * inv : 0.f;
     }
     return;
   }
-  if (a.kind == SAMPLING_TOKEN) {
-    const int t = r.total ? row_draw(z, V, r, -1, a.u[row], sm) : -1;
-    if (threadIdx.x == 0) {
-      a.token[row] = t;
+  const bool verify = a.kind == SAMPLING_VERIFY;
+  int x = -1;       // the draft's token
+  u64 x_mass = 0;   // and its kept mass
+  if (list && rank != 0) return;  // the rest is the first CTA's
+  if (verify && i < nd) {
+    x = a.path[(size_t)seq * (a.rows - 1) + i];
+    if (!empty && x >= 0 && x < V) {
+      const float zx = ld(z_row + x);
+      x_mass = kept(okey(zx), x, cut) ? mass_of(zx, sc) : 0ull;
+    }
+  }
+  auto passes = [&]() {
+    const float u = fminf(fmaxf(a.u_accept[(size_t)seq * (a.rows - 1) + i], 0.f), 0.99999994f);
+    return (double)u * (double)total < (double)x_mass;
+  };
+  auto threshold = [&](u64 sum) { return (u64)((double)fminf(fmaxf(a.u[seq], 0.f), 0.99999994f) * (double)sum); };
+  auto finish = [&](int token, bool pass) {  // one thread of the cluster
+    if (verify) {
+      a.rowout[row] = make_int2(pass, token);
+    } else {
+      a.token[row] = token;
       if (a.prob)
-        a.prob[row] = t < 0 ? 0.f : mass_f32(ld(z + t), r.s) * (float)(4398046511104.0 / (double)r.total);
+        a.prob[row] = token < 0 ? 0.f : mass_f32(ld(z_row + token), sc) * (float)(4398046511104.0 / (double)total);
+    }
+  };
+  if (empty) {
+    if (rank == 0 && tid == 0) finish(-1, false);
+    return;
+  }
+  if (greedy) {
+    if (rank == 0 && tid == 0) {
+      const bool pass = verify && i < nd && x == cut.id;
+      finish(cut.id, pass);
     }
     return;
   }
-  // verification: whether draft i passes, and the token emitted if it does not
-  bool pass = false;
-  int x = -1;
-  if (i < nd) {
-    x = a.path[(size_t)s * (a.rows - 1) + i];
-    if (r.total && x >= 0 && x < V) {
-      const float zx = ld(z + x);
-      const u64 mx = kept(okey(zx), x, r.cut) ? mass_of(zx, r.s) : 0ull;
-      const float u = fminf(fmaxf(a.u_accept[(size_t)s * (a.rows - 1) + i], 0.f), 0.99999994f);
-      pass = (double)u * (double)r.total < (double)mx;
+  if (list) {
+    const bool pass = verify && i < nd && passes();
+    if (!pass) {
+      // the kept tokens in id order, and the first whose running mass exceeds the draw
+      for (int p = tid; p < n_kept; p += NT) {
+        const u64 v = sm.cand[p];
+        sm.cand[p] = (v << 32) | (v >> 32);  // (~id, key): descending is ascending ids
+      }
+      __syncthreads();
+      sort_desc(sm.cand, n_kept);
+      u64 e[CAP / NT], sum = 0, all;
+#pragma unroll
+      for (int j = 0; j < CAP / NT; ++j) {
+        const int p = tid * (CAP / NT) + j;
+        e[j] = 0;
+        if (p < n_kept && (int)~(unsigned)(sm.cand[p] >> 32) != x) e[j] = mass_of(okey_value((unsigned)sm.cand[p]), sc);
+        sum += e[j];
+      }
+      u64 c = block_scan_u64(sum, &all, sm);
+      if (all) {
+        const u64 t = threshold(all);
+#pragma unroll
+        for (int j = 0; j < CAP / NT; ++j) {
+          if (c <= t && t < c + e[j]) sm.pick = (int)~(unsigned)(sm.cand[tid * (CAP / NT) + j] >> 32);
+          c += e[j];
+        }
+      }
+      __syncthreads();
     }
+    if (tid == 0) finish(pass ? -1 : sm.pick, pass);
+    return;
   }
-  const int t = r.total && !pass ? row_draw(z, V, r, x, a.u[s], sm) : -1;
-  if (threadIdx.x == 0) a.rowout[row] = make_int2(pass, t);
+  // no list: masses by warp, each a contiguous range of the slice's groups
+  const int g0 = (int)((long long)s.groups * warp / NW), g1 = (int)((long long)s.groups * (warp + 1) / NW);
+  auto mass4 = [&](int q, u64 (&e)[4]) {
+    const float4 v = q < g1 ? s.get4(q) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    const float zz[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int id = s.first + 4 * q + j;
+      e[j] = id != x && kept(okey(zz[j]), id, cut) ? mass_of(zz[j], sc) : 0ull;
+    }
+  };
+  u64 wm = 0;
+  for (int q = g0 + lane; q < g1; q += 32) {
+    u64 e[4];
+    mass4(q, e);
+    wm += e[0] + e[1] + e[2] + e[3];
+  }
+  wm = warp_sum_u64(wm);
+  __syncthreads();
+  if (lane == 0) sm.wsum[warp] = wm;
+  __syncthreads();
+  u64 before = 0, mine = 0;
+  for (int w = 0; w < NW; ++w) {
+    if (w < warp) before += sm.wsum[w];
+    mine += sm.wsum[w];
+  }
+  if (tid < C) st_cl(dsmem_addr(&sm.xm[turn][rank], tid), mine);
+  cluster_sync();
+  u64 rest = 0;
+  for (int r = 0; r < C; ++r) {
+    if (r < rank) before += sm.xm[turn][r];
+    rest += sm.xm[turn][r];
+  }
+  total = rest + x_mass;
+  const bool pass = verify && i < nd && passes();
+  if (pass || rest == 0) {
+    if (rank == 0 && tid == 0) finish(-1, pass);
+    return;
+  }
+  const u64 t = threshold(rest);
+  if (!(before <= t && t < before + wm)) return;
+  // this warp holds the token
+  u64 c = before;
+  for (int q0 = g0; q0 < g1; q0 += 32) {
+    u64 e[4];
+    mass4(q0 + lane, e);
+    const u64 sum = e[0] + e[1] + e[2] + e[3];
+    u64 inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const u64 step_sum = __shfl_sync(0xffffffffu, inc, 31);
+    if (t < c + step_sum) {
+      u64 d = c + inc - sum;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (d <= t && t < d + e[j]) finish(s.first + 4 * (q0 + lane) + j, false);
+        d += e[j];
+      }
+      return;
+    }
+    c += step_sum;
+  }
 }
 
 // The accepted prefix of each sequence, its emitted tokens and the counters.
@@ -418,12 +971,38 @@ __global__ void verify_rows_kernel(SamplingArgs a) {
   }
 }
 
+template <typename T, bool RES>
+int launch_one(const SamplingArgs& a, int slice, const Ctx& c) {
+  auto kern = sample_kernel<T, RES>;
+  static std::atomic<unsigned long long> opted{0};  // devices whose kernel may use the largest size
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DFLASH2_ERR_CUDA;
+  if (RES && !(opted.load(std::memory_order_relaxed) >> dev & 1)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (SLICE1 + 16) * 4) != cudaSuccess)
+      return DFLASH2_ERR_CUDA;
+    opted.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
+  const size_t smem = RES ? (size_t)((slice + 15 + 8) / 8 * 8) * 4 : 0;
+  return launch_kx(kern, dim3(a.batch * a.rows * a.cluster), dim3(NT), smem, c, a.cluster, a, slice);
+}
+
+// A row's cluster: as few CTAs as hold it with two of them an SM (one, for the
+// largest vocabularies that still fit), more while the rows leave SMs idle.
+template <typename T>
+int launch_rows(SamplingArgs a, const Ctx& c) {
+  const int rows = a.batch * a.rows;
+  a.cluster = 1;
+  while (a.cluster < CMAX && (a.vocab > a.cluster * SLICE2 ||
+                              (rows * a.cluster < c.nsm && a.vocab > a.cluster * 4096)))
+    a.cluster *= 2;
+  const int slice = ((a.vocab + a.cluster - 1) / a.cluster + 7) / 8 * 8;
+  return slice <= SLICE1 ? launch_one<T, true>(a, slice, c) : launch_one<T, false>(a, slice, c);
+}
+
 }  // namespace
 
 int launch_sampling(const SamplingArgs& a, const Ctx& c) {
-  const dim3 grid(a.batch * a.rows);
-  const int k = a.bf16_logits ? launch_k(sample_kernel<bf16>, grid, dim3(NT), 0, c, a)
-                              : launch_k(sample_kernel<float>, grid, dim3(NT), 0, c, a);
+  const int k = a.bf16_logits ? launch_rows<bf16>(a, c) : launch_rows<float>(a, c);
   if (k != DFLASH2_OK || a.kind != SAMPLING_VERIFY) return k;
   return launch_k(verify_rows_kernel, dim3((a.batch + 127) / 128), dim3(128), 0, c, a);
 }
