@@ -53,7 +53,7 @@ struct ExpTab {
   long long fix[33];
   float hi[33], lo[33];
 };
-__constant__ ExpTab c_exp = {
+__device__ const ExpTab c_exp = {
     {6219777023951ll, 6086500028053ll, 5956078883349ll, 5828452394836ll, 5703560678795ll,
      5581345134690ll, 5461748417677ll, 5344714411690ll, 5230188203118ll, 5118116055032ll,
      5008445381977ll, 4901124725294ll, 4796103728980ll, 4693333116055ll, 4592764665442ll,
@@ -91,7 +91,7 @@ __device__ __forceinline__ Scale make_scale(float zmax, float T) {
 // log2(e) / T held as p + e (the difference exact by two-sum, the product by
 // fma), y = n + j/32 + g + e, |g| <= 1/64, and 2^-(g+e) = 1 - (g + e) ln 2 +
 // ..., whose linear term keeps its rounding error.
-__device__ __forceinline__ u64 mass_of(float z, const Scale& s) {
+__device__ __forceinline__ u64 mass_of(float z, const Scale& s, const ExpTab& tab) {
   if (z == s.zmax || s.hi == 0.f) return 1ull << 42;
   const float dh = s.zmax - z;
   const float p = __fmul_rn(dh, s.hi);  // never contracted: its rounding error goes to e
@@ -109,10 +109,10 @@ __device__ __forceinline__ u64 mass_of(float z, const Scale& s) {
   const float glr = fmaf(g, L1lo, fmaf(e, L1, fmaf(g, L1, -gl)));
   const float x = (g + e) * L1;
   const float q = x * x * fmaf(x, fmaf(x, 0.0416666667f, -0.1666666667f), 0.5f) - glr;  // 2^-(g+e) - 1 + gl
-  const float th = c_exp.hi[j], tl = c_exp.lo[j];
+  const float th = tab.hi[j], tl = tab.lo[j];
   const float m = __fmul_rn(th, gl);
   const float small = fmaf(th, q, -fmaf(th, gl, -m)) - tl * gl;
-  const long long v = c_exp.fix[j] - ((long long)__float2int_rn(m * 68719476736.f) << 6) +
+  const long long v = tab.fix[j] - ((long long)__float2int_rn(m * 68719476736.f) << 6) +
                       (long long)__float2int_rn(small * 4398046511104.f);
   const int sh = (int)n;  // 0..44
   return sh == 0 ? (u64)v : ((u64)v + (1ull << (sh - 1))) >> sh;
@@ -178,7 +178,9 @@ struct Decision {
 constexpr int DW = sizeof(Decision) / 4;
 
 struct Smem {
+  ExpTab tab;     // copy of c_exp: lanes read different entries
   u64 cand[CAP];  // first CTA: gathered tokens, (key, ~id)
+  float ecum[NB + 1];  // first CTA: estimated mass ahead of each bin
   unsigned hist[NB];
   u64 radix[256];
   u64 wsum[NW];
@@ -311,7 +313,7 @@ __device__ Cut select_slow(const T* row, int V, const Scale& s, Cut c, bool by_c
       const float z = ld(row + v);
       const unsigned k = okey(z);
       if ((k & mask) == prefix && kept(k, v, c))
-        atomicAdd(&sm.radix[(k >> (8 * level)) & 255u], by_count ? 1ull : mass_of(z, s));
+        atomicAdd(&sm.radix[(k >> (8 * level)) & 255u], by_count ? 1ull : mass_of(z, s, sm.tab));
     }
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -328,7 +330,7 @@ __device__ Cut select_slow(const T* row, int V, const Scale& s, Cut c, bool by_c
     __syncthreads();
   }
   // equal keys: the need-th of them in id order (each has the same weight)
-  const u64 w = by_count ? 1ull : mass_of(okey_value(prefix), s);
+  const u64 w = by_count ? 1ull : mass_of(okey_value(prefix), s, sm.tab);
   const u64 need = w ? max(1ull, (target - before + w - 1) / w) : 1ull;
   const int per = (V + NT - 1) / NT;
   const int a = min(V, (int)threadIdx.x * per), b = min(V, a + per);
@@ -381,6 +383,9 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     if (a.n_draft) nd = min(max(a.n_draft[seq], 0), nd);
     if (i > nd) return;  // the whole cluster
   }
+  static_assert(sizeof(ExpTab) / 4 <= NT, "one word of the table a thread");
+  const bool has_word = tid < (int)(sizeof(ExpTab) / 4);
+  const unsigned word = has_word ? reinterpret_cast<const unsigned*>(&c_exp)[tid] : 0u;
   const T* z_row = static_cast<const T*>(a.logits) + (size_t)row * a.stride;
   const float temp = a.temperature ? a.temperature[seq] : 1.f;
   const int top_k = a.top_k ? a.top_k[seq] : 0;
@@ -436,6 +441,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     for_each(s, [&](float z, int) { see(z); });
   }
   for (int b = tid; b < NB; b += NT) sm.hist[b] = 0;
+  if (has_word) reinterpret_cast<unsigned*>(&sm.tab)[tid] = word;
   if (tid == 0) {
     sm.ncand = 0;
     sm.pick = -1;
@@ -503,7 +509,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
   auto mass_kept = [&]() {
     u64 m = 0, g = 0;
     for_each(s, [&](float z, int id) {
-      if (kept(okey(z), id, cut)) m += mass_of(z, sc);
+      if (kept(okey(z), id, cut)) m += mass_of(z, sc, sm.tab);
     });
     exchange(m, g);
     return m;
@@ -597,7 +603,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
 #pragma unroll
       for (int j = 0; j < CAP / NT; ++j) {
         const int p = tid * (CAP / NT) + j;
-        lm[j] = p < n ? mass_of(okey_value((unsigned)(sm.cand[p] >> 32)), sc) : 0ull;
+        lm[j] = p < n ? mass_of(okey_value((unsigned)(sm.cand[p] >> 32)), sc, sm.tab) : 0ull;
         sum += lm[j];
       }
       lbefore = block_scan_u64(sum, &lall, sm);
@@ -667,93 +673,120 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
         cut = broadcast().cut;
       }
       if (by_p) {
-        // the border's bin by the counts and each bin's middle: an estimate
-        // that only decides which bins are gathered; the exact masses decide
+        // The border's bin is guessed from the counts and each bin's middle;
+        // the exact masses decide, and where they put the border elsewhere they
+        // correct the next guess.
+        float want_f = 0.f;
+        int lo_least = 0, hi_most = NB - 1;  // bins the border may still be in
         if (rank == 0) {
-          const int last = dec.step == STEP_NONE ? NB - 1 : dec.lo;
+          if (dec.step != STEP_NONE) hi_most = dec.lo;
           __syncthreads();
-          float w2[2], f = 0.f;
+          float w2[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int b = 2 * tid + h;
-            w2[h] = b <= last ? (float)c2[h] * exp2f(-((float)b + 0.5f) / per * sc.hi) : 0.f;
-            f += w2[h];
+            w2[h] = b <= hi_most && c2[h] ? (float)c2[h] * exp2f(-((float)b + 0.5f) / per * sc.hi) : 0.f;
           }
-          float inc = f;
+          float inc = w2[0] + w2[1];
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
             const float y = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += y;
           }
           if (lane == 31) sm.fsum[warp] = inc;
-          if (tid == 0) sm.pick2 = 0;
           __syncthreads();
-          float before = inc - f, all = 0.f;
+          float before = inc - w2[0] - w2[1], all = 0.f;
           for (int w = 0; w < NW; ++w) {
             if (w < warp) before += sm.fsum[w];
             all += sm.fsum[w];
           }
-          const float want = top_p * all;
-          if (w2[0] > 0.f && before < want) atomicMax(&sm.pick2, 2 * tid);
-          if (w2[1] > 0.f && before + w2[0] < want) atomicMax(&sm.pick2, 2 * tid + 1);
-          __syncthreads();
-          if (tid == 0) {
-            int lo = sm.pick2, hi = lo;
-            unsigned n = sm.hist[lo];
-            for (int d = 0; d < 32; ++d) {  // widen by turns, down to the top and to 16 bins a side
-              const bool up = d & 1;
-              if (up ? lo == 0 : hi == last) continue;
-              const unsigned m = sm.hist[up ? lo - 1 : hi + 1];
-              if (n + m > CAP / 2) continue;
-              n += m;
-              if (up) --lo; else ++hi;
-            }
-            sm.mk.lo = lo;
-            sm.mk.hi = hi;
-            sm.mk.step = n <= CAP ? STEP_TOPP : STEP_SLOW_P;
-          }
+          sm.ecum[2 * tid] = before;
+          sm.ecum[2 * tid + 1] = before + w2[0];
+          if (tid == 0) sm.ecum[NB] = all;
+          want_f = top_p * all;
         }
-        dec = broadcast();
-        const int lo = dec.lo, hi = dec.hi;
-        u64 m = 0, g = 0;  // kept mass, and what of it lies ahead of the gathered bins
-        for_each(s, [&](float z, int id) {
-          if (kept(okey(z), id, cut)) {
-            const u64 e = mass_of(z, sc);
-            m += e;
-            if (bin_of(z) < lo) g += e;
-          }
-        });
-        if (dec.step == STEP_TOPP) gather(lo, hi);
-        exchange(m, g);
-        const u64 want = share_of(top_p, m);
-        if (rank == 0) {
-          bool found = false;
-          if (dec.step == STEP_TOPP) {
-            const int n = (int)sm.ncand;
-            sort_desc(sm.cand, n);
-            scan_list(n);
-            // (tokens of the last bin past the top-k cut stay behind the border:
-            // the mass up to the cut is m, and want <= m)
-            if (g < want && want <= g + lall) {
-              found = true;
-              const int p = find_mass(n, g, want);
-              total = g + mass_to(p);
-              if (tid == 0) sm.mk.cut = cut_at(p);
-              n_kept = p + 1;
+        for (int tries = 0;; ++tries) {
+          if (rank == 0) {
+            if (tid == 0) sm.pick2 = lo_least;
+            __syncthreads();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int b = 2 * tid + h;
+              if (b > lo_least && b <= hi_most && sm.hist[b] && sm.ecum[b] < want_f) atomicMax(&sm.pick2, b);
+            }
+            __syncthreads();
+            if (tid == 0) {
+              int lo = sm.pick2, hi = lo;
+              unsigned n = sm.hist[lo];
+              bool up = true, down = true;
+              for (int d = 0; d < 32 && (up || down); ++d) {  // widen by turns, by 16 bins a side at most
+                bool& side = d & 1 ? up : down;
+                if (!side) continue;
+                const int b = d & 1 ? lo - 1 : hi + 1;
+                side = b >= lo_least && b <= hi_most && n + sm.hist[b] <= CAP;
+                if (!side) continue;
+                n += sm.hist[b];
+                lo = min(lo, b);
+                hi = max(hi, b);
+              }
+              sm.mk.lo = lo;
+              sm.mk.hi = hi;
+              sm.mk.step = n <= CAP && tries < 8 ? STEP_TOPP : STEP_SLOW_P;
+              sm.ncand = 0;
             }
           }
-          if (!found) {
-            const Cut c = select_slow(z_row, V, sc, cut, false, want, sm);
-            if (tid == 0) sm.mk.cut = c;
-            total = 0;
+          dec = broadcast();
+          const int lo = dec.lo, hi = dec.hi;
+          u64 m = 0, g = 0;  // kept mass, and what of it lies ahead of the gathered bins
+          for_each(s, [&](float z, int id) {
+            if (kept(okey(z), id, cut)) {
+              const u64 e = mass_of(z, sc, sm.tab);
+              m += e;
+              if (bin_of(z) < lo) g += e;
+            }
+          });
+          if (dec.step == STEP_TOPP) gather(lo, hi);
+          exchange(m, g);
+          if (rank == 0) {
+            const u64 want = share_of(top_p, m);
+            bool found = false, slow = dec.step == STEP_SLOW_P;
+            if (!slow) {
+              const int n = (int)sm.ncand;
+              sort_desc(sm.cand, n);
+              scan_list(n);
+              // (tokens of the last bin past the top-k cut stay behind the border:
+              // the mass up to the cut is m, and want <= m)
+              if (g < want && want <= g + lall) {
+                found = true;
+                const int p = find_mass(n, g, want);
+                total = g + mass_to(p);
+                if (tid == 0) sm.mk.cut = cut_at(p);
+                n_kept = p + 1;
+              } else {
+                const bool later = want > g;
+                const u64 at = later ? g + lall : g;
+                want_f = sm.ecum[later ? hi + 1 : lo] +
+                         (float)(((double)want - (double)at) * (1.0 / 4398046511104.0));
+                if (later) lo_least = hi + 1;
+                else hi_most = lo - 1;
+                slow = lo_least > hi_most;
+                __syncthreads();
+              }
+            }
+            if (slow) {
+              const Cut c = select_slow(z_row, V, sc, cut, false, want, sm);
+              if (tid == 0) sm.mk.cut = c;
+              total = 0;
+            }
+            if (tid == 0) {
+              sm.mk.step = found && lo == 0 ? STEP_LIST : found || slow ? STEP_NONE : STEP_TOPP;
+              sm.mk.total_lo = (unsigned)total;
+              sm.mk.total_hi = (unsigned)(total >> 32);
+            }
           }
-          if (tid == 0) {
-            sm.mk.step = found && lo == 0 ? STEP_LIST : STEP_NONE;
-            sm.mk.total_lo = (unsigned)total;
-            sm.mk.total_hi = (unsigned)(total >> 32);
-          }
+          dec = broadcast();
+          if (dec.step != STEP_TOPP) break;
         }
-        dec = broadcast();
         cut = dec.cut;
         total = ((u64)dec.total_hi << 32) | dec.total_lo;
         list = dec.step == STEP_LIST;
@@ -816,7 +849,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     x = a.path[(size_t)seq * (a.rows - 1) + i];
     if (!empty && x >= 0 && x < V) {
       const float zx = ld(z_row + x);
-      x_mass = kept(okey(zx), x, cut) ? mass_of(zx, sc) : 0ull;
+      x_mass = kept(okey(zx), x, cut) ? mass_of(zx, sc, sm.tab) : 0ull;
     }
   }
   auto passes = [&]() {
@@ -859,7 +892,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
       for (int j = 0; j < CAP / NT; ++j) {
         const int p = tid * (CAP / NT) + j;
         e[j] = 0;
-        if (p < n_kept && (int)~(unsigned)(sm.cand[p] >> 32) != x) e[j] = mass_of(okey_value((unsigned)sm.cand[p]), sc);
+        if (p < n_kept && (int)~(unsigned)(sm.cand[p] >> 32) != x) e[j] = mass_of(okey_value((unsigned)sm.cand[p]), sc, sm.tab);
         sum += e[j];
       }
       u64 c = block_scan_u64(sum, &all, sm);
@@ -884,7 +917,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int id = s.first + 4 * q + j;
-      e[j] = id != x && kept(okey(zz[j]), id, cut) ? mass_of(zz[j], sc) : 0ull;
+      e[j] = id != x && kept(okey(zz[j]), id, cut) ? mass_of(zz[j], sc, sm.tab) : 0ull;
     }
   };
   u64 wm = 0;
