@@ -955,7 +955,7 @@ int dflash2_target_probs(int dtype, int batch, int rows, int vocab, const void* 
 
 size_t dflash2_verify_logits_workspace(int batch, int block_size) {
   if (batch <= 0 || block_size < 2 || block_size > 32) return 0;
-  return 256 + al((size_t)batch * block_size * sizeof(int2));
+  return 256 + kSamplingJoin * sizeof(int) + al((size_t)batch * block_size * sizeof(int2));
 }
 
 int dflash2_verify_logits(int dtype, int batch, int block_size, int vocab, const int32_t* path,
@@ -989,7 +989,9 @@ int dflash2_verify_logits(int dtype, int batch, int block_size, int vocab, const
   a.path = path;
   a.n_draft = n_draft;
   a.u_accept = u_accept;
-  a.rowout = at<int2>(workspace, 256);
+  // (the same offsets for every size: counters left at zero by one call are zero for the next)
+  a.arrived = batch <= kSamplingJoin ? at<int>(workspace, 256) : nullptr;
+  a.rowout = at<int2>(workspace, 256 + kSamplingJoin * sizeof(int));
   a.accept_len = accept_len;
   a.out_tok = out_tok;
   a.n_out = n_out;

@@ -304,9 +304,13 @@ struct SamplingArgs {
   const int32_t *path, *n_draft;
   const float* u_accept;
   int2* rowout;  // workspace [batch * rows]: (draft passes, token emitted if it does not)
+  int* arrived;  // workspace [kSamplingJoin], or null: a sequence's rows that have ended, zero between calls
   int32_t *accept_len, *out_tok, *n_out, *next_anchor, *seq_len;
   int64_t* counters;
 };
+// Sequences up to which a verification's rows are joined by the last row to
+// end; more take a second kernel (whose launch, about 2 us, they hide).
+constexpr int kSamplingJoin = 256;
 int launch_sampling(const SamplingArgs& a, const Ctx& c);
 
 }  // namespace df2

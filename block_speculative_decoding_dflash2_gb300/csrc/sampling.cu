@@ -32,7 +32,8 @@ typedef unsigned long long u64;
 
 constexpr int NT = 512, NW = NT / 32;
 constexpr int NB = 1024;    // bins of a row's histogram
-constexpr int CAP = 2048;   // tokens of a sorted list
+constexpr int CAP = 2048;   // tokens of a list
+constexpr int SMALL = 256;  // tokens of a list that is ranked instead of sorted
 constexpr int CMAX = 8;     // CTAs of a row's cluster
 constexpr int SLICE2 = 20480, SLICE1 = 50000;  // logits a CTA holds, two CTAs and one CTA an SM
 constexpr unsigned KEY_NINF = 0x007fffffu;  // order of -inf; NaN maps to 0
@@ -190,6 +191,11 @@ struct Smem {
   float fsum[NW];
   Decision mk;      // first CTA: the next decision
   Decision dec[2];  // the last one received, two turns
+  struct {
+    u64 total;
+    Cut cut;
+    int n;
+  } sel[3];  // small lists: the kept tokens after top-k, top-p and min-p
   unsigned ncand;
   unsigned sel_key;
   u64 sel_before;
@@ -369,6 +375,38 @@ __device__ __forceinline__ unsigned min_p_key(float zmax, float temp, float min_
   return okey(fminf(zf, zmax));
 }
 
+// The accepted prefix of a sequence, its emitted tokens and the counters, by
+// one warp (lane i looks after row i).
+__device__ void join_rows(const SamplingArgs& a, int s, int nd) {
+  const int lane = threadIdx.x & 31, B = a.rows, D = B - 1;
+  const int2 ro = lane <= nd ? __ldcg(a.rowout + (size_t)s * B + lane) : make_int2(0, -1);
+  const int n = __ffs(~__ballot_sync(0xffffffffu, lane < nd && ro.x)) - 1;  // drafts accepted
+  const int tok = __shfl_sync(0xffffffffu, ro.y, n);
+  if (lane < B) a.out_tok[(size_t)s * B + lane] = lane < n ? a.path[(size_t)s * D + lane] : (lane == n ? tok : -1);
+  u64* c = reinterpret_cast<u64*>(a.counters);
+  if (c && lane < n) atomicAdd(c + 4 + B + lane, 1ull);
+  if (lane == 0) {
+    a.accept_len[s] = n;
+    a.n_out[s] = n + 1;
+    a.next_anchor[s] = tok;
+    if (a.seq_len) a.seq_len[s] += n + 1;
+    if (c) {
+      atomicAdd(c + 0, 1ull);
+      atomicAdd(c + 1, (u64)nd);
+      atomicAdd(c + 2, (u64)n);
+      atomicAdd(c + 3, (u64)(nd - n));
+      atomicAdd(c + 4 + n, 1ull);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(128) join_kernel(SamplingArgs a) {
+  pdl_launch_next();
+  pdl_wait();
+  const int s = blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (s < a.batch) join_rows(a, s, a.n_draft ? min(max(a.n_draft[s], 0), a.rows - 1) : a.rows - 1);
+}
+
 template <typename T, bool RES>
 __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice) {
   extern __shared__ __align__(16) float zs_buf[];
@@ -474,8 +512,11 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
 
   Cut cut = {KEY_NINF + 1, V};  // everything above -inf
   u64 total = 0;                // mass of the cut, when known
-  bool list = false;            // the kept tokens are the first `n_kept` of the first CTA's sorted list
-  int n_kept = 0;
+  bool list = false;            // the kept tokens are the first `n_kept` of the first CTA's list,
+  int n_kept = 0;               // sorted, or ranked if it is small (then thread t holds token t)
+  bool small = false;
+  u64 lkey = 0, lmass = 0, lcum = 0;
+  int lrank = 0;
 
   // Broadcasts the first CTA's sm.mk.  (Two turns: a CTA that still reads one
   // decision is at least a cluster barrier ahead of the next but one.)
@@ -637,19 +678,59 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
       return v;
     };
 
+    // Small lists are not sorted: thread t holds token t and finds by one pass
+    // over the list how many tokens are ahead of it and their mass.
+    auto rank_list = [&](int n) {
+      lkey = tid < n ? sm.cand[tid] : 0;
+      lmass = tid < n ? mass_of(okey_value((unsigned)(lkey >> 32)), sc, sm.tab) : 0ull;
+      if (tid < n) sm.radix[tid] = lmass;
+      if (tid == 0) sm.pick2 = 0;
+      __syncthreads();
+      lrank = 0;  // tokens up to and with this one
+      lcum = 0;
+      if (tid < n)
+        for (int j = 0; j < n; ++j)
+          if (sm.cand[j] >= lkey) {
+            ++lrank;
+            lcum += sm.radix[j];
+          }
+    };
+    // the thread of the list's p-th token (from 1) tells the others
+    auto tell = [&](int slot, bool mine, u64 ahead) {
+      if (mine) {
+        sm.sel[slot].total = ahead + lcum;
+        sm.sel[slot].cut = {(unsigned)(lkey >> 32), (int)~(unsigned)lkey};
+        sm.sel[slot].n = lrank;
+      }
+      __syncthreads();
+      total = sm.sel[slot].total;
+      cut = sm.sel[slot].cut;
+      n_kept = sm.sel[slot].n;
+    };
+
     if (dec.step == STEP_LIST) {
       gather(0, dec.hi);
       cluster_sync();
       list = true;
       if (rank == 0) {
         const int n = (int)sm.ncand;
-        sort_desc(sm.cand, n);
-        scan_list(n);
-        n_kept = min(top_k, n);
-        total = mass_to(n_kept - 1);
-        if (by_p) {
-          n_kept = min(n_kept, find_mass(n, 0, share_of(top_p, total)) + 1);
+        small = n <= SMALL;
+        if (small) {
+          rank_list(n);
+          tell(0, lrank > 0 && lrank == min(top_k, n), 0);
+          if (by_p) {
+            const u64 want = share_of(top_p, total);
+            tell(1, lrank > 0 && lcum >= want && lcum - lmass < want, 0);
+          }
+        } else {
+          sort_desc(sm.cand, n);
+          scan_list(n);
+          n_kept = min(top_k, n);
           total = mass_to(n_kept - 1);
+          if (by_p) {
+            n_kept = min(n_kept, find_mass(n, 0, share_of(top_p, total)) + 1);
+            total = mass_to(n_kept - 1);
+          }
         }
       }
     } else {
@@ -752,16 +833,28 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
             bool found = false, slow = dec.step == STEP_SLOW_P;
             if (!slow) {
               const int n = (int)sm.ncand;
-              sort_desc(sm.cand, n);
-              scan_list(n);
+              small = n <= SMALL;
+              if (small) {
+                rank_list(n);
+                tell(0, lrank > 0 && lrank == n, 0);
+                lall = n ? total : 0ull;
+              } else {
+                sort_desc(sm.cand, n);
+                scan_list(n);
+              }
               // (tokens of the last bin past the top-k cut stay behind the border:
               // the mass up to the cut is m, and want <= m)
               if (g < want && want <= g + lall) {
                 found = true;
-                const int p = find_mass(n, g, want);
-                total = g + mass_to(p);
-                if (tid == 0) sm.mk.cut = cut_at(p);
-                n_kept = p + 1;
+                if (small) {
+                  tell(1, lrank > 0 && g + lcum >= want && g + lcum - lmass < want, g);
+                } else {
+                  const int p = find_mass(n, g, want);
+                  total = g + mass_to(p);
+                  cut = cut_at(p);
+                  n_kept = p + 1;
+                }
+                if (tid == 0) sm.mk.cut = cut;
               } else {
                 const bool later = want > g;
                 const u64 at = later ? g + lall : g;
@@ -793,19 +886,27 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
       }
     }
     if (list && rank == 0) {
-      if (min_p > 0.f) {
-        const unsigned mk = min_p_key(zmax, temp, min_p);
-        if (tid == 0) sm.pick2 = 0;
-        __syncthreads();
-        for (int p = tid; p < n_kept; p += NT)
-          if ((unsigned)(sm.cand[p] >> 32) >= mk) atomicMax(&sm.pick2, p);
-        __syncthreads();
-        n_kept = sm.pick2 + 1;
-        __syncthreads();
-        total = mass_to(n_kept - 1);
+      const unsigned mk = min_p > 0.f ? min_p_key(zmax, temp, min_p) : 0u;
+      if (small) {
+        if (min_p > 0.f) {
+          if (lrank > 0 && lrank <= n_kept && (unsigned)(lkey >> 32) >= mk) atomicMax(&sm.pick2, lrank);
+          __syncthreads();
+          tell(2, lrank > 0 && lrank == sm.pick2, 0);
+        }
+      } else {
+        if (min_p > 0.f) {
+          if (tid == 0) sm.pick2 = 0;
+          __syncthreads();
+          for (int p = tid; p < n_kept; p += NT)
+            if ((unsigned)(sm.cand[p] >> 32) >= mk) atomicMax(&sm.pick2, p);
+          __syncthreads();
+          n_kept = sm.pick2 + 1;
+          __syncthreads();
+          total = mass_to(n_kept - 1);
+        }
+        cut = cut_at(n_kept - 1);
+        __syncthreads();  // the list is reordered below
       }
-      cut = cut_at(n_kept - 1);
-      __syncthreads();  // the list is reordered below
     }
   }
   if (!list && !empty && !greedy && min_p > 0.f) {
@@ -857,29 +958,56 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     return (double)u * (double)total < (double)x_mass;
   };
   auto threshold = [&](u64 sum) { return (u64)((double)fminf(fmaxf(a.u[seq], 0.f), 0.99999994f) * (double)sum); };
-  auto finish = [&](int token, bool pass) {  // one thread of the cluster
-    if (verify) {
-      a.rowout[row] = make_int2(pass, token);
-    } else {
-      a.token[row] = token;
-      if (a.prob)
-        a.prob[row] = token < 0 ? 0.f : mass_f32(ld(z_row + token), sc) * (float)(4398046511104.0 / (double)total);
+  // One warp of the cluster ends the row; of a verified sequence's rows, the
+  // last to end joins them.
+  auto finish = [&](int token, bool pass) {
+    if (!verify) {
+      if (lane == 0) {
+        a.token[row] = token;
+        if (a.prob)
+          a.prob[row] = token < 0 ? 0.f : mass_f32(ld(z_row + token), sc) * (float)(4398046511104.0 / (double)total);
+      }
+      return;
     }
+    if (!a.arrived) {
+      if (lane == 0) a.rowout[row] = make_int2(pass, token);
+      return;
+    }
+    int last = 0;
+    if (lane == 0) {
+      a.rowout[row] = make_int2(pass, token);
+      __threadfence();
+      last = atomicAdd(a.arrived + seq, 1) == nd;
+      if (last) a.arrived[seq] = 0;
+      __threadfence();
+    }
+    if (__shfl_sync(0xffffffffu, last, 0)) join_rows(a, seq, nd);
   };
   if (empty) {
-    if (rank == 0 && tid == 0) finish(-1, false);
+    if (rank == 0 && warp == 0) finish(-1, false);
     return;
   }
   if (greedy) {
-    if (rank == 0 && tid == 0) {
-      const bool pass = verify && i < nd && x == cut.id;
-      finish(cut.id, pass);
-    }
+    if (rank == 0 && warp == 0) finish(cut.id, verify && i < nd && x == cut.id);
     return;
   }
   if (list) {
     const bool pass = verify && i < nd && passes();
-    if (!pass) {
+    if (!pass && small) {
+      // the running mass in id order at this thread's token
+      const u64 e = lrank > 0 && lrank <= n_kept && (int)~(unsigned)lkey != x ? lmass : 0ull;
+      const int n = (int)sm.ncand;
+      if (tid < n) sm.radix[tid] = e;
+      __syncthreads();
+      if (e) {
+        u64 c = 0;
+        for (int j = 0; j < n; ++j)
+          if ((unsigned)sm.cand[j] >= (unsigned)lkey) c += sm.radix[j];
+        const u64 t = threshold(total - x_mass);
+        if (c - e <= t && t < c) sm.pick = (int)~(unsigned)lkey;
+      }
+      __syncthreads();
+    } else if (!pass) {
       // the kept tokens in id order, and the first whose running mass exceeds the draw
       for (int p = tid; p < n_kept; p += NT) {
         const u64 v = sm.cand[p];
@@ -906,7 +1034,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
       }
       __syncthreads();
     }
-    if (tid == 0) finish(pass ? -1 : sm.pick, pass);
+    if (warp == 0) finish(pass ? -1 : sm.pick, pass);
     return;
   }
   // no list: masses by warp, each a contiguous range of the slice's groups
@@ -945,7 +1073,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
   total = rest + x_mass;
   const bool pass = verify && i < nd && passes();
   if (pass || rest == 0) {
-    if (rank == 0 && tid == 0) finish(-1, pass);
+    if (rank == 0 && warp == 0) finish(-1, pass);
     return;
   }
   const u64 t = threshold(rest);
@@ -965,42 +1093,17 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     const u64 step_sum = __shfl_sync(0xffffffffu, inc, 31);
     if (t < c + step_sum) {
       u64 d = c + inc - sum;
+      int token = -1;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (d <= t && t < d + e[j]) finish(s.first + 4 * (q0 + lane) + j, false);
+        if (d <= t && t < d + e[j]) token = s.first + 4 * (q0 + lane) + j;
         d += e[j];
       }
+      const unsigned m = __ballot_sync(0xffffffffu, token >= 0);
+      finish(__shfl_sync(0xffffffffu, token, __ffs(m) - 1), false);
       return;
     }
     c += step_sum;
-  }
-}
-
-// The accepted prefix of each sequence, its emitted tokens and the counters.
-__global__ void verify_rows_kernel(SamplingArgs a) {
-  pdl_launch_next();
-  pdl_wait();
-  const int s = blockIdx.x * blockDim.x + threadIdx.x;
-  if (s >= a.batch) return;
-  const int B = a.rows, D = B - 1;
-  const int nd = a.n_draft ? min(max(a.n_draft[s], 0), D) : D;
-  const int2* ro = a.rowout + (size_t)s * B;
-  int n = 0;
-  while (n < nd && ro[n].x) ++n;
-  const int tok = ro[n].y;
-  for (int i = 0; i < B; ++i) a.out_tok[(size_t)s * B + i] = i < n ? a.path[(size_t)s * D + i] : (i == n ? tok : -1);
-  a.accept_len[s] = n;
-  a.n_out[s] = n + 1;
-  a.next_anchor[s] = tok;
-  if (a.seq_len) a.seq_len[s] += n + 1;
-  if (a.counters) {
-    u64* c = reinterpret_cast<u64*>(a.counters);
-    atomicAdd(c + 0, 1ull);
-    atomicAdd(c + 1, (u64)nd);
-    atomicAdd(c + 2, (u64)n);
-    atomicAdd(c + 3, (u64)(nd - n));
-    atomicAdd(c + 4 + n, 1ull);
-    for (int i = 0; i < n; ++i) atomicAdd(c + 4 + B + i, 1ull);
   }
 }
 
@@ -1035,9 +1138,9 @@ int launch_rows(SamplingArgs a, const Ctx& c) {
 }  // namespace
 
 int launch_sampling(const SamplingArgs& a, const Ctx& c) {
-  const int k = a.bf16_logits ? launch_rows<bf16>(a, c) : launch_rows<float>(a, c);
-  if (k != DFLASH2_OK || a.kind != SAMPLING_VERIFY) return k;
-  return launch_k(verify_rows_kernel, dim3((a.batch + 127) / 128), dim3(128), 0, c, a);
+  const int rc = a.bf16_logits ? launch_rows<bf16>(a, c) : launch_rows<float>(a, c);
+  if (rc != DFLASH2_OK || a.kind != SAMPLING_VERIFY || a.arrived) return rc;
+  return launch_k(join_kernel, dim3((a.batch + 3) / 4), dim3(128), 0, c, a);
 }
 
 }  // namespace df2

@@ -520,7 +520,8 @@ int dflash2_target_probs(int dtype, int batch, int rows, int vocab, const void *
  *   u_sample   [batch] float, the draw of the emitted token
  * Outputs, seq_len and counters as dflash2_verify_accept_ex.  The workspace
  * needs dflash2_verify_logits_workspace bytes (0 for bad sizes; host only),
- * 16-byte aligned, and serves one call at a time.
+ * 16-byte aligned and zeroed once before its first use; it serves one call at
+ * a time, of any batch and block size that fit.
  */
 size_t dflash2_verify_logits_workspace(int batch, int block_size);
 int dflash2_verify_logits(int dtype, int batch, int block_size, int vocab, const int32_t *path,

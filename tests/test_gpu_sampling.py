@@ -378,6 +378,35 @@ def test_greedy_is_verify_accept_of_the_largest_logits():
         np.testing.assert_array_equal(x, y.cpu().numpy())
 
 
+def test_one_workspace_serves_calls_of_any_size():
+    """Batches around the size from which the rows are joined by a kernel of
+    their own, and block sizes in any order, on one workspace."""
+    import torch
+    B = lib()
+    ws = torch.zeros(B.dflash2_verify_logits_workspace(600, 32), dtype=torch.uint8, device="cuda")
+    for b, B_ in ((2, 32), (257, 2), (256, 3), (600, 5), (1, 2), (255, 8), (7, 32), (300, 4)):
+        z, zv, path, ua, u = verify_inputs(b, B_, 37, "peaked", b + B_)
+        nd = np.random.default_rng(b).integers(0, B_, b).astype(np.int32)
+        got = run_verify(B, z, path, nd, settings_of(b, (1.0, 5, 0.95, None)), ua, u, ws=ws)
+        check_verify(got, zv, path, nd, lambda s: (1.0, 5, float(np.float32(0.95)), 0.0), ua, u)
+
+
+@pytest.mark.parametrize("n", [255, 256, 257, 300, 1000, 2047, 2048])
+@pytest.mark.parametrize("p,m", [(None, None), (0.8, None), (0.8, 0.3), (None, 0.3)])
+def test_lists_around_their_sizes(n, p, m):
+    """Kept sets around the list that is ranked, the one that is sorted and the
+    largest one, draws and drafts among them."""
+    B = lib()
+    V, b, B_ = 7001, 5, 2
+    z, zv, path, ua, u = verify_inputs(b, B_, V, "normal", n, agree=0.5)
+    spec = (0.7, n, p, m)
+    got = run_probs(B, z, settings_of(b, spec)).cpu().numpy()
+    for s in range(b):
+        for i in range(B_):
+            check_probs(got[s, i], R.masses(zv[s, i], *plain(spec)))
+    check_verify(run_verify(B, z, path, None, settings_of(b, spec), ua, u), zv, path, None, lambda s: plain(spec), ua, u)
+
+
 @pytest.mark.parametrize("spec", [(1.0, 20, 0.95, None), (0.8, None, 0.9, 0.01)], ids=str)
 def test_verify_logits_is_target_probs_then_verify_sampled(spec):
     import torch
