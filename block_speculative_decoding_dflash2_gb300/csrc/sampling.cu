@@ -79,13 +79,10 @@ __device__ const ExpTab c_exp = {
 struct Scale {
   float zmax, hi, lo;
 };
-__device__ __forceinline__ Scale make_scale(float zmax, float T) {
-  const double c = 1.4426950408889634074 / (double)T;
-  Scale s;
-  s.zmax = zmax;
-  s.hi = (float)c;
-  s.lo = (float)(c - (double)s.hi);
-  return s;
+// x as a float pair.
+__device__ __forceinline__ float2 pair_of(double x) {
+  const float h = (float)x;
+  return make_float2(h, (float)(x - (double)h));
 }
 
 // exp((z - zmax) / T) in units of 2^-42, for z > -inf.  With y = (zmax - z)
@@ -189,6 +186,7 @@ struct Smem {
   float xmax[CMAX], xmin[CMAX];
   int xid[CMAX];
   float fsum[NW];
+  float2 c_pair, off_pair;  // log2(e) / T and T ln(min_p)
   Decision mk;      // first CTA: the next decision
   Decision dec[2];  // the last one received, two turns
   struct {
@@ -360,19 +358,25 @@ __device__ Cut select_slow(const T* row, int V, const Scale& s, Cut c, bool by_c
   return out;
 }
 
-// The smallest number of mass units that holds `p` of `total`.
+// floor(u total) and ceil(p total), exactly, for u and p in [0, 1) (in units
+// of 2^-64: below 2^-41 a float's last bits are dropped).
+__device__ __forceinline__ u64 units(float u) { return (u64)(fminf(fmaxf(u, 0.f), 0.99999994f) * 18446744073709551616.f); }
+__device__ __forceinline__ u64 floor_share(float u, u64 total) { return __umul64hi(units(u), total); }
 __device__ __forceinline__ u64 share_of(float p, u64 total) {
-  const double want = (double)p * (double)total;
-  const u64 t = want > 0.0 ? (u64)ceil(want) : 1ull;
+  const u64 q = units(p);
+  const u64 t = __umul64hi(q, total) + (q * total != 0);
   return min(max(t, 1ull), total);
 }
 
-// The cut of min_p: max z + T ln(min_p), as the smallest float not below it.
-__device__ __forceinline__ unsigned min_p_key(float zmax, float temp, float min_p) {
-  const double zt = (double)zmax + (double)temp * log((double)min_p);
-  float zf = (float)zt;
-  if ((double)zf < zt) zf = nextafterf(zf, INFINITY);
-  return okey(fminf(zf, zmax));
+// The cut of min_p: max z + T ln(min_p), the second term as a pair, as the
+// smallest float not below it.
+__device__ __forceinline__ unsigned min_p_key(float zmax, float2 off) {
+  const float t = zmax + off.x, bb = t - zmax;
+  const float r = ((zmax - (t - bb)) + (off.x - bb)) + off.y;  // t + r: the exact sum to 2^-48
+  if (!(fabsf(t) < INFINITY)) return okey(fminf(t, zmax));
+  float f = t + r;
+  if (f - t < r) f = nextafterf(f, INFINITY);
+  return okey(fminf(f, zmax));
 }
 
 // The accepted prefix of a sequence, its emitted tokens and the counters, by
@@ -429,6 +433,9 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
   const int top_k = a.top_k ? a.top_k[seq] : 0;
   const float top_p = a.top_p ? a.top_p[seq] : 1.f, min_p = a.min_p ? a.min_p[seq] : 0.f;
   const bool greedy = !(temp > 0.f);
+  // (64-bit floats are slow here: one lane each, while the logits load)
+  if (tid == 64) sm.c_pair = pair_of(1.4426950408889634074 / (greedy ? 1.0 : (double)temp));
+  if (tid == 96 && min_p > 0.f) sm.off_pair = pair_of((double)temp * log((double)min_p));
 
   // ---- 1. the slice into shared memory, its largest and smallest logit
   Slice<T, RES> s;
@@ -507,7 +514,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     zmax = fmaxf(zmax, sm.xmax[r]);
     zmin = fminf(zmin, sm.xmin[r]);
   }
-  const Scale sc = make_scale(zmax, greedy ? 1.f : temp);
+  const Scale sc = {zmax, sm.c_pair.x, sm.c_pair.y};
   const bool empty = !(zmax > -INFINITY);
 
   Cut cut = {KEY_NINF + 1, V};  // everything above -inf
@@ -859,7 +866,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
                 const bool later = want > g;
                 const u64 at = later ? g + lall : g;
                 want_f = sm.ecum[later ? hi + 1 : lo] +
-                         (float)(((double)want - (double)at) * (1.0 / 4398046511104.0));
+                         (float)((long long)want - (long long)at) * (1.f / 4398046511104.f);
                 if (later) lo_least = hi + 1;
                 else hi_most = lo - 1;
                 slow = lo_least > hi_most;
@@ -886,7 +893,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
       }
     }
     if (list && rank == 0) {
-      const unsigned mk = min_p > 0.f ? min_p_key(zmax, temp, min_p) : 0u;
+      const unsigned mk = min_p > 0.f ? min_p_key(zmax, sm.off_pair) : 0u;
       if (small) {
         if (min_p > 0.f) {
           if (lrank > 0 && lrank <= n_kept && (unsigned)(lkey >> 32) >= mk) atomicMax(&sm.pick2, lrank);
@@ -910,7 +917,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     }
   }
   if (!list && !empty && !greedy && min_p > 0.f) {
-    const unsigned mk = min_p_key(zmax, temp, min_p);
+    const unsigned mk = min_p_key(zmax, sm.off_pair);
     if (mk > cut.key) {
       cut = {mk, V};
       total = 0;
@@ -933,7 +940,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
       total = mass_kept();
     }
     float* p = a.prob + (size_t)row * V;
-    const float inv = empty ? 0.f : (float)(4398046511104.0 / (double)total);
+    const float inv = empty ? 0.f : 4398046511104.f / (float)total;
     for (int q = tid; q < 4 * s.groups; q += NT) {
       const int id = s.first + q;
       if (id < s.begin || id >= s.end) continue;
@@ -954,10 +961,9 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     }
   }
   auto passes = [&]() {
-    const float u = fminf(fmaxf(a.u_accept[(size_t)seq * (a.rows - 1) + i], 0.f), 0.99999994f);
-    return (double)u * (double)total < (double)x_mass;
+    return floor_share(a.u_accept[(size_t)seq * (a.rows - 1) + i], total) < x_mass;
   };
-  auto threshold = [&](u64 sum) { return (u64)((double)fminf(fmaxf(a.u[seq], 0.f), 0.99999994f) * (double)sum); };
+  auto threshold = [&](u64 sum) { return floor_share(a.u[seq], sum); };
   // One warp of the cluster ends the row; of a verified sequence's rows, the
   // last to end joins them.
   auto finish = [&](int token, bool pass) {
@@ -965,7 +971,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
       if (lane == 0) {
         a.token[row] = token;
         if (a.prob)
-          a.prob[row] = token < 0 ? 0.f : mass_f32(ld(z_row + token), sc) * (float)(4398046511104.0 / (double)total);
+          a.prob[row] = token < 0 ? 0.f : mass_f32(ld(z_row + token), sc) * 4398046511104.f / (float)total;
       }
       return;
     }
