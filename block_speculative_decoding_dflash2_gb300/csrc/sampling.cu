@@ -35,7 +35,9 @@ constexpr int NB = 1024;    // bins of a row's histogram
 constexpr int CAP = 2048;   // tokens of a list
 constexpr int SMALL = 256;  // tokens of a list that is ranked instead of sorted
 constexpr int CMAX = 8;     // CTAs of a row's cluster
-constexpr int SLICE2 = 20480, SLICE1 = 50000;  // logits a CTA holds, two CTAs and one CTA an SM
+constexpr int LOCAL_K = 128;  // largest top-k whose tokens each CTA picks on its own
+constexpr int SUB = NT;       // finer bins of a list
+constexpr int SLICE2 = 19456, SLICE1 = 48000;  // logits a CTA holds, two CTAs and one CTA an SM
 constexpr unsigned KEY_NINF = 0x007fffffu;  // order of -inf; NaN maps to 0
 
 // Order-preserving map of a logit (a larger one has a larger key; -0 equals 0).
@@ -48,32 +50,28 @@ __device__ __forceinline__ float okey_value(unsigned k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-// 2^(-j/32) for j = -16..16, in units of 2^-42 and as a float pair (the
-// table's values are those powers rounded from 50 decimal digits).
+// 2^(-j/32) for j = 0..31, in units of 2^-42 and as a float pair (the powers
+// rounded from 50 decimal digits).
 struct ExpTab {
-  long long fix[33];
-  float hi[33], lo[33];
+  u64 fix[32];
+  float2 pair[32];
 };
 __device__ const ExpTab c_exp = {
-    {6219777023951ll, 6086500028053ll, 5956078883349ll, 5828452394836ll, 5703560678795ll,
-     5581345134690ll, 5461748417677ll, 5344714411690ll, 5230188203118ll, 5118116055032ll,
-     5008445381977ll, 4901124725294ll, 4796103728980ll, 4693333116055ll, 4592764665442ll,
-     4494351189345ll, 4398046511104ll, 4303805443529ll, 4211583767698ll, 4121338212211ll,
-     4033026432885ll, 3946606992882ll, 3862039343274ll, 3779283804012ll, 3698301545306ll,
-     3619054569413ll, 3541505692798ll, 3465618528697ll, 3391357470036ll, 3318687672730ll,
-     3247575039328ll, 3177986203020ll, 3109888511975ll},
-    {0x1.6a09e60000000p+0f, 0x1.6247ec0000000p+0f, 0x1.5ab07e0000000p+0f, 0x1.5342b60000000p+0f, 0x1.4bfdae0000000p+0f, 0x1.44e0860000000p+0f,
-     0x1.3dea640000000p+0f, 0x1.371a740000000p+0f, 0x1.306fe00000000p+0f, 0x1.29e9e00000000p+0f, 0x1.2387a60000000p+0f, 0x1.1d48740000000p+0f,
-     0x1.172b840000000p+0f, 0x1.11301e0000000p+0f, 0x1.0b55860000000p+0f, 0x1.059b0e0000000p+0f, 0x1.0000000000000p+0f, 0x1.f507660000000p-1f,
-     0x1.ea4afa0000000p-1f, 0x1.dfc9740000000p-1f, 0x1.d5818e0000000p-1f, 0x1.cb720e0000000p-1f, 0x1.c199be0000000p-1f, 0x1.b7f7700000000p-1f,
-     0x1.ae89fa0000000p-1f, 0x1.a5503c0000000p-1f, 0x1.9c49180000000p-1f, 0x1.93737c0000000p-1f, 0x1.8ace540000000p-1f, 0x1.82589a0000000p-1f,
-     0x1.7a11480000000p-1f, 0x1.71f75e0000000p-1f, 0x1.6a09e60000000p-1f},
-    {0x1.9fcef40000000p-26f, -0x1.f8b5500000000p-25f, -0x1.5bd5ec0000000p-27f, -0x1.2c56100000000p-25f, -0x1.593abc0000000p-25f, 0x1.8624b40000000p-30f,
-     0x1.8246840000000p-25f, -0x1.18aac60000000p-25f, 0x1.4636e20000000p-25f, -0x1.5c04240000000p-25f, 0x1.ceac480000000p-25f, -0x1.d2e8ca0000000p-25f,
-     -0x1.c157420000000p-27f, -0x1.fdb4960000000p-25f, 0x1.9f31220000000p-25f, -0x1.9d4f520000000p-25f, 0x0.0p+0f, -0x1.246eb00000000p-27f,
-     0x1.52486c0000000p-28f, -0x1.908c940000000p-26f, -0x1.822dbc0000000p-28f, -0x1.8837cc0000000p-28f, -0x1.3d56b20000000p-28f, -0x1.a094380000000p-26f,
-     -0x1.a94b140000000p-27f, -0x1.b83b540000000p-26f, 0x1.51f8480000000p-28f, -0x1.e647440000000p-26f, 0x1.15506e0000000p-28f, -0x1.accc7c0000000p-27f,
-     -0x1.829fd00000000p-26f, 0x1.1d8bee0000000p-26f, 0x1.9fcef40000000p-27f}};
+    {4398046511104ull, 4303805443529ull, 4211583767698ull, 4121338212211ull, 4033026432885ull,
+     3946606992882ull, 3862039343274ull, 3779283804012ull, 3698301545306ull, 3619054569413ull,
+     3541505692798ull, 3465618528697ull, 3391357470036ull, 3318687672730ull, 3247575039328ull,
+     3177986203020ull, 3109888511975ull, 3043250014027ull, 2978039441675ull, 2914226197418ull,
+     2851780339397ull, 2790672567345ull, 2730874208839ull, 2672357205845ull, 2615094101559ull,
+     2559058027516ull, 2504222690988ull, 2450562362647ull, 2398051864490ull, 2346666558027ull,
+     2296382332721ull, 2247175594673ull},
+    {{0x1p+0f, 0x0p+0f}, {0x1.f50766p-1f, -0x1.246ebp-27f}, {0x1.ea4afap-1f, 0x1.52486cp-28f}, {0x1.dfc974p-1f, -0x1.908c94p-26f},
+     {0x1.d5818ep-1f, -0x1.822dbcp-28f}, {0x1.cb720ep-1f, -0x1.8837ccp-28f}, {0x1.c199bep-1f, -0x1.3d56b2p-28f}, {0x1.b7f77p-1f, -0x1.a09438p-26f},
+     {0x1.ae89fap-1f, -0x1.a94b14p-27f}, {0x1.a5503cp-1f, -0x1.b83b54p-26f}, {0x1.9c4918p-1f, 0x1.51f848p-28f}, {0x1.93737cp-1f, -0x1.e64744p-26f},
+     {0x1.8ace54p-1f, 0x1.15506ep-28f}, {0x1.82589ap-1f, -0x1.accc7cp-27f}, {0x1.7a1148p-1f, -0x1.829fdp-26f}, {0x1.71f75ep-1f, 0x1.1d8beep-26f},
+     {0x1.6a09e6p-1f, 0x1.9fcef4p-27f}, {0x1.6247ecp-1f, -0x1.f8b55p-26f}, {0x1.5ab07ep-1f, -0x1.5bd5ecp-28f}, {0x1.5342b6p-1f, -0x1.2c561p-26f},
+     {0x1.4bfdaep-1f, -0x1.593abcp-26f}, {0x1.44e086p-1f, 0x1.8624b4p-31f}, {0x1.3dea64p-1f, 0x1.824684p-26f}, {0x1.371a74p-1f, -0x1.18aac6p-26f},
+     {0x1.306fep-1f, 0x1.4636e2p-26f}, {0x1.29e9ep-1f, -0x1.5c0424p-26f}, {0x1.2387a6p-1f, 0x1.ceac48p-26f}, {0x1.1d4874p-1f, -0x1.d2e8cap-26f},
+     {0x1.172b84p-1f, -0x1.c15742p-28f}, {0x1.11301ep-1f, -0x1.fdb496p-26f}, {0x1.0b5586p-1f, 0x1.9f3122p-26f}, {0x1.059b0ep-1f, -0x1.9d4f52p-26f}}};
 
 // The row's exponent scale log2(e) / T as a float pair.
 struct Scale {
@@ -85,10 +83,11 @@ __device__ __forceinline__ float2 pair_of(double x) {
   return make_float2(h, (float)(x - (double)h));
 }
 
-// exp((z - zmax) / T) in units of 2^-42, for z > -inf.  With y = (zmax - z)
-// log2(e) / T held as p + e (the difference exact by two-sum, the product by
-// fma), y = n + j/32 + g + e, |g| <= 1/64, and 2^-(g+e) = 1 - (g + e) ln 2 +
-// ..., whose linear term keeps its rounding error.
+// exp((z - zmax) / T) in units of 2^-42, for z > -inf.  y = (zmax - z) log2(e)
+// / T is held as p + e (the difference exact by two-sum, the product by fma).
+// From y = 16 on, an fp32 exponential is good to 2^-38 of the largest mass.
+// Before, y = n + j/32 + g + e with |g| <= 1/64, and 2^-(g+e) = 1 - w + w^2/2 -
+// ... with w = (g + e) ln 2, whose linear term keeps its rounding error.
 __device__ __forceinline__ u64 mass_of(float z, const Scale& s, const ExpTab& tab) {
   if (z == s.zmax || s.hi == 0.f) return 1ull << 42;
   const float dh = s.zmax - z;
@@ -96,24 +95,27 @@ __device__ __forceinline__ u64 mass_of(float z, const Scale& s, const ExpTab& ta
   if (!(p < 44.f)) return 0ull;
   const float bb = dh - s.zmax;
   const float dl = (s.zmax - (dh - bb)) - (z + bb);
-  float e = fmaf(dh, s.hi, -p);
-  e = fmaf(dh, s.lo, e);
-  e = fmaf(dl, s.hi, e);
-  const float n = rintf(p), r = p - n;
-  const float jf = rintf(r * 32.f), g = fmaf(jf, -0.03125f, r);
-  const int j = (int)jf + 16;
   const float L1 = 0.693147182464599609f, L1lo = -1.90465429995776e-9f;  // ln 2
+  const float e = fmaf(dl, s.hi, fmaf(dh, s.lo, fmaf(dh, s.hi, -p)));
+  if (p >= 16.f) {
+    float f;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(42.f - p));
+    return (u64)__float2uint_rn(fmaf(f, -L1 * e, f));
+  }
+  const float kf = fmaf(p, 32.f, 12582912.f);  // 1.5 2^23: rounds to a whole number of 32nds
+  const unsigned k = __float_as_uint(kf);
+  const float g = fmaf(kf - 12582912.f, -0.03125f, p);
   const float gl = __fmul_rn(g, L1);
   const float glr = fmaf(g, L1lo, fmaf(e, L1, fmaf(g, L1, -gl)));
-  const float x = (g + e) * L1;
-  const float q = x * x * fmaf(x, fmaf(x, 0.0416666667f, -0.1666666667f), 0.5f) - glr;  // 2^-(g+e) - 1 + gl
-  const float th = tab.hi[j], tl = tab.lo[j];
-  const float m = __fmul_rn(th, gl);
-  const float small = fmaf(th, q, -fmaf(th, gl, -m)) - tl * gl;
-  const long long v = tab.fix[j] - ((long long)__float2int_rn(m * 68719476736.f) << 6) +
-                      (long long)__float2int_rn(small * 4398046511104.f);
-  const int sh = (int)n;  // 0..44
-  return sh == 0 ? (u64)v : ((u64)v + (1ull << (sh - 1))) >> sh;
+  const float w = (g + e) * L1;
+  const float q = w * w * fmaf(w, fmaf(w, 0.0416666667f, -0.1666666667f), 0.5f) - glr;  // 2^-(g+e) - 1 + gl
+  const float2 t = tab.pair[k & 31];
+  const float m = __fmul_rn(t.x, gl);
+  const float small = fmaf(t.x, q, -fmaf(t.x, gl, -m)) - t.y * gl;
+  const u64 v = tab.fix[k & 31] - (u64)((long long)__float2int_rn(m * 68719476736.f) << 6) +
+                (u64)(long long)__float2int_rn(small * 4398046511104.f);
+  const int n = (k >> 5) & 31;  // 0..16
+  return (v + ((1ull << n) >> 1)) >> n;
 }
 
 // The same to fp32 accuracy relative to the mass, however small.
@@ -125,7 +127,7 @@ __device__ __forceinline__ float mass_f32(float z, const Scale& s) {
   float e = fmaf(dh, s.hi, -p);
   e = fmaf(dh, s.lo, e);
   e = fmaf(dl, s.hi, e);
-  const float f = exp2f(-p);
+  const float f = exp2f(-p);  // (below 2^-126 a subnormal: the sum of a row is at least 1)
   return fmaf(f, -0.693147182f * e, f);
 }
 
@@ -154,6 +156,10 @@ __device__ __forceinline__ unsigned add_cl(uint32_t addr, unsigned v) {
   return o;
 }
 
+// The two halves of cluster_sync (every thread of the cluster, in turn).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 // The kept prefix of a row's order: every token with (key, id) ahead of or
 // equal to (key, id) here.
 struct Cut {
@@ -163,6 +169,9 @@ struct Cut {
 __device__ __forceinline__ bool kept(unsigned k, int id, const Cut& c) {
   return k > c.key || (k == c.key && id <= c.id);
 }
+
+// The same on a logit, `zc` being the value of the cut's key.
+__device__ __forceinline__ bool kept_z(float z, int id, float zc, int idc) { return z > zc || (z == zc && id <= idc); }
 
 // What the cluster's first CTA decides for the others.
 enum { STEP_NONE = 0, STEP_LIST = 1, STEP_TOPK = 2, STEP_TOPP = 3, STEP_SLOW_K = 4, STEP_SLOW_P = 5 };
@@ -180,12 +189,13 @@ struct Smem {
   u64 cand[CAP];  // first CTA: gathered tokens, (key, ~id)
   float ecum[NB + 1];  // first CTA: estimated mass ahead of each bin
   unsigned hist[NB];
-  u64 radix[256];
+  u64 radix[SMALL];
+  u64 sub[SUB];  // first CTA: masses of a list's finer bins
   u64 wsum[NW];
   u64 xm[2][CMAX], xg[2][CMAX];  // exchanged masses, two turns
-  float xmax[CMAX], xmin[CMAX];
+  float xmax[CMAX], xmin[CMAX], xlow[CMAX];
   int xid[CMAX];
-  float fsum[NW];
+  float fsum[NW], fmin[NW];
   float2 c_pair, off_pair;  // log2(e) / T and T ln(min_p)
   Decision mk;      // first CTA: the next decision
   Decision dec[2];  // the last one received, two turns
@@ -299,6 +309,38 @@ __device__ __forceinline__ void for_each(const S& s, F f) {
     const int id = s.first + 4 * i;
     f(v.x, id), f(v.y, id + 1), f(v.z, id + 2), f(v.w, id + 3);
   }
+}
+
+// Calls f(four logits, id of the first) on every group of the slice.
+template <typename S, typename F>
+__device__ __forceinline__ void for_each4(const S& s, F f) {
+  for (int i0 = 0; i0 < s.groups; i0 += NT) {
+    const int i = i0 + threadIdx.x;
+    f(i < s.groups ? s.get4(i) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY), s.first + 4 * i);
+  }
+}
+
+// Appends the logits for which in(z) holds, none of them below `low`, to a
+// list: `counter` is this CTA's, `base` the first CTA's list or this CTA's
+// part of it, which takes `most`.
+template <typename S, typename F>
+__device__ __forceinline__ void collect(const S& s, float low, F in, uint32_t counter, uint32_t base, unsigned most) {
+  const int lane = threadIdx.x & 31;
+  for_each4(s, [&](const float4& v, int id) {
+    if (!__any_sync(0xffffffffu, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) >= low)) return;
+    const float zz[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool yes = zz[j] >= low && zz[j] > -INFINITY && in(zz[j]);
+      const unsigned m = __ballot_sync(0xffffffffu, yes);
+      if (m) {
+        unsigned at = 0;
+        if (lane == 0) at = add_cl(counter, __popc(m));
+        at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1));
+        if (yes && at < most) st_cl(base + 8 * at, ((u64)okey(zz[j]) << 32) | (unsigned)~(id + j));
+      }
+    }
+  });
 }
 
 // The first token of the order, among those kept by `c`, at which the running
@@ -425,6 +467,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     if (a.n_draft) nd = min(max(a.n_draft[seq], 0), nd);
     if (i > nd) return;  // the whole cluster
   }
+  cluster_arrive();  // waited for before the first access to another CTA's memory
   static_assert(sizeof(ExpTab) / 4 <= NT, "one word of the table a thread");
   const bool has_word = tid < (int)(sizeof(ExpTab) / 4);
   const unsigned word = has_word ? reinterpret_cast<const unsigned*>(&c_exp)[tid] : 0u;
@@ -492,27 +535,76 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     sm.pick = -1;
     sm.pick2 = 0x7fffffff;
   }
+  const float thread_max = mx;
   mx = warp_max(mx);
   mn = -warp_max(-mn);
   if (lane == 0) {
     sm.fsum[warp] = mx;
-    reinterpret_cast<float*>(sm.wsum)[warp] = mn;
+    sm.fmin[warp] = mn;
   }
   __syncthreads();
-  if (tid < C) {
-    float x = sm.fsum[0], y = reinterpret_cast<float*>(sm.wsum)[0];
-    for (int w = 1; w < NW; ++w) {
-      x = fmaxf(x, sm.fsum[w]);
-      y = fminf(y, reinterpret_cast<float*>(sm.wsum)[w]);
-    }
-    st_cl(dsmem_addr(&sm.xmax[rank], tid), __float_as_uint(x));
-    st_cl(dsmem_addr(&sm.xmin[rank], tid), __float_as_uint(y));
+  for (int w = 0; w < NW; ++w) {
+    mx = fmaxf(mx, sm.fsum[w]);
+    mn = fminf(mn, sm.fmin[w]);
   }
-  cluster_sync();
-  float zmin = INFINITY, zmax = -INFINITY;
-  for (int r = 0; r < C; ++r) {
-    zmax = fmaxf(zmax, sm.xmax[r]);
-    zmin = fminf(zmin, sm.xmin[r]);
+  float zmax = -INFINITY, zmin = INFINITY;
+  // A small top-k: each CTA picks its own candidates.  The k-th largest of its
+  // threads' largest logits has at least k logits that are not below it, so no
+  // token of the row's top k lies below it; few others do not.
+  const bool by_k0 = !greedy && top_k > 0 && top_k < V;
+  bool local = by_k0 && top_k <= LOCAL_K;
+  if (local) {
+    const float range = fminf(mx - mn, 64.f);
+    const float per = range > 0.f ? fminf((float)SUB / range, 1e30f) : 1.f;
+    const int bin = thread_max == mx ? 0 : (int)fminf((mx - thread_max) * per, (float)(SUB - 1));
+    if (thread_max > -INFINITY) atomicAdd(&sm.hist[bin], 1u);
+    __syncthreads();
+    u64 all;
+    const unsigned c = sm.hist[tid];
+    const u64 before = block_scan_u64(c, &all, sm);
+    const bool enough = all >= (u64)top_k;
+    if (before < (u64)top_k && (u64)top_k <= before + c) sm.pick = tid;
+    __syncthreads();
+    float low = enough && thread_max > -INFINITY && bin <= sm.pick ? thread_max : INFINITY;
+    low = -warp_max(-low);
+    if (lane == 0) sm.fmin[warp] = low;
+    __syncthreads();
+    for (int w = 0; w < NW; ++w) low = fminf(low, sm.fmin[w]);
+    if (!enough) low = -3.402823466e+38f;  // fewer logits than that: all of them
+    const unsigned part = CAP / C;
+    cluster_wait();
+    collect(s, low, [](float) { return true; }, smem_u32(&sm.ncand), dsmem_addr(sm.cand + rank * part, 0), part);
+    __syncthreads();
+    if (tid < C) {
+      st_cl(dsmem_addr(&sm.xmax[rank], tid), __float_as_uint(mx));
+      st_cl(dsmem_addr(&sm.xlow[rank], tid), __float_as_uint(low));
+      st_cl(dsmem_addr(&sm.xid[rank], tid), sm.ncand);
+    }
+    cluster_sync();
+    for (int r = 0; r < C; ++r) {
+      zmax = fmaxf(zmax, sm.xmax[r]);
+      local = local && sm.xid[r] <= (int)part;
+    }
+    if (!local) {  // too many in one part: the ways below
+      for (int b = tid; b < NB; b += NT) sm.hist[b] = 0;
+      if (tid == 0) {
+        sm.ncand = 0;
+        sm.pick = -1;
+      }
+    }
+  } else {
+    cluster_wait();
+  }
+  if (!local) {
+    if (tid < C) {
+      st_cl(dsmem_addr(&sm.xmax[rank], tid), __float_as_uint(mx));
+      st_cl(dsmem_addr(&sm.xmin[rank], tid), __float_as_uint(mn));
+    }
+    cluster_sync();
+    for (int r = 0; r < C; ++r) {
+      zmax = fmaxf(zmax, sm.xmax[r]);
+      zmin = fminf(zmin, sm.xmin[r]);
+    }
   }
   const Scale sc = {zmax, sm.c_pair.x, sm.c_pair.y};
   const bool empty = !(zmax > -INFINITY);
@@ -556,8 +648,9 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
   };
   auto mass_kept = [&]() {
     u64 m = 0, g = 0;
+    const float zc = okey_value(cut.key);
     for_each(s, [&](float z, int id) {
-      if (kept(okey(z), id, cut)) m += mass_of(z, sc, sm.tab);
+      if (kept_z(z, id, zc, cut.id)) m += mass_of(z, sc, sm.tab);
     });
     exchange(m, g);
     return m;
@@ -581,68 +674,8 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
 
   // ---- 2. top-k and top-p: a histogram of the row's range finds the bins that
   // hold a border; their tokens are gathered and sorted by the first CTA
-  const bool by_k = !empty && !greedy && top_k > 0 && top_k < V, by_p = !empty && !greedy && top_p < 1.f;
+  const bool by_k = !empty && by_k0, by_p = !empty && !greedy && top_p < 1.f;
   if (by_k || by_p) {
-    // bins of equal width over [zmax - 64, zmax] or the row's own range if that
-    // is smaller; what lies lower falls into the last bin
-    const float range = fminf(zmax - zmin, 64.f);
-    const float per = range > 0.f ? fminf((float)NB / range, 1e30f) : 1.f;
-    auto bin_of = [&](float z) { return z == zmax ? 0 : (int)fminf((zmax - z) * per, (float)(NB - 1)); };
-    for_each(s, [&](float z, int) {
-      if (z > -INFINITY) atomicAdd(&sm.hist[bin_of(z)], 1u);
-    });
-    cluster_sync();
-    unsigned c2[2] = {0, 0};  // the first CTA's threads: counts of bins 2 tid, 2 tid + 1, then of those before
-    u64 n_all = 0, n_before = 0;
-    if (rank == 0) {
-      for (int r = 0; r < C; ++r) {
-        c2[0] += ld_cl(dsmem_addr(&sm.hist[2 * tid], r));
-        c2[1] += ld_cl(dsmem_addr(&sm.hist[2 * tid + 1], r));
-      }
-      n_before = block_scan_u64(c2[0] + c2[1], &n_all, sm);
-      __syncthreads();
-      sm.hist[2 * tid] = c2[0];  // from here on the row's counts
-      sm.hist[2 * tid + 1] = c2[1];
-      if (tid == 0) sm.mk.step = STEP_NONE;
-      __syncthreads();
-      if (by_k && (u64)top_k < n_all) {
-        for (int h = 0; h < 2; ++h) {
-          const u64 b0 = n_before + (h ? c2[0] : 0);
-          if (b0 < (u64)top_k && (u64)top_k <= b0 + c2[h]) {  // one thread
-            const int b = 2 * tid + h;
-            sm.mk.lo = b;
-            sm.mk.hi = b;
-            sm.mk.before = (unsigned)b0;
-            if (b0 + c2[h] <= CAP) {
-              sm.mk.lo = 0;
-              sm.mk.before = 0;
-              sm.mk.step = STEP_LIST;
-            } else {
-              sm.mk.step = c2[h] <= CAP ? STEP_TOPK : STEP_SLOW_K;
-            }
-          }
-        }
-      }
-    }
-    Decision dec = broadcast();
-    // Gathers the tokens of the decision's bins into the first CTA's list.
-    auto gather = [&](int lo, int hi) {
-      const uint32_t counter = dsmem_addr(&sm.ncand, 0), base = dsmem_addr(sm.cand, 0);
-      for_each(s, [&](float z, int id) {
-        bool in = z > -INFINITY;
-        if (in) {
-          const int b = bin_of(z);
-          in = b >= lo && b <= hi;
-        }
-        const unsigned m = __ballot_sync(0xffffffffu, in);
-        if (m) {
-          unsigned at = 0;
-          if (lane == 0) at = add_cl(counter, __popc(m));
-          at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1));
-          if (in && at < CAP) st_cl(base + 8 * at, ((u64)okey(z) << 32) | (unsigned)~id);
-        }
-      });
-    };
     auto cut_at = [&](int p) { return Cut{(unsigned)(sm.cand[p] >> 32), (int)~(unsigned)sm.cand[p]}; };
     // masses of the list in order: this thread's four, and the mass before them
     u64 lm[CAP / NT], lbefore = 0, lall = 0;
@@ -715,31 +748,111 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
       n_kept = sm.sel[slot].n;
     };
 
+    // top-k and top-p of a list that holds the row's first tokens
+    auto cut_list = [&](int n) {
+      small = n <= SMALL;
+      if (small) {
+        rank_list(n);
+        tell(0, lrank > 0 && lrank == min(top_k, n), 0);
+        if (by_p) {
+          const u64 want = share_of(top_p, total);
+          tell(1, lrank > 0 && lcum >= want && lcum - lmass < want, 0);
+        }
+      } else {
+        sort_desc(sm.cand, n);
+        scan_list(n);
+        n_kept = min(top_k, n);
+        total = mass_to(n_kept - 1);
+        if (by_p) {
+          n_kept = min(n_kept, find_mass(n, 0, share_of(top_p, total)) + 1);
+          total = mass_to(n_kept - 1);
+        }
+      }
+    };
+    if (local) {
+      list = true;
+      if (rank == 0) {
+        // the parts without what lies below any of their bounds, in one piece
+        float low = -INFINITY;
+        for (int r = 0; r < C; ++r) low = fmaxf(low, sm.xlow[r]);
+        const unsigned low_key = okey(low), part = CAP / C;
+        u64 v[CAP / NT];
+        unsigned n = 0;
+#pragma unroll
+        for (int j = 0; j < CAP / NT; ++j) {
+          const unsigned e = tid + j * NT;
+          v[j] = e % part < (unsigned)sm.xid[e / part] ? sm.cand[e] : 0ull;
+          if ((unsigned)(v[j] >> 32) < low_key) v[j] = 0;
+          n += v[j] != 0;
+        }
+        u64 all;
+        unsigned at = (unsigned)block_scan_u64(n, &all, sm);
+#pragma unroll
+        for (int j = 0; j < CAP / NT; ++j)
+          if (v[j]) sm.cand[at++] = v[j];
+        if (tid == 0) {
+          sm.ncand = (unsigned)all;
+          sm.pick = -1;
+        }
+        __syncthreads();
+        cut_list((int)all);
+      }
+    } else {
+    // bins of equal width over [zmax - 64, zmax] or the row's own range if that
+    // is smaller; what lies lower falls into the last bin
+    const float range = fminf(zmax - zmin, 64.f);
+    const float per = range > 0.f ? fminf((float)NB / range, 1e30f) : 1.f;
+    auto bin_of = [&](float z) { return z == zmax ? 0 : (int)fminf((zmax - z) * per, (float)(NB - 1)); };
+    for_each(s, [&](float z, int) {
+      if (z > -INFINITY) atomicAdd(&sm.hist[bin_of(z)], 1u);
+    });
+    cluster_sync();
+    unsigned c2[2] = {0, 0};  // the first CTA's threads: counts of bins 2 tid, 2 tid + 1, then of those before
+    u64 n_all = 0, n_before = 0;
+    if (rank == 0) {
+      for (int r = 0; r < C; ++r) {
+        c2[0] += ld_cl(dsmem_addr(&sm.hist[2 * tid], r));
+        c2[1] += ld_cl(dsmem_addr(&sm.hist[2 * tid + 1], r));
+      }
+      n_before = block_scan_u64(c2[0] + c2[1], &n_all, sm);
+      __syncthreads();
+      sm.hist[2 * tid] = c2[0];  // from here on the row's counts
+      sm.hist[2 * tid + 1] = c2[1];
+      if (tid == 0) sm.mk.step = STEP_NONE;
+      __syncthreads();
+      if (by_k && (u64)top_k < n_all) {
+        for (int h = 0; h < 2; ++h) {
+          const u64 b0 = n_before + (h ? c2[0] : 0);
+          if (b0 < (u64)top_k && (u64)top_k <= b0 + c2[h]) {  // one thread
+            const int b = 2 * tid + h;
+            sm.mk.lo = b;
+            sm.mk.hi = b;
+            sm.mk.before = (unsigned)b0;
+            if (b0 + c2[h] <= CAP) {
+              sm.mk.lo = 0;
+              sm.mk.before = 0;
+              sm.mk.step = STEP_LIST;
+            } else {
+              sm.mk.step = c2[h] <= CAP ? STEP_TOPK : STEP_SLOW_K;
+            }
+          }
+        }
+      }
+    }
+    Decision dec = broadcast();
+    // Gathers the tokens of the decision's bins into the first CTA's list.
+    auto gather = [&](int lo, int hi) {
+      // (a bound below the last bin's end, roundings included, skips most)
+      const float low = hi == NB - 1 ? -INFINITY : zmax - (float)(hi + 1) / per * 1.0001f;
+      collect(s, low, [&](float z) { const int b = bin_of(z); return b >= lo && b <= hi; },
+              dsmem_addr(&sm.ncand, 0), dsmem_addr(sm.cand, 0), CAP);
+    };
+
     if (dec.step == STEP_LIST) {
       gather(0, dec.hi);
       cluster_sync();
       list = true;
-      if (rank == 0) {
-        const int n = (int)sm.ncand;
-        small = n <= SMALL;
-        if (small) {
-          rank_list(n);
-          tell(0, lrank > 0 && lrank == min(top_k, n), 0);
-          if (by_p) {
-            const u64 want = share_of(top_p, total);
-            tell(1, lrank > 0 && lcum >= want && lcum - lmass < want, 0);
-          }
-        } else {
-          sort_desc(sm.cand, n);
-          scan_list(n);
-          n_kept = min(top_k, n);
-          total = mass_to(n_kept - 1);
-          if (by_p) {
-            n_kept = min(n_kept, find_mass(n, 0, share_of(top_p, total)) + 1);
-            total = mass_to(n_kept - 1);
-          }
-        }
-      }
+      if (rank == 0) cut_list((int)sm.ncand);
     } else {
       if (dec.step == STEP_TOPK) {
         gather(dec.lo, dec.hi);
@@ -826,8 +939,9 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
           dec = broadcast();
           const int lo = dec.lo, hi = dec.hi;
           u64 m = 0, g = 0;  // kept mass, and what of it lies ahead of the gathered bins
+          const float zc = okey_value(cut.key);
           for_each(s, [&](float z, int id) {
-            if (kept(okey(z), id, cut)) {
+            if (kept_z(z, id, zc, cut.id)) {
               const u64 e = mass_of(z, sc, sm.tab);
               m += e;
               if (bin_of(z) < lo) g += e;
@@ -840,11 +954,59 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
             bool found = false, slow = dec.step == STEP_SLOW_P;
             if (!slow) {
               const int n = (int)sm.ncand;
+              int n_list = n;
               small = n <= SMALL;
+              u64 ga = g;  // mass ahead of the part of the list that is ranked
               if (small) {
                 rank_list(n);
                 tell(0, lrank > 0 && lrank == n, 0);
                 lall = n ? total : 0ull;
+              } else if (lo > 0) {
+                // finer bins find the border's few tokens; the rest is not needed
+                const float top = zmax - (float)lo / per, fine = (float)SUB / ((float)(hi + 1 - lo) / per);
+                u64 v[CAP / NT];
+                int sb[CAP / NT];
+                sm.sub[tid] = 0;
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < CAP / NT; ++j) {
+                  const int e = tid + j * NT;
+                  v[j] = e < n ? sm.cand[e] : 0ull;
+                  const float z = okey_value((unsigned)(v[j] >> 32));
+                  sb[j] = (int)fminf(fmaxf((top - z) * fine, 0.f), (float)(SUB - 1));
+                  if (v[j]) atomicAdd(&sm.sub[sb[j]], mass_of(z, sc, sm.tab));
+                }
+                __syncthreads();
+                const u64 mine = sm.sub[tid];
+                const u64 before = block_scan_u64(mine, &lall, sm);
+                if (g + before < want && want <= g + before + mine) {
+                  sm.pick2 = tid;
+                  sm.sel_before = g + before;
+                }
+                __syncthreads();
+                if (g < want && want <= g + lall) {
+                  const int b = sm.pick2;
+                  ga = sm.sel_before;
+                  unsigned c = 0;
+#pragma unroll
+                  for (int j = 0; j < CAP / NT; ++j) c += v[j] && sb[j] == b;
+                  u64 n2;
+                  unsigned at = (unsigned)block_scan_u64(c, &n2, sm);
+#pragma unroll
+                  for (int j = 0; j < CAP / NT; ++j)
+                    if (v[j] && sb[j] == b) sm.cand[at++] = v[j];
+                  __syncthreads();
+                  small = n2 <= SMALL;
+                  if (small) {
+                    rank_list((int)n2);
+                  } else {
+                    const u64 whole = lall;
+                    sort_desc(sm.cand, (int)n2);
+                    scan_list((int)n2);
+                    lall = whole;
+                  }
+                  n_list = (int)n2;
+                }
               } else {
                 sort_desc(sm.cand, n);
                 scan_list(n);
@@ -854,10 +1016,10 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
               if (g < want && want <= g + lall) {
                 found = true;
                 if (small) {
-                  tell(1, lrank > 0 && g + lcum >= want && g + lcum - lmass < want, g);
+                  tell(1, lrank > 0 && ga + lcum >= want && ga + lcum - lmass < want, ga);
                 } else {
-                  const int p = find_mass(n, g, want);
-                  total = g + mass_to(p);
+                  const int p = find_mass(n_list, ga, want);
+                  total = ga + mass_to(p);
                   cut = cut_at(p);
                   n_kept = p + 1;
                 }
@@ -891,6 +1053,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
         total = ((u64)dec.total_hi << 32) | dec.total_lo;
         list = dec.step == STEP_LIST;
       }
+    }
     }
     if (list && rank == 0) {
       const unsigned mk = min_p > 0.f ? min_p_key(zmax, sm.off_pair) : 0u;
@@ -940,12 +1103,13 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
       total = mass_kept();
     }
     float* p = a.prob + (size_t)row * V;
+    const float zc = okey_value(cut.key);
     const float inv = empty ? 0.f : 4398046511104.f / (float)total;
     for (int q = tid; q < 4 * s.groups; q += NT) {
       const int id = s.first + q;
       if (id < s.begin || id >= s.end) continue;
       const float z = RES ? zs_buf[q] : ld(z_row + id);
-      p[id] = !empty && kept(okey(z), id, cut) ? mass_f32(z, sc) * inv : 0.f;
+      p[id] = !empty && kept_z(z, id, zc, cut.id) ? mass_f32(z, sc) * inv : 0.f;
     }
     return;
   }
@@ -1045,13 +1209,14 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
   }
   // no list: masses by warp, each a contiguous range of the slice's groups
   const int g0 = (int)((long long)s.groups * warp / NW), g1 = (int)((long long)s.groups * (warp + 1) / NW);
+  const float zc = okey_value(cut.key);
   auto mass4 = [&](int q, u64 (&e)[4]) {
     const float4 v = q < g1 ? s.get4(q) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     const float zz[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int id = s.first + 4 * q + j;
-      e[j] = id != x && kept(okey(zz[j]), id, cut) ? mass_of(zz[j], sc, sm.tab) : 0ull;
+      e[j] = id != x && kept_z(zz[j], id, zc, cut.id) ? mass_of(zz[j], sc, sm.tab) : 0ull;
     }
   };
   u64 wm = 0;
