@@ -289,7 +289,7 @@ int launch_linear_w4(const W4Op& g, const Ctx& c);
 enum { SAMPLING_TOKEN = 0, SAMPLING_PROBS = 1, SAMPLING_VERIFY = 2 };
 struct SamplingArgs {
   int kind, batch, rows, vocab;  // rows of logits per sequence; settings are per sequence
-  int cluster;                   // CTAs per row (the launcher's choice)
+  int lg_cluster;                // CTAs per row, a power of two (the launcher's choice)
   bool bf16_logits;
   const void* logits;  // [batch * rows, vocab], row stride `stride` elements
   long long stride;

@@ -35,7 +35,8 @@ constexpr int NB = 1024;    // bins of a row's histogram
 constexpr int CAP = 2048;   // tokens of a list
 constexpr int SMALL = 256;  // tokens of a list that is ranked instead of sorted
 constexpr int CMAX = 8;     // CTAs of a row's cluster
-constexpr int LOCAL_K = 128;  // largest top-k whose tokens each CTA picks on its own
+constexpr int LOCAL_K = 100;  // largest top-k whose tokens each CTA picks on its own
+constexpr int PARTS = 1024;   // room for what they pick
 constexpr int SUB = NT;       // finer bins of a list
 constexpr int SLICE2 = 19456, SLICE1 = 48000;  // logits a CTA holds, two CTAs and one CTA an SM
 constexpr unsigned KEY_NINF = 0x007fffffu;  // order of -inf; NaN maps to 0
@@ -88,34 +89,56 @@ __device__ __forceinline__ float2 pair_of(double x) {
 // From y = 16 on, an fp32 exponential is good to 2^-38 of the largest mass.
 // Before, y = n + j/32 + g + e with |g| <= 1/64, and 2^-(g+e) = 1 - w + w^2/2 -
 // ... with w = (g + e) ln 2, whose linear term keeps its rounding error.
-__device__ __forceinline__ u64 mass_of(float z, const Scale& s, const ExpTab& tab) {
-  if (z == s.zmax || s.hi == 0.f) return 1ull << 42;
-  const float dh = s.zmax - z;
-  const float p = __fmul_rn(dh, s.hi);  // never contracted: its rounding error goes to e
-  if (!(p < 44.f)) return 0ull;
-  const float bb = dh - s.zmax;
-  const float dl = (s.zmax - (dh - bb)) - (z + bb);
+// No branch depends on one value, so the N evaluations overlap; with VOTE a
+// warp whose values are all far skips the near form (same results).
+template <int N, bool VOTE>
+__device__ __forceinline__ void masses_of(const float (&z)[N], const Scale& s, const ExpTab& tab, u64 (&v)[N]) {
   const float L1 = 0.693147182464599609f, L1lo = -1.90465429995776e-9f;  // ln 2
-  const float e = fmaf(dl, s.hi, fmaf(dh, s.lo, fmaf(dh, s.hi, -p)));
-  if (p >= 16.f) {
-    float f;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(42.f - p));
-    return (u64)__float2uint_rn(fmaf(f, -L1 * e, f));
+  float p[N], e[N];
+  bool far = true;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float dh = s.zmax - z[i];
+    p[i] = __fmul_rn(dh, s.hi);  // never contracted: its rounding error goes to e
+    const float bb = dh - s.zmax;
+    const float dl = (s.zmax - (dh - bb)) - (z[i] + bb);
+    e[i] = fmaf(dl, s.hi, fmaf(dh, s.lo, fmaf(dh, s.hi, -p[i])));
+    far = far && p[i] >= 16.f;
   }
-  const float kf = fmaf(p, 32.f, 12582912.f);  // 1.5 2^23: rounds to a whole number of 32nds
-  const unsigned k = __float_as_uint(kf);
-  const float g = fmaf(kf - 12582912.f, -0.03125f, p);
-  const float gl = __fmul_rn(g, L1);
-  const float glr = fmaf(g, L1lo, fmaf(e, L1, fmaf(g, L1, -gl)));
-  const float w = (g + e) * L1;
-  const float q = w * w * fmaf(w, fmaf(w, 0.0416666667f, -0.1666666667f), 0.5f) - glr;  // 2^-(g+e) - 1 + gl
-  const float2 t = tab.pair[k & 31];
-  const float m = __fmul_rn(t.x, gl);
-  const float small = fmaf(t.x, q, -fmaf(t.x, gl, -m)) - t.y * gl;
-  const u64 v = tab.fix[k & 31] - (u64)((long long)__float2int_rn(m * 68719476736.f) << 6) +
-                (u64)(long long)__float2int_rn(small * 4398046511104.f);
-  const int n = (k >> 5) & 31;  // 0..16
-  return (v + ((1ull << n) >> 1)) >> n;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float f;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(42.f - p[i]));
+    v[i] = (u64)__float2uint_rn(fmaf(f, -L1 * e[i], f));  // (0 from y = 44 on, infinity included)
+  }
+  if (!VOTE || !__all_sync(0xffffffffu, far)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float kf = fmaf(p[i], 32.f, 12582912.f);  // 1.5 2^23: rounds to a whole number of 32nds
+      const unsigned k = __float_as_uint(kf);
+      const float g = fmaf(kf - 12582912.f, -0.03125f, p[i]);
+      const float gl = __fmul_rn(g, L1);
+      const float glr = fmaf(g, L1lo, fmaf(e[i], L1, fmaf(g, L1, -gl)));
+      const float w = (g + e[i]) * L1;
+      const float q = w * w * fmaf(w, fmaf(w, 0.0416666667f, -0.1666666667f), 0.5f) - glr;  // 2^-(g+e) - 1 + gl
+      const float2 t = tab.pair[k & 31];
+      const float m = __fmul_rn(t.x, gl);
+      const float small = fmaf(t.x, q, -fmaf(t.x, gl, -m)) - t.y * gl;
+      const u64 near = tab.fix[k & 31] - (u64)((long long)__float2int_rn(m * 68719476736.f) << 6) +
+                       (u64)(long long)__float2int_rn(small * 4398046511104.f);
+      const int n = (k >> 5) & 31;  // 0..16
+      v[i] = p[i] < 16.f ? (near + ((1ull << n) >> 1)) >> n : v[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (z[i] == s.zmax || s.hi == 0.f) v[i] = 1ull << 42;
+}
+__device__ __forceinline__ u64 mass_of(float z, const Scale& s, const ExpTab& tab) {
+  const float x[1] = {z};
+  u64 v[1];
+  masses_of<1, false>(x, s, tab, v);
+  return v[0];
 }
 
 // The same to fp32 accuracy relative to the mass, however small.
@@ -187,10 +210,15 @@ constexpr int DW = sizeof(Decision) / 4;
 struct Smem {
   ExpTab tab;     // copy of c_exp: lanes read different entries
   u64 cand[CAP];  // first CTA: gathered tokens, (key, ~id)
-  float ecum[NB + 1];  // first CTA: estimated mass ahead of each bin
   unsigned hist[NB];
   u64 radix[SMALL];
-  u64 sub[SUB];  // first CTA: masses of a list's finer bins
+  union {  // first CTA
+    u64 parts[PARTS];  // what each CTA picked on its own, for a small top-k
+    struct {
+      float ecum[NB + 1];                 // estimated mass ahead of each bin
+      unsigned sub_lo[SUB], sub_hi[SUB];  // masses of a list's finer bins: the low 21 bits, the rest
+    };
+  };
   u64 wsum[NW];
   u64 xm[2][CMAX], xg[2][CMAX];  // exchanged masses, two turns
   float xmax[CMAX], xmin[CMAX], xlow[CMAX];
@@ -204,6 +232,7 @@ struct Smem {
     Cut cut;
     int n;
   } sel[3];  // small lists: the kept tokens after top-k, top-p and min-p
+  u64 bound;
   unsigned ncand;
   unsigned sel_key;
   u64 sel_before;
@@ -245,7 +274,7 @@ __device__ __forceinline__ u64 block_scan_u64(u64 mine, u64* total, Smem& sm) {
 
 // Descending sort of the first n entries of `a` (n <= CAP, padded with zeros
 // to a power of two; every entry is above zero).
-__device__ void sort_desc(u64* a, int n) {
+__device__ __noinline__ void sort_desc(u64* a, int n) {
   int p = 32;
   while (p < n) p <<= 1;
   for (int i = n + threadIdx.x; i < p; i += NT) a[i] = 0;
@@ -320,18 +349,22 @@ __device__ __forceinline__ void for_each4(const S& s, F f) {
   }
 }
 
-// Appends the logits for which in(z) holds, none of them below `low`, to a
+// Appends the logits for which in(z) holds, all of them in [low, high], to a
 // list: `counter` is this CTA's, `base` the first CTA's list or this CTA's
 // part of it, which takes `most`.
 template <typename S, typename F>
-__device__ __forceinline__ void collect(const S& s, float low, F in, uint32_t counter, uint32_t base, unsigned most) {
+__device__ __forceinline__ void collect(const S& s, float low, float high, F in, uint32_t counter, uint32_t base,
+                                        unsigned most) {
   const int lane = threadIdx.x & 31;
   for_each4(s, [&](const float4& v, int id) {
-    if (!__any_sync(0xffffffffu, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) >= low)) return;
     const float zz[4] = {v.x, v.y, v.z, v.w};
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) any = any || (zz[j] >= low && zz[j] <= high);
+    if (!__any_sync(0xffffffffu, any)) return;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const bool yes = zz[j] >= low && zz[j] > -INFINITY && in(zz[j]);
+      const bool yes = zz[j] >= low && zz[j] <= high && zz[j] > -INFINITY && in(zz[j]);
       const unsigned m = __ballot_sync(0xffffffffu, yes);
       if (m) {
         unsigned at = 0;
@@ -349,7 +382,7 @@ __device__ __forceinline__ void collect(const S& s, float low, F in, uint32_t co
 // on the ids of equal keys.  By one CTA on the whole row: the way out for
 // rows with more equal or nearly equal tokens than a list holds.
 template <typename T>
-__device__ Cut select_slow(const T* row, int V, const Scale& s, Cut c, bool by_count, u64 target, Smem& sm) {
+__device__ __noinline__ Cut select_slow(const T* row, int V, Scale s, Cut c, bool by_count, u64 target, Smem& sm) {
   unsigned prefix = 0, mask = 0;
   u64 before = 0;  // weight ahead of the keys that match the prefix
   for (int level = 3; level >= 0; --level) {
@@ -459,7 +492,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
   __shared__ Smem sm;
   pdl_launch_next();
   pdl_wait();
-  const int C = a.cluster, row = blockIdx.x / C, rank = blockIdx.x - row * C, V = a.vocab;
+  const int C = 1 << a.lg_cluster, row = blockIdx.x >> a.lg_cluster, rank = blockIdx.x & (C - 1), V = a.vocab;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int seq = row / a.rows, i = row - seq * a.rows;  // sequence and its row
   int nd = a.rows - 1;
@@ -479,6 +512,13 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
   // (64-bit floats are slow here: one lane each, while the logits load)
   if (tid == 64) sm.c_pair = pair_of(1.4426950408889634074 / (greedy ? 1.0 : (double)temp));
   if (tid == 96 && min_p > 0.f) sm.off_pair = pair_of((double)temp * log((double)min_p));
+
+  int x = -1;          // the draft's token
+  float zx = -INFINITY;  // and its logit
+  if (a.kind == SAMPLING_VERIFY && i < nd) {
+    x = a.path[(size_t)seq * (a.rows - 1) + i];
+    if (x >= 0 && x < V) zx = ld(z_row + x);
+  }
 
   // ---- 1. the slice into shared memory, its largest and smallest logit
   Slice<T, RES> s;
@@ -571,9 +611,9 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     __syncthreads();
     for (int w = 0; w < NW; ++w) low = fminf(low, sm.fmin[w]);
     if (!enough) low = -3.402823466e+38f;  // fewer logits than that: all of them
-    const unsigned part = CAP / C;
+    const unsigned part = PARTS >> a.lg_cluster;
     cluster_wait();
-    collect(s, low, [](float) { return true; }, smem_u32(&sm.ncand), dsmem_addr(sm.cand + rank * part, 0), part);
+    collect(s, low, INFINITY, [](float) { return true; }, smem_u32(&sm.ncand), dsmem_addr(sm.parts + rank * part, 0), part);
     __syncthreads();
     if (tid < C) {
       st_cl(dsmem_addr(&sm.xmax[rank], tid), __float_as_uint(mx));
@@ -612,10 +652,10 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
   Cut cut = {KEY_NINF + 1, V};  // everything above -inf
   u64 total = 0;                // mass of the cut, when known
   bool list = false;            // the kept tokens are the first `n_kept` of the first CTA's list,
-  int n_kept = 0;               // sorted, or ranked if it is small (then thread t holds token t)
+  int n_kept = 0;               // sorted, or ranked if it is small (then `lanes` lanes hold a token)
   bool small = false;
   u64 lkey = 0, lmass = 0, lcum = 0;
-  int lrank = 0;
+  int lrank = 0, lanes = 1;
 
   // Broadcasts the first CTA's sm.mk.  (Two turns: a CTA that still reads one
   // decision is at least a cluster barrier ahead of the next but one.)
@@ -649,8 +689,13 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
   auto mass_kept = [&]() {
     u64 m = 0, g = 0;
     const float zc = okey_value(cut.key);
-    for_each(s, [&](float z, int id) {
-      if (kept_z(z, id, zc, cut.id)) m += mass_of(z, sc, sm.tab);
+    for_each4(s, [&](const float4& v, int id) {
+      const float z[4] = {v.x, v.y, v.z, v.w};
+      if (!__any_sync(0xffffffffu, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) >= zc)) return;
+      u64 e[4];
+      masses_of<4, true>(z, sc, sm.tab, e);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m += kept_z(z[j], id + j, zc, cut.id) ? e[j] : 0ull;
     });
     exchange(m, g);
     return m;
@@ -718,24 +763,34 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
       return v;
     };
 
-    // Small lists are not sorted: thread t holds token t and finds by one pass
-    // over the list how many tokens are ahead of it and their mass.
+    // Small lists are not sorted: a token's lanes (a power of two of them, as
+    // many as there are threads for) find by one pass over the list how many
+    // tokens are not behind it, and their mass.
     auto rank_list = [&](int n) {
-      lkey = tid < n ? sm.cand[tid] : 0;
-      lmass = tid < n ? mass_of(okey_value((unsigned)(lkey >> 32)), sc, sm.tab) : 0ull;
-      if (tid < n) sm.radix[tid] = lmass;
+      lanes = 32;
+      while (lanes > 1 && n * lanes > NT) lanes >>= 1;
+      const int t = tid / lanes;
+      lkey = t < n ? sm.cand[t] : 0;
+      lmass = t < n ? mass_of(okey_value((unsigned)(lkey >> 32)), sc, sm.tab) : 0ull;
+      if (t < n) sm.radix[t] = lmass;
       if (tid == 0) sm.pick2 = 0;
       __syncthreads();
       lrank = 0;  // tokens up to and with this one
       lcum = 0;
-      if (tid < n)
-        for (int j = 0; j < n; ++j)
-          if (sm.cand[j] >= lkey) {
-            ++lrank;
-            lcum += sm.radix[j];
-          }
+      if (t < n) {
+#pragma unroll 4
+        for (int j = tid & (lanes - 1); j < n; j += lanes) {
+          const bool in = sm.cand[j] >= lkey;
+          lrank += in;
+          lcum += in ? sm.radix[j] : 0ull;
+        }
+      }
+      for (int o = 1; o < lanes; o <<= 1) {
+        lrank += __shfl_xor_sync(0xffffffffu, lrank, o);
+        lcum += __shfl_xor_sync(0xffffffffu, lcum, o);
+      }
     };
-    // the thread of the list's p-th token (from 1) tells the others
+    // the lanes of the list's p-th token (from 1) tell the others
     auto tell = [&](int slot, bool mine, u64 ahead) {
       if (mine) {
         sm.sel[slot].total = ahead + lcum;
@@ -772,30 +827,61 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     if (local) {
       list = true;
       if (rank == 0) {
-        // the parts without what lies below any of their bounds, in one piece
+        // The parts in one piece (in any order), without what lies below any of
+        // their bounds.  Then, if that leaves several warps' worth, each full
+        // warp sorts 32 of them: with F warps, at least top_k tokens are not
+        // below the least of the warps' ceil(top_k / F)-th tokens.
         float low = -INFINITY;
         for (int r = 0; r < C; ++r) low = fmaxf(low, sm.xlow[r]);
-        const unsigned low_key = okey(low), part = CAP / C;
-        u64 v[CAP / NT];
-        unsigned n = 0;
-#pragma unroll
-        for (int j = 0; j < CAP / NT; ++j) {
-          const unsigned e = tid + j * NT;
-          v[j] = e % part < (unsigned)sm.xid[e / part] ? sm.cand[e] : 0ull;
-          if ((unsigned)(v[j] >> 32) < low_key) v[j] = 0;
-          n += v[j] != 0;
-        }
-        u64 all;
-        unsigned at = (unsigned)block_scan_u64(n, &all, sm);
-#pragma unroll
-        for (int j = 0; j < CAP / NT; ++j)
-          if (v[j]) sm.cand[at++] = v[j];
+        const unsigned low_key = okey(low), lg_part = 10 - a.lg_cluster;
+        static_assert(PARTS == 1 << 10, "lg_part");
         if (tid == 0) {
-          sm.ncand = (unsigned)all;
-          sm.pick = -1;
+          sm.ncand = 0;
+          sm.bound = ~0ull;
         }
         __syncthreads();
-        cut_list((int)all);
+        auto append = [&](bool yes, u64 v) {
+          const unsigned m = __ballot_sync(0xffffffffu, yes);
+          if (!m) return;
+          unsigned at = 0;
+          if (lane == 0) at = atomicAdd(&sm.ncand, __popc(m));
+          at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1));
+          if (yes) sm.cand[at] = v;
+        };
+#pragma unroll
+        for (int j = 0; j < PARTS / NT; ++j) {
+          const unsigned e = tid + j * NT, r = e >> lg_part;
+          const u64 v = e - (r << lg_part) < (unsigned)sm.xid[r] ? sm.parts[e] : 0ull;
+          append((unsigned)(v >> 32) >= low_key && v, v);
+        }
+        if (tid == 0) sm.pick = -1;
+        __syncthreads();
+        int all = (int)sm.ncand;
+        const int full = all / 32;
+        if (full >= 2 && all <= NT && top_k <= 32 * full) {
+          u64 v = tid < all ? sm.cand[tid] : 0ull;
+          if (warp < full) {
+            u64 y = v;
+#pragma unroll
+            for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+              for (int j = k >> 1; j > 0; j >>= 1) {
+                const u64 o = __shfl_xor_sync(0xffffffffu, y, j);
+                const bool larger = ((lane & j) == 0) == ((lane & k) == 0);
+                y = larger ? (y > o ? y : o) : (y < o ? y : o);
+              }
+            y = __shfl_sync(0xffffffffu, y, (top_k + full - 1) / full - 1);
+            if (lane == 0) atomicMin(&sm.bound, y);
+          }
+          __syncthreads();
+          if (tid == 0) sm.ncand = 0;
+          const u64 bound = sm.bound;
+          __syncthreads();
+          append(v >= bound && v, v);
+          __syncthreads();
+          all = (int)sm.ncand;
+        }
+        cut_list(all);
       }
     } else {
     // bins of equal width over [zmax - 64, zmax] or the row's own range if that
@@ -842,9 +928,10 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     Decision dec = broadcast();
     // Gathers the tokens of the decision's bins into the first CTA's list.
     auto gather = [&](int lo, int hi) {
-      // (a bound below the last bin's end, roundings included, skips most)
+      // (bounds beyond the bins' ends, roundings included, skip most)
       const float low = hi == NB - 1 ? -INFINITY : zmax - (float)(hi + 1) / per * 1.0001f;
-      collect(s, low, [&](float z) { const int b = bin_of(z); return b >= lo && b <= hi; },
+      const float high = lo == 0 ? INFINITY : zmax - (float)lo / per * 0.9999f;
+      collect(s, low, high, [&](float z) { const int b = bin_of(z); return b >= lo && b <= hi; },
               dsmem_addr(&sm.ncand, 0), dsmem_addr(sm.cand, 0), CAP);
     };
 
@@ -940,11 +1027,16 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
           const int lo = dec.lo, hi = dec.hi;
           u64 m = 0, g = 0;  // kept mass, and what of it lies ahead of the gathered bins
           const float zc = okey_value(cut.key);
-          for_each(s, [&](float z, int id) {
-            if (kept_z(z, id, zc, cut.id)) {
-              const u64 e = mass_of(z, sc, sm.tab);
-              m += e;
-              if (bin_of(z) < lo) g += e;
+          for_each4(s, [&](const float4& v, int id) {
+            const float z[4] = {v.x, v.y, v.z, v.w};
+            if (!__any_sync(0xffffffffu, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) >= zc)) return;
+            u64 e[4];
+            masses_of<4, true>(z, sc, sm.tab, e);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (!kept_z(z[j], id + j, zc, cut.id)) e[j] = 0;
+              m += e[j];
+              g += bin_of(z[j]) < lo ? e[j] : 0ull;
             }
           });
           if (dec.step == STEP_TOPP) gather(lo, hi);
@@ -966,7 +1058,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
                 const float top = zmax - (float)lo / per, fine = (float)SUB / ((float)(hi + 1 - lo) / per);
                 u64 v[CAP / NT];
                 int sb[CAP / NT];
-                sm.sub[tid] = 0;
+                sm.sub_lo[tid] = sm.sub_hi[tid] = 0;
                 __syncthreads();
 #pragma unroll
                 for (int j = 0; j < CAP / NT; ++j) {
@@ -974,10 +1066,14 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
                   v[j] = e < n ? sm.cand[e] : 0ull;
                   const float z = okey_value((unsigned)(v[j] >> 32));
                   sb[j] = (int)fminf(fmaxf((top - z) * fine, 0.f), (float)(SUB - 1));
-                  if (v[j]) atomicAdd(&sm.sub[sb[j]], mass_of(z, sc, sm.tab));
+                  if (v[j]) {  // (below 2^42 each, as the largest logit's bin is not here: no sum of 2048 overflows)
+                    const u64 e2 = mass_of(z, sc, sm.tab);
+                    atomicAdd(&sm.sub_lo[sb[j]], (unsigned)e2 & 0x1fffffu);
+                    atomicAdd(&sm.sub_hi[sb[j]], (unsigned)(e2 >> 21));
+                  }
                 }
                 __syncthreads();
-                const u64 mine = sm.sub[tid];
+                const u64 mine = ((u64)sm.sub_hi[tid] << 21) + sm.sub_lo[tid];
                 const u64 before = block_scan_u64(mine, &lall, sm);
                 if (g + before < want && want <= g + before + mine) {
                   sm.pick2 = tid;
@@ -1114,16 +1210,9 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     return;
   }
   const bool verify = a.kind == SAMPLING_VERIFY;
-  int x = -1;       // the draft's token
-  u64 x_mass = 0;   // and its kept mass
+  u64 x_mass = 0;  // kept mass of the draft's token
   if (list && rank != 0) return;  // the rest is the first CTA's
-  if (verify && i < nd) {
-    x = a.path[(size_t)seq * (a.rows - 1) + i];
-    if (!empty && x >= 0 && x < V) {
-      const float zx = ld(z_row + x);
-      x_mass = kept(okey(zx), x, cut) ? mass_of(zx, sc, sm.tab) : 0ull;
-    }
-  }
+  if (!empty && x >= 0 && x < V && kept(okey(zx), x, cut)) x_mass = mass_of(zx, sc, sm.tab);
   auto passes = [&]() {
     return floor_share(a.u_accept[(size_t)seq * (a.rows - 1) + i], total) < x_mass;
   };
@@ -1166,16 +1255,18 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     if (!pass && small) {
       // the running mass in id order at this thread's token
       const u64 e = lrank > 0 && lrank <= n_kept && (int)~(unsigned)lkey != x ? lmass : 0ull;
-      const int n = (int)sm.ncand;
-      if (tid < n) sm.radix[tid] = e;
+      const int n = (int)sm.ncand, t0 = tid / lanes;
+      if (t0 < n) sm.radix[t0] = e;
       __syncthreads();
+      u64 c = 0;
       if (e) {
-        u64 c = 0;
-        for (int j = 0; j < n; ++j)
-          if ((unsigned)sm.cand[j] >= (unsigned)lkey) c += sm.radix[j];
-        const u64 t = threshold(total - x_mass);
-        if (c - e <= t && t < c) sm.pick = (int)~(unsigned)lkey;
+#pragma unroll 4
+        for (int j = tid & (lanes - 1); j < n; j += lanes)
+          c += (unsigned)sm.cand[j] >= (unsigned)lkey ? sm.radix[j] : 0ull;
       }
+      for (int o = 1; o < lanes; o <<= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+      const u64 t = threshold(total - x_mass);
+      if (e && c - e <= t && t < c) sm.pick = (int)~(unsigned)lkey;
       __syncthreads();
     } else if (!pass) {
       // the kept tokens in id order, and the first whose running mass exceeds the draw
@@ -1213,16 +1304,17 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
   auto mass4 = [&](int q, u64 (&e)[4]) {
     const float4 v = q < g1 ? s.get4(q) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     const float zz[4] = {v.x, v.y, v.z, v.w};
+    masses_of<4, true>(zz, sc, sm.tab, e);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int id = s.first + 4 * q + j;
-      e[j] = id != x && kept_z(zz[j], id, zc, cut.id) ? mass_of(zz[j], sc, sm.tab) : 0ull;
+      if (id == x || !kept_z(zz[j], id, zc, cut.id)) e[j] = 0;
     }
   };
   u64 wm = 0;
-  for (int q = g0 + lane; q < g1; q += 32) {
+  for (int q0 = g0; q0 < g1; q0 += 32) {
     u64 e[4];
-    mass4(q, e);
+    mass4(q0 + lane, e);
     wm += e[0] + e[1] + e[2] + e[3];
   }
   wm = warp_sum_u64(wm);
@@ -1290,7 +1382,7 @@ int launch_one(const SamplingArgs& a, int slice, const Ctx& c) {
     opted.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
   const size_t smem = RES ? (size_t)((slice + 15 + 8) / 8 * 8) * 4 : 0;
-  return launch_kx(kern, dim3(a.batch * a.rows * a.cluster), dim3(NT), smem, c, a.cluster, a, slice);
+  return launch_kx(kern, dim3((a.batch * a.rows) << a.lg_cluster), dim3(NT), smem, c, 1 << a.lg_cluster, a, slice);
 }
 
 // A row's cluster: as few CTAs as hold it with two of them an SM (one, for the
@@ -1298,11 +1390,11 @@ int launch_one(const SamplingArgs& a, int slice, const Ctx& c) {
 template <typename T>
 int launch_rows(SamplingArgs a, const Ctx& c) {
   const int rows = a.batch * a.rows;
-  a.cluster = 1;
-  while (a.cluster < CMAX && (a.vocab > a.cluster * SLICE2 ||
-                              (rows * a.cluster < c.nsm && a.vocab > a.cluster * 4096)))
-    a.cluster *= 2;
-  const int slice = ((a.vocab + a.cluster - 1) / a.cluster + 7) / 8 * 8;
+  a.lg_cluster = 0;
+  while (1 << a.lg_cluster < CMAX && (a.vocab > SLICE2 << a.lg_cluster ||
+                                      (rows << a.lg_cluster < c.nsm && a.vocab > 4096 << a.lg_cluster)))
+    ++a.lg_cluster;
+  const int slice = ((a.vocab + (1 << a.lg_cluster) - 1 >> a.lg_cluster) + 7) / 8 * 8;
   return slice <= SLICE1 ? launch_one<T, true>(a, slice, c) : launch_one<T, false>(a, slice, c);
 }
 
