@@ -182,8 +182,8 @@ def _ptr(x):
 
 
 def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the handle of torch's current stream, without building a Stream around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -331,85 +331,75 @@ def dflash2_verify_sampled(batch, block_size, vocab, path, n_draft, target_prob,
 # a tensor of another type, shape or layout, or on another device than the
 # current one, is refused before the call.
 
-def _refuse(fn, status, why):
-    raise DFlash2Error(fn, status, why)
-
-
-def _here(t):
-    if t is None:
-        return False
-    d = t.get_device()
-    return d >= 0 and d == torch.cuda.current_device()
-
-
-def _need(fn, name, t, dtype, shape, null=False):
-    """A contiguous tensor of this type and shape on the current device (or
-    None where the call allows it)."""
-    if t is None and null:
-        return
-    if not _here(t):
-        _refuse(fn, -1, f"{name} must be on the current device")
+def _refuse(fn, name, t, dev, dtype, shape):
+    if t is None or t.get_device() != dev or dev < 0:
+        raise DFlash2Error(fn, -1, f"{name} must be on the current device")
     if t.dtype is not dtype:
-        _refuse(fn, -4, f"{name} must be {dtype}")
-    if t.shape != shape or not t.is_contiguous():
-        _refuse(fn, -2, f"{name} must be contiguous, of shape {tuple(shape)}")
+        raise DFlash2Error(fn, -4, f"{name} must be {dtype}")
+    raise DFlash2Error(fn, -2, f"{name} must be contiguous, of shape {tuple(shape)}")
+
+
+def _at(fn, name, t, dev, dtype, shape):
+    """Address of a contiguous tensor of this type and shape on device dev."""
+    if (t is None or t.get_device() != dev or t.dtype is not dtype or t.shape != shape
+            or not t.is_contiguous()):
+        _refuse(fn, name, t, dev, dtype, shape)
+    return t.data_ptr()
 
 
 _LOGIT_TYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
 def _rows_of(fn, name, t, dims):
-    """Type code and the distance of the rows of a [..., n] tensor whose rows
-    are evenly spaced."""
-    if not _here(t):
-        _refuse(fn, -1, f"{name} must be on the current device")
+    """(device, type code, distance of the rows) of a [..., n] tensor on the
+    current device whose rows are evenly spaced."""
+    dev = -1 if t is None else t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise DFlash2Error(fn, -1, f"{name} must be on the current device")
     code = _LOGIT_TYPES.get(t.dtype)
     if code is None:
-        _refuse(fn, -4, f"{name} must be float32 or bfloat16")
+        raise DFlash2Error(fn, -4, f"{name} must be float32 or bfloat16")
     st, sz = t.stride(), t.shape
-    if len(sz) != dims or (sz[-1] > 1 and st[-1] != 1):
-        _refuse(fn, -2, f"{name} must have {dims} dimensions, the last one contiguous")
+    if len(sz) != dims or (st[-1] != 1 and sz[-1] > 1):
+        raise DFlash2Error(fn, -2, f"{name} must have {dims} dimensions, the last one contiguous")
     if dims == 2:
-        return code, st[0] if sz[0] > 1 else sz[1]
+        return dev, code, st[0] if sz[0] > 1 else sz[1]
     row = st[1] if sz[1] > 1 else (st[0] if sz[0] > 1 else sz[2])
     if sz[0] > 1 and sz[1] > 1 and st[0] != sz[1] * row:
-        _refuse(fn, -2, f"the rows of {name} must be evenly spaced")
-    return code, row
+        raise DFlash2Error(fn, -2, f"the rows of {name} must be evenly spaced")
+    return dev, code, row
 
 
-def _check_settings(fn, n, temperature, top_k, top_p, min_p):
-    _need(fn, "temperature", temperature, torch.float32, (n,), True)
-    _need(fn, "top_k", top_k, torch.int32, (n,), True)
-    _need(fn, "top_p", top_p, torch.float32, (n,), True)
-    _need(fn, "min_p", min_p, torch.float32, (n,), True)
+def _settings(fn, dev, n, temperature, top_k, top_p, min_p):
+    f32, shape = torch.float32, (n,)
+    return (None if temperature is None else _at(fn, "temperature", temperature, dev, f32, shape),
+            None if top_k is None else _at(fn, "top_k", top_k, dev, torch.int32, shape),
+            None if top_p is None else _at(fn, "top_p", top_p, dev, f32, shape),
+            None if min_p is None else _at(fn, "min_p", min_p, dev, f32, shape))
 
 
 def dflash2_sample(logits, temperature, top_k, top_p, min_p, u, token, prob=None, workspace=None, stream=None):
     """logits: [rows, vocab] float32 or bfloat16, rows evenly spaced; the
     settings: [rows] tensors or None; u, token, prob: [rows]."""
     fn = "dflash2_sample"
-    code, stride = _rows_of(fn, "logits", logits, 2)
+    dev, code, stride = _rows_of(fn, "logits", logits, 2)
     n, vocab = logits.shape
-    _check_settings(fn, n, temperature, top_k, top_p, min_p)
-    _need(fn, "u", u, torch.float32, (n,))
-    _need(fn, "token", token, torch.int32, (n,))
-    _need(fn, "prob", prob, torch.float32, (n,), True)
     return _check(fn, lib().dflash2_sample(
-        code, n, vocab, _ptr(logits), stride, _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(u),
-        _ptr(token), _ptr(prob), _ptr(workspace), _stream(stream)))
+        code, n, vocab, logits.data_ptr(), stride, *_settings(fn, dev, n, temperature, top_k, top_p, min_p),
+        _at(fn, "u", u, dev, torch.float32, (n,)), _at(fn, "token", token, dev, torch.int32, (n,)),
+        None if prob is None else _at(fn, "prob", prob, dev, torch.float32, (n,)), _ptr(workspace), _stream(stream)))
 
 
 def dflash2_target_probs(logits, temperature, top_k, top_p, min_p, prob, workspace=None, stream=None):
     """logits: [batch, rows, vocab] float32 or bfloat16, rows evenly spaced;
     the settings: [batch] tensors or None; prob: [batch, rows, vocab] float32."""
     fn = "dflash2_target_probs"
-    code, stride = _rows_of(fn, "logits", logits, 3)
+    dev, code, stride = _rows_of(fn, "logits", logits, 3)
     batch, rows, vocab = logits.shape
-    _check_settings(fn, batch, temperature, top_k, top_p, min_p)
-    _need(fn, "prob", prob, torch.float32, logits.shape)
     return _check(fn, lib().dflash2_target_probs(
-        code, batch, rows, vocab, _ptr(logits), stride, _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
-        _ptr(prob), _ptr(workspace), _stream(stream)))
+        code, batch, rows, vocab, logits.data_ptr(), stride,
+        *_settings(fn, dev, batch, temperature, top_k, top_p, min_p),
+        _at(fn, "prob", prob, dev, torch.float32, logits.shape), _ptr(workspace), _stream(stream)))
 
 
 def dflash2_verify_logits_workspace(batch, block_size):
@@ -422,26 +412,21 @@ def dflash2_verify_logits(path, n_draft, logits, temperature, top_k, top_p, min_
     spaced; path, u_accept: [batch, block_size - 1]; the settings: [batch]
     tensors or None."""
     fn = "dflash2_verify_logits"
-    code, stride = _rows_of(fn, "logits", logits, 3)
+    dev, code, stride = _rows_of(fn, "logits", logits, 3)
     batch, B, vocab = logits.shape
-    i32 = torch.int32
-    _check_settings(fn, batch, temperature, top_k, top_p, min_p)
-    _need(fn, "path", path, i32, (batch, B - 1))
-    _need(fn, "n_draft", n_draft, i32, (batch,), True)
-    _need(fn, "u_accept", u_accept, torch.float32, (batch, B - 1))
-    _need(fn, "u_sample", u_sample, torch.float32, (batch,))
-    for name, t in (("accept_len", accept_len), ("n_out", n_out), ("next_anchor", next_anchor)):
-        _need(fn, name, t, i32, (batch,))
-    _need(fn, "out_tok", out_tok, i32, (batch, B))
-    _need(fn, "seq_len", seq_len, i32, (batch,), True)
-    _need(fn, "counters", counters, torch.int64, (4 + 2 * B - 1,), True)
-    if not _here(workspace):
-        _refuse(fn, -5, "workspace must be on the current device")
+    i32, f32, one, drafts = torch.int32, torch.float32, (batch,), (batch, B - 1)
+    if workspace is None or workspace.get_device() != dev:
+        raise DFlash2Error(fn, -5, "workspace must be on the current device")
     return _check(fn, lib().dflash2_verify_logits(
-        code, batch, B, vocab, _ptr(path), _ptr(n_draft), _ptr(logits), stride, _ptr(temperature), _ptr(top_k),
-        _ptr(top_p), _ptr(min_p), _ptr(u_accept), _ptr(u_sample), _ptr(accept_len), _ptr(out_tok), _ptr(n_out),
-        _ptr(next_anchor), _ptr(seq_len), _ptr(counters), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        code, batch, B, vocab, _at(fn, "path", path, dev, i32, drafts),
+        None if n_draft is None else _at(fn, "n_draft", n_draft, dev, i32, one), logits.data_ptr(), stride,
+        *_settings(fn, dev, batch, temperature, top_k, top_p, min_p),
+        _at(fn, "u_accept", u_accept, dev, f32, drafts), _at(fn, "u_sample", u_sample, dev, f32, one),
+        _at(fn, "accept_len", accept_len, dev, i32, one), _at(fn, "out_tok", out_tok, dev, i32, (batch, B)),
+        _at(fn, "n_out", n_out, dev, i32, one), _at(fn, "next_anchor", next_anchor, dev, i32, one),
+        None if seq_len is None else _at(fn, "seq_len", seq_len, dev, i32, one),
+        None if counters is None else _at(fn, "counters", counters, dev, torch.int64, (4 + 2 * B - 1,)),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def dflash2_linear_w4(codes, scale, group, x, out, accumulate=False, stream=None):
@@ -449,18 +434,18 @@ def dflash2_linear_w4(codes, scale, group, x, out, accumulate=False, stream=None
     in_features / group] bfloat16; x: [rows, in_features] bfloat16, out:
     [rows, out_features] float32 or bfloat16, both with evenly spaced rows."""
     fn = "dflash2_linear_w4"
-    xcode, xs = _rows_of(fn, "x", x, 2)
-    code, os_ = _rows_of(fn, "out", out, 2)
+    dev, xcode, x_stride = _rows_of(fn, "x", x, 2)
+    _, code, out_stride = _rows_of(fn, "out", out, 2)
     if xcode != BF16:
-        _refuse(fn, -4, "x must be bfloat16")
+        raise DFlash2Error(fn, -4, "x must be bfloat16")
     n, k = x.shape
-    m = out.shape[1]
-    if group not in (32, 64, 128) or k % group or out.shape[0] != n:
-        _refuse(fn, -2, "group must be 32, 64 or 128 and divide in_features, x and out have as many rows")
-    _need(fn, "codes", codes, torch.uint8, (m, k // 2))
-    _need(fn, "scale", scale, torch.bfloat16, (m, k // group))
+    rows, m = out.shape
+    if group not in (32, 64, 128) or k % group or rows != n:
+        raise DFlash2Error(fn, -2, "group must be 32, 64 or 128 and divide in_features, x and out have as many rows")
     return _check(fn, lib().dflash2_linear_w4(
-        _ptr(codes), _ptr(scale), group, m, k, _ptr(x), xs, n, _ptr(out), os_, code, int(accumulate), _stream(stream)))
+        _at(fn, "codes", codes, dev, torch.uint8, (m, k // 2)),
+        _at(fn, "scale", scale, dev, torch.bfloat16, (m, k // group)), group, m, k, x.data_ptr(), x_stride, n,
+        out.data_ptr(), out_stride, code, int(accumulate), _stream(stream)))
 
 
 def dflash2_verify_accept_ex(batch, block_size, path, n_draft, target, accept_len, out_tok, n_out, next_anchor,
