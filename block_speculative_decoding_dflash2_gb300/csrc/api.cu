@@ -880,6 +880,7 @@ int dflash2_linear_w4(const uint8_t* codes, const void* scale, int group, int ou
                       int accumulate, void* stream) {
   if (group != 32 && group != 64 && group != 128) return DFLASH2_ERR_SHAPE;
   if (out_features <= 0 || in_features <= 0 || in_features % group || rows < 0) return DFLASH2_ERR_SHAPE;
+  if (out_features > 1 << 24 || in_features > 1 << 24) return DFLASH2_ERR_SHAPE;
   if (out_dtype != DFLASH2_F32 && out_dtype != DFLASH2_BF16) return DFLASH2_ERR_DTYPE;
   if (rows == 0) return DFLASH2_OK;
   if (!codes || !scale || !x || !out) return DFLASH2_ERR_INVALID_ARG;

@@ -283,7 +283,8 @@ struct W4Op {
   long long ldo;
   bool out_bf16, accumulate;
 };
-int launch_linear_w4(const W4Op& g, const Ctx& c);
+int launch_linear_w4(const W4Op& g, const Ctx& c);     // any number of rows
+int launch_linear_w4_tc(const W4Op& g, const Ctx& c);  // tcgen05 (linear_w4_tc.cu); up to 2^20 rows
 
 // logits to tokens (sampling.cu)
 enum { SAMPLING_TOKEN = 0, SAMPLING_PROBS = 1, SAMPLING_VERIFY = 2 };

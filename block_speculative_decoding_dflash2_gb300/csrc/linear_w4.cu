@@ -292,10 +292,7 @@ int launch(Args a, const Ctx& c) {
 
 template <int G, typename OutT>
 int launch_n(const Args& a, const Ctx& c) {
-  if (a.N <= 8) return launch<G, 1, OutT>(a, c);
-  if (a.N <= 16) return launch<G, 2, OutT>(a, c);
-  if (a.N <= 32) return launch<G, 4, OutT>(a, c);
-  return launch<G, 8, OutT>(a, c);
+  return a.N <= 8 ? launch<G, 1, OutT>(a, c) : launch<G, 2, OutT>(a, c);
 }
 
 template <typename OutT>
@@ -306,21 +303,30 @@ int launch_g(int group, const Args& a, const Ctx& c) {
 }  // namespace
 
 int launch_linear_w4(const W4Op& g, const Ctx& c) {
-  const int most = 64 * 65535;  // rows of a launch (grid y)
+  const int most = 1 << 20;  // rows of a launch (its tiles are counted in ints)
   for (int n = 0; n < g.N; n += most) {
+    W4Op p = g;
+    p.x = static_cast<const bf16*>(g.x) + (size_t)n * g.ldx;
+    p.N = std::min(most, g.N - n);
+    p.out = static_cast<char*>(g.out) + (size_t)n * g.ldo * (g.out_bf16 ? 2 : 4);
+    if (p.N > 16) {
+      const int rc = launch_linear_w4_tc(p, c);
+      if (rc != DFLASH2_OK) return rc;
+      continue;
+    }
     Args a = {};
-    a.codes = static_cast<const uint8_t*>(g.codes);
-    a.scale = static_cast<const bf16*>(g.scale);
-    a.M = g.M;
-    a.K = g.K;
-    a.chunks = (g.K + CK - 1) / CK;
-    a.x = static_cast<const bf16*>(g.x) + (size_t)n * g.ldx;
-    a.ldx = g.ldx;
-    a.N = std::min(most, g.N - n);
-    a.out = static_cast<char*>(g.out) + (size_t)n * g.ldo * (g.out_bf16 ? 2 : 4);
-    a.ldo = g.ldo;
-    a.accumulate = g.accumulate;
-    const int rc = g.out_bf16 ? launch_g<bf16>(g.group, a, c) : launch_g<float>(g.group, a, c);
+    a.codes = static_cast<const uint8_t*>(p.codes);
+    a.scale = static_cast<const bf16*>(p.scale);
+    a.M = p.M;
+    a.K = p.K;
+    a.chunks = (p.K + CK - 1) / CK;
+    a.x = static_cast<const bf16*>(p.x);
+    a.ldx = p.ldx;
+    a.N = p.N;
+    a.out = p.out;
+    a.ldo = p.ldo;
+    a.accumulate = p.accumulate;
+    const int rc = p.out_bf16 ? launch_g<bf16>(p.group, a, c) : launch_g<float>(p.group, a, c);
     if (rc != DFLASH2_OK) return rc;
   }
   return DFLASH2_OK;

@@ -1,0 +1,372 @@
+// Product with 4-bit weights for many activation rows, on the 5th-generation
+// tensor cores (the definition, and the kernel for few rows, are in
+// linear_w4.cu).
+//
+// A 128-row weight tile is operand A of tcgen05.mma, BN activation rows are
+// operand B, and every group of inputs is summed on its own: the whole numbers
+// q - 8 are exact in bf16, a group's fp32 sums lie in one of two TMEM
+// accumulators, and the epilogue warps read them, multiply them by the row's
+// group scale and add them to the row's sums in registers while the tensor
+// core fills the other one.  (Scaled weights would need 11 bits, three more
+// than bf16 has.)
+//
+// Warp roles (576 threads, one CTA an SM):
+//   warp 0       TMA producer (one lane): codes and activations -> ring
+//   warp 1       MMA issuer (one lane) and TMEM owner
+//   warps 2-9    epilogue: two sets of four, each with half of the columns
+//   warps 10-17  converters: 32 bytes of codes of a row -> 64 bf16 values in
+//                the swizzled operand layout
+// With few tiles the inputs are split over a cluster, whose partial tiles are
+// added in rank order through distributed shared memory.
+//
+// Every wait is bounded (1 s).  A wait that gives up lets the other roles bail
+// out, the tile's outputs become NaN, and the kernel waits (bounded) for its
+// own copies and products, frees TMEM and returns.
+#include <algorithm>
+#include <atomic>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace df2 {
+
+namespace {
+
+constexpr int BM = 128, BK = 64;
+constexpr int EPI_THREADS = 256, CONV_THREADS = 256, THREADS = 64 + EPI_THREADS + CONV_THREADS;
+constexpr int SMEM_BUDGET = 227 * 1024 - 2048;  // 1 KB of alignment, 1 KB of barriers
+constexpr uint64_t WAIT_NS = 1000000000ull;
+
+template <int BN>
+struct Cfg {
+  static constexpr int A_BYTES = BM * BK * 2, Q_BYTES = BM * BK / 2, B_BYTES = BN * BK * 2;
+  static constexpr int STAGE = A_BYTES + Q_BYTES + B_BYTES;
+  static constexpr int STAGES = SMEM_BUDGET / STAGE < 8 ? SMEM_BUDGET / STAGE : 8;
+  static constexpr int SMEM = STAGES * STAGE + 2048;
+  static constexpr uint32_t TMEM_COLS = 2 * BN;  // 64, 128 or 256
+  static_assert(STAGES * (A_BYTES + B_BYTES) >= BM * BN * 4, "the ring holds a partial tile");
+};
+
+struct Args {
+  const bf16* scale;
+  int M, K, N;
+  int chunks, tiles, n_tiles, split, slice;  // chunks of 64 inputs; per CTA of a cluster (even)
+  void* out;
+  long long ldo;
+  int accumulate;
+};
+
+// 8 nibbles, in order, as bf16 values (128 + q) - 136 = q - 8.
+__device__ __forceinline__ uint4 nibbles8(uint32_t w) {
+  const uint32_t lo = w & 0x0f0f0f0fu, hi = (w >> 4) & 0x0f0f0f0fu;
+  const uint32_t p01 = __byte_perm(lo, hi, 0x5140), p23 = __byte_perm(lo, hi, 0x7362);
+  const __nv_bfloat162 off = __float2bfloat162_rn(136.f);
+  auto two = [&](uint32_t p, uint32_t sel) {
+    const uint32_t r = __byte_perm(p, 0x43434343u, sel);
+    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&r), off);
+    return *reinterpret_cast<const uint32_t*>(&d);
+  };
+  return make_uint4(two(p01, 0x4140), two(p01, 0x4342), two(p23, 0x4140), two(p23, 0x4342));
+}
+
+template <int BN, int G, typename OutT>
+__global__ void __launch_bounds__(THREADS, 1)
+    linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmX, Args a) {
+  using C = Cfg<BN>;
+  constexpr int S = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* stA = smem;
+  uint8_t* stB = stA + S * C::A_BYTES;
+  uint8_t* stQ = stB + S * C::B_BYTES;
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(stQ + S * C::Q_BYTES);  // codes and activations have landed
+  uint64_t* full = raw_full + S;                                           // the codes are converted
+  uint64_t* empty = full + S;
+  uint64_t* acc_full = empty + S;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);  // then the abort flag, in one 8-byte word
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  pdl_launch_next();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(raw_full + s, 1);
+      mbar_init(full + s, CONV_THREADS);
+      mbar_init(empty + s, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(acc_full + i, 1);
+      mbar_init(acc_empty + i, EPI_THREADS);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmX);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+
+  const int rank = blockIdx.x % a.split, first = blockIdx.x / a.split, step = gridDim.x / a.split;
+  const int c0 = min(a.chunks, rank * a.slice), c1 = min(a.chunks, c0 + a.slice);
+  float* part = reinterpret_cast<float*>(smem);  // [BN][BM], in the idle ring
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
+      int stage = 0;
+      uint32_t phase = 0;
+      long issued = 0;
+      bool ok = true;
+      for (int t = first; ok && t < a.tiles; t += step) {
+        const int nt = t % a.n_tiles, mt = t / a.n_tiles;
+        for (int c = c0; c < c1; ++c) {
+          if (!mbar_wait(empty + stage, phase ^ 1u, abort_flag, WAIT_NS)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(raw_full + stage, C::Q_BYTES + C::B_BYTES);
+          // (codes as pairs of bytes: 16 of them are 64 inputs)
+          tma_load_2d(stQ + stage * C::Q_BYTES, &tmQ, raw_full + stage, c * (BK / 4), mt * BM, pol_w);
+          tma_load_2d(stB + stage * C::B_BYTES, &tmX, raw_full + stage, c * BK, nt * BN, pol_x);
+          ++issued;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (*abort_flag) {  // wait (bounded) for every copy this thread issued to land
+        for (int s = 0; s < S; ++s) {
+          const long cnt = issued / S + (s < issued % S ? 1 : 0);
+          volatile int never = 0;
+          if (cnt > 0) mbar_wait(raw_full + s, (uint32_t)((cnt - 1) & 1), &never, WAIT_NS);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16_f32(BM, BN);
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int t = first; ok && t < a.tiles; t += step) {
+        for (int c = c0; ok && c < c1; ++c) {
+          if (!mbar_wait(full + stage, phase, abort_flag, WAIT_NS) ||
+              !mbar_wait(raw_full + stage, phase, abort_flag, WAIT_NS)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = sdesc_sw128(smem_u32(stA + stage * C::A_BYTES));
+          const uint64_t bd = sdesc_sw128(smem_u32(stB + stage * C::B_BYTES));
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const bool begin = G == 128 ? (c & 1) == 0 && kk == 0 : kk % (G / 16) == 0;
+            const bool end = G == 128 ? ((c & 1) || c + 1 == c1) && kk == 3 : kk % (G / 16) == G / 16 - 1;
+            if (begin) {
+              if (!mbar_wait(acc_empty + buf, acc_phase ^ 1u, abort_flag, WAIT_NS)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+            }
+            umma_bf16(tmem + (uint32_t)(buf * BN), ad + 2u * kk, bd + 2u * kk, idesc, begin ? 0u : 1u);
+            if (end) {
+              umma_commit(acc_full + buf);
+              buf ^= 1;
+              if (buf == 0) acc_phase ^= 1u;
+            }
+          }
+          umma_commit(empty + stage);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) *abort_flag = 1;
+      umma_commit(drain);  // every product of this thread completes before TMEM can be freed
+      volatile int never = 0;
+      mbar_wait(drain, 0, &never, WAIT_NS);
+    }
+    __syncwarp();
+  } else if (warp >= 2 + EPI_THREADS / 32) {
+    // converters: thread ct takes half h of row r (16 bytes, 32 inputs)
+    const int ct = threadIdx.x - 64 - EPI_THREADS, r = ct >> 1, h = ct & 1;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = first; ok && t < a.tiles; t += step) {
+      for (int c = c0; c < c1; ++c) {
+        if (!mbar_wait(raw_full + stage, phase, abort_flag, WAIT_NS)) {
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        const uint4 q = *reinterpret_cast<const uint4*>(stQ + stage * C::Q_BYTES + ct * 16);
+        uint8_t* row = stA + stage * C::A_BYTES + r * 128;
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(row + (((h * 4 + i) ^ (r & 7)) << 4)) = nibbles8(w[i]);
+        fence_proxy_async_smem();  // the operand is read by tcgen05.mma (async proxy)
+        mbar_arrive(full + stage);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else {
+    // epilogue
+    constexpr int COLS = BN / 2;
+    const int q = warp & 3, row = q * 32 + lane, set = (warp - 2) >> 2;
+    const int g0 = c0 * BK / G, g1 = (c1 * BK + G - 1) / G, groups = a.K / G;
+    int buf = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int t = first; t < a.tiles; t += step) {
+      const int nt = t % a.n_tiles, mt = t / a.n_tiles, m = mt * BM + row;
+      const bf16* srow = a.scale + (size_t)min(m, a.M - 1) * groups;
+      float acc[COLS];
+#pragma unroll
+      for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
+      float s_next = g0 < min(g1, groups) ? __bfloat162float(srow[g0]) : 0.f;
+      for (int g = g0; ok && g < g1; ++g) {
+        const float s = s_next;
+        s_next = g + 1 < min(g1, groups) ? __bfloat162float(srow[g + 1]) : 0.f;
+        // (the whole warp goes on or gives up: TMEM reads are warp-wide)
+        const bool got = mbar_wait(acc_full + buf, acc_phase, abort_flag, WAIT_NS);
+        if (!__all_sync(0xffffffffu, got)) {
+          *abort_flag = 1;
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN + set * COLS);
+#pragma unroll
+        for (int j0 = 0; j0 < COLS; j0 += 16) {
+          float v[16];
+          tmem_ld16(d + j0, v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[j0 + j] = fmaf(s, v[j], acc[j0 + j]);
+        }
+        tc_fence_before();
+        mbar_arrive(acc_empty + buf);
+        buf ^= 1;
+        if (buf == 0) acc_phase ^= 1u;
+      }
+      if (!ok) {
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) acc[j] = __int_as_float(0x7fffffff);
+      }
+      if (a.split == 1) {
+        if (m < a.M) {
+#pragma unroll
+          for (int j = 0; j < COLS; ++j) {
+            const int n = nt * BN + set * COLS + j;
+            if (n < a.N) {
+              OutT* o = static_cast<OutT*>(a.out) + (size_t)n * a.ldo + m;
+              st(o, a.accumulate ? ld(o) + acc[j] : acc[j]);
+            }
+          }
+        }
+      } else {  // (one tile: every copy and product of it is done)
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) part[(set * COLS + j) * BM + row] = acc[j];
+      }
+    }
+  }
+  if (a.split > 1) {
+    cluster_sync();
+    const int nt = first % a.n_tiles, mt = first / a.n_tiles;
+    bool bad = false;  // a CTA of the cluster gave up
+    for (int r = 0; r < a.split; ++r) bad = bad || __float_as_int(ld_dsmem2(dsmem_addr(tmem_slot, r)).y) != 0;
+    for (int i = rank * THREADS + threadIdx.x; i < BN * BM / 4; i += a.split * THREADS) {
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int r = 0; r < a.split; ++r) {
+        const float4 v = ld_dsmem4(dsmem_addr(part + i * 4, r));
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+      }
+      const float nan = __int_as_float(0x7fffffff);
+      const float e[4] = {bad ? nan : s.x, bad ? nan : s.y, bad ? nan : s.z, bad ? nan : s.w};
+      const int n = nt * BN + i * 4 / BM, m = mt * BM + i * 4 % BM;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (n < a.N && m + j < a.M) {
+          OutT* o = static_cast<OutT*>(a.out) + (size_t)n * a.ldo + m + j;
+          st(o, a.accumulate ? ld(o) + e[j] : e[j]);
+        }
+    }
+    cluster_sync();  // every partial tile has been read
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+template <int BN, int G, typename OutT>
+int launch(const W4Op& g, const Ctx& c) {
+  using C = Cfg<BN>;
+  CUtensorMap mq, mx;
+  int rc = make_rows_map(&mq, g.codes, g.M, g.K / 4, g.K / 4, BK / 4, BM);
+  if (rc) return rc;
+  rc = make_sw128_map(&mx, g.x, g.N, g.K, g.ldx, BN);
+  if (rc) return rc;
+  Args a = {};
+  a.scale = static_cast<const bf16*>(g.scale);
+  a.M = g.M;
+  a.K = g.K;
+  a.N = g.N;
+  a.chunks = (g.K + BK - 1) / BK;
+  a.n_tiles = (g.N + BN - 1) / BN;
+  a.tiles = (g.M + BM - 1) / BM * a.n_tiles;
+  // inputs split while that leaves every tile's cluster an SM each and a CTA at least 8 chunks
+  a.split = std::max(1, std::min({8, c.nsm / a.tiles, a.chunks / 8}));
+  a.slice = ((a.chunks + a.split - 1) / a.split + 1) / 2 * 2;
+  a.out = g.out;
+  a.ldo = g.ldo;
+  a.accumulate = g.accumulate;
+  auto kern = linear_w4_tc_kernel<BN, G, OutT>;
+  static std::atomic<unsigned long long> opted{0};  // devices whose kernel may use this much shared memory
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DFLASH2_ERR_CUDA;
+  if (!(opted.load(std::memory_order_relaxed) >> dev & 1)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+      return DFLASH2_ERR_CUDA;
+    opted.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
+  const int grid = a.split > 1 ? a.tiles * a.split : std::min(a.tiles, c.nsm);
+  return launch_kx(kern, dim3(grid), dim3(THREADS), C::SMEM, c, a.split, mq, mx, a);
+}
+
+template <int G, typename OutT>
+int launch_n(const W4Op& g, const Ctx& c) {
+  if (g.N <= 32) return launch<32, G, OutT>(g, c);
+  if (g.N <= 64) return launch<64, G, OutT>(g, c);
+  return launch<128, G, OutT>(g, c);
+}
+
+template <typename OutT>
+int launch_g(const W4Op& g, const Ctx& c) {
+  return g.group == 32 ? launch_n<32, OutT>(g, c) : g.group == 64 ? launch_n<64, OutT>(g, c) : launch_n<128, OutT>(g, c);
+}
+
+}  // namespace
+
+int launch_linear_w4_tc(const W4Op& g, const Ctx& c) {
+  return g.out_bf16 ? launch_g<bf16>(g, c) : launch_g<float>(g, c);
+}
+
+}  // namespace df2

@@ -541,6 +541,7 @@ int dflash2_verify_logits(int dtype, int batch, int block_size, int vocab, const
  *                weight's whole number -8..7 plus 8
  *   scale        [out_features, in_features / group] bfloat16
  *   group        32, 64 or 128; in_features must be a multiple of it
+ *   out_features, in_features   at most 2^24
  *   x            [rows, in_features] bfloat16, rows x_stride elements apart
  *                (a multiple of 8, at least in_features)
  *   rows         >= 0 (0: nothing is done)
@@ -549,7 +550,8 @@ int dflash2_verify_logits(int dtype, int batch, int block_size, int vocab, const
  *                (>= out_features); must not overlap the inputs
  *   accumulate   0: store, else add to out
  * codes, scale and x are 16-byte aligned.  The call needs no workspace and
- * gives the same bits for the same inputs.
+ * gives the same bits for the same inputs.  (Without a status word, a bounded
+ * pipeline wait that gives up leaves NaN in the outputs it was for.)
  */
 int dflash2_linear_w4(const uint8_t *codes, const void *scale, int group, int out_features, int in_features,
                       const void *x, int64_t x_stride, int rows, void *out, int64_t out_stride, int out_dtype,

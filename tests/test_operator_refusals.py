@@ -77,6 +77,7 @@ def test_linear_w4_refusals(B):
     for group in (0, 16, 48, 256, -64):
         assert call(group=group) == -2
     assert call(k=96) == -2 and call(k=0) == -2 and call(m=0) == -2 and call(rows=-1) == -2
+    assert call(m=(1 << 24) + 1, os_=1 << 25) == -2 and call(k=(1 << 24) + 64, xs=1 << 25) == -2
     assert call(xs=120) == -2 and call(xs=132) == -2 and call(os_=7) == -2
     assert call(dt=2) == -4 and call(dt=-1) == -4
     for name in ("codes", "scale", "x", "out"):
