@@ -33,7 +33,8 @@ namespace df2 {
 namespace {
 
 constexpr int BM = 128, BK = 64;
-constexpr int EPI_THREADS = 256, CONV_THREADS = 256, THREADS = 64 + EPI_THREADS + CONV_THREADS;
+constexpr int CONV_GROUPS = 4, CONV_GROUP = 64;  // converters: groups of two warps on alternate chunks
+constexpr int EPI_THREADS = 256, CONV_THREADS = CONV_GROUPS * CONV_GROUP, THREADS = 64 + EPI_THREADS + CONV_THREADS;
 constexpr int SMEM_BUDGET = 227 * 1024 - 2048;  // 1 KB of alignment, 1 KB of barriers
 constexpr uint64_t WAIT_NS = 1000000000ull;
 
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(raw_full + s, 1);
-      mbar_init(full + s, CONV_THREADS);
+      mbar_init(full + s, CONV_GROUP);
       mbar_init(empty + s, 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -203,30 +204,30 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp >= 2 + EPI_THREADS / 32) {
-    // converters: thread ct takes half h of row r (16 bytes, 32 inputs)
-    const int ct = threadIdx.x - 64 - EPI_THREADS, r = ct >> 1, h = ct & 1;
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int t = first; ok && t < a.tiles; t += step) {
-      for (int c = c0; c < c1; ++c) {
-        if (!mbar_wait(raw_full + stage, phase, abort_flag, WAIT_NS)) {
-          *abort_flag = 1;
-          ok = false;
-          break;
-        }
-        const uint4 q = *reinterpret_cast<const uint4*>(stQ + stage * C::Q_BYTES + ct * 16);
-        uint8_t* row = stA + stage * C::A_BYTES + r * 128;
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(row + (((h * 4 + i) ^ (r & 7)) << 4)) = nibbles8(w[i]);
-        fence_proxy_async_smem();  // the operand is read by tcgen05.mma (async proxy)
-        mbar_arrive(full + stage);
-        if (++stage == S) {
-          stage = 0;
-          phase ^= 1u;
-        }
+    // converters: a group takes every CONV_GROUPS-th chunk, so that several are
+    // on their way; its thread ct takes 16 bytes (32 inputs) of four rows
+    const int ct = (threadIdx.x - 64 - EPI_THREADS) % CONV_GROUP, cg = (threadIdx.x - 64 - EPI_THREADS) / CONV_GROUP;
+    const long total = a.tiles > first ? (long)((a.tiles - first + step - 1) / step) * (c1 - c0) : 0;  // chunks of this CTA
+    for (long i = cg; i < total; i += CONV_GROUPS) {
+      const int stage = (int)(i % S);
+      if (!mbar_wait(raw_full + stage, (uint32_t)(i / S) & 1u, abort_flag, WAIT_NS)) {
+        *abort_flag = 1;
+        break;
       }
+      uint4 q[C::Q_BYTES / 16 / CONV_GROUP];
+#pragma unroll
+      for (int p = 0; p < C::Q_BYTES / 16 / CONV_GROUP; ++p)
+        q[p] = *reinterpret_cast<const uint4*>(stQ + stage * C::Q_BYTES + (ct + p * CONV_GROUP) * 16);
+#pragma unroll
+      for (int p = 0; p < C::Q_BYTES / 16 / CONV_GROUP; ++p) {
+        const int piece = ct + p * CONV_GROUP, r = piece >> 1, h = piece & 1;
+        uint8_t* row = stA + stage * C::A_BYTES + r * 128;
+        const uint32_t w[4] = {q[p].x, q[p].y, q[p].z, q[p].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(row + (((h * 4 + j) ^ (r & 7)) << 4)) = nibbles8(w[j]);
+      }
+      fence_proxy_async_smem();  // the operand is read by tcgen05.mma (async proxy)
+      mbar_arrive(full + stage);
     }
   } else {
     // epilogue
