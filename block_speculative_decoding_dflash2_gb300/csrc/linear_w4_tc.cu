@@ -14,8 +14,8 @@
 //   warp 0       TMA producer (one lane): codes and activations -> ring
 //   warp 1       MMA issuer (one lane) and TMEM owner
 //   warps 2-9    epilogue: two sets of four, each with half of the columns
-//   warps 10-17  converters: 32 bytes of codes of a row -> 64 bf16 values in
-//                the swizzled operand layout
+//   warps 10-17  converters, in four groups: 32 bytes of codes of a row -> 64
+//                bf16 values in the swizzled operand layout
 // With few tiles the inputs are split over a cluster, whose partial tiles are
 // added in rank order through distributed shared memory.
 //
@@ -38,20 +38,26 @@ constexpr int EPI_THREADS = 256, CONV_THREADS = CONV_GROUPS * CONV_GROUP, THREAD
 constexpr int SMEM_BUDGET = 227 * 1024 - 2048;  // 1 KB of alignment, 1 KB of barriers
 constexpr uint64_t WAIT_NS = 1000000000ull;
 
+constexpr int QC = 4;  // chunks of a block of codes (128 bytes of a row)
+
+// Two rings: blocks of codes, which set how many bytes are on their way (4 KB a
+// chunk in the operand ring were too few: 1.5 TB/s), and the operands of
+// single chunks.
 template <int BN>
 struct Cfg {
-  static constexpr int A_BYTES = BM * BK * 2, Q_BYTES = BM * BK / 2, B_BYTES = BN * BK * 2;
-  static constexpr int STAGE = A_BYTES + Q_BYTES + B_BYTES;
-  static constexpr int STAGES = SMEM_BUDGET / STAGE < 8 ? SMEM_BUDGET / STAGE : 8;
-  static constexpr int SMEM = STAGES * STAGE + 2048;
+  static constexpr int A_BYTES = BM * BK * 2, Q_BYTES = BM * BK / 2 * QC, B_BYTES = BN * BK * 2;
+  static constexpr int QS = BN <= 64 ? 4 : 3;
+  static constexpr int FIT = (SMEM_BUDGET - QS * Q_BYTES) / (A_BYTES + B_BYTES);
+  static constexpr int S = FIT < 8 ? FIT : 8;
+  static constexpr int SMEM = QS * Q_BYTES + S * (A_BYTES + B_BYTES) + 2048;
   static constexpr uint32_t TMEM_COLS = 2 * BN;  // 64, 128 or 256
-  static_assert(STAGES * (A_BYTES + B_BYTES) >= BM * BN * 4, "the ring holds a partial tile");
+  static_assert(S * (A_BYTES + B_BYTES) >= BM * BN * 4, "the ring holds a partial tile");
 };
 
 struct Args {
   const bf16* scale;
   int M, K, N;
-  int chunks, tiles, n_tiles, split, slice;  // chunks of 64 inputs; per CTA of a cluster (even)
+  int chunks, tiles, n_tiles, split, slice;  // chunks of 64 inputs; per CTA of a cluster (a multiple of QC)
   void* out;
   long long ldo;
   int accumulate;
@@ -74,14 +80,16 @@ template <int BN, int G, typename OutT>
 __global__ void __launch_bounds__(THREADS, 1)
     linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmX, Args a) {
   using C = Cfg<BN>;
-  constexpr int S = C::STAGES;
+  constexpr int S = C::S, QS = C::QS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stA = smem;
   uint8_t* stB = stA + S * C::A_BYTES;
   uint8_t* stQ = stB + S * C::B_BYTES;
-  uint64_t* raw_full = reinterpret_cast<uint64_t*>(stQ + S * C::Q_BYTES);  // codes and activations have landed
-  uint64_t* full = raw_full + S;                                           // the codes are converted
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(stQ + QS * C::Q_BYTES);  // a block of codes has landed
+  uint64_t* q_empty = q_full + QS;
+  uint64_t* raw_full = q_empty + QS;  // a chunk's activations have landed
+  uint64_t* full = raw_full + S;      // its codes are converted
   uint64_t* empty = full + S;
   uint64_t* acc_full = empty + S;
   uint64_t* acc_empty = acc_full + 2;
@@ -92,6 +100,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   pdl_launch_next();
   if (threadIdx.x == 0) {
+    for (int s = 0; s < QS; ++s) {
+      mbar_init(q_full + s, 1);
+      mbar_init(q_empty + s, CONV_THREADS);
+    }
     for (int s = 0; s < S; ++s) {
       mbar_init(raw_full + s, 1);
       mbar_init(full + s, CONV_GROUP);
@@ -124,34 +136,50 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == 0) {
     if (lane == 0) {
       const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
-      int stage = 0;
-      uint32_t phase = 0;
-      long issued = 0;
+      // The codes run ahead of the activations by as many blocks as their ring
+      // holds: block j is issued when chunk QC (j - QS + 1) is about to be.
+      const int nb = (c1 - c0 + QC - 1) / QC;  // blocks of a tile
+      const int mine = a.tiles > first ? (a.tiles - first + step - 1) / step : 0;
+      const long blocks = (long)mine * nb;
+      long qi = 0, issued = 0;
       bool ok = true;
-      for (int t = first; ok && t < a.tiles; t += step) {
-        const int nt = t % a.n_tiles, mt = t / a.n_tiles;
-        for (int c = c0; c < c1; ++c) {
-          if (!mbar_wait(empty + stage, phase ^ 1u, abort_flag, WAIT_NS)) {
-            *abort_flag = 1;
+      auto load_block = [&]() {
+        const int s = (int)(qi % QS), t = first + (int)(qi / nb) * step, b = (int)(qi % nb);
+        if (!mbar_wait(q_empty + s, ((uint32_t)(qi / QS) & 1u) ^ 1u, abort_flag, WAIT_NS)) return false;
+        mbar_arrive_expect_tx(q_full + s, C::Q_BYTES);
+        // (codes as pairs of bytes: 64 of them are 256 inputs)
+        tma_load_2d(stQ + s * C::Q_BYTES, &tmQ, q_full + s, (c0 / QC + b) * 64, t / a.n_tiles * BM, pol_w);
+        ++qi;
+        return true;
+      };
+      while (ok && qi < blocks && qi < QS - 1) ok = load_block();
+      for (int i = 0; ok && i < mine; ++i) {
+        const int nt = (first + i * step) % a.n_tiles;
+        for (int c = c0; ok && c < c1; ++c) {
+          if ((c - c0) % QC == 0 && qi < blocks && !load_block()) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(raw_full + stage, C::Q_BYTES + C::B_BYTES);
-          // (codes as pairs of bytes: 16 of them are 64 inputs)
-          tma_load_2d(stQ + stage * C::Q_BYTES, &tmQ, raw_full + stage, c * (BK / 4), mt * BM, pol_w);
-          tma_load_2d(stB + stage * C::B_BYTES, &tmX, raw_full + stage, c * BK, nt * BN, pol_x);
-          ++issued;
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
+          const int s = (int)(issued % S);
+          if (!mbar_wait(empty + s, ((uint32_t)(issued / S) & 1u) ^ 1u, abort_flag, WAIT_NS)) {
+            ok = false;
+            break;
           }
+          mbar_arrive_expect_tx(raw_full + s, C::B_BYTES);
+          tma_load_2d(stB + s * C::B_BYTES, &tmX, raw_full + s, c * BK, nt * BN, pol_x);
+          ++issued;
         }
       }
+      if (!ok) *abort_flag = 1;
       if (*abort_flag) {  // wait (bounded) for every copy this thread issued to land
+        volatile int never = 0;
         for (int s = 0; s < S; ++s) {
           const long cnt = issued / S + (s < issued % S ? 1 : 0);
-          volatile int never = 0;
           if (cnt > 0) mbar_wait(raw_full + s, (uint32_t)((cnt - 1) & 1), &never, WAIT_NS);
+        }
+        for (int s = 0; s < QS; ++s) {
+          const long cnt = qi / QS + (s < qi % QS ? 1 : 0);
+          if (cnt > 0) mbar_wait(q_full + s, (uint32_t)((cnt - 1) & 1), &never, WAIT_NS);
         }
       }
     }
@@ -204,31 +232,57 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp >= 2 + EPI_THREADS / 32) {
-    // converters: a group takes every CONV_GROUPS-th chunk, so that several are
-    // on their way; its thread ct takes 16 bytes (32 inputs) of four rows
+    // converters: group cg takes chunk cg of every block, so that several chunks
+    // are on their way; its thread ct takes 16 bytes (32 inputs) of four rows.
+    // (Both sides are in the 128-byte swizzle: piece i of row r lies at i ^ (r & 7).)
+    static_assert(CONV_GROUPS == QC, "a group for every chunk of a block");
     const int ct = (threadIdx.x - 64 - EPI_THREADS) % CONV_GROUP, cg = (threadIdx.x - 64 - EPI_THREADS) / CONV_GROUP;
-    const long total = a.tiles > first ? (long)((a.tiles - first + step - 1) / step) * (c1 - c0) : 0;  // chunks of this CTA
-    for (long i = cg; i < total; i += CONV_GROUPS) {
-      const int stage = (int)(i % S);
-      if (!mbar_wait(raw_full + stage, (uint32_t)(i / S) & 1u, abort_flag, WAIT_NS)) {
-        *abort_flag = 1;
-        break;
+    const int nb = (c1 - c0 + QC - 1) / QC;
+    long qi = 0, chunk0 = 0;  // blocks so far, and chunks of the tiles so far
+    bool ok = true;
+    for (int t = first; ok && t < a.tiles; t += step, chunk0 += c1 - c0) {
+      for (int b = 0; b < nb; ++b, ++qi) {
+        const int qs = (int)(qi % QS);
+        if (!mbar_wait(q_full + qs, (uint32_t)(qi / QS) & 1u, abort_flag, WAIT_NS)) {
+          ok = false;
+          break;
+        }
+        constexpr int P = BM * BK / 2 / 16 / CONV_GROUP;  // pieces of a thread
+        uint4 q[P];
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const int piece = ct + p * CONV_GROUP, r = piece >> 1, i = cg * 2 + (piece & 1);
+          q[p] = *reinterpret_cast<const uint4*>(stQ + qs * C::Q_BYTES + r * 128 + ((i ^ (r & 7)) << 4));
+        }
+        mbar_arrive(q_empty + qs);
+        const int c = b * QC + cg;
+        if (c < c1 - c0) {
+          const long idx = chunk0 + c;
+          const int stage = (int)(idx % S);
+          // The slot is free when the products of chunk idx - S are done.  (Not
+          // when this chunk's activations have landed: copies land in any order,
+          // and a parity cannot tell this chunk's from the one 2 S before it,
+          // which this group has not waited for.  Of the products, in order,
+          // those of chunk idx - S - QC at least are done: idx - 2 S is.)
+          static_assert(S >= QC, "a slot's parity is unambiguous");
+          if (!mbar_wait(empty + stage, ((uint32_t)(idx / S) & 1u) ^ 1u, abort_flag, WAIT_NS)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int p = 0; p < P; ++p) {
+            const int piece = ct + p * CONV_GROUP, r = piece >> 1, h = piece & 1;
+            uint8_t* row = stA + stage * C::A_BYTES + r * 128;
+            const uint32_t w[4] = {q[p].x, q[p].y, q[p].z, q[p].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(row + (((h * 4 + j) ^ (r & 7)) << 4)) = nibbles8(w[j]);
+          }
+          fence_proxy_async_smem();  // the operand is read by tcgen05.mma (async proxy)
+          mbar_arrive(full + stage);
+        }
       }
-      uint4 q[C::Q_BYTES / 16 / CONV_GROUP];
-#pragma unroll
-      for (int p = 0; p < C::Q_BYTES / 16 / CONV_GROUP; ++p)
-        q[p] = *reinterpret_cast<const uint4*>(stQ + stage * C::Q_BYTES + (ct + p * CONV_GROUP) * 16);
-#pragma unroll
-      for (int p = 0; p < C::Q_BYTES / 16 / CONV_GROUP; ++p) {
-        const int piece = ct + p * CONV_GROUP, r = piece >> 1, h = piece & 1;
-        uint8_t* row = stA + stage * C::A_BYTES + r * 128;
-        const uint32_t w[4] = {q[p].x, q[p].y, q[p].z, q[p].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(row + (((h * 4 + j) ^ (r & 7)) << 4)) = nibbles8(w[j]);
-      }
-      fence_proxy_async_smem();  // the operand is read by tcgen05.mma (async proxy)
-      mbar_arrive(full + stage);
     }
+    if (!ok) *abort_flag = 1;
   } else {
     // epilogue
     constexpr int COLS = BN / 2;
@@ -321,7 +375,7 @@ template <int BN, int G, typename OutT>
 int launch(const W4Op& g, const Ctx& c) {
   using C = Cfg<BN>;
   CUtensorMap mq, mx;
-  int rc = make_rows_map(&mq, g.codes, g.M, g.K / 4, g.K / 4, BK / 4, BM);
+  int rc = make_sw128_map(&mq, g.codes, g.M, g.K / 4, g.K / 4, BM);
   if (rc) return rc;
   rc = make_sw128_map(&mx, g.x, g.N, g.K, g.ldx, BN);
   if (rc) return rc;
@@ -335,7 +389,7 @@ int launch(const W4Op& g, const Ctx& c) {
   a.tiles = (g.M + BM - 1) / BM * a.n_tiles;
   // inputs split while that leaves every tile's cluster an SM each and a CTA at least 8 chunks
   a.split = std::max(1, std::min({8, c.nsm / a.tiles, a.chunks / 8}));
-  a.slice = ((a.chunks + a.split - 1) / a.split + 1) / 2 * 2;
+  a.slice = ((a.chunks + a.split - 1) / a.split + QC - 1) / QC * QC;
   a.out = g.out;
   a.ldo = g.ldo;
   a.accumulate = g.accumulate;
