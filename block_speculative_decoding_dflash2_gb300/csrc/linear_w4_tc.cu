@@ -4,10 +4,10 @@
 //
 // A 128-row weight tile is operand A of tcgen05.mma, BN activation rows are
 // operand B, and every group of inputs is summed on its own: the whole numbers
-// q - 8 are exact in bf16, a group's fp32 sums lie in one of two TMEM
+// q - 8 are exact in bf16, a group's fp32 sums lie in one of four TMEM
 // accumulators, and the epilogue warps read them, multiply them by the row's
 // group scale and add them to the row's sums in registers while the tensor
-// core fills the other one.  (Scaled weights would need 11 bits, three more
+// core fills the others.  (Scaled weights would need 11 bits, three more
 // than bf16 has.)
 //
 // Warp roles (576 threads, one CTA an SM):
@@ -38,7 +38,8 @@ constexpr int EPI_THREADS = 256, CONV_THREADS = CONV_GROUPS * CONV_GROUP, THREAD
 constexpr int SMEM_BUDGET = 227 * 1024 - 2048;  // 1 KB of alignment, 1 KB of barriers
 constexpr uint64_t WAIT_NS = 1000000000ull;
 
-constexpr int QC = 4;  // chunks of a block of codes (128 bytes of a row)
+constexpr int ACC = 4;  // TMEM accumulators
+constexpr int QC = 4;   // chunks of a block of codes (128 bytes of a row)
 
 // Two rings: blocks of codes, which set how many bytes are on their way (4 KB a
 // chunk in the operand ring were too few: 1.5 TB/s), and the operands of
@@ -50,7 +51,7 @@ struct Cfg {
   static constexpr int FIT = (SMEM_BUDGET - QS * Q_BYTES) / (A_BYTES + B_BYTES);
   static constexpr int S = FIT < 8 ? FIT : 8;
   static constexpr int SMEM = QS * Q_BYTES + S * (A_BYTES + B_BYTES) + 2048;
-  static constexpr uint32_t TMEM_COLS = 2 * BN;  // 64, 128 or 256
+  static constexpr uint32_t TMEM_COLS = ACC * BN;  // 128, 256 or 512
   static_assert(S * (A_BYTES + B_BYTES) >= BM * BN * 4, "the ring holds a partial tile");
 };
 
@@ -62,6 +63,21 @@ struct Args {
   long long ldo;
   int accumulate;
 };
+
+// Bounded wait for the phase of the given parity.  The clock, whose reading
+// takes longer than most waits, is looked at every 256 tries.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const uint32_t b = smem_u32(bar);
+  uint64_t t0 = 0;
+  for (unsigned i = 0;; ++i) {
+    if (mbar_try_wait(b, parity)) return true;
+    if ((i & 255) != 255) continue;
+    if (*abort) return false;
+    const uint64_t t = globaltimer();
+    if (t0 == 0) t0 = t;
+    else if (t - t0 > WAIT_NS) return false;
+  }
+}
 
 // 8 nibbles, in order, as bf16 values (128 + q) - 136 = q - 8.
 __device__ __forceinline__ uint4 nibbles8(uint32_t w) {
@@ -88,12 +104,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* stQ = stB + S * C::B_BYTES;
   uint64_t* q_full = reinterpret_cast<uint64_t*>(stQ + QS * C::Q_BYTES);  // a block of codes has landed
   uint64_t* q_empty = q_full + QS;
-  uint64_t* raw_full = q_empty + QS;  // a chunk's activations have landed
-  uint64_t* full = raw_full + S;      // its codes are converted
+  uint64_t* full = q_empty + QS;  // a chunk's activations have landed and its codes are converted
   uint64_t* empty = full + S;
   uint64_t* acc_full = empty + S;
-  uint64_t* acc_empty = acc_full + 2;
-  uint64_t* drain = acc_empty + 2;
+  uint64_t* acc_empty = acc_full + ACC;
+  uint64_t* drain = acc_empty + ACC;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);  // then the abort flag, in one 8-byte word
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -105,11 +120,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(q_empty + s, CONV_THREADS);
     }
     for (int s = 0; s < S; ++s) {
-      mbar_init(raw_full + s, 1);
-      mbar_init(full + s, CONV_GROUP);
+      mbar_init(full + s, 1 + CONV_GROUP);
       mbar_init(empty + s, 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < ACC; ++i) {
       mbar_init(acc_full + i, 1);
       mbar_init(acc_empty + i, EPI_THREADS);
     }
@@ -145,7 +159,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       bool ok = true;
       auto load_block = [&]() {
         const int s = (int)(qi % QS), t = first + (int)(qi / nb) * step, b = (int)(qi % nb);
-        if (!mbar_wait(q_empty + s, ((uint32_t)(qi / QS) & 1u) ^ 1u, abort_flag, WAIT_NS)) return false;
+        if (!wait_for(q_empty + s, ((uint32_t)(qi / QS) & 1u) ^ 1u, abort_flag)) return false;
         mbar_arrive_expect_tx(q_full + s, C::Q_BYTES);
         // (codes as pairs of bytes: 64 of them are 256 inputs)
         tma_load_2d(stQ + s * C::Q_BYTES, &tmQ, q_full + s, (c0 / QC + b) * 64, t / a.n_tiles * BM, pol_w);
@@ -161,25 +175,24 @@ __global__ void __launch_bounds__(THREADS, 1)
             break;
           }
           const int s = (int)(issued % S);
-          if (!mbar_wait(empty + s, ((uint32_t)(issued / S) & 1u) ^ 1u, abort_flag, WAIT_NS)) {
+          if (!wait_for(empty + s, ((uint32_t)(issued / S) & 1u) ^ 1u, abort_flag)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(raw_full + s, C::B_BYTES);
-          tma_load_2d(stB + s * C::B_BYTES, &tmX, raw_full + s, c * BK, nt * BN, pol_x);
+          mbar_arrive_expect_tx(full + s, C::B_BYTES);
+          tma_load_2d(stB + s * C::B_BYTES, &tmX, full + s, c * BK, nt * BN, pol_x);
           ++issued;
         }
       }
       if (!ok) *abort_flag = 1;
       if (*abort_flag) {  // wait (bounded) for every copy this thread issued to land
         volatile int never = 0;
-        for (int s = 0; s < S; ++s) {
-          const long cnt = issued / S + (s < issued % S ? 1 : 0);
-          if (cnt > 0) mbar_wait(raw_full + s, (uint32_t)((cnt - 1) & 1), &never, WAIT_NS);
-        }
+        // (the activations' barriers also count converters that may have left:
+        // a millisecond, some hundred times what a copy takes, stands for them)
+        for (const uint64_t t = globaltimer(); globaltimer() - t < 1000000;) {}
         for (int s = 0; s < QS; ++s) {
           const long cnt = qi / QS + (s < qi % QS ? 1 : 0);
-          if (cnt > 0) mbar_wait(q_full + s, (uint32_t)((cnt - 1) & 1), &never, WAIT_NS);
+          if (cnt > 0) wait_for(q_full + s, (uint32_t)((cnt - 1) & 1), &never);
         }
       }
     }
@@ -192,8 +205,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       bool ok = true;
       for (int t = first; ok && t < a.tiles; t += step) {
         for (int c = c0; ok && c < c1; ++c) {
-          if (!mbar_wait(full + stage, phase, abort_flag, WAIT_NS) ||
-              !mbar_wait(raw_full + stage, phase, abort_flag, WAIT_NS)) {
+          if (!wait_for(full + stage, phase, abort_flag)) {
             ok = false;
             break;
           }
@@ -205,7 +217,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool begin = G == 128 ? (c & 1) == 0 && kk == 0 : kk % (G / 16) == 0;
             const bool end = G == 128 ? ((c & 1) || c + 1 == c1) && kk == 3 : kk % (G / 16) == G / 16 - 1;
             if (begin) {
-              if (!mbar_wait(acc_empty + buf, acc_phase ^ 1u, abort_flag, WAIT_NS)) {
+              if (!wait_for(acc_empty + buf, acc_phase ^ 1u, abort_flag)) {
                 ok = false;
                 break;
               }
@@ -214,8 +226,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             umma_bf16(tmem + (uint32_t)(buf * BN), ad + 2u * kk, bd + 2u * kk, idesc, begin ? 0u : 1u);
             if (end) {
               umma_commit(acc_full + buf);
-              buf ^= 1;
-              if (buf == 0) acc_phase ^= 1u;
+              if (++buf == ACC) {
+                buf = 0;
+                acc_phase ^= 1u;
+              }
             }
           }
           umma_commit(empty + stage);
@@ -228,7 +242,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!ok) *abort_flag = 1;
       umma_commit(drain);  // every product of this thread completes before TMEM can be freed
       volatile int never = 0;
-      mbar_wait(drain, 0, &never, WAIT_NS);
+      wait_for(drain, 0, &never);
     }
     __syncwarp();
   } else if (warp >= 2 + EPI_THREADS / 32) {
@@ -243,7 +257,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int t = first; ok && t < a.tiles; t += step, chunk0 += c1 - c0) {
       for (int b = 0; b < nb; ++b, ++qi) {
         const int qs = (int)(qi % QS);
-        if (!mbar_wait(q_full + qs, (uint32_t)(qi / QS) & 1u, abort_flag, WAIT_NS)) {
+        if (!wait_for(q_full + qs, (uint32_t)(qi / QS) & 1u, abort_flag)) {
           ok = false;
           break;
         }
@@ -265,7 +279,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           // which this group has not waited for.  Of the products, in order,
           // those of chunk idx - S - QC at least are done: idx - 2 S is.)
           static_assert(S >= QC, "a slot's parity is unambiguous");
-          if (!mbar_wait(empty + stage, ((uint32_t)(idx / S) & 1u) ^ 1u, abort_flag, WAIT_NS)) {
+          if (!wait_for(empty + stage, ((uint32_t)(idx / S) & 1u) ^ 1u, abort_flag)) {
             ok = false;
             break;
           }
@@ -302,7 +316,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float s = s_next;
         s_next = g + 1 < min(g1, groups) ? __bfloat162float(srow[g + 1]) : 0.f;
         // (the whole warp goes on or gives up: TMEM reads are warp-wide)
-        const bool got = mbar_wait(acc_full + buf, acc_phase, abort_flag, WAIT_NS);
+        const bool got = wait_for(acc_full + buf, acc_phase, abort_flag);
         if (!__all_sync(0xffffffffu, got)) {
           *abort_flag = 1;
           ok = false;
@@ -319,8 +333,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         tc_fence_before();
         mbar_arrive(acc_empty + buf);
-        buf ^= 1;
-        if (buf == 0) acc_phase ^= 1u;
+        if (++buf == ACC) {
+          buf = 0;
+          acc_phase ^= 1u;
+        }
       }
       if (!ok) {
 #pragma unroll
