@@ -2,8 +2,8 @@
 // tensor cores (the definition, and the kernel for few rows, are in
 // linear_w4.cu).
 //
-// A 128-row weight tile is operand A of tcgen05.mma, BN activation rows are
-// operand B, and every group of inputs is summed on its own: the whole numbers
+// A 128-row weight tile is operand A of tcgen05.mma, held in TMEM, BN
+// activation rows are operand B in shared memory, and every group of inputs is summed on its own: the whole numbers
 // q - 8 are exact in bf16, a group's fp32 sums lie in one of four TMEM
 // accumulators, and the epilogue warps read them, multiply them by the row's
 // group scale and add them to the row's sums in registers while the tensor
@@ -14,8 +14,14 @@
 //   warp 0       TMA producer (one lane): codes and activations -> ring
 //   warp 1       MMA issuer (one lane) and TMEM owner
 //   warps 2-9    epilogue: two sets of four, each with half of the columns
-//   warps 10-17  converters, in four groups: 32 bytes of codes of a row -> 64
-//                bf16 values in the swizzled operand layout
+//   warps 10-17  converters, in two groups of four on alternate chunks:
+//                thread = weight row, its 32 bytes of codes -> 64 bf16 values
+//                in 32 columns of its TMEM lane
+// Operand A in TMEM because shared memory bounds the alternative: reading both
+// operands of a 128 x 128 product takes all of its 128 bytes a cycle, and
+// writing the converted tile as much again as a copy of the activations
+// (measured with A in shared memory: 830 cycles a chunk of 64 inputs whatever
+// BN, where the products alone take 260 at BN = 128).
 // With few tiles the inputs are split over a cluster, whose partial tiles are
 // added in rank order through distributed shared memory.
 //
@@ -33,26 +39,26 @@ namespace df2 {
 namespace {
 
 constexpr int BM = 128, BK = 64;
-constexpr int CONV_GROUPS = 4, CONV_GROUP = 64;  // converters: groups of two warps on alternate chunks
+constexpr int CONV_GROUPS = 2, CONV_GROUP = 128;
 constexpr int EPI_THREADS = 256, CONV_THREADS = CONV_GROUPS * CONV_GROUP, THREADS = 64 + EPI_THREADS + CONV_THREADS;
 constexpr int SMEM_BUDGET = 227 * 1024 - 2048;  // 1 KB of alignment, 1 KB of barriers
 constexpr uint64_t WAIT_NS = 1000000000ull;
 
-constexpr int ACC = 4;  // TMEM accumulators
-constexpr int QC = 4;   // chunks of a block of codes (128 bytes of a row)
+constexpr int QC = 4;            // chunks of a block of codes (128 bytes of a row)
+constexpr int A_COLS = BK / 2;   // TMEM columns of a chunk's operand A
+constexpr uint32_t TMEM_COLS = 512;
 
-// Two rings: blocks of codes, which set how many bytes are on their way (4 KB a
-// chunk in the operand ring were too few: 1.5 TB/s), and the operands of
-// single chunks.
+// Rings: blocks of codes, which set how many bytes are on their way, and the
+// operands of single chunks (A in TMEM, B in shared memory).
 template <int BN>
 struct Cfg {
-  static constexpr int A_BYTES = BM * BK * 2, Q_BYTES = BM * BK / 2 * QC, B_BYTES = BN * BK * 2;
-  static constexpr int QS = BN <= 64 ? 4 : 3;
-  static constexpr int FIT = (SMEM_BUDGET - QS * Q_BYTES) / (A_BYTES + B_BYTES);
-  static constexpr int S = FIT < 8 ? FIT : 8;
-  static constexpr int SMEM = QS * Q_BYTES + S * (A_BYTES + B_BYTES) + 2048;
-  static constexpr uint32_t TMEM_COLS = ACC * BN;  // 128, 256 or 512
-  static_assert(S * (A_BYTES + B_BYTES) >= BM * BN * 4, "the ring holds a partial tile");
+  static constexpr int Q_BYTES = BM * BK / 2 * QC, B_BYTES = BN * BK * 2;
+  static constexpr int S = 8, QS = BN == 128 ? 5 : 6;
+  static constexpr int ACC = BN == 128 ? 2 : 4;  // accumulators
+  static constexpr int SMEM = QS * Q_BYTES + S * B_BYTES + 2048;
+  static_assert(SMEM <= SMEM_BUDGET + 2048, "shared memory");
+  static_assert(ACC * BN + S * A_COLS <= (int)TMEM_COLS, "TMEM");
+  static_assert(S * B_BYTES >= BM * BN * 4, "the ring holds a partial tile");
 };
 
 struct Args {
@@ -92,15 +98,25 @@ __device__ __forceinline__ uint4 nibbles8(uint32_t w) {
   return make_uint4(two(p01, 0x4140), two(p01, 0x4342), two(p23, 0x4140), two(p23, 0x4342));
 }
 
+// D[tmem] (+)= A[tmem] * B[smem]^T: A's rows are lanes, two bf16 of a row a column.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 template <int BN, int G, typename OutT>
 __global__ void __launch_bounds__(THREADS, 1)
     linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmX, Args a) {
   using C = Cfg<BN>;
-  constexpr int S = C::S, QS = C::QS;
+  constexpr int S = C::S, QS = C::QS, ACC = C::ACC;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* stA = smem;
-  uint8_t* stB = stA + S * C::A_BYTES;
+  uint8_t* stB = smem;
   uint8_t* stQ = stB + S * C::B_BYTES;
   uint64_t* q_full = reinterpret_cast<uint64_t*>(stQ + QS * C::Q_BYTES);  // a block of codes has landed
   uint64_t* q_empty = q_full + QS;
@@ -134,13 +150,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     tma_prefetch_desc(&tmX);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = *tmem_slot, tmem_a = tmem + ACC * BN;  // accumulators, then the A ring
   pdl_wait();
 
   const int rank = blockIdx.x % a.split, first = blockIdx.x / a.split, step = gridDim.x / a.split;
@@ -210,7 +226,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             break;
           }
           tc_fence_after();
-          const uint64_t ad = sdesc_sw128(smem_u32(stA + stage * C::A_BYTES));
+          const uint32_t at = tmem_a + (uint32_t)(stage * A_COLS);
           const uint64_t bd = sdesc_sw128(smem_u32(stB + stage * C::B_BYTES));
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk) {
@@ -223,7 +239,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               }
               tc_fence_after();
             }
-            umma_bf16(tmem + (uint32_t)(buf * BN), ad + 2u * kk, bd + 2u * kk, idesc, begin ? 0u : 1u);
+            umma_bf16_ts(tmem + (uint32_t)(buf * BN), at + 8u * kk, bd + 2u * kk, idesc, begin ? 0u : 1u);
             if (end) {
               umma_commit(acc_full + buf);
               if (++buf == ACC) {
@@ -246,54 +262,58 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp >= 2 + EPI_THREADS / 32) {
-    // converters: group cg takes chunk cg of every block, so that several chunks
-    // are on their way; its thread ct takes 16 bytes (32 inputs) of four rows.
-    // (Both sides are in the 128-byte swizzle: piece i of row r lies at i ^ (r & 7).)
-    static_assert(CONV_GROUPS == QC, "a group for every chunk of a block");
-    const int ct = (threadIdx.x - 64 - EPI_THREADS) % CONV_GROUP, cg = (threadIdx.x - 64 - EPI_THREADS) / CONV_GROUP;
+    // converters: group cg takes chunks cg, cg + 2 of every block; the codes lie
+    // in the 128-byte swizzle (piece i of row r at i ^ (r & 7))
+    const int cw = warp - 2 - EPI_THREADS / 32, cg = cw / 4, q = warp & 3, r = q * 32 + lane;
     const int nb = (c1 - c0 + QC - 1) / QC;
     long qi = 0, chunk0 = 0;  // blocks so far, and chunks of the tiles so far
     bool ok = true;
     for (int t = first; ok && t < a.tiles; t += step, chunk0 += c1 - c0) {
-      for (int b = 0; b < nb; ++b, ++qi) {
+      for (int b = 0; ok && b < nb; ++b, ++qi) {
         const int qs = (int)(qi % QS);
-        if (!wait_for(q_full + qs, (uint32_t)(qi / QS) & 1u, abort_flag)) {
-          ok = false;
-          break;
-        }
-        constexpr int P = BM * BK / 2 / 16 / CONV_GROUP;  // pieces of a thread
-        uint4 q[P];
+        bool got = wait_for(q_full + qs, (uint32_t)(qi / QS) & 1u, abort_flag);
+        uint4 codes[QC / CONV_GROUPS][2];
+        if (got) {
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const int piece = ct + p * CONV_GROUP, r = piece >> 1, i = cg * 2 + (piece & 1);
-          q[p] = *reinterpret_cast<const uint4*>(stQ + qs * C::Q_BYTES + r * 128 + ((i ^ (r & 7)) << 4));
+          for (int k = 0; k < QC / CONV_GROUPS; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int i = (cg + k * CONV_GROUPS) * 2 + h;
+              codes[k][h] = *reinterpret_cast<const uint4*>(stQ + qs * C::Q_BYTES + r * 128 + ((i ^ (r & 7)) << 4));
+            }
+          mbar_arrive(q_empty + qs);
         }
-        mbar_arrive(q_empty + qs);
-        const int c = b * QC + cg;
-        if (c < c1 - c0) {
+#pragma unroll
+        for (int k = 0; k < QC / CONV_GROUPS; ++k) {
+          const int c = b * QC + cg + k * CONV_GROUPS;
+          if (c >= c1 - c0) break;
           const long idx = chunk0 + c;
           const int stage = (int)(idx % S);
-          // The slot is free when the products of chunk idx - S are done.  (Not
-          // when this chunk's activations have landed: copies land in any order,
-          // and a parity cannot tell this chunk's from the one 2 S before it,
-          // which this group has not waited for.  Of the products, in order,
-          // those of chunk idx - S - QC at least are done: idx - 2 S is.)
-          static_assert(S >= QC, "a slot's parity is unambiguous");
-          if (!wait_for(empty + stage, ((uint32_t)(idx / S) & 1u) ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
+          // The slot is free when the products of chunk idx - S are done.
+          // (Products are done in order, and this group has waited for those of
+          // idx - CONV_GROUPS - S: the barrier cannot be two phases behind,
+          // which a parity could not tell.)
+          static_assert(S >= CONV_GROUPS, "a slot's parity is unambiguous");
+          got = got && wait_for(empty + stage, ((uint32_t)(idx / S) & 1u) ^ 1u, abort_flag);
+          ok = __all_sync(0xffffffffu, got);  // TMEM stores are warp-wide
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t dst = tmem_a + ((uint32_t)(q * 32) << 16) + (uint32_t)(stage * A_COLS);
 #pragma unroll
-          for (int p = 0; p < P; ++p) {
-            const int piece = ct + p * CONV_GROUP, r = piece >> 1, h = piece & 1;
-            uint8_t* row = stA + stage * C::A_BYTES + r * 128;
-            const uint32_t w[4] = {q[p].x, q[p].y, q[p].z, q[p].w};
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t w[4] = {codes[k][h].x, codes[k][h].y, codes[k][h].z, codes[k][h].w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(row + (((h * 4 + j) ^ (r & 7)) << 4)) = nibbles8(w[j]);
+            for (int j = 0; j < 4; j += 2) {
+              const uint4 x = nibbles8(w[j]), y = nibbles8(w[j + 1]);
+              const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+              tmem_st8(dst + h * 16 + j * 4, v);
+            }
           }
-          fence_proxy_async_smem();  // the operand is read by tcgen05.mma (async proxy)
+          tmem_st_wait();
+          tc_fence_before();
           mbar_arrive(full + stage);
         }
+        ok = __all_sync(0xffffffffu, got);
       }
     }
     if (!ok) *abort_flag = 1;
@@ -384,7 +404,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, C::TMEM_COLS);
+  if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
 }
 
 template <int BN, int G, typename OutT>
