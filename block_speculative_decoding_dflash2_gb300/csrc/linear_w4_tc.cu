@@ -70,6 +70,12 @@ struct Args {
   int accumulate;
 };
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // Bounded wait for the phase of the given parity.  The clock, whose reading
 // takes longer than most waits, is looked at every 256 tries.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
@@ -127,7 +133,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* drain = acc_empty + ACC;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);  // then the abort flag, in one 8-byte word
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the shuffle tells the compiler that the warp index is uniform)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   pdl_launch_next();
   if (threadIdx.x == 0) {
@@ -214,48 +221,48 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(BM, BN);
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      bool ok = true;
-      for (int t = first; ok && t < a.tiles; t += step) {
-        for (int c = c0; ok && c < c1; ++c) {
-          if (!wait_for(full + stage, phase, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t at = tmem_a + (uint32_t)(stage * A_COLS);
-          const uint64_t bd = sdesc_sw128(smem_u32(stB + stage * C::B_BYTES));
+    // The whole warp walks the chunks, so that descriptors stay in uniform
+    // registers; one lane issues.
+    const bool leader = elect_one();
+    constexpr uint32_t idesc = idesc_bf16_f32(BM, BN);
+    int stage = 0, buf = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true;
+    for (int t = first; ok && t < a.tiles; t += step) {
+      for (int c = c0; c < c1; ++c) {
+        ok = __all_sync(0xffffffffu, wait_for(full + stage, phase, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t at = tmem_a + (uint32_t)(stage * A_COLS);
+        const uint64_t bd = sdesc_sw128(smem_u32(stB + stage * C::B_BYTES));
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const bool begin = G == 128 ? (c & 1) == 0 && kk == 0 : kk % (G / 16) == 0;
-            const bool end = G == 128 ? ((c & 1) || c + 1 == c1) && kk == 3 : kk % (G / 16) == G / 16 - 1;
-            if (begin) {
-              if (!wait_for(acc_empty + buf, acc_phase ^ 1u, abort_flag)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-            }
-            umma_bf16_ts(tmem + (uint32_t)(buf * BN), at + 8u * kk, bd + 2u * kk, idesc, begin ? 0u : 1u);
-            if (end) {
-              umma_commit(acc_full + buf);
-              if (++buf == ACC) {
-                buf = 0;
-                acc_phase ^= 1u;
-              }
-            }
+        for (int kk = 0; kk < BK / 16; ++kk) {
+          const bool begin = G == 128 ? (c & 1) == 0 && kk == 0 : kk % (G / 16) == 0;
+          const bool end = G == 128 ? ((c & 1) || c + 1 == c1) && kk == 3 : kk % (G / 16) == G / 16 - 1;
+          if (begin) {
+            ok = __all_sync(0xffffffffu, wait_for(acc_empty + buf, acc_phase ^ 1u, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
           }
-          umma_commit(empty + stage);
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
+          if (leader) umma_bf16_ts(tmem + (uint32_t)(buf * BN), at + 8u * kk, bd + 2u * kk, idesc, begin ? 0u : 1u);
+          if (end) {
+            if (leader) umma_commit(acc_full + buf);
+            if (++buf == ACC) {
+              buf = 0;
+              acc_phase ^= 1u;
+            }
           }
         }
+        if (!ok) break;
+        if (leader) umma_commit(empty + stage);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      if (!ok) *abort_flag = 1;
+    }
+    if (!ok) *abort_flag = 1;
+    if (leader) {
       umma_commit(drain);  // every product of this thread completes before TMEM can be freed
       volatile int never = 0;
       wait_for(drain, 0, &never);
