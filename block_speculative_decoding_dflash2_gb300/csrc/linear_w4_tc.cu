@@ -170,54 +170,62 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int c0 = min(a.chunks, rank * a.slice), c1 = min(a.chunks, c0 + a.slice);
   float* part = reinterpret_cast<float*>(smem);  // [BN][BM], in the idle ring
 
+  const int nb = (c1 - c0 + QC - 1) / QC;  // blocks of codes of a tile
   if (warp == 0) {
-    if (lane == 0) {
-      const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
-      // The codes run ahead of the activations by as many blocks as their ring
-      // holds: block j is issued when chunk QC (j - QS + 1) is about to be.
-      const int nb = (c1 - c0 + QC - 1) / QC;  // blocks of a tile
-      const int mine = a.tiles > first ? (a.tiles - first + step - 1) / step : 0;
-      const long blocks = (long)mine * nb;
-      long qi = 0, issued = 0;
-      bool ok = true;
-      auto load_block = [&]() {
-        const int s = (int)(qi % QS), t = first + (int)(qi / nb) * step, b = (int)(qi % nb);
-        if (!wait_for(q_empty + s, ((uint32_t)(qi / QS) & 1u) ^ 1u, abort_flag)) return false;
-        mbar_arrive_expect_tx(q_full + s, C::Q_BYTES);
+    // (as the MMA warp: all lanes walk, one issues)
+    const bool leader = elect_one();
+    const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
+    // The codes run ahead of the activations by QS - 1 blocks.
+    int qs = 0, qb = 0, qt = first;  // next block's ring slot, its number in its tile, and its tile
+    int s = 0, issued = 0, loaded = 0;
+    uint32_t q_phase = 0, phase = 0;
+    bool ok = true;
+    auto load_block = [&]() {
+      if (!__all_sync(0xffffffffu, wait_for(q_empty + qs, q_phase ^ 1u, abort_flag))) return false;
+      if (leader) {
+        mbar_arrive_expect_tx(q_full + qs, C::Q_BYTES);
         // (codes as pairs of bytes: 64 of them are 256 inputs)
-        tma_load_2d(stQ + s * C::Q_BYTES, &tmQ, q_full + s, (c0 / QC + b) * 64, t / a.n_tiles * BM, pol_w);
-        ++qi;
-        return true;
-      };
-      while (ok && qi < blocks && qi < QS - 1) ok = load_block();
-      for (int i = 0; ok && i < mine; ++i) {
-        const int nt = (first + i * step) % a.n_tiles;
-        for (int c = c0; ok && c < c1; ++c) {
-          if ((c - c0) % QC == 0 && qi < blocks && !load_block()) {
-            ok = false;
-            break;
-          }
-          const int s = (int)(issued % S);
-          if (!wait_for(empty + s, ((uint32_t)(issued / S) & 1u) ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
+        tma_load_2d(stQ + qs * C::Q_BYTES, &tmQ, q_full + qs, (c0 / QC + qb) * 64, qt / a.n_tiles * BM, pol_w);
+      }
+      if (loaded < QS) ++loaded;
+      if (++qs == QS) {
+        qs = 0;
+        q_phase ^= 1u;
+      }
+      if (++qb == nb) {
+        qb = 0;
+        qt += step;
+      }
+      return true;
+    };
+    if (nb > 0)
+      for (int i = 0; ok && i < QS - 1 && qt < a.tiles; ++i) ok = load_block();
+    for (int t = first; ok && t < a.tiles; t += step) {
+      const int nt = t % a.n_tiles;
+      for (int c = c0; c < c1; ++c) {
+        if ((c - c0) % QC == 0 && qt < a.tiles) {
+          ok = load_block();
+          if (!ok) break;
+        }
+        ok = __all_sync(0xffffffffu, wait_for(empty + s, phase ^ 1u, abort_flag));
+        if (!ok) break;
+        if (leader) {
           mbar_arrive_expect_tx(full + s, C::B_BYTES);
           tma_load_2d(stB + s * C::B_BYTES, &tmX, full + s, c * BK, nt * BN, pol_x);
-          ++issued;
+        }
+        issued = 1;
+        if (++s == S) {
+          s = 0;
+          phase ^= 1u;
         }
       }
-      if (!ok) *abort_flag = 1;
-      if (*abort_flag) {  // wait (bounded) for every copy this thread issued to land
-        volatile int never = 0;
-        // (the activations' barriers also count converters that may have left:
-        // a millisecond, some hundred times what a copy takes, stands for them)
-        for (const uint64_t t = globaltimer(); globaltimer() - t < 1000000;) {}
-        for (int s = 0; s < QS; ++s) {
-          const long cnt = qi / QS + (s < qi % QS ? 1 : 0);
-          if (cnt > 0) wait_for(q_full + s, (uint32_t)((cnt - 1) & 1), &never);
-        }
-      }
+    }
+    if (!ok) *abort_flag = 1;
+    if (*abort_flag && (issued || loaded)) {
+      // Copies of this warp may be in flight, on barriers that also count
+      // converters which may have left: a millisecond, some hundred times what
+      // a copy takes, stands for waiting on them.
+      for (const uint64_t t = globaltimer(); globaltimer() - t < 1000000;) {}
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -272,13 +280,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     // converters: group cg takes chunks cg, cg + 2 of every block; the codes lie
     // in the 128-byte swizzle (piece i of row r at i ^ (r & 7))
     const int cw = warp - 2 - EPI_THREADS / 32, cg = cw / 4, q = warp & 3, r = q * 32 + lane;
-    const int nb = (c1 - c0 + QC - 1) / QC;
-    long qi = 0, chunk0 = 0;  // blocks so far, and chunks of the tiles so far
+    int qs = 0;
+    uint32_t q_phase = 0, chunk0 = 0;  // (chunks of the tiles so far: only the last bits are used)
     bool ok = true;
     for (int t = first; ok && t < a.tiles; t += step, chunk0 += c1 - c0) {
-      for (int b = 0; ok && b < nb; ++b, ++qi) {
-        const int qs = (int)(qi % QS);
-        bool got = wait_for(q_full + qs, (uint32_t)(qi / QS) & 1u, abort_flag);
+      for (int b = 0; ok && b < nb; ++b) {
+        bool got = wait_for(q_full + qs, q_phase, abort_flag);
         uint4 codes[QC / CONV_GROUPS][2];
         if (got) {
 #pragma unroll
@@ -294,14 +301,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int k = 0; k < QC / CONV_GROUPS; ++k) {
           const int c = b * QC + cg + k * CONV_GROUPS;
           if (c >= c1 - c0) break;
-          const long idx = chunk0 + c;
-          const int stage = (int)(idx % S);
+          const uint32_t idx = chunk0 + c;
+          const int stage = idx % S;
           // The slot is free when the products of chunk idx - S are done.
           // (Products are done in order, and this group has waited for those of
           // idx - CONV_GROUPS - S: the barrier cannot be two phases behind,
           // which a parity could not tell.)
           static_assert(S >= CONV_GROUPS, "a slot's parity is unambiguous");
-          got = got && wait_for(empty + stage, ((uint32_t)(idx / S) & 1u) ^ 1u, abort_flag);
+          got = got && wait_for(empty + stage, (idx / S & 1u) ^ 1u, abort_flag);
           ok = __all_sync(0xffffffffu, got);  // TMEM stores are warp-wide
           if (!ok) break;
           tc_fence_after();
@@ -321,6 +328,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           mbar_arrive(full + stage);
         }
         ok = __all_sync(0xffffffffu, got);
+        if (++qs == QS) {
+          qs = 0;
+          q_phase ^= 1u;
+        }
       }
     }
     if (!ok) *abort_flag = 1;
