@@ -15,13 +15,11 @@
 //   warp 1       MMA issuer (one lane) and TMEM owner
 //   warps 2-9    epilogue: two sets of four, each with half of the columns
 //   warps 10-17  converters, in two groups of four on alternate chunks:
-//                thread = weight row, its 32 bytes of codes -> 64 bf16 values
-//                in 32 columns of its TMEM lane
+//                thread = weight row, its 64 bytes of codes -> 128 bf16 values
+//                in 64 columns of its TMEM lane
 // Operand A in TMEM because shared memory bounds the alternative: reading both
 // operands of a 128 x 128 product takes all of its 128 bytes a cycle, and
-// writing the converted tile as much again as a copy of the activations
-// (measured with A in shared memory: 830 cycles a chunk of 64 inputs whatever
-// BN, where the products alone take 260 at BN = 128).
+// writing the converted tile as much again as a copy of the activations.
 // With few tiles the inputs are split over a cluster, whose partial tiles are
 // added in rank order through distributed shared memory.
 //
@@ -38,13 +36,13 @@ namespace df2 {
 
 namespace {
 
-constexpr int BM = 128, BK = 64;
+constexpr int BM = 128, BK = 128;  // weight rows of a tile, inputs of a chunk
 constexpr int CONV_GROUPS = 2, CONV_GROUP = 128;
 constexpr int EPI_THREADS = 256, CONV_THREADS = CONV_GROUPS * CONV_GROUP, THREADS = 64 + EPI_THREADS + CONV_THREADS;
 constexpr int SMEM_BUDGET = 227 * 1024 - 2048;  // 1 KB of alignment, 1 KB of barriers
 constexpr uint64_t WAIT_NS = 1000000000ull;
 
-constexpr int QC = 4;            // chunks of a block of codes (128 bytes of a row)
+constexpr int QC = 2;            // chunks of a block of codes (128 bytes of a row)
 constexpr int A_COLS = BK / 2;   // TMEM columns of a chunk's operand A
 constexpr uint32_t TMEM_COLS = 512;
 
@@ -53,7 +51,7 @@ constexpr uint32_t TMEM_COLS = 512;
 template <int BN>
 struct Cfg {
   static constexpr int Q_BYTES = BM * BK / 2 * QC, B_BYTES = BN * BK * 2;
-  static constexpr int S = 8, QS = BN == 128 ? 5 : 6;
+  static constexpr int S = 4, QS = BN == 128 ? 5 : 6;
   static constexpr int ACC = BN == 128 ? 2 : 4;  // accumulators
   static constexpr int SMEM = QS * Q_BYTES + S * B_BYTES + 2048;
   static_assert(SMEM <= SMEM_BUDGET + 2048, "shared memory");
@@ -64,7 +62,7 @@ struct Cfg {
 struct Args {
   const bf16* scale;
   int M, K, N;
-  int chunks, tiles, n_tiles, split, slice;  // chunks of 64 inputs; per CTA of a cluster (a multiple of QC)
+  int chunks, tiles, n_tiles, split, slice;  // chunks of 128 inputs; per CTA of a cluster (a multiple of QC)
   void* out;
   long long ldo;
   int accumulate;
@@ -185,7 +183,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (leader) {
         mbar_arrive_expect_tx(q_full + qs, C::Q_BYTES);
         // (codes as pairs of bytes: 64 of them are 256 inputs)
-        tma_load_2d(stQ + qs * C::Q_BYTES, &tmQ, q_full + qs, (c0 / QC + qb) * 64, qt / a.n_tiles * BM, pol_w);
+        tma_load_2d(stQ + qs * C::Q_BYTES, &tmQ, q_full + qs, (c0 / QC + qb) * (QC * BK / 4), qt / a.n_tiles * BM, pol_w);
       }
       if (loaded < QS) ++loaded;
       if (++qs == QS) {
@@ -211,7 +209,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         if (leader) {
           mbar_arrive_expect_tx(full + s, C::B_BYTES);
+          // (two halves of 64 inputs, each in the 128-byte swizzle)
           tma_load_2d(stB + s * C::B_BYTES, &tmX, full + s, c * BK, nt * BN, pol_x);
+          tma_load_2d(stB + s * C::B_BYTES + C::B_BYTES / 2, &tmX, full + s, c * BK + 64, nt * BN, pol_x);
         }
         issued = 1;
         if (++s == S) {
@@ -245,14 +245,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint64_t bd = sdesc_sw128(smem_u32(stB + stage * C::B_BYTES));
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk) {
-          const bool begin = G == 128 ? (c & 1) == 0 && kk == 0 : kk % (G / 16) == 0;
-          const bool end = G == 128 ? ((c & 1) || c + 1 == c1) && kk == 3 : kk % (G / 16) == G / 16 - 1;
+          const bool begin = kk % (G / 16) == 0, end = kk % (G / 16) == G / 16 - 1;
           if (begin) {
             ok = __all_sync(0xffffffffu, wait_for(acc_empty + buf, acc_phase ^ 1u, abort_flag));
             if (!ok) break;
             tc_fence_after();
           }
-          if (leader) umma_bf16_ts(tmem + (uint32_t)(buf * BN), at + 8u * kk, bd + 2u * kk, idesc, begin ? 0u : 1u);
+          if (leader) umma_bf16_ts(tmem + (uint32_t)(buf * BN), at + 8u * kk, bd + (uint64_t)((kk >> 2) * (C::B_BYTES / 32) + 2 * (kk & 3)),
+                                   idesc, begin ? 0u : 1u);
           if (end) {
             if (leader) umma_commit(acc_full + buf);
             if (++buf == ACC) {
@@ -277,8 +277,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp >= 2 + EPI_THREADS / 32) {
-    // converters: group cg takes chunks cg, cg + 2 of every block; the codes lie
-    // in the 128-byte swizzle (piece i of row r at i ^ (r & 7))
+    // converters: group cg takes chunk cg of every block; the codes lie in the
+    // 128-byte swizzle (piece i of row r at i ^ (r & 7))
     const int cw = warp - 2 - EPI_THREADS / 32, cg = cw / 4, q = warp & 3, r = q * 32 + lane;
     int qs = 0;
     uint32_t q_phase = 0, chunk0 = 0;  // (chunks of the tiles so far: only the last bits are used)
@@ -286,36 +286,32 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int t = first; ok && t < a.tiles; t += step, chunk0 += c1 - c0) {
       for (int b = 0; ok && b < nb; ++b) {
         bool got = wait_for(q_full + qs, q_phase, abort_flag);
-        uint4 codes[QC / CONV_GROUPS][2];
+        uint4 codes[4];
         if (got) {
 #pragma unroll
-          for (int k = 0; k < QC / CONV_GROUPS; ++k)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int i = (cg + k * CONV_GROUPS) * 2 + h;
-              codes[k][h] = *reinterpret_cast<const uint4*>(stQ + qs * C::Q_BYTES + r * 128 + ((i ^ (r & 7)) << 4));
-            }
+          for (int h = 0; h < 4; ++h)
+            codes[h] = *reinterpret_cast<const uint4*>(stQ + qs * C::Q_BYTES + r * 128 + (((cg * 4 + h) ^ (r & 7)) << 4));
           mbar_arrive(q_empty + qs);
         }
-#pragma unroll
-        for (int k = 0; k < QC / CONV_GROUPS; ++k) {
-          const int c = b * QC + cg + k * CONV_GROUPS;
-          if (c >= c1 - c0) break;
+        const int c = b * QC + cg;
+        if (c < c1 - c0) {
           const uint32_t idx = chunk0 + c;
           const int stage = idx % S;
           // The slot is free when the products of chunk idx - S are done.
           // (Products are done in order, and this group has waited for those of
-          // idx - CONV_GROUPS - S: the barrier cannot be two phases behind,
-          // which a parity could not tell.)
-          static_assert(S >= CONV_GROUPS, "a slot's parity is unambiguous");
+          // idx - QC - S: the barrier cannot be two phases behind, which a
+          // parity could not tell.)
+          static_assert(S >= QC && CONV_GROUPS == QC, "a slot's parity is unambiguous, a group per chunk of a block");
           got = got && wait_for(empty + stage, (idx / S & 1u) ^ 1u, abort_flag);
-          ok = __all_sync(0xffffffffu, got);  // TMEM stores are warp-wide
-          if (!ok) break;
+          if (!__all_sync(0xffffffffu, got)) {  // TMEM stores are warp-wide
+            ok = false;
+            break;
+          }
           tc_fence_after();
           const uint32_t dst = tmem_a + ((uint32_t)(q * 32) << 16) + (uint32_t)(stage * A_COLS);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t w[4] = {codes[k][h].x, codes[k][h].y, codes[k][h].z, codes[k][h].w};
+          for (int h = 0; h < 4; ++h) {
+            const uint32_t w[4] = {codes[h].x, codes[h].y, codes[h].z, codes[h].w};
 #pragma unroll
             for (int j = 0; j < 4; j += 2) {
               const uint4 x = nibbles8(w[j]), y = nibbles8(w[j + 1]);
@@ -442,7 +438,7 @@ int launch(const W4Op& g, const Ctx& c) {
   a.n_tiles = (g.N + BN - 1) / BN;
   a.tiles = (g.M + BM - 1) / BM * a.n_tiles;
   // inputs split while that leaves every tile's cluster an SM each and a CTA at least 8 chunks
-  a.split = std::max(1, std::min({8, c.nsm / a.tiles, a.chunks / 8}));
+  a.split = std::max(1, std::min({8, c.nsm / a.tiles, a.chunks / 4}));
   a.slice = ((a.chunks + a.split - 1) / a.split + QC - 1) / QC * QC;
   a.out = g.out;
   a.ldo = g.ldo;
