@@ -10,11 +10,11 @@
 // core fills the others.  (Scaled weights would need 11 bits, three more
 // than bf16 has.)
 //
-// Warp roles (576 threads, one CTA an SM):
+// Warp roles (one CTA an SM):
 //   warp 0       TMA producer (one lane): codes and activations -> ring
 //   warp 1       MMA issuer (one lane) and TMEM owner
-//   warps 2-9    epilogue: two sets of four, each with half of the columns
-//   warps 10-17  converters, in two groups of four on alternate chunks:
+//   then         epilogue: a set of four warps for every 32 columns
+//   last 8       converters, in two groups of four on alternate chunks:
 //                thread = weight row, its 64 bytes of codes -> 128 bf16 values
 //                in 64 columns of its TMEM lane
 // Operand A in TMEM because shared memory bounds the alternative: reading both
@@ -38,7 +38,7 @@ namespace {
 
 constexpr int BM = 128, BK = 128;  // weight rows of a tile, inputs of a chunk
 constexpr int CONV_GROUPS = 2, CONV_GROUP = 128;
-constexpr int EPI_THREADS = 256, CONV_THREADS = CONV_GROUPS * CONV_GROUP, THREADS = 64 + EPI_THREADS + CONV_THREADS;
+constexpr int CONV_THREADS = CONV_GROUPS * CONV_GROUP;
 constexpr int SMEM_BUDGET = 227 * 1024 - 2048;  // 1 KB of alignment, 1 KB of barriers
 constexpr uint64_t WAIT_NS = 1000000000ull;
 
@@ -53,6 +53,8 @@ struct Cfg {
   static constexpr int Q_BYTES = BM * BK / 2 * QC, B_BYTES = BN * BK * 2;
   static constexpr int S = 4, QS = BN == 128 ? 5 : 6;
   static constexpr int ACC = BN == 128 ? 2 : 4;  // accumulators
+  static constexpr int COLS = 32;                // columns of an epilogue thread
+  static constexpr int EPI_THREADS = BN / COLS * 128, THREADS = 64 + EPI_THREADS + CONV_THREADS;
   static constexpr int SMEM = QS * Q_BYTES + S * B_BYTES + 2048;
   static_assert(SMEM <= SMEM_BUDGET + 2048, "shared memory");
   static_assert(ACC * BN + S * A_COLS <= (int)TMEM_COLS, "TMEM");
@@ -67,6 +69,31 @@ struct Args {
   long long ldo;
   int accumulate;
 };
+
+// 32 lanes x W consecutive TMEM columns -> W registers per thread.
+template <int W>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&v)[W]) {
+  static_assert(W == 16 || W == 32, "columns");
+  if constexpr (W == 32) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(addr));
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(addr));
+  }
+  tmem_ld_wait();
+}
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -114,10 +141,10 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
 }
 
 template <int BN, int G, typename OutT>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
     linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmX, Args a) {
   using C = Cfg<BN>;
-  constexpr int S = C::S, QS = C::QS, ACC = C::ACC;
+  constexpr int S = C::S, QS = C::QS, ACC = C::ACC, EPI_THREADS = C::EPI_THREADS, THREADS = C::THREADS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stB = smem;
@@ -333,7 +360,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (!ok) *abort_flag = 1;
   } else {
     // epilogue
-    constexpr int COLS = BN / 2;
+    constexpr int COLS = C::COLS;
     const int q = warp & 3, row = q * 32 + lane, set = (warp - 2) >> 2;
     const int g0 = c0 * BK / G, g1 = (c1 * BK + G - 1) / G, groups = a.K / G;
     int buf = 0;
@@ -358,15 +385,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         tc_fence_after();
         const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN + set * COLS);
+        constexpr int W = BN == 128 ? 16 : 32;  // columns of a TMEM read (with 832 threads, 72 registers each)
 #pragma unroll
-        for (int j0 = 0; j0 < COLS; j0 += 16) {
-          float v[16];
-          tmem_ld16(d + j0, v);
+        for (int j0 = 0; j0 < COLS; j0 += W) {
+          uint32_t v[W];
+          tmem_ld<W>(d + j0, v);
+          if (j0 + W == COLS) {  // the last read: the accumulator is free before its values are used
+            tc_fence_before();
+            mbar_arrive(acc_empty + buf);
+          }
 #pragma unroll
-          for (int j = 0; j < 16; ++j) acc[j0 + j] = fmaf(s, v[j], acc[j0 + j]);
+          for (int j = 0; j < W; ++j) acc[j0 + j] = fmaf(s, __uint_as_float(v[j]), acc[j0 + j]);
         }
-        tc_fence_before();
-        mbar_arrive(acc_empty + buf);
         if (++buf == ACC) {
           buf = 0;
           acc_phase ^= 1u;
@@ -453,7 +483,7 @@ int launch(const W4Op& g, const Ctx& c) {
     opted.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
   const int grid = a.split > 1 ? a.tiles * a.split : std::min(a.tiles, c.nsm);
-  return launch_kx(kern, dim3(grid), dim3(THREADS), C::SMEM, c, a.split, mq, mx, a);
+  return launch_kx(kern, dim3(grid), dim3(C::THREADS), C::SMEM, c, a.split, mq, mx, a);
 }
 
 template <int G, typename OutT>
