@@ -16,8 +16,10 @@
 // subtraction, so every product is exact; a group's fp32 sums are then scaled
 // and added to the row's, which keeps the scale out of bf16.
 //
-// A CTA of 8 warps owns 128 weight rows at a time (16 a warp).  With few row
-// blocks the inputs are split over a cluster of up to 8 CTAs, whose partial
+// A CTA of 8 warps owns 128 weight rows at a time (16 a warp), or 256 where
+// there are enough of them: two tiles of a warp share the activations' reads,
+// which otherwise bound it (151936 x 4096 with groups of 64 and 8 rows: 76.9 us
+// with 79% of the shared-memory cycles taken).  With few row blocks the inputs are split over a cluster of up to 8 CTAs, whose partial
 // sums are added in rank order through distributed shared memory.
 #include <algorithm>
 #include <atomic>
@@ -29,7 +31,7 @@ namespace df2 {
 
 namespace {
 
-constexpr int WARPS = 8, RB = WARPS * 16;  // weight rows of a CTA's block
+constexpr int WARPS = 8;
 constexpr int CK = 128;                    // inputs of a chunk
 constexpr int XS_MAX = 96 * 1024;          // activation bytes of a CTA (two CTAs share an SM)
 
@@ -85,24 +87,25 @@ __device__ __forceinline__ int word_k(int i, int t) {
   return G == 128 ? t * 32 + i * 8 : G == 64 ? (i >> 1) * 64 + t * 16 + (i & 1) * 8 : i * 32 + t * 8;
 }
 
-constexpr int U = 4;  // chunks of weights in flight per warp
+constexpr int U = 4;  // chunks whose scales are loaded together
 
-// One lane's share of a chunk: 32 nibbles of two rows.
+// One lane's share of a chunk: 32 nibbles of two rows of each tile.
+template <int R>
 struct Chunk {
-  uint32_t w[2][4];
+  uint32_t w[R][4];
 };
 
 // The group scales of four chunks of two rows: lane t of a row's four holds
 // chunk t's (a request of 2-byte loads costs as much as one of 16-byte loads,
 // so four chunks share it; the products fetch them by shuffles).
-template <int G>
+template <int G, int R>
 struct Scales {
-  float s[2][CK / G];
+  float s[R][CK / G];
 };
-template <int G>
-__device__ __forceinline__ void load_scales(Scales<G>& c, const bf16* const (&srow)[2], int chunk, int K, int t) {
+template <int G, int R>
+__device__ __forceinline__ void load_scales(Scales<G, R>& c, const bf16* const (&srow)[R], int chunk, int K, int t) {
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
+  for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int i = 0; i < CK / G; ++i) {
       const int k = (chunk + t) * CK + i * G;
@@ -110,10 +113,10 @@ __device__ __forceinline__ void load_scales(Scales<G>& c, const bf16* const (&sr
     }
 }
 
-template <int G>
-__device__ __forceinline__ void load_chunk(Chunk& c, const uint8_t* const (&row)[2], int chunk, int K, int t) {
+template <int G, int R>
+__device__ __forceinline__ void load_chunk(Chunk<R>& c, const uint8_t* const (&row)[R], int chunk, int K, int t) {
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
+  for (int r = 0; r < R; ++r) {
     const uint8_t* p = row[r] + (size_t)chunk * (CK / 2);
     if constexpr (G == 128) {
       const uint4 v = ldw128(p + t * 16);
@@ -133,8 +136,10 @@ __device__ __forceinline__ void load_chunk(Chunk& c, const uint8_t* const (&row)
   }
 }
 
-template <int G, int NT, typename OutT>
-__global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 2 : 1) linear_w4_kernel(Args a) {
+template <int G, int NT, int MT, typename OutT>
+__global__ void __launch_bounds__(WARPS * 32, 2) linear_w4_kernel(Args a) {
+  constexpr int RB = WARPS * MT * 16;  // weight rows of a block
+  constexpr int D = 4 / MT;            // chunks of weights in flight per warp
   extern __shared__ uint4 xs[];  // [window][4 words][NT][32 lanes], then the partial sums [NT * 8][RB]
   float* part = reinterpret_cast<float*>(xs + (size_t)a.window * 4 * NT * 32);
   pdl_launch_next();
@@ -162,20 +167,22 @@ __global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 2 : 1) linear_w4_kernel(
     __syncthreads();
   }
   for (int blk = blockIdx.x / a.split; blk < a.blocks; blk += gridDim.x / a.split) {
-    const int m0 = blk * RB + warp * 16 + g;
-    const uint8_t* row[2];
-    const bf16* srow[2];
+    const int m0 = blk * RB + warp * (MT * 16) + g;
+    const uint8_t* row[2 * MT];
+    const bf16* srow[2 * MT];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {  // rows past the end read the last one and are not stored
+    for (int r = 0; r < 2 * MT; ++r) {  // rows past the end read the last one and are not stored
       const size_t m = min(m0 + 8 * r, a.M - 1);
       row[r] = a.codes + m * (a.K / 2);
       srow[r] = a.scale + m * (a.K / G);
     }
-    float acc[NT][4];
+    float acc[MT][NT][4];
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int k = 0; k < MT; ++k)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[k][j][i] = 0.f;
 
     for (int w0 = c_begin; w0 < c_end; w0 += a.window) {
       const int w1 = min(c_end, w0 + a.window);
@@ -184,11 +191,11 @@ __global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 2 : 1) linear_w4_kernel(
         stage(w0, w1);
         __syncthreads();
       }
-      Chunk buf[U];
-      Scales<G> sc, sn;
+      Chunk<2 * MT> buf[D];
+      Scales<G, 2 * MT> sc, sn;
       load_scales<G>(sn, srow, w0, a.K, t);
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int u = 0; u < D; ++u)
         if (w0 + u < w1) load_chunk<G>(buf[u], row, w0 + u, a.K, t);
       for (int c0 = w0; c0 < w1; c0 += U) {
         sc = sn;
@@ -197,37 +204,48 @@ __global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 2 : 1) linear_w4_kernel(
         for (int u = 0; u < U; ++u) {
           const int c = c0 + u;
           if (c >= w1) break;
-          float p[NT][4];
+          Chunk<2 * MT>& q = buf[u % D];
+          float p[MT][NT][4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             if (i % (G / 32) == 0) {
 #pragma unroll
-              for (int j = 0; j < NT; ++j)
+              for (int k = 0; k < MT; ++k)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) p[j][e] = 0.f;
-            }
-            const uint32_t wl = buf[u].w[0][i], wh = buf[u].w[1][i];
-            const uint32_t a0 = nib2(wl, 0), a1 = nib2(wh, 0), a2 = nib2(wl, 1), a3 = nib2(wh, 1);
-            const uint32_t b0 = nib2(wl, 2), b1 = nib2(wh, 2), b2 = nib2(wl, 3), b3 = nib2(wh, 3);
+                for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-              const uint4 xv = xs[(((c - w0) * 4 + i) * NT + j) * 32 + lane];
-              mma16816(p[j], a0, a1, a2, a3, xv.x, xv.y);
-              mma16816(p[j], b0, b1, b2, b3, xv.z, xv.w);
+                  for (int e = 0; e < 4; ++e) p[k][j][e] = 0.f;
             }
-            if (i % (G / 32) == G / 32 - 1) {
-              const float s0 = __shfl_sync(0xffffffffu, sc.s[0][i / (G / 32)], u, 4);
-              const float s1 = __shfl_sync(0xffffffffu, sc.s[1][i / (G / 32)], u, 4);
+            uint4 xv[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) xv[j] = xs[(((c - w0) * 4 + i) * NT + j) * 32 + lane];
+#pragma unroll
+            for (int k = 0; k < MT; ++k) {
+              const uint32_t wl = q.w[2 * k][i], wh = q.w[2 * k + 1][i];
+              const uint32_t a0 = nib2(wl, 0), a1 = nib2(wh, 0), a2 = nib2(wl, 1), a3 = nib2(wh, 1);
+              const uint32_t b0 = nib2(wl, 2), b1 = nib2(wh, 2), b2 = nib2(wl, 3), b3 = nib2(wh, 3);
 #pragma unroll
               for (int j = 0; j < NT; ++j) {
-                acc[j][0] = fmaf(s0, p[j][0], acc[j][0]);
-                acc[j][1] = fmaf(s0, p[j][1], acc[j][1]);
-                acc[j][2] = fmaf(s1, p[j][2], acc[j][2]);
-                acc[j][3] = fmaf(s1, p[j][3], acc[j][3]);
+                mma16816(p[k][j], a0, a1, a2, a3, xv[j].x, xv[j].y);
+                mma16816(p[k][j], b0, b1, b2, b3, xv[j].z, xv[j].w);
+              }
+            }
+            if (i % (G / 32) == G / 32 - 1) {
+#pragma unroll
+              for (int k = 0; k < MT; ++k) {
+                const float s0 = __shfl_sync(0xffffffffu, sc.s[2 * k][i / (G / 32)], u, 4);
+                const float s1 = __shfl_sync(0xffffffffu, sc.s[2 * k + 1][i / (G / 32)], u, 4);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                  acc[k][j][0] = fmaf(s0, p[k][j][0], acc[k][j][0]);
+                  acc[k][j][1] = fmaf(s0, p[k][j][1], acc[k][j][1]);
+                  acc[k][j][2] = fmaf(s1, p[k][j][2], acc[k][j][2]);
+                  acc[k][j][3] = fmaf(s1, p[k][j][3], acc[k][j][3]);
+                }
               }
             }
           }
-          if (c + U < w1) load_chunk<G>(buf[u], row, c + U, a.K, t);
+          if (c + D < w1) load_chunk<G>(q, row, c + D, a.K, t);
         }
       }
     }
@@ -239,14 +257,19 @@ __global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 2 : 1) linear_w4_kernel(
     };
     if (a.split == 1) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int k = 0; k < MT; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) put(n0 + j * 8 + 2 * t + (e & 1), m0 + 8 * (e >> 1), acc[j][e]);
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) put(n0 + j * 8 + 2 * t + (e & 1), m0 + 16 * k + 8 * (e >> 1), acc[k][j][e]);
     } else {
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int k = 0; k < MT; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) part[(j * 8 + 2 * t + (e & 1)) * RB + warp * 16 + g + 8 * (e >> 1)] = acc[j][e];
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            part[(j * 8 + 2 * t + (e & 1)) * RB + warp * (MT * 16) + 16 * k + g + 8 * (e >> 1)] = acc[k][j][e];
       cluster_sync();
       // CTA `rank` adds a share of the block's sums, in rank order
       for (int i = rank * (WARPS * 32) + threadIdx.x; i < NT * 8 * RB / 4; i += a.split * WARPS * 32) {
@@ -263,36 +286,87 @@ __global__ void __launch_bounds__(WARPS * 32, NT <= 2 ? 2 : 1) linear_w4_kernel(
   }
 }
 
-template <int G, int NT, typename OutT>
-int launch(Args a, const Ctx& c) {
-  const int nb = (a.N + NT * 8 - 1) / (NT * 8);
+// Largest dynamic shared memory of an instantiation.
+template <int NT, int MT>
+constexpr int smem_most() {
+  return XS_MAX + NT * 8 * (WARPS * MT * 16) * 4;
+}
+
+// Lets the kernel use that much on the current device, and counts the clusters
+// of `split` CTAs that run at once on it (both once per device and size).
+template <int G, int NT, int MT, typename OutT>
+int wave_of(int split, int nsm) {
+  static std::atomic<int> waves[64][9];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
+  int n = waves[dev][split].load(std::memory_order_relaxed);
+  if (n) return n;
+  auto kern = linear_w4_kernel<G, NT, MT, OutT>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_most<NT, MT>()) != cudaSuccess)
+    return -1;
+  n = 2 * nsm;
+  if (split > 1) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(split * 64);
+    cfg.blockDim = dim3(WARPS * 32);
+    cfg.dynamicSmemBytes = smem_most<NT, MT>();
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = split;
+    at.val.clusterDim.y = 1;
+    at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+      (void)cudaGetLastError();
+      return -1;
+    }
+  }
+  waves[dev][split].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// CTAs of a cluster: the most (up to 8) whose clusters hold every block in one
+// wave with at least four chunks a CTA, but enough for the activations to fit.
+// (Measured at 8 rows, groups of 128, us for splits of 1, 2, 4, 8: 6144 x 4096
+// 13.5, 11.2, 8.2, 10.9 (48 blocks of 128 rows); 4096 x 12288 44, 28, 15, 11
+// (32 blocks); 704 x 256 in 2 slices 3.3 against 2.6 in one.)
+template <int G, int NT, int MT, typename OutT>
+int split_of(int blocks, int chunks, int nsm) {
+  constexpr int fit = XS_MAX / (NT * 8 * CK * 2);
+  int split = std::min(8, (chunks + fit - 1) / fit);
+  for (int s = std::min(8, chunks / 4); s > split; --s)
+    if (wave_of<G, NT, MT, OutT>(s, nsm) >= blocks) return s;
+  return split;
+}
+
+template <int G, int NT, int MT, typename OutT>
+int launch(Args a, int split, const Ctx& c) {
+  constexpr int RB = WARPS * MT * 16, per_chunk = NT * 8 * CK * 2, fit = XS_MAX / per_chunk;
+  const int nb = (a.N + NT * 8 - 1) / (NT * 8), wave = wave_of<G, NT, MT, OutT>(split, c.nsm);
+  if (wave < 1) return DFLASH2_ERR_CUDA;
   a.blocks = (a.M + RB - 1) / RB;
-  // split the inputs until two CTAs an SM have work and the activations fit
-  const int per_chunk = NT * 8 * CK * 2, fit = XS_MAX / per_chunk;
-  a.split = 1;
-  while (a.split < 8 && a.chunks >= 2 * a.split * 2 &&
-         ((long long)a.blocks * nb * a.split < 2 * c.nsm || (a.chunks + a.split - 1) / a.split > fit))
-    a.split *= 2;
+  a.split = split;
   a.slice = (a.chunks + a.split - 1) / a.split;
   a.window = std::min(a.slice, fit);
   const size_t smem = (size_t)a.window * per_chunk + (size_t)NT * 8 * RB * 4;
-  int clusters = std::max(1, (NT <= 2 ? 2 : 1) * c.nsm / a.split);
-  clusters = std::min(clusters, a.blocks);
-  auto kern = linear_w4_kernel<G, NT, OutT>;
-  static std::atomic<unsigned long long> opted{0};  // devices whose kernel may use the largest size
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return DFLASH2_ERR_CUDA;
-  if (!(opted.load(std::memory_order_relaxed) >> dev & 1)) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, XS_MAX + NT * 8 * RB * 4) != cudaSuccess)
-      return DFLASH2_ERR_CUDA;
-    opted.fetch_or(1ull << dev, std::memory_order_relaxed);
-  }
+  const int clusters = std::min(wave, a.blocks);
+  auto kern = linear_w4_kernel<G, NT, MT, OutT>;
   return launch_kx(kern, dim3(clusters * a.split, nb), dim3(WARPS * 32), smem, c, a.split, a);
+}
+
+// Blocks of 256 rows unless blocks of 128 fill more of a wave.
+template <int G, int NT, typename OutT>
+int launch_m(const Args& a, const Ctx& c) {
+  const int b2 = (a.M + 255) / 256, b1 = (a.M + 127) / 128, wave = 2 * c.nsm;
+  const int s2 = split_of<G, NT, 2, OutT>(b2, a.chunks, c.nsm), s1 = split_of<G, NT, 1, OutT>(b1, a.chunks, c.nsm);
+  return std::min(b2 * s2, wave) >= std::min(b1 * s1, wave) ? launch<G, NT, 2, OutT>(a, s2, c)
+                                                            : launch<G, NT, 1, OutT>(a, s1, c);
 }
 
 template <int G, typename OutT>
 int launch_n(const Args& a, const Ctx& c) {
-  return a.N <= 8 ? launch<G, 1, OutT>(a, c) : launch<G, 2, OutT>(a, c);
+  return a.N <= 8 ? launch_m<G, 1, OutT>(a, c) : launch_m<G, 2, OutT>(a, c);
 }
 
 template <typename OutT>
