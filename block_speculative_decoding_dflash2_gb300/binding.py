@@ -18,6 +18,8 @@ TEST_LIB_PATH = os.path.join(_PKG, "libdflash2_testing.so")
 F32 = 0
 BF16 = 1
 FP8W = 2
+W4 = 3
+W4_GROUP = 64
 
 STATUS = {0: "ok", -1: "invalid argument", -2: "shape", -3: "block size", -4: "dtype",
           -5: "workspace", -6: "cuda", -7: "unsupported"}
@@ -201,7 +203,7 @@ def make_config(d):
     for name, _ in Config._fields_:
         v = d.get(name, 0) if name == "sliding_window" else d[name]
         if name == "dtype" and isinstance(v, str):
-            v = {"f32": F32, "bf16": BF16, "fp8w": FP8W}[v]
+            v = {"f32": F32, "bf16": BF16, "fp8w": FP8W, "w4": W4}[v]
         setattr(c, name, v)
     return c
 
@@ -212,7 +214,7 @@ class DraftOpts(ctypes.Structure):
 
 class WeightSet:
     """Holds a Weights struct over torch device tensors (kept alive here);
-    tensors["scales"] (fp8 weights) fills its Scales struct."""
+    tensors["scales"] (fp8 and 4-bit weights) fills its Scales struct."""
 
     def __init__(self, tensors):
         self.tensors = tensors

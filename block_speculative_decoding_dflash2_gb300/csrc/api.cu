@@ -52,15 +52,16 @@ int stage_event(int i, cudaStream_t st) {
 // Bytes of an activation / cache element (fp8 weights run on bf16 activations).
 int esize(int dtype) { return dtype == DFLASH2_F32 ? 4 : 2; }
 
-// The config as the activation path sees it: fp8-weight configs compute with
-// bf16 activations, cache and norm gains.
+// The config as the activation path sees it: fp8- and 4-bit-weight configs
+// compute with bf16 activations, cache and norm gains.
 dflash2_config act_config(const dflash2_config& c) {
   dflash2_config a = c;
-  if (a.dtype == DFLASH2_FP8W) a.dtype = DFLASH2_BF16;
+  if (a.dtype == DFLASH2_FP8W || a.dtype == DFLASH2_W4) a.dtype = DFLASH2_BF16;
   return a;
 }
 
-// Row scales of the fp8 weights (all null for F32 / BF16 configs).
+// Scales of the fp8 weights (per row) or the 4-bit ones (bf16, per group);
+// all null for F32 / BF16 configs.
 struct Scales {
   const float *lm_head = nullptr, *fc = nullptr, *sel = nullptr;
   const dflash2_layer_scales* layers = nullptr;
@@ -68,7 +69,7 @@ struct Scales {
 };
 Scales scales_of(const dflash2_config& cfg, const dflash2_weights& w) {
   Scales s;
-  if (cfg.dtype == DFLASH2_FP8W && w.scales) {
+  if ((cfg.dtype == DFLASH2_FP8W || cfg.dtype == DFLASH2_W4) && w.scales) {
     s.lm_head = w.scales->lm_head;
     s.fc = w.scales->fc;
     s.sel = w.scales->sel;
@@ -81,7 +82,8 @@ size_t al(size_t x) { return (x + 255) & ~size_t(255); }
 
 int check_config(const dflash2_config* c) {
   if (!c) return DFLASH2_ERR_INVALID_ARG;
-  if (c->dtype != DFLASH2_F32 && c->dtype != DFLASH2_BF16 && c->dtype != DFLASH2_FP8W) return DFLASH2_ERR_DTYPE;
+  if (c->dtype != DFLASH2_F32 && c->dtype != DFLASH2_BF16 && c->dtype != DFLASH2_FP8W && c->dtype != DFLASH2_W4)
+    return DFLASH2_ERR_DTYPE;
   if (c->block_size < 2 || c->block_size > 32) return DFLASH2_ERR_BLOCK_SIZE;
   if (c->hidden <= 0 || c->n_q_heads <= 0 || c->n_kv_heads <= 0 || c->intermediate <= 0 || c->vocab <= 0 ||
       c->n_layers <= 0 || c->n_taps <= 0 || c->page_size <= 0)
@@ -92,6 +94,9 @@ int check_config(const dflash2_config* c) {
   if (c->sliding_window < 0) return DFLASH2_ERR_SHAPE;
   // fp8 weight rows are read in 16-byte units (TMA rows, staged tap rows)
   if (c->dtype == DFLASH2_FP8W && (c->hidden % 16 || c->intermediate % 16)) return DFLASH2_ERR_SHAPE;
+  // 4-bit weight rows are whole groups (n_q_heads * head_dim always is)
+  if (c->dtype == DFLASH2_W4 && (c->hidden % DFLASH2_W4_GROUP || c->intermediate % DFLASH2_W4_GROUP))
+    return DFLASH2_ERR_SHAPE;
   if (c->conv_group_size <= 0 || c->hidden % c->conv_group_size) return DFLASH2_ERR_SHAPE;
   if (c->top_k < 1 || c->top_k > KMAX || c->top_k > c->vocab) return DFLASH2_ERR_SHAPE;
   if (c->selector_rank < 1 || c->selector_rank > 128) return DFLASH2_ERR_SHAPE;
@@ -120,6 +125,7 @@ struct Layout {
 
 Layout plan(const dflash2_config& c0, int batch, int n_new, int max_ctx) {
   const dflash2_config c = act_config(c0);
+  const bool w4 = c0.dtype == DFLASH2_W4;
   const int H = c.hidden, B = c.block_size, D = B - 1, es = esize(c.dtype);
   const int nq = c.n_q_heads, nkv = c.n_kv_heads, d = c.head_dim, I = c.intermediate;
   const int G = H / c.conv_group_size, r = c.selector_rank, k = c.top_k;
@@ -178,7 +184,7 @@ Layout plan(const dflash2_config& c0, int batch, int n_new, int max_ctx) {
   L.O = take((size_t)rows * nq * d * es);
   L.act = take((size_t)rows * I * es);
   L.hn = take((size_t)batch * D * H * es);
-  L.logits = take(c.dtype == DFLASH2_F32 ? (size_t)batch * D * c.vocab * 4 : 0);
+  L.logits = take(c.dtype == DFLASH2_F32 || w4 ? (size_t)batch * D * c.vocab * 4 : 0);
   L.lv = take((size_t)n_lists * batch * D * KMAX * 4);
   L.li = take((size_t)n_lists * batch * D * KMAX * 4);
   L.selx = take((size_t)nsel * H * es);
@@ -280,10 +286,12 @@ int gemm_fused(GemmOp g, const Ctx& ctx, void* ws, const Layout& L, bool append_
   return gemm_bf16(g, ctx);
 }
 
-// c: the activation config (act_config); wscale: the fp8 row scales of W, or null.
+// c: the activation config (act_config); wscale: the scales of W (fp8 rows, or
+// bf16 groups with ctx.w4), or null.
 int gemm(const dflash2_config& c, const Ctx& ctx, void* ws, const Layout& L, const void* W, int M, int K,
          const void* X, int N, float* out, bool accumulate, bool append_branch = false,
          const float* wscale = nullptr) {
+  if (ctx.w4) return launch_linear_w4({W, wscale, DFLASH2_W4_GROUP, M, K, X, K, N, out, M, false, accumulate}, ctx);
   GemmOp g;
   std::memset(&g, 0, sizeof(g));
   g.W = W;
@@ -316,7 +324,7 @@ int check_weights(const dflash2_config& c, const dflash2_weights* w) {
       return DFLASH2_ERR_INVALID_ARG;
     if (c.conv_kernel_size > 0 && (!L.tapgen_attn || !L.tapgen_mlp)) return DFLASH2_ERR_INVALID_ARG;
   }
-  if (c.dtype == DFLASH2_FP8W) {
+  if (c.dtype == DFLASH2_FP8W || c.dtype == DFLASH2_W4) {
     const dflash2_scales* s = w->scales;
     if (!s || !s->lm_head || !s->fc || !s->sel || !s->layers) return DFLASH2_ERR_INVALID_ARG;
     for (int l = 0; l < c.n_layers; ++l) {
@@ -374,7 +382,7 @@ int run_append(const dflash2_config& c, const dflash2_weights& w, const Scales& 
   const int H = c.hidden, nq = c.n_q_heads, nkv = c.n_kv_heads, d = c.head_dim;
   float* Y = at<float>(ws, L.Ya);
   void* f = at<char>(ws, L.f);
-  const bool fused_kv = c.dtype == DFLASH2_BF16 && gemm_fusable(2 * nkv * d, n_new, kEpiHeads);
+  const bool fused_kv = c.dtype == DFLASH2_BF16 && !ctx.w4 && gemm_fusable(2 * nkv * d, n_new, kEpiHeads);
   Ctx rest;
   TRY(project_features(c, w, sc, n_pages, block_table, max_pages, batch, ctx_len, n_new, taps, new_off, ws, L,
                        fused_kv, ctx, &rest));
@@ -386,8 +394,12 @@ int run_append(const dflash2_config& c, const dflash2_weights& w, const Scales& 
     Ctx lrest = rest;
     if (kv_nsm > 0 && l == 0) lrest.nsm = kv_nsm;
     // the k and v rows of the qkv matrix (fp8: bytes, and their scales)
-    const float* skv = sc.layers ? sc.layers[l].qkv + (size_t)nq * d : nullptr;
-    const void* wkv = skv ? static_cast<const void*>(static_cast<const uint8_t*>(Lw.qkv) + (size_t)nq * d * H)
+    const float* skv = sc.layers && !ctx.w4 ? sc.layers[l].qkv + (size_t)nq * d : nullptr;
+    if (ctx.w4)
+      skv = reinterpret_cast<const float*>(reinterpret_cast<const bf16*>(sc.layers[l].qkv) +
+                                           (size_t)nq * d * (H / DFLASH2_W4_GROUP));
+    const void* wkv = ctx.w4 ? static_cast<const void*>(static_cast<const uint8_t*>(Lw.qkv) + (size_t)nq * d * H / 2)
+                      : skv  ? static_cast<const void*>(static_cast<const uint8_t*>(Lw.qkv) + (size_t)nq * d * H)
                           : static_cast<const void*>(elem_ptr(Lw.qkv, (size_t)nq * d * H, c.dtype));
     char* kcl = const_cast<char*>(elem_ptr(kc, l * layer_elems, c.dtype));
     char* vcl = const_cast<char*>(elem_ptr(vc, l * layer_elems, c.dtype));
@@ -496,6 +508,7 @@ int dflash2_append_context(const dflash2_config* cfg, const dflash2_weights* w, 
   if (ws_bytes < L.total) return DFLASH2_ERR_WORKSPACE;
   Ctx ctx;
   TRY(device_ctx(&ctx, stream, workspace));
+  ctx.w4 = cfg->dtype == DFLASH2_W4;
   return run_append(act_config(*cfg), *w, scales_of(*cfg, *w), k_cache, v_cache, n_pages, block_table, max_pages,
                     batch, ctx_len, n_new, new_taps, new_off, workspace, L, ctx);
 }
@@ -513,11 +526,13 @@ int dflash2_draft_step(const dflash2_config* cfg, const dflash2_weights* w, void
   const dflash2_config c = act_config(*cfg);
   const Scales sc = scales_of(*cfg, *w);
   const int max_ctx = max_pages * c.page_size;
-  const Layout L = plan(c, batch, n_new, max_ctx);
+  const Layout L = plan(*cfg, batch, n_new, max_ctx);
   if (ws_bytes < L.total) return DFLASH2_ERR_WORKSPACE;
   if ((long long)batch * (c.block_size - 1) > kMaxTopkRows) return DFLASH2_ERR_SHAPE;
   Ctx ctx;
   TRY(device_ctx(&ctx, stream, workspace));
+  const bool w4 = cfg->dtype == DFLASH2_W4;  // 4-bit weights take the unfused arrangement
+  ctx.w4 = w4;
 
   const int H = c.hidden, B = c.block_size, D = B - 1, nq = c.n_q_heads, nkv = c.n_kv_heads, d = c.head_dim;
   const int I = c.intermediate, G = H / c.conv_group_size, rows = batch * B;
@@ -540,7 +555,7 @@ int dflash2_draft_step(const dflash2_config* cfg, const dflash2_weights* w, void
   // so v1 runs the separate one
   const bool conv = c.conv_kernel_size > 0;
   const bool merged =
-      conv && c.n_layers > 1 && c.dtype == DFLASH2_BF16 && gemm_fusable(qkvM, rows + n_new, kEpiHeads);
+      conv && c.n_layers > 1 && c.dtype == DFLASH2_BF16 && !w4 && gemm_fusable(qkvM, rows + n_new, kEpiHeads);
   std::unique_lock<std::mutex> side_lock(g_side_mu, std::defer_lock);
   SideStream side;
   const bool forked = n_new > 0;
@@ -548,14 +563,14 @@ int dflash2_draft_step(const dflash2_config* cfg, const dflash2_weights* w, void
   // contraction bandwidth-bound, and neither fits an SM beside the other: a
   // forked step splits the SMs, kForkPrologueSMs for the prologue (on fewer,
   // wider CTAs) and the rest for the contraction, so the two overlap.
-  const bool fused = conv && conv_prologue_fits(c.dtype, batch, B, H, G, ctx.nsm);
+  const bool fused = conv && !w4 && conv_prologue_fits(c.dtype, batch, B, H, G, ctx.nsm);
   const bool split_sms = forked && fused && ctx.nsm > 2 * kForkPrologueSMs &&
                          conv_prologue_fits(c.dtype, batch, B, H, G, kForkPrologueSMs / 2);
   // sublayer prologues: one fused kernel (norm, tap logits, conv) when the
   // sequence's B rows fit its shared memory, else norm + tap GEMM + conv;
   // the QKV contraction with its q/k-norm + RoPE epilogue when its
   // activation tile allows
-  const bool fused_qkv = merged || (c.dtype == DFLASH2_BF16 && gemm_fusable(qkvM, rows, kEpiHeads));
+  const bool fused_qkv = merged || (c.dtype == DFLASH2_BF16 && !w4 && gemm_fusable(qkvM, rows, kEpiHeads));
   // separate arrangement with the fused QKV: the block's first QKV
   // contraction leaves kForkKvSMs SMs free, where the side stream's K/V
   // contraction runs beside it instead of waiting for the QKV's CTAs to exit
@@ -702,7 +717,7 @@ int dflash2_draft_step(const dflash2_config* cfg, const dflash2_weights* w, void
         TRY(launch_dyn_conv(c.dtype, u, Y, rows, H, c.conv_group_size, B, u2, ctx));
       }
     }
-    if (c.dtype == DFLASH2_BF16 && gemm_fusable(2 * I, rows, kEpiSwiglu)) {
+    if (c.dtype == DFLASH2_BF16 && !w4 && gemm_fusable(2 * I, rows, kEpiSwiglu)) {
       GemmOp g = gemm_op(Lw.gate_up, 2 * I, H, u2, rows, s_gu);  // SiLU(gate) * up fused into the epilogue
       g.epi = kEpiSwiglu;
       g.act = act;
@@ -722,7 +737,7 @@ int dflash2_draft_step(const dflash2_config* cfg, const dflash2_weights* w, void
   int* li = at<int>(workspace, L.li);
   int n_lists = 0;
   const int nrow = batch * D;
-  if (c.dtype == DFLASH2_BF16) {
+  if (c.dtype == DFLASH2_BF16 && !w4) {
     GemmOp g;
     std::memset(&g, 0, sizeof(g));
     g.W = w->lm_head;
@@ -744,7 +759,7 @@ int dflash2_draft_step(const dflash2_config* cfg, const dflash2_weights* w, void
     n_lists = gemm_topk_lists(c.vocab, nrow, H, ctx.nsm, c.dtype);
   } else {
     float* logits = at<float>(workspace, L.logits);
-    TRY(gemm(c, ctx, workspace, L, w->lm_head, c.vocab, H, hn, nrow, logits, false));
+    TRY(gemm(c, ctx, workspace, L, w->lm_head, c.vocab, H, hn, nrow, logits, false, false, sc.lm_head));
     TRY(launch_topk_scan(logits, nrow, c.vocab, c.output_multiplier, c.final_logit_softcap, debug_logits, lv, li,
                          &n_lists, ctx));
   }
@@ -763,13 +778,15 @@ int dflash2_select_path_ex(const dflash2_config* cfg, const dflash2_weights* w, 
   if (batch <= 0) return DFLASH2_ERR_SHAPE;
   if (!anchor || !cand_id || !cand_logit || !path) return DFLASH2_ERR_INVALID_ARG;
   if (!workspace) return DFLASH2_ERR_WORKSPACE;
-  if (cfg->dtype == DFLASH2_FP8W && (!w->scales || !w->scales->sel)) return DFLASH2_ERR_INVALID_ARG;
+  if ((cfg->dtype == DFLASH2_FP8W || cfg->dtype == DFLASH2_W4) && (!w->scales || !w->scales->sel))
+    return DFLASH2_ERR_INVALID_ARG;
   const dflash2_config c = act_config(*cfg);
   const Scales sc = scales_of(*cfg, *w);
-  const Layout L = plan(c, batch, 0, 0);
+  const Layout L = plan(*cfg, batch, 0, 0);
   if (ws_bytes < L.total) return DFLASH2_ERR_WORKSPACE;
   Ctx ctx;
   TRY(device_ctx(&ctx, stream, workspace));
+  ctx.w4 = cfg->dtype == DFLASH2_W4;
   const int D = c.block_size - 1, k = c.top_k, r = c.selector_rank, H = c.hidden;
   void* x = at<char>(workspace, L.selx);
   float* Y = at<float>(workspace, L.Y);
@@ -794,10 +811,15 @@ size_t dflash2_selector_table_bytes(const dflash2_config* cfg) {
 int dflash2_build_selector_table(const dflash2_config* cfg, const dflash2_weights* w, float* table, void* stream) {
   TRY(check_config(cfg));
   if (!w || !w->embed || !w->sel || !table) return DFLASH2_ERR_INVALID_ARG;
-  if (cfg->dtype == DFLASH2_FP8W && (!w->scales || !w->scales->sel)) return DFLASH2_ERR_INVALID_ARG;
+  if ((cfg->dtype == DFLASH2_FP8W || cfg->dtype == DFLASH2_W4) && (!w->scales || !w->scales->sel))
+    return DFLASH2_ERR_INVALID_ARG;
   Ctx ctx;
   TRY(device_ctx(&ctx, stream, nullptr));
   const dflash2_config c = act_config(*cfg);
+  if (cfg->dtype == DFLASH2_W4)
+    return launch_linear_w4({w->sel, w->scales->sel, DFLASH2_W4_GROUP, 2 * c.selector_rank, c.hidden, w->embed, c.hidden,
+                             c.vocab, table, 2 * c.selector_rank, false, false},
+                            ctx);
   // table[v][m] = sum_h sel[m][h] E[v][h]: the selector contraction with the
   // whole vocabulary as its activation rows (whole tiles: no workspace)
   GemmOp g = gemm_op(w->sel, 2 * c.selector_rank, c.hidden, w->embed, c.vocab, scales_of(*cfg, *w).sel);

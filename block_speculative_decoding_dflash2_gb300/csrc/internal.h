@@ -16,6 +16,7 @@ struct Ctx {
   int nsm;           // SMs of the current device
   bool pdl = true;   // launch with programmatic stream serialization
   int prio = 0;      // launch priority (0: the stream's own; lower numbers run first)
+  bool w4 = false;   // the call's weight matrices are 4-bit codes (DFLASH2_W4)
 };
 
 // One dense contraction out[n][m] = sum_k W[m][k] * X[n][k]  (swap-AB: the

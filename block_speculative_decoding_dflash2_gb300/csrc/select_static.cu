@@ -86,6 +86,7 @@ int dflash2_select_path_static(const dflash2_config* cfg, const dflash2_weights*
   if (!w || !w->embed || !w->sel) return DFLASH2_ERR_INVALID_ARG;
   if (batch <= 0) return DFLASH2_ERR_SHAPE;
   if (!anchor || !cand_id || !cand_logit || !path) return DFLASH2_ERR_INVALID_ARG;
+  if (cfg->dtype == DFLASH2_W4) return DFLASH2_ERR_UNSUPPORTED;
   const bool fp8 = cfg->dtype == DFLASH2_FP8W;
   if (fp8 && (!w->scales || !w->scales->sel)) return DFLASH2_ERR_INVALID_ARG;
   dflash2_config c = *cfg;

@@ -56,6 +56,7 @@ class DraftRunner:
         self.next_anchor = parts[4]
         self.path_score = torch.zeros((batch,), dtype=torch.float32, device=device)
         self.counters = torch.zeros((4 + 2 * (D + 1) - 1,), dtype=torch.int64, device=device)
+        self.verify_ws = torch.zeros(B.dflash2_verify_logits_workspace(batch, D + 1), dtype=torch.uint8, device=device)
 
     def append(self, ctx_len, taps, new_off, stream=None):
         n_new = int(taps.shape[0]) if taps is not None else 0
@@ -87,6 +88,14 @@ class DraftRunner:
     def verify(self, target, seq_len=None, stream=None):
         B.dflash2_verify_accept(self.batch, self.cfgd["block_size"], self.path, target, self.accept_len,
                                 self.out_tok, self.n_out, self.next_anchor, seq_len, self.counters, stream)
+
+    def verify_logits(self, logits, u_accept, u_sample, temperature=None, top_k=None, top_p=None, min_p=None,
+                      n_draft=None, seq_len=None, stream=None):
+        """Sampled verification of the selected path straight from the target's
+        logits [batch, block_size, vocab] (its status word is verify_ws's)."""
+        B.dflash2_verify_logits(self.path, n_draft, logits, temperature, top_k, top_p, min_p, u_accept, u_sample,
+                                self.accept_len, self.out_tok, self.n_out, self.next_anchor, self.verify_ws, seq_len,
+                                self.counters, stream)
 
     def device_status(self, stream=None):
         return B.dflash2_read_device_status(self.workspace, stream)

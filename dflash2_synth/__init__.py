@@ -82,7 +82,8 @@ def bf16_bits_to_f32(bits):
 
 class Tensor:
     """A drawn tensor: exact values plus its stored form: bf16 bit patterns,
-    or, for an fp8 matrix, e4m3 codes `q` with per-row float32 scales (then
+    or, for an fp8 matrix, e4m3 codes `q` with per-row float32 scales, or, for
+    a 4-bit matrix, packed codes `q` with group scales [rows, groups] (then
     `values` = decoded code * scale, exactly, in float64)."""
 
     __slots__ = ("values", "bits", "q", "scale")
@@ -143,6 +144,26 @@ def quantize_rows_e4m3(w):
     return Tensor(values, q=q, scale=scale)
 
 
+W4_GROUP = 64
+
+
+def quantize_groups_w4(w, group=W4_GROUP):
+    """4-bit quantisation of a [rows, cols] matrix: per group of `group`
+    columns of a row, scale = max|group| / 7 rounded to bfloat16, q =
+    round(w / scale) in -8..7 (ties to even).  Codes are q + 8, column 2j in
+    the low and 2j + 1 in the high nibble of byte j.  Returns a Tensor whose
+    values are the dequantised q * scale (float64, exact)."""
+    w = np.asarray(w, dtype=np.float32)
+    rows, cols = w.shape
+    g = w.astype(np.float64).reshape(rows, cols // group, group)
+    amax = np.max(np.abs(g), axis=2)
+    scale = bf16_bits_to_f32(to_bf16_bits(np.where(amax > 0, amax / 7, 1.0)))
+    q = np.clip(np.rint(g / scale[:, :, None]), -8, 7)
+    values = (q * scale[:, :, None]).reshape(rows, cols)
+    code = (q.reshape(rows, cols) + 8).astype(np.uint8)
+    return Tensor(values, q=code[:, 0::2] | (code[:, 1::2] << np.uint8(4)), scale=scale)
+
+
 def _rng(seed, name):
     h = int.from_bytes(hashlib.sha256(name.encode()).digest()[:8], "little")
     return np.random.Generator(np.random.PCG64([seed, h]))
@@ -186,13 +207,18 @@ def _draw(seed, name, shape, std, dtype, mean=0.0):
 def make_weights(cfg, seed=None):
     """All draft weights of a workload, as a dict of Tensor (layers: list).
     With dtype "fp8w" the matrices other than the embedding are drawn in
-    float32 and quantised per output channel to e4m3 (quantize_rows_e4m3);
-    the embedding and the norm gains are bf16."""
+    float32 and quantised per output channel to e4m3 (quantize_rows_e4m3),
+    with "w4" to 4 bits per group (quantize_groups_w4); the embedding and the
+    norm gains are bf16."""
     seed = 1000 + cfg["index"] if seed is None else seed
     dt = cfg["dtype"]
     if dt == "fp8w":
         def mat(name, shape):
             return quantize_rows_e4m3(_draw(seed, name, shape, 0.02, "f32").values)
+        dt = "bf16"
+    elif dt == "w4":
+        def mat(name, shape):
+            return quantize_groups_w4(_draw(seed, name, shape, 0.02, "f32").values)
         dt = "bf16"
     else:
         def mat(name, shape):
@@ -321,7 +347,7 @@ def paged_layout(ctx_cap, page_size, batch, seed, spare_pages=0):
 
 def to_torch(t, device="cuda"):
     """Tensor -> torch tensor on `device` (bf16 from its bit patterns; an fp8
-    matrix as its uint8 e4m3 codes)."""
+    or 4-bit matrix as its uint8 codes)."""
     import torch
     if t.q is not None:
         return torch.from_numpy(np.ascontiguousarray(t.q)).to(device)
@@ -332,12 +358,15 @@ def to_torch(t, device="cuda"):
 
 def device_weights(w, device="cuda"):
     """Weight dict of Tensor -> weight dict of torch device tensors; with fp8
-    matrices, also "scales": their per-row float32 scales in the same nesting."""
+    matrices, also "scales": their per-row float32 scales in the same nesting
+    (4-bit matrices: bfloat16 group scales)."""
     import torch
     out = {k: to_torch(v, device) for k, v in w.items() if k != "layers"}
     out["layers"] = [{k: to_torch(v, device) for k, v in L.items()} for L in w["layers"]]
     if w["lm_head"].q is not None:
-        sc = lambda t: torch.from_numpy(t.scale).to(device)
+        def sc(t):
+            s = torch.from_numpy(t.scale).to(device)
+            return s if s.dim() == 1 else s.to(torch.bfloat16)
         out["scales"] = {k: sc(w[k]) for k in ("lm_head", "fc", "sel")}
         out["scales"]["layers"] = [{k: sc(v) for k, v in L.items() if v.q is not None} for L in w["layers"]]
     return out

@@ -78,6 +78,13 @@ extern "C" {
                             cache; fp32 accumulation.  A weight element is q * scale[row]:
                             the contractions run on the exact bf16 value of q and apply
                             the row's scale to the fp32 result. */
+#define DFLASH2_W4    3  /* 4-bit linear weights with bfloat16 scales per group of
+                            DFLASH2_W4_GROUP inputs, in the format of dflash2_linear_w4,
+                            which every contraction takes; bfloat16 embed, norm gains,
+                            activations and cache; fp32 accumulation.  hidden and
+                            intermediate must be multiples of the group.  Not served by
+                            dflash2_select_path_static (DFLASH2_ERR_UNSUPPORTED). */
+#define DFLASH2_W4_GROUP 64
 
 /*
  * Draft model configuration ("Key Config Fields"; dflash_config of
@@ -97,7 +104,7 @@ extern "C" {
  *   selector_rank          r, 1..128
  *   page_size              context KV page length (tokens per page)
  *   mask_token_id          token filling block slots 1..B-1 ("Data" note)
- *   dtype                  DFLASH2_F32, DFLASH2_BF16 or DFLASH2_FP8W
+ *   dtype                  DFLASH2_F32, DFLASH2_BF16, DFLASH2_FP8W or DFLASH2_W4
  *   rms_eps                RMSNorm epsilon
  *   rope_theta             rotary base
  *   input_embedding_scale  multiplies the embedded block (1 = identity)
@@ -119,7 +126,9 @@ typedef struct dflash2_config {
 
 /*
  * Weights of one draft layer (device pointers, element type = cfg.dtype;
- * with DFLASH2_FP8W the matrices are e4m3 bytes and the norm gains bf16).
+ * with DFLASH2_FP8W the matrices are e4m3 bytes and the norm gains bf16;
+ * with DFLASH2_W4 the matrices are 4-bit codes [out, in / 2] and the norm
+ * gains bf16).
  * G = hidden / conv_group_size.  Matrices are [out_features, in_features].
  *   attn_norm    [H]                      RMSNorm gain before attention
  *   tapgen_attn  [2G, H]                  conv tap generator, row 2g+j = tap j of group g
@@ -139,9 +148,11 @@ typedef struct dflash2_layer_weights {
 } dflash2_layer_weights;
 
 /*
- * DFLASH2_FP8W only: the fp32 per-output-channel scales of the e4m3 matrices
+ * DFLASH2_FP8W: the fp32 per-output-channel scales of the e4m3 matrices
  * (device pointers; one float per matrix row, in the row order of the
  * matrix: qkv scales are q rows, then k rows, then v rows).
+ * DFLASH2_W4: the same members point to the bfloat16 group scales
+ * [rows, in / DFLASH2_W4_GROUP] of the matrices, cast to const float *.
  */
 typedef struct dflash2_layer_scales {
     const float *tapgen_attn, *qkv, *o, *tapgen_mlp, *gate_up, *down;
@@ -164,12 +175,14 @@ typedef struct dflash2_scales {
  *   sel          [2r, H]    selector factors: rows 0..r-1 = W_a (predecessor),
  *                           rows r..2r-1 = W_b (candidate)
  * With DFLASH2_FP8W, lm_head, fc, sel and the layer matrices are e4m3 bytes
- * with the row scales of `scales`; embed and the norm gains are bf16.
+ * with the row scales of `scales`; embed and the norm gains are bf16.  With
+ * DFLASH2_W4 the same matrices are 4-bit codes with the group scales of
+ * `scales`.
  */
 typedef struct dflash2_weights {
     const void *embed, *lm_head, *fc, *hidden_norm, *final_norm, *sel;
     const dflash2_layer_weights *layers;
-    const dflash2_scales *scales;  /* host pointer; DFLASH2_FP8W only (NULL otherwise) */
+    const dflash2_scales *scales;  /* host pointer; DFLASH2_FP8W and DFLASH2_W4 only (NULL otherwise) */
 } dflash2_weights;
 
 /*
