@@ -33,20 +33,30 @@ __global__ void __launch_bounds__(128) topk_scan_kernel(const float* __restrict_
   const int v0 = c * len, v1 = min(V, v0 + len);
   float lv = -INFINITY, tv = -INFINITY;
   int li = INT_MAX, ti = INT_MAX;
-  for (int base = v0 + warp * 32; base < v1; base += 128) {
-    const int id = base + lane;
-    float z = -INFINITY;
-    const bool valid = id < v1;
-    if (valid) {
-      z = mult * logits[(size_t)row * V + id];
-      if (cap > 0.f) z = cap * tanhf(z / cap);
-      if (debug) debug[(size_t)row * V + id] = z;
+  constexpr int U = 8;  // loads in flight per lane
+  for (int b0 = v0 + warp * 32; b0 < v1; b0 += 128 * U) {
+    float zz[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int id = b0 + u * 128 + lane;
+      zz[u] = id < v1 ? logits[(size_t)row * V + id] : -INFINITY;
     }
-    unsigned mask = __ballot_sync(0xffffffffu, valid && beats(z, id, tv, ti));
-    while (mask) {
-      const int src = __ffs(mask) - 1;
-      mask &= mask - 1;
-      warp_list_offer(lv, li, tv, ti, __shfl_sync(0xffffffffu, z, src), base + src);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int base = b0 + u * 128, id = base + lane;
+      const bool valid = id < v1;
+      float z = -INFINITY;
+      if (valid) {
+        z = mult * zz[u];
+        if (cap > 0.f) z = cap * tanhf(z / cap);
+        if (debug) debug[(size_t)row * V + id] = z;
+      }
+      unsigned mask = __ballot_sync(0xffffffffu, valid && beats(z, id, tv, ti));
+      while (mask) {
+        const int src = __ffs(mask) - 1;
+        mask &= mask - 1;
+        warp_list_offer(lv, li, tv, ti, __shfl_sync(0xffffffffu, z, src), base + src);
+      }
     }
   }
   if (lane < KMAX) {
