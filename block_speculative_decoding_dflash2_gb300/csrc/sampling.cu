@@ -36,9 +36,10 @@ constexpr int CAP = 2048;   // tokens of a list
 constexpr int SMALL = 256;  // tokens of a list that is ranked instead of sorted
 constexpr int CMAX = 8;     // CTAs of a row's cluster
 constexpr int LOCAL_K = 100;  // largest top-k whose tokens each CTA picks on its own
+constexpr int PROBE_K = 16;   // tokens each CTA picks to try for a top-p border
 constexpr int PARTS = 1024;   // room for what they pick
 constexpr int SUB = NT;       // finer bins of a list
-constexpr int SLICE2 = 19456, SLICE1 = 48000;  // logits a CTA holds, two CTAs and one CTA an SM
+constexpr int SLICE = 19456;  // logits a CTA holds in shared memory, with two CTAs an SM
 constexpr unsigned KEY_NINF = 0x007fffffu;  // order of -inf; NaN maps to 0
 
 // Order-preserving map of a logit (a larger one has a larger key; -0 equals 0).
@@ -84,60 +85,51 @@ __device__ __forceinline__ float2 pair_of(double x) {
   return make_float2(h, (float)(x - (double)h));
 }
 
-// exp((z - zmax) / T) in units of 2^-42, for z > -inf.  y = (zmax - z) log2(e)
-// / T is held as p + e (the difference exact by two-sum, the product by fma).
-// From y = 16 on, an fp32 exponential is good to 2^-38 of the largest mass.
-// Before, y = n + j/32 + g + e with |g| <= 1/64, and 2^-(g+e) = 1 - w + w^2/2 -
-// ... with w = (g + e) ln 2, whose linear term keeps its rounding error.
-// No branch depends on one value, so the N evaluations overlap; with VOTE a
-// warp whose values are all far skips the near form (same results).
-template <int N, bool VOTE>
-__device__ __forceinline__ void masses_of(const float (&z)[N], const Scale& s, const ExpTab& tab, u64 (&v)[N]) {
+// exp((z - zmax) / T) in units of 2^-42, for z > -inf.  From y = (zmax - z)
+// log2(e) / T = 18 on, plain fp32 is good to 2^-37 of the largest mass.  Before,
+// y is held as p + e (the difference exact by two-sum, the product by fma), y =
+// n + j/32 + g + e with |g| <= 1/64, and 2^-(g+e) = 1 - w + w^2/2 - ... with w =
+// (g + e) ln 2, whose linear term keeps its rounding error.
+constexpr float FAR = 18.f;
+__device__ __forceinline__ float y_of(float z, const Scale& s) {
+  return __fmul_rn(s.zmax - z, s.hi);  // never contracted: its rounding error is formed below
+}
+__device__ __forceinline__ unsigned far_mass(float y) {  // 0 from y = 44 on, infinity and NaN included
+  float f;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(42.f - y));
+  return __float2uint_rn(f);
+}
+// No branch depends on one value, so the N evaluations overlap.
+template <int N>
+__device__ __forceinline__ void masses_of(const float (&z)[N], const float (&p)[N], const Scale& s, const ExpTab& tab,
+                                          u64 (&v)[N]) {
   const float L1 = 0.693147182464599609f, L1lo = -1.90465429995776e-9f;  // ln 2
-  float p[N], e[N];
-  bool far = true;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const float dh = s.zmax - z[i];
-    p[i] = __fmul_rn(dh, s.hi);  // never contracted: its rounding error goes to e
-    const float bb = dh - s.zmax;
+    const float dh = s.zmax - z[i], bb = dh - s.zmax;
     const float dl = (s.zmax - (dh - bb)) - (z[i] + bb);
-    e[i] = fmaf(dl, s.hi, fmaf(dh, s.lo, fmaf(dh, s.hi, -p[i])));
-    far = far && p[i] >= 16.f;
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float f;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(42.f - p[i]));
-    v[i] = (u64)__float2uint_rn(fmaf(f, -L1 * e[i], f));  // (0 from y = 44 on, infinity included)
-  }
-  if (!VOTE || !__all_sync(0xffffffffu, far)) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float kf = fmaf(p[i], 32.f, 12582912.f);  // 1.5 2^23: rounds to a whole number of 32nds
-      const unsigned k = __float_as_uint(kf);
-      const float g = fmaf(kf - 12582912.f, -0.03125f, p[i]);
-      const float gl = __fmul_rn(g, L1);
-      const float glr = fmaf(g, L1lo, fmaf(e[i], L1, fmaf(g, L1, -gl)));
-      const float w = (g + e[i]) * L1;
-      const float q = w * w * fmaf(w, fmaf(w, 0.0416666667f, -0.1666666667f), 0.5f) - glr;  // 2^-(g+e) - 1 + gl
-      const float2 t = tab.pair[k & 31];
-      const float m = __fmul_rn(t.x, gl);
-      const float small = fmaf(t.x, q, -fmaf(t.x, gl, -m)) - t.y * gl;
-      const u64 near = tab.fix[k & 31] - (u64)((long long)__float2int_rn(m * 68719476736.f) << 6) +
-                       (u64)(long long)__float2int_rn(small * 4398046511104.f);
-      const int n = (k >> 5) & 31;  // 0..16
-      v[i] = p[i] < 16.f ? (near + ((1ull << n) >> 1)) >> n : v[i];
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i)
+    const float e = fmaf(dl, s.hi, fmaf(dh, s.lo, fmaf(dh, s.hi, -p[i])));
+    const float kf = fmaf(p[i], 32.f, 12582912.f);  // 1.5 2^23: rounds to a whole number of 32nds
+    const unsigned k = __float_as_uint(kf);
+    const float g = fmaf(kf - 12582912.f, -0.03125f, p[i]);
+    const float gl = __fmul_rn(g, L1);
+    const float glr = fmaf(g, L1lo, fmaf(e, L1, fmaf(g, L1, -gl)));
+    const float w = (g + e) * L1;
+    const float q = w * w * fmaf(w, fmaf(w, 0.0416666667f, -0.1666666667f), 0.5f) - glr;  // 2^-(g+e) - 1 + gl
+    const float2 t = tab.pair[k & 31];
+    const float m = __fmul_rn(t.x, gl);
+    const float small = fmaf(t.x, q, -fmaf(t.x, gl, -m)) - t.y * gl;
+    const u64 near = tab.fix[k & 31] - (u64)((long long)__float2int_rn(m * 68719476736.f) << 6) +
+                     (u64)(long long)__float2int_rn(small * 4398046511104.f);
+    const int n = (k >> 5) & 31;  // 0..18
+    v[i] = p[i] < FAR ? (near + ((1ull << n) >> 1)) >> n : (u64)far_mass(p[i]);
     if (z[i] == s.zmax || s.hi == 0.f) v[i] = 1ull << 42;
+  }
 }
 __device__ __forceinline__ u64 mass_of(float z, const Scale& s, const ExpTab& tab) {
-  const float x[1] = {z};
+  const float x[1] = {z}, y[1] = {y_of(z, s)};
   u64 v[1];
-  masses_of<1, false>(x, s, tab, v);
+  masses_of<1>(x, y, s, tab, v);
   return v[0];
 }
 
@@ -196,6 +188,31 @@ __device__ __forceinline__ bool kept(unsigned k, int id, const Cut& c) {
 // The same on a logit, `zc` being the value of the cut's key.
 __device__ __forceinline__ bool kept_z(float z, int id, float zc, int idc) { return z > zc || (z == zc && id <= idc); }
 
+// The masses of four logits (ids id .. id + 3), 0 for those the cut drops and
+// for id x.  A warp whose kept logits are all far takes the short way.
+__device__ __forceinline__ bool masses4(const float4& v, int id, const Scale& s, const ExpTab& tab, float zc, int idc,
+                                        int x, u64 (&e)[4]) {
+  const float z[4] = {v.x, v.y, v.z, v.w};
+  bool keep[4], near = false;
+  float y[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    keep[j] = kept_z(z[j], id + j, zc, idc) && id + j != x;
+    y[j] = y_of(z[j], s);
+    near = near || (keep[j] && !(y[j] >= FAR));
+  }
+  if (!__any_sync(0xffffffffu, near)) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) e[j] = keep[j] ? far_mass(y[j]) : 0u;
+    return false;
+  }
+  masses_of<4>(z, y, s, tab, e);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (!keep[j]) e[j] = 0;
+  return true;
+}
+
 // What the cluster's first CTA decides for the others.
 enum { STEP_NONE = 0, STEP_LIST = 1, STEP_TOPK = 2, STEP_TOPP = 3, STEP_SLOW_K = 4, STEP_SLOW_P = 5 };
 struct Decision {
@@ -219,7 +236,7 @@ struct Smem {
       unsigned sub_lo[SUB], sub_hi[SUB];  // masses of a list's finer bins: the low 21 bits, the rest
     };
   };
-  u64 wsum[NW];
+  u64 wsum[NW], wsum2[NW];
   u64 xm[2][CMAX], xg[2][CMAX];  // exchanged masses, two turns
   float xmax[CMAX], xmin[CMAX], xlow[CMAX];
   int xid[CMAX];
@@ -238,17 +255,6 @@ struct Smem {
   u64 sel_before;
   int pick, pick2;
 };
-
-__device__ __forceinline__ u64 block_sum_u64(u64 v, Smem& sm) {
-  v = warp_sum_u64(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sm.wsum[threadIdx.x >> 5] = v;
-  __syncthreads();
-  u64 t = 0;
-#pragma unroll
-  for (int i = 0; i < NW; ++i) t += sm.wsum[i];
-  return t;
-}
 
 // Sum over the threads before this one (and the block's total).
 __device__ __forceinline__ u64 block_scan_u64(u64 mine, u64* total, Smem& sm) {
@@ -296,18 +302,26 @@ __device__ __noinline__ void sort_desc(u64* a, int n) {
 // outside the slice reads as -inf.
 template <typename T, bool RES>
 struct Slice {
+  static constexpr int U = RES ? 1 : 4;  // groups whose loads are in flight
   const T* row;
   float* zs;
   int begin, end, first, groups;
   __device__ __forceinline__ float4 get4(int i) const {
     if constexpr (RES) return *reinterpret_cast<const float4*>(zs + 4 * i);
+    const int id = first + 4 * i;
+    if (id >= begin && id + 4 <= end) {
+      if constexpr (sizeof(T) == 4) {
+        return __ldg(reinterpret_cast<const float4*>(row + id));
+      } else {
+        const uint2 q = __ldg(reinterpret_cast<const uint2*>(row + id));
+        return make_float4(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u), __uint_as_float(q.y << 16),
+                           __uint_as_float(q.y & 0xffff0000u));
+      }
+    }
     float4 v;
     float* e = &v.x;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int id = first + 4 * i + j;
-      e[j] = id >= begin && id < end ? ld(row + id) : -INFINITY;
-    }
+    for (int j = 0; j < 4; ++j) e[j] = id + j >= begin && id + j < end ? ld(row + id + j) : -INFINITY;
     return v;
   }
 };
@@ -328,25 +342,26 @@ __device__ __forceinline__ void unpack16<bf16>(const uint4& v, float (&e)[8]) {
   }
 }
 
-// Calls f(z, id) on every element of the slice, each lane its own; every
+// Calls f(four logits, id of the first) on every group of the slice; every
 // thread makes the same number of calls (elements outside read as -inf).
 template <typename S, typename F>
-__device__ __forceinline__ void for_each(const S& s, F f) {
-  for (int i0 = 0; i0 < s.groups; i0 += NT) {
-    const int i = i0 + threadIdx.x;
-    const float4 v = i < s.groups ? s.get4(i) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-    const int id = s.first + 4 * i;
-    f(v.x, id), f(v.y, id + 1), f(v.z, id + 2), f(v.w, id + 3);
+__device__ __forceinline__ void for_each4(const S& s, F f) {
+  for (int i0 = 0; i0 < s.groups; i0 += NT * S::U) {
+    float4 v[S::U];
+#pragma unroll
+    for (int u = 0; u < S::U; ++u) {
+      const int i = i0 + u * NT + threadIdx.x;
+      v[u] = i < s.groups ? s.get4(i) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    }
+#pragma unroll
+    for (int u = 0; u < S::U; ++u)
+      if (u == 0 || i0 + u * NT < s.groups) f(v[u], s.first + 4 * (i0 + u * NT + (int)threadIdx.x));
   }
 }
-
-// Calls f(four logits, id of the first) on every group of the slice.
+// The same for single elements.
 template <typename S, typename F>
-__device__ __forceinline__ void for_each4(const S& s, F f) {
-  for (int i0 = 0; i0 < s.groups; i0 += NT) {
-    const int i = i0 + threadIdx.x;
-    f(i < s.groups ? s.get4(i) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY), s.first + 4 * i);
-  }
+__device__ __forceinline__ void for_each(const S& s, F f) {
+  for_each4(s, [&](const float4& v, int id) { f(v.x, id), f(v.y, id + 1), f(v.z, id + 2), f(v.w, id + 3); });
 }
 
 // Appends the logits for which in(z) holds, all of them in [low, high], to a
@@ -591,8 +606,11 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
   // A small top-k: each CTA picks its own candidates.  The k-th largest of its
   // threads' largest logits has at least k logits that are not below it, so no
   // token of the row's top k lies below it; few others do not.
-  const bool by_k0 = !greedy && top_k > 0 && top_k < V;
-  bool local = by_k0 && top_k <= LOCAL_K;
+  // (A top-p alone tries the same with a few tokens: the nucleus of a peaked
+  // row is among them.)
+  const bool by_k0 = !greedy && top_k > 0 && top_k < V, probe = !greedy && !by_k0 && top_p < 1.f;
+  const int pick_k = by_k0 ? top_k : PROBE_K;
+  bool local = probe || (by_k0 && top_k <= LOCAL_K);
   if (local) {
     const float range = fminf(mx - mn, 64.f);
     const float per = range > 0.f ? fminf((float)SUB / range, 1e30f) : 1.f;
@@ -602,8 +620,8 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     u64 all;
     const unsigned c = sm.hist[tid];
     const u64 before = block_scan_u64(c, &all, sm);
-    const bool enough = all >= (u64)top_k;
-    if (before < (u64)top_k && (u64)top_k <= before + c) sm.pick = tid;
+    const bool enough = all >= (u64)pick_k;
+    if (before < (u64)pick_k && (u64)pick_k <= before + c) sm.pick = tid;
     __syncthreads();
     float low = enough && thread_max > -INFINITY && bin <= sm.pick ? thread_max : INFINITY;
     low = -warp_max(-low);
@@ -623,19 +641,17 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     cluster_sync();
     for (int r = 0; r < C; ++r) {
       zmax = fmaxf(zmax, sm.xmax[r]);
-      local = local && sm.xid[r] <= (int)part;
-    }
-    if (!local) {  // too many in one part: the ways below
-      for (int b = tid; b < NB; b += NT) sm.hist[b] = 0;
-      if (tid == 0) {
-        sm.ncand = 0;
-        sm.pick = -1;
-      }
+      local = local && sm.xid[r] <= (int)part;  // (else too many in one part: the ways below)
     }
   } else {
     cluster_wait();
   }
-  if (!local) {
+  auto full_range = [&]() {  // the row's range, and a clean start of the ways below
+    for (int b = tid; b < NB; b += NT) sm.hist[b] = 0;
+    if (tid == 0) {
+      sm.ncand = 0;
+      sm.pick = -1;
+    }
     if (tid < C) {
       st_cl(dsmem_addr(&sm.xmax[rank], tid), __float_as_uint(mx));
       st_cl(dsmem_addr(&sm.xmin[rank], tid), __float_as_uint(mn));
@@ -645,7 +661,8 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
       zmax = fmaxf(zmax, sm.xmax[r]);
       zmin = fminf(zmin, sm.xmin[r]);
     }
-  }
+  };
+  if (!local) full_range();
   const Scale sc = {zmax, sm.c_pair.x, sm.c_pair.y};
   const bool empty = !(zmax > -INFINITY);
 
@@ -675,9 +692,17 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
   // Sums two masses over the cluster.
   int turn = 0;
   auto exchange = [&](u64& m, u64& g) {
-    m = block_sum_u64(m, sm);
-    g = block_sum_u64(g, sm);
+    m = warp_sum_u64(m);
+    g = warp_sum_u64(g);
+    __syncthreads();
+    if (lane == 0) {
+      sm.wsum[warp] = m;
+      sm.wsum2[warp] = g;
+    }
+    __syncthreads();
     if (tid < C) {
+      m = g = 0;
+      for (int w = 0; w < NW; ++w) m += sm.wsum[w], g += sm.wsum2[w];
       st_cl(dsmem_addr(&sm.xm[turn][rank], tid), m);
       st_cl(dsmem_addr(&sm.xg[turn][rank], tid), g);
     }
@@ -686,17 +711,17 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     for (int r = 0; r < C; ++r) m += sm.xm[turn][r], g += sm.xg[turn][r];
     turn ^= 1;
   };
-  auto mass_kept = [&]() {
-    u64 m = 0, g = 0;
+  auto mass_into = [&](u64& m) {  // adds this thread's share of the kept mass
     const float zc = okey_value(cut.key);
     for_each4(s, [&](const float4& v, int id) {
-      const float z[4] = {v.x, v.y, v.z, v.w};
-      if (!__any_sync(0xffffffffu, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) >= zc)) return;
       u64 e[4];
-      masses_of<4, true>(z, sc, sm.tab, e);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) m += kept_z(z[j], id + j, zc, cut.id) ? e[j] : 0ull;
+      if (masses4(v, id, sc, sm.tab, zc, cut.id, -1, e)) m += (e[0] + e[1]) + (e[2] + e[3]);
+      else m += ((unsigned)e[0] + (unsigned)e[1]) + ((unsigned)e[2] + (unsigned)e[3]);  // (below 2^26)
     });
+  };
+  auto mass_kept = [&]() {
+    u64 m = 0, g = 0;
+    mass_into(m);
     exchange(m, g);
     return m;
   };
@@ -824,66 +849,98 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
         }
       }
     };
-    if (local) {
-      list = true;
-      if (rank == 0) {
-        // The parts in one piece (in any order), without what lies below any of
-        // their bounds.  Then, if that leaves several warps' worth, each full
-        // warp sorts 32 of them: with F warps, at least top_k tokens are not
-        // below the least of the warps' ceil(top_k / F)-th tokens.
-        float low = -INFINITY;
-        for (int r = 0; r < C; ++r) low = fmaxf(low, sm.xlow[r]);
-        const unsigned low_key = okey(low), lg_part = 10 - a.lg_cluster;
-        static_assert(PARTS == 1 << 10, "lg_part");
-        if (tid == 0) {
-          sm.ncand = 0;
-          sm.bound = ~0ull;
-        }
-        __syncthreads();
-        auto append = [&](bool yes, u64 v) {
-          const unsigned m = __ballot_sync(0xffffffffu, yes);
-          if (!m) return;
-          unsigned at = 0;
-          if (lane == 0) at = atomicAdd(&sm.ncand, __popc(m));
-          at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1));
-          if (yes) sm.cand[at] = v;
-        };
+    auto merge_parts = [&]() {
+      // The parts in one piece (in any order), without what lies below any of
+      // their bounds.  Then, if that leaves several warps' worth, each full
+      // warp sorts 32 of them: with F warps, at least top_k tokens are not
+      // below the least of the warps' ceil(top_k / F)-th tokens.
+      float low = -INFINITY;
+      for (int r = 0; r < C; ++r) low = fmaxf(low, sm.xlow[r]);
+      const unsigned low_key = okey(low), lg_part = 10 - a.lg_cluster;
+      static_assert(PARTS == 1 << 10, "lg_part");
+      if (tid == 0) {
+        sm.ncand = 0;
+        sm.bound = ~0ull;
+      }
+      __syncthreads();
+      auto append = [&](bool yes, u64 v) {
+        const unsigned m = __ballot_sync(0xffffffffu, yes);
+        if (!m) return;
+        unsigned at = 0;
+        if (lane == 0) at = atomicAdd(&sm.ncand, __popc(m));
+        at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1));
+        if (yes) sm.cand[at] = v;
+      };
 #pragma unroll
-        for (int j = 0; j < PARTS / NT; ++j) {
-          const unsigned e = tid + j * NT, r = e >> lg_part;
-          const u64 v = e - (r << lg_part) < (unsigned)sm.xid[r] ? sm.parts[e] : 0ull;
-          append((unsigned)(v >> 32) >= low_key && v, v);
-        }
-        if (tid == 0) sm.pick = -1;
-        __syncthreads();
-        int all = (int)sm.ncand;
-        const int full = all / 32;
-        if (full >= 2 && all <= NT && top_k <= 32 * full) {
-          u64 v = tid < all ? sm.cand[tid] : 0ull;
-          if (warp < full) {
-            u64 y = v;
+      for (int j = 0; j < PARTS / NT; ++j) {
+        const unsigned e = tid + j * NT, r = e >> lg_part;
+        const u64 v = e - (r << lg_part) < (unsigned)sm.xid[r] ? sm.parts[e] : 0ull;
+        append((unsigned)(v >> 32) >= low_key && v, v);
+      }
+      if (tid == 0) sm.pick = -1;
+      __syncthreads();
+      int all = (int)sm.ncand;
+      const int full = all / 32;
+      if (by_k && full >= 2 && top_k <= 32 * full) {
+        static_assert(PARTS <= 2 * NT, "two tokens a thread");
+        u64 v[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int e = tid + j * NT;
+          v[j] = e < all ? sm.cand[e] : 0ull;
+          if (warp + j * NW < full) {
+            u64 y = v[j];
 #pragma unroll
             for (int k = 2; k <= 32; k <<= 1)
 #pragma unroll
-              for (int j = k >> 1; j > 0; j >>= 1) {
-                const u64 o = __shfl_xor_sync(0xffffffffu, y, j);
-                const bool larger = ((lane & j) == 0) == ((lane & k) == 0);
-                y = larger ? (y > o ? y : o) : (y < o ? y : o);
+              for (int o = k >> 1; o > 0; o >>= 1) {
+                const u64 w = __shfl_xor_sync(0xffffffffu, y, o);
+                const bool larger = ((lane & o) == 0) == ((lane & k) == 0);
+                y = larger ? (y > w ? y : w) : (y < w ? y : w);
               }
             y = __shfl_sync(0xffffffffu, y, (top_k + full - 1) / full - 1);
             if (lane == 0) atomicMin(&sm.bound, y);
           }
-          __syncthreads();
-          if (tid == 0) sm.ncand = 0;
-          const u64 bound = sm.bound;
-          __syncthreads();
-          append(v >= bound && v, v);
-          __syncthreads();
-          all = (int)sm.ncand;
         }
-        cut_list(all);
+        __syncthreads();
+        if (tid == 0) sm.ncand = 0;
+        const u64 bound = sm.bound;
+        __syncthreads();
+        append(v[0] >= bound && v[0], v[0]);
+        append(v[1] >= bound && v[1], v[1]);
+        __syncthreads();
+        all = (int)sm.ncand;
       }
-    } else {
+      return all;
+    };
+    if (local && by_k) {
+      list = true;
+      if (rank == 0) cut_list(merge_parts());
+    } else if (local) {
+      u64 m = 0, g = 0;
+      mass_into(m);
+      exchange(m, g);
+      if (rank == 0) {
+        const int n = merge_parts();
+        small = n <= SMALL;
+        bool found = false;
+        if (small) {
+          const u64 want = share_of(top_p, m);
+          rank_list(n);
+          tell(0, lrank > 0 && lrank == n, 0);
+          found = want <= total;
+          if (found) tell(1, lrank > 0 && lcum >= want && lcum - lmass < want, 0);
+        }
+        if (tid == 0) sm.mk.step = found ? STEP_LIST : STEP_NONE;
+      }
+      list = broadcast().step == STEP_LIST;
+      if (!list) {
+        cut = {KEY_NINF + 1, V};
+        total = 0;
+        full_range();
+      }
+    }
+    if (!list) {
     // bins of equal width over [zmax - 64, zmax] or the row's own range if that
     // is smaller; what lies lower falls into the last bin
     const float range = fminf(zmax - zmin, 64.f);
@@ -1028,13 +1085,11 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
           u64 m = 0, g = 0;  // kept mass, and what of it lies ahead of the gathered bins
           const float zc = okey_value(cut.key);
           for_each4(s, [&](const float4& v, int id) {
-            const float z[4] = {v.x, v.y, v.z, v.w};
-            if (!__any_sync(0xffffffffu, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) >= zc)) return;
             u64 e[4];
-            masses_of<4, true>(z, sc, sm.tab, e);
+            masses4(v, id, sc, sm.tab, zc, cut.id, -1, e);
+            const float z[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              if (!kept_z(z[j], id + j, zc, cut.id)) e[j] = 0;
               m += e[j];
               g += bin_of(z[j]) < lo ? e[j] : 0ull;
             }
@@ -1253,20 +1308,27 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
   if (list) {
     const bool pass = verify && i < nd && passes();
     if (!pass && small) {
-      // the running mass in id order at this thread's token
-      const u64 e = lrank > 0 && lrank <= n_kept && (int)~(unsigned)lkey != x ? lmass : 0ull;
-      const int n = (int)sm.ncand, t0 = tid / lanes;
-      if (t0 < n) sm.radix[t0] = e;
+      // the kept tokens in one piece (by rank), then the running mass in id
+      // order at each of them, its lanes as many as there are threads for
+      if (lrank > 0 && lrank <= n_kept) {
+        sm.cand[CAP - 1 - lrank] = lkey;  // (the list itself lies below)
+        sm.radix[lrank - 1] = (int)~(unsigned)lkey != x ? lmass : 0ull;
+      }
       __syncthreads();
+      lanes = 32;
+      while (lanes > 1 && n_kept * lanes > NT) lanes >>= 1;
+      const int t0 = tid / lanes;
+      const u64* kept_list = sm.cand + CAP - 2;  // token of rank r + 1 at kept_list[-r]
+      const unsigned me = t0 < n_kept ? (unsigned)kept_list[-t0] : 0u;
+      const u64 e = t0 < n_kept ? sm.radix[t0] : 0ull;
       u64 c = 0;
       if (e) {
 #pragma unroll 4
-        for (int j = tid & (lanes - 1); j < n; j += lanes)
-          c += (unsigned)sm.cand[j] >= (unsigned)lkey ? sm.radix[j] : 0ull;
+        for (int j = tid & (lanes - 1); j < n_kept; j += lanes) c += (unsigned)kept_list[-j] >= me ? sm.radix[j] : 0ull;
       }
       for (int o = 1; o < lanes; o <<= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
       const u64 t = threshold(total - x_mass);
-      if (e && c - e <= t && t < c) sm.pick = (int)~(unsigned)lkey;
+      if (e && c - e <= t && t < c) sm.pick = (int)~me;
       __syncthreads();
     } else if (!pass) {
       // the kept tokens in id order, and the first whose running mass exceeds the draw
@@ -1303,13 +1365,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
   const float zc = okey_value(cut.key);
   auto mass4 = [&](int q, u64 (&e)[4]) {
     const float4 v = q < g1 ? s.get4(q) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-    const float zz[4] = {v.x, v.y, v.z, v.w};
-    masses_of<4, true>(zz, sc, sm.tab, e);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int id = s.first + 4 * q + j;
-      if (id == x || !kept_z(zz[j], id, zc, cut.id)) e[j] = 0;
-    }
+    masses4(v, s.first + 4 * q, sc, sm.tab, zc, cut.id, x, e);
   };
   u64 wm = 0;
   for (int q0 = g0; q0 < g1; q0 += 32) {
@@ -1377,7 +1433,7 @@ int launch_one(const SamplingArgs& a, int slice, const Ctx& c) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DFLASH2_ERR_CUDA;
   if (RES && !(opted.load(std::memory_order_relaxed) >> dev & 1)) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (SLICE1 + 16) * 4) != cudaSuccess)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (SLICE + 16) * 4) != cudaSuccess)
       return DFLASH2_ERR_CUDA;
     opted.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
@@ -1385,17 +1441,21 @@ int launch_one(const SamplingArgs& a, int slice, const Ctx& c) {
   return launch_kx(kern, dim3((a.batch * a.rows) << a.lg_cluster), dim3(NT), smem, c, 1 << a.lg_cluster, a, slice);
 }
 
-// A row's cluster: as few CTAs as hold it with two of them an SM (one, for the
-// largest vocabularies that still fit), more while the rows leave SMs idle.
+// A row's cluster: as few CTAs as hold it in shared memory with two of them an
+// SM, more while the rows leave SMs idle.  (Rows shared out over one wave
+// instead, up to one CTA a row that reads its logits again from L2 in every
+// pass, took 315 us against 106 at 256 rows of 151936: the few rows without a
+// small top-k keep their one CTA long after the others are done.)  What does
+// not fit is read again from L2.
 template <typename T>
 int launch_rows(SamplingArgs a, const Ctx& c) {
-  const int rows = a.batch * a.rows;
+  const long long rows = (long long)a.batch * a.rows;
   a.lg_cluster = 0;
-  while (1 << a.lg_cluster < CMAX && (a.vocab > SLICE2 << a.lg_cluster ||
+  while (1 << a.lg_cluster < CMAX && (a.vocab > SLICE << a.lg_cluster ||
                                       (rows << a.lg_cluster < c.nsm && a.vocab > 4096 << a.lg_cluster)))
     ++a.lg_cluster;
   const int slice = ((a.vocab + (1 << a.lg_cluster) - 1 >> a.lg_cluster) + 7) / 8 * 8;
-  return slice <= SLICE1 ? launch_one<T, true>(a, slice, c) : launch_one<T, false>(a, slice, c);
+  return slice <= SLICE ? launch_one<T, true>(a, slice, c) : launch_one<T, false>(a, slice, c);
 }
 
 }  // namespace
