@@ -239,6 +239,7 @@ struct Smem {
   u64 wsum[NW], wsum2[NW];
   u64 xm[2][CMAX], xg[2][CMAX];  // exchanged masses, two turns
   float xmax[CMAX], xmin[CMAX], xlow[CMAX];
+  float2 xest[CMAX];
   int xid[CMAX];
   float fsum[NW], fmin[NW];
   float2 c_pair, off_pair;  // log2(e) / T and T ln(min_p)
@@ -250,7 +251,7 @@ struct Smem {
     int n;
   } sel[3];  // small lists: the kept tokens after top-k, top-p and min-p
   u64 bound;
-  unsigned ncand;
+  unsigned ncand, nlocal;  // tokens in the first CTA's list, and in this CTA's own
   unsigned sel_key;
   u64 sel_before;
   int pick, pick2;
@@ -364,11 +365,10 @@ __device__ __forceinline__ void for_each(const S& s, F f) {
   for_each4(s, [&](const float4& v, int id) { f(v.x, id), f(v.y, id + 1), f(v.z, id + 2), f(v.w, id + 3); });
 }
 
-// Appends the logits for which in(z) holds, all of them in [low, high], to a
-// list: `counter` is this CTA's, `base` the first CTA's list or this CTA's
-// part of it, which takes `most`.
+// Appends the logits for which in(z) holds, all of them in [low, high], to this
+// CTA's list of room `most`, counted in `counter`.
 template <typename S, typename F>
-__device__ __forceinline__ void collect(const S& s, float low, float high, F in, uint32_t counter, uint32_t base,
+__device__ __forceinline__ void collect(const S& s, float low, float high, F in, unsigned* counter, u64* list,
                                         unsigned most) {
   const int lane = threadIdx.x & 31;
   for_each4(s, [&](const float4& v, int id) {
@@ -377,16 +377,23 @@ __device__ __forceinline__ void collect(const S& s, float low, float high, F in,
 #pragma unroll
     for (int j = 0; j < 4; ++j) any = any || (zz[j] >= low && zz[j] <= high);
     if (!__any_sync(0xffffffffu, any)) return;
+    unsigned m[4], n = 0, mine = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const bool yes = zz[j] >= low && zz[j] <= high && zz[j] > -INFINITY && in(zz[j]);
-      const unsigned m = __ballot_sync(0xffffffffu, yes);
-      if (m) {
-        unsigned at = 0;
-        if (lane == 0) at = add_cl(counter, __popc(m));
-        at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1));
-        if (yes && at < most) st_cl(base + 8 * at, ((u64)okey(zz[j]) << 32) | (unsigned)~(id + j));
-      }
+      m[j] = __ballot_sync(0xffffffffu, yes);
+      n += __popc(m[j]);
+      mine |= (unsigned)yes << j;
+    }
+    if (!n) return;
+    unsigned at = 0;
+    if (lane == 0) at = atomicAdd(counter, n);
+    at = __shfl_sync(0xffffffffu, at, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const unsigned pos = at + __popc(m[j] & ((1u << lane) - 1));
+      if ((mine >> j & 1) && pos < most) list[pos] = ((u64)okey(zz[j]) << 32) | (unsigned)~(id + j);
+      at += __popc(m[j]);
     }
   });
 }
@@ -586,7 +593,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
   for (int b = tid; b < NB; b += NT) sm.hist[b] = 0;
   if (has_word) reinterpret_cast<unsigned*>(&sm.tab)[tid] = word;
   if (tid == 0) {
-    sm.ncand = 0;
+    sm.ncand = sm.nlocal = 0;
     sm.pick = -1;
     sm.pick2 = 0x7fffffff;
   }
@@ -631,17 +638,55 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     if (!enough) low = -3.402823466e+38f;  // fewer logits than that: all of them
     const unsigned part = PARTS >> a.lg_cluster;
     cluster_wait();
-    collect(s, low, INFINITY, [](float) { return true; }, smem_u32(&sm.ncand), dsmem_addr(sm.parts + rank * part, 0), part);
+    collect(s, low, INFINITY, [](float) { return true; }, &sm.nlocal, sm.cand, part);
     __syncthreads();
+    for (unsigned e = tid; e < min(sm.nlocal, part); e += NT) st_cl(dsmem_addr(sm.parts + rank * part + e, 0), sm.cand[e]);
+    if (probe) {
+      // whether the picked tokens can hold the nucleus at all: their mass, and
+      // that of the others from a sample (a group a thread), relative to this
+      // CTA's largest logit; it only decides which way is tried
+      float picked = 0.f, others = 0.f;
+      const float c = sm.c_pair.x;
+      for (unsigned e = tid; e < min(sm.nlocal, part); e += NT)
+        picked += exp2f((okey_value((unsigned)(sm.cand[e] >> 32)) - mx) * c);
+      if (tid < s.groups) {
+        const float4 v = s.get4(tid);
+        const float z[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) others += z[j] < low ? exp2f((z[j] - mx) * c) : 0.f;
+      }
+      picked = warp_sum(picked);
+      others = warp_sum(others) * (float)s.groups / (float)min(s.groups, NT);
+      if (lane == 0) {
+        sm.fsum[warp] = picked;
+        sm.fmin[warp] = others;
+      }
+      __syncthreads();
+    }
     if (tid < C) {
       st_cl(dsmem_addr(&sm.xmax[rank], tid), __float_as_uint(mx));
       st_cl(dsmem_addr(&sm.xlow[rank], tid), __float_as_uint(low));
-      st_cl(dsmem_addr(&sm.xid[rank], tid), sm.ncand);
+      st_cl(dsmem_addr(&sm.xid[rank], tid), sm.nlocal);
+      if (probe) {
+        float x = 0.f, y = 0.f;
+        for (int w = 0; w < NW; ++w) x += sm.fsum[w], y += sm.fmin[w];
+        st_cl(dsmem_addr(&sm.xest[rank].x, tid), __float_as_uint(x));
+        st_cl(dsmem_addr(&sm.xest[rank].y, tid), __float_as_uint(y));
+      }
     }
     cluster_sync();
     for (int r = 0; r < C; ++r) {
       zmax = fmaxf(zmax, sm.xmax[r]);
       local = local && sm.xid[r] <= (int)part;  // (else too many in one part: the ways below)
+    }
+    if (probe) {
+      float picked = 0.f, all = 0.f;
+      for (int r = 0; r < C; ++r) {
+        const float f = sm.xmax[r] == zmax ? 1.f : exp2f((sm.xmax[r] - zmax) * sm.c_pair.x);
+        picked += f * sm.xest[r].x;
+        all += f * (sm.xest[r].x + sm.xest[r].y);
+      }
+      local = local && picked >= 0.9f * top_p * all;  // (false for NaN)
     }
   } else {
     cluster_wait();
@@ -988,8 +1033,21 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
       // (bounds beyond the bins' ends, roundings included, skip most)
       const float low = hi == NB - 1 ? -INFINITY : zmax - (float)(hi + 1) / per * 1.0001f;
       const float high = lo == 0 ? INFINITY : zmax - (float)lo / per * 0.9999f;
-      collect(s, low, high, [&](float z) { const int b = bin_of(z); return b >= lo && b <= hi; },
-              dsmem_addr(&sm.ncand, 0), dsmem_addr(sm.cand, 0), CAP);
+      auto in = [&](float z) { const int b = bin_of(z); return b >= lo && b <= hi; };
+      if (rank == 0) {
+        collect(s, low, high, in, &sm.ncand, sm.cand, CAP);
+      } else {  // to a list of its own, copied behind one reservation in the first CTA's
+        if (tid == 0) sm.nlocal = 0;
+        __syncthreads();
+        collect(s, low, high, in, &sm.nlocal, sm.cand, CAP);
+        __syncthreads();
+        const unsigned n = min(sm.nlocal, (unsigned)CAP);
+        if (tid == 0) sm.sel_key = add_cl(dsmem_addr(&sm.ncand, 0), n);
+        __syncthreads();
+        const unsigned at = sm.sel_key;
+        for (unsigned e = tid; e < n; e += NT)
+          if (at + e < CAP) st_cl(dsmem_addr(sm.cand + at + e, 0), sm.cand[e]);
+      }
     };
 
     if (dec.step == STEP_LIST) {
