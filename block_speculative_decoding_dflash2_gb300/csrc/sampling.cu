@@ -78,6 +78,7 @@ __device__ const ExpTab c_exp = {
 // The row's exponent scale log2(e) / T as a float pair.
 struct Scale {
   float zmax, hi, lo;
+  bool odd;  // zmax or the temperature is infinite
 };
 // x as a float pair.
 __device__ __forceinline__ float2 pair_of(double x) {
@@ -119,11 +120,20 @@ __device__ __forceinline__ void masses_of(const float (&z)[N], const float (&p)[
     const float2 t = tab.pair[k & 31];
     const float m = __fmul_rn(t.x, gl);
     const float small = fmaf(t.x, q, -fmaf(t.x, gl, -m)) - t.y * gl;
-    const u64 near = tab.fix[k & 31] - (u64)((long long)__float2int_rn(m * 68719476736.f) << 6) +
-                     (u64)(long long)__float2int_rn(small * 4398046511104.f);
-    const int n = (k >> 5) & 31;  // 0..18
-    v[i] = p[i] < FAR ? (near + ((1ull << n) >> 1)) >> n : (u64)far_mass(p[i]);
-    if (z[i] == s.zmax || s.hi == 0.f) v[i] = 1ull << 42;
+    u64 near = tab.fix[k & 31];
+    asm("mad.wide.s32 %0, %1, -64, %0;" : "+l"(near) : "r"(__float2int_rn(m * 68719476736.f)));
+    asm("mad.wide.s32 %0, %1, 1, %0;" : "+l"(near) : "r"(__float2int_rn(small * 4398046511104.f)));
+    const unsigned n = (k >> 5) & 31;  // 0..18
+    near += (1u << n) >> 1;
+    const unsigned lo = __funnelshift_r((unsigned)near, (unsigned)(near >> 32), n), hi = (unsigned)(near >> 32) >> n;
+    const bool is_near = p[i] < FAR;
+    v[i] = is_near ? ((u64)hi << 32 | lo) : (u64)far_mass(p[i]);
+  }
+  // (a difference or a product without a value: an infinite maximum, T = infinity)
+  if (s.odd) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (z[i] == s.zmax || s.hi == 0.f) v[i] = 1ull << 42;
   }
 }
 __device__ __forceinline__ u64 mass_of(float z, const Scale& s, const ExpTab& tab) {
@@ -188,16 +198,36 @@ __device__ __forceinline__ bool kept(unsigned k, int id, const Cut& c) {
 // The same on a logit, `zc` being the value of the cut's key.
 __device__ __forceinline__ bool kept_z(float z, int id, float zc, int idc) { return z > zc || (z == zc && id <= idc); }
 
+// The same as one comparison where every token at the cut's value stays.
+struct CutZ {
+  float below, at;  // kept: z > below, unless z == at and the id is past idc
+  int idc;
+  bool ties;  // some token at the cut's value does not stay
+};
+__device__ __forceinline__ CutZ cut_z(const Cut& c, int V) {
+  // (the key below that of 0 is that of -0, which equals 0)
+  return {okey_value(c.key - (c.key == 0x80000000u ? 2 : 1)), okey_value(c.key), c.id, c.id < V - 1};
+}
+
 // The masses of four logits (ids id .. id + 3), 0 for those the cut drops and
 // for id x.  A warp whose kept logits are all far takes the short way.
-__device__ __forceinline__ bool masses4(const float4& v, int id, const Scale& s, const ExpTab& tab, float zc, int idc,
+__device__ __forceinline__ bool masses4(const float4& v, int id, const Scale& s, const ExpTab& tab, const CutZ& c,
                                         int x, u64 (&e)[4]) {
   const float z[4] = {v.x, v.y, v.z, v.w};
   bool keep[4], near = false;
   float y[4];
 #pragma unroll
+  for (int j = 0; j < 4; ++j) keep[j] = z[j] > c.below;
+  if (c.ties) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) keep[j] = keep[j] && (z[j] > c.at || id + j <= c.idc);
+  }
+  if ((unsigned)(x - id) < 4u) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) keep[j] = keep[j] && id + j != x;
+  }
+#pragma unroll
   for (int j = 0; j < 4; ++j) {
-    keep[j] = kept_z(z[j], id + j, zc, idc) && id + j != x;
     y[j] = y_of(z[j], s);
     near = near || (keep[j] && !(y[j] >= FAR));
   }
@@ -708,7 +738,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     }
   };
   if (!local) full_range();
-  const Scale sc = {zmax, sm.c_pair.x, sm.c_pair.y};
+  const Scale sc = {zmax, sm.c_pair.x, sm.c_pair.y, zmax == INFINITY || sm.c_pair.x == 0.f};
   const bool empty = !(zmax > -INFINITY);
 
   Cut cut = {KEY_NINF + 1, V};  // everything above -inf
@@ -757,10 +787,10 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     turn ^= 1;
   };
   auto mass_into = [&](u64& m) {  // adds this thread's share of the kept mass
-    const float zc = okey_value(cut.key);
+    const CutZ cz = cut_z(cut, V);
     for_each4(s, [&](const float4& v, int id) {
       u64 e[4];
-      if (masses4(v, id, sc, sm.tab, zc, cut.id, -1, e)) m += (e[0] + e[1]) + (e[2] + e[3]);
+      if (masses4(v, id, sc, sm.tab, cz, -1, e)) m += (e[0] + e[1]) + (e[2] + e[3]);
       else m += ((unsigned)e[0] + (unsigned)e[1]) + ((unsigned)e[2] + (unsigned)e[3]);  // (below 2^26)
     });
   };
@@ -1141,10 +1171,10 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
           dec = broadcast();
           const int lo = dec.lo, hi = dec.hi;
           u64 m = 0, g = 0;  // kept mass, and what of it lies ahead of the gathered bins
-          const float zc = okey_value(cut.key);
+          const CutZ cz = cut_z(cut, V);
           for_each4(s, [&](const float4& v, int id) {
             u64 e[4];
-            masses4(v, id, sc, sm.tab, zc, cut.id, -1, e);
+            masses4(v, id, sc, sm.tab, cz, -1, e);
             const float z[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -1420,10 +1450,10 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
   }
   // no list: masses by warp, each a contiguous range of the slice's groups
   const int g0 = (int)((long long)s.groups * warp / NW), g1 = (int)((long long)s.groups * (warp + 1) / NW);
-  const float zc = okey_value(cut.key);
+  const CutZ cz = cut_z(cut, V);
   auto mass4 = [&](int q, u64 (&e)[4]) {
     const float4 v = q < g1 ? s.get4(q) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-    masses4(v, s.first + 4 * q, sc, sm.tab, zc, cut.id, x, e);
+    masses4(v, s.first + 4 * q, sc, sm.tab, cz, x, e);
   };
   u64 wm = 0;
   for (int q0 = g0; q0 < g1; q0 += 32) {

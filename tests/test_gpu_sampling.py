@@ -208,6 +208,24 @@ def test_rows_masked_with_the_lowest_bf16_value():
             check_probs(got[r], R.masses(zv[r], *plain(spec)))
 
 
+def test_borders_at_zero_and_among_its_neighbours():
+    """Cuts whose last token is +0, -0 or a subnormal next to them."""
+    B = lib()
+    V = 3000
+    tiny = np.float32(1.4e-45)
+    z = np.random.default_rng(4).choice(np.array([0.0, -0.0, tiny, -tiny, 1.0, -1.0], np.float32), (3, V))
+    zt = dev(z)
+    u = np.array([0.2, 0.5, 0.95], np.float32)
+    for spec in ((1.0, None, 0.5, None), (1.0, None, 0.8, None), (1.0, 900, None, None), (1.0, 1700, 0.9, None),
+                 (1.0, 60, None, None), (1.0, 2400, 0.7, 0.5)):
+        got = run_probs(B, zt[:, None], settings_of(3, spec))[:, 0].cpu().numpy()
+        tok, _ = run_sample(B, zt, settings_of(3, spec), u, prob=False)
+        for r in range(3):
+            w = R.masses(z[r], *plain(spec))
+            check_probs(got[r], w)
+            assert tok[r] == R.draw(w, u[r])
+
+
 def test_draws_of_wide_flat_rows_are_exact():
     """400 draws from 50257 nearly equal tokens: one part in 10^7 of error in
     the running sum would move several of them."""
