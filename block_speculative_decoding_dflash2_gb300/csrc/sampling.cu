@@ -39,7 +39,7 @@ constexpr int LOCAL_K = 100;  // largest top-k whose tokens each CTA picks on it
 constexpr int PROBE_K = 16;   // tokens each CTA picks to try for a top-p border
 constexpr int PARTS = 1024;   // room for what they pick
 constexpr int SUB = NT;       // finer bins of a list
-constexpr int SLICE = 19456;  // logits a CTA holds in shared memory, with two CTAs an SM
+constexpr int SLICE_BYTES = 19456 * 4;  // logits a CTA holds in shared memory, with two CTAs an SM
 constexpr unsigned KEY_NINF = 0x007fffffu;  // order of -inf; NaN maps to 0
 
 // Order-preserving map of a logit (a larger one has a larger key; -0 equals 0).
@@ -335,19 +335,21 @@ template <typename T, bool RES>
 struct Slice {
   static constexpr int U = RES ? 1 : 4;  // groups whose loads are in flight
   const T* row;
-  float* zs;
+  T* zs;
   int begin, end, first, groups;
   __device__ __forceinline__ float4 get4(int i) const {
-    if constexpr (RES) return *reinterpret_cast<const float4*>(zs + 4 * i);
+    auto four = [](const uint2& q) {  // of bf16
+      return make_float4(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u), __uint_as_float(q.y << 16),
+                         __uint_as_float(q.y & 0xffff0000u));
+    };
+    if constexpr (RES) {
+      if constexpr (sizeof(T) == 4) return *reinterpret_cast<const float4*>(zs + 4 * i);
+      else return four(*reinterpret_cast<const uint2*>(zs + 4 * i));
+    }
     const int id = first + 4 * i;
     if (id >= begin && id + 4 <= end) {
-      if constexpr (sizeof(T) == 4) {
-        return __ldg(reinterpret_cast<const float4*>(row + id));
-      } else {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(row + id));
-        return make_float4(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u), __uint_as_float(q.y << 16),
-                           __uint_as_float(q.y & 0xffff0000u));
-      }
+      if constexpr (sizeof(T) == 4) return __ldg(reinterpret_cast<const float4*>(row + id));
+      else return four(__ldg(reinterpret_cast<const uint2*>(row + id)));
     }
     float4 v;
     float* e = &v.x;
@@ -540,7 +542,8 @@ __global__ void __launch_bounds__(128) join_kernel(SamplingArgs a) {
 
 template <typename T, bool RES>
 __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice) {
-  extern __shared__ __align__(16) float zs_buf[];
+  extern __shared__ uint4 zs_raw[];
+  T* zs_buf = reinterpret_cast<T*>(zs_raw);
   __shared__ Smem sm;
   pdl_launch_next();
   pdl_wait();
@@ -606,15 +609,16 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
         float e[VEC];
         if (id >= s.begin && id + VEC <= s.end) {
           unpack16<T>(q[u], e);
+          zs_raw[v] = q[u];
         } else {
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) e[j] = id + j >= s.begin && id + j < s.end ? ld(z_row + id + j) : -INFINITY;
+          for (int j = 0; j < VEC; ++j) {
+            e[j] = id + j >= s.begin && id + j < s.end ? ld(z_row + id + j) : -INFINITY;
+            st(zs_buf + v * VEC + j, e[j]);
+          }
         }
 #pragma unroll
         for (int j = 0; j < VEC; ++j) see(e[j]);
-#pragma unroll
-        for (int j = 0; j < VEC; j += 4)
-          *reinterpret_cast<float4*>(zs_buf + v * VEC + j) = make_float4(e[j], e[j + 1], e[j + 2], e[j + 3]);
       }
     }
   } else {
@@ -1347,7 +1351,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     for (int q = tid; q < 4 * s.groups; q += NT) {
       const int id = s.first + q;
       if (id < s.begin || id >= s.end) continue;
-      const float z = RES ? zs_buf[q] : ld(z_row + id);
+      const float z = RES ? ld(zs_buf + q) : ld(z_row + id);
       p[id] = !empty && kept_z(z, id, zc, cut.id) ? mass_f32(z, sc) * inv : 0.f;
     }
     return;
@@ -1521,11 +1525,11 @@ int launch_one(const SamplingArgs& a, int slice, const Ctx& c) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DFLASH2_ERR_CUDA;
   if (RES && !(opted.load(std::memory_order_relaxed) >> dev & 1)) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (SLICE + 16) * 4) != cudaSuccess)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SLICE_BYTES + 64) != cudaSuccess)
       return DFLASH2_ERR_CUDA;
     opted.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  const size_t smem = RES ? (size_t)((slice + 15 + 8) / 8 * 8) * 4 : 0;
+  const size_t smem = RES ? (size_t)((slice + 15 + 8) / 8 * 8) * sizeof(T) : 0;
   return launch_kx(kern, dim3((a.batch * a.rows) << a.lg_cluster), dim3(NT), smem, c, 1 << a.lg_cluster, a, slice);
 }
 
@@ -1538,6 +1542,7 @@ int launch_one(const SamplingArgs& a, int slice, const Ctx& c) {
 template <typename T>
 int launch_rows(SamplingArgs a, const Ctx& c) {
   const long long rows = (long long)a.batch * a.rows;
+  constexpr int SLICE = SLICE_BYTES / (int)sizeof(T);
   a.lg_cluster = 0;
   while (1 << a.lg_cluster < CMAX && (a.vocab > SLICE << a.lg_cluster ||
                                       (rows << a.lg_cluster < c.nsm && a.vocab > 4096 << a.lg_cluster)))
