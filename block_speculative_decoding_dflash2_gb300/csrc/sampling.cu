@@ -13,12 +13,11 @@
 // token (value, id).  T <= 0 keeps the first token alone.  Tokens at -inf or
 // NaN have no mass and are never kept.
 //
-// Masses are whole numbers: e_v in units of 2^-42, from a two-float
-// evaluation good to about 2^-37 of the mass.  Their 64-bit sums are exact
-// and do not depend on the order of the additions, so draws and cuts are
-// deterministic and sit within 2^-37 of the exact ones; in plain fp32 a cut
-// or a draw next to a border falls on the wrong side about once in a
-// thousand rows of a 150k vocabulary.
+// Masses are whole numbers: e_v in units of 2^-42, each good to about 2^-35 of
+// itself.  Their 64-bit sums are exact and do not depend on the order of the
+// additions, so draws and cuts are deterministic and sit within 2^-35 of the
+// exact ones; in plain fp32 a cut or a draw next to a border falls on the wrong
+// side about once in a thousand rows of a 150k vocabulary.
 #include <atomic>
 
 #include "common.cuh"
@@ -52,13 +51,15 @@ __device__ __forceinline__ float okey_value(unsigned k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-// 2^(-j/32) for j = 0..31, in units of 2^-42 and as a float pair (the powers
-// rounded from 50 decimal digits).
-struct ExpTab {
-  u64 fix[32];
-  float2 pair[32];
+// Powers of two for mass_of, rounded from 60 decimal digits: 2^(-j/32) in units
+// of 2^-42, and 2^(-j/1024) as the whole number (1 - 2^(-j/1024)) 2^37 and as a
+// float, for j = 0..31.
+struct ExpConst {
+  u64 pow32[32];
+  unsigned drop[32];
+  float pow1024[32];
 };
-__device__ const ExpTab c_exp = {
+__device__ const ExpConst c_exp = {
     {4398046511104ull, 4303805443529ull, 4211583767698ull, 4121338212211ull, 4033026432885ull,
      3946606992882ull, 3862039343274ull, 3779283804012ull, 3698301545306ull, 3619054569413ull,
      3541505692798ull, 3465618528697ull, 3391357470036ull, 3318687672730ull, 3247575039328ull,
@@ -66,14 +67,21 @@ __device__ const ExpTab c_exp = {
      2851780339397ull, 2790672567345ull, 2730874208839ull, 2672357205845ull, 2615094101559ull,
      2559058027516ull, 2504222690988ull, 2450562362647ull, 2398051864490ull, 2346666558027ull,
      2296382332721ull, 2247175594673ull},
-    {{0x1p+0f, 0x0p+0f}, {0x1.f50766p-1f, -0x1.246ebp-27f}, {0x1.ea4afap-1f, 0x1.52486cp-28f}, {0x1.dfc974p-1f, -0x1.908c94p-26f},
-     {0x1.d5818ep-1f, -0x1.822dbcp-28f}, {0x1.cb720ep-1f, -0x1.8837ccp-28f}, {0x1.c199bep-1f, -0x1.3d56b2p-28f}, {0x1.b7f77p-1f, -0x1.a09438p-26f},
-     {0x1.ae89fap-1f, -0x1.a94b14p-27f}, {0x1.a5503cp-1f, -0x1.b83b54p-26f}, {0x1.9c4918p-1f, 0x1.51f848p-28f}, {0x1.93737cp-1f, -0x1.e64744p-26f},
-     {0x1.8ace54p-1f, 0x1.15506ep-28f}, {0x1.82589ap-1f, -0x1.accc7cp-27f}, {0x1.7a1148p-1f, -0x1.829fdp-26f}, {0x1.71f75ep-1f, 0x1.1d8beep-26f},
-     {0x1.6a09e6p-1f, 0x1.9fcef4p-27f}, {0x1.6247ecp-1f, -0x1.f8b55p-26f}, {0x1.5ab07ep-1f, -0x1.5bd5ecp-28f}, {0x1.5342b6p-1f, -0x1.2c561p-26f},
-     {0x1.4bfdaep-1f, -0x1.593abcp-26f}, {0x1.44e086p-1f, 0x1.8624b4p-31f}, {0x1.3dea64p-1f, 0x1.824684p-26f}, {0x1.371a74p-1f, -0x1.18aac6p-26f},
-     {0x1.306fep-1f, 0x1.4636e2p-26f}, {0x1.29e9ep-1f, -0x1.5c0424p-26f}, {0x1.2387a6p-1f, 0x1.ceac48p-26f}, {0x1.1d4874p-1f, -0x1.d2e8cap-26f},
-     {0x1.172b84p-1f, -0x1.c15742p-28f}, {0x1.11301ep-1f, -0x1.fdb496p-26f}, {0x1.0b5586p-1f, 0x1.9f3122p-26f}, {0x1.059b0ep-1f, -0x1.9d4f52p-26f}}};
+    {0u, 93001160u, 185939388u, 278814728u, 371627222u, 464376912u, 557063841u, 649688051u,
+     742249585u, 834748485u, 927184793u, 1019558553u, 1111869805u, 1204118593u, 1296304959u, 1388428945u,
+     1480490593u, 1572489946u, 1664427045u, 1756301933u, 1848114652u, 1939865243u, 2031553750u, 2123180213u,
+     2214744675u, 2306247178u, 2397687764u, 2489066475u, 2580383352u, 2671638437u, 2762831773u, 2853963400u},
+    {0x1p+0f, 0x1.ffa74ep-1f, 0x1.ff4eacp-1f, 0x1.fef61ap-1f, 0x1.fe9d96p-1f, 0x1.fe4522p-1f,
+     0x1.fdecbep-1f, 0x1.fd9468p-1f, 0x1.fd3c22p-1f, 0x1.fce3ecp-1f, 0x1.fc8bc4p-1f, 0x1.fc33acp-1f,
+     0x1.fbdba4p-1f, 0x1.fb83aap-1f, 0x1.fb2bcp-1f, 0x1.fad3e4p-1f, 0x1.fa7c18p-1f, 0x1.fa245cp-1f,
+     0x1.f9ccaep-1f, 0x1.f9751p-1f, 0x1.f91d8p-1f, 0x1.f8c6p-1f, 0x1.f86e9p-1f, 0x1.f8172ep-1f,
+     0x1.f7bfdap-1f, 0x1.f76898p-1f, 0x1.f71164p-1f, 0x1.f6ba3ep-1f, 0x1.f66328p-1f, 0x1.f60c2p-1f,
+     0x1.f5b528p-1f, 0x1.f55e4p-1f}};
+constexpr float FAR = 18.f;  // where the tables end
+struct ExpTab {  // in shared memory
+  u64 pow32[(int)FAR * 32 + 1];  // 2^(-k/32) in units of 2^-42
+  uint2 pow1024[32];             // c_exp's drop, and its pow1024 as bits
+};
 
 // The row's exponent scale log2(e) / T as a float pair.
 struct Scale {
@@ -88,10 +96,10 @@ __device__ __forceinline__ float2 pair_of(double x) {
 
 // exp((z - zmax) / T) in units of 2^-42, for z > -inf.  From y = (zmax - z)
 // log2(e) / T = 18 on, plain fp32 is good to 2^-37 of the largest mass.  Before,
-// y is held as p + e (the difference exact by two-sum, the product by fma), y =
-// n + j/32 + g + e with |g| <= 1/64, and 2^-(g+e) = 1 - w + w^2/2 - ... with w =
-// (g + e) ln 2, whose linear term keeps its rounding error.
-constexpr float FAR = 18.f;
+// y is held as p + e (the difference exact by two-sum, the product by fma) and
+// cut into k/1024 + g + e with |g| <= 2^-11: 2^(-k/1024) is a product of two
+// table entries in whole numbers, and the rest, 1 - 2^-(g+e) = w - w^2/2 with w =
+// (g + e) ln 2 below 2^-11, is good to 2^-24 of itself in fp32: 2^-35 of the mass.
 __device__ __forceinline__ float y_of(float z, const Scale& s) {
   return __fmul_rn(s.zmax - z, s.hi);  // never contracted: its rounding error is formed below
 }
@@ -100,34 +108,35 @@ __device__ __forceinline__ unsigned far_mass(float y) {  // 0 from y = 44 on, in
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(42.f - y));
   return __float2uint_rn(f);
 }
-// No branch depends on one value, so the N evaluations overlap.
-template <int N>
+// No branch depends on one value, so the N evaluations overlap; with VOTE, a
+// warp without far values skips their form (same results).
+template <int N, bool VOTE>
 __device__ __forceinline__ void masses_of(const float (&z)[N], const float (&p)[N], const Scale& s, const ExpTab& tab,
                                           u64 (&v)[N]) {
-  const float L1 = 0.693147182464599609f, L1lo = -1.90465429995776e-9f;  // ln 2
+  bool far = false;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const float dh = s.zmax - z[i], bb = dh - s.zmax;
     const float dl = (s.zmax - (dh - bb)) - (z[i] + bb);
     const float e = fmaf(dl, s.hi, fmaf(dh, s.lo, fmaf(dh, s.hi, -p[i])));
-    const float kf = fmaf(p[i], 32.f, 12582912.f);  // 1.5 2^23: rounds to a whole number of 32nds
-    const unsigned k = __float_as_uint(kf);
-    const float g = fmaf(kf - 12582912.f, -0.03125f, p[i]);
-    const float gl = __fmul_rn(g, L1);
-    const float glr = fmaf(g, L1lo, fmaf(e, L1, fmaf(g, L1, -gl)));
-    const float w = (g + e) * L1;
-    const float q = w * w * fmaf(w, fmaf(w, 0.0416666667f, -0.1666666667f), 0.5f) - glr;  // 2^-(g+e) - 1 + gl
-    const float2 t = tab.pair[k & 31];
-    const float m = __fmul_rn(t.x, gl);
-    const float small = fmaf(t.x, q, -fmaf(t.x, gl, -m)) - t.y * gl;
-    u64 near = tab.fix[k & 31];
-    asm("mad.wide.s32 %0, %1, -64, %0;" : "+l"(near) : "r"(__float2int_rn(m * 68719476736.f)));
-    asm("mad.wide.s32 %0, %1, 1, %0;" : "+l"(near) : "r"(__float2int_rn(small * 4398046511104.f)));
-    const unsigned n = (k >> 5) & 31;  // 0..18
-    near += (1u << n) >> 1;
-    const unsigned lo = __funnelshift_r((unsigned)near, (unsigned)(near >> 32), n), hi = (unsigned)(near >> 32) >> n;
-    const bool is_near = p[i] < FAR;
-    v[i] = is_near ? ((u64)hi << 32 | lo) : (u64)far_mass(p[i]);
+    // 1.5 2^23: rounds to a whole number of 1024ths (of far values only kept within the tables)
+    const float kf = fmaf(fminf(p[i], FAR), 1024.f, 12582912.f);
+    const unsigned k = __float_as_uint(kf) - 0x4b400000u;
+    const float w = (fmaf(kf - 12582912.f, -0x1p-10f, p[i]) + e) * 0.693147182f;
+    const float x = fmaf(-0.5f * w, w, w);
+    const u64 a = tab.pow32[k >> 5];
+    const uint2 t = tab.pow1024[k & 31];
+    const unsigned a11 = (unsigned)((a + 1024) >> 11);
+    u64 b = a - ((u64)a11 * t.x >> 26);  // 2^(-k/1024)
+    const float bf = (float)a11 * __uint_as_float(t.y);  // the same in units of 2^-31
+    asm("mad.wide.s32 %0, %1, -1, %0;" : "+l"(b) : "r"(__float2int_rn(bf * x * 2048.f)));
+    v[i] = b;
+    far = far || !(p[i] < FAR);
+  }
+  if (!VOTE || __any_sync(0xffffffffu, far)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (!(p[i] < FAR)) v[i] = far_mass(p[i]);
   }
   // (a difference or a product without a value: an infinite maximum, T = infinity)
   if (s.odd) {
@@ -139,7 +148,7 @@ __device__ __forceinline__ void masses_of(const float (&z)[N], const float (&p)[
 __device__ __forceinline__ u64 mass_of(float z, const Scale& s, const ExpTab& tab) {
   const float x[1] = {z}, y[1] = {y_of(z, s)};
   u64 v[1];
-  masses_of<1>(x, y, s, tab, v);
+  masses_of<1, false>(x, y, s, tab, v);
   return v[0];
 }
 
@@ -236,7 +245,7 @@ __device__ __forceinline__ bool masses4(const float4& v, int id, const Scale& s,
     for (int j = 0; j < 4; ++j) e[j] = keep[j] ? far_mass(y[j]) : 0u;
     return false;
   }
-  masses_of<4>(z, y, s, tab, e);
+  masses_of<4, true>(z, y, s, tab, e);
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if (!keep[j]) e[j] = 0;
@@ -556,9 +565,8 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     if (i > nd) return;  // the whole cluster
   }
   cluster_arrive();  // waited for before the first access to another CTA's memory
-  static_assert(sizeof(ExpTab) / 4 <= NT, "one word of the table a thread");
-  const bool has_word = tid < (int)(sizeof(ExpTab) / 4);
-  const unsigned word = has_word ? reinterpret_cast<const unsigned*>(&c_exp)[tid] : 0u;
+  const u64 pow32 = c_exp.pow32[lane];
+  const uint2 pow1024 = make_uint2(c_exp.drop[lane], __float_as_uint(c_exp.pow1024[lane]));
   const T* z_row = static_cast<const T*>(a.logits) + (size_t)row * a.stride;
   const float temp = a.temperature ? a.temperature[seq] : 1.f;
   const int top_k = a.top_k ? a.top_k[seq] : 0;
@@ -625,7 +633,9 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     for_each(s, [&](float z, int) { see(z); });
   }
   for (int b = tid; b < NB; b += NT) sm.hist[b] = 0;
-  if (has_word) reinterpret_cast<unsigned*>(&sm.tab)[tid] = word;
+  for (int n = warp; n <= (int)FAR; n += NW)
+    if (n < (int)FAR || lane == 0) sm.tab.pow32[n * 32 + lane] = n ? (pow32 + (1ull << (n - 1))) >> n : pow32;
+  if (warp == 0) sm.tab.pow1024[lane] = pow1024;
   if (tid == 0) {
     sm.ncand = sm.nlocal = 0;
     sm.pick = -1;
