@@ -276,6 +276,7 @@ struct Smem {
     };
   };
   u64 wsum[NW], wsum2[NW];
+  u64 wkept[NW];  // mass each warp's slice keeps of the bins that hold the top-p border
   u64 xm[2][CMAX], xg[2][CMAX];  // exchanged masses, two turns
   float xmax[CMAX], xmin[CMAX], xlow[CMAX];
   float2 xest[CMAX];
@@ -342,7 +343,7 @@ __device__ __noinline__ void sort_desc(u64* a, int n) {
 // outside the slice reads as -inf.
 template <typename T, bool RES>
 struct Slice {
-  static constexpr int U = RES ? 1 : 4;  // groups whose loads are in flight
+  static constexpr int U = 4;  // groups whose loads are in flight
   const T* row;
   T* zs;
   int begin, end, first, groups;
@@ -406,36 +407,41 @@ __device__ __forceinline__ void for_each(const S& s, F f) {
   for_each4(s, [&](const float4& v, int id) { f(v.x, id), f(v.y, id + 1), f(v.z, id + 2), f(v.w, id + 3); });
 }
 
-// Appends the logits for which in(z) holds, all of them in [low, high], to this
-// CTA's list of room `most`, counted in `counter`.
+// A warp appends the tokens of its groups of four (ids id .. id + 3) that are
+// marked to this CTA's list of room `most`, counted in `counter`.
+__device__ __forceinline__ void append4(const float (&z)[4], const bool (&yes)[4], int id, unsigned* counter, u64* list,
+                                        unsigned most) {
+  const int lane = threadIdx.x & 31;
+  unsigned m[4], n = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    m[j] = __ballot_sync(0xffffffffu, yes[j]);
+    n += __popc(m[j]);
+  }
+  if (!n) return;
+  unsigned at = 0;
+  if (lane == 0) at = atomicAdd(counter, n);
+  at = __shfl_sync(0xffffffffu, at, 0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const unsigned pos = at + __popc(m[j] & ((1u << lane) - 1));
+    if (yes[j] && pos < most) list[pos] = ((u64)okey(z[j]) << 32) | (unsigned)~(id + j);
+    at += __popc(m[j]);
+  }
+}
+// The same for the slice's logits for which in(z) holds, all of them in [low, high].
 template <typename S, typename F>
 __device__ __forceinline__ void collect(const S& s, float low, float high, F in, unsigned* counter, u64* list,
                                         unsigned most) {
-  const int lane = threadIdx.x & 31;
   for_each4(s, [&](const float4& v, int id) {
-    const float zz[4] = {v.x, v.y, v.z, v.w};
-    bool any = false;
+    const float z[4] = {v.x, v.y, v.z, v.w};
+    bool yes[4], any = false;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) any = any || (zz[j] >= low && zz[j] <= high);
+    for (int j = 0; j < 4; ++j) any = any || (z[j] >= low && z[j] <= high);
     if (!__any_sync(0xffffffffu, any)) return;
-    unsigned m[4], n = 0, mine = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool yes = zz[j] >= low && zz[j] <= high && zz[j] > -INFINITY && in(zz[j]);
-      m[j] = __ballot_sync(0xffffffffu, yes);
-      n += __popc(m[j]);
-      mine |= (unsigned)yes << j;
-    }
-    if (!n) return;
-    unsigned at = 0;
-    if (lane == 0) at = atomicAdd(counter, n);
-    at = __shfl_sync(0xffffffffu, at, 0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const unsigned pos = at + __popc(m[j] & ((1u << lane) - 1));
-      if ((mine >> j & 1) && pos < most) list[pos] = ((u64)okey(zz[j]) << 32) | (unsigned)~(id + j);
-      at += __popc(m[j]);
-    }
+    for (int j = 0; j < 4; ++j) yes[j] = z[j] >= low && z[j] <= high && z[j] > -INFINITY && in(z[j]);
+    append4(z, yes, id, counter, list, most);
   });
 }
 
@@ -763,6 +769,21 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
   u64 lkey = 0, lmass = 0, lcum = 0;
   int lrank = 0, lanes = 1;
 
+  // Each warp's range of the slice's groups, and the warp (of the cluster) that
+  // has a token.
+  const int g0 = (int)((long long)s.groups * warp / NW), g1 = (int)((long long)s.groups * (warp + 1) / NW);
+  auto group4 = [&](int q) {
+    return q < g1 ? s.get4(q) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+  };
+  auto warp_of = [&](int id) {
+    const int r = id / slice, begin = r * slice;
+    const int first = begin - (int)((reinterpret_cast<uintptr_t>(z_row + begin) / sizeof(T)) % VEC);
+    const int groups = (min(V, begin + slice) - first + VEC - 1) / VEC * (VEC / 4);
+    return r * NW + (((id - first) / 4 + 1) * NW - 1) / groups;
+  };
+  bool by_warp = false;  // known: the mass each warp keeps, g_warp + sm.wkept[warp]
+  u64 g_warp = 0;
+
   // Broadcasts the first CTA's sm.mk.  (Two turns: a CTA that still reads one
   // decision is at least a cluster barrier ahead of the next but one.)
   int told = 0;
@@ -1072,6 +1093,16 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
       }
     }
     Decision dec = broadcast();
+    // Copies this CTA's own list behind one reservation in the first CTA's.
+    auto deliver = [&]() {
+      __syncthreads();
+      const unsigned n = min(sm.nlocal, (unsigned)CAP);
+      if (tid == 0) sm.sel_key = add_cl(dsmem_addr(&sm.ncand, 0), n);
+      __syncthreads();
+      const unsigned at = sm.sel_key;
+      for (unsigned e = tid; e < n; e += NT)
+        if (at + e < CAP) st_cl(dsmem_addr(sm.cand + at + e, 0), sm.cand[e]);
+    };
     // Gathers the tokens of the decision's bins into the first CTA's list.
     auto gather = [&](int lo, int hi) {
       // (bounds beyond the bins' ends, roundings included, skip most)
@@ -1080,18 +1111,31 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
       auto in = [&](float z) { const int b = bin_of(z); return b >= lo && b <= hi; };
       if (rank == 0) {
         collect(s, low, high, in, &sm.ncand, sm.cand, CAP);
-      } else {  // to a list of its own, copied behind one reservation in the first CTA's
+      } else {
         if (tid == 0) sm.nlocal = 0;
         __syncthreads();
         collect(s, low, high, in, &sm.nlocal, sm.cand, CAP);
-        __syncthreads();
-        const unsigned n = min(sm.nlocal, (unsigned)CAP);
-        if (tid == 0) sm.sel_key = add_cl(dsmem_addr(&sm.ncand, 0), n);
-        __syncthreads();
-        const unsigned at = sm.sel_key;
-        for (unsigned e = tid; e < n; e += NT)
-          if (at + e < CAP) st_cl(dsmem_addr(sm.cand + at + e, 0), sm.cand[e]);
+        deliver();
       }
+    };
+    // The smallest logit in a bin ahead of bin b > 0 (bins fall as logits rise):
+    // a search over the keys, 32 at a time, from a bracket around the bin's end.
+    auto bin_end = [&](int b) {
+      const float d = (float)b / per;
+      unsigned lo = KEY_NINF + 1, hi = okey(zmax);
+      const unsigned k0 = okey(zmax - d * 1.0001f), k1 = okey(zmax - d * 0.9999f);
+      if (k0 > lo && k0 <= hi && bin_of(okey_value(k0)) >= b) lo = k0;
+      if (k1 < hi && k1 >= lo && bin_of(okey_value(k1)) < b) hi = k1;
+      while (lo < hi) {
+        const unsigned step = (hi - lo + 31) >> 5, k = lo + min(step * lane, hi - lo);
+        const unsigned yes = __ballot_sync(0xffffffffu, bin_of(okey_value(k)) < b);
+        const int f = yes ? __ffs(yes) - 1 : 32;
+        const unsigned last = __shfl_sync(0xffffffffu, k, max(f - 1, 0));
+        const unsigned first = __shfl_sync(0xffffffffu, k, f & 31);
+        if (f < 32) hi = first;
+        if (f > 0) lo = last + 1;
+      }
+      return okey_value(hi);
     };
 
     if (dec.step == STEP_LIST) {
@@ -1184,19 +1228,36 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
           }
           dec = broadcast();
           const int lo = dec.lo, hi = dec.hi;
-          u64 m = 0, g = 0;  // kept mass, and what of it lies ahead of the gathered bins
+          // One pass: the kept mass, what of it lies ahead of the decision's bins
+          // (by warp too, each a contiguous range of groups, for the draw), and
+          // those bins' tokens into the first CTA's list.
+          u64 m = 0, g = 0;
+          const bool take = dec.step == STEP_TOPP;
+          const float ahead = lo ? bin_end(lo) : NAN;
+          const float least = !take ? NAN : hi == NB - 1 ? -3.402823466e+38f : bin_end(hi + 1);
+          unsigned* counter = rank ? &sm.nlocal : &sm.ncand;
+          if (tid == 0) sm.nlocal = 0;
+          __syncthreads();
           const CutZ cz = cut_z(cut, V);
-          for_each4(s, [&](const float4& v, int id) {
+          for (int q0 = g0; q0 < g1; q0 += 32) {
+            const float4 v = group4(q0 + lane);
+            const float z[4] = {v.x, v.y, v.z, v.w};
+            const int id = s.first + 4 * (q0 + lane);
             u64 e[4];
             masses4(v, id, sc, sm.tab, cz, -1, e);
-            const float z[4] = {v.x, v.y, v.z, v.w};
+            bool in[4], any = false;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
+              const bool before = z[j] >= ahead;
               m += e[j];
-              g += bin_of(z[j]) < lo ? e[j] : 0ull;
+              g += before ? e[j] : 0ull;
+              in[j] = !before && z[j] >= least;
+              any = any || in[j];
             }
-          });
-          if (dec.step == STEP_TOPP) gather(lo, hi);
+            if (__any_sync(0xffffffffu, any)) append4(z, in, id, counter, sm.cand, CAP);
+          }
+          g_warp = warp_sum_u64(g);
+          if (take && rank) deliver();
           exchange(m, g);
           if (rank == 0) {
             const u64 want = share_of(top_p, m);
@@ -1206,6 +1267,9 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
               int n_list = n;
               small = n <= SMALL;
               u64 ga = g;  // mass ahead of the part of the list that is ranked
+              u64 v[CAP / NT];
+#pragma unroll
+              for (int j = 0; j < CAP / NT; ++j) v[j] = tid + j * NT < n ? sm.cand[tid + j * NT] : 0ull;
               if (small) {
                 rank_list(n);
                 tell(0, lrank > 0 && lrank == n, 0);
@@ -1213,14 +1277,11 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
               } else if (lo > 0) {
                 // finer bins find the border's few tokens; the rest is not needed
                 const float top = zmax - (float)lo / per, fine = (float)SUB / ((float)(hi + 1 - lo) / per);
-                u64 v[CAP / NT];
                 int sb[CAP / NT];
                 sm.sub_lo[tid] = sm.sub_hi[tid] = 0;
                 __syncthreads();
 #pragma unroll
                 for (int j = 0; j < CAP / NT; ++j) {
-                  const int e = tid + j * NT;
-                  v[j] = e < n ? sm.cand[e] : 0ull;
                   const float z = okey_value((unsigned)(v[j] >> 32));
                   sb[j] = (int)fminf(fmaxf((top - z) * fine, 0.f), (float)(SUB - 1));
                   if (v[j]) {  // (below 2^42 each, as the largest logit's bin is not here: no sum of 2048 overflows)
@@ -1277,6 +1338,26 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
                   n_kept = p + 1;
                 }
                 if (tid == 0) sm.mk.cut = cut;
+                if (lo > 0 && a.kind != SAMPLING_PROBS) {
+                  // what each warp of the cluster keeps of these bins
+                  __syncthreads();
+                  if (tid < CMAX * NW) sm.sub_lo[tid] = sm.sub_hi[tid] = 0;
+                  __syncthreads();
+#pragma unroll
+                  for (int j = 0; j < CAP / NT; ++j) {
+                    const unsigned key = (unsigned)(v[j] >> 32);
+                    const int id = (int)~(unsigned)v[j];
+                    if (v[j] && kept(key, id, cut)) {
+                      const int w = warp_of(id);
+                      const u64 e = mass_of(okey_value(key), sc, sm.tab);  // (below 2^42, as above)
+                      atomicAdd(&sm.sub_lo[w], (unsigned)e & 0x1fffffu);
+                      atomicAdd(&sm.sub_hi[w], (unsigned)(e >> 21));
+                    }
+                  }
+                  __syncthreads();
+                  if (tid < C * NW)
+                    st_cl(dsmem_addr(&sm.wkept[tid % NW], tid / NW), ((u64)sm.sub_hi[tid] << 21) + sm.sub_lo[tid]);
+                }
               } else {
                 const bool later = want > g;
                 const u64 at = later ? g + lall : g;
@@ -1305,6 +1386,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
         cut = dec.cut;
         total = ((u64)dec.total_hi << 32) | dec.total_lo;
         list = dec.step == STEP_LIST;
+        by_warp = total > 0;
       }
     }
     }
@@ -1337,6 +1419,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     if (mk > cut.key) {
       cut = {mk, V};
       total = 0;
+      by_warp = false;
     }
   }
 
@@ -1462,20 +1545,21 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     if (warp == 0) finish(pass ? -1 : sm.pick, pass);
     return;
   }
-  // no list: masses by warp, each a contiguous range of the slice's groups
-  const int g0 = (int)((long long)s.groups * warp / NW), g1 = (int)((long long)s.groups * (warp + 1) / NW);
+  // no list: masses by warp
   const CutZ cz = cut_z(cut, V);
-  auto mass4 = [&](int q, u64 (&e)[4]) {
-    const float4 v = q < g1 ? s.get4(q) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-    masses4(v, s.first + 4 * q, sc, sm.tab, cz, x, e);
-  };
+  auto mass4 = [&](int q, u64 (&e)[4]) { masses4(group4(q), s.first + 4 * q, sc, sm.tab, cz, x, e); };
   u64 wm = 0;
-  for (int q0 = g0; q0 < g1; q0 += 32) {
-    u64 e[4];
-    mass4(q0 + lane, e);
-    wm += e[0] + e[1] + e[2] + e[3];
+  if (by_warp) {
+    wm = g_warp + sm.wkept[warp];
+    if (x_mass && x >= s.begin && x < s.end && warp_of(x) == rank * NW + warp) wm -= x_mass;
+  } else {
+    for (int q0 = g0; q0 < g1; q0 += 32) {
+      u64 e[4];
+      mass4(q0 + lane, e);
+      wm += e[0] + e[1] + e[2] + e[3];
+    }
+    wm = warp_sum_u64(wm);
   }
-  wm = warp_sum_u64(wm);
   __syncthreads();
   if (lane == 0) sm.wsum[warp] = wm;
   __syncthreads();
