@@ -11,12 +11,13 @@
 // than bf16 has.)
 //
 // Warp roles (one CTA an SM):
-//   warp 0       TMA producer (one lane): codes and activations -> ring
-//   warp 1       MMA issuer (one lane) and TMEM owner
+//   warp 0       TMA producer of codes (one lane)
+//   warp 1       MMA issuer (one lane) of even chunks, and TMEM owner
 //   then         epilogue: a set of four warps for every 32 columns
-//   last 8       converters, in two groups of four on alternate chunks:
+//   then 8       converters, in two groups of four on alternate chunks:
 //                thread = weight row, its 64 bytes of codes -> 128 bf16 values
 //                in 64 columns of its TMEM lane
+//   last 2       MMA issuer of odd chunks; TMA producer of activations
 // Operand A in TMEM because shared memory bounds the alternative: reading both
 // operands of a 128 x 128 product takes all of its 128 bytes a cycle, and
 // writing the converted tile as much again as a copy of the activations.
@@ -28,6 +29,7 @@
 // own copies and products, frees TMEM and returns.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -51,14 +53,15 @@ constexpr uint32_t TMEM_COLS = 512;
 template <int BN>
 struct Cfg {
   static constexpr int Q_BYTES = BM * BK / 2 * QC, B_BYTES = BN * BK * 2;
-  static constexpr int S = 4, QS = BN == 128 ? 5 : 6;
-  static constexpr int ACC = BN == 128 ? 2 : 4;  // accumulators
+  static constexpr int S = 4, SB = BN == 128 ? 4 : 8, QS = 6;
+  static constexpr int ACC = 256 / BN;           // accumulators
   static constexpr int COLS = 32;                // columns of an epilogue thread
-  static constexpr int EPI_THREADS = BN / COLS * 128, THREADS = 64 + EPI_THREADS + CONV_THREADS;
-  static constexpr int SMEM = QS * Q_BYTES + S * B_BYTES + 2048;
+  static constexpr int EPI_THREADS = BN / COLS * 128, THREADS = 128 + EPI_THREADS + CONV_THREADS;
+  static constexpr int SMEM = QS * Q_BYTES + SB * B_BYTES + 2048;
   static_assert(SMEM <= SMEM_BUDGET + 2048, "shared memory");
+  static_assert(S % 2 == 0 && SB % 2 == 0, "half of each to either issuer");
   static_assert(ACC * BN + S * A_COLS <= (int)TMEM_COLS, "TMEM");
-  static_assert(S * B_BYTES >= BM * BN * 4, "the ring holds a partial tile");
+  static_assert(SB * B_BYTES >= BM * BN * 4, "the ring holds a partial tile");
 };
 
 struct Args {
@@ -93,6 +96,15 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&v)[W]) {
         : "r"(addr));
   }
   tmem_ld_wait();
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -144,16 +156,19 @@ template <int BN, int G, typename OutT>
 __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
     linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmX, Args a) {
   using C = Cfg<BN>;
-  constexpr int S = C::S, QS = C::QS, ACC = C::ACC, EPI_THREADS = C::EPI_THREADS, THREADS = C::THREADS;
+  constexpr int S = C::S, SB = C::SB, QS = C::QS, ACC = C::ACC, EPI_THREADS = C::EPI_THREADS, THREADS = C::THREADS;
+  constexpr int SP = S / 2, BP = SB / 2;  // of either issuer
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stB = smem;
-  uint8_t* stQ = stB + S * C::B_BYTES;
+  uint8_t* stQ = stB + SB * C::B_BYTES;
   uint64_t* q_full = reinterpret_cast<uint64_t*>(stQ + QS * C::Q_BYTES);  // a block of codes has landed
   uint64_t* q_empty = q_full + QS;
-  uint64_t* full = q_empty + QS;  // a chunk's activations have landed and its codes are converted
+  uint64_t* full = q_empty + QS;  // a chunk's codes are converted
   uint64_t* empty = full + S;
-  uint64_t* acc_full = empty + S;
+  uint64_t* b_full = empty + S;  // a chunk's activations have landed
+  uint64_t* b_empty = b_full + SB;
+  uint64_t* acc_full = b_empty + SB;
   uint64_t* acc_empty = acc_full + ACC;
   uint64_t* drain = acc_empty + ACC;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);  // then the abort flag, in one 8-byte word
@@ -165,17 +180,21 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < QS; ++s) {
       mbar_init(q_full + s, 1);
-      mbar_init(q_empty + s, CONV_THREADS);
+      mbar_init(q_empty + s, CONV_THREADS / 32);
     }
     for (int s = 0; s < S; ++s) {
-      mbar_init(full + s, 1 + CONV_GROUP);
+      mbar_init(full + s, CONV_GROUP / 32);
       mbar_init(empty + s, 1);
+    }
+    for (int s = 0; s < SB; ++s) {
+      mbar_init(b_full + s, 1);
+      mbar_init(b_empty + s, 1);
     }
     for (int i = 0; i < ACC; ++i) {
       mbar_init(acc_full + i, 1);
-      mbar_init(acc_empty + i, EPI_THREADS);
+      mbar_init(acc_empty + i, EPI_THREADS / 32);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, 2);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmQ);
@@ -196,80 +215,36 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
   float* part = reinterpret_cast<float*>(smem);  // [BN][BM], in the idle ring
 
   const int nb = (c1 - c0 + QC - 1) / QC;  // blocks of codes of a tile
-  if (warp == 0) {
-    // (as the MMA warp: all lanes walk, one issues)
-    const bool leader = elect_one();
-    const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
-    // The codes run ahead of the activations by QS - 1 blocks.
-    int qs = 0, qb = 0, qt = first;  // next block's ring slot, its number in its tile, and its tile
-    int s = 0, issued = 0, loaded = 0;
-    uint32_t q_phase = 0, phase = 0;
-    bool ok = true;
-    auto load_block = [&]() {
-      if (!__all_sync(0xffffffffu, wait_for(q_empty + qs, q_phase ^ 1u, abort_flag))) return false;
-      if (leader) {
-        mbar_arrive_expect_tx(q_full + qs, C::Q_BYTES);
-        // (codes as pairs of bytes: 64 of them are 256 inputs)
-        tma_load_2d(stQ + qs * C::Q_BYTES, &tmQ, q_full + qs, (c0 / QC + qb) * (QC * BK / 4), qt / a.n_tiles * BM, pol_w);
-      }
-      if (loaded < QS) ++loaded;
-      if (++qs == QS) {
-        qs = 0;
-        q_phase ^= 1u;
-      }
-      if (++qb == nb) {
-        qb = 0;
-        qt += step;
-      }
-      return true;
-    };
-    if (nb > 0)
-      for (int i = 0; ok && i < QS - 1 && qt < a.tiles; ++i) ok = load_block();
-    for (int t = first; ok && t < a.tiles; t += step) {
-      const int nt = t % a.n_tiles;
-      for (int c = c0; c < c1; ++c) {
-        if ((c - c0) % QC == 0 && qt < a.tiles) {
-          ok = load_block();
-          if (!ok) break;
-        }
-        ok = __all_sync(0xffffffffu, wait_for(empty + s, phase ^ 1u, abort_flag));
-        if (!ok) break;
-        if (leader) {
-          mbar_arrive_expect_tx(full + s, C::B_BYTES);
-          // (two halves of 64 inputs, each in the 128-byte swizzle)
-          tma_load_2d(stB + s * C::B_BYTES, &tmX, full + s, c * BK, nt * BN, pol_x);
-          tma_load_2d(stB + s * C::B_BYTES + C::B_BYTES / 2, &tmX, full + s, c * BK + 64, nt * BN, pol_x);
-        }
-        issued = 1;
-        if (++s == S) {
-          s = 0;
-          phase ^= 1u;
-        }
-      }
-    }
-    if (!ok) *abort_flag = 1;
-    if (*abort_flag && (issued || loaded)) {
-      // Copies of this warp may be in flight, on barriers that also count
-      // converters which may have left: a millisecond, some hundred times what
-      // a copy takes, stands for waiting on them.
-      for (const uint64_t t = globaltimer(); globaltimer() - t < 1000000;) {}
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // The whole warp walks the chunks, so that descriptors stay in uniform
+  auto issue = [&](auto parity) {
+    // The whole warp walks its chunks, so that descriptors stay in uniform
     // registers; one lane issues.
+    constexpr int p = decltype(parity)::value;
     const bool leader = elect_one();
     constexpr uint32_t idesc = idesc_bf16_f32(BM, BN);
-    int stage = 0, buf = 0;
-    uint32_t phase = 0, acc_phase = 0;
+    int stage = p * SP, slot = p * BP, buf = 0;
+    uint32_t phase = 0, b_phase = 0, acc_phase = 0;
     bool ok = true;
     for (int t = first; ok && t < a.tiles; t += step) {
       for (int c = c0; c < c1; ++c) {
-        ok = __all_sync(0xffffffffu, wait_for(full + stage, phase, abort_flag));
+        if (((c - c0) & 1) != p) {
+          // The other's chunk.  Its accumulators' phases are waited for as well:
+          // a parity could not tell two phases from none.
+          for (int i = 0; ok && i < BK / G; ++i) {
+            ok = __all_sync(0xffffffffu, wait_for(acc_empty + buf, acc_phase ^ 1u, abort_flag));
+            if (++buf == ACC) {
+              buf = 0;
+              acc_phase ^= 1u;
+            }
+          }
+          if (!ok) break;
+          continue;
+        }
+        const bool landed = wait_for(b_full + slot, b_phase, abort_flag);
+        ok = __all_sync(0xffffffffu, landed && wait_for(full + stage, phase, abort_flag));
         if (!ok) break;
         tc_fence_after();
         const uint32_t at = tmem_a + (uint32_t)(stage * A_COLS);
-        const uint64_t bd = sdesc_sw128(smem_u32(stB + stage * C::B_BYTES));
+        const uint64_t bd = sdesc_sw128(smem_u32(stB + slot * C::B_BYTES));
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk) {
           const bool begin = kk % (G / 16) == 0, end = kk % (G / 16) == G / 16 - 1;
@@ -289,10 +264,17 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
           }
         }
         if (!ok) break;
-        if (leader) umma_commit(empty + stage);
-        if (++stage == S) {
-          stage = 0;
+        if (leader) {
+          umma_commit(empty + stage);
+          umma_commit(b_empty + slot);
+        }
+        if (++stage == (p + 1) * SP) {
+          stage = p * SP;
           phase ^= 1u;
+        }
+        if (++slot == (p + 1) * BP) {
+          slot = p * BP;
+          b_phase ^= 1u;
         }
       }
     }
@@ -303,14 +285,78 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
       wait_for(drain, 0, &never);
     }
     __syncwarp();
+  };
+  // A producer that gives up, or that others' giving up stopped, stays until its
+  // copies have landed: a millisecond, some hundred times what a copy takes,
+  // stands for waiting on each.
+  auto settle = [&](bool ok, bool issued) {
+    if (!ok) *abort_flag = 1;
+    if (*abort_flag && issued)
+      for (const uint64_t t = globaltimer(); globaltimer() - t < 1000000;) {}
+    __syncwarp();
+  };
+  if (warp == 0) {
+    // codes (as the MMA warps: all lanes walk, one issues)
+    const bool leader = elect_one();
+    const uint64_t policy = policy_evict_first();
+    int s = 0;
+    uint32_t phase = 0;
+    bool ok = true, issued = false;
+    for (int t = first; ok && t < a.tiles; t += step)
+      for (int b = 0; b < nb; ++b) {
+        ok = __all_sync(0xffffffffu, wait_for(q_empty + s, phase ^ 1u, abort_flag));
+        if (!ok) break;
+        if (leader) {
+          mbar_arrive_expect_tx(q_full + s, C::Q_BYTES);
+          // (codes as pairs of bytes: 64 of them are 256 inputs)
+          tma_load_2d(stQ + s * C::Q_BYTES, &tmQ, q_full + s, (c0 / QC + b) * (QC * BK / 4), t / a.n_tiles * BM, policy);
+        }
+        issued = true;
+        if (++s == QS) {
+          s = 0;
+          phase ^= 1u;
+        }
+      }
+    settle(ok, issued);
+  } else if (warp == THREADS / 32 - 1) {
+    // activations
+    const bool leader = elect_one();
+    const uint64_t policy = policy_evict_last();
+    uint32_t j[2] = {0, 0};  // chunks of either parity so far
+    bool ok = true, issued = false;
+    for (int t = first; ok && t < a.tiles; t += step) {
+      const int nt = t % a.n_tiles;
+      for (int b = 0; ok && b < nb; ++b) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int c = c0 + 2 * b + p, s = p * BP + j[p] % BP;
+          if (!ok || c >= c1) break;
+          ok = __all_sync(0xffffffffu, wait_for(b_empty + s, (j[p] / BP & 1u) ^ 1u, abort_flag));
+          if (!ok) break;
+          if (leader) {
+            mbar_arrive_expect_tx(b_full + s, C::B_BYTES);
+            // (two halves of 64 inputs, each in the 128-byte swizzle)
+            tma_load_2d(stB + s * C::B_BYTES, &tmX, b_full + s, c * BK, nt * BN, policy);
+            tma_load_2d(stB + s * C::B_BYTES + C::B_BYTES / 2, &tmX, b_full + s, c * BK + 64, nt * BN, policy);
+          }
+          issued = true;
+          ++j[p];
+        }
+      }
+    }
+    settle(ok, issued);
+  } else if (warp == 1) {
+    issue(std::integral_constant<int, 0>());
+  } else if (warp == THREADS / 32 - 2) {
+    issue(std::integral_constant<int, 1>());
   } else if (warp >= 2 + EPI_THREADS / 32) {
     // converters: group cg takes chunk cg of every block; the codes lie in the
     // 128-byte swizzle (piece i of row r at i ^ (r & 7))
     const int cw = warp - 2 - EPI_THREADS / 32, cg = cw / 4, q = warp & 3, r = q * 32 + lane;
     int qs = 0;
-    uint32_t q_phase = 0, chunk0 = 0;  // (chunks of the tiles so far: only the last bits are used)
+    uint32_t q_phase = 0, j = 0;  // j: chunks of this group so far
     bool ok = true;
-    for (int t = first; ok && t < a.tiles; t += step, chunk0 += c1 - c0) {
+    for (int t = first; ok && t < a.tiles; t += step) {
       for (int b = 0; ok && b < nb; ++b) {
         bool got = wait_for(q_full + qs, q_phase, abort_flag);
         uint4 codes[4];
@@ -318,18 +364,17 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
 #pragma unroll
           for (int h = 0; h < 4; ++h)
             codes[h] = *reinterpret_cast<const uint4*>(stQ + qs * C::Q_BYTES + r * 128 + (((cg * 4 + h) ^ (r & 7)) << 4));
-          mbar_arrive(q_empty + qs);
         }
-        const int c = b * QC + cg;
-        if (c < c1 - c0) {
-          const uint32_t idx = chunk0 + c;
-          const int stage = idx % S;
-          // The slot is free when the products of chunk idx - S are done.
-          // (Products are done in order, and this group has waited for those of
-          // idx - QC - S: the barrier cannot be two phases behind, which a
-          // parity could not tell.)
-          static_assert(S >= QC && CONV_GROUPS == QC, "a slot's parity is unambiguous, a group per chunk of a block");
-          got = got && wait_for(empty + stage, (idx / S & 1u) ^ 1u, abort_flag);
+        __syncwarp();
+        if (got && lane == 0) mbar_arrive(q_empty + qs);
+        if (b * QC + cg < c1 - c0) {
+          // The slot is free when the products of this group's chunk j - SP are
+          // done.  (Every phase of a barrier is waited for in turn: a parity
+          // could not tell two phases from none.)
+          const int stage = cg * SP + j % SP;
+          static_assert(CONV_GROUPS == QC && QC == 2, "a group per chunk of a block");
+          got = got && wait_for(empty + stage, (j / SP & 1u) ^ 1u, abort_flag);
+          ++j;
           if (!__all_sync(0xffffffffu, got)) {  // TMEM stores are warp-wide
             ok = false;
             break;
@@ -339,16 +384,18 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             const uint32_t w[4] = {codes[h].x, codes[h].y, codes[h].z, codes[h].w};
+            uint32_t v[16];
 #pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-              const uint4 x = nibbles8(w[j]), y = nibbles8(w[j + 1]);
-              const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-              tmem_st8(dst + h * 16 + j * 4, v);
+            for (int j = 0; j < 4; ++j) {
+              const uint4 x = nibbles8(w[j]);
+              v[4 * j] = x.x, v[4 * j + 1] = x.y, v[4 * j + 2] = x.z, v[4 * j + 3] = x.w;
             }
+            tmem_st16(dst + h * 16, v);
           }
           tmem_st_wait();
           tc_fence_before();
-          mbar_arrive(full + stage);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full + stage);
         }
         ok = __all_sync(0xffffffffu, got);
         if (++qs == QS) {
@@ -372,10 +419,10 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
       float acc[COLS];
 #pragma unroll
       for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
-      float s_next = g0 < min(g1, groups) ? __bfloat162float(srow[g0]) : 0.f;
+      bf16 s_next = g0 < min(g1, groups) ? srow[g0] : __float2bfloat16(0.f);
       for (int g = g0; ok && g < g1; ++g) {
-        const float s = s_next;
-        s_next = g + 1 < min(g1, groups) ? __bfloat162float(srow[g + 1]) : 0.f;
+        const float s = __bfloat162float(s_next);  // (here, not behind its load: it has landed)
+        s_next = g + 1 < min(g1, groups) ? srow[g + 1] : __float2bfloat16(0.f);
         // (the whole warp goes on or gives up: TMEM reads are warp-wide)
         const bool got = wait_for(acc_full + buf, acc_phase, abort_flag);
         if (!__all_sync(0xffffffffu, got)) {
@@ -392,7 +439,8 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
           tmem_ld<W>(d + j0, v);
           if (j0 + W == COLS) {  // the last read: the accumulator is free before its values are used
             tc_fence_before();
-            mbar_arrive(acc_empty + buf);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty + buf);
           }
 #pragma unroll
           for (int j = 0; j < W; ++j) acc[j0 + j] = fmaf(s, __uint_as_float(v[j]), acc[j0 + j]);
