@@ -59,7 +59,7 @@ struct Cfg {
   static constexpr int EPI_THREADS = BN / COLS * 128, THREADS = 128 + EPI_THREADS + CONV_THREADS;
   static constexpr int SMEM = QS * Q_BYTES + SB * B_BYTES + 2048;
   static_assert(SMEM <= SMEM_BUDGET + 2048, "shared memory");
-  static_assert(S % 2 == 0 && SB % 2 == 0, "half of each to either issuer");
+  static_assert(S % 2 == 0 && SB % 2 == 0 && ACC % 2 == 0, "half of each to either parity");
   static_assert(ACC * BN + S * A_COLS <= (int)TMEM_COLS, "TMEM");
   static_assert(SB * B_BYTES >= BM * BN * 4, "the ring holds a partial tile");
 };
@@ -157,7 +157,9 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
     linear_w4_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmX, Args a) {
   using C = Cfg<BN>;
   constexpr int S = C::S, SB = C::SB, QS = C::QS, ACC = C::ACC, EPI_THREADS = C::EPI_THREADS, THREADS = C::THREADS;
-  constexpr int SP = S / 2, BP = SB / 2;  // of either issuer
+  constexpr int SP = S / 2, BP = SB / 2;  // of chunks of either parity
+  constexpr int AP = ACC / 2;             // of either issuer
+  constexpr bool EVERY = G < BK;          // both issuers work on every chunk
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stB = smem;
@@ -184,11 +186,11 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
     }
     for (int s = 0; s < S; ++s) {
       mbar_init(full + s, CONV_GROUP / 32);
-      mbar_init(empty + s, 1);
+      mbar_init(empty + s, EVERY ? 2 : 1);
     }
     for (int s = 0; s < SB; ++s) {
       mbar_init(b_full + s, 1);
-      mbar_init(b_empty + s, 1);
+      mbar_init(b_empty + s, EVERY ? 2 : 1);
     }
     for (int i = 0; i < ACC; ++i) {
       mbar_init(acc_full + i, 1);
@@ -215,69 +217,59 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
   float* part = reinterpret_cast<float*>(smem);  // [BN][BM], in the idle ring
 
   const int nb = (c1 - c0 + QC - 1) / QC;  // blocks of codes of a tile
+  // A group's products are the work of issuer 0 or 1 in turn: chunks alternate
+  // where a chunk is one group, otherwise both issuers take their groups of
+  // every chunk.  Each has accumulators of its own.  (On every barrier every
+  // phase is waited for, by warps without which the next cannot complete: a
+  // parity cannot tell two phases from none.)
   auto issue = [&](auto parity) {
-    // The whole warp walks its chunks, so that descriptors stay in uniform
+    // The whole warp walks the chunks, so that descriptors stay in uniform
     // registers; one lane issues.
     constexpr int p = decltype(parity)::value;
     const bool leader = elect_one();
     constexpr uint32_t idesc = idesc_bf16_f32(BM, BN);
-    int stage = p * SP, slot = p * BP, buf = 0;
-    uint32_t phase = 0, b_phase = 0, acc_phase = 0;
+    int buf = p * AP;
+    uint32_t acc_phase = 0, n[2] = {0, 0};  // n: chunks of either parity so far
     bool ok = true;
-    for (int t = first; ok && t < a.tiles; t += step) {
-      for (int c = c0; c < c1; ++c) {
-        if (((c - c0) & 1) != p) {
-          // The other's chunk.  Its accumulators' phases are waited for as well:
-          // a parity could not tell two phases from none.
-          for (int i = 0; ok && i < BK / G; ++i) {
-            ok = __all_sync(0xffffffffu, wait_for(acc_empty + buf, acc_phase ^ 1u, abort_flag));
-            if (++buf == ACC) {
-              buf = 0;
-              acc_phase ^= 1u;
-            }
-          }
-          if (!ok) break;
-          continue;
-        }
-        const bool landed = wait_for(b_full + slot, b_phase, abort_flag);
-        ok = __all_sync(0xffffffffu, landed && wait_for(full + stage, phase, abort_flag));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t at = tmem_a + (uint32_t)(stage * A_COLS);
-        const uint64_t bd = sdesc_sw128(smem_u32(stB + slot * C::B_BYTES));
+    auto products = [&](auto chunk_parity, uint32_t i) {
+      constexpr int cp = decltype(chunk_parity)::value;
+      const int stage = cp * SP + i % SP, slot = cp * BP + i % BP;
+      const bool landed = wait_for(b_full + slot, i / BP & 1u, abort_flag);
+      if (!__all_sync(0xffffffffu, landed && wait_for(full + stage, i / SP & 1u, abort_flag))) return false;
+      tc_fence_after();
+      const uint32_t at = tmem_a + (uint32_t)(stage * A_COLS);
+      const uint64_t bd = sdesc_sw128(smem_u32(stB + slot * C::B_BYTES));
 #pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk) {
-          const bool begin = kk % (G / 16) == 0, end = kk % (G / 16) == G / 16 - 1;
+      for (int kk = 0; kk < BK / 16; ++kk) {
+        const bool begin = kk % (G / 16) == 0, end = kk % (G / 16) == G / 16 - 1;
+        if (!EVERY || kk / (G / 16) % 2 == p) {
           if (begin) {
-            ok = __all_sync(0xffffffffu, wait_for(acc_empty + buf, acc_phase ^ 1u, abort_flag));
-            if (!ok) break;
+            if (!__all_sync(0xffffffffu, wait_for(acc_empty + buf, acc_phase ^ 1u, abort_flag))) return false;
             tc_fence_after();
           }
-          if (leader) umma_bf16_ts(tmem + (uint32_t)(buf * BN), at + 8u * kk, bd + (uint64_t)((kk >> 2) * (C::B_BYTES / 32) + 2 * (kk & 3)),
-                                   idesc, begin ? 0u : 1u);
+          if (leader)
+            umma_bf16_ts(tmem + (uint32_t)(buf * BN), at + 8u * kk,
+                         bd + (uint64_t)((kk >> 2) * (C::B_BYTES / 32) + 2 * (kk & 3)), idesc, begin ? 0u : 1u);
           if (end) {
             if (leader) umma_commit(acc_full + buf);
-            if (++buf == ACC) {
-              buf = 0;
+            if (++buf == (p + 1) * AP) {
+              buf = p * AP;
               acc_phase ^= 1u;
             }
           }
         }
-        if (!ok) break;
-        if (leader) {
-          umma_commit(empty + stage);
-          umma_commit(b_empty + slot);
-        }
-        if (++stage == (p + 1) * SP) {
-          stage = p * SP;
-          phase ^= 1u;
-        }
-        if (++slot == (p + 1) * BP) {
-          slot = p * BP;
-          b_phase ^= 1u;
-        }
       }
-    }
+      if (leader) {
+        umma_commit(empty + stage);
+        umma_commit(b_empty + slot);
+      }
+      return true;
+    };
+    for (int t = first; ok && t < a.tiles; t += step)
+      for (int c = c0; ok && c < c1; c += 2) {
+        if (EVERY || p == 0) ok = products(std::integral_constant<int, 0>(), n[0]++);
+        if ((EVERY || p == 1) && c + 1 < c1) ok = ok && products(std::integral_constant<int, 1>(), n[1]++);
+      }
     if (!ok) *abort_flag = 1;
     if (leader) {
       umma_commit(drain);  // every product of this thread completes before TMEM can be freed
@@ -410,8 +402,7 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
     constexpr int COLS = C::COLS;
     const int q = warp & 3, row = q * 32 + lane, set = (warp - 2) >> 2;
     const int g0 = c0 * BK / G, g1 = (c1 * BK + G - 1) / G, groups = a.K / G;
-    int buf = 0;
-    uint32_t acc_phase = 0;
+    uint32_t k0 = 0, k1 = 0;  // groups of either issuer so far
     bool ok = true;
     for (int t = first; t < a.tiles; t += step) {
       const int nt = t % a.n_tiles, mt = t / a.n_tiles, m = mt * BM + row;
@@ -423,8 +414,10 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
       for (int g = g0; ok && g < g1; ++g) {
         const float s = __bfloat162float(s_next);  // (here, not behind its load: it has landed)
         s_next = g + 1 < min(g1, groups) ? srow[g + 1] : __float2bfloat16(0.f);
+        const bool odd = (g - g0) & 1;
+        const uint32_t k = odd ? k1++ : k0++, buf = (odd ? AP : 0) + k % AP;
         // (the whole warp goes on or gives up: TMEM reads are warp-wide)
-        const bool got = wait_for(acc_full + buf, acc_phase, abort_flag);
+        const bool got = wait_for(acc_full + buf, k / AP & 1u, abort_flag);
         if (!__all_sync(0xffffffffu, got)) {
           *abort_flag = 1;
           ok = false;
@@ -444,10 +437,6 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
           }
 #pragma unroll
           for (int j = 0; j < W; ++j) acc[j0 + j] = fmaf(s, __uint_as_float(v[j]), acc[j0 + j]);
-        }
-        if (++buf == ACC) {
-          buf = 0;
-          acc_phase ^= 1u;
         }
       }
       if (!ok) {
