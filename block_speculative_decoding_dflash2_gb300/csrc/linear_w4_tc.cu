@@ -141,6 +141,18 @@ __device__ __forceinline__ uint4 nibbles8(uint32_t w) {
   return make_uint4(two(p01, 0x4140), two(p01, 0x4342), two(p23, 0x4140), two(p23, 0x4342));
 }
 
+// (a, b) += s (x, y), one instruction for both.
+__device__ __forceinline__ void fma2(float& a, float& b, uint32_t x, uint32_t y, float s) {
+  asm("{\n\t.reg .b64 d, e, f;\n\t"
+      "mov.b64 d, {%0, %1};\n\t"
+      "mov.b64 e, {%2, %3};\n\t"
+      "mov.b64 f, {%4, %4};\n\t"
+      "fma.rn.f32x2 d, e, f, d;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "r"(x), "r"(y), "f"(s));
+}
+
 // D[tmem] (+)= A[tmem] * B[smem]^T: A's rows are lanes, two bf16 of a row a column.
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                              uint32_t accumulate) {
@@ -436,7 +448,7 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
             if (lane == 0) mbar_arrive(acc_empty + buf);
           }
 #pragma unroll
-          for (int j = 0; j < W; ++j) acc[j0 + j] = fmaf(s, __uint_as_float(v[j]), acc[j0 + j]);
+          for (int j = 0; j < W; j += 2) fma2(acc[j0 + j], acc[j0 + j + 1], v[j], v[j + 1], s);
         }
       }
       if (!ok) {
