@@ -12,8 +12,8 @@
 // (16, 8 or 4 bytes for groups of 128, 64 or 32: the four lanes of a row then
 // always hold the same group) and the activations are stored in shared memory
 // in the matching order, one 16-byte read per lane for two products.  A
-// nibble becomes a bf16 whole number in -8..7 by two integer steps and one
-// subtraction, so every product is exact; a group's fp32 sums are then scaled
+// nibble becomes the bf16 value (q - 8) / 64 by a mask and a multiply-add (the
+// 64 is put back at the end), so every product is exact; a group's fp32 sums are then scaled
 // and added to the row's, which keeps the scale out of bf16.
 //
 // A CTA of 8 warps owns 128 weight rows at a time (16 a warp), or 256 where
@@ -50,12 +50,15 @@ struct Args {
   int accumulate;
 };
 
-// Nibbles e and e + 4 of a word as bf16x2 (128 + q) - 136 = q - 8, exactly.
-__device__ __forceinline__ uint32_t nib2(uint32_t w, int e) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(r) : "r"(w >> (4 * e)));
-  const __nv_bfloat162 d =
-      __hsub2(*reinterpret_cast<__nv_bfloat162*>(&r), __float2bfloat162_rn(136.f));
+// Nibbles e and e + 4 of a word (w8 = w >> 8) as bf16x2 (q - 8) / 64, exactly.
+// A nibble's bits alone, at the bottom of a half or four above, are the values
+// q 2^-133 and q 2^-129 (bf16 is linear up to 255 2^-133), so nothing is shifted
+// but the word, once.
+constexpr float UNSCALE = 64.f;
+__device__ __forceinline__ uint32_t nib2(uint32_t w, uint32_t w8, int e) {
+  const uint32_t r = (e < 2 ? w : w8) & (e & 1 ? 0x00f000f0u : 0x000f000fu);
+  const __nv_bfloat162 d = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&r),
+                                   __float2bfloat162_rn(e & 1 ? 0x1p+123f : 0x1p+127f), __float2bfloat162_rn(-0.125f));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 
@@ -222,8 +225,9 @@ __global__ void __launch_bounds__(WARPS * 32, 2) linear_w4_kernel(Args a) {
 #pragma unroll
             for (int k = 0; k < MT; ++k) {
               const uint32_t wl = q.w[2 * k][i], wh = q.w[2 * k + 1][i];
-              const uint32_t a0 = nib2(wl, 0), a1 = nib2(wh, 0), a2 = nib2(wl, 1), a3 = nib2(wh, 1);
-              const uint32_t b0 = nib2(wl, 2), b1 = nib2(wh, 2), b2 = nib2(wl, 3), b3 = nib2(wh, 3);
+              const uint32_t ul = wl >> 8, uh = wh >> 8;
+              const uint32_t a0 = nib2(wl, ul, 0), a1 = nib2(wh, uh, 0), a2 = nib2(wl, ul, 1), a3 = nib2(wh, uh, 1);
+              const uint32_t b0 = nib2(wl, ul, 2), b1 = nib2(wh, uh, 2), b2 = nib2(wl, ul, 3), b3 = nib2(wh, uh, 3);
 #pragma unroll
               for (int j = 0; j < NT; ++j) {
                 mma16816(p[k][j], a0, a1, a2, a3, xv[j].x, xv[j].y);
@@ -252,7 +256,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) linear_w4_kernel(Args a) {
     auto put = [&](int n, int m, float v) {
       if (n < a.N && m < a.M) {
         OutT* o = static_cast<OutT*>(a.out) + (size_t)n * a.ldo + m;
-        st(o, a.accumulate ? ld(o) + v : v);
+        st(o, a.accumulate ? fmaf(v, UNSCALE, ld(o)) : v * UNSCALE);
       }
     };
     if (a.split == 1) {
