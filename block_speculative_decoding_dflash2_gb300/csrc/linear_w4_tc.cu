@@ -502,6 +502,41 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
   if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
 }
 
+// Lets the kernel use its shared memory on the current device, and counts the
+// clusters of `split` CTAs that run at once on it (both once per device and
+// size).
+template <int BN, int G, typename OutT>
+int wave_of(int split, int nsm) {
+  using C = Cfg<BN>;
+  static std::atomic<int> waves[64][9];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
+  int n = waves[dev][split].load(std::memory_order_relaxed);
+  if (n) return n;
+  auto kern = linear_w4_tc_kernel<BN, G, OutT>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return -1;
+  n = nsm;
+  if (split > 1) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(split * 64);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = split;
+    at.val.clusterDim.y = 1;
+    at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+      (void)cudaGetLastError();
+      return -1;
+    }
+  }
+  waves[dev][split].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 template <int BN, int G, typename OutT>
 int launch(const W4Op& g, const Ctx& c) {
   using C = Cfg<BN>;
@@ -518,21 +553,18 @@ int launch(const W4Op& g, const Ctx& c) {
   a.chunks = (g.K + BK - 1) / BK;
   a.n_tiles = (g.N + BN - 1) / BN;
   a.tiles = (g.M + BM - 1) / BM * a.n_tiles;
-  // inputs split while that leaves every tile's cluster an SM each and a CTA at least 8 chunks
+  // Inputs split as far as all tiles' clusters run at once and a CTA has at
+  // least 4 chunks.  (Clusters do not fill every group of SMs: 48 of 3 CTAs
+  // need a second wave on 152 SMs, 6144 x 4096 x 17 took 16.6 us; 48 of 2, 9.9.)
   a.split = std::max(1, std::min({8, c.nsm / a.tiles, a.chunks / 4}));
+  int wave;
+  while ((wave = wave_of<BN, G, OutT>(a.split, c.nsm)) >= 0 && a.split > 1 && wave < a.tiles) --a.split;
+  if (wave < 0) return DFLASH2_ERR_CUDA;
   a.slice = ((a.chunks + a.split - 1) / a.split + QC - 1) / QC * QC;
   a.out = g.out;
   a.ldo = g.ldo;
   a.accumulate = g.accumulate;
   auto kern = linear_w4_tc_kernel<BN, G, OutT>;
-  static std::atomic<unsigned long long> opted{0};  // devices whose kernel may use this much shared memory
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return DFLASH2_ERR_CUDA;
-  if (!(opted.load(std::memory_order_relaxed) >> dev & 1)) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-      return DFLASH2_ERR_CUDA;
-    opted.fetch_or(1ull << dev, std::memory_order_relaxed);
-  }
   const int grid = a.split > 1 ? a.tiles * a.split : std::min(a.tiles, c.nsm);
   return launch_kx(kern, dim3(grid), dim3(C::THREADS), C::SMEM, c, a.split, mq, mx, a);
 }
