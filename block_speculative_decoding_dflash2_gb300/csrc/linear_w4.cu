@@ -359,13 +359,16 @@ int launch(Args a, int split, const Ctx& c) {
   return launch_kx(kern, dim3(clusters * a.split, nb), dim3(WARPS * 32), smem, c, a.split, a);
 }
 
-// Blocks of 256 rows unless blocks of 128 fill more of a wave.
+// Blocks of 256 rows unless blocks of 128 fill more of a wave; for more than 8
+// activation rows, whose reads weigh more, also where those fill an SM each
+// (16 rows, groups of 64, us with 256 and 128: 24576 x 4096 22.1, 28.7; 34816 x
+// 5120 34.6, 37.7; but 12288 x 4096 16.0, 13.6).
 template <int G, int NT, typename OutT>
 int launch_m(const Args& a, const Ctx& c) {
   const int b2 = (a.M + 255) / 256, b1 = (a.M + 127) / 128, wave = 2 * c.nsm;
   const int s2 = split_of<G, NT, 2, OutT>(b2, a.chunks, c.nsm), s1 = split_of<G, NT, 1, OutT>(b1, a.chunks, c.nsm);
-  return std::min(b2 * s2, wave) >= std::min(b1 * s1, wave) ? launch<G, NT, 2, OutT>(a, s2, c)
-                                                            : launch<G, NT, 1, OutT>(a, s1, c);
+  const bool two = (NT == 2 && b1 >= c.nsm) || std::min(b2 * s2, wave) >= std::min(b1 * s1, wave);
+  return two ? launch<G, NT, 2, OutT>(a, s2, c) : launch<G, NT, 1, OutT>(a, s1, c);
 }
 
 template <int G, typename OutT>
