@@ -555,6 +555,23 @@ __global__ void __launch_bounds__(128) join_kernel(SamplingArgs a) {
   if (s < a.batch) join_rows(a, s, a.n_draft ? min(max(a.n_draft[s], 0), a.rows - 1) : a.rows - 1);
 }
 
+// One thread-block cluster per row, a slice of the row in each CTA's shared
+// memory (RES; a vocabulary above 155,648 in fp32 stays in global memory): the
+// logits are read from HBM once, and a row's steps are passes over shared
+// memory joined by cluster barriers.
+//   a small top-k    each CTA picks its candidates by its threads' largest
+//                    logits, the first CTA ranks what they picked (no pass
+//                    over all masses)
+//   a top-p alone    the same with a few tokens, if a sample of the masses says
+//                    that they may hold the nucleus; otherwise, as for a large
+//                    top-k: a histogram of counts guesses the border's bins,
+//                    and one pass over all masses takes their tokens, the mass
+//                    ahead of them and the kept mass of each warp
+//   neither          the kept mass of each warp decides which one holds the draw
+// What bounds it: one row, the latency of those steps (151936 fp32 logits with
+// top-k 20 and top-p 0.95: 11.8 us; a nucleus over a flat row 45 us).  Many rows,
+// instructions per mass, about 40 (128 flat bf16 rows of 151936: 80 us drawn at a
+// temperature alone, 168 us from a nucleus, 12 us being their bytes at HBM speed).
 template <typename T, bool RES>
 __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice) {
   extern __shared__ uint4 zs_raw[];
@@ -579,7 +596,9 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
   const float top_p = a.top_p ? a.top_p[seq] : 1.f, min_p = a.min_p ? a.min_p[seq] : 0.f;
   const bool greedy = !(temp > 0.f);
   // (64-bit floats are slow here: one lane each, while the logits load)
-  if (tid == 64) sm.c_pair = pair_of(1.4426950408889634074 / (greedy ? 1.0 : (double)temp));
+  // (a scale above fp32's range, from subnormal temperatures, is its largest value:
+  // 0 times it is still 0)
+  if (tid == 64) sm.c_pair = pair_of(fmin(1.4426950408889634074 / (greedy ? 1.0 : (double)temp), 3.4028234663852886e38));
   if (tid == 96 && min_p > 0.f) sm.off_pair = pair_of((double)temp * log((double)min_p));
 
   int x = -1;          // the draft's token
@@ -1628,8 +1647,12 @@ int launch_one(const SamplingArgs& a, int slice, const Ctx& c) {
 }
 
 // A row's cluster: as few CTAs as hold it in shared memory with two of them an
-// SM, more while the rows leave SMs idle.  (Rows shared out over one wave
-// instead, up to one CTA a row that reads its logits again from L2 in every
+// SM, more while the rows leave SMs idle.  (64 bf16 rows of 151936 in clusters of
+// 4 and 8, us: small top-k 18 and 28, flat nucleus 90 and 144, but settings of
+// their own 82 and 62, the few rows of the long way taking half as long.
+// Clusters of 3, 5, 6 or 7 where those suffice: 256 fp32 rows of 102400 77 to 309
+// us against 87 to 354, but 64 to 200 rows of 50257 and 128256 2 to 9% longer.)
+// (Rows shared out over one wave instead, up to one CTA a row that reads its logits again from L2 in every
 // pass, took 315 us against 106 at 256 rows of 151936: the few rows without a
 // small top-k keep their one CTA long after the others are done.)  What does
 // not fit is read again from L2.

@@ -3,7 +3,7 @@ dflash2_target_probs, dflash2_verify_logits) against the definition in
 float64 (tests/sampling_reference.py).
 
 Tolerance of a probability: p = e / M with e from exp2f (2 ulp), a first-order
-correction (1 ulp), the whole masses' sum M (exact to 2^-37) rounded to fp32 as
+correction (1 ulp), the whole masses' sum M (good to 2^-35) rounded to fp32 as
 a reciprocal (1 ulp) and the product (half an ulp): below 2^-20 relative, plus
 the smallest normal float where e / M underflows.  Tokens, kept sets and
 accepted lengths are compared exactly.
@@ -194,6 +194,24 @@ def test_masked_and_extreme_rows(dtype, spec):
     assert len(keep) == (7 if dtype == "f32" else 6)
     run_probs(B, z[keep][:, None], settings_of(len(keep), spec), ws)
     assert B.dflash2_read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("spec", [(None, None, None, None), (None, 4, None, None), (None, 4, 0.9, 0.1),
+                                  (None, None, 0.9, None), (None, 500, 0.9, None), (None, None, None, 0.1)], ids=str)
+@pytest.mark.parametrize("temp", [1.4e-45, 1e-40, 2e-39, 1e-38, 1e-20, 1e20, 3.4e38, np.inf])
+def test_temperatures_at_the_ends_of_their_range(temp, spec):
+    """Subnormal ones leave the largest logit all the mass, infinite ones give every token the same."""
+    B = lib()
+    z, zv = logits_of(5, 3001, "normal", 77)
+    spec = (temp,) + spec[1:]
+    mass = [R.masses(zv[r], *plain(spec)) for r in range(5)]
+    got = run_probs(B, z[:, None], settings_of(5, spec))[:, 0].cpu().numpy()
+    for r in range(5):
+        check_probs(got[r], mass[r])
+    for u in (0.0, 0.37, 0.9999999):
+        u = np.full(5, u, np.float32)
+        tok, _ = run_sample(B, z, settings_of(5, spec), u)
+        assert list(tok) == [R.draw(mass[r], u[r]) for r in range(5)]
 
 
 def test_rows_masked_with_the_lowest_bf16_value():
