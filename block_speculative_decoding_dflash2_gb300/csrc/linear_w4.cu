@@ -19,8 +19,15 @@
 // A CTA of 8 warps owns 128 weight rows at a time (16 a warp), or 256 where
 // there are enough of them: two tiles of a warp share the activations' reads,
 // which otherwise bound it (151936 x 4096 with groups of 64 and 8 rows: 76.9 us
-// with 79% of the shared-memory cycles taken).  With few row blocks the inputs are split over a cluster of up to 8 CTAs, whose partial
-// sums are added in rank order through distributed shared memory.
+// with 79% of the shared-memory cycles taken; 69.8 with two).  With few row blocks
+// the inputs are split over a cluster of up to 8 CTAs, whose partial sums are
+// added in rank order through distributed shared memory.
+//
+// What bounds it: 151936 x 4096 for one row takes 55.5 us with groups of 128 (5.8
+// TB/s), where HBM needs 47; 69.5 and 111 with groups of 64 and 32, whose sums
+// are scaled two and four times as often by the same 16 warps an SM (more do not
+// fit beside the weights in flight).  A small matrix takes its launch and two
+// trips to memory: 704 x 256 2.0 us.
 #include <algorithm>
 #include <atomic>
 

@@ -3,26 +3,37 @@
 // linear_w4.cu).
 //
 // A 128-row weight tile is operand A of tcgen05.mma, held in TMEM, BN
-// activation rows are operand B in shared memory, and every group of inputs is summed on its own: the whole numbers
-// q - 8 are exact in bf16, a group's fp32 sums lie in one of four TMEM
-// accumulators, and the epilogue warps read them, multiply them by the row's
-// group scale and add them to the row's sums in registers while the tensor
-// core fills the others.  (Scaled weights would need 11 bits, three more
-// than bf16 has.)
+// activation rows are operand B in shared memory, and every group of inputs is
+// summed on its own: (q - 8) / 64 is exact in bf16, a group's fp32 sums lie in
+// one of two to eight TMEM accumulators, and the epilogue warps read them,
+// multiply them by the row's group scale and add them to the row's sums in
+// registers while the tensor core fills the others.  (Scaled weights would need
+// 11 bits, three more than bf16 has.)
 //
 // Warp roles (one CTA an SM):
 //   warp 0       TMA producer of codes (one lane)
-//   warp 1       MMA issuer (one lane) of even chunks, and TMEM owner
+//   warp 1       MMA issuer (one lane) of even groups, and TMEM owner
 //   then         epilogue: a set of four warps for every 32 columns
 //   then 8       converters, in two groups of four on alternate chunks:
 //                thread = weight row, its 64 bytes of codes -> 128 bf16 values
 //                in 64 columns of its TMEM lane
-//   last 2       MMA issuer of odd chunks; TMA producer of activations
+//   last 2       MMA issuer of odd groups; TMA producer of activations
+// Two issuers because a group's fences, waits and commits take one longer than
+// its products (24576 x 4096 x 1024, with the activations' own producer: 187 us
+// against 202).
 // Operand A in TMEM because shared memory bounds the alternative: reading both
 // operands of a 128 x 128 product takes all of its 128 bytes a cycle, and
 // writing the converted tile as much again as a copy of the activations.
 // With few tiles the inputs are split over a cluster, whose partial tiles are
 // added in rank order through distributed shared memory.
+//
+// What bounds it: the CUDA cores beside the tensor core, 11 instructions for 8
+// weights and one for two sums.  24576 x 4096 for 1024 rows takes 173 us (1.20
+// PFLOP/s), 5120 x 17408 for 128 rows 26.9, the readout of 151936 x 4096 for 32
+// rows 85; groups of 64 and 32 double and quadruple the sums to scale (207 against
+// 137 us at 128 rows of that readout).  Timed copies of the kernel without the
+// conversion's arithmetic took 15% less, with an eighth of the products, without
+// the TMEM reads or without the activations' copies 0 to 2%.
 //
 // Every wait is bounded (1 s).  A wait that gives up lets the other roles bail
 // out, the tile's outputs become NaN, and the kernel waits (bounded) for its
