@@ -1215,6 +1215,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
           if (tid == 0) sm.ecum[NB] = all;
           want_f = top_p * all;
         }
+        const Cut given = cut;
         for (int tries = 0;; ++tries) {
           if (rank == 0) {
             if (tid == 0) sm.pick2 = lo_least;
@@ -1378,6 +1379,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
                     st_cl(dsmem_addr(&sm.wkept[tid % NW], tid / NW), ((u64)sm.sub_hi[tid] << 21) + sm.sub_lo[tid]);
                 }
               } else {
+                cut = given;  // not the list's
                 const bool later = want > g;
                 const u64 at = later ? g + lall : g;
                 want_f = sm.ecum[later ? hi + 1 : lo] +

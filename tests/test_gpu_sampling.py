@@ -244,6 +244,28 @@ def test_borders_at_zero_and_among_its_neighbours():
             assert tok[r] == R.draw(w, u[r])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("by_k", [False, True])
+def test_borders_among_few_distinct_values(dtype, by_k):
+    """Logits on a coarse grid: large ties, so that the first guess of a top-p border is often wrong."""
+    import torch
+    B = lib()
+    rows, V = 400, 15000
+    g = np.random.default_rng(31 + by_k)
+    z = dev(np.rint(4 * g.standard_normal((rows, V))).astype(np.float32), torch.bfloat16 if dtype == "bf16" else torch.float32)
+    zv = z.double().cpu().numpy()
+    t, p = g.uniform(1.2, 2, rows).astype(np.float32), g.uniform(0.05, 1, rows).astype(np.float32)
+    k = g.integers(101, 4000, rows).astype(np.int32) if by_k else np.zeros(rows, np.int32)
+    settings = (dev(t), dev(k), dev(p), None)
+    u = g.random(rows, dtype=np.float32)
+    got = run_probs(B, z[:, None], settings)[:, 0].cpu().numpy()
+    tok, _ = run_sample(B, z, settings, u)
+    for r in range(rows):
+        w = R.masses(zv[r], float(t[r]), int(k[r]), float(p[r]), 0.0)
+        check_probs(got[r], w)
+        assert tok[r] == R.draw(w, u[r]), r
+
+
 def test_draws_of_wide_flat_rows_are_exact():
     """400 draws from 50257 nearly equal tokens: one part in 10^7 of error in
     the running sum would move several of them."""
