@@ -32,6 +32,9 @@ typedef unsigned long long u64;
 constexpr int NT = 512, NW = NT / 32;
 constexpr int NB = 1024;    // bins of a row's histogram
 constexpr int CAP = 2048;   // tokens of a list
+// Tokens of a list at a top-p border, whose masses (up to 2^42 each: any token's
+// at a very high temperature) are summed as 21 low bits and the rest, in 32 bits each.
+constexpr int TOPP_CAP = CAP - 1;
 constexpr int SMALL = 256;  // tokens of a list that is ranked instead of sorted
 constexpr int CMAX = 8;     // CTAs of a row's cluster
 constexpr int LOCAL_K = 100;  // largest top-k whose tokens each CTA picks on its own
@@ -1234,7 +1237,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
                 bool& side = d & 1 ? up : down;
                 if (!side) continue;
                 const int b = d & 1 ? lo - 1 : hi + 1;
-                side = b >= lo_least && b <= hi_most && n + sm.hist[b] <= CAP;
+                side = b >= lo_least && b <= hi_most && n + sm.hist[b] <= TOPP_CAP;
                 if (!side) continue;
                 n += sm.hist[b];
                 lo = min(lo, b);
@@ -1242,7 +1245,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
               }
               sm.mk.lo = lo;
               sm.mk.hi = hi;
-              sm.mk.step = n <= CAP && tries < 8 ? STEP_TOPP : STEP_SLOW_P;
+              sm.mk.step = n <= TOPP_CAP && tries < 8 ? STEP_TOPP : STEP_SLOW_P;
               sm.ncand = 0;
             }
           }
@@ -1304,7 +1307,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
                 for (int j = 0; j < CAP / NT; ++j) {
                   const float z = okey_value((unsigned)(v[j] >> 32));
                   sb[j] = (int)fminf(fmaxf((top - z) * fine, 0.f), (float)(SUB - 1));
-                  if (v[j]) {  // (below 2^42 each, as the largest logit's bin is not here: no sum of 2048 overflows)
+                  if (v[j]) {
                     const u64 e2 = mass_of(z, sc, sm.tab);
                     atomicAdd(&sm.sub_lo[sb[j]], (unsigned)e2 & 0x1fffffu);
                     atomicAdd(&sm.sub_hi[sb[j]], (unsigned)(e2 >> 21));
@@ -1369,7 +1372,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
                     const int id = (int)~(unsigned)v[j];
                     if (v[j] && kept(key, id, cut)) {
                       const int w = warp_of(id);
-                      const u64 e = mass_of(okey_value(key), sc, sm.tab);  // (below 2^42, as above)
+                      const u64 e = mass_of(okey_value(key), sc, sm.tab);
                       atomicAdd(&sm.sub_lo[w], (unsigned)e & 0x1fffffu);
                       atomicAdd(&sm.sub_hi[w], (unsigned)(e >> 21));
                     }

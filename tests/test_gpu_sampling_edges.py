@@ -1,0 +1,61 @@
+"""Sampling at the ends of its ranges, against the definition in float64
+(tests/sampling_reference.py).  Tokens and kept sets are compared exactly;
+a probability is good to 2^-20 relative (two ulp of the exponential, one of
+its correction, one of the reciprocal, half a one of the product)."""
+
+import numpy as np
+import pytest
+
+from tests import sampling_reference as R
+from tests.helpers import lib
+
+pytestmark = pytest.mark.gpu
+
+RTOL = 2.0 ** -20
+
+
+def settings_of(n, t, k, p, m):
+    import torch
+    f = lambda v, dt: None if v is None else torch.full((n,), v, dtype=dt, device="cuda")
+    return f(t, torch.float32), f(k, torch.int32), f(p, torch.float32), f(m, torch.float32)
+
+
+def draws(B, z, settings, u):
+    import torch
+    tok = torch.full((z.shape[0],), -7, dtype=torch.int32, device="cuda")
+    B.dflash2_sample(z, *settings, torch.from_numpy(u).cuda(), tok)
+    return tok.cpu().numpy()
+
+
+def probs(B, z, settings):
+    import torch
+    out = torch.full((z.shape[0], 1, z.shape[1]), float("nan"), device="cuda")
+    B.dflash2_target_probs(z[:, None], *settings, out)
+    return out[:, 0].cpu().numpy()
+
+
+@pytest.mark.parametrize("temp", [np.inf, 1e30])
+@pytest.mark.parametrize("n_border", [2047, 2048, 2049])
+def test_a_full_list_of_equal_masses_at_the_top_p_border(temp, n_border):
+    """At such temperatures every token has the largest mass.  The border's
+    tokens, as many as a list holds and all of them in one warp's part of the
+    row (36000 bf16 logits, 200 rows: one CTA of 16 warps a row, 2250 tokens
+    each), are two values of one bin; the draws go over all that is kept."""
+    import torch
+    B = lib()
+    n, V, ahead = 200, 36000, 20000
+    z = np.full(V, -63.0, np.float32)
+    first = 11300                                   # in the range of warp 5: 11248 .. 13499
+    border = np.arange(first, first + n_border)
+    z[border] = np.where(np.arange(n_border) % 2, -1 / 32, 0.0)
+    rest = np.setdiff1d(np.arange(V), border)
+    z[np.random.default_rng(1).permutation(rest)[:ahead]] = 1.0
+    p = np.float32((ahead + n_border - 0.5) / V)
+    u = np.random.default_rng(2).random(n, dtype=np.float32)
+    zt = torch.from_numpy(np.broadcast_to(z, (n, V)).copy()).cuda().to(torch.bfloat16)
+    mass = R.masses(z, temp, 0, float(p))
+    assert np.count_nonzero(mass) == ahead + n_border
+    got = draws(B, zt, settings_of(n, temp, None, float(p), None), u)
+    np.testing.assert_array_equal(got, [R.draw(mass, x) for x in u])
+    pr = probs(B, zt[:2], settings_of(2, temp, None, float(p), None))
+    np.testing.assert_allclose(pr, np.broadcast_to(mass / mass.sum(), (2, V)), rtol=RTOL)
