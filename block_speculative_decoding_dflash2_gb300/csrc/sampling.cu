@@ -602,7 +602,9 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
   // (a scale above fp32's range, from subnormal temperatures, is its largest value:
   // 0 times it is still 0)
   if (tid == 64) sm.c_pair = pair_of(fmin(1.4426950408889634074 / (greedy ? 1.0 : (double)temp), 3.4028234663852886e38));
-  if (tid == 96 && min_p > 0.f) sm.off_pair = pair_of((double)temp * log((double)min_p));
+  // (at an infinite temperature every mass is 1 and min(min_p, 1) drops none)
+  if (tid == 96 && min_p > 0.f)
+    sm.off_pair = temp == INFINITY ? make_float2(-INFINITY, 0.f) : pair_of((double)temp * log(fmin((double)min_p, 1.0)));
 
   int x = -1;          // the draft's token
   float zx = -INFINITY;  // and its logit

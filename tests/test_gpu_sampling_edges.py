@@ -59,3 +59,22 @@ def test_a_full_list_of_equal_masses_at_the_top_p_border(temp, n_border):
     np.testing.assert_array_equal(got, [R.draw(mass, x) for x in u])
     pr = probs(B, zt[:2], settings_of(2, temp, None, float(p), None))
     np.testing.assert_allclose(pr, np.broadcast_to(mass / mass.sum(), (2, V)), rtol=RTOL)
+
+
+@pytest.mark.parametrize("k,p", [(None, None), (4, None), (500, None), (None, 0.9), (500, 0.5)])
+@pytest.mark.parametrize("m", [0.5, 1.0, 3.0])
+def test_min_p_at_an_infinite_temperature_keeps_every_token(k, p, m):
+    """Every mass is 1, so none is below min(min_p, 1)."""
+    import torch
+    B = lib()
+    n, V = 4, 3001
+    z = np.random.default_rng(3).standard_normal((n, V)).astype(np.float32)
+    z[:, ::7] = -np.inf
+    zt = torch.from_numpy(z).cuda()
+    st = settings_of(n, np.inf, k, p, m)
+    mass = [R.masses(z[r], np.inf, k or 0, 1.0 if p is None else float(np.float32(p)), m) for r in range(n)]
+    got = probs(B, zt, st)
+    for r in range(n):
+        np.testing.assert_allclose(got[r], mass[r] / mass[r].sum(), rtol=RTOL)
+    u = np.array([0.1, 0.4, 0.7, 0.99], np.float32)
+    np.testing.assert_array_equal(draws(B, zt, st, u), [R.draw(mass[r], u[r]) for r in range(n)])
