@@ -141,11 +141,11 @@ __device__ __forceinline__ void masses_of(const float (&z)[N], const float (&p)[
     for (int i = 0; i < N; ++i)
       if (!(p[i] < FAR)) v[i] = far_mass(p[i]);
   }
-  // (a difference or a product without a value: an infinite maximum, T = infinity)
+  // (a difference or a product without a value: an infinite maximum, which
+  // shares the mass with its equals alone, or T = infinity)
   if (s.odd) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (z[i] == s.zmax || s.hi == 0.f) v[i] = 1ull << 42;
+    for (int i = 0; i < N; ++i) v[i] = z[i] == s.zmax || s.zmax < INFINITY ? 1ull << 42 : 0ull;
   }
 }
 __device__ __forceinline__ u64 mass_of(float z, const Scale& s, const ExpTab& tab) {
@@ -157,7 +157,8 @@ __device__ __forceinline__ u64 mass_of(float z, const Scale& s, const ExpTab& ta
 
 // The same to fp32 accuracy relative to the mass, however small.
 __device__ __forceinline__ float mass_f32(float z, const Scale& s) {
-  if (z == s.zmax || s.hi == 0.f) return 1.f;
+  if (z == s.zmax) return 1.f;
+  if (s.odd) return s.zmax < INFINITY ? 1.f : 0.f;
   const float dh = s.zmax - z, p = __fmul_rn(dh, s.hi);
   if (!(p < 160.f)) return 0.f;
   const float bb = dh - s.zmax, dl = (s.zmax - (dh - bb)) - (z + bb);

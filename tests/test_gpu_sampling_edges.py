@@ -78,3 +78,26 @@ def test_min_p_at_an_infinite_temperature_keeps_every_token(k, p, m):
         np.testing.assert_allclose(got[r], mass[r] / mass[r].sum(), rtol=RTOL)
     u = np.array([0.1, 0.4, 0.7, 0.99], np.float32)
     np.testing.assert_array_equal(draws(B, zt, st, u), [R.draw(mass[r], u[r]) for r in range(n)])
+
+
+@pytest.mark.parametrize("k,p,m", [(None, None, None), (2, None, None), (150, None, None), (None, 0.6, None),
+                                   (None, None, 0.5), (None, None, 1.0), (300, 0.5, 0.5)])
+@pytest.mark.parametrize("temp", [1.0, 1e38, np.inf])
+def test_infinite_logits_share_the_whole_mass_at_any_temperature(temp, k, p, m):
+    import torch
+    B = lib()
+    V = 3001
+    z = np.random.default_rng(4).standard_normal((1, V)).astype(np.float32)
+    tops = [5, 1700, 2999]
+    z[0, tops] = np.inf
+    z[0, 9] = -np.inf
+    zt = torch.from_numpy(z).cuda()
+    kept = tops[:2] if k == 2 else tops
+    if p is not None:
+        kept = kept[:int(np.ceil(float(np.float32(p)) * len(kept)))]
+    want = np.zeros(V)
+    want[kept] = 1 / len(kept)
+    st = settings_of(1, temp, k, p, m)
+    np.testing.assert_allclose(probs(B, zt, st)[0], want, rtol=RTOL)
+    for u in (0.0, 0.4, 0.9):
+        assert draws(B, zt, st, np.array([u], np.float32))[0] == kept[int(float(np.float32(u)) * len(kept))]
