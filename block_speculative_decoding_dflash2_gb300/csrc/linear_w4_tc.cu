@@ -124,15 +124,16 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// Bounded wait for the phase of the given parity.  The clock, whose reading
-// takes longer than most waits, is looked at every 256 tries.
+// Bounded wait for the phase of the given parity, given up too when *abort
+// (nullable) becomes non-zero.  The clock, whose reading takes longer than most
+// waits, is looked at every 256 tries.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
   const uint32_t b = smem_u32(bar);
   uint64_t t0 = 0;
   for (unsigned i = 0;; ++i) {
     if (mbar_try_wait(b, parity)) return true;
     if ((i & 255) != 255) continue;
-    if (*abort) return false;
+    if (abort && *abort) return false;
     const uint64_t t = globaltimer();
     if (t0 == 0) t0 = t;
     else if (t - t0 > WAIT_NS) return false;
@@ -239,6 +240,8 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
   const uint32_t tmem = *tmem_slot, tmem_a = tmem + ACC * BN;  // accumulators, then the A ring
   pdl_wait();
 
+  auto fail = [&]() { *abort_flag = 1; };
+
   const int rank = blockIdx.x % a.split, first = blockIdx.x / a.split, step = gridDim.x / a.split;
   const int c0 = min(a.chunks, rank * a.slice), c1 = min(a.chunks, c0 + a.slice);
   float* part = reinterpret_cast<float*>(smem);  // [BN][BM], in the idle ring
@@ -297,30 +300,20 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
         if (EVERY || p == 0) ok = products(std::integral_constant<int, 0>(), n[0]++);
         if ((EVERY || p == 1) && c + 1 < c1) ok = ok && products(std::integral_constant<int, 1>(), n[1]++);
       }
-    if (!ok) *abort_flag = 1;
+    if (!ok) fail();
     if (leader) {
       umma_commit(drain);  // every product of this thread completes before TMEM can be freed
-      volatile int never = 0;
-      wait_for(drain, 0, &never);
+      if (!wait_for(drain, 0, nullptr)) fail();
     }
-    __syncwarp();
-  };
-  // A producer that gives up, or that others' giving up stopped, stays until its
-  // copies have landed: a millisecond, some hundred times what a copy takes,
-  // stands for waiting on each.
-  auto settle = [&](bool ok, bool issued) {
-    if (!ok) *abort_flag = 1;
-    if (*abort_flag && issued)
-      for (const uint64_t t = globaltimer(); globaltimer() - t < 1000000;) {}
     __syncwarp();
   };
   if (warp == 0) {
     // codes (as the MMA warps: all lanes walk, one issues)
     const bool leader = elect_one();
     const uint64_t policy = policy_evict_first();
-    int s = 0;
+    int s = 0, issued = 0;  // issued: up to QS
     uint32_t phase = 0;
-    bool ok = true, issued = false;
+    bool ok = true;
     for (int t = first; ok && t < a.tiles; t += step)
       for (int b = 0; b < nb; ++b) {
         ok = __all_sync(0xffffffffu, wait_for(q_empty + s, phase ^ 1u, abort_flag));
@@ -330,19 +323,28 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
           // (codes as pairs of bytes: 64 of them are 256 inputs)
           tma_load_2d(stQ + s * C::Q_BYTES, &tmQ, q_full + s, (c0 / QC + b) * (QC * BK / 4), t / a.n_tiles * BM, policy);
         }
-        issued = true;
+        issued = min(issued + 1, QS);
         if (++s == QS) {
           s = 0;
           phase ^= 1u;
         }
       }
-    settle(ok, issued);
+    if (!ok) fail();
+    // every copy has landed before the CTA can end (consumers that gave up do not wait for theirs)
+    for (; issued > 0; --issued) {
+      if (s == 0) {
+        s = QS;
+        phase ^= 1u;
+      }
+      if (!wait_for(q_full + --s, phase, nullptr)) fail();
+    }
+    __syncwarp();
   } else if (warp == THREADS / 32 - 1) {
     // activations
     const bool leader = elect_one();
     const uint64_t policy = policy_evict_last();
     uint32_t j[2] = {0, 0};  // chunks of either parity so far
-    bool ok = true, issued = false;
+    bool ok = true;
     for (int t = first; ok && t < a.tiles; t += step) {
       const int nt = t % a.n_tiles;
       for (int b = 0; ok && b < nb; ++b) {
@@ -358,12 +360,15 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
             tma_load_2d(stB + s * C::B_BYTES, &tmX, b_full + s, c * BK, nt * BN, policy);
             tma_load_2d(stB + s * C::B_BYTES + C::B_BYTES / 2, &tmX, b_full + s, c * BK + 64, nt * BN, policy);
           }
-          issued = true;
           ++j[p];
         }
       }
     }
-    settle(ok, issued);
+    if (!ok) fail();
+    for (int p = 0; p < 2; ++p)  // (as above)
+      for (uint32_t i = j[p] - min(j[p], (uint32_t)BP); i != j[p]; ++i)
+        if (!wait_for(b_full + p * BP + i % BP, i / BP & 1u, nullptr)) fail();
+    __syncwarp();
   } else if (warp == 1) {
     issue(std::integral_constant<int, 0>());
   } else if (warp == THREADS / 32 - 2) {
@@ -423,7 +428,7 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
         }
       }
     }
-    if (!ok) *abort_flag = 1;
+    if (!ok) fail();
   } else {
     // epilogue
     constexpr int COLS = C::COLS;
@@ -446,7 +451,7 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
         // (the whole warp goes on or gives up: TMEM reads are warp-wide)
         const bool got = wait_for(acc_full + buf, k / AP & 1u, abort_flag);
         if (!__all_sync(0xffffffffu, got)) {
-          *abort_flag = 1;
+          fail();
           ok = false;
           break;
         }
