@@ -95,6 +95,8 @@ def testing_lib():
         T.dflash2_test_force_cluster_split.argtypes = [I]
         T.dflash2_test_force_attention.restype = I
         T.dflash2_test_force_attention.argtypes = [I]
+        T.dflash2_test_w4_withhold.restype = I
+        T.dflash2_test_w4_withhold.argtypes = [I]
         T.dflash2_test_last_attention.restype = I
         T.dflash2_test_last_attention.argtypes = []
         T.dflash2_test_gemm_fp8.argtypes = [P, P, I, I, P, I, I, I, P, P, S, P]

@@ -287,6 +287,8 @@ struct W4Op {
 int launch_linear_w4(const W4Op& g, const Ctx& c);     // any number of rows
 int launch_linear_w4_tc(const W4Op& g, const Ctx& c);  // tcgen05 (linear_w4_tc.cu); up to 2^20 rows
 
+void linear_w4_withhold(bool on);  // test hook: no activations are copied, so its waits (tcgen05; of 1 ms then) run out
+
 // logits to tokens (sampling.cu)
 enum { SAMPLING_TOKEN = 0, SAMPLING_PROBS = 1, SAMPLING_VERIFY = 2 };
 struct SamplingArgs {

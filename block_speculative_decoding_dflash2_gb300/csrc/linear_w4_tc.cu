@@ -35,9 +35,10 @@
 // conversion's arithmetic took 15% less, with an eighth of the products, without
 // the TMEM reads or without the activations' copies 0 to 2%.
 //
-// Every wait is bounded (1 s).  A wait that gives up lets the other roles bail
-// out, the tile's outputs become NaN, and the kernel waits (bounded) for its
-// own copies and products, frees TMEM and returns.
+// Every wait is bounded (1 s).  A wait that gives up records
+// DFLASH2_DEV_WAIT_TIMEOUT (where the call has a status word) and lets the other
+// roles bail out, the tile's outputs become NaN, and the kernel waits (bounded)
+// for its own copies and products, frees TMEM and returns.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -82,7 +83,12 @@ struct Args {
   void* out;
   long long ldo;
   int accumulate;
+  unsigned* status;   // or null
+  uint64_t limit_ns;  // of a wait
+  int x_tiles;        // tiles whose activations are copied: all, or none (a test's)
 };
+
+std::atomic<bool> g_withhold{false};
 
 // 32 lanes x W consecutive TMEM columns -> W registers per thread.
 template <int W>
@@ -127,7 +133,7 @@ __device__ __forceinline__ bool elect_one() {
 // Bounded wait for the phase of the given parity, given up too when *abort
 // (nullable) becomes non-zero.  The clock, whose reading takes longer than most
 // waits, is looked at every 256 tries.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
   const uint32_t b = smem_u32(bar);
   uint64_t t0 = 0;
   for (unsigned i = 0;; ++i) {
@@ -136,7 +142,7 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatil
     if (abort && *abort) return false;
     const uint64_t t = globaltimer();
     if (t0 == 0) t0 = t;
-    else if (t - t0 > WAIT_NS) return false;
+    else if (t - t0 > limit_ns) return false;
   }
 }
 
@@ -240,7 +246,10 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
   const uint32_t tmem = *tmem_slot, tmem_a = tmem + ACC * BN;  // accumulators, then the A ring
   pdl_wait();
 
-  auto fail = [&]() { *abort_flag = 1; };
+  auto fail = [&]() {
+    *abort_flag = 1;
+    flag(a.status, DFLASH2_DEV_WAIT_TIMEOUT);
+  };
 
   const int rank = blockIdx.x % a.split, first = blockIdx.x / a.split, step = gridDim.x / a.split;
   const int c0 = min(a.chunks, rank * a.slice), c1 = min(a.chunks, c0 + a.slice);
@@ -264,8 +273,8 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
     auto products = [&](auto chunk_parity, uint32_t i) {
       constexpr int cp = decltype(chunk_parity)::value;
       const int stage = cp * SP + i % SP, slot = cp * BP + i % BP;
-      const bool landed = wait_for(b_full + slot, i / BP & 1u, abort_flag);
-      if (!__all_sync(0xffffffffu, landed && wait_for(full + stage, i / SP & 1u, abort_flag))) return false;
+      const bool landed = wait_for(b_full + slot, i / BP & 1u, abort_flag, a.limit_ns);
+      if (!__all_sync(0xffffffffu, landed && wait_for(full + stage, i / SP & 1u, abort_flag, a.limit_ns))) return false;
       tc_fence_after();
       const uint32_t at = tmem_a + (uint32_t)(stage * A_COLS);
       const uint64_t bd = sdesc_sw128(smem_u32(stB + slot * C::B_BYTES));
@@ -274,7 +283,7 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
         const bool begin = kk % (G / 16) == 0, end = kk % (G / 16) == G / 16 - 1;
         if (!EVERY || kk / (G / 16) % 2 == p) {
           if (begin) {
-            if (!__all_sync(0xffffffffu, wait_for(acc_empty + buf, acc_phase ^ 1u, abort_flag))) return false;
+            if (!__all_sync(0xffffffffu, wait_for(acc_empty + buf, acc_phase ^ 1u, abort_flag, a.limit_ns))) return false;
             tc_fence_after();
           }
           if (leader)
@@ -303,7 +312,7 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
     if (!ok) fail();
     if (leader) {
       umma_commit(drain);  // every product of this thread completes before TMEM can be freed
-      if (!wait_for(drain, 0, nullptr)) fail();
+      if (!wait_for(drain, 0, nullptr, WAIT_NS)) fail();
     }
     __syncwarp();
   };
@@ -316,7 +325,7 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
     bool ok = true;
     for (int t = first; ok && t < a.tiles; t += step)
       for (int b = 0; b < nb; ++b) {
-        ok = __all_sync(0xffffffffu, wait_for(q_empty + s, phase ^ 1u, abort_flag));
+        ok = __all_sync(0xffffffffu, wait_for(q_empty + s, phase ^ 1u, abort_flag, a.limit_ns));
         if (!ok) break;
         if (leader) {
           mbar_arrive_expect_tx(q_full + s, C::Q_BYTES);
@@ -336,7 +345,7 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
         s = QS;
         phase ^= 1u;
       }
-      if (!wait_for(q_full + --s, phase, nullptr)) fail();
+      if (!wait_for(q_full + --s, phase, nullptr, WAIT_NS)) fail();
     }
     __syncwarp();
   } else if (warp == THREADS / 32 - 1) {
@@ -345,14 +354,14 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
     const uint64_t policy = policy_evict_last();
     uint32_t j[2] = {0, 0};  // chunks of either parity so far
     bool ok = true;
-    for (int t = first; ok && t < a.tiles; t += step) {
+    for (int t = first; ok && t < a.x_tiles; t += step) {
       const int nt = t % a.n_tiles;
       for (int b = 0; ok && b < nb; ++b) {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           const int c = c0 + 2 * b + p, s = p * BP + j[p] % BP;
           if (!ok || c >= c1) break;
-          ok = __all_sync(0xffffffffu, wait_for(b_empty + s, (j[p] / BP & 1u) ^ 1u, abort_flag));
+          ok = __all_sync(0xffffffffu, wait_for(b_empty + s, (j[p] / BP & 1u) ^ 1u, abort_flag, a.limit_ns));
           if (!ok) break;
           if (leader) {
             mbar_arrive_expect_tx(b_full + s, C::B_BYTES);
@@ -367,7 +376,7 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
     if (!ok) fail();
     for (int p = 0; p < 2; ++p)  // (as above)
       for (uint32_t i = j[p] - min(j[p], (uint32_t)BP); i != j[p]; ++i)
-        if (!wait_for(b_full + p * BP + i % BP, i / BP & 1u, nullptr)) fail();
+        if (!wait_for(b_full + p * BP + i % BP, i / BP & 1u, nullptr, WAIT_NS)) fail();
     __syncwarp();
   } else if (warp == 1) {
     issue(std::integral_constant<int, 0>());
@@ -382,7 +391,7 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
     bool ok = true;
     for (int t = first; ok && t < a.tiles; t += step) {
       for (int b = 0; ok && b < nb; ++b) {
-        bool got = wait_for(q_full + qs, q_phase, abort_flag);
+        bool got = wait_for(q_full + qs, q_phase, abort_flag, a.limit_ns);
         uint4 codes[4];
         if (got) {
 #pragma unroll
@@ -397,7 +406,7 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
           // could not tell two phases from none.)
           const int stage = cg * SP + j % SP;
           static_assert(CONV_GROUPS == QC && QC == 2, "a group per chunk of a block");
-          got = got && wait_for(empty + stage, (j / SP & 1u) ^ 1u, abort_flag);
+          got = got && wait_for(empty + stage, (j / SP & 1u) ^ 1u, abort_flag, a.limit_ns);
           ++j;
           if (!__all_sync(0xffffffffu, got)) {  // TMEM stores are warp-wide
             ok = false;
@@ -449,7 +458,7 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
         const bool odd = (g - g0) & 1;
         const uint32_t k = odd ? k1++ : k0++, buf = (odd ? AP : 0) + k % AP;
         // (the whole warp goes on or gives up: TMEM reads are warp-wide)
-        const bool got = wait_for(acc_full + buf, k / AP & 1u, abort_flag);
+        const bool got = wait_for(acc_full + buf, k / AP & 1u, abort_flag, a.limit_ns);
         if (!__all_sync(0xffffffffu, got)) {
           fail();
           ok = false;
@@ -580,6 +589,10 @@ int launch(const W4Op& g, const Ctx& c) {
   a.out = g.out;
   a.ldo = g.ldo;
   a.accumulate = g.accumulate;
+  a.status = c.status;
+  const bool withhold = g_withhold.load(std::memory_order_relaxed);
+  a.limit_ns = withhold ? 1000000 : WAIT_NS;
+  a.x_tiles = withhold ? 0 : a.tiles;
   auto kern = linear_w4_tc_kernel<BN, G, OutT>;
   const int grid = a.split > 1 ? a.tiles * a.split : std::min(a.tiles, c.nsm);
   return launch_kx(kern, dim3(grid), dim3(C::THREADS), C::SMEM, c, a.split, mq, mx, a);
@@ -598,6 +611,8 @@ int launch_g(const W4Op& g, const Ctx& c) {
 }
 
 }  // namespace
+
+void linear_w4_withhold(bool on) { g_withhold.store(on); }
 
 int launch_linear_w4_tc(const W4Op& g, const Ctx& c) {
   return g.out_bf16 ? launch_g<bf16>(g, c) : launch_g<float>(g, c);

@@ -76,6 +76,15 @@ int dflash2_test_force_attention(int mode);
  * partial + combine kernels; 0 before any.
  */
 int dflash2_test_last_attention(void);
+
+/*
+ * From now on in this process, on = 1: the tcgen05 4-bit contraction (more
+ * than 16 rows) copies no activations and limits its pipeline waits to 1 ms
+ * (otherwise one second), so they run out: the kernel writes NaN, records
+ * DFLASH2_DEV_WAIT_TIMEOUT and ends.  on = 0 ends this.  Returns 0, or
+ * DFLASH2_ERR_INVALID_ARG for another value.
+ */
+int dflash2_test_w4_withhold(int on);
 int dflash2_test_gemm(int dtype, const void *W, int M, int K, const void *X, int N, int ctas, int accumulate,
                       float *out, void *workspace, size_t ws_bytes, void *stream);
 
