@@ -315,6 +315,11 @@ const char* elem_ptr(const void* base, size_t elems, int dtype) {
   return static_cast<const char*>(base) + elems * esize(dtype);
 }
 
+// What the 4-bit contraction reads in 16-byte units (codes, activations), and
+// its bf16 scales.
+bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
+bool w4_aligned(const void* codes, const float* scale) { return aligned16(codes) && (uintptr_t)scale % 2 == 0; }
+
 int check_weights(const dflash2_config& c, const dflash2_weights* w) {
   if (!w || !w->embed || !w->lm_head || !w->fc || !w->hidden_norm || !w->final_norm || !w->sel || !w->layers)
     return DFLASH2_ERR_INVALID_ARG;
@@ -332,6 +337,19 @@ int check_weights(const dflash2_config& c, const dflash2_weights* w) {
       if (!L.qkv || !L.o || !L.gate_up || !L.down) return DFLASH2_ERR_INVALID_ARG;
       if (c.conv_kernel_size > 0 && (!L.tapgen_attn || !L.tapgen_mlp)) return DFLASH2_ERR_INVALID_ARG;
     }
+  }
+  if (c.dtype == DFLASH2_W4) {
+    const dflash2_scales* s = w->scales;
+    bool ok = w4_aligned(w->lm_head, s->lm_head) && w4_aligned(w->fc, s->fc) && w4_aligned(w->sel, s->sel);
+    for (int l = 0; l < c.n_layers; ++l) {
+      const dflash2_layer_weights& L = w->layers[l];
+      const dflash2_layer_scales& S = s->layers[l];
+      ok = ok && w4_aligned(L.qkv, S.qkv) && w4_aligned(L.o, S.o) && w4_aligned(L.gate_up, S.gate_up) &&
+           w4_aligned(L.down, S.down);
+      if (c.conv_kernel_size > 0)
+        ok = ok && w4_aligned(L.tapgen_attn, S.tapgen_attn) && w4_aligned(L.tapgen_mlp, S.tapgen_mlp);
+    }
+    if (!ok) return DFLASH2_ERR_INVALID_ARG;
   }
   return DFLASH2_OK;
 }
@@ -434,6 +452,13 @@ int check_cache_args(void* kc, void* vc, int n_pages, const int32_t* block_table
   return DFLASH2_OK;
 }
 
+// The activations of a DFLASH2_W4 call: the appended taps and the workspace.
+int check_w4_inputs(const dflash2_config& c, int n_new, const void* taps, const void* ws) {
+  if (c.dtype != DFLASH2_W4) return DFLASH2_OK;
+  if (n_new > 0 && !aligned16(taps)) return DFLASH2_ERR_INVALID_ARG;
+  return aligned16(ws) ? DFLASH2_OK : DFLASH2_ERR_WORKSPACE;
+}
+
 }  // namespace
 
 RopeFreq rope_freq(int d, float theta) {
@@ -504,6 +529,7 @@ int dflash2_append_context(const dflash2_config* cfg, const dflash2_weights* w, 
   TRY(check_weights(*cfg, w));
   TRY(check_cache_args(k_cache, v_cache, n_pages, block_table, max_pages, batch, ctx_len, n_new, new_taps, new_off));
   if (!workspace) return DFLASH2_ERR_WORKSPACE;
+  TRY(check_w4_inputs(*cfg, n_new, new_taps, workspace));
   const Layout L = plan(*cfg, 0, n_new, 0);
   if (ws_bytes < L.total) return DFLASH2_ERR_WORKSPACE;
   Ctx ctx;
@@ -523,6 +549,7 @@ int dflash2_draft_step(const dflash2_config* cfg, const dflash2_weights* w, void
   TRY(check_cache_args(k_cache, v_cache, n_pages, block_table, max_pages, batch, ctx_len, n_new, new_taps, new_off));
   if (!anchor || !cand_id || !cand_logit) return DFLASH2_ERR_INVALID_ARG;
   if (!workspace) return DFLASH2_ERR_WORKSPACE;
+  TRY(check_w4_inputs(*cfg, n_new, new_taps, workspace));
   const dflash2_config c = act_config(*cfg);
   const Scales sc = scales_of(*cfg, *w);
   const int max_ctx = max_pages * c.page_size;
@@ -780,6 +807,8 @@ int dflash2_select_path_ex(const dflash2_config* cfg, const dflash2_weights* w, 
   if (!workspace) return DFLASH2_ERR_WORKSPACE;
   if ((cfg->dtype == DFLASH2_FP8W || cfg->dtype == DFLASH2_W4) && (!w->scales || !w->scales->sel))
     return DFLASH2_ERR_INVALID_ARG;
+  if (cfg->dtype == DFLASH2_W4 && !w4_aligned(w->sel, w->scales->sel)) return DFLASH2_ERR_INVALID_ARG;
+  TRY(check_w4_inputs(*cfg, 0, nullptr, workspace));
   const dflash2_config c = act_config(*cfg);
   const Scales sc = scales_of(*cfg, *w);
   const Layout L = plan(*cfg, batch, 0, 0);
@@ -812,6 +841,8 @@ int dflash2_build_selector_table(const dflash2_config* cfg, const dflash2_weight
   TRY(check_config(cfg));
   if (!w || !w->embed || !w->sel || !table) return DFLASH2_ERR_INVALID_ARG;
   if ((cfg->dtype == DFLASH2_FP8W || cfg->dtype == DFLASH2_W4) && (!w->scales || !w->scales->sel))
+    return DFLASH2_ERR_INVALID_ARG;
+  if (cfg->dtype == DFLASH2_W4 && !(w4_aligned(w->sel, w->scales->sel) && aligned16(w->embed)))
     return DFLASH2_ERR_INVALID_ARG;
   Ctx ctx;
   TRY(device_ctx(&ctx, stream, nullptr));

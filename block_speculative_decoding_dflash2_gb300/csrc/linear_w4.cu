@@ -391,6 +391,10 @@ int launch_g(int group, const Args& a, const Ctx& c) {
 }  // namespace
 
 int launch_linear_w4(const W4Op& g, const Ctx& c) {
+  // (entry points refuse these before their first launch)
+  if ((uintptr_t)g.codes % 16 || (uintptr_t)g.x % 16 || (uintptr_t)g.scale % 2 || (g.N > 1 && g.ldx % 8) ||
+      (uintptr_t)g.out % (g.out_bf16 ? 2 : 4))
+    return DFLASH2_ERR_INVALID_ARG;
   const int most = 1 << 20;  // rows of a launch (its tiles are counted in ints)
   for (int n = 0; n < g.N; n += most) {
     W4Op p = g;

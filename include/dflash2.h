@@ -82,7 +82,9 @@ extern "C" {
                             DFLASH2_W4_GROUP inputs, in the format of dflash2_linear_w4,
                             which every contraction takes; bfloat16 embed, norm gains,
                             activations and cache; fp32 accumulation.  hidden and
-                            intermediate must be multiples of the group.  Not served by
+                            intermediate must be multiples of the group.  Codes, taps,
+                            embed and the workspace are 16-byte aligned (others are
+                            refused).  Not served by
                             dflash2_select_path_static (DFLASH2_ERR_UNSUPPORTED). */
 #define DFLASH2_W4_GROUP 64
 
@@ -227,7 +229,7 @@ size_t dflash2_workspace_size(const dflash2_config *cfg, int max_batch,
  *   n_new      host int, total appended rows (sum over the batch), >= 0
  *   new_taps   [n_new, T*H] target taps of the newly committed positions,
  *              concatenated in target_layer_ids order, rows grouped by
- *              sequence in batch order
+ *              sequence in batch order (16-byte aligned with DFLASH2_W4)
  *   new_off    [batch+1] int32 row offsets of each sequence into new_taps
  *              (new_off[0] = 0, new_off[batch] = n_new)
  *   ctx_len    [batch] int32 committed context positions BEFORE the append;
