@@ -20,6 +20,7 @@ BF16 = 1
 FP8W = 2
 W4 = 3
 W4_GROUP = 64
+STATUS_BYTES = 256  # of a workspace that only its status word is used of
 
 STATUS = {0: "ok", -1: "invalid argument", -2: "shape", -3: "block size", -4: "dtype",
           -5: "workspace", -6: "cuda", -7: "unsupported"}
@@ -351,6 +352,18 @@ def _at(fn, name, t, dev, dtype, shape):
     return t.data_ptr()
 
 
+def _workspace(fn, ws, dev, least=0):
+    """Address of a workspace (or None, or a raw address): contiguous, on
+    device dev, of at least `least` bytes."""
+    if ws is None or isinstance(ws, int):
+        return ws
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise DFlash2Error(fn, -5, "workspace must be contiguous and on the current device")
+    if ws.numel() * ws.element_size() < least:
+        raise DFlash2Error(fn, -5, f"workspace must have at least {least} bytes")
+    return ws.data_ptr()
+
+
 _LOGIT_TYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
@@ -391,7 +404,8 @@ def dflash2_sample(logits, temperature, top_k, top_p, min_p, u, token, prob=None
     return _check(fn, lib().dflash2_sample(
         code, n, vocab, logits.data_ptr(), stride, *_settings(fn, dev, n, temperature, top_k, top_p, min_p),
         _at(fn, "u", u, dev, torch.float32, (n,)), _at(fn, "token", token, dev, torch.int32, (n,)),
-        None if prob is None else _at(fn, "prob", prob, dev, torch.float32, (n,)), _ptr(workspace), _stream(stream)))
+        None if prob is None else _at(fn, "prob", prob, dev, torch.float32, (n,)),
+        _workspace(fn, workspace, dev, STATUS_BYTES), _stream(stream)))
 
 
 def dflash2_target_probs(logits, temperature, top_k, top_p, min_p, prob, workspace=None, stream=None):
@@ -403,7 +417,8 @@ def dflash2_target_probs(logits, temperature, top_k, top_p, min_p, prob, workspa
     return _check(fn, lib().dflash2_target_probs(
         code, batch, rows, vocab, logits.data_ptr(), stride,
         *_settings(fn, dev, batch, temperature, top_k, top_p, min_p),
-        _at(fn, "prob", prob, dev, torch.float32, logits.shape), _ptr(workspace), _stream(stream)))
+        _at(fn, "prob", prob, dev, torch.float32, logits.shape), _workspace(fn, workspace, dev, STATUS_BYTES),
+        _stream(stream)))
 
 
 def dflash2_verify_logits_workspace(batch, block_size):
@@ -419,8 +434,9 @@ def dflash2_verify_logits(path, n_draft, logits, temperature, top_k, top_p, min_
     dev, code, stride = _rows_of(fn, "logits", logits, 3)
     batch, B, vocab = logits.shape
     i32, f32, one, drafts = torch.int32, torch.float32, (batch,), (batch, B - 1)
-    if workspace is None or workspace.get_device() != dev:
+    if workspace is None:
         raise DFlash2Error(fn, -5, "workspace must be on the current device")
+    ws = _workspace(fn, workspace, dev)
     return _check(fn, lib().dflash2_verify_logits(
         code, batch, B, vocab, _at(fn, "path", path, dev, i32, drafts),
         None if n_draft is None else _at(fn, "n_draft", n_draft, dev, i32, one), logits.data_ptr(), stride,
@@ -430,7 +446,7 @@ def dflash2_verify_logits(path, n_draft, logits, temperature, top_k, top_p, min_
         _at(fn, "n_out", n_out, dev, i32, one), _at(fn, "next_anchor", next_anchor, dev, i32, one),
         None if seq_len is None else _at(fn, "seq_len", seq_len, dev, i32, one),
         None if counters is None else _at(fn, "counters", counters, dev, torch.int64, (4 + 2 * B - 1,)),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
+        ws, workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def dflash2_linear_w4(codes, scale, group, x, out, accumulate=False, stream=None):

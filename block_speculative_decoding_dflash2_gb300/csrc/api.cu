@@ -962,6 +962,7 @@ int dflash2_sample(int dtype, int rows, int vocab, const void* logits, int64_t s
                    float* prob, void* workspace, void* stream) {
   TRY(check_sampling(dtype, rows, 1, vocab, logits, stride));
   if (!u || !token) return DFLASH2_ERR_INVALID_ARG;
+  if ((uintptr_t)workspace % 4) return DFLASH2_ERR_WORKSPACE;
   Ctx ctx;
   TRY(device_ctx(&ctx, stream, workspace));
   SamplingArgs a = {};
@@ -988,6 +989,7 @@ int dflash2_target_probs(int dtype, int batch, int rows, int vocab, const void* 
                          float* prob, void* workspace, void* stream) {
   TRY(check_sampling(dtype, batch, rows, vocab, logits, stride));
   if (!prob) return DFLASH2_ERR_INVALID_ARG;
+  if ((uintptr_t)workspace % 4) return DFLASH2_ERR_WORKSPACE;
   Ctx ctx;
   TRY(device_ctx(&ctx, stream, workspace));
   SamplingArgs a = {};

@@ -504,7 +504,8 @@ int dflash2_verify_sampled(int batch, int block_size, int vocab, const int32_t *
  *   u          [rows] float, the draws
  *   token      [rows] int32 out
  *   prob       nullable [rows] float out, the drawn token's probability
- *   workspace  nullable: its status word only (the call needs no scratch)
+ *   workspace  nullable: its status word only (256 bytes, 4-byte aligned;
+ *              the call needs no scratch)
  */
 int dflash2_sample(int dtype, int rows, int vocab, const void *logits, int64_t stride,
                    const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
@@ -515,7 +516,8 @@ int dflash2_sample(int dtype, int rows, int vocab, const void *logits, int64_t s
  * dflash2_verify_sampled takes it (rows = block_size).  Row i of sequence s
  * is row s * rows + i of `logits`; the settings have one entry per sequence.
  *   prob       [batch, rows, vocab] float out
- *   workspace  nullable: its status word only (the call needs no scratch)
+ *   workspace  nullable: its status word only (256 bytes, 4-byte aligned;
+ *              the call needs no scratch)
  */
 int dflash2_target_probs(int dtype, int batch, int rows, int vocab, const void *logits, int64_t stride,
                          const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
