@@ -1507,7 +1507,9 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
       if (last) a.arrived[seq] = 0;
       __threadfence();
     }
-    if (__shfl_sync(0xffffffffu, last, 0)) join_rows(a, seq, nd);
+    last = __shfl_sync(0xffffffffu, last, 0);
+    __syncwarp();  // what lane 0 has seen, the warp has (a shuffle orders no memory)
+    if (last) join_rows(a, seq, nd);
   };
   if (empty) {
     if (rank == 0 && warp == 0) finish(-1, false);
