@@ -396,11 +396,11 @@ int launch_linear_w4(const W4Op& g, const Ctx& c) {
       (uintptr_t)g.out % (g.out_bf16 ? 2 : 4))
     return DFLASH2_ERR_INVALID_ARG;
   const int most = 1 << 20;  // rows of a launch (its tiles are counted in ints)
-  for (int n = 0; n < g.N; n += most) {
+  for (long long n = 0; n < g.N; n += most) {
     W4Op p = g;
-    p.x = static_cast<const bf16*>(g.x) + (size_t)n * g.ldx;
-    p.N = std::min(most, g.N - n);
-    p.out = static_cast<char*>(g.out) + (size_t)n * g.ldo * (g.out_bf16 ? 2 : 4);
+    p.x = static_cast<const bf16*>(g.x) + n * g.ldx;
+    p.N = (int)std::min<long long>(most, g.N - n);
+    p.out = static_cast<char*>(g.out) + n * g.ldo * (g.out_bf16 ? 2 : 4);
     if (p.N > 16) {
       const int rc = launch_linear_w4_tc(p, c);
       if (rc != DFLASH2_OK) return rc;
