@@ -51,7 +51,7 @@ struct Args {
   int split;                // CTAs of a cluster
   const bf16* x;
   long long ldx;
-  int N;
+  int N;  // up to 8 NT
   void* out;
   long long ldo;
   int accumulate;
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) linear_w4_kernel(Args a) {
   pdl_launch_next();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int rank = blockIdx.x % a.split, n0 = blockIdx.y * (NT * 8);
+  const int rank = blockIdx.x % a.split;
   const int c_begin = min(a.chunks, rank * a.slice), c_end = min(a.chunks, c_begin + a.slice);
   const bool once = c_end - c_begin <= a.window;  // the activations stay for every row block
 
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) linear_w4_kernel(Args a) {
       const int word = kb >> 2, tt = kb & 3;
       const int k = (c0 + c) * CK + word_k<G>(word, tt);
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (n0 + n < a.N && k < a.K) v = __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)(n0 + n) * a.ldx + k));
+      if (n < a.N && k < a.K) v = __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)n * a.ldx + k));
       const uint4 o = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
                                  __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
       xs[((c * 4 + word) * NT + (n >> 3)) * 32 + (n & 7) * 4 + tt] = o;
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) linear_w4_kernel(Args a) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) put(n0 + j * 8 + 2 * t + (e & 1), m0 + 16 * k + 8 * (e >> 1), acc[k][j][e]);
+          for (int e = 0; e < 4; ++e) put(j * 8 + 2 * t + (e & 1), m0 + 16 * k + 8 * (e >> 1), acc[k][j][e]);
     } else {
 #pragma unroll
       for (int k = 0; k < MT; ++k)
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(WARPS * 32, 2) linear_w4_kernel(Args a) {
           const float4 v = ld_dsmem4(dsmem_addr(part + i * 4, r));
           s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
         }
-        const int n = n0 + i * 4 / RB, m = blk * RB + i * 4 % RB;
+        const int n = i * 4 / RB, m = blk * RB + i * 4 % RB;
         put(n, m, s.x), put(n, m + 1, s.y), put(n, m + 2, s.z), put(n, m + 3, s.w);
       }
       cluster_sync();  // every partial sum has been read
@@ -354,7 +354,7 @@ int split_of(int blocks, int chunks, int nsm) {
 template <int G, int NT, int MT, typename OutT>
 int launch(Args a, int split, const Ctx& c) {
   constexpr int RB = WARPS * MT * 16, per_chunk = NT * 8 * CK * 2, fit = XS_MAX / per_chunk;
-  const int nb = (a.N + NT * 8 - 1) / (NT * 8), wave = wave_of<G, NT, MT, OutT>(split, c.nsm);
+  const int wave = wave_of<G, NT, MT, OutT>(split, c.nsm);
   if (wave < 1) return DFLASH2_ERR_CUDA;
   a.blocks = (a.M + RB - 1) / RB;
   a.split = split;
@@ -363,7 +363,7 @@ int launch(Args a, int split, const Ctx& c) {
   const size_t smem = (size_t)a.window * per_chunk + (size_t)NT * 8 * RB * 4;
   const int clusters = std::min(wave, a.blocks);
   auto kern = linear_w4_kernel<G, NT, MT, OutT>;
-  return launch_kx(kern, dim3(clusters * a.split, nb), dim3(WARPS * 32), smem, c, a.split, a);
+  return launch_kx(kern, dim3(clusters * a.split), dim3(WARPS * 32), smem, c, a.split, a);
 }
 
 // Blocks of 256 rows unless blocks of 128 fill more of a wave; for more than 8
