@@ -23,11 +23,13 @@
 // the inputs are split over a cluster of up to 8 CTAs, whose partial sums are
 // added in rank order through distributed shared memory.
 //
-// What bounds it: 151936 x 4096 for one row takes 55.5 us with groups of 128 (5.8
-// TB/s), where HBM needs 47; 69.5 and 111 with groups of 64 and 32, whose sums
+// What bounds it: 151936 x 4096 for one row takes 52 us with groups of 128 (6.2
+// TB/s), where HBM needs 47; 68 and 109 with groups of 64 and 32, whose sums
 // are scaled two and four times as often by the same 16 warps an SM (more do not
-// fit beside the weights in flight).  A small matrix takes its launch and two
-// trips to memory: 704 x 256 2.0 us.
+// fit beside the weights in flight); 54, 69 and 110 for 8 rows, 78, 98 and 138 for
+// 16.  At 8 rows with groups of 64 shared memory and L1 are busy 75% of their
+// cycles, DRAM 56%, and warps wait for loads most.  A small matrix takes its launch
+// and two trips to memory: 704 x 256 for one row 2.6 us.
 #include <algorithm>
 #include <atomic>
 
@@ -340,8 +342,8 @@ int wave_of(int split, int nsm) {
 // CTAs of a cluster: the most (up to 8) whose clusters hold every block in one
 // wave with at least four chunks a CTA, but enough for the activations to fit.
 // (Measured at 8 rows, groups of 128, us for splits of 1, 2, 4, 8: 6144 x 4096
-// 13.5, 11.2, 8.2, 10.9 (48 blocks of 128 rows); 4096 x 12288 44, 28, 15, 11
-// (32 blocks); 704 x 256 in 2 slices 3.3 against 2.6 in one.)
+// 13.3, 10.9, 7.6, 10.4 (48 blocks of 128 rows); 4096 x 12288 35, 34, 15, 10
+// (32 blocks); 704 x 256 in 2 slices 3.1 against 2.2 in one.)
 template <int G, int NT, int MT, typename OutT>
 int split_of(int blocks, int chunks, int nsm) {
   constexpr int fit = XS_MAX / (NT * 8 * CK * 2);

@@ -27,13 +27,16 @@
 // With few tiles the inputs are split over a cluster, whose partial tiles are
 // added in rank order through distributed shared memory.
 //
-// What bounds it: the CUDA cores beside the tensor core, 11 instructions for 8
-// weights and one for two sums.  24576 x 4096 for 1024 rows takes 173 us (1.20
-// PFLOP/s), 5120 x 17408 for 128 rows 26.9, the readout of 151936 x 4096 for 32
-// rows 85; groups of 64 and 32 double and quadruple the sums to scale (207 against
-// 137 us at 128 rows of that readout).  Timed copies of the kernel without the
-// conversion's arithmetic took 15% less, with an eighth of the products, without
-// the TMEM reads or without the activations' copies 0 to 2%.
+// What it takes: 24576 x 4096 for 1024 rows 180 us (1.15 PFLOP/s), 5120 x 17408
+// for 128 rows 27, the readout of 151936 x 4096 for 32, 64 and 128 rows 83, 103 and
+// 136; groups of 64 and 32 double and quadruple the sums to scale (205 us at 128
+// rows of that readout with 64).  What bounds it is known in part: it is not the
+// products, the TMEM reads or the activations' copies (timed copies of the kernel
+// with an eighth of the first, without the second or the third took 0 to 2% less),
+// and the conversion's arithmetic is 15%.  At 5120 x 17408 x 128 a CTA issues 122k
+// warp instructions, of which conversion (11 for 8 weights) and scaling (one for two
+// sums) are 44k; the rest are its roles' loads, stores, polls and barriers.  That
+// shape fills 120 of 152 SMs (40 tiles in clusters of 3).
 //
 // Every wait is bounded (1 s).  A wait that gives up records
 // DFLASH2_DEV_WAIT_TIMEOUT (where the call has a status word) and lets the other
@@ -466,7 +469,7 @@ __global__ void __launch_bounds__(Cfg<BN>::THREADS, 1)
         }
         tc_fence_after();
         const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN + set * COLS);
-        constexpr int W = BN == 128 ? 16 : 32;  // columns of a TMEM read (with 832 threads, 72 registers each)
+        constexpr int W = BN == 128 ? 16 : 32;  // columns of a TMEM read (with 896 threads, 72 registers each)
 #pragma unroll
         for (int j0 = 0; j0 < COLS; j0 += W) {
           uint32_t v[W];

@@ -35,11 +35,27 @@ constexpr int CAP = 2048;   // tokens of a list
 // Tokens of a list at a top-p border, whose masses (up to 2^42 each: any token's
 // at a very high temperature) are summed as 21 low bits and the rest, in 32 bits each.
 constexpr int TOPP_CAP = CAP - 1;
-constexpr int SMALL = 256;  // tokens of a list that is ranked instead of sorted
-constexpr int CMAX = 8;     // CTAs of a row's cluster
-constexpr int LOCAL_K = 100;  // largest top-k whose tokens each CTA picks on its own
-constexpr int PROBE_K = 16;   // tokens each CTA picks to try for a top-p border
-constexpr int PARTS = 1024;   // room for what they pick
+// Tokens of a list that is ranked (n^2 / 512 steps) instead of sorted.  With 128
+// in its place top-k 96 takes 21.8 us for a row of 151936 instead of 17.1, and
+// 29.3 for 64 rows instead of 23.3; the ranks' masses have room for 256.
+constexpr int SMALL = 256;
+constexpr int CMAX = 8;      // CTAs of a row's cluster
+constexpr int PARTS = 1024;  // room for what a row's CTAs pick on their own: 128 each at CMAX
+// Largest top-k whose tokens each CTA picks on its own: above 100 a peaked
+// row's picks, which are at least top-k, soon do not fit their 128, and the
+// histogram starts late.  Picked and by histogram, one row of 151936 takes (us)
+// 11.3 and 14.3 at top-k 20, 13.1 and 14.5 at 64, 17.1 and 15.3 at 96, 20.4 and
+// 15.6 at 120; 64 rows 16.7 and 23.5, 19.8 and 24.5, 23.2 and 25.8, 28.8 and 26.7.
+constexpr int LOCAL_K = 100;
+// Tokens each CTA picks to try for a top-p border alone, where a sample says that
+// what was picked may hold it (0.9 of the nucleus by that estimate, which allows
+// for the sample's error; trying always costs a flat row of 151936 59 us instead
+// of 47, without the 0.9 the peaked row at top-p 0.99 takes 43 instead of 53).  One
+// peaked row at top-p 0.9 takes 18.6 us with it and 31.1 without, 47 with 48 tokens
+// (the row's picks no longer fit a ranked list) and 17.8 with 8; 64 such rows 80,
+// 64, 48 and 103; a row whose nucleus is missed pays the try (0.99: 53 instead of
+// 37).
+constexpr int PROBE_K = 16;
 constexpr int SUB = NT;       // finer bins of a list
 constexpr int SLICE_BYTES = 19456 * 4;  // logits a CTA holds in shared memory, with two CTAs an SM
 constexpr unsigned KEY_NINF = 0x007fffffu;  // order of -inf; NaN maps to 0
@@ -103,6 +119,9 @@ __device__ __forceinline__ float2 pair_of(double x) {
 // cut into k/1024 + g + e with |g| <= 2^-11: 2^(-k/1024) is a product of two
 // table entries in whole numbers, and the rest, 1 - 2^-(g+e) = w - w^2/2 with w =
 // (g + e) ln 2 below 2^-11, is good to 2^-24 of itself in fp32: 2^-35 of the mass.
+// (A form good to 2^-37 takes 6% longer for 200 rows of 50257, 11% for 128 drawn
+// flat rows of 151936; a draw's number has 24 bits, and a border next to which
+// 2^-35 decides is met once in 10^5 rows of 150k tokens or less.)
 __device__ __forceinline__ float y_of(float z, const Scale& s) {
   return __fmul_rn(s.zmax - z, s.hi);  // never contracted: its rounding error is formed below
 }
@@ -155,7 +174,11 @@ __device__ __forceinline__ u64 mass_of(float z, const Scale& s, const ExpTab& ta
   return v[0];
 }
 
-// The same to fp32 accuracy relative to the mass, however small.
+// The same to fp32 accuracy relative to the mass, however small.  Only written
+// probabilities use it: two ulp of exp2f, one of the correction, then one of the
+// fp32 reciprocal of the row's mass and half a one of the product, up to 8e-8 of a
+// flat row's probabilities (rounded once from 64 bits they are off by 2.5e-8).
+// What is kept, drawn and accepted is decided on the whole masses.
 __device__ __forceinline__ float mass_f32(float z, const Scale& s) {
   if (z == s.zmax) return 1.f;
   if (s.odd) return s.zmax < INFINITY ? 1.f : 0.f;
@@ -572,10 +595,16 @@ __global__ void __launch_bounds__(128) join_kernel(SamplingArgs a) {
 //                    and one pass over all masses takes their tokens, the mass
 //                    ahead of them and the kept mass of each warp
 //   neither          the kept mass of each warp decides which one holds the draw
-// What bounds it: one row, the latency of those steps (151936 fp32 logits with
-// top-k 20 and top-p 0.95: 11.8 us; a nucleus over a flat row 45 us).  Many rows,
-// instructions per mass, about 40 (128 flat bf16 rows of 151936: 80 us drawn at a
-// temperature alone, 168 us from a nucleus, 12 us being their bytes at HBM speed).
+// What bounds it: one row with a small top-k, the latency of those steps (151936
+// fp32 logits with top-k 20 and top-p 0.95: 11.3 us); a nucleus over a flat row,
+// 47 us, is passes of 19k tokens by each of its 8 CTAs.  Many rows, instructions,
+// at 1.9 to 2.5 a cycle: 27 per token with top-k 20 (64 bf16 rows of 151936, 17
+// us), 82 at a temperature alone (128 such rows, 81 us; 113 for 200 fp32 rows of
+// 50257, 55 us), 161 for a nucleus (128 flat rows, 167 us; their bytes take 6 us at
+// the copy's rate).  A mass is about 40 of them; the others are the load with its
+// maximum, the histogram, the sums by warp and the lists.  Rows run in whole waves
+// (128 rows of 151936 in clusters of 4 are 512 CTAs on 304 places), each CTA its
+// steps one after the other.
 template <typename T, bool RES>
 __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice) {
   extern __shared__ uint4 zs_raw[];
@@ -1236,7 +1265,12 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
               int lo = sm.pick2, hi = lo;
               unsigned n = sm.hist[lo];
               bool up = true, down = true;
-              for (int d = 0; d < 32 && (up || down); ++d) {  // widen by turns, by 16 bins a side at most
+              // Widen by turns, by 16 bins a side at most, so that a guess that is
+              // a few bins off still holds the border (not at all: one flat row
+              // 43.6 us instead of 46.6, a peaked one whose border is in the
+              // tail 65 instead of 53; by 64: 53 again, and 64 rows of a steep
+              // distribution 107 instead of 95).
+              for (int d = 0; d < 32 && (up || down); ++d) {
                 bool& side = d & 1 ? up : down;
                 if (!side) continue;
                 const int b = d & 1 ? lo - 1 : hi + 1;
@@ -1248,6 +1282,8 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
               }
               sm.mk.lo = lo;
               sm.mk.hi = hi;
+              // (guesses corrected by exact masses: more than two were not seen to
+              // matter, times are the same with 2; 8 bounds them)
               sm.mk.step = n <= TOPP_CAP && tries < 8 ? STEP_TOPP : STEP_SLOW_P;
               sm.ncand = 0;
             }

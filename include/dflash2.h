@@ -483,7 +483,8 @@ int dflash2_verify_sampled(int batch, int block_size, int vocab, const int32_t *
  * first token alone: greedy.  Tokens whose logit is -inf or NaN have no mass
  * and are never kept; a row without any other token gives no token (-1) and
  * zeros, and records DFLASH2_DEV_EMPTY_ROW when a workspace is given.
- * Logits of +inf share the whole mass.
+ * Logits of +inf share the whole mass; in a row without any, T = +inf gives
+ * every token the same.
  *   dtype        DFLASH2_F32 or DFLASH2_BF16, the type of the logits
  *   vocab        1 .. DFLASH2_SAMPLING_MAX_VOCAB
  *   logits       rows of vocab values, the rows `stride` elements apart
@@ -494,7 +495,9 @@ int dflash2_verify_sampled(int batch, int block_size, int vocab, const int32_t *
  * Random numbers are inputs in [0, 1), so a call is deterministic.  A draw
  * with number u takes the first token, in id order, whose cumulative kept
  * mass exceeds u times the total.  Cuts and draws are decided on 64-bit whole
- * masses in units of 2^-42 of the largest one, each good to about 2^-35.
+ * masses in units of 2^-42 of the largest one, each good to about 2^-35 (for
+ * differences of logits within fp32's range; beyond it they count as
+ * infinite).
  */
 #define DFLASH2_SAMPLING_MAX_VOCAB 1048576
 
