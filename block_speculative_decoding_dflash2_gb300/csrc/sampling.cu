@@ -13,11 +13,15 @@
 // token (value, id).  T <= 0 keeps the first token alone.  Tokens at -inf or
 // NaN have no mass and are never kept.
 //
-// Masses are whole numbers: e_v in units of 2^-42, each good to about 2^-35 of
-// itself.  Their 64-bit sums are exact and do not depend on the order of the
-// additions, so draws and cuts are deterministic and sit within 2^-35 of the
-// exact ones; in plain fp32 a cut or a draw next to a border falls on the wrong
-// side about once in a thousand rows of a 150k vocabulary.
+// Masses are whole numbers: e_v in units of 2^-lg, lg as large as a bound of the
+// row's mass leaves room for in 62 bits (42 to 62), each good to about 2^-35 of
+// itself and a unit.  Their 64-bit sums are exact and do not depend on the order
+// of the additions, so draws and cuts are deterministic and sit within 2^-35 of
+// the exact ones; in plain fp32 a cut or a draw next to a border falls on the wrong
+// side about once in a thousand rows of a 150k vocabulary.  (Units of 2^-42 for
+// every row would do for a flat one.  But errors of equal tokens add up: of a row
+// with one token 14 above 150k equal ones, where a mass is 2^22 such units, 2 draws
+// in 1000 gave another token.)
 #include <atomic>
 
 #include "common.cuh"
@@ -32,29 +36,26 @@ typedef unsigned long long u64;
 constexpr int NT = 512, NW = NT / 32;
 constexpr int NB = 1024;    // bins of a row's histogram
 constexpr int CAP = 2048;   // tokens of a list
-// Tokens of a list at a top-p border, whose masses (up to 2^42 each: any token's
-// at a very high temperature) are summed as 21 low bits and the rest, in 32 bits each.
-constexpr int TOPP_CAP = CAP - 1;
 // Tokens of a list that is ranked (n^2 / 512 steps) instead of sorted.  With 128
-// in its place top-k 96 takes 21.8 us for a row of 151936 instead of 17.1, and
-// 29.3 for 64 rows instead of 23.3; the ranks' masses have room for 256.
+// in its place top-k 96 takes 21.3 us for a row of 151936 instead of 17.1, and
+// 29.1 for 64 rows instead of 23.3; the ranks' masses have room for 256.
 constexpr int SMALL = 256;
 constexpr int CMAX = 8;      // CTAs of a row's cluster
 constexpr int PARTS = 1024;  // room for what a row's CTAs pick on their own: 128 each at CMAX
 // Largest top-k whose tokens each CTA picks on its own: above 100 a peaked
 // row's picks, which are at least top-k, soon do not fit their 128, and the
 // histogram starts late.  Picked and by histogram, one row of 151936 takes (us)
-// 11.3 and 14.3 at top-k 20, 13.1 and 14.5 at 64, 17.1 and 15.3 at 96, 20.4 and
-// 15.6 at 120; 64 rows 16.7 and 23.5, 19.8 and 24.5, 23.2 and 25.8, 28.8 and 26.7.
+// 11.2 and 14.5 at top-k 20, 13.1 and 14.8 at 64, 17.1 and 15.5 at 96, 20.7 and
+// 15.9 at 120; 64 rows 16.9 and 24.1, 20.0 and 25.1, 23.3 and 26.2, 28.4 and 27.3.
 constexpr int LOCAL_K = 100;
 // Tokens each CTA picks to try for a top-p border alone, where a sample says that
 // what was picked may hold it (0.9 of the nucleus by that estimate, which allows
-// for the sample's error; trying always costs a flat row of 151936 59 us instead
-// of 47, without the 0.9 the peaked row at top-p 0.99 takes 43 instead of 53).  One
-// peaked row at top-p 0.9 takes 18.6 us with it and 31.1 without, 47 with 48 tokens
-// (the row's picks no longer fit a ranked list) and 17.8 with 8; 64 such rows 80,
-// 64, 48 and 103; a row whose nucleus is missed pays the try (0.99: 53 instead of
-// 37).
+// for the sample's error; trying always costs a flat row of 151936 60 us instead
+// of 48, without the 0.9 the peaked row at top-p 0.99 takes 47 instead of 59).  One
+// peaked row at top-p 0.9 takes 20.4 us with it and 34.4 without, 52 with 48 tokens
+// (the row's picks no longer fit a ranked list) and 19.7 with 8; 64 such rows 80,
+// 65, 49 and 107; a row whose nucleus is missed pays the try (0.99: 59 instead of
+// 41).
 constexpr int PROBE_K = 16;
 constexpr int SUB = NT;       // finer bins of a list
 constexpr int SLICE_BYTES = 19456 * 4;  // logits a CTA holds in shared memory, with two CTAs an SM
@@ -96,38 +97,41 @@ __device__ const ExpConst c_exp = {
      0x1.f9ccaep-1f, 0x1.f9751p-1f, 0x1.f91d8p-1f, 0x1.f8c6p-1f, 0x1.f86e9p-1f, 0x1.f8172ep-1f,
      0x1.f7bfdap-1f, 0x1.f76898p-1f, 0x1.f71164p-1f, 0x1.f6ba3ep-1f, 0x1.f66328p-1f, 0x1.f60c2p-1f,
      0x1.f5b528p-1f, 0x1.f55e4p-1f}};
-constexpr float FAR = 18.f;  // where the tables end
+constexpr float FAR = 40.f;  // from here on masses are plain fp32
 struct ExpTab {  // in shared memory
-  u64 pow32[(int)FAR * 32 + 1];  // 2^(-k/32) in units of 2^-42
-  uint2 pow1024[32];             // c_exp's drop, and its pow1024 as bits
+  u64 pow32[32];      // 2^(-k/32) in units of 2^-62
+  uint2 pow1024[32];  // c_exp's drop, and its pow1024 as bits
 };
 
-// The row's exponent scale log2(e) / T as a float pair.
+// The row's exponent scale log2(e) / T as a float pair, and the masses' unit.
 struct Scale {
   float zmax, hi, lo;
   bool odd;  // zmax or the temperature is infinite
+  int lg;    // masses are in units of 2^-lg
 };
+// 2^n as a float, n in -126..127.
+__device__ __forceinline__ float pow2f(int n) { return __int_as_float((127 + n) << 23); }
 // x as a float pair.
 __device__ __forceinline__ float2 pair_of(double x) {
   const float h = (float)x;
   return make_float2(h, (float)(x - (double)h));
 }
 
-// exp((z - zmax) / T) in units of 2^-42, for z > -inf.  From y = (zmax - z)
-// log2(e) / T = 18 on, plain fp32 is good to 2^-37 of the largest mass.  Before,
-// y is held as p + e (the difference exact by two-sum, the product by fma) and
+// exp((z - zmax) / T) in units of 2^-lg, for z > -inf.  y = (zmax - z) log2(e) / T
+// is held as p + e (the difference exact by two-sum, the product by fma) and
 // cut into k/1024 + g + e with |g| <= 2^-11: 2^(-k/1024) is a product of two
-// table entries in whole numbers, and the rest, 1 - 2^-(g+e) = w - w^2/2 with w =
-// (g + e) ln 2 below 2^-11, is good to 2^-24 of itself in fp32: 2^-35 of the mass.
-// (A form good to 2^-37 takes 6% longer for 200 rows of 50257, 11% for 128 drawn
-// flat rows of 151936; a draw's number has 24 bits, and a border next to which
-// 2^-35 decides is met once in 10^5 rows of 150k tokens or less.)
+// table entries in whole numbers and a shift, and the rest, 1 - 2^-(g+e) = w -
+// w^2/2 with w = (g + e) ln 2 below 2^-11, is good to 2^-24 of itself in fp32:
+// 2^-35 of the mass.  (A form good to 2^-37 takes about 10% longer; a draw's number
+// has 24 bits, and a border next to which 2^-35 decides is met once in 10^5 rows of
+// 150k tokens or less.)  From y = 40 on plain fp32 is good to 2^-58 of the largest
+// mass.
 __device__ __forceinline__ float y_of(float z, const Scale& s) {
   return __fmul_rn(s.zmax - z, s.hi);  // never contracted: its rounding error is formed below
 }
-__device__ __forceinline__ unsigned far_mass(float y) {  // 0 from y = 44 on, infinity and NaN included
+__device__ __forceinline__ unsigned far_mass(float y, int lg) {  // below 2^23; 0 from y = 64 on, infinity and NaN included
   float f;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(42.f - y));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"((float)lg - y));
   return __float2uint_rn(f);
 }
 // No branch depends on one value, so the N evaluations overlap; with VOTE, a
@@ -141,30 +145,30 @@ __device__ __forceinline__ void masses_of(const float (&z)[N], const float (&p)[
     const float dh = s.zmax - z[i], bb = dh - s.zmax;
     const float dl = (s.zmax - (dh - bb)) - (z[i] + bb);
     const float e = fmaf(dl, s.hi, fmaf(dh, s.lo, fmaf(dh, s.hi, -p[i])));
-    // 1.5 2^23: rounds to a whole number of 1024ths (of far values only kept within the tables)
+    // 1.5 2^23: rounds to a whole number of 1024ths (of far values only kept within the shift)
     const float kf = fmaf(fminf(p[i], FAR), 1024.f, 12582912.f);
     const unsigned k = __float_as_uint(kf) - 0x4b400000u;
     const float w = (fmaf(kf - 12582912.f, -0x1p-10f, p[i]) + e) * 0.693147182f;
     const float x = fmaf(-0.5f * w, w, w);
-    const u64 a = tab.pow32[k >> 5];
+    const u64 a = tab.pow32[k >> 5 & 31];
     const uint2 t = tab.pow1024[k & 31];
-    const unsigned a11 = (unsigned)((a + 1024) >> 11);
-    u64 b = a - ((u64)a11 * t.x >> 26);  // 2^(-k/1024)
-    const float bf = (float)a11 * __uint_as_float(t.y);  // the same in units of 2^-31
-    asm("mad.wide.s32 %0, %1, -1, %0;" : "+l"(b) : "r"(__float2int_rn(bf * x * 2048.f)));
-    v[i] = b;
+    const unsigned a31 = (unsigned)(a >> 31);
+    u64 b = a - ((u64)a31 * t.x >> 6);  // 2^(-(k mod 1024)/1024) in units of 2^-62
+    const float bf = (float)a31 * __uint_as_float(t.y);  // the same in units of 2^-31
+    asm("mad.wide.s32 %0, %1, -1048576, %0;" : "+l"(b) : "r"(__float2int_rn(bf * x * 2048.f)));
+    v[i] = b >> ((k >> 10) + (62 - s.lg));
     far = far || !(p[i] < FAR);
   }
   if (!VOTE || __any_sync(0xffffffffu, far)) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (!(p[i] < FAR)) v[i] = far_mass(p[i]);
+      if (!(p[i] < FAR)) v[i] = far_mass(p[i], s.lg);
   }
   // (a difference or a product without a value: an infinite maximum, which
   // shares the mass with its equals alone, or T = infinity)
   if (s.odd) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = z[i] == s.zmax || s.zmax < INFINITY ? 1ull << 42 : 0ull;
+    for (int i = 0; i < N; ++i) v[i] = z[i] == s.zmax || s.zmax < INFINITY ? 1ull << s.lg : 0ull;
   }
 }
 __device__ __forceinline__ u64 mass_of(float z, const Scale& s, const ExpTab& tab) {
@@ -269,7 +273,7 @@ __device__ __forceinline__ bool masses4(const float4& v, int id, const Scale& s,
   }
   if (!__any_sync(0xffffffffu, near)) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) e[j] = keep[j] ? far_mass(y[j]) : 0u;
+    for (int j = 0; j < 4; ++j) e[j] = keep[j] ? far_mass(y[j], s.lg) : 0u;
     return false;
   }
   masses_of<4, true>(z, y, s, tab, e);
@@ -299,16 +303,16 @@ struct Smem {
     u64 parts[PARTS];  // what each CTA picked on its own, for a small top-k
     struct {
       float ecum[NB + 1];                 // estimated mass ahead of each bin
-      unsigned sub_lo[SUB], sub_hi[SUB];  // masses of a list's finer bins: the low 21 bits, the rest
+      unsigned sub[3][SUB];  // masses of a list's finer bins, 21 bits in each
     };
   };
   u64 wsum[NW], wsum2[NW];
   u64 wkept[NW];  // mass each warp's slice keeps of the bins that hold the top-p border
   u64 xm[2][CMAX], xg[2][CMAX];  // exchanged masses, two turns
-  float xmax[CMAX], xmin[CMAX], xlow[CMAX];
+  float xmax[CMAX], xmin[CMAX], xlow[CMAX], xub[CMAX];
   float2 xest[CMAX];
   int xid[CMAX];
-  float fsum[NW], fmin[NW];
+  float fsum[NW], fmin[NW], fub[NW];
   float2 c_pair, off_pair;  // log2(e) / T and T ln(min_p)
   Decision mk;      // first CTA: the next decision
   Decision dec[2];  // the last one received, two turns
@@ -323,6 +327,17 @@ struct Smem {
   u64 sel_before;
   int pick, pick2;
 };
+
+// Adds a mass to bin b of a list's finer bins (2048 masses of 62 bits at most: no
+// part overflows), and reads one.
+__device__ __forceinline__ void sub_add(Smem& sm, int b, u64 e) {
+  atomicAdd(&sm.sub[0][b], (unsigned)e & 0x1fffffu);
+  atomicAdd(&sm.sub[1][b], (unsigned)(e >> 21) & 0x1fffffu);
+  atomicAdd(&sm.sub[2][b], (unsigned)(e >> 42));
+}
+__device__ __forceinline__ u64 sub_get(const Smem& sm, int b) {
+  return ((u64)sm.sub[2][b] << 42) + ((u64)sm.sub[1][b] << 21) + sm.sub[0][b];
+}
 
 // Sum over the threads before this one (and the block's total).
 __device__ __forceinline__ u64 block_scan_u64(u64 mine, u64* total, Smem& sm) {
@@ -596,12 +611,12 @@ __global__ void __launch_bounds__(128) join_kernel(SamplingArgs a) {
 //                    ahead of them and the kept mass of each warp
 //   neither          the kept mass of each warp decides which one holds the draw
 // What bounds it: one row with a small top-k, the latency of those steps (151936
-// fp32 logits with top-k 20 and top-p 0.95: 11.3 us); a nucleus over a flat row,
-// 47 us, is passes of 19k tokens by each of its 8 CTAs.  Many rows, instructions,
-// at 1.9 to 2.5 a cycle: 27 per token with top-k 20 (64 bf16 rows of 151936, 17
-// us), 82 at a temperature alone (128 such rows, 81 us; 113 for 200 fp32 rows of
-// 50257, 55 us), 161 for a nucleus (128 flat rows, 167 us; their bytes take 6 us at
-// the copy's rate).  A mass is about 40 of them; the others are the load with its
+// fp32 logits with top-k 20 and top-p 0.95: 11.2 us); a nucleus over a flat row,
+// 48 us, is passes of 19k tokens by each of its 8 CTAs.  Many rows, instructions,
+// at 1.8 to 2.5 a cycle: 27 per token with top-k 20 (64 bf16 rows of 151936, 17
+// us), 85 at a temperature alone (128 such rows, 84 us; 118 for 200 fp32 rows of
+// 50257, 58 us), 164 for a nucleus (128 flat rows, 171 us; their bytes take 6 us at
+// the copy's rate).  A mass is about 45 of them; the others are the load with its
 // maximum, the histogram, the sums by warp and the lists.  Rows run in whole waves
 // (128 rows of 151936 in clusters of 4 are 512 CTAs on 304 places), each CTA its
 // steps one after the other.
@@ -693,9 +708,10 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     for_each(s, [&](float z, int) { see(z); });
   }
   for (int b = tid; b < NB; b += NT) sm.hist[b] = 0;
-  for (int n = warp; n <= (int)FAR; n += NW)
-    if (n < (int)FAR || lane == 0) sm.tab.pow32[n * 32 + lane] = n ? (pow32 + (1ull << (n - 1))) >> n : pow32;
-  if (warp == 0) sm.tab.pow1024[lane] = pow1024;
+  if (warp == 0) {
+    sm.tab.pow32[lane] = pow32 << 20;
+    sm.tab.pow1024[lane] = pow1024;
+  }
   if (tid == 0) {
     sm.ncand = sm.nlocal = 0;
     sm.pick = -1;
@@ -714,6 +730,19 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     mn = fminf(mn, sm.fmin[w]);
   }
   float zmax = -INFINITY, zmin = INFINITY;
+  // The mass of this thread's logits, relative to the CTA's largest, is at most
+  // their number times that of the largest of them.
+  auto bound = [&]() {
+    const float per_thread = (float)((s.groups / (VEC / 4) + NT - 1) / NT * VEC);
+    float ub = thread_max == mx ? 1.f : exp2f((thread_max - mx) * sm.c_pair.x);
+    ub = warp_sum(thread_max > -INFINITY ? ub * per_thread : 0.f);
+    if (lane == 0) sm.fub[warp] = ub;
+  };
+  auto tell_bound = [&]() {  // (by threads below C, after a barrier)
+    float ub = 0.f;
+    for (int w = 0; w < NW; ++w) ub += sm.fub[w];
+    st_cl(dsmem_addr(&sm.xub[rank], tid), __float_as_uint(ub));
+  };
   // A small top-k: each CTA picks its own candidates.  The k-th largest of its
   // threads' largest logits has at least k logits that are not below it, so no
   // token of the row's top k lies below it; few others do not.
@@ -765,6 +794,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
         sm.fsum[warp] = picked;
         sm.fmin[warp] = others;
       }
+      bound();
       __syncthreads();
     }
     if (tid < C) {
@@ -776,6 +806,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
         for (int w = 0; w < NW; ++w) x += sm.fsum[w], y += sm.fmin[w];
         st_cl(dsmem_addr(&sm.xest[rank].x, tid), __float_as_uint(x));
         st_cl(dsmem_addr(&sm.xest[rank].y, tid), __float_as_uint(y));
+        tell_bound();
       }
     }
     cluster_sync();
@@ -801,9 +832,12 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
       sm.ncand = 0;
       sm.pick = -1;
     }
+    bound();
+    __syncthreads();
     if (tid < C) {
       st_cl(dsmem_addr(&sm.xmax[rank], tid), __float_as_uint(mx));
       st_cl(dsmem_addr(&sm.xmin[rank], tid), __float_as_uint(mn));
+      tell_bound();
     }
     cluster_sync();
     for (int r = 0; r < C; ++r) {
@@ -812,8 +846,21 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     }
   };
   if (!local) full_range();
-  const Scale sc = {zmax, sm.c_pair.x, sm.c_pair.y, zmax == INFINITY || sm.c_pair.x == 0.f};
   const bool empty = !(zmax > -INFINITY);
+  const bool odd = zmax == INFINITY || sm.c_pair.x == 0.f;
+  // The unit of the masses: 2^lg times the bound is at most 2^62 (a vocabulary is
+  // at most 2^20, and so is what a small top-k's lists hold, 2^10).
+  int lg = 42;
+  if (local && by_k0) {
+    static_assert(PARTS == 1 << 10, "tokens of such a list");
+    lg = 52;
+  } else if (!odd && !empty) {
+    float ub = 0.f;
+    for (int r = 0; r < C; ++r)
+      ub += sm.xub[r] * (sm.xmax[r] == zmax ? 1.f : exp2f((sm.xmax[r] - zmax) * sm.c_pair.x));
+    lg = min(max(61 - (int)(__float_as_uint(ub * 1.001f) >> 23) + 127, 42), 62);
+  }
+  const Scale sc = {zmax, sm.c_pair.x, sm.c_pair.y, odd, lg};
 
   Cut cut = {KEY_NINF + 1, V};  // everything above -inf
   u64 total = 0;                // mass of the cut, when known
@@ -903,7 +950,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     id0 = 0x7fffffff;
     for (int r = 0; r < C; ++r) id0 = min(id0, sm.xid[r]);
     cut = {okey(zmax), id0};
-    total = 1ull << 42;
+    total = 1ull << lg;
   }
 
   // ---- 2. top-k and top-p: a histogram of the row's range finds the bins that
@@ -1267,14 +1314,14 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
               bool up = true, down = true;
               // Widen by turns, by 16 bins a side at most, so that a guess that is
               // a few bins off still holds the border (not at all: one flat row
-              // 43.6 us instead of 46.6, a peaked one whose border is in the
-              // tail 65 instead of 53; by 64: 53 again, and 64 rows of a steep
-              // distribution 107 instead of 95).
+              // 44.6 us instead of 48.0, a peaked one whose border is in the
+              // tail 73 instead of 59; by 64: 59 again, and 64 rows of a steep
+              // distribution 106 instead of 95).
               for (int d = 0; d < 32 && (up || down); ++d) {
                 bool& side = d & 1 ? up : down;
                 if (!side) continue;
                 const int b = d & 1 ? lo - 1 : hi + 1;
-                side = b >= lo_least && b <= hi_most && n + sm.hist[b] <= TOPP_CAP;
+                side = b >= lo_least && b <= hi_most && n + sm.hist[b] <= CAP;
                 if (!side) continue;
                 n += sm.hist[b];
                 lo = min(lo, b);
@@ -1284,7 +1331,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
               sm.mk.hi = hi;
               // (guesses corrected by exact masses: more than two were not seen to
               // matter, times are the same with 2; 8 bounds them)
-              sm.mk.step = n <= TOPP_CAP && tries < 8 ? STEP_TOPP : STEP_SLOW_P;
+              sm.mk.step = n <= CAP && tries < 8 ? STEP_TOPP : STEP_SLOW_P;
               sm.ncand = 0;
             }
           }
@@ -1340,20 +1387,16 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
                 // finer bins find the border's few tokens; the rest is not needed
                 const float top = zmax - (float)lo / per, fine = (float)SUB / ((float)(hi + 1 - lo) / per);
                 int sb[CAP / NT];
-                sm.sub_lo[tid] = sm.sub_hi[tid] = 0;
+                sm.sub[0][tid] = sm.sub[1][tid] = sm.sub[2][tid] = 0;
                 __syncthreads();
 #pragma unroll
                 for (int j = 0; j < CAP / NT; ++j) {
                   const float z = okey_value((unsigned)(v[j] >> 32));
                   sb[j] = (int)fminf(fmaxf((top - z) * fine, 0.f), (float)(SUB - 1));
-                  if (v[j]) {
-                    const u64 e2 = mass_of(z, sc, sm.tab);
-                    atomicAdd(&sm.sub_lo[sb[j]], (unsigned)e2 & 0x1fffffu);
-                    atomicAdd(&sm.sub_hi[sb[j]], (unsigned)(e2 >> 21));
-                  }
+                  if (v[j]) sub_add(sm, sb[j], mass_of(z, sc, sm.tab));
                 }
                 __syncthreads();
-                const u64 mine = ((u64)sm.sub_hi[tid] << 21) + sm.sub_lo[tid];
+                const u64 mine = sub_get(sm, tid);
                 const u64 before = block_scan_u64(mine, &lall, sm);
                 if (g + before < want && want <= g + before + mine) {
                   sm.pick2 = tid;
@@ -1403,29 +1446,23 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
                 if (lo > 0 && a.kind != SAMPLING_PROBS) {
                   // what each warp of the cluster keeps of these bins
                   __syncthreads();
-                  if (tid < CMAX * NW) sm.sub_lo[tid] = sm.sub_hi[tid] = 0;
+                  if (tid < CMAX * NW) sm.sub[0][tid] = sm.sub[1][tid] = sm.sub[2][tid] = 0;
                   __syncthreads();
 #pragma unroll
                   for (int j = 0; j < CAP / NT; ++j) {
                     const unsigned key = (unsigned)(v[j] >> 32);
                     const int id = (int)~(unsigned)v[j];
-                    if (v[j] && kept(key, id, cut)) {
-                      const int w = warp_of(id);
-                      const u64 e = mass_of(okey_value(key), sc, sm.tab);
-                      atomicAdd(&sm.sub_lo[w], (unsigned)e & 0x1fffffu);
-                      atomicAdd(&sm.sub_hi[w], (unsigned)(e >> 21));
-                    }
+                    if (v[j] && kept(key, id, cut)) sub_add(sm, warp_of(id), mass_of(okey_value(key), sc, sm.tab));
                   }
                   __syncthreads();
-                  if (tid < C * NW)
-                    st_cl(dsmem_addr(&sm.wkept[tid % NW], tid / NW), ((u64)sm.sub_hi[tid] << 21) + sm.sub_lo[tid]);
+                  if (tid < C * NW) st_cl(dsmem_addr(&sm.wkept[tid % NW], tid / NW), sub_get(sm, tid));
                 }
               } else {
                 cut = given;  // not the list's
                 const bool later = want > g;
                 const u64 at = later ? g + lall : g;
                 want_f = sm.ecum[later ? hi + 1 : lo] +
-                         (float)((long long)want - (long long)at) * (1.f / 4398046511104.f);
+                         (float)((long long)want - (long long)at) * pow2f(-lg);
                 if (later) lo_least = hi + 1;
                 else hi_most = lo - 1;
                 slow = lo_least > hi_most;
@@ -1503,7 +1540,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
     }
     float* p = a.prob + (size_t)row * V;
     const float zc = okey_value(cut.key);
-    const float inv = empty ? 0.f : 4398046511104.f / (float)total;
+    const float inv = empty ? 0.f : pow2f(lg) / (float)total;
     for (int q = tid; q < 4 * s.groups; q += NT) {
       const int id = s.first + q;
       if (id < s.begin || id >= s.end) continue;
@@ -1527,7 +1564,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(SamplingArgs a, int slice
       if (lane == 0) {
         a.token[row] = token;
         if (a.prob)
-          a.prob[row] = token < 0 ? 0.f : mass_f32(ld(z_row + token), sc) * 4398046511104.f / (float)total;
+          a.prob[row] = token < 0 ? 0.f : mass_f32(ld(z_row + token), sc) * pow2f(lg) / (float)total;
       }
       return;
     }

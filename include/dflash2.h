@@ -495,7 +495,7 @@ int dflash2_verify_sampled(int batch, int block_size, int vocab, const int32_t *
  * Random numbers are inputs in [0, 1), so a call is deterministic.  A draw
  * with number u takes the first token, in id order, whose cumulative kept
  * mass exceeds u times the total.  Cuts and draws are decided on 64-bit whole
- * masses in units of 2^-42 of the largest one, each good to about 2^-35 (for
+ * masses, each good to about 2^-35 of itself and 2^-52 of the row's mass (for
  * differences of logits within fp32's range; beyond it they count as
  * infinite).
  */
