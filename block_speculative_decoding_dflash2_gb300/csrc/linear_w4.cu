@@ -29,7 +29,7 @@
 // fit beside the weights in flight); 54, 69 and 110 for 8 rows, 78, 98 and 138 for
 // 16.  At 8 rows with groups of 64 shared memory and L1 are busy 75% of their
 // cycles, DRAM 56%, and warps wait for loads most.  A small matrix takes its launch
-// and two trips to memory: 704 x 256 for one row 2.6 us.
+// and two trips to memory: 704 x 256 for one row 2.7 us.
 #include <algorithm>
 #include <atomic>
 
