@@ -340,7 +340,7 @@ int check_weights(const dflash2_config& c, const dflash2_weights* w) {
   }
   if (c.dtype == DFLASH2_W4) {
     const dflash2_scales* s = w->scales;
-    bool ok = w4_aligned(w->lm_head, s->lm_head) && w4_aligned(w->fc, s->fc) && w4_aligned(w->sel, s->sel);
+    bool ok = aligned16(w->embed) && w4_aligned(w->lm_head, s->lm_head) && w4_aligned(w->fc, s->fc) && w4_aligned(w->sel, s->sel);
     for (int l = 0; l < c.n_layers; ++l) {
       const dflash2_layer_weights& L = w->layers[l];
       const dflash2_layer_scales& S = s->layers[l];
@@ -807,7 +807,8 @@ int dflash2_select_path_ex(const dflash2_config* cfg, const dflash2_weights* w, 
   if (!workspace) return DFLASH2_ERR_WORKSPACE;
   if ((cfg->dtype == DFLASH2_FP8W || cfg->dtype == DFLASH2_W4) && (!w->scales || !w->scales->sel))
     return DFLASH2_ERR_INVALID_ARG;
-  if (cfg->dtype == DFLASH2_W4 && !w4_aligned(w->sel, w->scales->sel)) return DFLASH2_ERR_INVALID_ARG;
+  if (cfg->dtype == DFLASH2_W4 && !(w4_aligned(w->sel, w->scales->sel) && aligned16(w->embed)))
+    return DFLASH2_ERR_INVALID_ARG;
   TRY(check_w4_inputs(*cfg, 0, nullptr, workspace));
   const dflash2_config c = act_config(*cfg);
   const Scales sc = scales_of(*cfg, *w);

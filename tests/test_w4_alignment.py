@@ -59,6 +59,11 @@ def test_misaligned_weights_are_refused(B, name, off):
     assert draft(B, w) == -1 and append(B, w) == -1
 
 
+def test_a_misaligned_embedding_is_refused(B):
+    w = weights(B, config(B).n_layers, embed=8)
+    assert draft(B, w) == -1 and append(B, w) == -1
+
+
 @pytest.mark.parametrize("off", [2, 4, 8])
 def test_misaligned_taps_and_workspaces_are_refused(B, off):
     w = weights(B, config(B).n_layers)
@@ -72,9 +77,8 @@ def test_misaligned_selector_weights_are_refused(B, name, off):
     c = config(B)
     w = weights(B, c.n_layers, **{name: off})
     assert B.lib().dflash2_build_selector_table(ctypes.byref(c), ctypes.byref(w.struct), P, None) == -1
-    if name != "embed":
-        assert B.lib().dflash2_select_path(ctypes.byref(c), ctypes.byref(w.struct), 2, P, P, P, P, None, P, 1 << 40,
-                                           None) == -1
+    assert B.lib().dflash2_select_path(ctypes.byref(c), ctypes.byref(w.struct), 2, P, P, P, P, None, P, 1 << 40,
+                                       None) == -1
     w = weights(B, c.n_layers)
     assert B.lib().dflash2_select_path(ctypes.byref(c), ctypes.byref(w.struct), 2, P, P, P, P, None, P + 8, 1 << 40,
                                        None) == -5
