@@ -20,6 +20,7 @@ BF16 = 1
 FP8W = 2
 W4 = 3
 W4_GROUP = 64
+E4M3 = 4
 STATUS_BYTES = 256  # of a workspace that only its status word is used of
 
 STATUS = {0: "ok", -1: "invalid argument", -2: "shape", -3: "block size", -4: "dtype",
@@ -69,6 +70,11 @@ class Scales(ctypes.Structure):
 class Weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in _TOP_FIELDS] + [("layers", ctypes.POINTER(LayerWeights)),
                                                               ("scales", ctypes.POINTER(Scales))]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("dtype", "n_pages", "page_size", "n_kv_heads", "head_dim")] + \
+        [(n, ctypes.c_void_p) for n in ("k", "v", "k_exp", "v_exp")]
 
 
 _lib = None
@@ -171,6 +177,17 @@ def lib():
         L.dflash2_verify_logits.argtypes = [I, I, I, I, P, P, P, I64] + [P] * 13 + [S, P]
         L.dflash2_linear_w4.restype = I
         L.dflash2_linear_w4.argtypes = [P, P, I, I, I, P, I64, I, P, I64, I, I, P]
+        C = F(Cache)
+        L.dflash2_cache_append.restype = I
+        L.dflash2_cache_append.argtypes = [C, P, I, I, P, I, P, I64, P, I64, P, P, P]
+        L.dflash2_cache_read.restype = I
+        L.dflash2_cache_read.argtypes = [C, P, I, I, P, I, P, P, I64, P, I64, P, P]
+        L.dflash2_attend_workspace.restype = S
+        L.dflash2_attend_workspace.argtypes = [C, I, I, I, I]
+        L.dflash2_attend.restype = I
+        L.dflash2_attend.argtypes = [C, P, I, I, I, P, P, I, P, I64, P, I64, ctypes.c_float, I, I, I, P, S, P]
+        L.dflash2_adjust_logits.restype = I
+        L.dflash2_adjust_logits.argtypes = [I, I, I, I, P, I64, P, I] + [P] * 8 + [I, P, P, I64, P, P]
         L.dflash2_launch_count.restype = ctypes.c_int64
         L.dflash2_set_stage_events.restype = None
         L.dflash2_set_stage_events.argtypes = [P]
@@ -466,6 +483,145 @@ def dflash2_linear_w4(codes, scale, group, x, out, accumulate=False, stream=None
         _at(fn, "codes", codes, dev, torch.uint8, (m, k // 2)),
         _at(fn, "scale", scale, dev, torch.bfloat16, (m, k // group)), group, m, k, x.data_ptr(), x_stride, n,
         out.data_ptr(), out_stride, code, int(accumulate), _stream(stream)))
+
+
+class PagedCache:
+    """One layer of a paged cache (dflash2_cache) over torch device tensors,
+    kept alive here: k, v [n_pages, page_size, n_kv_heads, head_dim] bfloat16,
+    or float8_e4m3fn with the exponent bytes k_exp, v_exp [n_pages, page_size,
+    n_kv_heads] uint8."""
+
+    def __init__(self, k, v, k_exp=None, v_exp=None):
+        fn = "PagedCache"
+        code = {torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3}.get(k.dtype)
+        if code is None or v.dtype is not k.dtype:
+            raise DFlash2Error(fn, -4, "k and v must both be bfloat16 or float8_e4m3fn")
+        if k.dim() != 4 or v.shape != k.shape or not k.is_contiguous() or not v.is_contiguous():
+            raise DFlash2Error(fn, -2, "k and v must be contiguous, of one shape [pages, page size, heads, head width]")
+        self.device = k.get_device()
+        if self.device < 0 or v.get_device() != self.device:
+            raise DFlash2Error(fn, -1, "k and v must be on one CUDA device")
+        if (k_exp is None) != (code == BF16) or (v_exp is None) != (code == BF16):
+            raise DFlash2Error(fn, -1, "k_exp and v_exp go with float8_e4m3fn, and only with it")
+        if code == E4M3:
+            for name, t in (("k_exp", k_exp), ("v_exp", v_exp)):
+                _at(fn, name, t, self.device, torch.uint8, k.shape[:3])
+        self.tensors = (k, v, k_exp, v_exp)
+        self.heads, self.width = k.shape[2:]
+        self.struct = Cache(code, *k.shape, _ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp))
+
+    def at(self, fn):
+        """The struct's reference, on the current device only."""
+        if self.device != torch.cuda.current_device():
+            raise DFlash2Error(fn, -1, "the cache must be on the current device")
+        return ctypes.byref(self.struct)
+
+
+def _tokens_of(fn, name, t, dev, shape):
+    """(address, distance of the tokens) of a bfloat16 [..., heads, width]
+    tensor whose tokens are evenly spaced and contiguous in themselves."""
+    if t is None or t.get_device() != dev or t.dtype is not torch.bfloat16 or t.shape != shape:
+        _refuse(fn, name, t, dev, torch.bfloat16, shape)
+    st, n = t.stride(), len(shape)
+    if t.numel() and ((st[-1] != 1 and shape[-1] > 1) or (st[-2] != shape[-1] and shape[-2] > 1)):
+        raise DFlash2Error(fn, -2, f"a token of {name} must be contiguous")
+    row = shape[-1] * shape[-2]
+    if shape[n - 3] > 1:
+        row = st[n - 3]
+    elif n == 4 and shape[0] > 1:
+        row = st[0]
+    if n == 4 and shape[0] > 1 and shape[1] > 1 and st[0] != shape[1] * row:
+        raise DFlash2Error(fn, -2, f"the tokens of {name} must be evenly spaced")
+    return t.data_ptr(), row
+
+
+def _table(fn, t, dev):
+    """(address, max_pages, batch) of a block table."""
+    if t is None or t.dim() != 2:
+        _refuse(fn, "block_table", t, dev, torch.int32, ("batch", "max_pages"))
+    return _at(fn, "block_table", t, dev, torch.int32, t.shape), t.shape[1], t.shape[0]
+
+
+def dflash2_cache_append(cache, block_table, ctx_len, k, v, new_off, workspace=None, stream=None):
+    """k, v: [n_new, n_kv_heads, head_dim] bfloat16, rows evenly spaced;
+    ctx_len: [batch], new_off: [batch + 1] int32."""
+    fn, dev = "dflash2_cache_append", cache.device
+    ref = cache.at(fn)
+    table, max_pages, batch = _table(fn, block_table, dev)
+    n = 0 if k is None else k.shape[0]
+    shape = (n, cache.heads, cache.width)
+    (kp, ks), (vp, vs) = _tokens_of(fn, "k", k, dev, shape), _tokens_of(fn, "v", v, dev, shape)
+    return _check(fn, lib().dflash2_cache_append(
+        ref, table, max_pages, batch, _at(fn, "ctx_len", ctx_len, dev, torch.int32, (batch,)), n, kp, ks, vp, vs,
+        _at(fn, "new_off", new_off, dev, torch.int32, (batch + 1,)), _workspace(fn, workspace, dev, STATUS_BYTES),
+        _stream(stream)))
+
+
+def dflash2_cache_read(cache, block_table, start, off, k, v, workspace=None, stream=None):
+    """k, v: [n_rows, n_kv_heads, head_dim] bfloat16 out, rows evenly spaced;
+    start: [batch] or None, off: [batch + 1] int32."""
+    fn, dev = "dflash2_cache_read", cache.device
+    ref = cache.at(fn)
+    table, max_pages, batch = _table(fn, block_table, dev)
+    n = 0 if k is None else k.shape[0]
+    shape = (n, cache.heads, cache.width)
+    (kp, ks), (vp, vs) = _tokens_of(fn, "k", k, dev, shape), _tokens_of(fn, "v", v, dev, shape)
+    return _check(fn, lib().dflash2_cache_read(
+        ref, table, max_pages, batch, None if start is None else _at(fn, "start", start, dev, torch.int32, (batch,)), n,
+        _at(fn, "off", off, dev, torch.int32, (batch + 1,)), kp, ks, vp, vs,
+        _workspace(fn, workspace, dev, STATUS_BYTES), _stream(stream)))
+
+
+def dflash2_attend_workspace(cache, batch, n_tok, n_q_heads, shared_len=0):
+    return lib().dflash2_attend_workspace(ctypes.byref(cache.struct), batch, n_tok, n_q_heads, shared_len)
+
+
+def dflash2_attend(cache, block_table, kv_len, q, out, workspace, n_new=None, scale=None, causal=True, window=0,
+                   shared_len=0, stream=None):
+    """q, out: [batch, n_tok, n_q_heads, head_dim] bfloat16, tokens evenly
+    spaced; kv_len: [batch], n_new: [batch] or None, int32; scale: by default
+    1/sqrt(head_dim)."""
+    fn, dev = "dflash2_attend", cache.device
+    ref = cache.at(fn)
+    table, max_pages, batch = _table(fn, block_table, dev)
+    if q is None or q.dim() != 4 or q.shape[0] != batch or q.shape[3] != cache.width:
+        _refuse(fn, "q", q, dev, torch.bfloat16, (batch, "n_tok", "n_q_heads", cache.width))
+    (qp, qs), (op, os_) = _tokens_of(fn, "q", q, dev, q.shape), _tokens_of(fn, "out", out, dev, q.shape)
+    if workspace is None:
+        raise DFlash2Error(fn, -5, "workspace must be on the current device")
+    return _check(fn, lib().dflash2_attend(
+        ref, table, max_pages, batch, q.shape[1],
+        None if n_new is None else _at(fn, "n_new", n_new, dev, torch.int32, (batch,)),
+        _at(fn, "kv_len", kv_len, dev, torch.int32, (batch,)), q.shape[2], qp, qs, op, os_,
+        cache.width ** -0.5 if scale is None else scale, int(causal), window, shared_len,
+        _workspace(fn, workspace, dev), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def dflash2_adjust_logits(logits, tokens, n_tokens, out, prompt_len=None, path=None, repetition=None, presence=None,
+                          frequency=None, bias_id=None, bias=None, mask=None, workspace=None, stream=None):
+    """logits, out: [batch, rows, vocab] float32 or bfloat16, rows evenly
+    spaced (out may be logits); tokens: [batch, max_tokens] int32 or None,
+    n_tokens, prompt_len: [batch] int32; path: [batch, rows - 1] int32;
+    repetition, presence, frequency: [batch] float32; bias_id, bias: [batch,
+    n_bias]; mask: [batch, rows, ceil(vocab / 32)] int32 words."""
+    fn = "dflash2_adjust_logits"
+    dev, code, stride = _rows_of(fn, "logits", logits, 3)
+    _, out_code, out_stride = _rows_of(fn, "out", out, 3)
+    batch, rows, vocab = logits.shape
+    if out.shape != logits.shape or out_code != code:
+        _refuse(fn, "out", out, dev, logits.dtype, logits.shape)
+    i32, f32, one = torch.int32, torch.float32, (batch,)
+    opt = lambda name, t, dtype, shape: None if t is None else _at(fn, name, t, dev, dtype, shape)  # noqa: E731
+    most = 0 if tokens is None or tokens.dim() != 2 else tokens.shape[1]
+    n_bias = 0 if bias_id is None or bias_id.dim() != 2 else bias_id.shape[1]
+    return _check(fn, lib().dflash2_adjust_logits(
+        code, batch, rows, vocab, logits.data_ptr(), stride, opt("tokens", tokens, i32, (batch, most)), most,
+        opt("n_tokens", n_tokens, i32, one), opt("prompt_len", prompt_len, i32, one),
+        opt("path", path, i32, (batch, rows - 1)), opt("repetition", repetition, f32, one),
+        opt("presence", presence, f32, one), opt("frequency", frequency, f32, one),
+        opt("bias_id", bias_id, i32, (batch, n_bias)), opt("bias", bias, f32, (batch, n_bias)), n_bias,
+        opt("mask", mask, i32, (batch, rows, -(-vocab // 32))), out.data_ptr(), out_stride,
+        _workspace(fn, workspace, dev, STATUS_BYTES), _stream(stream)))
 
 
 def dflash2_verify_accept_ex(batch, block_size, path, n_draft, target, accept_len, out_tok, n_out, next_anchor,

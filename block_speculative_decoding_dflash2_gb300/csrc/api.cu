@@ -117,6 +117,8 @@ constexpr int kMaxTopkRows = 32 * 256;
 
 // Most rows of logits a sampling call takes.
 constexpr int64_t kMaxSamplingRows = 1 << 20;
+// limits of the cache operators and the attention (grid dimensions and 32-bit row numbers hold them)
+constexpr int kMaxCacheBatch = 65535, kMaxCacheHeads = 256, kMaxAttendHeads = 1024, kMaxAttendTokens = 1024;
 
 struct Layout {
   size_t status, cnt, cnta, thr, f, Y, P, Ya, Pa, h, u, u2, ua, u2a, q, kb, vb, attn, O, act, hn, logits, lv, li, selx,
@@ -1056,6 +1058,177 @@ int dflash2_verify_logits(int dtype, int batch, int block_size, int vocab, const
   a.seq_len = seq_len;
   a.counters = counters;
   return launch_sampling(a, ctx);
+}
+
+static int check_cache(const dflash2_cache* cache, const int32_t* block_table, int max_pages, int batch) {
+  if (!cache) return DFLASH2_ERR_INVALID_ARG;
+  const dflash2_cache& c = *cache;
+  if (c.dtype != DFLASH2_BF16 && c.dtype != DFLASH2_E4M3) return DFLASH2_ERR_DTYPE;
+  if (c.head_dim != 64 && c.head_dim != 128) return DFLASH2_ERR_SHAPE;
+  if (c.n_kv_heads <= 0 || c.n_kv_heads > kMaxCacheHeads || c.page_size <= 0 || c.n_pages <= 0) return DFLASH2_ERR_SHAPE;
+  if (max_pages <= 0 || (int64_t)max_pages * c.page_size > INT32_MAX - 4096) return DFLASH2_ERR_SHAPE;
+  if (batch <= 0 || batch > kMaxCacheBatch) return DFLASH2_ERR_SHAPE;
+  if (!c.k || !c.v || !block_table) return DFLASH2_ERR_INVALID_ARG;
+  if ((uintptr_t)c.k % 16 || (uintptr_t)c.v % 16 || (uintptr_t)block_table % 4) return DFLASH2_ERR_INVALID_ARG;
+  if (c.dtype == DFLASH2_E4M3 && (!c.k_exp || !c.v_exp)) return DFLASH2_ERR_INVALID_ARG;
+  return DFLASH2_OK;
+}
+
+static int cache_rows(const dflash2_cache* cache, const int32_t* block_table, int max_pages, int batch,
+                      const int32_t* start, int rows, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                      const int32_t* off, bool read, void* workspace, void* stream) {
+  TRY(check_cache(cache, block_table, max_pages, batch));
+  const dflash2_cache& c = *cache;
+  if (rows < 0) return DFLASH2_ERR_SHAPE;
+  if (!off || (uintptr_t)off % 4 || (uintptr_t)start % 4) return DFLASH2_ERR_INVALID_ARG;
+  if ((uintptr_t)workspace % 4) return DFLASH2_ERR_WORKSPACE;
+  if (rows == 0) return DFLASH2_OK;
+  if (!k || !v || (uintptr_t)k % 16 || (uintptr_t)v % 16) return DFLASH2_ERR_INVALID_ARG;
+  const int64_t width = (int64_t)c.n_kv_heads * c.head_dim;
+  if (rows > 1 && (k_stride < width || v_stride < width || k_stride % 8 || v_stride % 8)) return DFLASH2_ERR_SHAPE;
+  Ctx ctx;
+  TRY(device_ctx(&ctx, stream, workspace));
+  CacheRowsArgs a = {};
+  a.e4m3 = c.dtype == DFLASH2_E4M3;
+  a.nkv = c.n_kv_heads;
+  a.d = c.head_dim;
+  a.n_pages = c.n_pages;
+  a.page_size = c.page_size;
+  a.max_pages = max_pages;
+  a.batch = batch;
+  a.k = c.k;
+  a.v = c.v;
+  a.k_exp = c.k_exp;
+  a.v_exp = c.v_exp;
+  a.block_table = block_table;
+  a.start = start;
+  a.off = off;
+  a.rows = rows;
+  a.k_rows = const_cast<void*>(k);
+  a.v_rows = const_cast<void*>(v);
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.status = ctx.status;
+  return launch_cache_rows(a, read, ctx);
+}
+
+int dflash2_cache_append(const dflash2_cache* cache, const int32_t* block_table, int max_pages, int batch,
+                         const int32_t* ctx_len, int n_new, const void* k, int64_t k_stride, const void* v,
+                         int64_t v_stride, const int32_t* new_off, void* workspace, void* stream) {
+  if (!ctx_len) return DFLASH2_ERR_INVALID_ARG;
+  return cache_rows(cache, block_table, max_pages, batch, ctx_len, n_new, k, k_stride, v, v_stride, new_off, false,
+                    workspace, stream);
+}
+
+int dflash2_cache_read(const dflash2_cache* cache, const int32_t* block_table, int max_pages, int batch,
+                       const int32_t* start, int n_rows, const int32_t* off, void* k, int64_t k_stride, void* v,
+                       int64_t v_stride, void* workspace, void* stream) {
+  return cache_rows(cache, block_table, max_pages, batch, start, n_rows, k, k_stride, v, v_stride, off, true,
+                    workspace, stream);
+}
+
+static int check_attend(const dflash2_cache* cache, int batch, int n_tok, int n_q_heads, int shared_len) {
+  const dflash2_cache& c = *cache;
+  if (n_tok <= 0 || n_tok > kMaxAttendTokens || shared_len < 0) return DFLASH2_ERR_SHAPE;
+  if (n_q_heads <= 0 || n_q_heads > kMaxAttendHeads || n_q_heads % c.n_kv_heads) return DFLASH2_ERR_SHAPE;
+  return DFLASH2_OK;
+}
+
+size_t dflash2_attend_workspace(const dflash2_cache* cache, int batch, int n_tok, int n_q_heads, int shared_len) {
+  if (!cache || batch <= 0 || batch > kMaxCacheBatch || cache->n_kv_heads <= 0) return 0;
+  if (check_attend(cache, batch, n_tok, n_q_heads, shared_len) != DFLASH2_OK) return 0;
+  return 256;
+}
+
+int dflash2_attend(const dflash2_cache* cache, const int32_t* block_table, int max_pages, int batch, int n_tok,
+                   const int32_t* n_new, const int32_t* kv_len, int n_q_heads, const void* q, int64_t q_stride,
+                   void* out, int64_t out_stride, float scale, int causal, int window, int shared_len, void* workspace,
+                   size_t ws_bytes, void* stream) {
+  TRY(check_cache(cache, block_table, max_pages, batch));
+  TRY(check_attend(cache, batch, n_tok, n_q_heads, shared_len));
+  const dflash2_cache& c = *cache;
+  if (window < 0 || (int64_t)shared_len > (int64_t)max_pages * c.page_size) return DFLASH2_ERR_SHAPE;
+  if (!kv_len || !q || !out || (uintptr_t)q % 16 || (uintptr_t)out % 16) return DFLASH2_ERR_INVALID_ARG;
+  if ((uintptr_t)kv_len % 4 || (uintptr_t)n_new % 4) return DFLASH2_ERR_INVALID_ARG;
+  const int64_t width = (int64_t)n_q_heads * c.head_dim;
+  const bool one = batch == 1 && n_tok == 1;
+  if (!one && (q_stride < width || out_stride < width || q_stride % 8 || out_stride % 8)) return DFLASH2_ERR_SHAPE;
+  if (!workspace || (uintptr_t)workspace % 16 ||
+      ws_bytes < dflash2_attend_workspace(cache, batch, n_tok, n_q_heads, shared_len))
+    return DFLASH2_ERR_WORKSPACE;
+  Ctx ctx;
+  TRY(device_ctx(&ctx, stream, workspace));
+  AttendArgs a = {};
+  a.e4m3 = c.dtype == DFLASH2_E4M3;
+  a.causal = causal != 0;
+  a.nq = n_q_heads;
+  a.nkv = c.n_kv_heads;
+  a.d = c.head_dim;
+  a.n_pages = c.n_pages;
+  a.page_size = c.page_size;
+  a.max_pages = max_pages;
+  a.batch = batch;
+  a.n_tok = n_tok;
+  a.window = window;
+  a.shared_len = shared_len;
+  a.k = c.k;
+  a.v = c.v;
+  a.k_exp = c.k_exp;
+  a.v_exp = c.v_exp;
+  a.block_table = block_table;
+  a.n_new = n_new;
+  a.kv_len = kv_len;
+  a.q = static_cast<const bf16*>(q);
+  a.out = static_cast<bf16*>(out);
+  a.q_stride = one ? width : q_stride;
+  a.out_stride = one ? width : out_stride;
+  a.scale = scale;
+  a.status = ctx.status;
+  return launch_attend(a, ctx);
+}
+
+int dflash2_adjust_logits(int dtype, int batch, int rows, int vocab, const void* logits, int64_t stride,
+                          const int32_t* tokens, int max_tokens, const int32_t* n_tokens, const int32_t* prompt_len,
+                          const int32_t* path, const float* repetition, const float* presence, const float* frequency,
+                          const int32_t* bias_id, const float* bias, int n_bias, const uint32_t* mask, void* out,
+                          int64_t out_stride, void* workspace, void* stream) {
+  TRY(check_sampling(dtype, batch, rows, vocab, logits, stride));
+  if (batch > kMaxCacheBatch || max_tokens < 0 || n_bias < 0 || n_bias > 65535) return DFLASH2_ERR_SHAPE;
+  if (path && (rows < 2 || rows > 32)) return DFLASH2_ERR_BLOCK_SIZE;
+  if ((int64_t)batch * rows > 1 && out_stride < vocab) return DFLASH2_ERR_SHAPE;
+  if (!out || (uintptr_t)out % (dtype == DFLASH2_F32 ? 4 : 2)) return DFLASH2_ERR_INVALID_ARG;
+  if (max_tokens > 0 && (!tokens || !n_tokens)) return DFLASH2_ERR_INVALID_ARG;
+  if (n_bias > 0 && (!bias_id || !bias)) return DFLASH2_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)tokens, (const void*)n_tokens, (const void*)prompt_len, (const void*)path,
+                        (const void*)repetition, (const void*)presence, (const void*)frequency, (const void*)bias_id,
+                        (const void*)bias, (const void*)mask})
+    if ((uintptr_t)p % 4) return DFLASH2_ERR_INVALID_ARG;
+  if ((uintptr_t)workspace % 4) return DFLASH2_ERR_WORKSPACE;
+  Ctx ctx;
+  TRY(device_ctx(&ctx, stream, workspace));
+  AdjustArgs a = {};
+  a.bf16_logits = dtype == DFLASH2_BF16;
+  a.batch = batch;
+  a.rows = rows;
+  a.vocab = vocab;
+  a.max_tokens = max_tokens;
+  a.n_bias = n_bias;
+  a.logits = logits;
+  a.stride = (int64_t)batch * rows > 1 ? stride : vocab;
+  a.out = out;
+  a.out_stride = (int64_t)batch * rows > 1 ? out_stride : vocab;
+  a.tokens = tokens;
+  a.n_tokens = max_tokens > 0 ? n_tokens : nullptr;
+  a.prompt_len = prompt_len;
+  a.path = path;
+  a.repetition = repetition;
+  a.presence = presence;
+  a.frequency = frequency;
+  a.bias_id = bias_id;
+  a.bias = bias;
+  a.mask = mask;
+  a.status = ctx.status;
+  return launch_adjust(a, ctx);
 }
 
 int dflash2_read_device_status(void* workspace, size_t ws_bytes, void* stream) {

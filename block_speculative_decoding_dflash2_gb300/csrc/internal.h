@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -9,6 +10,8 @@
 #include "../../include/dflash2.h"
 
 namespace df2 {
+
+typedef __nv_bfloat16 bf16;
 
 struct Ctx {
   cudaStream_t stream;
@@ -316,5 +319,53 @@ struct SamplingArgs {
 // end; more take a second kernel (whose launch, about 2 us, they hide).
 constexpr int kSamplingJoin = 256;
 int launch_sampling(const SamplingArgs& a, const Ctx& c);
+
+// rows written into a paged cache and read back (paged_cache.cu)
+struct CacheRowsArgs {
+  bool e4m3;
+  int nkv, d, n_pages, page_size, max_pages, batch;
+  void *k, *v;             // pools [n_pages, page_size, nkv, d]
+  uint8_t *k_exp, *v_exp;  // exponent bytes [n_pages, page_size, nkv] of an 8-bit cache
+  const int32_t* block_table;
+  const int32_t* start;  // nullable [batch]: position of each sequence's first row
+  const int32_t* off;    // [batch + 1] row offsets
+  int rows;
+  void *k_rows, *v_rows;  // [rows, nkv, d] bf16, written when reading the cache
+  long long k_stride, v_stride;
+  unsigned* status;
+};
+int launch_cache_rows(const CacheRowsArgs& a, bool read, const Ctx& c);
+
+// attention over a paged cache (attend.cu)
+struct AttendArgs {
+  bool e4m3, causal;
+  int nq, nkv, d, n_pages, page_size, max_pages, batch, n_tok, window, shared_len;
+  const void *k, *v;
+  const uint8_t *k_exp, *v_exp;
+  const int32_t *block_table, *n_new, *kv_len;
+  const bf16* q;  // [batch, n_tok, nq, d], tokens q_stride elements apart
+  bf16* out;
+  long long q_stride, out_stride;
+  float scale;
+  unsigned* status;
+};
+int launch_attend(const AttendArgs& a, const Ctx& c);
+
+// penalties, biases and masks on logits (adjust.cu)
+struct AdjustArgs {
+  bool bf16_logits;
+  int batch, rows, vocab, max_tokens, n_bias;
+  const void* logits;
+  long long stride;
+  void* out;
+  long long out_stride;
+  const int32_t *tokens, *n_tokens, *prompt_len, *path;
+  const float *repetition, *presence, *frequency;
+  const int32_t* bias_id;
+  const float* bias;
+  const uint32_t* mask;
+  unsigned* status;
+};
+int launch_adjust(const AdjustArgs& a, const Ctx& c);
 
 }  // namespace df2

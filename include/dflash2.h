@@ -87,6 +87,7 @@ extern "C" {
                             refused).  Not served by
                             dflash2_select_path_static (DFLASH2_ERR_UNSUPPORTED). */
 #define DFLASH2_W4_GROUP 64
+#define DFLASH2_E4M3  4  /* 8-bit rows of a dflash2_cache: e4m3 codes and one exponent byte per row and head */
 
 /*
  * Draft model configuration ("Key Config Fields"; dflash_config of
@@ -576,6 +577,142 @@ int dflash2_verify_logits(int dtype, int batch, int block_size, int vocab, const
 int dflash2_linear_w4(const uint8_t *codes, const void *scale, int group, int out_features, int in_features,
                       const void *x, int64_t x_stride, int rows, void *out, int64_t out_stride, int out_dtype,
                       int accumulate, void *stream);
+
+/*
+ * A paged cache that the operators below write and read: one layer of a
+ * target's (or any model's) keys and values, in bfloat16 as the draft model's
+ * cache above, or in 8 bits.  Host struct of device pointers.
+ *   dtype         DFLASH2_BF16 or DFLASH2_E4M3
+ *   n_pages, page_size, n_kv_heads (at most 256), head_dim (64 or 128)
+ *   k, v          [n_pages, page_size, n_kv_heads, head_dim], 16-byte aligned
+ *   k_exp, v_exp  DFLASH2_E4M3: [n_pages, page_size, n_kv_heads] bytes
+ *                 (NULL otherwise)
+ * With DFLASH2_E4M3 a head's row of values x is held as e4m3 codes c and one
+ * exponent byte b = 1..254, a code standing for c * 2^(b - 127): b is the
+ * smallest byte with max|x| <= 448 * 2^(b - 127) over the finite x, and c the
+ * nearest e4m3 value of x * 2^(127 - b), ties to even, NaN where x is not
+ * finite.  What is stored is a bfloat16 value exactly (below 2^-126 up to its
+ * subnormals' step), so rows read back as they are.
+ *   block_table   [batch, max_pages] int32 as above; max_pages * page_size
+ *                 below 2^31 - 4096
+ *   batch         at most 65535
+ *   workspace     of append and read: nullable, its status word only (256
+ *                 bytes, 4-byte aligned)
+ */
+typedef struct dflash2_cache {
+    int dtype, n_pages, page_size, n_kv_heads, head_dim;
+    void *k, *v;
+    uint8_t *k_exp, *v_exp;
+} dflash2_cache;
+
+/*
+ * Writes rows of keys and values behind each sequence's ctx_len[s]
+ * positions, quantised on the way into an 8-bit cache.
+ *   ctx_len   [batch] int32 positions before the call (not modified)
+ *   n_new     rows in k and v (>= 0; 0: nothing is done)
+ *   k, v      [n_new, n_kv_heads, head_dim] bfloat16, 16-byte aligned, rows
+ *             k_stride and v_stride elements apart (multiples of 8)
+ *   new_off   [batch + 1] int32 row offsets of each sequence, new_off[0] = 0,
+ *             new_off[batch] <= n_new; rows behind it are not written
+ * A row past the block table (DFLASH2_DEV_BAD_LENGTH) or on a page outside
+ * [0, n_pages) (DFLASH2_DEV_BAD_PAGE) is skipped.
+ */
+int dflash2_cache_append(const dflash2_cache *cache, const int32_t *block_table, int max_pages, int batch,
+                         const int32_t *ctx_len, int n_new, const void *k, int64_t k_stride, const void *v,
+                         int64_t v_stride, const int32_t *new_off, void *workspace, void *stream);
+
+/*
+ * Reads rows back as bfloat16: rows off[s] .. off[s + 1] - 1 of k and v
+ * receive positions start[s], start[s] + 1, ... of sequence s.
+ *   start     nullable [batch] int32 (null: 0)
+ *   n_rows    rows that k and v have; those from off[batch] on are left as
+ *             they are
+ *   off       [batch + 1] int32, off[0] = 0, off[batch] <= n_rows
+ *   k, v      out, as in dflash2_cache_append
+ * Rows past the block table or on a page outside [0, n_pages) are zeros, and
+ * recorded as above.
+ */
+int dflash2_cache_read(const dflash2_cache *cache, const int32_t *block_table, int max_pages, int batch,
+                       const int32_t *start, int n_rows, const int32_t *off, void *k, int64_t k_stride, void *v,
+                       int64_t v_stride, void *workspace, void *stream);
+
+/*
+ * Attention of the last tokens of each sequence over its paged cache: plain
+ * decoding (n_tok = 1), a target's verification of a drafted block, a chunk
+ * of a prompt, or, without causality, a draft's block.  The tokens' own keys
+ * and values are in the cache already (dflash2_cache_append).
+ *   n_tok       tokens of a sequence in q and out, 1 .. 1024
+ *   n_new       nullable [batch] int32: the tokens that sequence s has of
+ *               them (0 .. n_tok); the rows behind are neither read nor
+ *               written (null: n_tok each)
+ *   kv_len      [batch] int32: keys of each sequence, its tokens' own last
+ *   n_q_heads   a multiple of n_kv_heads, at most 1024; query head h reads
+ *               kv head h / (n_q_heads / n_kv_heads)
+ *   q, out      [batch, n_tok, n_q_heads, head_dim] bfloat16, 16-byte
+ *               aligned, tokens q_stride and out_stride elements apart
+ *               (multiples of 8); out overlaps no input
+ *   scale       of the products, commonly 1/sqrt(head_dim)
+ *   causal      token i of n sees the keys below kv_len - n + 1 + i; with 0
+ *               every token sees all kv_len
+ *   window      > 0: of these only the last `window`; 0: all
+ *   shared_len  the first shared_len positions are the same pages in every
+ *               row of the block table (a common prompt): they are read
+ *               through row 0 and computed once for the whole batch.  0:
+ *               none.  A sequence may have fewer keys than that.
+ * out = softmax(scale * q k) v over the keys that a token sees, zeros where
+ * there is none; scores, weights and sums are fp32 and the result is rounded
+ * once.  Keys that a token does not see have no part in its result, whatever
+ * they hold.  Keys past the block table (DFLASH2_DEV_BAD_LENGTH) or on a page
+ * outside [0, n_pages) (DFLASH2_DEV_BAD_PAGE) are left out.
+ * The workspace needs dflash2_attend_workspace bytes (0 for bad sizes; host
+ * only), 16-byte aligned, its first 256 bytes zeroed once before the first
+ * use; it serves one call at a time, of any sizes that fit.
+ */
+size_t dflash2_attend_workspace(const dflash2_cache *cache, int batch, int n_tok, int n_q_heads, int shared_len);
+int dflash2_attend(const dflash2_cache *cache, const int32_t *block_table, int max_pages, int batch, int n_tok,
+                   const int32_t *n_new, const int32_t *kv_len, int n_q_heads, const void *q, int64_t q_stride,
+                   void *out, int64_t out_stride, float scale, int causal, int window, int shared_len, void *workspace,
+                   size_t ws_bytes, void *stream);
+
+/*
+ * What a request's settings change in its logits before dflash2_sample,
+ * dflash2_target_probs or dflash2_verify_logits: penalties of tokens that
+ * were there already, biases, and a mask of the tokens that a grammar allows.
+ * Row i of sequence s follows its tokens and its first i drafts.  In that
+ * row, with c(v) the count of token v in tokens[prompt_len ..] and the first
+ * i drafts, and "seen" for any token of tokens and the first i drafts:
+ *   z = z > 0 ? z / repetition : z * repetition   if v was seen
+ *   z = (z - frequency * c(v)) - presence         if c(v) > 0
+ *   z = z + bias                                  if v has one
+ *   z = -inf                                      if the mask has no bit for v
+ * computed in fp32 and rounded once.
+ *   dtype, vocab, logits, stride   as above; `rows` rows per sequence
+ *   tokens      [batch, max_tokens] int32, n_tokens [batch] of them used
+ *               (both nullable with max_tokens = 0)
+ *   prompt_len  nullable [batch]: tokens before it are seen but not counted
+ *               (null: 0)
+ *   path        nullable [batch, rows - 1] int32: the drafts (2 to 32 rows);
+ *               -1: no token.  Null: every row follows the tokens alone
+ *   repetition, presence, frequency
+ *               nullable [batch] float (null: 1, 0, 0)
+ *   bias_id     [batch, n_bias] int32 token ids, -1: unused; of several
+ *               entries of one id the last counts; n_bias up to 65535
+ *   bias        [batch, n_bias] float
+ *   mask        nullable [batch, rows, ceil(vocab / 32)] words, bit v % 32 of
+ *               word v / 32 set where token v is allowed
+ *   out         [batch * rows, vocab] of dtype, rows out_stride elements
+ *               apart; may be logits itself (the same address and stride),
+ *               and overlaps nothing else
+ *   workspace   nullable: its status word only (256 bytes, 4-byte aligned)
+ * Token ids outside [0, vocab) are skipped and recorded
+ * (DFLASH2_DEV_BAD_TOKEN), as is an n_tokens outside [0, max_tokens]
+ * (DFLASH2_DEV_BAD_LENGTH; it counts as the nearer end).
+ */
+int dflash2_adjust_logits(int dtype, int batch, int rows, int vocab, const void *logits, int64_t stride,
+                          const int32_t *tokens, int max_tokens, const int32_t *n_tokens, const int32_t *prompt_len,
+                          const int32_t *path, const float *repetition, const float *presence, const float *frequency,
+                          const int32_t *bias_id, const float *bias, int n_bias, const uint32_t *mask, void *out,
+                          int64_t out_stride, void *workspace, void *stream);
 
 /*
  * Instrumentation.  Number of kernel launches the library has issued since
