@@ -19,7 +19,8 @@ LIB = os.path.join(PKG, "libdflash2.so")
 
 SOURCES = ["api.cu", "gemm_tc.cu", "gemm_simt.cu", "elementwise.cu", "attention.cu", "attention_tc.cu",
            "topk.cu", "selector.cu", "verify.cu", "select_static.cu", "sampling.cu", "linear_w4.cu",
-           "linear_w4_tc.cu", "paged_cache.cu", "attend.cu", "adjust.cu"]
+           "linear_w4_tc.cu", "paged_cache.cu", "attend.cu", "attend_tc.cu",
+           "adjust.cu"]
 # the test hooks (include/dflash2_testing.h) live in a library of their own,
 # linked against libdflash2.so, so the product library exports only dflash2.h
 TEST_SOURCES = ["testing.cu"]

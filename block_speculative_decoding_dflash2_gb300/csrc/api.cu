@@ -1137,7 +1137,7 @@ static int check_attend(const dflash2_cache* cache, int batch, int n_tok, int n_
 size_t dflash2_attend_workspace(const dflash2_cache* cache, int batch, int n_tok, int n_q_heads, int shared_len) {
   if (!cache || batch <= 0 || batch > kMaxCacheBatch || cache->n_kv_heads <= 0) return 0;
   if (check_attend(cache, batch, n_tok, n_q_heads, shared_len) != DFLASH2_OK) return 0;
-  return 256;
+  return std::max<size_t>(256, attend_tc_workspace(batch, n_tok, n_q_heads, cache->n_kv_heads, shared_len));
 }
 
 int dflash2_attend(const dflash2_cache* cache, const int32_t* block_table, int max_pages, int batch, int n_tok,
@@ -1148,6 +1148,7 @@ int dflash2_attend(const dflash2_cache* cache, const int32_t* block_table, int m
   TRY(check_attend(cache, batch, n_tok, n_q_heads, shared_len));
   const dflash2_cache& c = *cache;
   if (window < 0 || (int64_t)shared_len > (int64_t)max_pages * c.page_size) return DFLASH2_ERR_SHAPE;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return DFLASH2_ERR_INVALID_ARG;
   if (!kv_len || !q || !out || (uintptr_t)q % 16 || (uintptr_t)out % 16) return DFLASH2_ERR_INVALID_ARG;
   if ((uintptr_t)kv_len % 4 || (uintptr_t)n_new % 4) return DFLASH2_ERR_INVALID_ARG;
   const int64_t width = (int64_t)n_q_heads * c.head_dim;
@@ -1184,7 +1185,7 @@ int dflash2_attend(const dflash2_cache* cache, const int32_t* block_table, int m
   a.out_stride = one ? width : out_stride;
   a.scale = scale;
   a.status = ctx.status;
-  return launch_attend(a, ctx);
+  return launch_attend(a, workspace, ctx);
 }
 
 int dflash2_adjust_logits(int dtype, int batch, int rows, int vocab, const void* logits, int64_t stride,

@@ -159,7 +159,8 @@ __global__ void __launch_bounds__(32 * kWarps) attend_rows_kernel(AttendArgs a) 
 
 }  // namespace
 
-int launch_attend(const AttendArgs& a, const Ctx& c) {
+int launch_attend(const AttendArgs& a, void* workspace, const Ctx& c) {
+  if (attend_tc_fits(a)) return launch_attend_tc(a, workspace, c);
   const dim3 grid((a.n_tok * (a.nq / a.nkv) + kRows - 1) / kRows, a.nkv, a.batch), block(32 * kWarps);
   if (a.d == 64)
     return a.e4m3 ? launch_k(attend_rows_kernel<64, true>, grid, block, 0, c, a)

@@ -349,7 +349,11 @@ struct AttendArgs {
   float scale;
   unsigned* status;
 };
-int launch_attend(const AttendArgs& a, const Ctx& c);
+int launch_attend(const AttendArgs& a, void* workspace, const Ctx& c);
+// tcgen05 attention (attend_tc.cu): head dimension 128, pages of whole 16-key groups
+bool attend_tc_fits(const AttendArgs& a);
+size_t attend_tc_workspace(int batch, int n_tok, int nq, int nkv, int shared_len);  // 0: sizes it does not take
+int launch_attend_tc(const AttendArgs& a, void* workspace, const Ctx& c);
 
 // penalties, biases and masks on logits (adjust.cu)
 struct AdjustArgs {

@@ -651,7 +651,7 @@ int dflash2_cache_read(const dflash2_cache *cache, const int32_t *block_table, i
  *   q, out      [batch, n_tok, n_q_heads, head_dim] bfloat16, 16-byte
  *               aligned, tokens q_stride and out_stride elements apart
  *               (multiples of 8); out overlaps no input
- *   scale       of the products, commonly 1/sqrt(head_dim)
+ *   scale       of the products, above 0 and finite, commonly 1/sqrt(head_dim)
  *   causal      token i of n sees the keys below kv_len - n + 1 + i; with 0
  *               every token sees all kv_len
  *   window      > 0: of these only the last `window`; 0: all
