@@ -29,11 +29,14 @@
 // three e5m2 codes (3 + 3 + 3 bits, 2^-9 of each weight over 2^30 of range).
 // The scales of keys multiply the scores; those of values the weights.
 //
-// Warps: 0-3 and 4-7 softmax of stream 0 and 1 (thread = query row), 8 loads
-// by TMA, 9 TMEM and MMA issue, 10 what a tile needs beside its rows: which
-// 16-key groups exist, the scales, and, in tiles that hold keys which some
-// row does not see, zeros for values that are not finite (a zero weight
-// would turn them into NaN; rows that do see one are marked).
+// Warps: 0-3 and 4-7 softmax of stream 0 and 1 (thread = query row); 8 loads
+// keys and values by TMA; 9 TMEM and MMA issue; 10 what a tile needs beside
+// its rows: which 16-key groups exist, the scales, and, in tiles that hold
+// keys which some row does not see, zeros for values that are not finite (a
+// zero weight would turn them into NaN; rows that do see one are marked); 11
+// the segments of this CTA, one ahead of the others, and their query rows.
+// Loops over a tile are rolled where they can be: five roles' code shares the
+// instruction cache, and unrolled it took most of the time to fetch.
 #include <algorithm>
 #include <cstring>
 
@@ -47,11 +50,10 @@ namespace {
 constexpr int kTile = 128;  // keys of a tile, query rows of a stream
 constexpr int kD = 128;     // head dimension
 constexpr int kSoftmax = 256;
-constexpr int kThreads = kSoftmax + 128;  // (the last warp only fills its group of four)
-// registers a thread: 384 threads start with 168 (64512 in all), of which the
-// softmax groups take 208 (53248) and the others keep 88 (11264)
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
-constexpr int kInfo = 4;  // tiles ahead of which warp 10 may run
+constexpr int kThreads = kSoftmax + 128;
+constexpr int kRowTile = 2 * kTile;  // query rows of a segment at most
+constexpr int kInfo = 4;  // tiles that warp 10 may be ahead
+constexpr int kSegs = 3;  // segments that warp 11 may be ahead (its query rows have two places)
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kMaxCtas = kMaxSM;
 constexpr float kNone = -INFINITY;
@@ -69,16 +71,32 @@ struct TileInfo {
   uint32_t pad;
 };
 
-template <bool E4M3, int QT>
+// A segment's share of this CTA, as its roles need it.
+struct SegInfo {
+  int tiles;            // 0: no more segments
+  int first, end;       // position of its first tile; keys end before `end`
+  int all_lo, all_hi;   // keys that every row sees
+  int shared, s, h;     // the shared part's (s = 0), or sequence s; kv head
+  int f0, rows;         // first query row (sequence, token, head of the group), their number
+  int n, len;           // tokens and keys of sequence s
+  int split;            // both streams take the same rows
+  int q;                // place of the query rows (split)
+  int slot;             // place of the partial result, -1: the CTA finishes the segment
+  int pad;
+};
+
+template <bool E4M3>
 struct Smem {
-  static constexpr int Q = 0;                                  // [QT][32 KB]
-  static constexpr int SLOT = E4M3 ? 16384 : 32768;            // K or V of a tile
-  static constexpr int SLOTS = E4M3 ? (QT == 2 ? 9 : 11) : (QT == 2 ? 5 : 6);
-  static constexpr int RING = QT * 32768;
+  static constexpr int Q = 0;                          // [2][32 KB]
+  static constexpr int SLOT = E4M3 ? 16384 : 32768;    // K or V of a tile
+  static constexpr int SLOTS = E4M3 ? 9 : 5;
+  static constexpr int RING = 65536;
   static constexpr int INFO = RING + SLOTS * SLOT;
   static constexpr int INFOS = E4M3 ? (int)sizeof(TileInfo) : 32;  // bf16 keeps the tail of TileInfo only
-  static constexpr int BAR = INFO + kInfo * INFOS;
-  static constexpr size_t bytes = 1024 + BAR + (2 * SLOTS + 2 * kInfo + 8) * 8 + 64;
+  static constexpr int SEG = INFO + kInfo * INFOS;
+  static constexpr int QSCALE = SEG + kSegs * (int)sizeof(SegInfo);  // float [kSegs][kRowTile], 8-bit only
+  static constexpr int BAR = QSCALE + (E4M3 ? kSegs * kRowTile * 4 : 0);
+  static constexpr size_t bytes = 1024 + BAR + (2 * SLOTS + 2 * kInfo + 2 * kSegs + 9) * 8 + 64;
   static_assert(bytes + 512 <= 227 * 1024, "shared memory");
 };
 
@@ -113,15 +131,14 @@ struct Segment {
   int end;          // keys end before this position
 };
 
-// Row tile i of sequence s (positions from shared_len on).
-template <int QT>
+// Row tile i of a sequence (positions from shared_len on).
 __device__ __forceinline__ Segment segment_of(const AttendArgs& a, int group, int2 nl, int i) {
   Segment g = {0, 0, 0, 0};
-  const int first = i * (kTile * QT), all = nl.x * group;
+  const int first = i * kRowTile, all = nl.x * group;
   if (first >= all) return g;
-  g.rows = min(kTile * QT, all - first);
-  const int lo = max(sees(a, nl, first / group).x, a.shared_len);
-  const int hi = sees(a, nl, (first + g.rows - 1) / group).y;
+  g.rows = min(kRowTile, all - first);
+  const int t0 = i == 0 ? 0 : first / group, t1 = first + g.rows == all ? nl.x - 1 : (first + g.rows - 1) / group;
+  const int lo = max(sees(a, nl, t0).x, a.shared_len), hi = sees(a, nl, t1).y;
   if (hi <= lo) return g;
   g.base = lo & ~15;
   g.end = hi;
@@ -136,72 +153,6 @@ __device__ __forceinline__ int bound_of(int units, int c, int n) { return (int)(
 __device__ __forceinline__ int owner_of(int units, int x, int n) {
   return (int)((((long long)x + 1) * n - 1) / units);
 }
-
-// Walks a CTA's segments; every role walks for itself.
-template <int QT>
-struct Walk {
-  const Plan* p;
-  int a, b, at;  // this CTA's share; position of the current segment's first tile
-  int base_p, tiles_p, end_p;
-  int entry, h;        // row tile (shared part first) and kv head
-  int2 nl;
-  Segment g;
-  int w;
-  int k0, k1;  // this CTA's tiles of it
-
-  __device__ __forceinline__ int s() const { return (entry - p->tiles_p) / p->tiles_s; }
-  __device__ __forceinline__ bool shared() const { return entry < p->tiles_p; }
-  __device__ __forceinline__ int first_row() const {  // flat query row (sequence, token, head of the group)
-    return shared() ? entry * (kTile * QT) : s() * p->rows + (entry - p->tiles_p) % p->tiles_s * (kTile * QT);
-  }
-  __device__ __forceinline__ int ordinal() const { return (shared() ? entry : entry - p->tiles_p) * p->a.nkv + h; }
-  __device__ __forceinline__ void load() {  // segment of `entry`
-    if (shared()) {
-      g.rows = (int)min((long long)kTile * QT, (long long)p->a.batch * p->rows - (long long)entry * (kTile * QT));
-      g.base = base_p;
-      g.tiles = tiles_p;
-      g.end = end_p;
-      w = QT == 2 ? p->row_weight : 1;
-    } else {
-      nl = lengths(p->a, s());
-      g = segment_of<QT>(p->a, p->group, nl, (entry - p->tiles_p) % p->tiles_s);
-      w = weight_of(*p, g.rows);
-    }
-  }
-  // Moves to the next segment with tiles of this CTA; `fresh`: the first call.
-  __device__ __forceinline__ bool next(bool fresh) {
-    const int entries = p->tiles_p + p->a.batch * p->tiles_s;
-    if (!fresh) {
-      at += g.tiles * w;
-      if (++h == p->a.nkv) {
-        h = 0;
-        ++entry;
-        if (entry < entries) load();
-      }
-    } else if (entry < entries) {
-      load();
-    }
-    while (at < b && entry < entries) {
-      const int size = g.tiles * w;
-      if (size == 0) {  // (all heads alike)
-        h = 0;
-        if (++entry < entries) load();
-        continue;
-      }
-      if (at + size > a) {
-        k0 = at >= a ? 0 : (a - at + w - 1) / w;
-        k1 = min(g.tiles, (b - at + w - 1) / w);
-        if (k0 < k1) return true;
-      }
-      at += size;
-      if (++h == p->a.nkv) {
-        h = 0;
-        if (++entry < entries) load();
-      }
-    }
-    return false;
-  }
-};
 
 // A place in a ring of N slots and the parity of its round.
 template <int N>
@@ -229,6 +180,17 @@ struct Ring {
 
 __device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
+__device__ __forceinline__ bool bar_softmax_or(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbar.red.or.pred p, 1, 256, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -239,32 +201,49 @@ __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
 
-// D += A B: A from TMEM or shared memory; kind::f16 or kind::f8f6f4
+// D (+)= A B, A from shared memory or from TMEM; kind::f16 or kind::f8f6f4.
+// The whole warp executes the code around, with the same values in every
+// lane, and only the instruction itself is left to the lane with `one`: its
+// operands then live in uniform registers.  (Issued from a branch that one
+// lane takes, every operand moves to a uniform register first: 110 to 200
+// cycles an instruction beside the softmax warps, where the products of one
+// take 64.)
 template <bool E4M3>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t one) {
   if (E4M3)
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one)
         : "memory");
   else
-    umma_bf16(d, a, b, idesc, acc);
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one)
+        : "memory");
 }
 template <bool E4M3>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t one) {
   if (E4M3)
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one)
         : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(one)
+      : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
@@ -286,10 +265,11 @@ __device__ __forceinline__ uint32_t bits2(__nv_bfloat162 x) { return *reinterpre
 
 // ------------------------------------------------------------------ main kernel
 
-template <bool E4M3, int QT>
-__global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const Plan p, const __grid_constant__ CUtensorMap tm_k,
+template <bool E4M3>
+__global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_constant__ Plan p,
+                                                               const __grid_constant__ CUtensorMap tm_k,
                                                                const __grid_constant__ CUtensorMap tm_v) {
-  using L = Smem<E4M3, QT>;
+  using L = Smem<E4M3>;
   constexpr int NS = L::SLOTS;
   extern __shared__ uint8_t raw_smem[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
@@ -298,40 +278,43 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const Plan p, co
   uint64_t* empty = full + NS;        // [NS] its products are done
   uint64_t* info_full = empty + NS;   // [kInfo] tile info is there (and V mended)
   uint64_t* info_empty = info_full + kInfo;
-  uint64_t* s_full = info_empty + kInfo;  // [2] scores of a stream's tile in TMEM
-  uint64_t* p_ready = s_full + 2;         // [2] its weights in TMEM (4 arrivals)
-  uint64_t* o_done = p_ready + 2;         // [2] a segment's last product of the stream is done
-  uint64_t* q_ready = o_done + 2;         // query rows in shared memory (8 arrivals)
-  uint64_t* drain = q_ready + 1;          // every product issued is done
+  uint64_t* seg_full = info_empty + kInfo;  // [kSegs] a segment and its query rows are there
+  uint64_t* seg_empty = seg_full + kSegs;   // [kSegs] every role has read it (11 arrivals)
+  uint64_t* s_full = seg_empty + kSegs;     // [2] scores of a stream's tile in TMEM
+  uint64_t* p_ready = s_full + 2;           // [2] its weights in TMEM (4 arrivals)
+  uint64_t* o_done = p_ready + 2;           // [2] a segment's last product of the stream is done
+  uint64_t* q_empty = o_done + 2;           // [2] a place of query rows is free (8 arrivals)
+  uint64_t* drain = q_empty + 2;            // every product issued is done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  __shared__ int start_at[2];
-  __shared__ int scan[kThreads / 32 + 1];
-  __shared__ int start_entry;
+  SegInfo* segs = reinterpret_cast<SegInfo*>(sm + L::SEG);
+  __shared__ int scan[kThreads / 32], ends[kThreads / 32][2], start[3];
 
   const AttendArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x, nctas = gridDim.x;
   pdl_launch_next();
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(full + i, 1);
-      mbar_init(empty + i, 1);
-    }
+  if (threadIdx.x < 2 * NS) mbar_init(bars + threadIdx.x, 1);
+  else if (threadIdx.x == 32) {
     for (int i = 0; i < kInfo; ++i) {
       mbar_init(info_full + i, 1);
       mbar_init(info_empty + i, 8);
     }
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(seg_full + i, 1);
+      mbar_init(seg_empty + i, 11);
+    }
+  } else if (threadIdx.x == 64) {
     for (int j = 0; j < 2; ++j) {
       mbar_init(s_full + j, 1);
       mbar_init(p_ready + j, 4);
       mbar_init(o_done + j, 1);
+      mbar_init(q_empty + j, 8);
     }
-    mbar_init(q_ready, 8);
     mbar_init(drain, 1);
     *abort_flag = 0;
-    fence_barrier_init();
   }
+  fence_barrier_init();
   if (warp == 9) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
@@ -339,111 +322,90 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const Plan p, co
   pdl_wait();
 
   // ------------------------------------------------ shares of the work
-  Walk<QT> wk;
-  wk.p = &p;
   const int entries = a.batch * p.tiles_s;  // row tiles of the sequences
   const int per = (entries + kThreads - 1) / kThreads, e0 = min(entries, (int)threadIdx.x * per);
   const int e1 = min(entries, e0 + per);
-  {
-    int sum = 0;
-    int lo = INT32_MAX, hi = 0;
-    for (int e = e0; e < e1; ++e) {
-      const int s = e / p.tiles_s;
-      const int2 nl = lengths(a, s);
-      if (cta == 0 && e % p.tiles_s == 0 && (a.kv_len[s] < 0 || a.kv_len[s] != nl.y)) flag(a.status, DFLASH2_DEV_BAD_LENGTH);
-      const Segment g = segment_of<QT>(a, p.group, nl, e % p.tiles_s);
-      sum += g.tiles * weight_of(p, g.rows) * a.nkv;
-      if (nl.x > 0) {
-        lo = min(lo, sees(a, nl, 0).x);
-        hi = max(hi, sees(a, nl, nl.x - 1).y);
-      }
+  // units (tiles times cost) of row tile e, of all kv heads
+  auto units_of = [&](int e, int2* nl) {
+    const int s = p.tiles_s == 1 ? e : e / p.tiles_s;
+    *nl = lengths(a, s);
+    const Segment g = segment_of(a, p.group, *nl, p.tiles_s == 1 ? 0 : e % p.tiles_s);
+    return g.tiles * weight_of(p, g.rows) * a.nkv;
+  };
+  int my_units = 0, lo = INT32_MAX, hi = 0;
+  for (int e = e0; e < e1; ++e) {
+    int2 nl;
+    my_units += units_of(e, &nl);
+    if (p.tiles_p > 0 && nl.x > 0) {
+      lo = min(lo, sees(a, nl, 0).x);
+      hi = max(hi, sees(a, nl, nl.x - 1).y);
     }
-    // block scan of the sums; minimum and maximum of the shared part's keys
-    int inc = sum;
-    int mn = lo, mx = hi;
+  }
+  int before = my_units;  // block scan; minimum and maximum of the shared part's keys
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-      mn = min(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    }
-    int* ends = reinterpret_cast<int*>(sm);  // (the query rows' place, not in use yet)
-    if (lane == 31) scan[warp + 1] = inc;
-    if (lane == 0) {
-      ends[2 * warp] = mn;
-      ends[2 * warp + 1] = mx;
-    }
-    if (threadIdx.x == 0) {
-      scan[0] = 0;
-      start_entry = p.tiles_p + entries;
-    }
-    __syncthreads();
-    int before = inc - sum, total = 0;
-    mn = INT32_MAX;
-    mx = 0;
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < warp) before += scan[i + 1];
-      total += scan[i + 1];
-      mn = min(mn, ends[2 * i]);
-      mx = max(mx, ends[2 * i + 1]);
-    }
-    mx = min(mx, a.shared_len);
-    wk.base_p = mn & ~15;
-    wk.end_p = mx;
-    wk.tiles_p = p.tiles_p > 0 && mx > mn ? (mx - wk.base_p + kTile - 1) / kTile : 0;
-    const int wp = QT == 2 ? p.row_weight : 1;
-    const int up = p.tiles_p * a.nkv * wk.tiles_p * wp;
-    const int units = up + total;
-    wk.a = bound_of(units, cta, nctas);
-    wk.b = bound_of(units, cta + 1, nctas);
-    if (cta == 0) {  // for the joining kernel
-      if (threadIdx.x == 0) {
-        p.head[0] = units;
-        p.head[1] = wk.tiles_p;
-      }
-      int x = up + before;
-      for (int e = e0; e < e1; ++e) {
-        p.head[2 + e] = x;
-        const Segment g = segment_of<QT>(a, p.group, lengths(a, e / p.tiles_s), e % p.tiles_s);
-        x += g.tiles * weight_of(p, g.rows) * a.nkv;
-      }
-    }
-    // the entry and head in which this CTA's share starts
-    if (wk.a < up) {
-      const int each = wk.tiles_p * wp, seg = wk.a / each;
-      if (threadIdx.x == 0) {
-        start_entry = seg / a.nkv;
-        start_at[0] = seg * each;
-        start_at[1] = seg % a.nkv;
-      }
-    } else if (wk.a < wk.b) {
-      const int x = wk.a - up;
-      if (sum > 0 && before <= x && x < before + sum) {
-        int y = before;
-        for (int e = e0; e < e1; ++e) {
-          const Segment g = segment_of<QT>(a, p.group, lengths(a, e / p.tiles_s), e % p.tiles_s);
-          const int each = g.tiles * weight_of(p, g.rows);
-          if (x < y + each * a.nkv) {
-            const int hh = (x - y) / each;
-            start_entry = p.tiles_p + e;
-            start_at[0] = up + y + hh * each;
-            start_at[1] = hh;
-            break;
-          }
-          y += each * a.nkv;
-        }
-      }
-    }
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += y;
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 31) {
+    scan[warp] = before;
+    ends[warp][0] = lo;
+    ends[warp][1] = hi;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  wk.entry = start_entry;
-  wk.at = start_at[0];
-  wk.h = start_at[1];
-  if (wk.a >= wk.b) wk.entry = p.tiles_p + entries;
+  before -= my_units;
+  int total = 0;
+  lo = INT32_MAX;
+  hi = 0;
+#pragma unroll 1
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < warp) before += scan[i];
+    total += scan[i];
+    lo = min(lo, ends[i][0]);
+    hi = max(hi, ends[i][1]);
+  }
+  hi = min(hi, a.shared_len);
+  const int base_p = lo & ~15, end_p = hi;
+  const int tiles_p = p.tiles_p > 0 && hi > lo ? (hi - base_p + kTile - 1) / kTile : 0;
+  const int up = p.tiles_p * a.nkv * tiles_p * p.row_weight, units = up + total;
+  const int share_a = bound_of(units, cta, nctas), share_b = bound_of(units, cta + 1, nctas);
+  if (cta == 0) {  // for the joining kernel
+    if (threadIdx.x == 0) {
+      p.head[0] = units;
+      p.head[1] = tiles_p;
+    }
+    int x = up + before;
+    for (int e = e0; e < e1; ++e) {
+      int2 nl;
+      p.head[2 + e] = x;
+      x += units_of(e, &nl);
+      const int s = e / p.tiles_s;
+      if (a.kv_len[s] != nl.y) flag(a.status, DFLASH2_DEV_BAD_LENGTH);
+    }
+  }
+  // the row tile and the position in which this CTA's share starts
+  {
+    const int x = share_a - up;
+    if (share_a < share_b && x >= 0 && before <= x && x < before + my_units) {
+      int y = before;
+      for (int e = e0; e < e1; ++e) {
+        int2 nl;
+        const int all = units_of(e, &nl);
+        if (x < y + all) {
+          start[0] = e;
+          start[1] = up + y;
+          break;
+        }
+        y += all;
+      }
+    }
+  }
+  __syncthreads();
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (mbar_wait(bar, parity, abort_flag, kWaitNs)) return true;
@@ -453,50 +415,222 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const Plan p, co
     }
     return false;
   };
-  // keys a tile of which is ahead of the weights': the streams' first tiles
-  auto lead_of = [&]() { return QT == 2 && wk.g.rows > kTile ? 1 : 2; };
+  // The next segment (tiles = 0: none, or the kernel is giving up).
+  Ring<kSegs> seg_at;
+  auto next_segment = [&](SegInfo* g) {
+    bool ok = __all_sync(0xffffffffu, wait(seg_full + seg_at.slot, seg_at.round & 1));
+    if (warp < 8) ok = !bar_softmax_or(!ok);  // (their barriers need all of them, or none)
+    *g = segs[seg_at.slot];
+    if (!ok) g->tiles = 0;
+    __syncwarp();
+    if (!E4M3 || warp >= 8) {  // (the softmax warps of an 8-bit cache read the rows' scales first)
+      if (lane == 0) mbar_arrive(seg_empty + seg_at.slot);
+    }
+    return g->tiles > 0;
+  };
 
-  if (warp >= 8) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-  if (warp == 8) {
+  if (warp == 11) {
+    // ---------------------------------------------------------------- segments and their query rows
+    int q_uses[2] = {0, 0}, q_next = 0;
+    bool ok = true;
+    // positions: `at` the current row tile's first, kv heads one behind the other
+    int entry, at;
+    bool shared = share_a < up;
+    if (shared) {
+      entry = share_a / (tiles_p * p.row_weight * a.nkv);
+      at = entry * (tiles_p * p.row_weight * a.nkv);
+    } else {
+      entry = start[0];
+      at = start[1];
+    }
+    if (share_a >= share_b) at = share_b;  // (no share: nothing has set `start`)
+    while (at < share_b && ok) {
+      SegInfo g;
+      int base, tiles, w;
+      if (shared) {
+        g.s = 0;
+        g.f0 = entry * kRowTile;
+        g.rows = min(kRowTile, a.batch * p.rows - g.f0);
+        base = base_p;
+        tiles = tiles_p;
+        w = p.row_weight;
+        g.end = end_p;
+        g.n = g.len = 0;
+        // keys that all of its rows see
+        const int s0 = g.f0 / p.rows, s1 = (g.f0 + g.rows - 1) / p.rows;
+        int from = 0, to = a.shared_len;
+        for (int s = s0 + lane; s <= s1; s += 32) {
+          const int2 nl = lengths(a, s);
+          if (nl.x == 0) continue;
+          from = max(from, sees(a, nl, nl.x - 1).x);
+          to = min(to, sees(a, nl, 0).y);
+        }
+        g.all_lo = __reduce_max_sync(0xffffffffu, from);
+        g.all_hi = __reduce_min_sync(0xffffffffu, to);
+      } else {
+        g.s = p.tiles_s == 1 ? entry : entry / p.tiles_s;
+        const int i = entry - g.s * p.tiles_s;
+        const int2 nl = lengths(a, g.s);
+        const Segment x = segment_of(a, p.group, nl, i);
+        g.f0 = g.s * p.rows + i * kRowTile;
+        g.rows = x.rows;
+        base = x.base;
+        tiles = x.tiles;
+        w = weight_of(p, g.rows);
+        g.end = x.end;
+        g.n = nl.x;
+        g.len = nl.y;
+        g.all_lo = max(sees(a, nl, (i * kRowTile + g.rows - 1) / p.group).x, a.shared_len);
+        g.all_hi = sees(a, nl, i * kRowTile / p.group).y;
+      }
+      g.shared = shared;
+      g.split = g.rows <= kTile;
+      for (int h = 0; h < a.nkv && ok; ++h, at += tiles * w) {
+        if (tiles == 0 || at >= share_b) break;
+        const int k0 = at >= share_a ? 0 : (share_a - at + w - 1) / w, k1 = min(tiles, (share_b - at + w - 1) / w);
+        if (k0 >= k1) continue;
+        g.h = h;
+        g.first = base + k0 * kTile;
+        g.tiles = k1 - k0;
+        g.slot = k0 == 0 && k1 == tiles && p.tiles_p == 0 ? -1 : entry * a.nkv + h + cta;
+        g.q = g.split ? q_next : 0;
+        // query rows of both or of one place, K-major with the 128-byte swizzle
+        for (int b = g.split ? g.q : 0; b < (g.split ? g.q + 1 : 2); ++b) {
+          if (q_uses[b] > 0) ok = wait(q_empty + b, (q_uses[b] - 1) & 1) && ok;
+          ++q_uses[b];
+        }
+        if (g.split) q_next ^= 1;
+        if (seg_at.round > 0) ok = wait(seg_empty + seg_at.slot, (seg_at.round - 1) & 1) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (E4M3) {
+          // A row's largest magnitude becomes 2^7 .. 2^8; high codes at 0, low
+          // codes at 16 KB of a place.  Eight lanes take a row.
+          float* qscale = reinterpret_cast<float*>(sm + L::QSCALE) + seg_at.slot * kRowTile;
+#pragma unroll 1
+          for (int r0 = 0; r0 < ((g.rows + 3) & ~3); r0 += 4) {
+            const int fr = r0 + (lane >> 3), f = g.f0 + fr, part = lane & 7;
+            const int s = g.shared ? f / p.rows : g.s, local = f - s * p.rows, t = local / p.group;
+            const bool real = fr < g.rows && (!g.shared || !a.n_new || t < a.n_new[s]);
+            uint4 x[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+            if (real) {
+              const bf16* src = a.q + ((size_t)s * a.n_tok + t) * a.q_stride + (size_t)(h * p.group + local - t * p.group) * kD;
+              x[0] = reinterpret_cast<const uint4*>(src)[2 * part];
+              x[1] = reinterpret_cast<const uint4*>(src)[2 * part + 1];
+            }
+            const uint32_t w8[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = max(max(top, w8[i] & 0x7f800000u), (w8[i] << 16) & 0x7f800000u);
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int e = top >= 0x7f800000u ? 254 : max(1, (int)(top >> 23));
+            // 2^(7 - (e - 127)) = 2^(134 - e), in two factors that are floats
+            const int e1_ = (134 - e) / 2, e2_ = (134 - e) - e1_;
+            const float up0 = __uint_as_float((uint32_t)(127 + e1_) << 23), up1 = __uint_as_float((uint32_t)(127 + e2_) << 23);
+            uint32_t hi_c[4], lo_c[4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float x0 = __uint_as_float(w8[i] << 16) * up0 * up1;
+              const float x1 = __uint_as_float(w8[i] & 0xffff0000u) * up0 * up1;
+              const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+              const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h2, __NV_E4M3);
+              const float2 back = __half22float2(__half2(hr));
+              const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(x0 - back.x, x1 - back.y), __NV_SATFINITE, __NV_E4M3);
+              hi_c[i >> 1] = (i & 1) ? hi_c[i >> 1] | (h2 << 16) : h2;
+              lo_c[i >> 1] = (i & 1) ? lo_c[i >> 1] | (l2 << 16) : l2;
+            }
+            const int r = fr & (kTile - 1);
+            uint8_t* dst = sm + L::Q + (g.split ? g.q : fr / kTile) * 32768 + r * 128 + ((part ^ (r & 7)) << 4);
+            *reinterpret_cast<uint4*>(dst) = make_uint4(hi_c[0], hi_c[1], hi_c[2], hi_c[3]);
+            *reinterpret_cast<uint4*>(dst + 16384) = make_uint4(lo_c[0], lo_c[1], lo_c[2], lo_c[3]);
+            // the factor of its scores; a row that is not finite has no result
+            if (part == 0)
+              qscale[fr] = top >= 0x7f800000u ? __int_as_float(0x7fffffff)
+                                              : __uint_as_float((uint32_t)(127 - e1_) << 23) *
+                                                    __uint_as_float((uint32_t)(127 - e2_) << 23);
+          }
+        } else {
+#pragma unroll 4
+          for (int i = lane; i < g.rows * 16; i += 32) {
+            const int fr = i >> 4, c = i & 15, f = g.f0 + fr;
+            const int s = g.shared ? f / p.rows : g.s, local = f - s * p.rows, t = local / p.group;
+            const bool real = !g.shared || !a.n_new || t < a.n_new[s];
+            const bf16* src = a.q + ((size_t)s * a.n_tok + t) * a.q_stride + (size_t)(h * p.group + local - t * p.group) * kD;
+            const int r = fr & (kTile - 1);
+            cp_async16(sm + L::Q + (g.split ? g.q : fr / kTile) * 32768 + (c >> 3) * 16384 + r * 128 +
+                           (((c & 7) ^ (r & 7)) << 4), real ? src + c * 8 : a.q, real);
+          }
+          cp_async_commit();
+          cp_async_wait<0>();
+        }
+        fence_proxy_async_smem();
+        if (lane == 0) segs[seg_at.slot] = g;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(seg_full + seg_at.slot);
+        seg_at.step();
+      }
+      // (after the last kv head `at` is the next row tile's first position)
+      ++entry;
+      if (shared && entry == p.tiles_p) {
+        shared = false;
+        entry = 0;
+      }
+    }
+    // the end
+    if (seg_at.round > 0) wait(seg_empty + seg_at.slot, (seg_at.round - 1) & 1);
+    if (lane == 0) segs[seg_at.slot].tiles = 0;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(seg_full + seg_at.slot);
+  } else if (warp == 8) {
     // ---------------------------------------------------------------- loads
     const uint64_t pol = policy_evict_first();
     const int absent = a.n_pages * a.page_size;  // a row past the pool: the copy fills zeros
     Ring<NS> at;
     bool ok = true;
-    for (bool more = wk.next(true); more && ok; more = wk.next(false)) {
-      const int nt = wk.k1 - wk.k0, lead = lead_of();
-      const int32_t* table = a.block_table + (size_t)(wk.shared() ? 0 : wk.s()) * a.max_pages;
-      auto load = [&](int t, bool value) {
-        const int slot = at.slot;
+    SegInfo g;
+    for (; ok && next_segment(&g); seg_at.step()) {
+      const int lead = g.split ? 2 : 1, x_h = g.h * (E4M3 ? 64 : 128);
+      const int32_t* table = a.block_table + (size_t)g.s * a.max_pages;
+      // lane i < 8: pool row of 16-key group i of a tile
+      auto row_of = [&](int t) {
+        const int pos = g.first + t * kTile + 16 * lane;
         int row = absent;
-        if (lane < 8) {
-          const int pos = wk.g.base + (wk.k0 + t) * kTile + 16 * lane;
-          if (pos < wk.g.end) {
-            const int page = table[pos / a.page_size];
-            if (page >= 0 && page < a.n_pages) row = page * a.page_size + pos % a.page_size;
-          }
+        if (lane < 8 && t < g.tiles && pos < g.end) {
+          const int page = table[pos / a.page_size];
+          if (page >= 0 && page < a.n_pages) row = page * a.page_size + pos % a.page_size;
         }
+        return row;
+      };
+      auto load = [&](int row, const void* map) {
+        const int slot = at.slot;
         if (at.round > 0) ok = wait(empty + slot, (at.round - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         uint8_t* dst = sm + L::RING + slot * L::SLOT;
         if (lane == 0) mbar_arrive_expect_tx(full + slot, L::SLOT);
         __syncwarp();
-        const void* map = value ? &tm_v : &tm_k;
         if (E4M3) {
-          if (lane < 8) tma_load_2d(dst + lane * 2048, map, full + slot, wk.h * 64, row, pol);
+          if (lane < 8) tma_load_2d(dst + lane * 2048, map, full + slot, x_h, row, pol);
         } else {
           const int r = __shfl_sync(0xffffffffu, row, lane & 7);
           if (lane < 16)
-            tma_load_2d(dst + (lane >> 3) * 16384 + (lane & 7) * 2048, map, full + slot, wk.h * 128 + (lane >> 3) * 64,
-                        r, pol);
+            tma_load_2d(dst + (lane >> 3) * 16384 + (lane & 7) * 2048, map, full + slot, x_h + (lane >> 3) * 64, r, pol);
         }
         at.step();
       };
-      for (int t = -lead; t < nt && ok; ++t) {
-        if (t >= 0) load(t, true);
-        if (t + lead < nt && ok) load(t + lead, false);
+      // rows of tiles t, t + 1, t + 2 and, on its way, t + 3
+      int r0 = row_of(0), r1 = row_of(1), r2 = row_of(2);
+      load(r0, &tm_k);
+      if (lead == 2 && g.tiles > 1 && ok) load(r1, &tm_k);
+#pragma unroll 1
+      for (int t = 0; t < g.tiles && ok; ++t) {
+        const int r3 = row_of(t + 3);
+        load(r0, &tm_v);
+        if (t + lead < g.tiles && ok) load(lead == 2 ? r2 : r1, &tm_k);
+        r0 = r1;
+        r1 = r2;
+        r2 = r3;
       }
     }
     // copies in flight land before the CTA ends
@@ -507,244 +641,234 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const Plan p, co
     }
   } else if (warp == 9) {
     // ---------------------------------------------------------------- MMA issue
-    if (lane == 0) {
-      const uint32_t ring = smem_u32(sm + L::RING), qs = smem_u32(sm + L::Q);
-      // A K-major, B = K rows K-major; B = V rows MN-major; 8-bit weights are e5m2
-      const uint32_t id_s = E4M3 ? (1u << 4) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24) : idesc_bf16_f32(kTile, kTile);
-      const uint32_t id_o =
-          (E4M3 ? (1u << 4) | (1u << 7) | ((kD >> 3) << 17) | ((kTile >> 4) << 24) : idesc_bf16_f32(kTile, kD)) |
-          (1u << 16);
-      Ring<NS> at;
-      uint32_t n_p = 0, segs = 0;  // bit j: parity of stream j's weights
-      bool ok = true;
-      for (bool more = wk.next(true); more && ok; more = wk.next(false)) {
-        const int nt = wk.k1 - wk.k0, lead = lead_of();
-        ok = wait(q_ready, segs & 1);
-        ++segs;
-        tc_fence_after();
-        auto scores = [&](int j, int slot) {  // stream j's rows against the keys in a slot
-          const uint64_t kd = sdesc_sw128(ring + slot * L::SLOT);
-          const uint64_t qd = sdesc_sw128(qs + (lead == 1 ? j : 0) * 32768);
-          const uint32_t d = tmem + s_col(j);
-          if (E4M3) {
-#pragma unroll
-            for (int x = 0; x < 8; ++x)  // high, then low codes of q; 32 dims each
-              mma_ss<true>(d, qd + (uint64_t)((x >> 2) * 1024 + (x & 3) * 2), kd + (uint64_t)((x & 3) * 2), id_s,
-                           x > 0 ? 1u : 0u);
-          } else {
-#pragma unroll
-            for (int x = 0; x < 8; ++x)  // 16 dims each
-              mma_ss<false>(d, qd + (uint64_t)((x >> 2) * 1024 + (x & 3) * 2),
-                            kd + (uint64_t)((x >> 2) * 1024 + (x & 3) * 2), id_s, x > 0 ? 1u : 0u);
-          }
-          umma_commit(s_full + j);
-        };
-        auto products = [&](int j, int slot, bool first) {
-          const uint64_t vd = sdesc_mn_sw128(ring + slot * L::SLOT, 16384, 1024);
-          const uint32_t d = tmem + o_col(j), pc = tmem + s_col(j);
-          if (E4M3) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x)  // 32 keys each, three parts
-#pragma unroll
-              for (int part = 0; part < 3; ++part)
-                mma_ts<true>(d, pc + 32u * x + 8u * part, vd + (uint64_t)(x * 256), id_o,
-                             (first && x == 0 && part == 0) ? 0u : 1u);
-          } else {
-#pragma unroll
-            for (int x = 0; x < 8; ++x)  // 16 keys each, high and low parts
-#pragma unroll
-              for (int part = 0; part < 2; ++part)
-                mma_ts<false>(d, pc + 32u * (x >> 1) + 8u * (x & 1) + 16u * part, vd + (uint64_t)(x * 128), id_o,
-                              (first && x == 0 && part == 0) ? 0u : 1u);
-          }
-        };
-        auto landed = [&](const Ring<NS>& i) {
-          ok = ok && wait(full + i.slot, i.round & 1);
-          tc_fence_after();
-        };
-        auto weights = [&](int j) {
-          ok = ok && wait(p_ready + j, (n_p >> j) & 1);
-          n_p ^= 1u << j;
-          tc_fence_after();
-        };
-        if (lead == 2) {
-          // stream t % 2 takes tile t; slots in order K0 K1 V0 K2 V1 K3 ...
-          for (int t = 0; t < min(2, nt) && ok; ++t) {
-            landed(at);
-            if (!ok) break;
-            scores(t, at.slot);
-            umma_commit(empty + at.slot);
-            at.step();
-          }
-          for (int t = 0; t < nt && ok; ++t) {
-            landed(at);
-            weights(t & 1);
-            if (!ok) break;
-            products(t & 1, at.slot, t < 2);
-            umma_commit(empty + at.slot);
-            if (t + 2 >= nt) umma_commit(o_done + (t & 1));
-            at.step();
-            if (t + 2 < nt) {
-              landed(at);
-              if (!ok) break;
-              scores(t & 1, at.slot);
-              umma_commit(empty + at.slot);
-              at.step();
-            }
-          }
+    const uint32_t one = lane == 0;
+    // shared addresses in the descriptors' 16-byte units; their upper words are constant
+    const uint32_t ring = __shfl_sync(0xffffffffu, smem_u32(sm + L::RING), 0) >> 4;
+    const uint32_t qs = __shfl_sync(0xffffffffu, smem_u32(sm + L::Q), 0) >> 4;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    constexpr uint64_t kKMajor = ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+    constexpr uint64_t kMnMajor = ((uint64_t)(16384 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+    // A K-major, B = K rows K-major; B = V rows MN-major; 8-bit weights are e5m2
+    constexpr uint32_t id_s = E4M3 ? (1u << 4) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24) : idesc_bf16_f32(kTile, kTile);
+    constexpr uint32_t id_o =
+        (E4M3 ? (1u << 4) | (1u << 7) | ((kD >> 3) << 17) | ((kTile >> 4) << 24) : idesc_bf16_f32(kTile, kD)) |
+        (1u << 16);
+    Ring<NS> at;
+    uint32_t n_p = 0;  // bit j: parity of stream j's weights
+    bool ok = true;
+    SegInfo g;
+    for (; ok && next_segment(&g); seg_at.step()) {
+      const int nt = __shfl_sync(0xffffffffu, g.tiles, 0), lead = __shfl_sync(0xffffffffu, g.split ? 2 : 1, 0);
+      const uint32_t q0 = qs + __shfl_sync(0xffffffffu, g.q, 0) * 2048;
+      auto scores = [&](int j, int slot) {  // stream j's rows against the keys in a slot
+        const uint32_t kd = ring + slot * (L::SLOT >> 4), qd = q0 + (lead == 1 ? j : 0) * 2048;
+        const uint32_t d = tm + s_col(j);
+#pragma unroll 4
+        for (int x = 0; x < 8; ++x)  // 16 dims each; 8 bits: 32 dims each, with the high, then the low codes of q
+          mma_ss<E4M3>(d, kKMajor | (qd + (x >> 2) * 1024 + (x & 3) * 2),
+                       kKMajor | (kd + (E4M3 ? 0 : (x >> 2) * 1024) + (x & 3) * 2), id_s, x > 0 ? 1u : 0u, one);
+        commit(s_full + j, one);
+      };
+      auto products = [&](int j, int slot, uint32_t acc) {
+        const uint32_t vd = ring + slot * (L::SLOT >> 4);
+        const uint32_t d = tm + o_col(j), pc = tm + s_col(j);
+        if (E4M3) {
+#pragma unroll 3
+          for (int x = 0; x < 12; ++x)  // 32 keys each, three parts
+            mma_ts<true>(d, pc + 32 * (x / 3) + 8 * (x % 3), kMnMajor | (vd + (x / 3) * 256), id_o, x > 0 ? 1u : acc, one);
         } else {
-          // both streams take every tile; slots in order K0 V0 K1 V1 ...
+#pragma unroll 4
+          for (int x = 0; x < 16; ++x)  // 16 keys each, high and low parts
+            mma_ts<false>(d, pc + 32 * (x >> 2) + 8 * ((x >> 1) & 1) + 16 * (x & 1), kMnMajor | (vd + (x >> 1) * 128), id_o,
+                          x > 0 ? 1u : acc, one);
+        }
+      };
+      auto landed = [&](const Ring<NS>& i) {
+        ok = ok && wait(full + i.slot, i.round & 1);
+        tc_fence_after();
+      };
+      auto weights = [&](int j) {
+        ok = ok && wait(p_ready + j, (n_p >> j) & 1);
+        n_p ^= 1u << j;
+        tc_fence_after();
+      };
+      if (lead == 2) {
+        // stream t % 2 takes tile t; slots in order K0 K1 V0 K2 V1 K3 ...
+        for (int t = 0; t < min(2, nt) && ok; ++t) {
           landed(at);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          scores(0, at.slot);
-          scores(1, at.slot);
-          umma_commit(empty + at.slot);
+          scores(t, at.slot);
+          commit(empty + at.slot, one);
           at.step();
-          for (int t = 0; t < nt && ok; ++t) {
-            const Ring<NS> iv = at, ik = at.ahead(1);
-            const bool again = t + 1 < nt;
-            landed(iv);
-            for (int j = 0; j < 2 && ok; ++j) {
-              weights(j);
-              if (!ok) break;
-              products(j, iv.slot, t == 0);
-              if (j == 1) umma_commit(empty + iv.slot);
-              if (again) {
-                if (j == 0) landed(ik);
-                if (!ok) break;
-                scores(j, ik.slot);
-                if (j == 1) umma_commit(empty + ik.slot);
-              } else {
-                umma_commit(o_done + j);
-              }
-            }
+        }
+        for (int t = 0; t < nt && ok; ++t) {
+          landed(at);
+          weights(t & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          products(t & 1, at.slot, t < 2 ? 0u : 1u);
+          commit(empty + at.slot, one);
+          if (t + 2 >= nt) commit(o_done + (t & 1), one);
+          at.step();
+          if (t + 2 < nt) {
+            landed(at);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            scores(t & 1, at.slot);
+            commit(empty + at.slot, one);
             at.step();
-            if (again) at.step();
           }
         }
+      } else {
+        // both streams take every tile; slots in order K0 V0 K1 V1 ...
+        landed(at);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        scores(0, at.slot);
+        scores(1, at.slot);
+        commit(empty + at.slot, one);
+        at.step();
+        for (int t = 0; t < nt && ok; ++t) {
+          const Ring<NS> iv = at, ik = at.ahead(1);
+          const bool again = t + 1 < nt;
+          landed(iv);
+#pragma unroll 1
+          for (int j = 0; j < 2; ++j) {
+            weights(j);
+            if (again && j == 0) landed(ik);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            products(j, iv.slot, t > 0 ? 1u : 0u);
+            if (j == 1) commit(empty + iv.slot, one);
+            if (again) {
+              scores(j, ik.slot);
+              if (j == 1) commit(empty + ik.slot, one);
+            } else {
+              commit(o_done + j, one);
+            }
+          }
+          at.step();
+          if (again) at.step();
+        }
       }
-      umma_commit(drain);
-      volatile int never = 0;
-      if (!mbar_wait(drain, 0, &never, kWaitNs)) flag(a.status, DFLASH2_DEV_WAIT_TIMEOUT);
+      ok = __all_sync(0xffffffffu, ok);
     }
+    commit(drain, one);
+    volatile int never = 0;
+    if (!mbar_wait(drain, 0, &never, kWaitNs) && lane == 0) flag(a.status, DFLASH2_DEV_WAIT_TIMEOUT);
     __syncwarp();
   } else if (warp == 10) {
     // ---------------------------------------------------------------- tile info
-    Ring<NS> vat;       // slot of the next value tile
+    Ring<NS> vat;  // slot of the next value tile
     Ring<kInfo> iat;
     bool ok = true;
-    for (bool more = wk.next(true); more && ok; more = wk.next(false)) {
-      const int nt = wk.k1 - wk.k0, lead = lead_of();
-      const int f0 = wk.first_row();
-      const int32_t* table = a.block_table + (size_t)(wk.shared() ? 0 : wk.s()) * a.max_pages;
-      // keys that all of the segment's rows see: [lo, hi)
-      int lo = 0, hi = INT32_MAX;
-      if (wk.shared()) {
-        const int s0 = f0 / p.rows, s1 = (f0 + wk.g.rows - 1) / p.rows;
-        for (int s = s0 + lane; s <= s1; s += 32) {
-          const int2 nl = lengths(a, s);
-          if (nl.x == 0) continue;
-          lo = max(lo, sees(a, nl, nl.x - 1).x);
-          hi = min(hi, sees(a, nl, 0).y);
+    SegInfo g;
+    for (; ok && next_segment(&g); seg_at.step()) {
+      const int lead = g.split ? 2 : 1;
+      const int32_t* table = a.block_table + (size_t)g.s * a.max_pages;
+      for (int x = min(lead, g.tiles); x > 0; --x) vat.step();  // lead tiles of keys go first
+      // lane i < 8: pool row of 16-key group i, or -1
+      auto row_of = [&](int t) {
+        const int pos = g.first + t * kTile + 16 * lane;
+        int row = -1;
+        if (lane < 8 && t < g.tiles && pos < g.end) {
+          const int page = table[pos / a.page_size];
+          if (page >= 0 && page < a.n_pages) row = page * a.page_size + pos % a.page_size;
+          else flag(a.status, DFLASH2_DEV_BAD_PAGE);
         }
-        lo = __reduce_max_sync(0xffffffffu, lo);
-        hi = min(__reduce_min_sync(0xffffffffu, hi), a.shared_len);
-      } else {
-        const int r0 = f0 - wk.s() * p.rows;
-        lo = max(sees(a, wk.nl, (r0 + wk.g.rows - 1) / p.group).x, a.shared_len);
-        hi = sees(a, wk.nl, r0 / p.group).y;
-      }
-      for (int x = min(lead, nt); x > 0; --x) vat.step();  // lead tiles of keys go first
-      for (int t = 0; t < nt && ok; ++t) {
-        const int slot = iat.slot;
+        return row;
+      };
+      // exponent bytes of keys 32 i + lane: keys' in the low halves, values' in the high ones
+      auto bytes_of = [&](int t, int row, uint32_t (&b)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = 32 * i + lane, r = __shfl_sync(0xffffffffu, row, key >> 4);
+          b[i] = 0;
+          if (r >= 0 && g.first + t * kTile + key < g.end) {
+            const size_t x = ((size_t)r + (key & 15)) * a.nkv + g.h;
+            b[i] = a.k_exp[x] | ((uint32_t)a.v_exp[x] << 16);
+          }
+        }
+      };
+      // what a tile takes is asked for one (8 bits: and two) tiles before
+      int r0 = row_of(0), r1 = row_of(1);
+      uint32_t b0[4];
+      if (E4M3) bytes_of(0, r0, b0);
+#pragma unroll 1
+      for (int t = 0; t < g.tiles && ok; ++t) {
+        const int r2 = row_of(t + 2);
+        uint32_t b1[4];
+        if (E4M3) bytes_of(t + 1, r1, b1);
+        const int slot = iat.slot, k0 = g.first + t * kTile;
         TileInfo* info;
         if (E4M3) info = reinterpret_cast<TileInfo*>(sm + L::INFO + slot * L::INFOS);
         else info = reinterpret_cast<TileInfo*>(sm + L::INFO + slot * L::INFOS - offsetof(TileInfo, bad));
-        const int k0 = wk.g.base + (wk.k0 + t) * kTile;
-        bool there = false;
-        int row = 0;
-        if (lane < 8 && k0 + 16 * lane < wk.g.end) {
-          const int pos = k0 + 16 * lane, page = table[pos / a.page_size];
-          there = page >= 0 && page < a.n_pages;
-          if (there) row = page * a.page_size + pos % a.page_size;
-          else flag(a.status, DFLASH2_DEV_BAD_PAGE);
-        }
-        const uint32_t groups = __ballot_sync(0xffffffffu, there);
-        const bool mixed = k0 < lo || k0 + kTile > hi || groups != 0xffu;
-        float ks[4], vs[4];
-        int top = 0;
-        if (E4M3) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {  // keys 32 i + lane
-            const int key = 32 * i + lane;
-            const int r = __shfl_sync(0xffffffffu, row, key >> 4);
-            const bool in = ((groups >> (key >> 4)) & 1) && k0 + key < wk.g.end;
-            const size_t at = ((size_t)r + (key & 15)) * a.nkv + wk.h;
-            const int kb = in ? min((int)a.k_exp[at], 254) : 0, vb = in ? min((int)a.v_exp[at], 254) : 0;
-            ks[i] = __uint_as_float((uint32_t)kb << 23);
-            vs[i] = __uint_as_float((uint32_t)vb << 23);
-            top = max(top, vb);
-          }
-          top = __reduce_max_sync(0xffffffffu, top);
-        }
+        const uint32_t groups = __ballot_sync(0xffffffffu, r0 >= 0);
+        const bool mixed = k0 < g.all_lo || k0 + kTile > g.all_hi || groups != 0xffu;
         if (iat.round > 0) ok = wait(info_empty + slot, (iat.round - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (E4M3) {
+          uint32_t top = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            info->ks[32 * i + lane] = ks[i];
-            info->vs[32 * i + lane] = vs[i];
+            const uint32_t kb = min(b0[i] & 0xffffu, 254u), vb = min(b0[i] >> 16, 254u);
+            info->ks[32 * i + lane] = __uint_as_float(kb << 23);
+            info->vs[32 * i + lane] = __uint_as_float(vb << 23);
+            top = max(top, vb);
+            b0[i] = b1[i];
           }
+          top = __reduce_max_sync(0xffffffffu, top);
+          if (lane == 0) info->vmax = (float)max((int)top - 127, -60);
         }
         if (lane < 4) info->bad[lane] = 0;
-        if (lane == 0) {
-          info->groups = groups;
-          info->mixed = mixed;
-          info->vmax = (float)max(top - 127, -60);
-        }
+        if (lane == 0) info->groups = groups;
         __syncwarp();
         if (mixed) {
-          if (!wait(full + vat.slot, vat.round & 1)) ok = false;
-          ok = __all_sync(0xffffffffu, ok);
+          ok = __all_sync(0xffffffffu, wait(full + vat.slot, vat.round & 1));
           if (!ok) break;
           uint8_t* v = sm + L::RING + vat.slot * L::SLOT;
-          const int from = k0 + kTile > hi ? max(0, hi - k0) : kTile;  // keys from here on, and below `to`
-          const int to = k0 < lo ? min(kTile, lo - k0) : 0;
-          for (int key = 0; key < kTile; ++key) {
-            if (key >= to && key < from) {
-              key = from - 1;
-              continue;
+          // keys below `to` and from `from` on are not seen by every row; behind
+          // `past` a page holds what it held before (whole absent groups are zeros)
+          const int to = min(kTile, g.all_lo - k0), past = g.end - k0, top = min(kTile, (past + 15) & ~15);
+          int key0 = to > 0 ? 0 : max(0, g.all_hi - k0) & ~3;
+          constexpr int W = E4M3 ? 8 : 16;  // lanes of a row, 16 bytes each
+#pragma unroll 1
+          while (key0 < top) {
+            const int key = key0 + lane / W, c = lane & (W - 1);
+            uint4* q = reinterpret_cast<uint4*>(v + (E4M3 ? 0 : (c >> 3) * 16384) + key * 128 + (c & 7) * 16);
+            const bool in = key < top;
+            uint32_t w[4] = {0u, 0u, 0u, 0u};
+            if (in) {
+              const uint4 x = *q;
+              w[0] = x.x;
+              w[1] = x.y;
+              w[2] = x.z;
+              w[3] = x.w;
             }
-            // keys past the end hold what the page held before
-            const bool past = k0 + key >= wk.g.end;
             bool bad = false;
-            if (E4M3) {
-              uint32_t* q = reinterpret_cast<uint32_t*>(v + key * 128 + lane * 4);
-              uint32_t x = *q, nan = 0;
 #pragma unroll
-              for (int b = 0; b < 4; ++b)
-                if (((x >> (8 * b)) & 0x7fu) == 0x7fu) nan |= 0xffu << (8 * b);
-              bad = nan != 0;
-              if (past || bad) *q = past ? 0u : x & ~nan;
-            } else {
-              uint2* q = reinterpret_cast<uint2*>(v + (lane >> 4) * 16384 + key * 128 + (lane & 15) * 8);
-              uint2 x = *q;
-              uint32_t w[2] = {x.x, x.y};
+            for (int i = 0; i < 4; ++i) {
+              uint32_t gone = 0;
+              if (E4M3) {
 #pragma unroll
-              for (int b = 0; b < 2; ++b) {
-                if ((w[b] & 0x7f80u) == 0x7f80u) {
-                  bad = true;
-                  w[b] &= 0xffff0000u;
-                }
-                if ((w[b] & 0x7f800000u) == 0x7f800000u) {
-                  bad = true;
-                  w[b] &= 0xffffu;
-                }
+                for (int b = 0; b < 4; ++b)
+                  if (((w[i] >> (8 * b)) & 0x7fu) == 0x7fu) gone |= 0xffu << (8 * b);
+              } else {
+                if ((w[i] & 0x7f80u) == 0x7f80u) gone |= 0xffffu;
+                if ((w[i] & 0x7f800000u) == 0x7f800000u) gone |= 0xffff0000u;
               }
-              if (past || bad) *q = past ? make_uint2(0u, 0u) : make_uint2(w[0], w[1]);
+              bad |= gone != 0;
+              w[i] &= ~gone;
             }
-            if (__any_sync(0xffffffffu, bad && !past) && lane == 0) info->bad[key >> 5] |= 1u << (key & 31);
+            const bool behind = key >= past;
+            if (in && (bad || behind))
+              *q = behind ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(w[0], w[1], w[2], w[3]);
+            const uint32_t votes = __ballot_sync(0xffffffffu, bad && !behind);
+            if (lane % W == 0 && ((votes >> lane) & ((1u << W) - 1u))) atomicOr(&info->bad[key >> 5], 1u << (key & 31));
+            key0 += 32 / W;
+            if (key0 >= to && key0 < ((g.all_hi - k0) & ~3)) key0 = (g.all_hi - k0) & ~3;
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -752,99 +876,43 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const Plan p, co
         if (lane == 0) mbar_arrive(info_full + slot);
         iat.step();
         vat.step();
-        if (t + lead < nt) vat.step();  // the next key tile's
+        if (t + lead < g.tiles) vat.step();  // the next key tile's
+        r0 = r1;
+        r1 = r2;
       }
     }
-  }
   } else {
     // ---------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int j = warp >> 2, r = threadIdx.x & 127;  // stream, row of its tile
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float scale = a.scale * 1.4426950408889634f;
-    const float head_room = E4M3 ? 15.f : 8.f;  // how far a weight may pass 2^0 (E4M3: of weight times scale)
+    const float head_room = E4M3 ? 15.f : 8.f;  // how far a weight may pass 2^0 (8 bits: weight times scale)
     uint32_t n_s = 0, n_o = 0, tiles = 0;
-    bool ok = true;
-    for (bool more = wk.next(true); more; more = wk.next(false)) {
-      const int nt = wk.k1 - wk.k0;
-      const bool split = lead_of() == 2;  // the streams share the rows
+    SegInfo g;
+    for (; next_segment(&g); seg_at.step()) {
+      const int nt = g.tiles;
+      const bool split = g.split != 0;  // the streams share the rows
       const int fr = (split ? 0 : j * kTile) + r;
-      const bool mine = fr < wk.g.rows;
-      const int f = wk.first_row() + (mine ? fr : 0);
-      const int s = f / p.rows, t_row = (f / p.group) % a.n_tok, head = wk.h * p.group + f % p.group;
+      const bool mine = fr < g.rows;
+      const int f = g.f0 + (mine ? fr : 0);
+      const int s = g.shared ? f / p.rows : g.s, local = f - s * p.rows, t_row = local / p.group;
+      const int head = g.h * p.group + local - t_row * p.group;
       int2 see = make_int2(0, INT32_MAX);  // (rows that do not exist see everything: nothing to mask)
       bool real = mine;
-      if (mine) {
-        const int2 nl = wk.shared() ? lengths(a, s) : wk.nl;
-        see = t_row < nl.x ? sees(a, nl, t_row) : make_int2(0, 0);
-        real = t_row < nl.x;
-        if (wk.shared()) see.y = min(see.y, a.shared_len);
-        else see.x = max(see.x, a.shared_len);
-      }
-      bar_softmax();  // both streams are done with the last segment
-      // query rows, K-major with the 128-byte swizzle
       float rs = scale;  // factor of a row's scores
-      uint8_t* qdst = sm + L::Q + (split ? 0 : j) * 32768;
-      const bf16* qrow = a.q + ((size_t)s * a.n_tok + t_row) * a.q_stride + (size_t)head * kD;
-      if (E4M3) {
-        // the row's largest magnitude becomes 2^7 .. 2^8; high codes at 0, low codes at 16 KB
-        uint4 x[16];
-        uint32_t top = 0;
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          x[c] = real ? reinterpret_cast<const uint4*>(qrow)[c] : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            top = max(top, w[i] & 0x7f800000u);
-            top = max(top, (w[i] << 16) & 0x7f800000u);
-          }
-        }
-        const int e = top >= 0x7f800000u ? 254 : max(1, (int)(top >> 23));
-        // 2^(7 - (e - 127)) = 2^(134 - e), in two factors that are floats
-        const int e_half = (134 - e) / 2;
-        const float up0 = __uint_as_float((uint32_t)(127 + e_half) << 23);
-        const float up1 = __uint_as_float((uint32_t)(127 + (134 - e) - e_half) << 23);
-        rs = scale * __uint_as_float((uint32_t)(127 - e_half) << 23) *
-             __uint_as_float((uint32_t)(127 - ((134 - e) - e_half)) << 23);
-        if (top >= 0x7f800000u) rs = __int_as_float(0x7fffffff);  // a row that is not finite has no result
-        if (!split || j == 0) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {  // 16 dims: 16 bytes of codes
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint4& u = x[2 * c + (i >> 1)];
-              const uint32_t w[2] = {(i & 1) ? u.z : u.x, (i & 1) ? u.w : u.y};
-              uint32_t h2[2], l2[2];
-#pragma unroll
-              for (int b = 0; b < 2; ++b) {
-                const float v0 = __uint_as_float(w[b] << 16) * up0 * up1;
-                const float v1 = __uint_as_float(w[b] & 0xffff0000u) * up0 * up1;
-                h2[b] = __nv_cvt_float2_to_fp8x2(make_float2(v0, v1), __NV_SATFINITE, __NV_E4M3);
-                const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h2[b], __NV_E4M3);
-                const float2 back = __half22float2(__half2(hr));
-                l2[b] = __nv_cvt_float2_to_fp8x2(make_float2(v0 - back.x, v1 - back.y), __NV_SATFINITE, __NV_E4M3);
-              }
-              hi[i] = h2[0] | (h2[1] << 16);
-              lo[i] = l2[0] | (l2[1] << 16);
-            }
-            const int at = r * 128 + ((c ^ (r & 7)) << 4);
-            *reinterpret_cast<uint4*>(qdst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(qdst + 16384 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
-        }
-      } else if (!split || j == 0) {
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const uint4 x = real ? reinterpret_cast<const uint4*>(qrow)[c] : make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(qdst + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
-        }
+      if (mine) {
+        const int2 nl = g.shared ? lengths(a, s) : make_int2(g.n, g.len);
+        real = t_row < nl.x;
+        see = real ? sees(a, nl, t_row) : make_int2(0, 0);
+        if (g.shared) see.y = min(see.y, a.shared_len);
+        else see.x = max(see.x, a.shared_len);
+        if (E4M3) rs *= reinterpret_cast<const float*>(sm + L::QSCALE)[seg_at.slot * kRowTile + fr];
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_ready);
-
+      if (E4M3) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(seg_empty + seg_at.slot);
+      }
+      const int first = g.first;
       float ref = kNone, sum = 0.f;
       bool poison = false;
       const bool idle = !__any_sync(0xffffffffu, mine);  // no row of this warp exists
@@ -855,49 +923,60 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const Plan p, co
         const TileInfo* info;
         if (E4M3) info = reinterpret_cast<const TileInfo*>(sm + L::INFO + slot * L::INFOS);
         else info = reinterpret_cast<const TileInfo*>(sm + L::INFO + slot * L::INFOS - offsetof(TileInfo, bad));
-        ok = wait(info_full + slot, (tile / kInfo) & 1) && ok;
-        ok = wait(s_full + j, n_s & 1) && ok;
+        wait(info_full + slot, (tile / kInfo) & 1);
+        wait(s_full + j, n_s & 1);
         ++n_s;
         __syncwarp();
         tc_fence_after();
         if (!idle) {
-          float x[kTile];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(lanes + s_col(j) + 32 * c, x + 32 * c);
-          tmem_ld_wait();
-          if (E4M3) {
-#pragma unroll
-            for (int i = 0; i < kTile; i += 4) {
-              const float4 k4 = *reinterpret_cast<const float4*>(info->ks + i);
-              x[i] *= k4.x;
-              x[i + 1] *= k4.y;
-              x[i + 2] *= k4.z;
-              x[i + 3] *= k4.w;
-            }
-          }
-          const int k0 = wk.g.base + (wk.k0 + t) * kTile;
+          const int k0 = first + t * kTile;
           const int v0 = see.x - k0, v1 = see.y > k0 + kTile ? kTile : see.y - k0;  // keys of the tile that it sees
           const uint32_t groups = info->groups;
           const bool cut = __any_sync(0xffffffffu, mine && (v0 > 0 || v1 < kTile)) || groups != 0xffu;
-          if (cut) {
+          // bit i: key 32 c + i is seen
+          auto seen = [&](int c) {
+            const int from = min(32, max(0, v0 - 32 * c)), to = min(32, max(0, v1 - 32 * c));
+            uint32_t m = (to == 32 ? 0xffffffffu : (1u << to) - 1u) & (from == 32 ? 0u : 0xffffffffu << from);
+            if (!((groups >> (2 * c)) & 1)) m &= 0xffff0000u;
+            if (!((groups >> (2 * c + 1)) & 1)) m &= 0x0000ffffu;
+            return m;
+          };
+          // The scores are read twice, in pieces of 32 keys by a loop that is
+          // not unrolled: the roles' code has to stay in the instruction
+          // cache (with all 128 scores in registers and the loops unrolled,
+          // fetching it took most of the time).
+          auto fetch = [&](int c, float (&x)[32]) {
+            tmem_ld32(lanes + s_col(j) + 32 * c, x);
+            tmem_ld_wait();
+            if (E4M3) {
 #pragma unroll
-            for (int i = 0; i < kTile; ++i)
-              if (i < v0 || i >= v1 || !((groups >> (i >> 4)) & 1)) x[i] = kNone;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int from = max(0, v0 - 32 * w), to = min(32, v1 - 32 * w);
-              if (from < to) {
-                const uint32_t m = (to == 32 ? 0xffffffffu : (1u << to) - 1u) & ~((1u << from) - 1u);
-                poison |= (info->bad[w] & m) != 0;
+              for (int i = 0; i < 32; i += 4) {
+                const float4 k4 = *reinterpret_cast<const float4*>(info->ks + 32 * c + i);
+                x[i] *= k4.x;
+                x[i + 1] *= k4.y;
+                x[i + 2] *= k4.z;
+                x[i + 3] *= k4.w;
               }
             }
-          }
-          float top = x[0];
+            if (cut) {
+              const uint32_t m = seen(c);
 #pragma unroll
-          for (int i = 1; i < kTile; ++i) top = fmaxf(top, x[i]);
+              for (int i = 0; i < 32; ++i)
+                if (!((m >> i) & 1)) x[i] = kNone;
+            }
+          };
+          float top = kNone;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float x[32];
+            fetch(c, x);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) top = fmaxf(top, x[i]);
+            if (cut) poison |= (info->bad[c] & seen(c)) != 0;
+          }
           top *= rs;
           if (E4M3) top += info->vmax;
-          if (__any_sync(0xffffffffu, top > ref + head_room)) {
+          if (__any_sync(0xffffffffu, mine && top > ref + head_room)) {
             // a new reference: what was summed up is scaled to it (the
             // products of the stream's last tile are done: its scores of this
             // tile were issued behind them)
@@ -923,8 +1002,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const Plan p, co
           }
           const float sub = ref == kNone ? 0.f : ref;
           float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 4; ++c) {
+            float x[32];
+            fetch(c, x);
             if (E4M3) {
               uint32_t w[3][8];
 #pragma unroll
@@ -934,8 +1015,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const Plan p, co
                 uint32_t h[2][3];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                  const float p0 = ex2(fmaf(x[32 * c + 4 * i + 2 * b], rs, -sub));
-                  const float p1 = ex2(fmaf(x[32 * c + 4 * i + 2 * b + 1], rs, -sub));
+                  const float p0 = ex2(fmaf(x[4 * i + 2 * b], rs, -sub));
+                  const float p1 = ex2(fmaf(x[4 * i + 2 * b + 1], rs, -sub));
                   part[2 * b] += p0;
                   part[2 * b + 1] += p1;
                   // the top byte of an f16 is an e5m2: cut, subtract, cut, subtract, round
@@ -959,8 +1040,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const Plan p, co
                 uint32_t hi[8], lo[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                  const float p0 = ex2(fmaf(x[32 * c + 16 * hf + 2 * i], rs, -sub));
-                  const float p1 = ex2(fmaf(x[32 * c + 16 * hf + 2 * i + 1], rs, -sub));
+                  const float p0 = ex2(fmaf(x[16 * hf + 2 * i], rs, -sub));
+                  const float p1 = ex2(fmaf(x[16 * hf + 2 * i + 1], rs, -sub));
                   part[(2 * i) & 3] += p0;
                   part[(2 * i + 1) & 3] += p1;
                   const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
@@ -987,26 +1068,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const Plan p, co
       // ------------------------------------------------ the segment's end
       const bool both = split && nt > 1;
       if (done > 0) {
-        ok = wait(o_done + j, n_o & 1) && ok;
+        wait(o_done + j, n_o & 1);
         ++n_o;
       }
       if (poison) sum = __int_as_float(0x7fffffff);
       float w0 = 1.f, w1 = 0.f;
       if (split) {
-        // (R, sum) change hands in the scores' columns, which nothing uses any
-        // more: the warps of a row in both streams have the same TMEM lanes
-        uint32_t mine8[8] = {__float_as_uint(ref), __float_as_uint(sum)}, other8[8];
-        tmem_st8(lanes + s_col(j), mine8);
-        tmem_st_wait();
+        // (R, sum) change hands in the place of the query rows, whose products are done
+        float2* xch = reinterpret_cast<float2*>(sm + L::Q + g.q * 32768);
+        bar_softmax();  // both streams' products
+        xch[j * kTile + r] = make_float2(ref, sum);
         tc_fence_before();
         bar_softmax();
         tc_fence_after();
-        tmem_ld8_nowait(lanes + s_col(1 - j), other8);
-        tmem_ld_wait();
         // (a stream without tiles has no reference, and its accumulator is not read)
-        const float2 me = make_float2(ref, sum);
-        const float2 you = make_float2(__uint_as_float(other8[0]), __uint_as_float(other8[1]));
-        const float2 x0 = j ? you : me, x1 = j ? me : you;
+        const float2 x0 = xch[r], x1 = xch[kTile + r];
         ref = fmaxf(x0.x, x1.x);
         const float base = ref == kNone ? 0.f : ref;
         w0 = ex2(x0.x - base);
@@ -1015,13 +1091,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const Plan p, co
       } else {
         tc_fence_after();
       }
-      const bool whole = wk.k0 == 0 && wk.k1 == wk.g.tiles && p.tiles_p == 0;
+      __syncwarp();
+      if (lane == 0) {
+        if (split) {
+          mbar_arrive(q_empty + g.q);
+        } else {
+          mbar_arrive(q_empty);
+          mbar_arrive(q_empty + 1);
+        }
+      }
+      const bool whole = g.slot < 0;
       if (!idle) {
         float* part = nullptr;
         if (!whole) {
-          const size_t row = (size_t)(wk.ordinal() + cta) * (wk.shared() ? kTile * QT : p.slot_rows) + fr;
-          part = (wk.shared() ? p.part_p : p.part_s) + row * kD;
-          if (mine && (!split || j == 0)) (wk.shared() ? p.ref_p : p.ref_s)[row] = make_float2(ref, sum);
+          const size_t row = (size_t)g.slot * (g.shared ? kRowTile : p.slot_rows) + fr;
+          part = (g.shared ? p.part_p : p.part_s) + row * kD;
+          if (mine && (!split || j == 0)) (g.shared ? p.ref_p : p.ref_s)[row] = make_float2(ref, sum);
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         bf16* orow = a.out + ((size_t)s * a.n_tok + t_row) * a.out_stride + (size_t)head * kD;
@@ -1062,8 +1147,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const Plan p, co
         }
       }
       tc_fence_before();
+      if (split) bar_softmax();  // both streams have read both accumulators
     }
-    (void)ok;
   }
   tc_fence_before();
   __syncthreads();
@@ -1077,8 +1162,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const Plan p, co
 
 // A warp per query row: the partial accumulators of its segments, weighted
 // to a common reference.  Rows that one CTA finished are there already.
-template <int QT>
-__global__ void __launch_bounds__(256) attend_join_kernel(const Plan p, int nctas) {
+__global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ Plan p, int nctas) {
   pdl_launch_next();
   pdl_wait();
   const AttendArgs& a = p.a;
@@ -1090,8 +1174,8 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const Plan p, int ncta
   const int2 nl = lengths(a, s);
   if (t >= nl.x) return;
   const int units = p.head[0];
-  const int i = local / (kTile * QT), entry = s * p.tiles_s + i;
-  const Segment g = segment_of<QT>(a, p.group, nl, i);
+  const int i = local / kRowTile, entry = s * p.tiles_s + i;
+  const Segment g = segment_of(a, p.group, nl, i);
   const int w = weight_of(p, g.rows);
   const int at = p.head[2 + entry] + h * g.tiles * w;
   if (p.tiles_p == 0 && g.tiles > 0 &&
@@ -1124,11 +1208,11 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const Plan p, int ncta
     }
   };
   if (p.tiles_p > 0) {
-    const int ip = f / (kTile * QT), tiles = p.head[1], ordinal = ip * a.nkv + h;
-    const int wp = QT == 2 ? p.row_weight : 1;
-    join(ordinal * tiles * wp, tiles, wp, ordinal, kTile * QT, f % (kTile * QT), p.part_p, p.ref_p);
+    const int ip = f / kRowTile, tiles = p.head[1], ordinal = ip * a.nkv + h;
+    const int wp = p.row_weight;
+    join(ordinal * tiles * wp, tiles, wp, ordinal, kRowTile, f % kRowTile, p.part_p, p.ref_p);
   }
-  join(at, g.tiles, w, entry * a.nkv + h, p.slot_rows, local % (kTile * QT), p.part_s, p.ref_s);
+  join(at, g.tiles, w, entry * a.nkv + h, p.slot_rows, local % kRowTile, p.part_s, p.ref_s);
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   uint2 out;
   out.x = sum == 0.f ? 0u : bits2(__floats2bfloat162_rn(o.x * inv, o.y * inv));
@@ -1142,15 +1226,14 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Sizes of a call's parts; `ctas` as large as any device's.
 struct Sizes {
-  int qt, rows, tiles_p, tiles_s, slot_rows;
+  int rows, tiles_p, tiles_s, slot_rows;
   size_t head, part_p, part_s, ref_p, ref_s, total;
 };
 bool sizes_of(int batch, int n_tok, int nq, int nkv, int shared_len, int ctas, Sizes* z) {
   const long long rows = (long long)n_tok * (nq / nkv);
   if (rows * batch >= (1ll << 31) - 512) return false;
   z->rows = (int)rows;
-  z->qt = rows > kTile || (shared_len > 0 && rows * batch > kTile) ? 2 : 1;
-  const int rt = kTile * z->qt;
+  const int rt = kRowTile;
   z->tiles_s = (int)((rows + rt - 1) / rt);
   z->tiles_p = shared_len > 0 ? (int)((rows * batch + rt - 1) / rt) : 0;
   z->slot_rows = (int)std::min<long long>(rt, rows);
@@ -1172,17 +1255,17 @@ bool sizes_of(int batch, int n_tok, int nq, int nkv, int shared_len, int ctas, S
   return true;
 }
 
-template <bool E4M3, int QT>
+template <bool E4M3>
 int launch(const Plan& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Ctx& c) {
   // an attribute of the kernel on the current device: set on every call (a
   // flag of what was set would have to be kept per device)
-  if (cudaFuncSetAttribute(attend_tc_kernel<E4M3, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)Smem<E4M3, QT>::bytes) != cudaSuccess)
+  if (cudaFuncSetAttribute(attend_tc_kernel<E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)Smem<E4M3>::bytes) != cudaSuccess)
     return DFLASH2_ERR_CUDA;
-  const int rc = launch_k(attend_tc_kernel<E4M3, QT>, dim3(c.nsm), dim3(kThreads), Smem<E4M3, QT>::bytes, c, p, tm_k, tm_v);
+  const int rc = launch_k(attend_tc_kernel<E4M3>, dim3(c.nsm), dim3(kThreads), Smem<E4M3>::bytes, c, p, tm_k, tm_v);
   if (rc != DFLASH2_OK) return rc;
   const long long rows = (long long)p.a.batch * p.rows * p.a.nkv;
-  return launch_k(attend_join_kernel<QT>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, c, p, c.nsm);
+  return launch_k(attend_join_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, c, p, c.nsm);
 }
 
 }  // namespace
@@ -1225,8 +1308,7 @@ int launch_attend_tc(const AttendArgs& a, void* workspace, const Ctx& c) {
   int rc = make_sw128_map(&tm_k, a.k, rows, cols, cols, 16);
   if (rc == DFLASH2_OK) rc = make_sw128_map(&tm_v, a.v, rows, cols, cols, 16);
   if (rc != DFLASH2_OK) return rc;
-  if (a.e4m3) return z.qt == 2 ? launch<true, 2>(p, tm_k, tm_v, c) : launch<true, 1>(p, tm_k, tm_v, c);
-  return z.qt == 2 ? launch<false, 2>(p, tm_k, tm_v, c) : launch<false, 1>(p, tm_k, tm_v, c);
+  return a.e4m3 ? launch<true>(p, tm_k, tm_v, c) : launch<false>(p, tm_k, tm_v, c);
 }
 
 }  // namespace df2
