@@ -1,6 +1,6 @@
 // Attention of a sequence's last tokens over its paged cache on the
-// 5th-generation tensor cores: head dimension 128, pages of whole 16-key
-// groups, bfloat16 or 8-bit rows.
+// 5th-generation tensor cores: head dimension 128, pages of 16, 32, 64, ...
+// keys, bfloat16 or 8-bit rows.
 //
 //   S = Q K^T       128 query rows x 128 keys, fp32 in TMEM
 //   P = 2^(s - R)   R: the row's reference, near its running maximum
@@ -96,7 +96,7 @@ struct Smem {
   static constexpr int SEG = INFO + kInfo * INFOS;
   static constexpr int QSCALE = SEG + kSegs * (int)sizeof(SegInfo);  // float [kSegs][kRowTile], 8-bit only
   static constexpr int BAR = QSCALE + (E4M3 ? kSegs * kRowTile * 4 : 0);
-  static constexpr size_t bytes = 1024 + BAR + (2 * SLOTS + 2 * kInfo + 2 * kSegs + 9) * 8 + 64;
+  static constexpr size_t bytes = 1024 + BAR + (2 * SLOTS + 2 * kInfo + 2 * kSegs + 10) * 8 + 64;
   static_assert(bytes + 512 <= 227 * 1024, "shared memory");
 };
 
@@ -107,6 +107,7 @@ struct Plan {
   int tiles_s;         // row tiles of a sequence at most
   int row_weight;      // cost of a tile for more than 128 rows, in tiles for fewer
   int slot_rows;       // rows of a sequence's partial slot
+  int page_shift;      // page_size = 2^page_shift
   int* head;           // workspace: all positions, tiles of the shared part, first position of each row tile
   float *part_p, *part_s;    // partial accumulators [slot][rows][kD] of the shared part and of the sequences
   float2 *ref_p, *ref_s;     // (R, sum) of their rows
@@ -147,11 +148,13 @@ __device__ __forceinline__ Segment segment_of(const AttendArgs& a, int group, in
 }
 __device__ __forceinline__ int weight_of(const Plan& p, int rows) { return rows > kTile ? p.row_weight : 1; }
 
-// Share of CTA c of n: tiles whose position lies in [bound(c), bound(c + 1)).
-// (positions fit 31 bits: the host sees to it)
-__device__ __forceinline__ int bound_of(int units, int c, int n) { return (int)((long long)units * c / n); }
+// Share of CTA c of n: tiles whose position lies in [bound(c), bound(c + 1));
+// the first units % n shares are one larger.  (Positions fit 31 bits: the
+// host sees to it.)
+__device__ __forceinline__ int bound_of(int units, int c, int n) { return units / n * c + min(c, units % n); }
 __device__ __forceinline__ int owner_of(int units, int x, int n) {
-  return (int)((((long long)x + 1) * n - 1) / units);
+  const int q = units / n, wide = units % n * (q + 1);
+  return x < wide ? x / (q + 1) : units % n + (x - wide) / q;
 }
 
 // A place in a ring of N slots and the parity of its round.
@@ -175,6 +178,17 @@ struct Ring {
     return r;
   }
 };
+
+// A bounded wait that did not succeed at once.  Not inlined: the roles wait in
+// many places.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
+  if (mbar_wait(bar, parity, abort_flag, kWaitNs)) return true;
+  if (!*abort_flag) {
+    *abort_flag = 1;
+    flag(status, DFLASH2_DEV_WAIT_TIMEOUT);
+  }
+  return false;
+}
 
 // ------------------------------------------------------------------ PTX
 
@@ -201,49 +215,45 @@ __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
 
+// One lane of the warp.  The compiler knows that no other lane is active
+// behind this: what the lane computes goes to uniform registers, where the
+// tensor core's instructions take their operands.  (Behind `lane == 0` every
+// operand is moved there instruction by instruction: 16 instructions a
+// product, which the softmax warps of the same scheduler hold up: 2830 to
+// 4970 cycles for 24 products beside busy warps, 1610 to 2570 this way, 1536
+// in the tensor core.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // D (+)= A B, A from shared memory or from TMEM; kind::f16 or kind::f8f6f4.
-// The whole warp executes the code around, with the same values in every
-// lane, and only the instruction itself is left to the lane with `one`: its
-// operands then live in uniform registers.  (Issued from a branch that one
-// lane takes, every operand moves to a uniform register first: 110 to 200
-// cycles an instruction beside the softmax warps, where the products of one
-// take 64.)
 template <bool E4M3>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t one) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   if (E4M3)
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one)
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    umma_bf16(d, a, b, idesc, acc);
+}
+template <bool E4M3>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if (E4M3)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one)
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
-}
-template <bool E4M3>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t one) {
-  if (E4M3)
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one)
-        : "memory");
-}
-__device__ __forceinline__ void commit(uint64_t* bar, uint32_t one) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
-      "r"(one)
-      : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
@@ -262,6 +272,179 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
 }
 
 __device__ __forceinline__ uint32_t bits2(__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+// Two f16 as three e5m2 each, in the upper bytes of the halves: an f16's
+// upper byte is an e5m2, so cut, subtract, cut, subtract, round.
+__device__ __forceinline__ void split3(__half2 u, uint32_t (&h)[3]) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t top = *reinterpret_cast<const uint32_t*>(&u) & 0xff00ff00u;
+    h[q] = top;
+    u = __hsub2(u, *reinterpret_cast<const __half2*>(&top));
+  }
+  h[2] = *reinterpret_cast<const uint32_t*>(&u) + 0x00800080u;
+}
+
+// Scales a row's accumulator (4 pieces of 32 columns, or none) and the
+// weights of the tile's first `chunks` pieces of 32 keys by `by`, a power of
+// two.  Rare, and so not inlined.
+template <bool E4M3>
+__device__ __noinline__ void rescale(uint32_t o, int pieces, uint32_t w, int chunks, float by) {
+#pragma unroll 1
+  for (int c = 0; c < pieces; ++c) {
+    float x[32];
+    tmem_ld32(o + 32 * c, x);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t r[8];
+#pragma unroll
+      for (int b = 0; b < 8; ++b) r[b] = __float_as_uint(x[8 * i + b] * by);
+      tmem_st8(o + 32 * c + 8 * i, r);
+    }
+  }
+  tmem_st_wait();  // (and the weights stored before)
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
+    uint32_t r[3][8];
+    if (E4M3) {
+      const __half2 by2 = __float2half2_rn(by);
+      uint32_t n[3][8];
+#pragma unroll
+      for (int q = 0; q < 3; ++q) tmem_ld8_nowait(w + 32 * c + 8 * q, r[q]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint32_t h[2][3];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          __half2 u[3];
+#pragma unroll
+          for (int q = 0; q < 3; ++q) {
+            const uint32_t x = __byte_perm(r[q][i], 0u, b ? 0x3424 : 0x1404);
+            u[q] = *reinterpret_cast<const __half2*>(&x);
+          }
+          split3(__hmul2(__hadd2(__hadd2(u[2], u[1]), u[0]), by2), h[b]);
+        }
+#pragma unroll
+        for (int q = 0; q < 3; ++q) n[q][i] = __byte_perm(h[0][q], h[1][q], 0x7531);
+      }
+#pragma unroll
+      for (int q = 0; q < 3; ++q) tmem_st8(w + 32 * c + 8 * q, n[q]);
+    } else {
+      const __nv_bfloat162 by2 = __float2bfloat162_rn(by);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        tmem_ld8_nowait(w + 32 * c + 8 * q, r[0]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[0][i] = bits2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&r[0][i]), by2));
+        tmem_st8(w + 32 * c + 8 * q, r[0]);
+      }
+    }
+  }
+  tmem_st_wait();
+}
+
+// ------------------------------------------------------------------ query rows
+
+// Rows [r0, r1) of a segment (r0 and r1 - r0 of one place of 128), by a warp,
+// into the place at `dst`: K-major with the 128-byte swizzle.  bfloat16: two
+// halves of 64 dims, 16 KB apart.  8-bit: the high codes and, 16 KB behind,
+// the low ones; a row's largest magnitude becomes 2^7 .. 2^8, and
+// qscale[row] the factor that its scores take.
+template <bool E4M3>
+__device__ __forceinline__ void load_rows(const Plan& p, const SegInfo& g, int r0, int r1, uint8_t* dst, float* qscale) {
+  const AttendArgs& a = p.a;
+  constexpr int W = E4M3 ? 8 : 16;  // lanes of a row
+  constexpr int STEP = 32 / W;
+  const int lane = threadIdx.x & 31, c = lane & (W - 1);
+  // this lane's row, stepped through the heads of the group, tokens and sequences without divisions
+  int row = r0 + lane / W;
+  int s = g.shared ? (g.f0 + row) / p.rows : g.s;
+  int gq = g.f0 + row - s * p.rows, t = gq / p.group;
+  gq -= t * p.group;
+  int n = !a.n_new ? a.n_tok : s < a.batch ? a.n_new[s] : 0;
+  auto source = [&]() {  // address of the row, or null; then the lane's next row
+    const bool real = row < r1 && t < n;
+    const bf16* src = a.q + ((size_t)s * a.n_tok + t) * a.q_stride + (size_t)(g.h * p.group + gq) * kD;
+    row += STEP;
+    gq += STEP;
+    while (gq >= p.group) {
+      gq -= p.group;
+      if (++t == a.n_tok) {
+        t = 0;
+        ++s;
+        if (a.n_new) n = s < a.batch ? a.n_new[s] : 0;
+      }
+    }
+    return real ? src : nullptr;
+  };
+  if (!E4M3) {
+#pragma unroll 2
+    for (int x = r0; x < r1; x += STEP) {
+      const int r = (x + lane / W) & (kTile - 1);
+      const bf16* src = source();
+      if (x + lane / W < r1)
+        cp_async16(dst + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4), src ? src + c * 8 : a.q, src != nullptr);
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    return;
+  }
+#pragma unroll 1
+  for (int x = r0; x < r1; x += 4 * STEP) {  // 16 rows: all their loads in flight, then their codes
+    uint4 v[4][2];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bf16* src = source();
+      v[u][0] = src ? reinterpret_cast<const uint4*>(src)[2 * c] : make_uint4(0u, 0u, 0u, 0u);
+      v[u][1] = src ? reinterpret_cast<const uint4*>(src)[2 * c + 1] : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int fr = x + u * STEP + lane / W, r = fr & (kTile - 1);
+      const uint32_t w8[8] = {v[u][0].x, v[u][0].y, v[u][0].z, v[u][0].w, v[u][1].x, v[u][1].y, v[u][1].z, v[u][1].w};
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(max(top, w8[i] & 0x7f800000u), (w8[i] << 16) & 0x7f800000u);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int e = top >= 0x7f800000u ? 254 : max(1, (int)(top >> 23));
+      // 2^(7 - (e - 127)) = 2^(134 - e), in two factors that are floats
+      const int ea = (134 - e) / 2, eb = (134 - e) - ea;
+      const float up0 = __uint_as_float((uint32_t)(127 + ea) << 23), up1 = __uint_as_float((uint32_t)(127 + eb) << 23);
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x0 = __uint_as_float(w8[i] << 16) * up0 * up1;
+        const float x1 = __uint_as_float(w8[i] & 0xffff0000u) * up0 * up1;
+        const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+        const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h2, __NV_E4M3);
+        const float2 back = __half22float2(__half2(hr));
+        const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(x0 - back.x, x1 - back.y), __NV_SATFINITE, __NV_E4M3);
+        hi[i >> 1] = (i & 1) ? hi[i >> 1] | (h2 << 16) : h2;
+        lo[i >> 1] = (i & 1) ? lo[i >> 1] | (l2 << 16) : l2;
+      }
+      if (fr < r1) {
+        uint8_t* q = dst + r * 128 + ((c ^ (r & 7)) << 4);
+        *reinterpret_cast<uint4*>(q) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(q + 16384) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        // a row that is not finite has no result
+        if (c == 0)
+          qscale[fr] = top >= 0x7f800000u ? __int_as_float(0x7fffffff)
+                                          : __uint_as_float((uint32_t)(127 - ea) << 23) *
+                                                __uint_as_float((uint32_t)(127 - eb) << 23);
+      }
+    }
+  }
+}
 
 // ------------------------------------------------------------------ main kernel
 
@@ -284,7 +467,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
   uint64_t* p_ready = s_full + 2;           // [2] its weights in TMEM (4 arrivals)
   uint64_t* o_done = p_ready + 2;           // [2] a segment's last product of the stream is done
   uint64_t* q_empty = o_done + 2;           // [2] a place of query rows is free (8 arrivals)
-  uint64_t* drain = q_empty + 2;            // every product issued is done
+  uint64_t* q_ready = q_empty + 2;          // query rows that the softmax warps load themselves (8 arrivals)
+  uint64_t* drain = q_ready + 1;            // every product issued is done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   SegInfo* segs = reinterpret_cast<SegInfo*>(sm + L::SEG);
@@ -311,6 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
       mbar_init(o_done + j, 1);
       mbar_init(q_empty + j, 8);
     }
+    mbar_init(q_ready, 8);
     mbar_init(drain, 1);
     *abort_flag = 0;
   }
@@ -408,12 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
   __syncthreads();
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (mbar_wait(bar, parity, abort_flag, kWaitNs)) return true;
-    if (!*abort_flag) {
-      *abort_flag = 1;
-      flag(a.status, DFLASH2_DEV_WAIT_TIMEOUT);
-    }
-    return false;
+    return mbar_try_wait(smem_u32(bar), parity) || wait_on(bar, parity, abort_flag, a.status);
   };
   // The next segment (tiles = 0: none, or the kernel is giving up).
   Ring<kSegs> seg_at;
@@ -503,67 +683,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         if (seg_at.round > 0) ok = wait(seg_empty + seg_at.slot, (seg_at.round - 1) & 1) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (E4M3) {
-          // A row's largest magnitude becomes 2^7 .. 2^8; high codes at 0, low
-          // codes at 16 KB of a place.  Eight lanes take a row.
-          float* qscale = reinterpret_cast<float*>(sm + L::QSCALE) + seg_at.slot * kRowTile;
-#pragma unroll 1
-          for (int r0 = 0; r0 < ((g.rows + 3) & ~3); r0 += 4) {
-            const int fr = r0 + (lane >> 3), f = g.f0 + fr, part = lane & 7;
-            const int s = g.shared ? f / p.rows : g.s, local = f - s * p.rows, t = local / p.group;
-            const bool real = fr < g.rows && (!g.shared || !a.n_new || t < a.n_new[s]);
-            uint4 x[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-            if (real) {
-              const bf16* src = a.q + ((size_t)s * a.n_tok + t) * a.q_stride + (size_t)(h * p.group + local - t * p.group) * kD;
-              x[0] = reinterpret_cast<const uint4*>(src)[2 * part];
-              x[1] = reinterpret_cast<const uint4*>(src)[2 * part + 1];
-            }
-            const uint32_t w8[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) top = max(max(top, w8[i] & 0x7f800000u), (w8[i] << 16) & 0x7f800000u);
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const int e = top >= 0x7f800000u ? 254 : max(1, (int)(top >> 23));
-            // 2^(7 - (e - 127)) = 2^(134 - e), in two factors that are floats
-            const int e1_ = (134 - e) / 2, e2_ = (134 - e) - e1_;
-            const float up0 = __uint_as_float((uint32_t)(127 + e1_) << 23), up1 = __uint_as_float((uint32_t)(127 + e2_) << 23);
-            uint32_t hi_c[4], lo_c[4];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float x0 = __uint_as_float(w8[i] << 16) * up0 * up1;
-              const float x1 = __uint_as_float(w8[i] & 0xffff0000u) * up0 * up1;
-              const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-              const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h2, __NV_E4M3);
-              const float2 back = __half22float2(__half2(hr));
-              const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(x0 - back.x, x1 - back.y), __NV_SATFINITE, __NV_E4M3);
-              hi_c[i >> 1] = (i & 1) ? hi_c[i >> 1] | (h2 << 16) : h2;
-              lo_c[i >> 1] = (i & 1) ? lo_c[i >> 1] | (l2 << 16) : l2;
-            }
-            const int r = fr & (kTile - 1);
-            uint8_t* dst = sm + L::Q + (g.split ? g.q : fr / kTile) * 32768 + r * 128 + ((part ^ (r & 7)) << 4);
-            *reinterpret_cast<uint4*>(dst) = make_uint4(hi_c[0], hi_c[1], hi_c[2], hi_c[3]);
-            *reinterpret_cast<uint4*>(dst + 16384) = make_uint4(lo_c[0], lo_c[1], lo_c[2], lo_c[3]);
-            // the factor of its scores; a row that is not finite has no result
-            if (part == 0)
-              qscale[fr] = top >= 0x7f800000u ? __int_as_float(0x7fffffff)
-                                              : __uint_as_float((uint32_t)(127 - e1_) << 23) *
-                                                    __uint_as_float((uint32_t)(127 - e2_) << 23);
-          }
-        } else {
-#pragma unroll 4
-          for (int i = lane; i < g.rows * 16; i += 32) {
-            const int fr = i >> 4, c = i & 15, f = g.f0 + fr;
-            const int s = g.shared ? f / p.rows : g.s, local = f - s * p.rows, t = local / p.group;
-            const bool real = !g.shared || !a.n_new || t < a.n_new[s];
-            const bf16* src = a.q + ((size_t)s * a.n_tok + t) * a.q_stride + (size_t)(h * p.group + local - t * p.group) * kD;
-            const int r = fr & (kTile - 1);
-            cp_async16(sm + L::Q + (g.split ? g.q : fr / kTile) * 32768 + (c >> 3) * 16384 + r * 128 +
-                           (((c & 7) ^ (r & 7)) << 4), real ? src + c * 8 : a.q, real);
-          }
-          cp_async_commit();
-          cp_async_wait<0>();
-        }
+        if (g.split)
+          load_rows<E4M3>(p, g, 0, g.rows, sm + L::Q + g.q * 32768,
+                          reinterpret_cast<float*>(sm + L::QSCALE) + seg_at.slot * kRowTile);
         fence_proxy_async_smem();
         if (lane == 0) segs[seg_at.slot] = g;
         __syncwarp();
@@ -597,8 +719,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         const int pos = g.first + t * kTile + 16 * lane;
         int row = absent;
         if (lane < 8 && t < g.tiles && pos < g.end) {
-          const int page = table[pos / a.page_size];
-          if (page >= 0 && page < a.n_pages) row = page * a.page_size + pos % a.page_size;
+          const int page = table[pos >> p.page_shift];
+          if (page >= 0 && page < a.n_pages) row = (page << p.page_shift) + (pos & (a.page_size - 1));
         }
         return row;
       };
@@ -641,122 +763,88 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     }
   } else if (warp == 9) {
     // ---------------------------------------------------------------- MMA issue
-    const uint32_t one = lane == 0;
-    // shared addresses in the descriptors' 16-byte units; their upper words are constant
-    const uint32_t ring = __shfl_sync(0xffffffffu, smem_u32(sm + L::RING), 0) >> 4;
-    const uint32_t qs = __shfl_sync(0xffffffffu, smem_u32(sm + L::Q), 0) >> 4;
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    constexpr uint64_t kKMajor = ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-    constexpr uint64_t kMnMajor = ((uint64_t)(16384 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-    // A K-major, B = K rows K-major; B = V rows MN-major; 8-bit weights are e5m2
-    constexpr uint32_t id_s = E4M3 ? (1u << 4) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24) : idesc_bf16_f32(kTile, kTile);
-    constexpr uint32_t id_o =
-        (E4M3 ? (1u << 4) | (1u << 7) | ((kD >> 3) << 17) | ((kTile >> 4) << 24) : idesc_bf16_f32(kTile, kD)) |
-        (1u << 16);
-    Ring<NS> at;
-    uint32_t n_p = 0;  // bit j: parity of stream j's weights
-    bool ok = true;
-    SegInfo g;
-    for (; ok && next_segment(&g); seg_at.step()) {
-      const int nt = __shfl_sync(0xffffffffu, g.tiles, 0), lead = __shfl_sync(0xffffffffu, g.split ? 2 : 1, 0);
-      const uint32_t q0 = qs + __shfl_sync(0xffffffffu, g.q, 0) * 2048;
-      auto scores = [&](int j, int slot) {  // stream j's rows against the keys in a slot
-        const uint32_t kd = ring + slot * (L::SLOT >> 4), qd = q0 + (lead == 1 ? j : 0) * 2048;
-        const uint32_t d = tm + s_col(j);
-#pragma unroll 4
-        for (int x = 0; x < 8; ++x)  // 16 dims each; 8 bits: 32 dims each, with the high, then the low codes of q
-          mma_ss<E4M3>(d, kKMajor | (qd + (x >> 2) * 1024 + (x & 3) * 2),
-                       kKMajor | (kd + (E4M3 ? 0 : (x >> 2) * 1024) + (x & 3) * 2), id_s, x > 0 ? 1u : 0u, one);
-        commit(s_full + j, one);
-      };
-      auto products = [&](int j, int slot, uint32_t acc) {
-        const uint32_t vd = ring + slot * (L::SLOT >> 4);
-        const uint32_t d = tm + o_col(j), pc = tm + s_col(j);
-        if (E4M3) {
-#pragma unroll 3
-          for (int x = 0; x < 12; ++x)  // 32 keys each, three parts
-            mma_ts<true>(d, pc + 32 * (x / 3) + 8 * (x % 3), kMnMajor | (vd + (x / 3) * 256), id_o, x > 0 ? 1u : acc, one);
-        } else {
-#pragma unroll 4
-          for (int x = 0; x < 16; ++x)  // 16 keys each, high and low parts
-            mma_ts<false>(d, pc + 32 * (x >> 2) + 8 * ((x >> 1) & 1) + 16 * (x & 1), kMnMajor | (vd + (x >> 1) * 128), id_o,
-                          x > 0 ? 1u : acc, one);
+    if (elect_one()) {
+      // shared addresses in the descriptors' 16-byte units; their upper words are constant
+      const uint32_t ring = smem_u32(sm + L::RING) >> 4, qs = smem_u32(sm + L::Q) >> 4;
+      constexpr uint64_t kKMajor =
+          ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+      constexpr uint64_t kMnMajor =
+          ((uint64_t)(16384 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+      // A K-major, B = K rows K-major; B = V rows MN-major; 8-bit weights are e5m2
+      constexpr uint32_t id_s =
+          E4M3 ? (1u << 4) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24) : idesc_bf16_f32(kTile, kTile);
+      constexpr uint32_t id_o =
+          (E4M3 ? (1u << 4) | (1u << 7) | ((kD >> 3) << 17) | ((kTile >> 4) << 24) : idesc_bf16_f32(kTile, kD)) |
+          (1u << 16);
+      Ring<NS> at;
+      uint32_t n_p = 0, n_q = 0;  // bit j: parity of stream j's weights; parity of the query rows
+      bool ok = true;
+      for (; ok; seg_at.step()) {
+        if (!wait(seg_full + seg_at.slot, seg_at.round & 1)) break;
+        const SegInfo& g = segs[seg_at.slot];
+        const int nt = g.tiles, lead = g.split ? 2 : 1;
+        const uint32_t q0 = qs + g.q * 2048;
+        mbar_arrive(seg_empty + seg_at.slot);
+        if (nt == 0) break;
+        if (lead == 1) {
+          if (!wait(q_ready, n_q & 1)) break;
+          ++n_q;
         }
-      };
-      auto landed = [&](const Ring<NS>& i) {
-        ok = ok && wait(full + i.slot, i.round & 1);
-        tc_fence_after();
-      };
-      auto weights = [&](int j) {
-        ok = ok && wait(p_ready + j, (n_p >> j) & 1);
-        n_p ^= 1u << j;
-        tc_fence_after();
-      };
-      if (lead == 2) {
-        // stream t % 2 takes tile t; slots in order K0 K1 V0 K2 V1 K3 ...
-        for (int t = 0; t < min(2, nt) && ok; ++t) {
-          landed(at);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          scores(t, at.slot);
-          commit(empty + at.slot, one);
-          at.step();
-        }
-        for (int t = 0; t < nt && ok; ++t) {
-          landed(at);
-          weights(t & 1);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          products(t & 1, at.slot, t < 2 ? 0u : 1u);
-          commit(empty + at.slot, one);
-          if (t + 2 >= nt) commit(o_done + (t & 1), one);
-          at.step();
-          if (t + 2 < nt) {
-            landed(at);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            scores(t & 1, at.slot);
-            commit(empty + at.slot, one);
-            at.step();
-          }
-        }
-      } else {
-        // both streams take every tile; slots in order K0 V0 K1 V1 ...
-        landed(at);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        scores(0, at.slot);
-        scores(1, at.slot);
-        commit(empty + at.slot, one);
-        at.step();
-        for (int t = 0; t < nt && ok; ++t) {
-          const Ring<NS> iv = at, ik = at.ahead(1);
-          const bool again = t + 1 < nt;
-          landed(iv);
+        // Work u: stream u % 2's products with a tile's values, and then its
+        // scores of the next one.  With shared rows stream u % 2 takes tile u
+        // and the slots go K0 K1 V0 K2 V1 K3 ...; otherwise both take tile
+        // u / 2 and they go K0 V0 K1 V1 ...
+        const int all = lead == 2 ? nt : 2 * nt;
 #pragma unroll 1
-          for (int j = 0; j < 2; ++j) {
-            weights(j);
-            if (again && j == 0) landed(ik);
-            ok = __all_sync(0xffffffffu, ok);
+        for (int u = -2; u < all; ++u) {
+          const int j = u & 1;
+          const bool release = lead == 2 || j == 1;
+          const uint32_t pc = tmem + s_col(0) + 128u * j;
+          if (u >= 0) {
+            ok = wait(full + at.slot, at.round & 1) && wait(p_ready + j, (n_p >> j) & 1);
             if (!ok) break;
-            products(j, iv.slot, t > 0 ? 1u : 0u);
-            if (j == 1) commit(empty + iv.slot, one);
-            if (again) {
-              scores(j, ik.slot);
-              if (j == 1) commit(empty + ik.slot, one);
+            n_p ^= 1u << j;
+            tc_fence_after();
+            const uint32_t vd = ring + at.slot * (L::SLOT >> 4), d = tmem + o_col(0) + 128u * j;
+            const uint32_t acc = u >= 2 ? 1u : 0u;
+            if (E4M3) {
+#pragma unroll
+              for (int x = 0; x < 12; ++x)  // 32 keys each, three parts
+                mma_ts<true>(d, pc + 32 * (x / 3) + 8 * (x % 3), kMnMajor | (vd + (x / 3) * 256), id_o, x > 0 ? 1u : acc);
             } else {
-              commit(o_done + j, one);
+#pragma unroll
+              for (int x = 0; x < 16; ++x)  // 16 keys each, high and low parts
+                mma_ts<false>(d, pc + 32 * (x >> 2) + 8 * ((x >> 1) & 1) + 16 * (x & 1), kMnMajor | (vd + (x >> 1) * 128),
+                              id_o, x > 0 ? 1u : acc);
+            }
+            if (release) {
+              umma_commit(empty + at.slot);
+              at.step();
+            }
+            if (u + 2 >= all) umma_commit(o_done + j);
+          }
+          if (u + 2 < all) {
+            const Ring<NS> k = u >= 0 && !release ? at.ahead(1) : at;
+            ok = wait(full + k.slot, k.round & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t kd = ring + k.slot * (L::SLOT >> 4), qd = q0 + (lead == 1 ? 2048u * j : 0u);
+#pragma unroll
+            for (int x = 0; x < 8; ++x)  // 16 dims each; 8 bits: 32 dims each, with the high, then the low codes of q
+              mma_ss<E4M3>(pc, kKMajor | (qd + (x >> 2) * 1024 + (x & 3) * 2),
+                           kKMajor | (kd + (E4M3 ? 0 : (x >> 2) * 1024) + (x & 3) * 2), id_s, x > 0 ? 1u : 0u);
+            umma_commit(s_full + j);
+            if (release) {
+              umma_commit(empty + k.slot);
+              at.step();
             }
           }
-          at.step();
-          if (again) at.step();
         }
       }
-      ok = __all_sync(0xffffffffu, ok);
+      umma_commit(drain);
+      volatile int never = 0;
+      if (!mbar_wait(drain, 0, &never, kWaitNs)) flag(a.status, DFLASH2_DEV_WAIT_TIMEOUT);
     }
-    commit(drain, one);
-    volatile int never = 0;
-    if (!mbar_wait(drain, 0, &never, kWaitNs) && lane == 0) flag(a.status, DFLASH2_DEV_WAIT_TIMEOUT);
     __syncwarp();
   } else if (warp == 10) {
     // ---------------------------------------------------------------- tile info
@@ -773,8 +861,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         const int pos = g.first + t * kTile + 16 * lane;
         int row = -1;
         if (lane < 8 && t < g.tiles && pos < g.end) {
-          const int page = table[pos / a.page_size];
-          if (page >= 0 && page < a.n_pages) row = page * a.page_size + pos % a.page_size;
+          const int page = table[pos >> p.page_shift];
+          if (page >= 0 && page < a.n_pages) row = (page << p.page_shift) + (pos & (a.page_size - 1));
           else flag(a.status, DFLASH2_DEV_BAD_PAGE);
         }
         return row;
@@ -886,7 +974,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     const int j = warp >> 2, r = threadIdx.x & 127;  // stream, row of its tile
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float scale = a.scale * 1.4426950408889634f;
-    const float head_room = E4M3 ? 15.f : 8.f;  // how far a weight may pass 2^0 (8 bits: weight times scale)
+    // how far a weight may pass 2^0: any float will do, or, times the value's
+    // scale, what an e5m2 holds
+    const float head_room = E4M3 ? 15.f : 64.f;
     uint32_t n_s = 0, n_o = 0, tiles = 0;
     SegInfo g;
     for (; next_segment(&g); seg_at.step()) {
@@ -897,6 +987,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
       const int f = g.f0 + (mine ? fr : 0);
       const int s = g.shared ? f / p.rows : g.s, local = f - s * p.rows, t_row = local / p.group;
       const int head = g.h * p.group + local - t_row * p.group;
+      if (!split) {
+        // (many rows are a long segment: no warp has to load them ahead)
+        const int w0 = warp * 32;
+        if (w0 < g.rows)
+          load_rows<E4M3>(p, g, w0, min(w0 + 32, g.rows), sm + L::Q + j * 32768,
+                          reinterpret_cast<float*>(sm + L::QSCALE) + seg_at.slot * kRowTile);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_ready);
+      }
       int2 see = make_int2(0, INT32_MAX);  // (rows that do not exist see everything: nothing to mask)
       bool real = mine;
       float rs = scale;  // factor of a row's scores
@@ -941,13 +1041,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
             if (!((groups >> (2 * c + 1)) & 1)) m &= 0x0000ffffu;
             return m;
           };
-          // The scores are read twice, in pieces of 32 keys by a loop that is
-          // not unrolled: the roles' code has to stay in the instruction
-          // cache (with all 128 scores in registers and the loops unrolled,
-          // fetching it took most of the time).
-          auto fetch = [&](int c, float (&x)[32]) {
-            tmem_ld32(lanes + s_col(j) + 32 * c, x);
-            tmem_ld_wait();
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
+          // 32 keys: their scores become weights in the same TMEM columns
+          auto weigh = [&](int c, float (&x)[32]) {
             if (E4M3) {
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
@@ -960,52 +1056,30 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
             }
             if (cut) {
               const uint32_t m = seen(c);
+              poison |= (info->bad[c] & m) != 0;
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (!((m >> i) & 1)) x[i] = kNone;
             }
-          };
-          float top = kNone;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float x[32];
-            fetch(c, x);
+            float y[11];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) top = fmaxf(top, x[i]);
-            if (cut) poison |= (info->bad[c] & seen(c)) != 0;
-          }
-          top *= rs;
-          if (E4M3) top += info->vmax;
-          if (__any_sync(0xffffffffu, mine && top > ref + head_room)) {
-            // a new reference: what was summed up is scaled to it (the
-            // products of the stream's last tile are done: its scores of this
-            // tile were issued behind them)
-            const float now = fmaxf(ref, E4M3 ? top - 11.f : top);
-            const float by = ref == kNone ? 0.f : ex2(ref - now);
-            sum *= by;
-            ref = now;
-            if (done > 0) {
-#pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                float o[32];
-                tmem_ld32(lanes + o_col(j) + 32 * c, o);
-                tmem_ld_wait();
+            for (int i = 0; i < 10; ++i) y[i] = max3(x[3 * i], x[3 * i + 1], x[3 * i + 2]);
+            y[10] = fmaxf(x[30], x[31]);
+            float top = max3(max3(y[0], y[1], y[2]), max3(y[3], y[4], y[5]), max3(max3(y[6], y[7], y[8]), y[9], y[10])) * rs;
+            if (E4M3) top += info->vmax;
+            if (__any_sync(0xffffffffu, mine && top > ref + head_room)) {
+              // a new reference (a whole number, so that what is scaled to it
+              // stays exact).  The products of the stream's last tile are
+              // done: this tile's scores were issued behind them.
+              const float now = fmaxf(ref, ceilf(top) - (E4M3 ? 11.f : 0.f));
+              const float by = ref == kNone ? 0.f : ex2(ref - now);
+              sum *= by;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  uint32_t w[8];
-#pragma unroll
-                  for (int b = 0; b < 8; ++b) w[b] = __float_as_uint(o[8 * i + b] * by);
-                  tmem_st8(lanes + o_col(j) + 32 * c + 8 * i, w);
-                }
-              }
+              for (int i = 0; i < 4; ++i) part[i] *= by;
+              ref = now;
+              rescale<E4M3>(lanes + o_col(j), done > 0 ? 4 : 0, lanes + s_col(j), c, by);
             }
-          }
-          const float sub = ref == kNone ? 0.f : ref;
-          float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float x[32];
-            fetch(c, x);
+            const float sub = ref == kNone ? 0.f : ref;
             if (E4M3) {
               uint32_t w[3][8];
 #pragma unroll
@@ -1019,15 +1093,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                   const float p1 = ex2(fmaf(x[4 * i + 2 * b + 1], rs, -sub));
                   part[2 * b] += p0;
                   part[2 * b + 1] += p1;
-                  // the top byte of an f16 is an e5m2: cut, subtract, cut, subtract, round
-                  __half2 u = __floats2half2_rn(p0 * vv[2 * b], p1 * vv[2 * b + 1]);
-#pragma unroll
-                  for (int q = 0; q < 2; ++q) {
-                    const uint32_t cutoff = *reinterpret_cast<uint32_t*>(&u) & 0xff00ff00u;
-                    h[b][q] = cutoff;
-                    u = __hsub2(u, *reinterpret_cast<const __half2*>(&cutoff));
-                  }
-                  h[b][2] = *reinterpret_cast<uint32_t*>(&u) + 0x00800080u;
+                  split3(__floats2half2_rn(p0 * vv[2 * b], p1 * vv[2 * b + 1]), h[b]);
                 }
 #pragma unroll
                 for (int q = 0; q < 3; ++q) w[q][i] = __byte_perm(h[0][q], h[1][q], 0x7531);
@@ -1053,6 +1119,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                 tmem_st8(lanes + s_col(j) + 32 * c + 16 + 8 * hf, lo);
               }
             }
+          };
+          // One pass: a weight may be larger than 1, so the reference need not
+          // be the maximum, only near enough.
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float x[32];
+            tmem_ld32(lanes + s_col(j) + 32 * c, x);
+            tmem_ld_wait();
+            weigh(c, x);
           }
           sum += (part[0] + part[1]) + (part[2] + part[3]);
           tmem_st_wait();
@@ -1187,6 +1262,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
                   const float2* refs) {
     if (tiles == 0) return;
     const int c0 = owner_of(units, first, nctas), c1 = owner_of(units, first + (tiles - 1) * weight, nctas);
+#pragma unroll 1
     for (int c = c0; c <= c1; ++c) {
       const int lo = bound_of(units, c, nctas), hi = bound_of(units, c + 1, nctas);
       const int k0 = first >= lo ? 0 : (lo - first + weight - 1) / weight;
@@ -1271,7 +1347,7 @@ int launch(const Plan& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, cons
 }  // namespace
 
 bool attend_tc_fits(const AttendArgs& a) {
-  if (a.d != kD || a.page_size % 16 || (long long)a.n_pages * a.page_size >= (1ll << 31) - 256) return false;
+  if (a.d != kD || a.page_size < 16 || (a.page_size & (a.page_size - 1)) || (long long)a.n_pages * a.page_size >= (1ll << 31) - 256) return false;
   // positions of tiles are 32-bit: the most that the block table allows
   Sizes z;
   if (!sizes_of(a.batch, a.n_tok, a.nq, a.nkv, a.shared_len, kMaxCtas, &z)) return false;
@@ -1296,6 +1372,7 @@ int launch_attend_tc(const AttendArgs& a, void* workspace, const Ctx& c) {
   p.tiles_s = z.tiles_s;
   p.row_weight = a.e4m3 ? 2 : 1;
   p.slot_rows = z.slot_rows;
+  while ((1 << p.page_shift) < a.page_size) ++p.page_shift;
   p.head = reinterpret_cast<int*>(ws + z.head);
   p.part_p = reinterpret_cast<float*>(ws + z.part_p);
   p.part_s = reinterpret_cast<float*>(ws + z.part_s);

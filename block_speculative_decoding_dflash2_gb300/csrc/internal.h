@@ -350,7 +350,7 @@ struct AttendArgs {
   unsigned* status;
 };
 int launch_attend(const AttendArgs& a, void* workspace, const Ctx& c);
-// tcgen05 attention (attend_tc.cu): head dimension 128, pages of whole 16-key groups
+// tcgen05 attention (attend_tc.cu): head dimension 128, pages of 2^n >= 16 keys
 bool attend_tc_fits(const AttendArgs& a);
 size_t attend_tc_workspace(int batch, int n_tok, int nq, int nkv, int shared_len);  // 0: sizes it does not take
 int launch_attend_tc(const AttendArgs& a, void* workspace, const Ctx& c);
