@@ -80,9 +80,9 @@ struct SegInfo {
   int f0, rows;         // first query row (sequence, token, head of the group), their number
   int n, len;           // tokens and keys of sequence s
   int split;            // both streams take the same rows
+  int copies;           // of the rows in the 128 of a stream (1, 2 or 4)
   int q;                // place of the query rows (split)
   int slot;             // place of the partial result, -1: the CTA finishes the segment
-  int pad;
 };
 
 template <bool E4M3>
@@ -105,7 +105,6 @@ struct Plan {
   int group, rows;     // query heads per kv head; query rows (n_tok * group) of a sequence
   int tiles_p;         // row tiles of the shared part (0: none)
   int tiles_s;         // row tiles of a sequence at most
-  int row_weight;      // cost of a tile for more than 128 rows, in tiles for fewer
   int slot_rows;       // rows of a sequence's partial slot
   int page_shift;      // page_size = 2^page_shift
   int* head;           // workspace: all positions, tiles of the shared part, first position of each row tile
@@ -146,7 +145,17 @@ __device__ __forceinline__ Segment segment_of(const AttendArgs& a, int group, in
   g.tiles = (hi - g.base + kTile - 1) / kTile;
   return g;
 }
-__device__ __forceinline__ int weight_of(const Plan& p, int rows) { return rows > kTile ? p.row_weight : 1; }
+// Cost of work in units of half a tile for up to 128 rows, near enough: a
+// tile for more of them, and a segment's start and end beside its tiles.
+constexpr int kSegCost = 10;
+__device__ __forceinline__ int weight_of(int rows) { return rows > kTile ? 4 : 2; }
+__device__ __forceinline__ int cost_of(int tiles, int w) { return tiles > 0 ? kSegCost + tiles * w : 0; }
+// The tiles [x, y) of a segment at position `at` that the share [a, b) has:
+// tile k counts as lying at at + kSegCost + k w.
+__device__ __forceinline__ int2 tiles_in(int at, int tiles, int w, int a, int b) {
+  at += kSegCost;
+  return make_int2(at >= a ? 0 : (a - at + w - 1) / w, b <= at ? 0 : min(tiles, (b - at + w - 1) / w));
+}
 
 // Share of CTA c of n: tiles whose position lies in [bound(c), bound(c + 1));
 // the first units % n shares are one larger.  (Positions fit 31 bits: the
@@ -194,6 +203,7 @@ __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile in
 
 __device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
+__device__ __forceinline__ void bar_stream(int j) { asm volatile("bar.sync %0, 128;" ::"r"(2 + j) : "memory"); }
 __device__ __forceinline__ bool bar_softmax_or(bool x) {
   uint32_t r;
   asm volatile(
@@ -365,6 +375,7 @@ __device__ __forceinline__ void load_rows(const Plan& p, const SegInfo& g, int r
   constexpr int W = E4M3 ? 8 : 16;  // lanes of a row
   constexpr int STEP = 32 / W;
   const int lane = threadIdx.x & 31, c = lane & (W - 1);
+  const int copy_rows = g.split ? kTile / g.copies : kTile;
   // this lane's row, stepped through the heads of the group, tokens and sequences without divisions
   int row = r0 + lane / W;
   int s = g.shared ? (g.f0 + row) / p.rows : g.s;
@@ -392,7 +403,9 @@ __device__ __forceinline__ void load_rows(const Plan& p, const SegInfo& g, int r
       const int r = (x + lane / W) & (kTile - 1);
       const bf16* src = source();
       if (x + lane / W < r1)
-        cp_async16(dst + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4), src ? src + c * 8 : a.q, src != nullptr);
+        for (int cp = 0; cp < kTile; cp += copy_rows)  // (a row's place in 8 is the same in every copy)
+          cp_async16(dst + (c >> 3) * 16384 + (cp + r) * 128 + (((c & 7) ^ (r & 7)) << 4), src ? src + c * 8 : a.q,
+                     src != nullptr);
     }
     cp_async_commit();
     cp_async_wait<0>();
@@ -433,9 +446,11 @@ __device__ __forceinline__ void load_rows(const Plan& p, const SegInfo& g, int r
         lo[i >> 1] = (i & 1) ? lo[i >> 1] | (l2 << 16) : l2;
       }
       if (fr < r1) {
-        uint8_t* q = dst + r * 128 + ((c ^ (r & 7)) << 4);
-        *reinterpret_cast<uint4*>(q) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(q + 16384) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        for (int cp = 0; cp < kTile; cp += copy_rows) {
+          uint8_t* q = dst + (cp + r) * 128 + ((c ^ (r & 7)) << 4);
+          *reinterpret_cast<uint4*>(q) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(q + 16384) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
         // a row that is not finite has no result
         if (c == 0)
           qscale[fr] = top >= 0x7f800000u ? __int_as_float(0x7fffffff)
@@ -515,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     const int s = p.tiles_s == 1 ? e : e / p.tiles_s;
     *nl = lengths(a, s);
     const Segment g = segment_of(a, p.group, *nl, p.tiles_s == 1 ? 0 : e % p.tiles_s);
-    return g.tiles * weight_of(p, g.rows) * a.nkv;
+    return cost_of(g.tiles, weight_of(g.rows)) * a.nkv;
   };
   int my_units = 0, lo = INT32_MAX, hi = 0;
   for (int e = e0; e < e1; ++e) {
@@ -557,7 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
   hi = min(hi, a.shared_len);
   const int base_p = lo & ~15, end_p = hi;
   const int tiles_p = p.tiles_p > 0 && hi > lo ? (hi - base_p + kTile - 1) / kTile : 0;
-  const int up = p.tiles_p * a.nkv * tiles_p * p.row_weight, units = up + total;
+  const int cost_p = cost_of(tiles_p, weight_of(kRowTile));  // (its last row tile may be cheaper: no matter)
+  const int up = p.tiles_p * a.nkv * cost_p, units = up + total;
   const int share_a = bound_of(units, cta, nctas), share_b = bound_of(units, cta + 1, nctas);
   if (cta == 0) {  // for the joining kernel
     if (threadIdx.x == 0) {
@@ -617,8 +633,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     int entry, at;
     bool shared = share_a < up;
     if (shared) {
-      entry = share_a / (tiles_p * p.row_weight * a.nkv);
-      at = entry * (tiles_p * p.row_weight * a.nkv);
+      entry = share_a / (cost_p * a.nkv);
+      at = entry * (cost_p * a.nkv);
     } else {
       entry = start[0];
       at = start[1];
@@ -633,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         g.rows = min(kRowTile, a.batch * p.rows - g.f0);
         base = base_p;
         tiles = tiles_p;
-        w = p.row_weight;
+        w = weight_of(kRowTile);
         g.end = end_p;
         g.n = g.len = 0;
         // keys that all of its rows see
@@ -656,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         g.rows = x.rows;
         base = x.base;
         tiles = x.tiles;
-        w = weight_of(p, g.rows);
+        w = weight_of(g.rows);
         g.end = x.end;
         g.n = nl.x;
         g.len = nl.y;
@@ -665,14 +681,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
       }
       g.shared = shared;
       g.split = g.rows <= kTile;
-      for (int h = 0; h < a.nkv && ok; ++h, at += tiles * w) {
+      g.copies = g.rows <= 32 ? 4 : g.rows <= 64 ? 2 : 1;
+      for (int h = 0; h < a.nkv && ok; ++h, at += cost_of(tiles, w)) {
         if (tiles == 0 || at >= share_b) break;
-        const int k0 = at >= share_a ? 0 : (share_a - at + w - 1) / w, k1 = min(tiles, (share_b - at + w - 1) / w);
-        if (k0 >= k1) continue;
+        const int2 k = tiles_in(at, tiles, w, share_a, share_b);
+        if (k.x >= k.y) continue;
         g.h = h;
-        g.first = base + k0 * kTile;
-        g.tiles = k1 - k0;
-        g.slot = k0 == 0 && k1 == tiles && p.tiles_p == 0 ? -1 : entry * a.nkv + h + cta;
+        g.first = base + k.x * kTile;
+        g.tiles = k.y - k.x;
+        g.slot = k.x == 0 && k.y == tiles && p.tiles_p == 0 ? -1 : entry * a.nkv + h + cta;
         g.q = g.split ? q_next : 0;
         // query rows of both or of one place, K-major with the 128-byte swizzle
         for (int b = g.split ? g.q : 0; b < (g.split ? g.q + 1 : 2); ++b) {
@@ -982,7 +999,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     for (; next_segment(&g); seg_at.step()) {
       const int nt = g.tiles;
       const bool split = g.split != 0;  // the streams share the rows
-      const int fr = (split ? 0 : j * kTile) + r;
+      // With few rows the 128 hold copies of them, and each copy weighs a part
+      // of a tile's keys, so that all four warps of a stream have work.
+      const int copies = split ? g.copies : 1, copy_rows = kTile / copies;
+      const int fr = split ? r & (copy_rows - 1) : j * kTile + r;
+      const int c_lo = r / copy_rows * (4 / copies), c_hi = c_lo + 4 / copies;  // its pieces of 32 keys
       const bool mine = fr < g.rows;
       const int f = g.f0 + (mine ? fr : 0);
       const int s = g.shared ? f / p.rows : g.s, local = f - s * p.rows, t_row = local / p.group;
@@ -1124,6 +1145,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
           // be the maximum, only near enough.
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
+            if (c < c_lo || c >= c_hi) {  // (the whole warp: copies are of 32 rows or more)
+              const uint32_t none[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+              for (int q = 0; q < (E4M3 ? 3 : 4); ++q) tmem_st8(lanes + s_col(j) + 32 * c + 8 * q, none);
+              continue;
+            }
             float x[32];
             tmem_ld32(lanes + s_col(j) + 32 * c, x);
             tmem_ld_wait();
@@ -1147,9 +1174,49 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         ++n_o;
       }
       if (poison) sum = __int_as_float(0x7fffffff);
-      float w0 = 1.f, w1 = 0.f;
-      if (split) {
-        // (R, sum) change hands in the place of the query rows, whose products are done
+      const bool whole = g.slot < 0;
+      if (!split) {
+        tc_fence_after();
+        if (!idle) {
+          float* part = nullptr;
+          if (!whole) {
+            const size_t row = (size_t)g.slot * (g.shared ? kRowTile : p.slot_rows) + fr;
+            part = (g.shared ? p.part_p : p.part_s) + row * kD;
+            if (mine) (g.shared ? p.ref_p : p.ref_s)[row] = make_float2(ref, sum);
+          }
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          bf16* orow = a.out + ((size_t)s * a.n_tok + t_row) * a.out_stride + (size_t)head * kD;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float o[32];
+            tmem_ld32(lanes + o_col(j) + 32 * c, o);
+            tmem_ld_wait();
+            if (whole) {
+              if (real) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  uint32_t w[4];
+#pragma unroll
+                  for (int b = 0; b < 4; ++b)
+                    w[b] = sum == 0.f ? 0u : bits2(__floats2bfloat162_rn(o[8 * i + 2 * b] * inv, o[8 * i + 2 * b + 1] * inv));
+                  reinterpret_cast<uint4*>(orow + 32 * c)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+              }
+            } else if (mine) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                reinterpret_cast<float4*>(part + 32 * c)[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(q_empty);
+          mbar_arrive(q_empty + 1);
+        }
+      } else {
+        // A row's parts are in both streams and in every copy.  They meet in
+        // the place of the query rows, whose products are done.
         float2* xch = reinterpret_cast<float2*>(sm + L::Q + g.q * 32768);
         bar_softmax();  // both streams' products
         xch[j * kTile + r] = make_float2(ref, sum);
@@ -1157,41 +1224,32 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         bar_softmax();
         tc_fence_after();
         // (a stream without tiles has no reference, and its accumulator is not read)
-        const float2 x0 = xch[r], x1 = xch[kTile + r];
-        ref = fmaxf(x0.x, x1.x);
+        const float mine0 = xch[r].x, mine1 = both ? xch[kTile + r].x : kNone;
+        ref = kNone;
+        sum = 0.f;
+        for (int i = fr; i < 2 * kTile; i += copy_rows)
+          if (i < kTile || both) ref = fmaxf(ref, xch[i].x);
         const float base = ref == kNone ? 0.f : ref;
-        w0 = ex2(x0.x - base);
-        w1 = both ? ex2(x1.x - base) : 0.f;
-        sum = x0.y * w0 + (both ? x1.y * w1 : 0.f);
-      } else {
-        tc_fence_after();
-      }
-      __syncwarp();
-      if (lane == 0) {
-        if (split) {
-          mbar_arrive(q_empty + g.q);
-        } else {
-          mbar_arrive(q_empty);
-          mbar_arrive(q_empty + 1);
-        }
-      }
-      const bool whole = g.slot < 0;
-      if (!idle) {
-        float* part = nullptr;
-        if (!whole) {
+        for (int i = fr; i < 2 * kTile; i += copy_rows)
+          if (i < kTile || both) sum = fmaf(xch[i].y, ex2(xch[i].x - base), sum);
+        const float w0 = ex2(mine0 - base), w1 = ex2(mine1 - base);
+        if (!whole && j == 0 && r < copy_rows && mine) {
           const size_t row = (size_t)g.slot * (g.shared ? kRowTile : p.slot_rows) + fr;
-          part = (g.shared ? p.part_p : p.part_s) + row * kD;
-          if (mine && (!split || j == 0)) (g.shared ? p.ref_p : p.ref_s)[row] = make_float2(ref, sum);
+          (g.shared ? p.ref_p : p.ref_s)[row] = make_float2(ref, sum);
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        bf16* orow = a.out + ((size_t)s * a.n_tok + t_row) * a.out_stride + (size_t)head * kD;
-        // streams that share rows take half of the dims each
+        // factor of the result: with `whole` the row's 1 / sum, in every copy
+        const float fin = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+        // Stream j's warps take dims 64 j .. 64 j + 63, 32 at a time: both
+        // accumulators' into shared memory (pieces of 16 bytes at piece ^
+        // row % 8), then the sums over the copies, out.
+        float4* box = reinterpret_cast<float4*>(sm + L::Q + g.q * 32768 + j * 16384);
 #pragma unroll 1
-        for (int c = split ? 2 * j : 0; c < (split ? 2 * j + 2 : 4); ++c) {
+        for (int part = 0; part < 2; ++part) {
+          const int c = 2 * j + part;
           float o[32];
-          tmem_ld32(lanes + o_col(split ? 0 : j) + 32 * c, o);
-          tmem_ld_wait();
-          if (split) {
+          if (!idle) {
+            tmem_ld32(lanes + o_col(0) + 32 * c, o);
+            tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] *= w0;
             if (both) {
@@ -1202,24 +1260,40 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
               for (int i = 0; i < 32; ++i) o[i] = fmaf(o1[i], w1, o[i]);
             }
           }
-          if (whole) {
-            if (real) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t w[4];
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-                  w[b] = bits2(__floats2bfloat162_rn(sum == 0.f ? 0.f : o[8 * i + 2 * b] * inv,
-                                                     sum == 0.f ? 0.f : o[8 * i + 2 * b + 1] * inv));
-                reinterpret_cast<uint4*>(orow + 32 * c)[i] = make_uint4(w[0], w[1], w[2], w[3]);
-              }
-            }
-          } else if (mine) {
+          if (part == 0) bar_softmax();  // everyone has read the references and sums,
+          else bar_stream(j);            // or the last part
+          if (!idle) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              reinterpret_cast<float4*>(part + 32 * c)[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              box[r * 8 + (i ^ (r & 7))] = sum == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                                     : make_float4(o[4 * i] * fin, o[4 * i + 1] * fin, o[4 * i + 2] * fin, o[4 * i + 3] * fin);
+          }
+          bar_stream(j);
+          for (int i = r; i < g.rows * 8; i += kTile) {
+            const int row = i >> 3, piece = i & 7;
+            float4 x = box[row * 8 + (piece ^ (row & 7))];
+            for (int cp = copy_rows; cp < kTile; cp += copy_rows) {
+              const float4 y = box[(cp + row) * 8 + (piece ^ (row & 7))];
+              x.x += y.x;
+              x.y += y.y;
+              x.z += y.z;
+              x.w += y.w;
+            }
+            if (!whole) {
+              const size_t at = ((size_t)g.slot * (g.shared ? kRowTile : p.slot_rows) + row) * kD + 32 * c + 4 * piece;
+              *reinterpret_cast<float4*>((g.shared ? p.part_p : p.part_s) + at) = x;
+            } else {  // (a sequence's own rows)
+              const int lr = g.f0 + row - g.s * p.rows, t = lr / p.group;
+              uint2 y;
+              y.x = bits2(__floats2bfloat162_rn(x.x, x.y));
+              y.y = bits2(__floats2bfloat162_rn(x.z, x.w));
+              *reinterpret_cast<uint2*>(a.out + ((size_t)g.s * a.n_tok + t) * a.out_stride +
+                                        (size_t)(g.h * p.group + lr - t * p.group) * kD + 32 * c + 4 * piece) = y;
+            }
           }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_empty + g.q);
       }
       tc_fence_before();
       if (split) bar_softmax();  // both streams have read both accumulators
@@ -1251,23 +1325,22 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   const int units = p.head[0];
   const int i = local / kRowTile, entry = s * p.tiles_s + i;
   const Segment g = segment_of(a, p.group, nl, i);
-  const int w = weight_of(p, g.rows);
-  const int at = p.head[2 + entry] + h * g.tiles * w;
+  const int w = weight_of(g.rows);
+  const int at = p.head[2 + entry] + h * cost_of(g.tiles, w);
   if (p.tiles_p == 0 && g.tiles > 0 &&
-      owner_of(units, at, nctas) == owner_of(units, at + (g.tiles - 1) * w, nctas))
+      owner_of(units, at + kSegCost, nctas) == owner_of(units, at + kSegCost + (g.tiles - 1) * w, nctas))
     return;
   float ref = kNone, sum = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   auto join = [&](int first, int tiles, int weight, int ordinal, int rows, int row, const float* part,
                   const float2* refs) {
     if (tiles == 0) return;
-    const int c0 = owner_of(units, first, nctas), c1 = owner_of(units, first + (tiles - 1) * weight, nctas);
+    const int c0 = owner_of(units, first + kSegCost, nctas);
+    const int c1 = owner_of(units, first + kSegCost + (tiles - 1) * weight, nctas);
 #pragma unroll 1
     for (int c = c0; c <= c1; ++c) {
-      const int lo = bound_of(units, c, nctas), hi = bound_of(units, c + 1, nctas);
-      const int k0 = first >= lo ? 0 : (lo - first + weight - 1) / weight;
-      const int k1 = min(tiles, (hi - first + weight - 1) / weight);
-      if (k0 >= k1) continue;  // no tile starts in this CTA's share
+      const int2 k = tiles_in(first, tiles, weight, bound_of(units, c, nctas), bound_of(units, c + 1, nctas));
+      if (k.x >= k.y) continue;  // no tile lies in this CTA's share
       const size_t at_row = (size_t)(ordinal + c) * rows + row;
       const float2 rl = refs[at_row];
       const float4 x = reinterpret_cast<const float4*>(part + at_row * kD)[lane];
@@ -1285,8 +1358,8 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   };
   if (p.tiles_p > 0) {
     const int ip = f / kRowTile, tiles = p.head[1], ordinal = ip * a.nkv + h;
-    const int wp = p.row_weight;
-    join(ordinal * tiles * wp, tiles, wp, ordinal, kRowTile, f % kRowTile, p.part_p, p.ref_p);
+    const int wp = weight_of(kRowTile);
+    join(ordinal * cost_of(tiles, wp), tiles, wp, ordinal, kRowTile, f % kRowTile, p.part_p, p.ref_p);
   }
   join(at, g.tiles, w, entry * a.nkv + h, p.slot_rows, local % kRowTile, p.part_s, p.ref_s);
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -1352,7 +1425,7 @@ bool attend_tc_fits(const AttendArgs& a) {
   Sizes z;
   if (!sizes_of(a.batch, a.n_tok, a.nq, a.nkv, a.shared_len, kMaxCtas, &z)) return false;
   const long long each = ((long long)a.max_pages * a.page_size + 15) / kTile + 2;
-  return ((long long)a.batch * z.tiles_s + z.tiles_p) * a.nkv * each * 2 < (1ll << 31);
+  return ((long long)a.batch * z.tiles_s + z.tiles_p) * a.nkv * (each * 4 + 16) < (1ll << 31);
 }
 
 size_t attend_tc_workspace(int batch, int n_tok, int nq, int nkv, int shared_len) {
@@ -1370,7 +1443,6 @@ int launch_attend_tc(const AttendArgs& a, void* workspace, const Ctx& c) {
   p.rows = z.rows;
   p.tiles_p = z.tiles_p;
   p.tiles_s = z.tiles_s;
-  p.row_weight = a.e4m3 ? 2 : 1;
   p.slot_rows = z.slot_rows;
   while ((1 << p.page_shift) < a.page_size) ++p.page_shift;
   p.head = reinterpret_cast<int*>(ws + z.head);
