@@ -96,7 +96,7 @@ struct Smem {
   static constexpr int SEG = INFO + kInfo * INFOS;
   static constexpr int QSCALE = SEG + kSegs * (int)sizeof(SegInfo);  // float [kSegs][kRowTile], 8-bit only
   static constexpr int BAR = QSCALE + (E4M3 ? kSegs * kRowTile * 4 : 0);
-  static constexpr size_t bytes = 1024 + BAR + (2 * SLOTS + 2 * kInfo + 2 * kSegs + 10) * 8 + 64;
+  static constexpr size_t bytes = 1024 + BAR + (2 * SLOTS + 2 * kInfo + 2 * kSegs + 12) * 8 + 64;
   static_assert(bytes + 512 <= 227 * 1024, "shared memory");
 };
 
@@ -282,6 +282,31 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
 }
 
 __device__ __forceinline__ uint32_t bits2(__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+
+// Two fp32 at a time.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
@@ -483,7 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
   uint64_t* o_done = p_ready + 2;           // [2] a segment's last product of the stream is done
   uint64_t* q_empty = o_done + 2;           // [2] a place of query rows is free (8 arrivals)
   uint64_t* q_ready = q_empty + 2;          // query rows that the softmax warps load themselves (8 arrivals)
-  uint64_t* drain = q_ready + 1;            // every product issued is done
+  uint64_t* q_full = q_ready + 1;           // [2] query rows that warp 11 loaded into a place
+  uint64_t* drain = q_full + 2;             // every product issued is done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   SegInfo* segs = reinterpret_cast<SegInfo*>(sm + L::SEG);
@@ -509,6 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
       mbar_init(p_ready + j, 4);
       mbar_init(o_done + j, 1);
       mbar_init(q_empty + j, 8);
+      mbar_init(q_full + j, 1);
     }
     mbar_init(q_ready, 8);
     mbar_init(drain, 1);
@@ -691,22 +718,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         g.tiles = k.y - k.x;
         g.slot = k.x == 0 && k.y == tiles && p.tiles_p == 0 ? -1 : entry * a.nkv + h + cta;
         g.q = g.split ? q_next : 0;
-        // query rows of both or of one place, K-major with the 128-byte swizzle
+        if (seg_at.round > 0) ok = wait(seg_empty + seg_at.slot, (seg_at.round - 1) & 1) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) segs[seg_at.slot] = g;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(seg_full + seg_at.slot);  // (its keys and values may be on their way before its rows)
+        // query rows: the place (both, where the softmax warps load them) has to be free
         for (int b = g.split ? g.q : 0; b < (g.split ? g.q + 1 : 2); ++b) {
           if (q_uses[b] > 0) ok = wait(q_empty + b, (q_uses[b] - 1) & 1) && ok;
           ++q_uses[b];
         }
-        if (g.split) q_next ^= 1;
-        if (seg_at.round > 0) ok = wait(seg_empty + seg_at.slot, (seg_at.round - 1) & 1) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (g.split)
+        if (g.split) {
+          q_next ^= 1;
           load_rows<E4M3>(p, g, 0, g.rows, sm + L::Q + g.q * 32768,
                           reinterpret_cast<float*>(sm + L::QSCALE) + seg_at.slot * kRowTile);
-        fence_proxy_async_smem();
-        if (lane == 0) segs[seg_at.slot] = g;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(seg_full + seg_at.slot);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_full + g.q);
+        }
         seg_at.step();
       }
       // (after the last kv head `at` is the next row tile's first position)
@@ -794,19 +826,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
           (E4M3 ? (1u << 4) | (1u << 7) | ((kD >> 3) << 17) | ((kTile >> 4) << 24) : idesc_bf16_f32(kTile, kD)) |
           (1u << 16);
       Ring<NS> at;
-      uint32_t n_p = 0, n_q = 0;  // bit j: parity of stream j's weights; parity of the query rows
+      uint32_t n_p = 0, n_q = 0;  // parities: of the streams' weights; of the places' query rows and of q_ready
       bool ok = true;
       for (; ok; seg_at.step()) {
         if (!wait(seg_full + seg_at.slot, seg_at.round & 1)) break;
         const SegInfo& g = segs[seg_at.slot];
-        const int nt = g.tiles, lead = g.split ? 2 : 1;
-        const uint32_t q0 = qs + g.q * 2048;
+        const int nt = g.tiles, lead = g.split ? 2 : 1, g_q = g.q;
+        const uint32_t q0 = qs + g_q * 2048;
         mbar_arrive(seg_empty + seg_at.slot);
         if (nt == 0) break;
-        if (lead == 1) {
-          if (!wait(q_ready, n_q & 1)) break;
-          ++n_q;
-        }
+        uint64_t* rows_there = lead == 1 ? q_ready : q_full + g_q;
+        const uint32_t bit = lead == 1 ? 4u : 1u << g_q;
+        if (!wait(rows_there, (n_q & bit) ? 1 : 0)) break;
+        n_q ^= bit;
         // Work u: stream u % 2's products with a tile's values, and then its
         // scores of the next one.  With shared rows stream u % 2 takes tile u
         // and the slots go K0 K1 V0 K2 V1 K3 ...; otherwise both take tile
@@ -994,7 +1026,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     // how far a weight may pass 2^0: any float will do, or, times the value's
     // scale, what an e5m2 holds
     const float head_room = E4M3 ? 15.f : 64.f;
-    uint32_t n_s = 0, n_o = 0, tiles = 0;
+    uint32_t n_s = 0, n_o = 0, n_q = 0, tiles = 0;
     SegInfo g;
     for (; next_segment(&g); seg_at.step()) {
       const int nt = g.tiles;
@@ -1011,6 +1043,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
       if (!split) {
         // (many rows are a long segment: no warp has to load them ahead)
         const int w0 = warp * 32;
+        // (both places are free: this warp has been through its last segment, and so has every other, by the vote)
         if (w0 < g.rows)
           load_rows<E4M3>(p, g, w0, min(w0 + 32, g.rows), sm + L::Q + j * 32768,
                           reinterpret_cast<float*>(sm + L::QSCALE) + seg_at.slot * kRowTile);
@@ -1027,7 +1060,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         see = real ? sees(a, nl, t_row) : make_int2(0, 0);
         if (g.shared) see.y = min(see.y, a.shared_len);
         else see.x = max(see.x, a.shared_len);
-        if (E4M3) rs *= reinterpret_cast<const float*>(sm + L::QSCALE)[seg_at.slot * kRowTile + fr];
+      }
+      if (E4M3) {
+        if (split) {
+          wait(q_full + g.q, (n_q >> g.q) & 1);
+          n_q ^= 1u << g.q;
+        }
+        if (mine) rs *= reinterpret_cast<const float*>(sm + L::QSCALE)[seg_at.slot * kRowTile + fr];
       }
       if (E4M3) {
         __syncwarp();
@@ -1062,17 +1101,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
             if (!((groups >> (2 * c + 1)) & 1)) m &= 0x0000ffffu;
             return m;
           };
-          float part[4] = {0.f, 0.f, 0.f, 0.f};
+          uint64_t part[2] = {0ull, 0ull};  // sums of weights, two each
+          const uint64_t rs2 = pack2(rs, rs);
           // 32 keys: their scores become weights in the same TMEM columns
           auto weigh = [&](int c, float (&x)[32]) {
             if (E4M3) {
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
-                const float4 k4 = *reinterpret_cast<const float4*>(info->ks + 32 * c + i);
-                x[i] *= k4.x;
-                x[i + 1] *= k4.y;
-                x[i + 2] *= k4.z;
-                x[i + 3] *= k4.w;
+                const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(info->ks + 32 * c + i);
+                unpack2(mul2(pack2(x[i], x[i + 1]), k4.x), x[i], x[i + 1]);
+                unpack2(mul2(pack2(x[i + 2], x[i + 3]), k4.y), x[i + 2], x[i + 3]);
               }
             }
             if (cut) {
@@ -1095,26 +1133,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
               const float now = fmaxf(ref, ceilf(top) - (E4M3 ? 11.f : 0.f));
               const float by = ref == kNone ? 0.f : ex2(ref - now);
               sum *= by;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) part[i] *= by;
+              part[0] = mul2(part[0], pack2(by, by));
+              part[1] = mul2(part[1], pack2(by, by));
               ref = now;
               rescale<E4M3>(lanes + o_col(j), done > 0 ? 4 : 0, lanes + s_col(j), c, by);
             }
-            const float sub = ref == kNone ? 0.f : ref;
+            const float sub = ref == kNone ? 0.f : -ref;
+            const uint64_t sub2 = pack2(sub, sub);
             if (E4M3) {
               uint32_t w[3][8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) {  // four keys: a column of each part
-                const float4 v4 = *reinterpret_cast<const float4*>(info->vs + 32 * c + 4 * i);
-                const float vv[4] = {v4.x, v4.y, v4.z, v4.w};
+                const ulonglong2 v4 = *reinterpret_cast<const ulonglong2*>(info->vs + 32 * c + 4 * i);
                 uint32_t h[2][3];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                  const float p0 = ex2(fmaf(x[4 * i + 2 * b], rs, -sub));
-                  const float p1 = ex2(fmaf(x[4 * i + 2 * b + 1], rs, -sub));
-                  part[2 * b] += p0;
-                  part[2 * b + 1] += p1;
-                  split3(__floats2half2_rn(p0 * vv[2 * b], p1 * vv[2 * b + 1]), h[b]);
+                  float p0, p1;
+                  unpack2(fma2(pack2(x[4 * i + 2 * b], x[4 * i + 2 * b + 1]), rs2, sub2), p0, p1);
+                  const uint64_t pp = pack2(ex2(p0), ex2(p1));
+                  part[b] = add2(part[b], pp);
+                  unpack2(mul2(pp, b ? v4.y : v4.x), p0, p1);
+                  split3(__floats2half2_rn(p0, p1), h[b]);
                 }
 #pragma unroll
                 for (int q = 0; q < 3; ++q) w[q][i] = __byte_perm(h[0][q], h[1][q], 0x7531);
@@ -1127,14 +1166,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                 uint32_t hi[8], lo[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                  const float p0 = ex2(fmaf(x[16 * hf + 2 * i], rs, -sub));
-                  const float p1 = ex2(fmaf(x[16 * hf + 2 * i + 1], rs, -sub));
-                  part[(2 * i) & 3] += p0;
-                  part[(2 * i + 1) & 3] += p1;
+                  float p0, p1;
+                  unpack2(fma2(pack2(x[16 * hf + 2 * i], x[16 * hf + 2 * i + 1]), rs2, sub2), p0, p1);
+                  p0 = ex2(p0);
+                  p1 = ex2(p1);
+                  const uint64_t pp = pack2(p0, p1);
+                  part[i & 1] = add2(part[i & 1], pp);
                   const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
-                  hi[i] = __byte_perm(b0, b1, 0x7632);  // cut to the top 16 bits
-                  lo[i] = bits2(__floats2bfloat162_rn(p0 - __uint_as_float(b0 & 0xffff0000u),
-                                                      p1 - __uint_as_float(b1 & 0xffff0000u)));
+                  hi[i] = __byte_perm(b0, b1, 0x7632);  // cut to the top 16 bits; what is left is exact
+                  unpack2(add2(pp, pack2(__uint_as_float((b0 & 0xffff0000u) ^ 0x80000000u),
+                                         __uint_as_float((b1 & 0xffff0000u) ^ 0x80000000u))), p0, p1);
+                  lo[i] = bits2(__floats2bfloat162_rn(p0, p1));
                 }
                 tmem_st8(lanes + s_col(j) + 32 * c + 8 * hf, hi);
                 tmem_st8(lanes + s_col(j) + 32 * c + 16 + 8 * hf, lo);
@@ -1156,7 +1198,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
             tmem_ld_wait();
             weigh(c, x);
           }
-          sum += (part[0] + part[1]) + (part[2] + part[3]);
+          float s0, s1;
+          unpack2(add2(part[0], part[1]), s0, s1);
+          sum += s0 + s1;
           tmem_st_wait();
         }
         tc_fence_before();
@@ -1309,64 +1353,115 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
 
 // ------------------------------------------------------------------ joining kernel
 
-// A warp per query row: the partial accumulators of its segments, weighted
-// to a common reference.  Rows that one CTA finished are there already.
+// A block per segment of the sequences: the partial accumulators of its rows,
+// weighted to a common reference.  Segments that one CTA finished are there
+// already.  The CTAs that have parts of it are found by all threads at once,
+// and a warp takes four rows at a time, so that their loads overlap.
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ Plan p, int nctas) {
+  __shared__ uint32_t has[3][(kMaxCtas + 31) / 32];  // CTAs with parts: the sequence's, and of two row tiles of the shared part
   pdl_launch_next();
   pdl_wait();
   const AttendArgs& a = p.a;
-  const int lane = threadIdx.x & 31;
-  const long long id = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (id >= (long long)a.batch * p.rows * a.nkv) return;
-  const int h = (int)(id % a.nkv), f = (int)(id / a.nkv);
-  const int s = f / p.rows, t = (f / p.group) % a.n_tok, local = f - s * p.rows;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int entry = blockIdx.x / a.nkv, h = blockIdx.x - entry * a.nkv;
+  const int s = p.tiles_s == 1 ? entry : entry / p.tiles_s, i = entry - s * p.tiles_s;
   const int2 nl = lengths(a, s);
-  if (t >= nl.x) return;
-  const int units = p.head[0];
-  const int i = local / kRowTile, entry = s * p.tiles_s + i;
+  const int units = p.head[0], tiles_p = p.head[1], start = p.head[2 + entry];
   const Segment g = segment_of(a, p.group, nl, i);
-  const int w = weight_of(g.rows);
-  const int at = p.head[2 + entry] + h * cost_of(g.tiles, w);
-  if (p.tiles_p == 0 && g.tiles > 0 &&
-      owner_of(units, at + kSegCost, nctas) == owner_of(units, at + kSegCost + (g.tiles - 1) * w, nctas))
-    return;
-  float ref = kNone, sum = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto join = [&](int first, int tiles, int weight, int ordinal, int rows, int row, const float* part,
-                  const float2* refs) {
-    if (tiles == 0) return;
-    const int c0 = owner_of(units, first + kSegCost, nctas);
-    const int c1 = owner_of(units, first + kSegCost + (tiles - 1) * weight, nctas);
-#pragma unroll 1
-    for (int c = c0; c <= c1; ++c) {
-      const int2 k = tiles_in(first, tiles, weight, bound_of(units, c, nctas), bound_of(units, c + 1, nctas));
-      if (k.x >= k.y) continue;  // no tile lies in this CTA's share
-      const size_t at_row = (size_t)(ordinal + c) * rows + row;
-      const float2 rl = refs[at_row];
-      const float4 x = reinterpret_cast<const float4*>(part + at_row * kD)[lane];
-      if (rl.y == 0.f) continue;
-      const float now = fmaxf(ref, rl.x);
-      const float base = now == kNone ? 0.f : now;
-      const float fo = ex2(ref - base), fx = ex2(rl.x - base);
-      sum = fmaf(sum, fo, rl.y * fx);
-      o.x = fmaf(o.x, fo, x.x * fx);
-      o.y = fmaf(o.y, fo, x.y * fx);
-      o.z = fmaf(o.z, fo, x.z * fx);
-      o.w = fmaf(o.w, fo, x.w * fx);
-      ref = now;
+  const int rows = min(kRowTile, nl.x * p.group - i * kRowTile);
+  if (rows <= 0) return;
+  const int w = weight_of(g.rows), wp = weight_of(kRowTile), f0 = s * p.rows + i * kRowTile;
+  const int at = start + h * cost_of(g.tiles, w), ip = f0 / kRowTile, cost_p = cost_of(tiles_p, wp);
+  // (a block looks at one CTA per thread)
+  uint32_t mine = 0;
+  {
+    const int c = threadIdx.x;
+    bool own = false, p0 = false, p1 = false;
+    if (c < nctas) {
+      const int lo = bound_of(units, c, nctas), hi = bound_of(units, c + 1, nctas);
+      if (g.tiles > 0) {
+        const int2 k = tiles_in(at, g.tiles, w, lo, hi);
+        own = k.x < k.y && (p.tiles_p > 0 || k.x > 0 || k.y < g.tiles);
+      }
+      if (tiles_p > 0) {
+        int2 k = tiles_in((ip * a.nkv + h) * cost_p, tiles_p, wp, lo, hi);
+        p0 = k.x < k.y;
+        k = tiles_in(((ip + 1) * a.nkv + h) * cost_p, tiles_p, wp, lo, hi);
+        p1 = k.x < k.y;
+      }
     }
-  };
-  if (p.tiles_p > 0) {
-    const int ip = f / kRowTile, tiles = p.head[1], ordinal = ip * a.nkv + h;
-    const int wp = weight_of(kRowTile);
-    join(ordinal * cost_of(tiles, wp), tiles, wp, ordinal, kRowTile, f % kRowTile, p.part_p, p.ref_p);
+    const uint32_t m0 = __ballot_sync(0xffffffffu, own), m1 = __ballot_sync(0xffffffffu, p0),
+                   m2 = __ballot_sync(0xffffffffu, p1);
+    if (lane == 0) {
+      has[0][warp] = m0;
+      has[1][warp] = m1;
+      has[2][warp] = m2;
+    }
+    mine = m0;
   }
-  join(at, g.tiles, w, entry * a.nkv + h, p.slot_rows, local % kRowTile, p.part_s, p.ref_s);
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  uint2 out;
-  out.x = sum == 0.f ? 0u : bits2(__floats2bfloat162_rn(o.x * inv, o.y * inv));
-  out.y = sum == 0.f ? 0u : bits2(__floats2bfloat162_rn(o.z * inv, o.w * inv));
-  reinterpret_cast<uint2*>(a.out + ((size_t)s * a.n_tok + t) * a.out_stride + (size_t)(h * p.group + f % p.group) * kD)[lane] = out;
+  const bool any = __syncthreads_or(mine);
+  if (!any && g.tiles > 0 && p.tiles_p == 0) return;  // one CTA has written it (without tiles nobody has: zeros)
+  constexpr int RW = 4;
+  for (int r0 = warp; r0 < rows; r0 += 8 * RW) {
+    float ref[RW], sum[RW];
+    float4 o[RW];
+#pragma unroll
+    for (int u = 0; u < RW; ++u) {
+      ref[u] = kNone;
+      sum[u] = 0.f;
+      o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll 1
+    for (int kind = 0; kind < 3; ++kind) {
+#pragma unroll 1
+      for (int word = 0; word < (nctas + 31) / 32; ++word) {
+        uint32_t m = has[kind][word];
+        while (m) {
+          const int c = word * 32 + __ffs(m) - 1;
+          m &= m - 1;
+          float2 rl[RW];
+          float4 x[RW];
+#pragma unroll
+          for (int u = 0; u < RW; ++u) {
+            const int r = r0 + 8 * u, f = f0 + r;
+            // (rows of a segment may lie in two row tiles of the shared part)
+            const bool in = r < rows && (kind == 0 || f / kRowTile == ip + kind - 1);
+            rl[u] = make_float2(kNone, 0.f);
+            x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (in) {
+              const size_t row = kind == 0 ? (size_t)(entry * a.nkv + h + c) * p.slot_rows + r
+                                           : (size_t)((ip + kind - 1) * a.nkv + h + c) * kRowTile + f % kRowTile;
+              rl[u] = (kind == 0 ? p.ref_s : p.ref_p)[row];
+              x[u] = reinterpret_cast<const float4*>((kind == 0 ? p.part_s : p.part_p) + row * kD)[lane];
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < RW; ++u) {
+            if (rl[u].y == 0.f) continue;
+            const float now = fmaxf(ref[u], rl[u].x), base = now == kNone ? 0.f : now;
+            const float fo = ex2(ref[u] - base), fx = ex2(rl[u].x - base);
+            sum[u] = fmaf(sum[u], fo, rl[u].y * fx);
+            o[u].x = fmaf(o[u].x, fo, x[u].x * fx);
+            o[u].y = fmaf(o[u].y, fo, x[u].y * fx);
+            o[u].z = fmaf(o[u].z, fo, x[u].z * fx);
+            o[u].w = fmaf(o[u].w, fo, x[u].w * fx);
+            ref[u] = now;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < RW; ++u) {
+      const int r = r0 + 8 * u;
+      if (r >= rows) continue;
+      const int lr = i * kRowTile + r, t = lr / p.group;
+      const float inv = sum[u] == 0.f ? 0.f : 1.f / sum[u];
+      uint2 y;
+      y.x = sum[u] == 0.f ? 0u : bits2(__floats2bfloat162_rn(o[u].x * inv, o[u].y * inv));
+      y.y = sum[u] == 0.f ? 0u : bits2(__floats2bfloat162_rn(o[u].z * inv, o[u].w * inv));
+      reinterpret_cast<uint2*>(a.out + ((size_t)s * a.n_tok + t) * a.out_stride + (size_t)(h * p.group + lr - t * p.group) * kD)[lane] = y;
+    }
+  }
 }
 
 // ------------------------------------------------------------------ host
@@ -1413,8 +1508,7 @@ int launch(const Plan& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, cons
     return DFLASH2_ERR_CUDA;
   const int rc = launch_k(attend_tc_kernel<E4M3>, dim3(c.nsm), dim3(kThreads), Smem<E4M3>::bytes, c, p, tm_k, tm_v);
   if (rc != DFLASH2_OK) return rc;
-  const long long rows = (long long)p.a.batch * p.rows * p.a.nkv;
-  return launch_k(attend_join_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, c, p, c.nsm);
+  return launch_k(attend_join_kernel, dim3(p.a.batch * p.tiles_s * p.a.nkv), dim3(256), 0, c, p, c.nsm);
 }
 
 }  // namespace
