@@ -763,45 +763,47 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     for (; ok && next_segment(&g); seg_at.step()) {
       const int lead = g.split ? 2 : 1, x_h = g.h * (E4M3 ? 64 : 128);
       const int32_t* table = a.block_table + (size_t)g.s * a.max_pages;
-      // lane i < 8: pool row of 16-key group i of a tile
-      auto row_of = [&](int t) {
-        const int pos = g.first + t * kTile + 16 * lane;
+      // lane 8 t + i: pool row of 16-key group i of tile t0 + t
+      auto rows_of = [&](int t0) {
+        const int t = t0 + (lane >> 3), pos = g.first + t * kTile + 16 * (lane & 7);
         int row = absent;
-        if (lane < 8 && t < g.tiles && pos < g.end) {
+        if (t < g.tiles && pos < g.end) {
           const int page = table[pos >> p.page_shift];
           if (page >= 0 && page < a.n_pages) row = (page << p.page_shift) + (pos & (a.page_size - 1));
         }
         return row;
       };
-      auto load = [&](int row, const void* map) {
+      auto load = [&](int rows, int t, const void* map) {
         const int slot = at.slot;
         if (at.round > 0) ok = wait(empty + slot, (at.round - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         uint8_t* dst = sm + L::RING + slot * L::SLOT;
         if (lane == 0) mbar_arrive_expect_tx(full + slot, L::SLOT);
-        __syncwarp();
+        const int row = __shfl_sync(0xffffffffu, rows, (t & 3) * 8 + (lane & 7));
         if (E4M3) {
           if (lane < 8) tma_load_2d(dst + lane * 2048, map, full + slot, x_h, row, pol);
         } else {
-          const int r = __shfl_sync(0xffffffffu, row, lane & 7);
           if (lane < 16)
-            tma_load_2d(dst + (lane >> 3) * 16384 + (lane & 7) * 2048, map, full + slot, x_h + (lane >> 3) * 64, r, pol);
+            tma_load_2d(dst + (lane >> 3) * 16384 + (lane & 7) * 2048, map, full + slot, x_h + (lane >> 3) * 64, row, pol);
         }
         at.step();
       };
-      // rows of tiles t, t + 1, t + 2 and, on its way, t + 3
-      int r0 = row_of(0), r1 = row_of(1), r2 = row_of(2);
-      load(r0, &tm_k);
-      if (lead == 2 && g.tiles > 1 && ok) load(r1, &tm_k);
+      // keys' tiles are `lead` ahead of the values'; the rows of the next four
+      // tiles are looked up while these are loaded
+      int v_rows = rows_of(0), k_rows = v_rows, next = rows_of(4);
 #pragma unroll 1
-      for (int t = 0; t < g.tiles && ok; ++t) {
-        const int r3 = row_of(t + 3);
-        load(r0, &tm_v);
-        if (t + lead < g.tiles && ok) load(lead == 2 ? r2 : r1, &tm_k);
-        r0 = r1;
-        r1 = r2;
-        r2 = r3;
+      for (int t = -lead; t < g.tiles && ok; ++t) {
+        if (t > 0 && (t & 3) == 0) v_rows = k_rows;  // (the keys have moved on before, by lead < 4 tiles)
+        if (t >= 0) load(v_rows, t, &tm_v);
+        const int tk = t + lead;
+        if (tk < g.tiles && ok) {
+          if (tk > 0 && (tk & 3) == 0) {
+            k_rows = next;
+            next = rows_of(tk + 4);
+          }
+          load(k_rows, tk, &tm_k);
+        }
       }
     }
     // copies in flight land before the CTA ends
@@ -900,48 +902,52 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     Ring<NS> vat;  // slot of the next value tile
     Ring<kInfo> iat;
     bool ok = true;
+    int rows4 = -1;
+    uint32_t bytes[4][4];
     SegInfo g;
     for (; ok && next_segment(&g); seg_at.step()) {
       const int lead = g.split ? 2 : 1;
       const int32_t* table = a.block_table + (size_t)g.s * a.max_pages;
       for (int x = min(lead, g.tiles); x > 0; --x) vat.step();  // lead tiles of keys go first
-      // lane i < 8: pool row of 16-key group i, or -1
-      auto row_of = [&](int t) {
-        const int pos = g.first + t * kTile + 16 * lane;
+      // lane 8 t + i: pool row of 16-key group i of tile t0 + t, or -1
+      auto rows_of = [&](int t0) {
+        const int t = t0 + (lane >> 3), pos = g.first + t * kTile + 16 * (lane & 7);
         int row = -1;
-        if (lane < 8 && t < g.tiles && pos < g.end) {
+        if (t < g.tiles && pos < g.end) {
           const int page = table[pos >> p.page_shift];
           if (page >= 0 && page < a.n_pages) row = (page << p.page_shift) + (pos & (a.page_size - 1));
           else flag(a.status, DFLASH2_DEV_BAD_PAGE);
         }
         return row;
       };
-      // exponent bytes of keys 32 i + lane: keys' in the low halves, values' in the high ones
-      auto bytes_of = [&](int t, int row, uint32_t (&b)[4]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int key = 32 * i + lane, r = __shfl_sync(0xffffffffu, row, key >> 4);
-          b[i] = 0;
-          if (r >= 0 && g.first + t * kTile + key < g.end) {
-            const size_t x = ((size_t)r + (key & 15)) * a.nkv + g.h;
-            b[i] = a.k_exp[x] | ((uint32_t)a.v_exp[x] << 16);
-          }
-        }
-      };
-      // what a tile takes is asked for one (8 bits: and two) tiles before
-      int r0 = row_of(0), r1 = row_of(1);
-      uint32_t b0[4];
-      if (E4M3) bytes_of(0, r0, b0);
+      int next = rows_of(0);
+      // Four tiles at a time: all their exponent bytes are asked for together
+      // (keys' in the low halves, values' in the high ones; keys 32 i + lane).
 #pragma unroll 1
       for (int t = 0; t < g.tiles && ok; ++t) {
-        const int r2 = row_of(t + 2);
-        uint32_t b1[4];
-        if (E4M3) bytes_of(t + 1, r1, b1);
         const int slot = iat.slot, k0 = g.first + t * kTile;
+        if ((t & 3) == 0) {
+          rows4 = next;
+          next = rows_of(t + 4);
+          if (E4M3) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int key = 32 * i + lane, r = __shfl_sync(0xffffffffu, rows4, 8 * u + (key >> 4));
+                uint32_t b = 0;
+                if (r >= 0 && k0 + u * kTile + key < g.end) {
+                  const size_t x = ((size_t)r + (key & 15)) * a.nkv + g.h;
+                  b = a.k_exp[x] | ((uint32_t)a.v_exp[x] << 16);
+                }
+                bytes[u][i] = b;
+              }
+          }
+        }
         TileInfo* info;
         if (E4M3) info = reinterpret_cast<TileInfo*>(sm + L::INFO + slot * L::INFOS);
         else info = reinterpret_cast<TileInfo*>(sm + L::INFO + slot * L::INFOS - offsetof(TileInfo, bad));
-        const uint32_t groups = __ballot_sync(0xffffffffu, r0 >= 0);
+        const uint32_t groups = (__ballot_sync(0xffffffffu, rows4 >= 0) >> (8 * (t & 3))) & 0xffu;
         const bool mixed = k0 < g.all_lo || k0 + kTile > g.all_hi || groups != 0xffu;
         if (iat.round > 0) ok = wait(info_empty + slot, (iat.round - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
@@ -950,11 +956,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
           uint32_t top = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t kb = min(b0[i] & 0xffffu, 254u), vb = min(b0[i] >> 16, 254u);
+            const uint32_t x = (t & 2) ? ((t & 1) ? bytes[3][i] : bytes[2][i]) : ((t & 1) ? bytes[1][i] : bytes[0][i]);
+            const uint32_t kb = min(x & 0xffffu, 254u), vb = min(x >> 16, 254u);
             info->ks[32 * i + lane] = __uint_as_float(kb << 23);
             info->vs[32 * i + lane] = __uint_as_float(vb << 23);
             top = max(top, vb);
-            b0[i] = b1[i];
           }
           top = __reduce_max_sync(0xffffffffu, top);
           if (lane == 0) info->vmax = (float)max((int)top - 127, -60);
@@ -1014,8 +1020,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         iat.step();
         vat.step();
         if (t + lead < g.tiles) vat.step();  // the next key tile's
-        r0 = r1;
-        r1 = r2;
       }
     }
   } else {
@@ -1287,30 +1291,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         // accumulators' into shared memory (pieces of 16 bytes at piece ^
         // row % 8), then the sums over the copies, out.
         float4* box = reinterpret_cast<float4*>(sm + L::Q + g.q * 32768 + j * 16384);
+        const float f0 = sum == 0.f ? 0.f : w0 * fin, f1 = sum == 0.f ? 0.f : w1 * fin;
+        bar_softmax();  // everyone has read the references and sums
 #pragma unroll 1
         for (int part = 0; part < 2; ++part) {
           const int c = 2 * j + part;
-          float o[32];
           if (!idle) {
-            tmem_ld32(lanes + o_col(0) + 32 * c, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= w0;
-            if (both) {
-              float o1[32];
-              tmem_ld32(lanes + o_col(1) + 32 * c, o1);
+#pragma unroll 1
+            for (int i = 0; i < 8; i += 2) {  // (small pieces: code that runs once a segment is slow to fetch)
+              uint32_t o0[8], o1[8];
+              float o[8];
+              tmem_ld8_nowait(lanes + o_col(0) + 32 * c + 4 * i, o0);
+              if (both) tmem_ld8_nowait(lanes + o_col(1) + 32 * c + 4 * i, o1);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = fmaf(o1[i], w1, o[i]);
+              for (int b = 0; b < 8; ++b) {
+                o[b] = __uint_as_float(o0[b]) * f0;
+                if (both) o[b] = fmaf(__uint_as_float(o1[b]), f1, o[b]);
+                if (sum == 0.f) o[b] = 0.f;
+              }
+              box[r * 8 + (i ^ (r & 7))] = make_float4(o[0], o[1], o[2], o[3]);
+              box[r * 8 + ((i + 1) ^ (r & 7))] = make_float4(o[4], o[5], o[6], o[7]);
             }
-          }
-          if (part == 0) bar_softmax();  // everyone has read the references and sums,
-          else bar_stream(j);            // or the last part
-          if (!idle) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              box[r * 8 + (i ^ (r & 7))] = sum == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                                     : make_float4(o[4 * i] * fin, o[4 * i + 1] * fin, o[4 * i + 2] * fin, o[4 * i + 3] * fin);
           }
           bar_stream(j);
           for (int i = r; i < g.rows * 8; i += kTile) {
@@ -1335,6 +1337,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                                         (size_t)(g.h * p.group + lr - t * p.group) * kD + 32 * c + 4 * piece) = y;
             }
           }
+          bar_stream(j);  // (the box has been read)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(q_empty + g.q);
