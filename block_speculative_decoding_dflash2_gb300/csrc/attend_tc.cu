@@ -107,6 +107,7 @@ struct Plan {
   int tiles_s;         // row tiles of a sequence at most
   int slot_rows;       // rows of a sequence's partial slot
   int page_shift;      // page_size = 2^page_shift
+  int seg_cost;
   int* head;           // workspace: all positions, tiles of the shared part, first position of each row tile
   float *part_p, *part_s;    // partial accumulators [slot][rows][kD] of the shared part and of the sequences
   float2 *ref_p, *ref_s;     // (R, sum) of their rows
@@ -146,14 +147,14 @@ __device__ __forceinline__ Segment segment_of(const AttendArgs& a, int group, in
   return g;
 }
 // Cost of work in units of half a tile for up to 128 rows, near enough: a
-// tile for more of them, and a segment's start and end beside its tiles.
-constexpr int kSegCost = 10;
+// tile for more of them, and (seg_cost) a segment's start and end beside its
+// tiles: measured, about 7 with bfloat16 rows and 16 with 8-bit ones.
 __device__ __forceinline__ int weight_of(int rows) { return rows > kTile ? 4 : 2; }
-__device__ __forceinline__ int cost_of(int tiles, int w) { return tiles > 0 ? kSegCost + tiles * w : 0; }
+__device__ __forceinline__ int cost_of(int seg_cost, int tiles, int w) { return tiles > 0 ? seg_cost + tiles * w : 0; }
 // The tiles [x, y) of a segment at position `at` that the share [a, b) has:
-// tile k counts as lying at at + kSegCost + k w.
-__device__ __forceinline__ int2 tiles_in(int at, int tiles, int w, int a, int b) {
-  at += kSegCost;
+// tile k counts as lying at at + seg_cost + k w.
+__device__ __forceinline__ int2 tiles_in(int seg_cost, int at, int tiles, int w, int a, int b) {
+  at += seg_cost;
   return make_int2(at >= a ? 0 : (a - at + w - 1) / w, b <= at ? 0 : min(tiles, (b - at + w - 1) / w));
 }
 
@@ -189,14 +190,33 @@ struct Ring {
 };
 
 // A bounded wait that did not succeed at once.  Not inlined: the roles wait in
-// many places.
-__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
-  if (mbar_wait(bar, parity, abort_flag, kWaitNs)) return true;
-  if (!*abort_flag) {
-    *abort_flag = 1;
-    flag(status, DFLASH2_DEV_WAIT_TIMEOUT);
+// many places.  The hardware suspends the thread for some microseconds a
+// try (polling as fast as it goes took a third of all issued instructions,
+// from the schedulers of the softmax warps); the clock is read now and then.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, uint32_t abort_flag, unsigned* status) {
+  const uint64_t t0 = globaltimer();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+      uint32_t ok;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(bar), "r"(parity), "r"(20000u)
+          : "memory");
+      if (ok) return true;
+    }
+    uint32_t given_up;
+    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(given_up) : "r"(abort_flag) : "memory");
+    if (given_up) return false;
+    if (globaltimer() - t0 > kWaitNs) {
+      asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort_flag), "r"(1u) : "memory");
+      flag(status, DFLASH2_DEV_WAIT_TIMEOUT);
+      return false;
+    }
   }
-  return false;
 }
 
 // ------------------------------------------------------------------ PTX
@@ -454,19 +474,18 @@ __device__ __forceinline__ void load_rows(const Plan& p, const SegInfo& g, int r
       for (int i = 0; i < 8; ++i) top = max(max(top, w8[i] & 0x7f800000u), (w8[i] << 16) & 0x7f800000u);
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int e = top >= 0x7f800000u ? 254 : max(1, (int)(top >> 23));
-      // 2^(7 - (e - 127)) = 2^(134 - e), in two factors that are floats
-      const int ea = (134 - e) / 2, eb = (134 - e) - ea;
-      const float up0 = __uint_as_float((uint32_t)(127 + ea) << 23), up1 = __uint_as_float((uint32_t)(127 + eb) << 23);
+      // 2^(134 - e), e the largest magnitude's exponent field (rows below
+      // 2^-119 are not scaled up all the way, and keep their bits all the same)
+      const uint32_t e = max(8u, top >= 0x7f800000u ? 254u : top >> 23);
+      const float up = __uint_as_float((261u - e) << 23);
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float x0 = __uint_as_float(w8[i] << 16) * up0 * up1;
-        const float x1 = __uint_as_float(w8[i] & 0xffff0000u) * up0 * up1;
-        const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-        const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h2, __NV_E4M3);
-        const float2 back = __half22float2(__half2(hr));
-        const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(x0 - back.x, x1 - back.y), __NV_SATFINITE, __NV_E4M3);
+        // (eight bits: an f16 holds the scaled value, and what the high code leaves of it, exactly)
+        const __half2 x = __floats2half2_rn(__uint_as_float(w8[i] << 16) * up, __uint_as_float(w8[i] & 0xffff0000u) * up);
+        const uint32_t h2 = __nv_cvt_halfraw2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+        const __half2 back(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h2, __NV_E4M3));
+        const uint32_t l2 = __nv_cvt_halfraw2_to_fp8x2(__hsub2(x, back), __NV_SATFINITE, __NV_E4M3);
         hi[i >> 1] = (i & 1) ? hi[i >> 1] | (h2 << 16) : h2;
         lo[i >> 1] = (i & 1) ? lo[i >> 1] | (l2 << 16) : l2;
       }
@@ -478,9 +497,7 @@ __device__ __forceinline__ void load_rows(const Plan& p, const SegInfo& g, int r
         }
         // a row that is not finite has no result
         if (c == 0)
-          qscale[fr] = top >= 0x7f800000u ? __int_as_float(0x7fffffff)
-                                          : __uint_as_float((uint32_t)(127 - ea) << 23) *
-                                                __uint_as_float((uint32_t)(127 - eb) << 23);
+          qscale[fr] = top >= 0x7f800000u ? __int_as_float(0x7fffffff) : __uint_as_float((e - 7u) << 23);
       }
     }
   }
@@ -495,7 +512,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
   using L = Smem<E4M3>;
   constexpr int NS = L::SLOTS;
   extern __shared__ uint8_t raw_smem[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
+  // (an offset, not a cast address: the compiler keeps to shared-memory accesses)
+  uint8_t* sm = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BAR);
   uint64_t* full = bars;              // [NS] a K or V tile landed
   uint64_t* empty = full + NS;        // [NS] its products are done
@@ -511,7 +529,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
   uint64_t* q_full = q_ready + 1;           // [2] query rows that warp 11 loaded into a place
   uint64_t* drain = q_full + 2;             // every product issued is done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* abort_flag = tmem_slot + 1;
+  const uint32_t abort_at = smem_u32(abort_flag);
   SegInfo* segs = reinterpret_cast<SegInfo*>(sm + L::SEG);
   __shared__ int scan[kThreads / 32], ends[kThreads / 32][2], start[3];
 
@@ -557,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     const int s = p.tiles_s == 1 ? e : e / p.tiles_s;
     *nl = lengths(a, s);
     const Segment g = segment_of(a, p.group, *nl, p.tiles_s == 1 ? 0 : e % p.tiles_s);
-    return cost_of(g.tiles, weight_of(g.rows)) * a.nkv;
+    return cost_of(p.seg_cost, g.tiles, weight_of(g.rows)) * a.nkv;
   };
   int my_units = 0, lo = INT32_MAX, hi = 0;
   for (int e = e0; e < e1; ++e) {
@@ -599,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
   hi = min(hi, a.shared_len);
   const int base_p = lo & ~15, end_p = hi;
   const int tiles_p = p.tiles_p > 0 && hi > lo ? (hi - base_p + kTile - 1) / kTile : 0;
-  const int cost_p = cost_of(tiles_p, weight_of(kRowTile));  // (its last row tile may be cheaper: no matter)
+  const int cost_p = cost_of(p.seg_cost, tiles_p, weight_of(kRowTile));  // (its last row tile may be cheaper: no matter)
   const int up = p.tiles_p * a.nkv * cost_p, units = up + total;
   const int share_a = bound_of(units, cta, nctas), share_b = bound_of(units, cta + 1, nctas);
   if (cta == 0) {  // for the joining kernel
@@ -636,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
   __syncthreads();
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return mbar_try_wait(smem_u32(bar), parity) || wait_on(bar, parity, abort_flag, a.status);
+    return mbar_try_wait(smem_u32(bar), parity) || wait_on(smem_u32(bar), parity, abort_at, a.status);
   };
   // The next segment (tiles = 0: none, or the kernel is giving up).
   Ring<kSegs> seg_at;
@@ -709,9 +728,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
       g.shared = shared;
       g.split = g.rows <= kTile;
       g.copies = g.rows <= 32 ? 4 : g.rows <= 64 ? 2 : 1;
-      for (int h = 0; h < a.nkv && ok; ++h, at += cost_of(tiles, w)) {
+      for (int h = 0; h < a.nkv && ok; ++h, at += cost_of(p.seg_cost, tiles, w)) {
         if (tiles == 0 || at >= share_b) break;
-        const int2 k = tiles_in(at, tiles, w, share_a, share_b);
+        const int2 k = tiles_in(p.seg_cost, at, tiles, w, share_a, share_b);
         if (k.x >= k.y) continue;
         g.h = h;
         g.first = base + k.x * kTile;
@@ -1374,7 +1393,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   const int rows = min(kRowTile, nl.x * p.group - i * kRowTile);
   if (rows <= 0) return;
   const int w = weight_of(g.rows), wp = weight_of(kRowTile), f0 = s * p.rows + i * kRowTile;
-  const int at = start + h * cost_of(g.tiles, w), ip = f0 / kRowTile, cost_p = cost_of(tiles_p, wp);
+  const int at = start + h * cost_of(p.seg_cost, g.tiles, w), ip = f0 / kRowTile, cost_p = cost_of(p.seg_cost, tiles_p, wp);
   // (a block looks at one CTA per thread)
   uint32_t mine = 0;
   {
@@ -1383,13 +1402,13 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     if (c < nctas) {
       const int lo = bound_of(units, c, nctas), hi = bound_of(units, c + 1, nctas);
       if (g.tiles > 0) {
-        const int2 k = tiles_in(at, g.tiles, w, lo, hi);
+        const int2 k = tiles_in(p.seg_cost, at, g.tiles, w, lo, hi);
         own = k.x < k.y && (p.tiles_p > 0 || k.x > 0 || k.y < g.tiles);
       }
       if (tiles_p > 0) {
-        int2 k = tiles_in((ip * a.nkv + h) * cost_p, tiles_p, wp, lo, hi);
+        int2 k = tiles_in(p.seg_cost, (ip * a.nkv + h) * cost_p, tiles_p, wp, lo, hi);
         p0 = k.x < k.y;
-        k = tiles_in(((ip + 1) * a.nkv + h) * cost_p, tiles_p, wp, lo, hi);
+        k = tiles_in(p.seg_cost, ((ip + 1) * a.nkv + h) * cost_p, tiles_p, wp, lo, hi);
         p1 = k.x < k.y;
       }
     }
@@ -1522,7 +1541,7 @@ bool attend_tc_fits(const AttendArgs& a) {
   Sizes z;
   if (!sizes_of(a.batch, a.n_tok, a.nq, a.nkv, a.shared_len, kMaxCtas, &z)) return false;
   const long long each = ((long long)a.max_pages * a.page_size + 15) / kTile + 2;
-  return ((long long)a.batch * z.tiles_s + z.tiles_p) * a.nkv * (each * 4 + 16) < (1ll << 31);
+  return ((long long)a.batch * z.tiles_s + z.tiles_p) * a.nkv * (each * 4 + 32) < (1ll << 31);
 }
 
 size_t attend_tc_workspace(int batch, int n_tok, int nq, int nkv, int shared_len) {
@@ -1541,6 +1560,7 @@ int launch_attend_tc(const AttendArgs& a, void* workspace, const Ctx& c) {
   p.tiles_p = z.tiles_p;
   p.tiles_s = z.tiles_s;
   p.slot_rows = z.slot_rows;
+  p.seg_cost = a.e4m3 ? 16 : 7;
   while ((1 << p.page_shift) < a.page_size) ++p.page_shift;
   p.head = reinterpret_cast<int*>(ws + z.head);
   p.part_p = reinterpret_cast<float*>(ws + z.part_p);
