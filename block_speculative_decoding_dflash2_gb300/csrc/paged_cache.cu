@@ -11,10 +11,10 @@
 // scaling itself is exact too, so the only rounding is the code's.
 //
 // Both directions are copies: what bounds them is memory, and for a few rows
-// the latency of the chain offsets -> block table -> row.  A thread holds 8
-// values (one 16-byte access of bf16), the d / 8 threads of a head form its
-// maximum by shuffles, and a block takes `rpb` rows, whose destinations its
-// threads find together while the values are on their way.
+// the latency of the chain offsets -> block table -> row.  A warp takes a row,
+// its keys and its values, 16 bytes of bfloat16 a lane and step; it finds the
+// row's place by itself (32 offsets a look), so no warp waits for another,
+// and the values to write are asked for before that.
 #include <algorithm>
 
 #include "common.cuh"
@@ -24,68 +24,85 @@ namespace df2 {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxRows = 16;  // rows of a block at most
+constexpr int kWarps = 8;
+constexpr int kAhead = 8;  // pieces of 16 bytes that a lane has in flight
 
-// Row of the pool (pages laid end to end) of each of the block's rows, or -1.
-__device__ __forceinline__ void find_rows(const CacheRowsArgs& a, int r0, int n, long long* place) {
-  for (int i = threadIdx.x; i < n; i += blockDim.x) place[i] = -1;
-  __syncthreads();
-  // every thread looks at some of the sequences for all rows of the block:
-  // one trip to memory, where a search would take several
-  for (int s = threadIdx.x; s < a.batch; s += blockDim.x) {
-    const int lo = a.off[s], hi = a.off[s + 1];
-    if (hi <= r0 || lo >= r0 + n) continue;
-    const long long first = a.start ? a.start[s] : 0;
-    for (int r = max(lo, r0); r < min(hi, r0 + n); ++r) {
-      const long long p = first + (r - lo);
+// Row of the pool (pages laid end to end) of row r, or -1; *past: behind the
+// last sequence.  All lanes of a warp, the same r.
+__device__ __forceinline__ long long place_of(const CacheRowsArgs& a, int r, bool* past) {
+  const int lane = threadIdx.x & 31;
+  // the last sequence whose offset is not above r
+  int lo = 0, n = a.batch;
+  *past = false;
+  while (true) {
+    const int step = (n + 31) / 32, i = lo + lane * step;
+    const int o = i < lo + n ? a.off[i] : INT32_MAX, end = n <= 32 ? (i < lo + n ? a.off[i + 1] : 0) : 0;
+    const uint32_t below = __ballot_sync(0xffffffffu, i < lo + n && o <= r);
+    if (!below) return -1;  // (offsets that do not start at 0)
+    const int k = 31 - __clz(below);
+    if (step == 1) {
+      const int s = lo + k, first = __shfl_sync(0xffffffffu, o, k);
+      if (r >= __shfl_sync(0xffffffffu, end, k)) {
+        *past = true;
+        return -1;
+      }
+      const long long p = (a.start ? a.start[s] : 0) + (long long)(r - first);
       if (p < 0 || p >= (long long)a.max_pages * a.page_size) {
-        flag(a.status, DFLASH2_DEV_BAD_LENGTH);
-        continue;
+        if (lane == 0) flag(a.status, DFLASH2_DEV_BAD_LENGTH);
+        return -1;
       }
-      const int page = a.block_table[(size_t)s * a.max_pages + p / a.page_size];
+      const int pi = (int)p / a.page_size, page = a.block_table[(size_t)s * a.max_pages + pi];
       if (page < 0 || page >= a.n_pages) {
-        flag(a.status, DFLASH2_DEV_BAD_PAGE);
-        continue;
+        if (lane == 0) flag(a.status, DFLASH2_DEV_BAD_PAGE);
+        return -1;
       }
-      place[r - r0] = (long long)page * a.page_size + p % a.page_size;
+      return (long long)page * a.page_size + ((int)p - pi * a.page_size);
     }
+    lo += k * step;
+    n = min(step, n - k * step);
   }
-  __syncthreads();
 }
 
-// 8 bf16 values -> 8 codes and the row's exponent byte; the threads of a row
-// are `width` (8 or 16) neighbouring lanes.
+// 8 bf16 values -> 8 codes and the row's exponent byte; the lanes of a head
+// are `width` (8 or 16) neighbours.
 __device__ __forceinline__ uint2 quantise8(const uint4& raw, int width, int* byte) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  float x[8];
-  uint32_t top = 0;  // bits of the largest finite magnitude
+  uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  // the largest magnitude (NaN is passed over)
+  __nv_bfloat162 m[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    const uint32_t x = w[i] & 0x7fff7fffu;
+    m[i] = *reinterpret_cast<const __nv_bfloat162*>(&x);
   }
+  m[0] = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
+  for (int o = width >> 1; o > 0; o >>= 1) {
+    const uint32_t x = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&m[0]), o);
+    m[0] = __hmax2(m[0], *reinterpret_cast<const __nv_bfloat162*>(&x));
+  }
+  uint32_t top = __float_as_uint(fmaxf(__low2float(m[0]), __high2float(m[0])));
+  if (__any_sync(0xffffffffu, !(top < 0x7f800000u))) {
+    // infinities or NaN alone: the largest finite magnitude, and NaN for the infinities, which e4m3 has not
+    top = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t m = __float_as_uint(x[i]) & 0x7fffffffu;
-    if (m >= 0x7f800000u) x[i] = __int_as_float(0x7fffffff);  // infinities become NaN, which e4m3 has
-    else top = max(top, m);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = (w[i] << 16) & 0x7fffffffu, hi = w[i] & 0x7fff0000u;
+      if (lo >= 0x7f800000u) w[i] |= 0x7fffu;
+      else top = max(top, lo);
+      if (hi >= 0x7f800000u) w[i] |= 0x7fff0000u;
+      else top = max(top, hi);
+    }
+    for (int o = width >> 1; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
   }
-  for (int o = width >> 1; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
   // top = 1.m * 2^(e - 127) against 448 = 1.75 * 2^8
   const int b = max(1, (int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0));
   *byte = b;
   const float inv = __uint_as_float((uint32_t)(254 - b) << 23);  // 2^(127 - b)
-  uint32_t c[2];
+  uint32_t c[4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * h] * inv, x[4 * h + 1] * inv), __NV_SATFINITE,
-                                                 __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * h + 2] * inv, x[4 * h + 3] * inv),
-                                                 __NV_SATFINITE, __NV_E4M3);
-    c[h] = lo | (hi << 16);
-  }
-  return make_uint2(c[0], c[1]);
+  for (int i = 0; i < 4; ++i)
+    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xffff0000u) * inv),
+                                    __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
 __device__ __forceinline__ uint4 widen8(const uint2& c, int byte) {
@@ -103,79 +120,77 @@ __device__ __forceinline__ uint4 widen8(const uint2& c, int byte) {
 }
 
 template <bool READ, bool E4M3>
-__global__ void __launch_bounds__(kThreads) cache_rows_kernel(CacheRowsArgs a, int rpb) {
-  __shared__ long long place[kMaxRows];
+__global__ void __launch_bounds__(32 * kWarps) cache_rows_kernel(const __grid_constant__ CacheRowsArgs a) {
   pdl_launch_next();
   pdl_wait();
-  const int r0 = blockIdx.x * rpb, n = min(rpb, a.rows - r0);
-  const int vec = a.nkv * a.d / 8;  // 16-byte pieces of a row of keys or values
-  const int items = n * vec * 2;
-  const int width = a.d / 8;
-  if (READ) {
-    find_rows(a, r0, n, place);
-    const int covered = a.off[a.batch];  // rows behind the last sequence are left as they are
-    for (int i0 = 0; i0 < items; i0 += kThreads) {
-      const int i = i0 + threadIdx.x;
-      if (i >= items) break;
-      const int part = i / (n * vec), j = i % (n * vec), r = j / vec, c = j % vec;
-      if (r0 + r >= covered) continue;
-      const long long p = place[r];
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      const void* pool = part ? a.v : a.k;
-      if (p >= 0) {
-        const size_t at = (size_t)p * vec + c;
-        if (E4M3) {
-          const int head = c / width;
-          v = widen8(static_cast<const uint2*>(pool)[at], (part ? a.v_exp : a.k_exp)[(size_t)p * a.nkv + head]);
-        } else {
-          v = static_cast<const uint4*>(pool)[at];
-        }
-      }
-      bf16* out = static_cast<bf16*>(part ? a.v_rows : a.k_rows);
-      reinterpret_cast<uint4*>(out + (size_t)(r0 + r) * (part ? a.v_stride : a.k_stride))[c] = v;
-    }
-    return;
-  }
-  // the values do not depend on where they go: they are asked for first
-  constexpr int kAhead = 8;
+  const int lane = threadIdx.x & 31, r = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (r >= a.rows) return;
+  const int width = a.d / 8, lg_width = width == 16 ? 4 : 3;  // pieces of a head
+  const int vec = a.nkv << lg_width;                          // pieces of a row of keys or values
+  uint4* rows[2] = {reinterpret_cast<uint4*>(static_cast<bf16*>(a.k_rows) + (size_t)r * a.k_stride),
+                    reinterpret_cast<uint4*>(static_cast<bf16*>(a.v_rows) + (size_t)r * a.v_stride)};
+  // pieces 0 .. vec - 1 are the keys', vec .. 2 vec - 1 the values'
   uint4 x[kAhead];
-  const int rounds = (items + kThreads - 1) / kThreads;
-#pragma unroll
-  for (int u = 0; u < kAhead; ++u) {
-    const int i = u * kThreads + threadIdx.x;
-    if (i < items) {
-      const int part = i / (n * vec), j = i % (n * vec), r = j / vec, c = j % vec;
-      const bf16* in = static_cast<const bf16*>(part ? a.v_rows : a.k_rows);
-      x[u] = reinterpret_cast<const uint4*>(in + (size_t)(r0 + r) * (part ? a.v_stride : a.k_stride))[c];
-    }
-  }
-  find_rows(a, r0, n, place);
-  for (int u0 = 0; u0 < rounds; u0 += kAhead) {
+  if (!READ) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int i = (u0 + u) * kThreads + threadIdx.x;
-      const bool in_range = i < items;
-      if (!__any_sync(0xffffffffu, in_range)) break;
-      const int part = in_range ? i / (n * vec) : 0, j = in_range ? i % (n * vec) : 0, r = j / vec, c = j % vec;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (in_range) {
-        if (u0 == 0) {
-          v = x[u];
-        } else {
-          const bf16* in = static_cast<const bf16*>(part ? a.v_rows : a.k_rows);
-          v = reinterpret_cast<const uint4*>(in + (size_t)(r0 + r) * (part ? a.v_stride : a.k_stride))[c];
+      const int q = 32 * u + lane;
+      x[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (q < 2 * vec) x[u] = __ldcs(q < vec ? rows[0] + q : rows[1] + (q - vec));
+    }
+  }
+  bool past;
+  const long long place = place_of(a, r, &past);
+  if (READ ? past : place < 0) return;  // rows behind the last sequence are left as they are
+  const size_t at = (size_t)max(place, 0ll) * vec;
+  for (int q0 = 0; q0 < 2 * vec; q0 += 32 * kAhead) {
+    if (READ) {
+      int byte[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int q = q0 + 32 * u + lane;
+        x[u] = make_uint4(0u, 0u, 0u, 0u);
+        byte[u] = 0;
+        if (q < 2 * vec && place >= 0) {
+          const bool v = q >= vec;
+          const int c = v ? q - vec : q;
+          if (E4M3) {
+            const uint2 y = __ldcs(static_cast<const uint2*>(v ? a.v : a.k) + at + c);
+            x[u].x = y.x;
+            x[u].y = y.y;
+            byte[u] = (v ? a.v_exp : a.k_exp)[(size_t)place * a.nkv + (c >> lg_width)];
+          } else {
+            x[u] = __ldcs(static_cast<const uint4*>(v ? a.v : a.k) + at + c);
+          }
         }
       }
-      const long long p = in_range ? place[r] : -1;
-      if (E4M3) {
-        int byte;
-        const uint2 q = quantise8(v, width, &byte);  // (whole warps: it shuffles)
-        if (p >= 0) {
-          static_cast<uint2*>(part ? a.v : a.k)[(size_t)p * vec + c] = q;
-          if (c % width == 0) (part ? a.v_exp : a.k_exp)[(size_t)p * a.nkv + c / width] = (uint8_t)byte;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int q = q0 + 32 * u + lane;
+        if (q < 2 * vec)
+          *(q < vec ? rows[0] + q : rows[1] + (q - vec)) = E4M3 ? widen8(make_uint2(x[u].x, x[u].y), byte[u]) : x[u];
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int q = q0 + 32 * u + lane;
+        if (q0 + 32 * u >= 2 * vec) break;  // (the whole warp)
+        if (q0 > 0) {
+          x[u] = make_uint4(0u, 0u, 0u, 0u);
+          if (q < 2 * vec) x[u] = __ldcs(q < vec ? rows[0] + q : rows[1] + (q - vec));
         }
-      } else if (p >= 0) {
-        static_cast<uint4*>(part ? a.v : a.k)[(size_t)p * vec + c] = v;
+        const bool v = q >= vec;
+        const int c = v ? q - vec : q;
+        if (E4M3) {
+          int byte;
+          const uint2 y = quantise8(x[u], width, &byte);  // (whole warps: it shuffles)
+          if (q < 2 * vec) {
+            static_cast<uint2*>(v ? a.v : a.k)[at + c] = y;
+            if ((c & (width - 1)) == 0) (v ? a.v_exp : a.k_exp)[(size_t)place * a.nkv + (c >> lg_width)] = (uint8_t)byte;
+          }
+        } else if (q < 2 * vec) {
+          static_cast<uint4*>(v ? a.v : a.k)[at + c] = x[u];
+        }
       }
     }
   }
@@ -184,17 +199,12 @@ __global__ void __launch_bounds__(kThreads) cache_rows_kernel(CacheRowsArgs a, i
 }  // namespace
 
 int launch_cache_rows(const CacheRowsArgs& a, bool read, const Ctx& c) {
-  // rows of a block: enough that a thread has several accesses in flight,
-  // few enough that the blocks cover the SMs
-  const int vec = a.nkv * a.d / 8 * 2;
-  int rpb = std::max(1, std::min(kMaxRows, 8 * kThreads / vec));
-  while (rpb > 1 && (a.rows + rpb - 1) / rpb < 2 * c.nsm) --rpb;
-  const dim3 grid((a.rows + rpb - 1) / rpb);
+  const dim3 grid((a.rows + kWarps - 1) / kWarps), block(32 * kWarps);
   if (read)
-    return a.e4m3 ? launch_k(cache_rows_kernel<true, true>, grid, dim3(kThreads), 0, c, a, rpb)
-                  : launch_k(cache_rows_kernel<true, false>, grid, dim3(kThreads), 0, c, a, rpb);
-  return a.e4m3 ? launch_k(cache_rows_kernel<false, true>, grid, dim3(kThreads), 0, c, a, rpb)
-                : launch_k(cache_rows_kernel<false, false>, grid, dim3(kThreads), 0, c, a, rpb);
+    return a.e4m3 ? launch_k(cache_rows_kernel<true, true>, grid, block, 0, c, a)
+                  : launch_k(cache_rows_kernel<true, false>, grid, block, 0, c, a);
+  return a.e4m3 ? launch_k(cache_rows_kernel<false, true>, grid, block, 0, c, a)
+                : launch_k(cache_rows_kernel<false, false>, grid, block, 0, c, a);
 }
 
 }  // namespace df2
