@@ -509,12 +509,18 @@ class PagedCache:
         self.tensors = (k, v, k_exp, v_exp)
         self.heads, self.width = k.shape[2:]
         self.struct = Cache(code, *k.shape, _ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp))
+        self.ref = ctypes.byref(self.struct)
 
     def at(self, fn):
         """The struct's reference, on the current device only."""
-        if self.device != torch.cuda.current_device():
+        if self.device != torch._C._cuda_getDevice():
             raise DFlash2Error(fn, -1, "the cache must be on the current device")
-        return ctypes.byref(self.struct)
+        return self.ref
+
+
+def _stream_on(stream, dev):
+    """_stream() where the current device is known."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _tokens_of(fn, name, t, dev, shape):
@@ -554,7 +560,7 @@ def dflash2_cache_append(cache, block_table, ctx_len, k, v, new_off, workspace=N
     return _check(fn, lib().dflash2_cache_append(
         ref, table, max_pages, batch, _at(fn, "ctx_len", ctx_len, dev, torch.int32, (batch,)), n, kp, ks, vp, vs,
         _at(fn, "new_off", new_off, dev, torch.int32, (batch + 1,)), _workspace(fn, workspace, dev, STATUS_BYTES),
-        _stream(stream)))
+        _stream_on(stream, dev)))
 
 
 def dflash2_cache_read(cache, block_table, start, off, k, v, workspace=None, stream=None):
@@ -569,11 +575,11 @@ def dflash2_cache_read(cache, block_table, start, off, k, v, workspace=None, str
     return _check(fn, lib().dflash2_cache_read(
         ref, table, max_pages, batch, None if start is None else _at(fn, "start", start, dev, torch.int32, (batch,)), n,
         _at(fn, "off", off, dev, torch.int32, (batch + 1,)), kp, ks, vp, vs,
-        _workspace(fn, workspace, dev, STATUS_BYTES), _stream(stream)))
+        _workspace(fn, workspace, dev, STATUS_BYTES), _stream_on(stream, dev)))
 
 
 def dflash2_attend_workspace(cache, batch, n_tok, n_q_heads, shared_len=0):
-    return lib().dflash2_attend_workspace(ctypes.byref(cache.struct), batch, n_tok, n_q_heads, shared_len)
+    return lib().dflash2_attend_workspace(cache.ref, batch, n_tok, n_q_heads, shared_len)
 
 
 def dflash2_attend(cache, block_table, kv_len, q, out, workspace, n_new=None, scale=None, causal=True, window=0,
@@ -594,7 +600,7 @@ def dflash2_attend(cache, block_table, kv_len, q, out, workspace, n_new=None, sc
         None if n_new is None else _at(fn, "n_new", n_new, dev, torch.int32, (batch,)),
         _at(fn, "kv_len", kv_len, dev, torch.int32, (batch,)), q.shape[2], qp, qs, op, os_,
         cache.width ** -0.5 if scale is None else scale, int(causal), window, shared_len,
-        _workspace(fn, workspace, dev), workspace.numel() * workspace.element_size(), _stream(stream)))
+        _workspace(fn, workspace, dev), workspace.numel() * workspace.element_size(), _stream_on(stream, dev)))
 
 
 def dflash2_adjust_logits(logits, tokens, n_tokens, out, prompt_len=None, path=None, repetition=None, presence=None,
@@ -621,7 +627,7 @@ def dflash2_adjust_logits(logits, tokens, n_tokens, out, prompt_len=None, path=N
         opt("presence", presence, f32, one), opt("frequency", frequency, f32, one),
         opt("bias_id", bias_id, i32, (batch, n_bias)), opt("bias", bias, f32, (batch, n_bias)), n_bias,
         opt("mask", mask, i32, (batch, rows, -(-vocab // 32))), out.data_ptr(), out_stride,
-        _workspace(fn, workspace, dev, STATUS_BYTES), _stream(stream)))
+        _workspace(fn, workspace, dev, STATUS_BYTES), _stream_on(stream, dev)))
 
 
 def dflash2_verify_accept_ex(batch, block_size, path, n_draft, target, accept_len, out_tok, n_out, next_anchor,

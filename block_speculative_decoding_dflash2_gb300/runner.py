@@ -97,5 +97,12 @@ class DraftRunner:
                                 self.accept_len, self.out_tok, self.n_out, self.next_anchor, self.verify_ws, seq_len,
                                 self.counters, stream)
 
+    def adjust_logits(self, logits, tokens, n_tokens, out=None, prompt_len=None, repetition=None, presence=None,
+                      frequency=None, bias_id=None, bias=None, mask=None, stream=None):
+        """Applies the requests' penalties, biases and grammar masks to the target's logits [batch, block_size,
+        vocab] of the selected path, in place or into out, for verify_logits (its status word is verify_ws's)."""
+        B.dflash2_adjust_logits(logits, tokens, n_tokens, logits if out is None else out, prompt_len, self.path,
+                                repetition, presence, frequency, bias_id, bias, mask, self.verify_ws, stream)
+
     def device_status(self, stream=None):
         return B.dflash2_read_device_status(self.workspace, stream)
