@@ -528,6 +528,8 @@ def _tokens_of(fn, name, t, dev, shape):
     tensor whose tokens are evenly spaced and contiguous in themselves."""
     if t is None or t.get_device() != dev or t.dtype is not torch.bfloat16 or t.shape != shape:
         _refuse(fn, name, t, dev, torch.bfloat16, shape)
+    if t.is_contiguous():
+        return t.data_ptr(), shape[-1] * shape[-2]
     st, n = t.stride(), len(shape)
     if t.numel() and ((st[-1] != 1 and shape[-1] > 1) or (st[-2] != shape[-1] and shape[-2] > 1)):
         raise DFlash2Error(fn, -2, f"a token of {name} must be contiguous")
@@ -543,9 +545,11 @@ def _tokens_of(fn, name, t, dev, shape):
 
 def _table(fn, t, dev):
     """(address, max_pages, batch) of a block table."""
-    if t is None or t.dim() != 2:
+    if (t is None or t.get_device() != dev or t.dtype is not torch.int32 or t.dim() != 2
+            or not t.is_contiguous()):
         _refuse(fn, "block_table", t, dev, torch.int32, ("batch", "max_pages"))
-    return _at(fn, "block_table", t, dev, torch.int32, t.shape), t.shape[1], t.shape[0]
+    batch, max_pages = t.shape
+    return t.data_ptr(), max_pages, batch
 
 
 def dflash2_cache_append(cache, block_table, ctx_len, k, v, new_off, workspace=None, stream=None):
