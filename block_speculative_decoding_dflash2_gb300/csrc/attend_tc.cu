@@ -72,7 +72,7 @@ struct TileInfo {
 };
 
 // A segment's share of this CTA, as its roles need it.
-struct SegInfo {
+struct alignas(16) SegInfo {
   int tiles;            // 0: no more segments
   int first, end;       // position of its first tile; keys end before `end`
   int all_lo, all_hi;   // keys that every row sees
@@ -82,6 +82,7 @@ struct SegInfo {
   int split;            // both streams take the same rows
   int copies;           // of the rows in the 128 of a stream (1, 2 or 4)
   int q;                // place of the query rows (split)
+  int own_q;            // the softmax warps load the query rows: of many rows, and of the first segment
   int slot;             // place of the partial result, -1: the CTA finishes the segment
 };
 
@@ -740,6 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         if (seg_at.round > 0) ok = wait(seg_empty + seg_at.slot, (seg_at.round - 1) & 1) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        g.own_q = !g.split || (seg_at.slot == 0 && seg_at.round == 0);
         if (lane == 0) segs[seg_at.slot] = g;
         __syncwarp();
         if (lane == 0) mbar_arrive(seg_full + seg_at.slot);  // (its keys and values may be on their way before its rows)
@@ -750,8 +752,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (g.split) {
-          q_next ^= 1;
+        if (g.split) q_next ^= 1;
+        if (!g.own_q) {
           load_rows<E4M3>(p, g, 0, g.rows, sm + L::Q + g.q * 32768,
                           reinterpret_cast<float*>(sm + L::QSCALE) + seg_at.slot * kRowTile);
           fence_proxy_async_smem();
@@ -852,12 +854,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
       for (; ok; seg_at.step()) {
         if (!wait(seg_full + seg_at.slot, seg_at.round & 1)) break;
         const SegInfo& g = segs[seg_at.slot];
-        const int nt = g.tiles, lead = g.split ? 2 : 1, g_q = g.q;
+        const int nt = g.tiles, lead = g.split ? 2 : 1, g_q = g.q, g_own = g.own_q;
         const uint32_t q0 = qs + g_q * 2048;
         mbar_arrive(seg_empty + seg_at.slot);
         if (nt == 0) break;
-        uint64_t* rows_there = lead == 1 ? q_ready : q_full + g_q;
-        const uint32_t bit = lead == 1 ? 4u : 1u << g_q;
+        uint64_t* rows_there = g_own ? q_ready : q_full + g_q;
+        const uint32_t bit = g_own ? 4u : 1u << g_q;
         if (!wait(rows_there, (n_q & bit) ? 1 : 0)) break;
         n_q ^= bit;
         // Work u: stream u % 2's products with a tile's values, and then its
@@ -1063,12 +1065,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
       const int f = g.f0 + (mine ? fr : 0);
       const int s = g.shared ? f / p.rows : g.s, local = f - s * p.rows, t_row = local / p.group;
       const int head = g.h * p.group + local - t_row * p.group;
-      if (!split) {
-        // (many rows are a long segment: no warp has to load them ahead)
-        const int w0 = warp * 32;
-        // (both places are free: this warp has been through its last segment, and so has every other, by the vote)
-        if (w0 < g.rows)
-          load_rows<E4M3>(p, g, w0, min(w0 + 32, g.rows), sm + L::Q + j * 32768,
+      if (g.own_q) {
+        // (many rows are a long segment, and the first segment has nothing to
+        // hide the loads behind; the places are free: this warp has been through
+        // its last segment, and so has every other, by the vote)
+        const int w0 = split ? warp * 16 : warp * 32, w1 = min(w0 + (split ? 16 : 32), g.rows);
+        if (w0 < w1)
+          load_rows<E4M3>(p, g, w0, w1, sm + L::Q + (split ? g.q : j) * 32768,
                           reinterpret_cast<float*>(sm + L::QSCALE) + seg_at.slot * kRowTile);
         fence_proxy_async_smem();
         __syncwarp();
@@ -1085,10 +1088,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         else see.x = max(see.x, a.shared_len);
       }
       if (E4M3) {
-        if (split) {
-          wait(q_full + g.q, (n_q >> g.q) & 1);
-          n_q ^= 1u << g.q;
-        }
+        const int bit = g.own_q ? 2 : g.q;  // (the rows' scales are other warps' work)
+        wait(g.own_q ? q_ready : q_full + g.q, (n_q >> bit) & 1);
+        n_q ^= 1u << bit;
         if (mine) rs *= reinterpret_cast<const float*>(sm + L::QSCALE)[seg_at.slot * kRowTile + fr];
       }
       if (E4M3) {
