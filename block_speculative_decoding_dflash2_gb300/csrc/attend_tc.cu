@@ -1377,10 +1377,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
 
 // ------------------------------------------------------------------ joining kernel
 
-// A block per segment of the sequences: the partial accumulators of its rows,
+// A block per 32 rows of a segment of the sequences: the partial accumulators,
 // weighted to a common reference.  Segments that one CTA finished are there
 // already.  The CTAs that have parts of it are found by all threads at once,
 // and a warp takes four rows at a time, so that their loads overlap.
+constexpr int kJoinRows = 32;
+
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ Plan p, int nctas) {
   __shared__ uint32_t has[3][(kMaxCtas + 31) / 32];  // CTAs with parts: the sequence's, and of two row tiles of the shared part
   pdl_launch_next();
@@ -1393,7 +1395,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   const int units = p.head[0], tiles_p = p.head[1], start = p.head[2 + entry];
   const Segment g = segment_of(a, p.group, nl, i);
   const int rows = min(kRowTile, nl.x * p.group - i * kRowTile);
-  if (rows <= 0) return;
+  if ((int)blockIdx.y * kJoinRows >= rows) return;
   const int w = weight_of(g.rows), wp = weight_of(kRowTile), f0 = s * p.rows + i * kRowTile;
   const int at = start + h * cost_of(p.seg_cost, g.tiles, w), ip = f0 / kRowTile, cost_p = cost_of(p.seg_cost, tiles_p, wp);
   // (a block looks at one CTA per thread)
@@ -1425,8 +1427,9 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   }
   const bool any = __syncthreads_or(mine);
   if (!any && g.tiles > 0 && p.tiles_p == 0) return;  // one CTA has written it (without tiles nobody has: zeros)
-  constexpr int RW = 4;
-  for (int r0 = warp; r0 < rows; r0 += 8 * RW) {
+  constexpr int RW = kJoinRows / 8;
+  {
+    const int r0 = blockIdx.y * kJoinRows + warp;
     float ref[RW], sum[RW];
     float4 o[RW];
 #pragma unroll
@@ -1532,7 +1535,8 @@ int launch(const Plan& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, cons
     return DFLASH2_ERR_CUDA;
   const int rc = launch_k(attend_tc_kernel<E4M3>, dim3(c.nsm), dim3(kThreads), Smem<E4M3>::bytes, c, p, tm_k, tm_v);
   if (rc != DFLASH2_OK) return rc;
-  return launch_k(attend_join_kernel, dim3(p.a.batch * p.tiles_s * p.a.nkv), dim3(256), 0, c, p, c.nsm);
+  return launch_k(attend_join_kernel, dim3(p.a.batch * p.tiles_s * p.a.nkv, (p.slot_rows + kJoinRows - 1) / kJoinRows),
+                  dim3(256), 0, c, p, c.nsm);
 }
 
 }  // namespace
