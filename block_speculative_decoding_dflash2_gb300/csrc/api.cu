@@ -1198,6 +1198,7 @@ int dflash2_adjust_logits(int dtype, int batch, int rows, int vocab, const void*
   if (path && (rows < 2 || rows > 32)) return DFLASH2_ERR_BLOCK_SIZE;
   if ((int64_t)batch * rows > 1 && out_stride < vocab) return DFLASH2_ERR_SHAPE;
   if (!out || (uintptr_t)out % (dtype == DFLASH2_F32 ? 4 : 2)) return DFLASH2_ERR_INVALID_ARG;
+  if (out == logits && (int64_t)batch * rows > 1 && out_stride != stride) return DFLASH2_ERR_SHAPE;
   if (max_tokens > 0 && (!tokens || !n_tokens)) return DFLASH2_ERR_INVALID_ARG;
   if (n_bias > 0 && (!bias_id || !bias)) return DFLASH2_ERR_INVALID_ARG;
   for (const void* p : {(const void*)tokens, (const void*)n_tokens, (const void*)prompt_len, (const void*)path,

@@ -52,7 +52,6 @@ constexpr int kD = 128;     // head dimension
 constexpr int kSoftmax = 256;
 constexpr int kThreads = kSoftmax + 128;
 constexpr int kRowTile = 2 * kTile;  // query rows of a segment at most
-constexpr int kInfo = 4;  // tiles that warp 10 may be ahead
 constexpr int kSegs = 3;  // segments that warp 11 may be ahead (its query rows have two places)
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kMaxCtas = kMaxSM;
@@ -92,12 +91,13 @@ struct Smem {
   static constexpr int SLOT = E4M3 ? 16384 : 32768;    // K or V of a tile
   static constexpr int SLOTS = E4M3 ? 9 : 5;
   static constexpr int RING = 65536;
+  static constexpr int INFOS_AHEAD = 4;  // tiles that warp 10 may be ahead of the softmax
   static constexpr int INFO = RING + SLOTS * SLOT;
   static constexpr int INFOS = E4M3 ? (int)sizeof(TileInfo) : 32;  // bf16 keeps the tail of TileInfo only
-  static constexpr int SEG = INFO + kInfo * INFOS;
+  static constexpr int SEG = INFO + INFOS_AHEAD * INFOS;
   static constexpr int QSCALE = SEG + kSegs * (int)sizeof(SegInfo);  // float [kSegs][kRowTile], 8-bit only
   static constexpr int BAR = QSCALE + (E4M3 ? kSegs * kRowTile * 4 : 0);
-  static constexpr size_t bytes = 1024 + BAR + (2 * SLOTS + 2 * kInfo + 2 * kSegs + 12) * 8 + 64;
+  static constexpr size_t bytes = 1024 + BAR + (2 * SLOTS + 2 * INFOS_AHEAD + 2 * kSegs + 12) * 8 + 64;
   static_assert(bytes + 512 <= 227 * 1024, "shared memory");
 };
 
@@ -168,6 +168,14 @@ __device__ __forceinline__ int owner_of(int units, int x, int n) {
   return x < wide ? x / (q + 1) : units % n + (x - wide) / q;
 }
 
+// Place of a CTA's part of a segment.  With a shared part every segment has
+// parts, and (segment, CTA) pairs in order take consecutive places; without,
+// a CTA leaves at most two: of the segment in which its share starts, and of
+// the one in which it ends.
+__device__ __forceinline__ int slot_of(const Plan& p, int segment, int cta, bool from_start) {
+  return p.tiles_p > 0 ? segment + cta : 2 * cta + from_start;
+}
+
 // A place in a ring of N slots and the parity of its round.
 template <int N>
 struct Ring {
@@ -217,6 +225,25 @@ __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, uint32_t abo
       flag(status, DFLASH2_DEV_WAIT_TIMEOUT);
       return false;
     }
+  }
+}
+
+// Waits, as long at most, until the count at `at` has come to n (counts differ
+// by less than 2^31).
+__device__ __noinline__ bool wait_count(uint32_t at, uint32_t n, uint32_t abort_flag, unsigned* status) {
+  const uint64_t t0 = globaltimer();
+  while (true) {
+    uint32_t x;
+    asm volatile("ld.acquire.cta.shared.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+    if ((int)(x - n) >= 0) return true;
+    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(x) : "r"(abort_flag) : "memory");
+    if (x) return false;
+    if (globaltimer() - t0 > kWaitNs) {
+      asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(abort_flag), "r"(1u) : "memory");
+      flag(status, DFLASH2_DEV_WAIT_TIMEOUT);
+      return false;
+    }
+    __nanosleep(100);
   }
 }
 
@@ -511,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                                                                const __grid_constant__ CUtensorMap tm_k,
                                                                const __grid_constant__ CUtensorMap tm_v) {
   using L = Smem<E4M3>;
-  constexpr int NS = L::SLOTS;
+  constexpr int NS = L::SLOTS, kInfo = L::INFOS_AHEAD;
   extern __shared__ uint8_t raw_smem[];
   // (an offset, not a cast address: the compiler keeps to shared-memory accesses)
   uint8_t* sm = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
@@ -531,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
   uint64_t* drain = q_full + 2;             // every product issued is done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   uint32_t* abort_flag = tmem_slot + 1;
-  const uint32_t abort_at = smem_u32(abort_flag);
+  const uint32_t abort_at = smem_u32(abort_flag), issued_at = abort_at + 4;  // loads issued
   SegInfo* segs = reinterpret_cast<SegInfo*>(sm + L::SEG);
   __shared__ int scan[kThreads / 32], ends[kThreads / 32][2], start[3];
 
@@ -559,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     }
     mbar_init(q_ready, 8);
     mbar_init(drain, 1);
-    *abort_flag = 0;
+    abort_flag[0] = abort_flag[1] = 0;
   }
   fence_barrier_init();
   if (warp == 9) {
@@ -633,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
       p.head[2 + e] = x;
       x += units_of(e, &nl);
       const int s = e / p.tiles_s;
-      if (a.kv_len[s] != nl.y) flag(a.status, DFLASH2_DEV_BAD_LENGTH);
+      if (a.kv_len[s] != nl.y || (a.n_new && a.n_new[s] != nl.x)) flag(a.status, DFLASH2_DEV_BAD_LENGTH);
     }
   }
   // the row tile and the position in which this CTA's share starts
@@ -736,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         g.h = h;
         g.first = base + k.x * kTile;
         g.tiles = k.y - k.x;
-        g.slot = k.x == 0 && k.y == tiles && p.tiles_p == 0 ? -1 : entry * a.nkv + h + cta;
+        g.slot = k.x == 0 && k.y == tiles && p.tiles_p == 0 ? -1 : slot_of(p, entry * a.nkv + h, cta, k.x == 0);
         g.q = g.split ? q_next : 0;
         if (seg_at.round > 0) ok = wait(seg_empty + seg_at.slot, (seg_at.round - 1) & 1) && ok;
         ok = __all_sync(0xffffffffu, ok);
@@ -800,7 +827,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         uint8_t* dst = sm + L::RING + slot * L::SLOT;
-        if (lane == 0) mbar_arrive_expect_tx(full + slot, L::SLOT);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(full + slot, L::SLOT);
+          asm volatile("st.release.cta.shared.u32 [%0], %1;" ::"r"(issued_at), "r"(at.round * NS + slot + 1) : "memory");
+        }
         const int row = __shfl_sync(0xffffffffu, rows, (t & 3) * 8 + (lane & 7));
         if (E4M3) {
           if (lane < 8) tma_load_2d(dst + lane * 2048, map, full + slot, x_h, row, pol);
@@ -990,7 +1020,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         if (lane == 0) info->groups = groups;
         __syncwarp();
         if (mixed) {
-          ok = __all_sync(0xffffffffu, wait(full + vat.slot, vat.round & 1));
+          // (This warp may be more than a round of the ring ahead of the loads,
+          // and a wait for a parity takes the phase before the last for the
+          // right one: it waits for the load to be issued first.)
+          ok = __all_sync(0xffffffffu, wait_count(issued_at, vat.round * NS + vat.slot + 1, abort_at, a.status) &&
+                                           wait(full + vat.slot, vat.round & 1));
           if (!ok) break;
           uint8_t* v = sm + L::RING + vat.slot * L::SLOT;
           // keys below `to` and from `from` on are not seen by every row; behind
@@ -1400,6 +1434,8 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   const int at = start + h * cost_of(p.seg_cost, g.tiles, w), ip = f0 / kRowTile, cost_p = cost_of(p.seg_cost, tiles_p, wp);
   // (a block looks at one CTA per thread)
   uint32_t mine = 0;
+  // the CTA that has the segment's first tile
+  const int c_first = g.tiles > 0 ? owner_of(units, at + p.seg_cost, nctas) : -1;
   {
     const int c = threadIdx.x;
     bool own = false, p0 = false, p1 = false;
@@ -1456,7 +1492,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
             rl[u] = make_float2(kNone, 0.f);
             x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (in) {
-              const size_t row = kind == 0 ? (size_t)(entry * a.nkv + h + c) * p.slot_rows + r
+              const size_t row = kind == 0 ? (size_t)slot_of(p, entry * a.nkv + h, c, c == c_first) * p.slot_rows + r
                                            : (size_t)((ip + kind - 1) * a.nkv + h + c) * kRowTile + f % kRowTile;
               rl[u] = (kind == 0 ? p.ref_s : p.ref_p)[row];
               x[u] = reinterpret_cast<const float4*>((kind == 0 ? p.part_s : p.part_p) + row * kD)[lane];
@@ -1510,7 +1546,7 @@ bool sizes_of(int batch, int n_tok, int nq, int nkv, int shared_len, int ctas, S
   z->slot_rows = (int)std::min<long long>(rt, rows);
   const long long segs_s = (long long)batch * z->tiles_s * nkv, segs_p = (long long)z->tiles_p * nkv;
   if (segs_s > (1 << 30) || segs_p > (1 << 30)) return false;
-  const size_t n_s = (size_t)(segs_s + ctas) * z->slot_rows, n_p = z->tiles_p ? (size_t)(segs_p + ctas) * rt : 0;
+  const size_t n_s = (size_t)(z->tiles_p ? segs_s + ctas : 2 * ctas) * z->slot_rows, n_p = z->tiles_p ? (size_t)(segs_p + ctas) * rt : 0;
   size_t at = 256;
   auto take = [&](size_t bytes) {
     const size_t x = at;

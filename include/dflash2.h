@@ -643,8 +643,9 @@ int dflash2_cache_read(const dflash2_cache *cache, const int32_t *block_table, i
  * and values are in the cache already (dflash2_cache_append).
  *   n_tok       tokens of a sequence in q and out, 1 .. 1024
  *   n_new       nullable [batch] int32: the tokens that sequence s has of
- *               them (0 .. n_tok); the rows behind are neither read nor
- *               written (null: n_tok each)
+ *               them (0 .. n_tok; one outside is recorded with
+ *               DFLASH2_DEV_BAD_LENGTH and counts as the nearer end); the rows
+ *               behind are neither read nor written (null: n_tok each)
  *   kv_len      [batch] int32: keys of each sequence, its tokens' own last
  *   n_q_heads   a multiple of n_kv_heads, at most 1024; query head h reads
  *               kv head h / (n_q_heads / n_kv_heads)
@@ -655,14 +656,16 @@ int dflash2_cache_read(const dflash2_cache *cache, const int32_t *block_table, i
  *   causal      token i of n sees the keys below kv_len - n + 1 + i; with 0
  *               every token sees all kv_len
  *   window      > 0: of these only the last `window`; 0: all
- *   shared_len  the first shared_len positions are the same pages in every
- *               row of the block table (a common prompt): they are read
- *               through row 0 and computed once for the whole batch.  0:
- *               none.  A sequence may have fewer keys than that.
+ *   shared_len  the first shared_len positions are the same in every
+ *               sequence (a common prompt): they are read through row 0 of the
+ *               block table, which has their pages whatever kv_len[0] is, and
+ *               computed once for the whole batch.  0: none.  A sequence may
+ *               have fewer keys than that.
  * out = softmax(scale * q k) v over the keys that a token sees, zeros where
  * there is none; scores, weights and sums are fp32 and the result is rounded
  * once.  Keys that a token does not see have no part in its result, whatever
- * they hold.  Keys past the block table (DFLASH2_DEV_BAD_LENGTH) or on a page
+ * they hold; of a token that sees a value which is not finite, the whole head's
+ * result may be NaN.  Keys past the block table (DFLASH2_DEV_BAD_LENGTH) or on a page
  * outside [0, n_pages) (DFLASH2_DEV_BAD_PAGE) are left out.
  * The workspace needs dflash2_attend_workspace bytes (0 for bad sizes; host
  * only), 16-byte aligned, its first 256 bytes zeroed once before the first

@@ -91,6 +91,7 @@ def test_adjust_logits(B):
     assert call(path=P, rows=1) == -3 and call(path=P, rows=33) == -3
     for name in ("tok", "n", "prompt", "path", "rho", "pres", "freq", "mask"):
         assert call(**{name: P + 2}) == -1, name
+    assert call(z=P, out=P, stride=12, os_=10) == -2  # in place, but not row upon row
     assert call(ws=P + 1) == -5
 
 

@@ -92,7 +92,7 @@ class Case:
         qv.copy_(self.q)
         n_new = None
         if self.count != [self.n_tok] * batch:
-            n_new = torch.tensor(self.count, dtype=torch.int32, device="cuda")
+            n_new = torch.tensor(getattr(self, "passed", self.count), dtype=torch.int32, device="cuda")
             for i, n in enumerate(self.count):
                 qv[i, n:] = float("nan")
         B.dflash2_attend(cache, torch.from_numpy(self.table).cuda(), torch.tensor(self.lens, dtype=torch.int32,
@@ -151,6 +151,15 @@ def test_shared_prefix(B, cache, nq, nkv, n_tok, lens, shared, causal, window):
 
 
 @pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("d", [128, 64])
+def test_token_counts_out_of_range_are_recorded(B, cache, d):
+    c = Case(B, cache, d, 16, 8, 2, 3, [50, 60, 70], n_new=[3, 0, 2], seed=12)
+    want = c.check()
+    c.passed = [7, -2, 2]  # counts as the nearer ends: 3 and 0
+    assert np.array_equal(c.run(status=B.DEV_BAD_LENGTH), want)
+
+
+@pytest.mark.parametrize("cache", CACHES)
 def test_ragged_tokens(B, cache):
     for shared in (0, 64):
         Case(B, cache, 128, 16, 8, 2, 9, [200, 100, 90, 300], shared=shared, n_new=[9, 0, 1, 4]).check(stride=24)
@@ -159,7 +168,8 @@ def test_ragged_tokens(B, cache):
 
 @pytest.mark.parametrize("cache", CACHES)
 @pytest.mark.parametrize("lens,nq,nkv,n_tok", [([3000, 10, 2000], 4, 1, 2), ([8200], 2, 1, 1), ([70] * 300, 2, 1, 1),
-                                               ([5000, 5000], 16, 1, 20), ([700], 2, 1, 200)])
+                                               ([5000, 5000], 16, 1, 20), ([700], 2, 1, 200), ([40, 3] * 500, 2, 1, 1),
+                                               ([66] * 210, 8, 1, 33), ([20, 700, 2] * 150, 8, 4, 2)])
 def test_long_and_many(B, cache, lens, nq, nkv, n_tok):
     Case(B, cache, 128, 16, nq, nkv, n_tok, lens, seed=3).check()
 
