@@ -74,9 +74,10 @@ __device__ constexpr uint32_t o_col(int j) { return 256u + 128u * j; }
 
 struct TileInfo {
   float ks[kTile], vs[kTile];  // scales 2^(byte - 127) of keys and values
+  float lv[kTile];             // log2 of the values' scales (at least -60)
   uint32_t bad[4];             // keys whose values were not finite and are zeros now
   uint32_t groups;             // bit i: 16-key group i exists
-  float vmax;                  // log2 of the largest value scale (at least -60)
+  float vmax;                  // the largest of lv
   uint32_t mixed;              // some row does not see some key
   uint32_t pad;
 };
@@ -1022,6 +1023,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
             const uint32_t kb = min(x & 0xffffu, 254u), vb = min(x >> 16, 254u);
             info->ks[32 * i + lane] = __uint_as_float(kb << 23);
             info->vs[32 * i + lane] = __uint_as_float(vb << 23);
+            info->lv[32 * i + lane] = (float)max((int)vb - 127, -60);
             top = max(top, vb);
           }
           top = __reduce_max_sync(0xffffffffu, top);
@@ -1196,7 +1198,23 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
             y[10] = fmaxf(x[30], x[31]);
             float top = max3(max3(y[0], y[1], y[2]), max3(y[3], y[4], y[5]), max3(max3(y[6], y[7], y[8]), y[9], y[10])) * rs;
             if (E4M3) top += info->vmax;
-            if (__any_sync(0xffffffffu, mine && top > ref + head_room)) {
+            bool over = __any_sync(0xffffffffu, mine && top > ref + head_room);
+            if (E4M3 && over) {
+              // (only a bound: the largest scale may be that of a key with a
+              // small weight, or of one that the row does not see, whose page
+              // may hold anything.  The reference comes from the keys' own.)
+              top = kNone;
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const ulonglong2 l4 = *reinterpret_cast<const ulonglong2*>(info->lv + 32 * c + i);
+                float a0, a1, a2, a3;
+                unpack2(fma2(pack2(x[i], x[i + 1]), rs2, l4.x), a0, a1);
+                unpack2(fma2(pack2(x[i + 2], x[i + 3]), rs2, l4.y), a2, a3);
+                top = max3(max3(top, a0, a1), a2, a3);
+              }
+              over = __any_sync(0xffffffffu, mine && top > ref + head_room);
+            }
+            if (over) {
               // a new reference (a whole number, so that what is scaled to it
               // stays exact).  The products of the stream's last tile are
               // done: this tile's scores were issued behind them.
