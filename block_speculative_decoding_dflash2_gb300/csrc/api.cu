@@ -1170,7 +1170,8 @@ int dflash2_attend(const dflash2_cache* cache, const int32_t* block_table, int m
   a.max_pages = max_pages;
   a.batch = batch;
   a.n_tok = n_tok;
-  a.window = window;
+  // (a window of all that there can be is none, and in the kernels no sum with it leaves 32 bits)
+  a.window = window < (int64_t)max_pages * c.page_size ? window : 0;
   a.shared_len = shared_len;
   a.k = c.k;
   a.v = c.v;

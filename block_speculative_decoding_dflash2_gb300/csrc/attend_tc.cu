@@ -1095,9 +1095,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     const int j = warp >> 2, r = threadIdx.x & 127;  // stream, row of its tile
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float scale = a.scale * 1.4426950408889634f;
-    // how far a weight may pass 2^0: any float will do, or, times the value's
-    // scale, what an e5m2 holds
-    const float head_room = E4M3 ? 15.f : 64.f;
+    // how far a weight may pass 2^0: times the value's scale what an e5m2
+    // holds; or little against a float's range, so that large values times
+    // such weights stay finite where their mean does, and enough that a new
+    // reference is rare
+    const float head_room = E4M3 ? 15.f : 16.f;
     uint32_t n_s = 0, n_o = 0, n_q = 0, tiles = 0;
     SegInfo g;
     for (; next_segment(&g); seg_at.step()) {
@@ -1139,6 +1141,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         wait(g.own_q ? q_ready : q_full + g.q, (n_q >> bit) & 1);
         n_q ^= 1u << bit;
         if (mine) rs *= reinterpret_cast<const float*>(sm + L::QSCALE)[seg_at.slot * kRowTile + fr];
+        if (rs < 1.17549435e-38f) rs = 1.17549435e-38f;  // (never 0: a hidden key's score is -inf times that)
       }
       if (E4M3) {
         __syncwarp();

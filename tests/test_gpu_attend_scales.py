@@ -95,3 +95,40 @@ def test_a_large_value_behind_a_small_weight(B, cache, lens, far):
     c.pool["v"][page, at, 0] *= 2.0 ** 50
     c.quantise()
     c.check()
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("step", [1, -1])
+def test_large_values_under_rising_and_falling_scores(B, cache, d, step):
+    """Scores from -30 to 30 along the keys, values of about 2^96: their weighted mean is far inside the range.  (Many
+    sequences, so that one block has whole ones.)"""
+    n, batch = 400, 48
+    c = Case(B, cache, d, 16, 8, 8, 1, [n] * batch, seed=24)
+    for i in range(batch):
+        q = c.q[i, 0].double()
+        unit = q / ((q * q).sum(-1, keepdim=True) * d ** -0.5)
+        for p in range(n):
+            z = step * (60.0 * p / (n - 1) - 30.0)
+            c.pool["k"][c.table[i, p // 16], p % 16] = (unit * z).to(torch.bfloat16)
+    c.pool["v"] *= 2.0 ** 96
+    c.quantise()
+    c.check()
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("d", [128, 64])
+def test_a_query_of_zeros_under_a_small_scale(B, cache, d):
+    c = Case(B, cache, d, 16, 4, 2, 5, [40, 5, 300], seed=25)
+    c.q[:, :, 1] = 0
+    c.q[:, :, 2] *= 2.0 ** -120
+    c.check(scale=1e-12)
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 5000, 320, 319])
+def test_windows_as_long_as_anything(B, cache, d, window):
+    """More tokens than keys too: the first of them see nothing."""
+    c = Case(B, cache, d, 16, 4, 2, 8, [3, 8, 320], seed=26)
+    c.check(window=window)
