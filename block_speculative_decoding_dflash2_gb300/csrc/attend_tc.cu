@@ -39,7 +39,7 @@
 // instruction cache, and unrolled it took most of the time to fetch.
 //
 // Measured.  32 x 8 tokens at contexts of 512 to 4096, 4 heads a kv head,
-// bfloat16: 68 us, 4.5 TB/s of the cache; 256 x 7 at 8192, 8-bit: 565 us, 3.8
+// bfloat16: 68 us, 4.5 TB/s of the cache; 256 x 7 at 8192, 8-bit: 575 us, 3.8
 // TB/s.  Few rows are bound by a tile's chain of scores, softmax and weighted
 // sums, of which a CTA has two under way (its values come late in the chain,
 // so their bytes wait in shared memory).  Behind a shared prefix: 64 x 16

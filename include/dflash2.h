@@ -615,7 +615,9 @@ typedef struct dflash2_cache {
  *   new_off   [batch + 1] int32 row offsets of each sequence, new_off[0] = 0,
  *             new_off[batch] <= n_new; rows behind it are not written
  * A row past the block table (DFLASH2_DEV_BAD_LENGTH) or on a page outside
- * [0, n_pages) (DFLASH2_DEV_BAD_PAGE) is skipped.
+ * [0, n_pages) (DFLASH2_DEV_BAD_PAGE) is skipped.  No position of the pool is
+ * written by two rows of a call (sequences may share pages that they only
+ * read).
  */
 int dflash2_cache_append(const dflash2_cache *cache, const int32_t *block_table, int max_pages, int batch,
                          const int32_t *ctx_len, int n_new, const void *k, int64_t k_stride, const void *v,
