@@ -102,6 +102,8 @@ def testing_lib():
         T.dflash2_test_force_cluster_split.argtypes = [I]
         T.dflash2_test_force_attention.restype = I
         T.dflash2_test_force_attention.argtypes = [I]
+        T.dflash2_test_force_attend.restype = I
+        T.dflash2_test_force_attend.argtypes = [I]
         T.dflash2_test_w4_withhold.restype = I
         T.dflash2_test_w4_withhold.argtypes = [I]
         T.dflash2_test_last_attention.restype = I
@@ -687,6 +689,12 @@ def dflash2_test_force_attention(mode):
     """Attention kernel of later draft steps: 0 the library's choice, 1 the
     mma.sync cluster kernel, 2 the tcgen05 kernel wherever it applies."""
     _check("dflash2_test_force_attention", testing_lib().dflash2_test_force_attention(int(mode)))
+
+
+def dflash2_test_force_attend(mode):
+    """Kernel of later dflash2_attend calls: 0 the library's choice, 1 the
+    general one, 2 the tensor cores' wherever it applies."""
+    _check("dflash2_test_force_attend", testing_lib().dflash2_test_force_attend(int(mode)))
 
 
 def dflash2_test_last_attention():

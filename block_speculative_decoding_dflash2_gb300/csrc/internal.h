@@ -237,6 +237,9 @@ int attn_cluster_ctas(int max_ctx, int B, int batch, int nkv, int nsm);
 // test hook: 0 = the library's choice, 1 = the mma.sync cluster kernel,
 // 2 = the tcgen05 kernel wherever it applies
 void attention_force_mode(int mode);
+// Test hook: the kernel of later dflash2_attend calls (0 the library's choice,
+// 1 the general one, 2 the tensor cores' wherever it applies).
+void attend_force_mode(int mode);
 int attention_last_kernel();  // test hook: 1 mma.sync cluster, 2 tcgen05, 3 SIMT (0 before any launch)
 // tcgen05 attention (attention_tc.cu): bf16 storage, head dimension 128,
 // 16-key pages, at most 80 query rows per kv head

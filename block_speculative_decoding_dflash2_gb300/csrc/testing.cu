@@ -107,6 +107,12 @@ int dflash2_test_force_attention(int mode) {
   return 0;
 }
 
+int dflash2_test_force_attend(int mode) {
+  if (mode < 0 || mode > 2) return DFLASH2_ERR_INVALID_ARG;
+  df2::attend_force_mode(mode);
+  return 0;
+}
+
 int dflash2_test_last_attention(void) { return df2::attention_last_kernel(); }
 
 int dflash2_test_w4_withhold(int on) {

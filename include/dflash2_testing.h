@@ -71,6 +71,13 @@ int dflash2_test_force_cluster_split(int cs);
 int dflash2_test_force_attention(int mode);
 
 /*
+ * The same for dflash2_attend: 0, the library's choice; 1, the general kernel;
+ * 2, the tensor cores' kernel wherever it applies (head dimension 128, pages
+ * of 2^n >= 16 keys).
+ */
+int dflash2_test_force_attend(int mode);
+
+/*
  * The attention kernel the last bf16 or fp32 draft step of this process
  * launched: 1 the mma.sync cluster kernel, 2 the tcgen05 kernel, 3 the SIMT
  * partial + combine kernels; 0 before any.

@@ -22,6 +22,14 @@ def B():
     return binding
 
 
+@pytest.fixture(autouse=True, params=[0, 2], ids=["choice", "tensor"])
+def kernel(request, B):
+    """The library's choice of a kernel, and the tensor cores' for short sequences too."""
+    B.dflash2_test_force_attend(request.param)
+    yield
+    B.dflash2_test_force_attend(0)
+
+
 def spoil(c, page, slots, kind, names=("k", "v"), byte=None):
     """Overwrites positions of a page on the device: the largest finite numbers, or none."""
     for name in names:
