@@ -13,9 +13,9 @@
 // what lies in them (a NaN, an infinity) does not matter.
 //
 // What bounds it: for a few keys the chain lengths, block table, keys and
-// values, meeting (5 us); then about 1 us for every 32 keys of a CTA, the
+// values, meeting (5 us); then about 0.8 us for every 32 keys of a CTA, the
 // latency of its loads and of scores, weights and sums in turn.  One token of
-// 300 keys and 8 kv heads: 7 us (one CTA a block, and its slots meeting in
+// 300 keys and 8 kv heads: 6.9 us (numbers one by one instead of by twos: 7.6; one CTA a block, and its slots meeting in
 // shared memory: 18; tensor cores: 18).
 #include <algorithm>
 #include <atomic>
@@ -56,18 +56,16 @@ struct Piece {
     }
     if (E4M3) s = __uint_as_float((uint32_t)exps[row] << 23);
   }
-  __device__ __forceinline__ void widen(float (&x)[D / 8]) const {
+  __device__ __forceinline__ void widen(uint64_t (&x)[D / 16]) const {  // two numbers each
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       if (E4M3) {
         const __half2_raw h =
             __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
         const float2 f = __half22float2(__half2(h));
-        x[2 * i] = f.x * s;
-        x[2 * i + 1] = f.y * s;
+        x[i] = mul2(pack2(f.x, f.y), pack2(s, s));
       } else {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        x[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
       }
     }
   }
@@ -93,7 +91,8 @@ __global__ void __launch_bounds__(32 * kWarps) attend_rows_kernel(const __grid_c
     if (threadIdx.x == 0) flag(a.status, DFLASH2_DEV_BAD_LENGTH);
     len = len < 0 ? 0 : a.max_pages * a.page_size;
   }
-  float q[kRows][E], acc[kRows][E], m[kRows], l[kRows];
+  uint64_t q[kRows][E / 2], acc[kRows][E / 2];
+  float m[kRows], l[kRows];
   int lo[kRows], hi[kRows];
   int from = len, to = 0, all_lo = 0, all_hi = len;  // keys that some and that all of the rows see
   const float scale = a.scale * 1.4426950408889634f;
@@ -104,9 +103,9 @@ __global__ void __launch_bounds__(32 * kWarps) attend_rows_kernel(const __grid_c
     p.load(a.q + ((size_t)s * a.n_tok + t) * a.q_stride + (size_t)(h * group + row % group) * D, nullptr, 0, sub);
     p.widen(q[r]);
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      q[r][i] *= scale;
-      acc[r][i] = 0.f;
+    for (int i = 0; i < E / 2; ++i) {
+      q[r][i] = mul2(q[r][i], pack2(scale, scale));
+      acc[r][i] = 0ull;
     }
     m[r] = -INFINITY;
     l[r] = 0.f;
@@ -144,35 +143,55 @@ __global__ void __launch_bounds__(32 * kWarps) attend_rows_kernel(const __grid_c
     page = next;
     next = page_of(j + step);
     fetch(j, page, next_k, next_v);
-    float x[E], dot[kRows];
+    uint64_t x[E / 2];
+    float dot[kRows];
     if (there) pk.widen(x);
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       dot[r] = 0.f;
-      if (there)
+      if (there) {
+        uint64_t two = 0ull;
 #pragma unroll
-        for (int i = 0; i < E; ++i) dot[r] = fmaf(q[r][i], x[i], dot[r]);
+        for (int i = 0; i < E / 2; ++i) two = fma2(q[r][i], x[i], two);
+        float even, odd;
+        unpack2(two, even, odd);
+        dot[r] = even + odd;
+      }
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) dot[r] += __shfl_xor_sync(0xffffffffu, dot[r], o);
     }
     if (there) pv.widen(x);
-    auto add = [&](int r) {
-      const float mn = fmaxf(m[r], dot[r]);
-      const float ref = mn == -INFINITY ? 0.f : mn;
-      const float f = exp2f(m[r] - ref), p = exp2f(dot[r] - ref);
+    auto raise = [&](int r) {  // the maximum, if the key's score is above it
+      const float mn = fmaxf(m[r], dot[r]), f = ex2(m[r] - (mn == -INFINITY ? 0.f : mn));
       m[r] = mn;
-      l[r] = fmaf(l[r], f, p);
+      l[r] *= f;
 #pragma unroll
-      for (int i = 0; i < E; ++i) acc[r][i] = fmaf(acc[r][i], f, p * x[i]);
+      for (int i = 0; i < E / 2; ++i) acc[r][i] = mul2(acc[r][i], pack2(f, f));
+    };
+    auto add = [&](int r) {
+      const float p = ex2(dot[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+      l[r] += p;
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) acc[r][i] = fma2(pack2(p, p), x[i], acc[r][i]);
     };
     // (without branches between them the rows' chains run side by side)
     if (__all_sync(0xffffffffu, there && at >= all_lo && at < all_hi)) {
+      bool up = false;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) up |= dot[r] > m[r];
+      if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) raise(r);
+      }
 #pragma unroll
       for (int r = 0; r < kRows; ++r) add(r);
     } else {
 #pragma unroll
       for (int r = 0; r < kRows; ++r)
-        if (there && at >= lo[r] && at < hi[r]) add(r);
+        if (there && at >= lo[r] && at < hi[r]) {
+          raise(r);
+          add(r);
+        }
     }
     pk = next_k;
     pv = next_v;
@@ -182,22 +201,25 @@ __global__ void __launch_bounds__(32 * kWarps) attend_rows_kernel(const __grid_c
   for (int r = 0; r < kRows; ++r) {
     float top = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 8));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-    const float f = exp2f(m[r] - (top == -INFINITY ? 0.f : top));
+    const float f = ex2(m[r] - (top == -INFINITY ? 0.f : top));
     l[r] *= f;
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 8);
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 16);
     if (lane == 0) part_ml[warp][r] = make_float2(top, l[r]);
+    float o[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      acc[r][i] *= f;
-      acc[r][i] += __shfl_xor_sync(0xffffffffu, acc[r][i], 8);
-      acc[r][i] += __shfl_xor_sync(0xffffffffu, acc[r][i], 16);
+    for (int i = 0; i < E / 2; ++i) {
+      unpack2(mul2(acc[r][i], pack2(f, f)), o[2 * i], o[2 * i + 1]);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        o[2 * i + b] += __shfl_xor_sync(0xffffffffu, o[2 * i + b], 8);
+        o[2 * i + b] += __shfl_xor_sync(0xffffffffu, o[2 * i + b], 16);
+      }
     }
     if (lane < 8)
 #pragma unroll
       for (int i = 0; i < E; i += 4)
-        *reinterpret_cast<float4*>(&part[warp][r][sub * E + i]) =
-            make_float4(acc[r][i], acc[r][i + 1], acc[r][i + 2], acc[r][i + 3]);
+        *reinterpret_cast<float4*>(&part[warp][r][sub * E + i]) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
   }
   __syncthreads();
   auto store = [&](int r, int d, float sum, float2 o) {
@@ -217,7 +239,7 @@ __global__ void __launch_bounds__(32 * kWarps) attend_rows_kernel(const __grid_c
     const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) {
-      const float f = exp2f(part_ml[k][r].x - ref);
+      const float f = ex2(part_ml[k][r].x - ref);
       const float2 x = *reinterpret_cast<const float2*>(&part[k][r][d]);
       sum = fmaf(part_ml[k][r].y, f, sum);
       o.x = fmaf(x.x, f, o.x);
@@ -251,7 +273,7 @@ __global__ void __launch_bounds__(32 * kWarps) attend_rows_kernel(const __grid_c
 #pragma unroll
       for (int k = 0; k < kMaxCluster; ++k) {
         if (k >= ctas) continue;
-        const float f = exp2f(from_ml[k].x - ref);
+        const float f = ex2(from_ml[k].x - ref);
         sum = fmaf(from_ml[k].y, f, sum);
         o.x = fmaf(x[k].x, f, o.x);
         o.y = fmaf(x[k].y, f, o.y);
@@ -277,12 +299,13 @@ int launch_attend(const AttendArgs& a, void* workspace, const Ctx& c) {
   while (ctas > 1 && (all * ctas > (ctas == 8 ? c.nsm / 2 : c.nsm) || (ctas / 2) * kSlots >= cap)) ctas /= 2;
   // The tensor cores wherever their kernel goes, but for little work: theirs
   // starts late (plan, tiles, a second kernel; 13 to 20 us), this one takes 5
-  // us and then 1 for every time a CTA goes over its slots, at most as often
+  // us and then 0.8 for every time a CTA goes over its slots, at most as often
   // as the block table allows.  us here and there, by times, bfloat16 and 8
-  // heads of 4: 1 token (12 times: 2976 keys) 17 and 26, 4 sequences (12: 1536)
-  // 17 and 22, 16 (15: 480) 18 and 23, (24: 768) 27 and 25, 32 (12: 192) 18 and
-  // 24, (30: 480) 35 and 29; 2 heads of 8, 16 sequences (12: 768) 17 and 18,
-  // (18: 1152) 22 and 19.
+  // heads of 4: 1 token (12 times: 2976 keys) 15 and 26, 4 sequences (12: 1536)
+  // 15 and 22, 16 (15: 480) 16 and 23, (24: 768) 23 and 25, 32 (12: 192) 16 and
+  // 24, (30: 480) 31 and 29; 8-bit, 16 (24: 768) 27 and 28.  (With 2 heads of 8
+  // the tensor cores start some us earlier: 18 us at 16 sequences of 768, 12
+  // times.)
   const long long times = (cap + kSlots * ctas - 1) / (kSlots * ctas) * ((all * ctas + c.nsm - 1) / c.nsm);
   const int mode = g_mode.load();
   if (mode != 1 && (times > 15 || mode == 2) && attend_tc_fits(a)) return launch_attend_tc(a, workspace, c);
