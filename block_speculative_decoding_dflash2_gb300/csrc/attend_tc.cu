@@ -78,7 +78,7 @@ struct TileInfo {
   uint32_t bad[4];             // keys whose values were not finite and are zeros now
   uint32_t groups;             // bit i: 16-key group i exists
   float vmax;                  // the largest of lv
-  uint32_t mixed;              // some row does not see some key
+  uint32_t spoilt;             // some bit of `bad` is set
   uint32_t pad;
 };
 
@@ -999,7 +999,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
           if (lane == 0) info->vmax = (float)max((int)top - 127, -60);
         }
         if (lane < 4) info->bad[lane] = 0;
-        if (lane == 0) info->groups = groups;
+        if (lane == 0) {
+          info->groups = groups;
+          info->spoilt = 0;
+        }
         __syncwarp();
         if (mixed) {
           // (This warp may be more than a round of the ring ahead of the loads,
@@ -1014,6 +1017,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
           const int to = min(kTile, g.all_lo - k0), past = g.end - k0, top = min(kTile, (past + 15) & ~15);
           int key0 = to > 0 ? 0 : max(0, g.all_hi - k0) & ~3;
           constexpr int W = E4M3 ? 8 : 16;  // lanes of a row, 16 bytes each
+          uint32_t any = 0;
 #pragma unroll 1
           while (key0 < top) {
             const int key = key0 + lane / W, c = lane & (W - 1);
@@ -1046,10 +1050,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
             if (in && (bad || behind))
               *q = behind ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(w[0], w[1], w[2], w[3]);
             const uint32_t votes = __ballot_sync(0xffffffffu, bad && !behind);
+            any |= votes;
             if (lane % W == 0 && ((votes >> lane) & ((1u << W) - 1u))) atomicOr(&info->bad[key >> 5], 1u << (key & 31));
             key0 += 32 / W;
             if (key0 >= to && key0 < ((g.all_hi - k0) & ~3)) key0 = (g.all_hi - k0) & ~3;
           }
+          if (lane == 0) info->spoilt = any;
           fence_proxy_async_smem();
           __syncwarp();
         }
@@ -1136,7 +1142,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
           const int k0 = first + t * kTile;
           const int v0 = see.x - k0, v1 = see.y > k0 + kTile ? kTile : see.y - k0;  // keys of the tile that it sees
           const uint32_t groups = info->groups;
-          const bool cut = __any_sync(0xffffffffu, mine && (v0 > 0 || v1 < kTile)) || groups != 0xffu;
+          // (a mended value is seen by rows that the whole tile is open to, too: other warps' rows made it a mended tile)
+          const bool cut =
+              __any_sync(0xffffffffu, mine && (v0 > 0 || v1 < kTile)) || groups != 0xffu || info->spoilt != 0;
           // bit i: key 32 c + i is seen
           auto seen = [&](int c) {
             const int from = min(32, max(0, v0 - 32 * c)), to = min(32, max(0, v1 - 32 * c));
