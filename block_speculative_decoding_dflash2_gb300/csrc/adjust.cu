@@ -269,10 +269,10 @@ int launch_adjust(const AdjustArgs& a, const Ctx& c) {
   const size_t smem = (size_t)slice * (group * size + 6) + slice / 8 + (a.mask ? (size_t)group * slice / 8 : 0) +
                       (a.n_bias > 0 ? (size_t)slice * 2 : 0);
   const dim3 grid((a.vocab + slice - 1) / slice, a.batch);
-  // (on every call: an attribute of the kernel on the current device)
+  // (an attribute of the kernel on the current device, so on every call; and
+  // whatever smem is: the limit without it counts the kernel's static bytes too)
   const void* kernel = a.bf16_logits ? (const void*)adjust_kernel<bf16> : (const void*)adjust_kernel<float>;
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024) != cudaSuccess)
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024) != cudaSuccess)
     return DFLASH2_ERR_CUDA;
   return a.bf16_logits ? launch_k(adjust_kernel<bf16>, grid, dim3(kThreads), smem, c, a, slice)
                        : launch_k(adjust_kernel<float>, grid, dim3(kThreads), smem, c, a, slice);
