@@ -139,12 +139,17 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant_
     if (!(atomicOr(touched + (e >> 5), bit) & bit)) list[atomicAdd(&listed, 1)] = (uint16_t)e;
   };
   __syncthreads();
-  if (penal) {
-    if (n < 0 || n > a.max_tokens) {
-      if (threadIdx.x == 0) flag(a.status, DFLASH2_DEV_BAD_LENGTH);
-      n = n < 0 ? 0 : a.max_tokens;
-    }
-    const int32_t* tok = a.tokens + (size_t)s * a.max_tokens;
+  if (n < 0 || n > a.max_tokens) {
+    if (threadIdx.x == 0) flag(a.status, DFLASH2_DEV_BAD_LENGTH);
+    n = n < 0 ? 0 : a.max_tokens;
+  }
+  const int32_t* tok = a.tokens + (size_t)s * a.max_tokens;
+  if (!penal) {
+    // nothing to count: the sequence's blocks share its ids, and only look whether they are any
+    if (a.status)
+      for (unsigned i = blockIdx.x * kThreads + threadIdx.x; i < (unsigned)n; i += gridDim.x * kThreads)
+        if ((unsigned)tok[i] >= (unsigned)a.vocab) flag(a.status, DFLASH2_DEV_BAD_TOKEN);
+  } else {
     for (int i0 = 0; i0 < n; i0 += kAhead * kThreads) {
       int t[kAhead];
 #pragma unroll
@@ -163,12 +168,12 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant_
         }
       }
     }
-    if (a.path && (int)threadIdx.x < a.rows - 1) {
-      const int t = a.path[(size_t)s * (a.rows - 1) + threadIdx.x], e = t - v0;
-      path[threadIdx.x] = t;
-      if (t < -1 || t >= a.vocab) flag(a.status, DFLASH2_DEV_BAD_TOKEN);
-      else if (t >= 0 && e >= 0 && e < nv) touch(e);
-    }
+  }
+  if (a.path && (int)threadIdx.x < a.rows - 1) {
+    const int t = a.path[(size_t)s * (a.rows - 1) + threadIdx.x], e = t - v0;
+    path[threadIdx.x] = t;
+    if (t < -1 || t >= a.vocab) flag(a.status, DFLASH2_DEV_BAD_TOKEN);
+    else if (penal && t >= 0 && e >= 0 && e < nv) touch(e);
   }
   if (biased) {
     // entries of the slice; of one token's several the last counts: 16-bit
