@@ -1196,6 +1196,7 @@ int dflash2_adjust_logits(int dtype, int batch, int rows, int vocab, const void*
                           int64_t out_stride, void* workspace, void* stream) {
   TRY(check_sampling(dtype, batch, rows, vocab, logits, stride));
   if (batch > kMaxCacheBatch || max_tokens < 0 || n_bias < 0 || n_bias > 65535) return DFLASH2_ERR_SHAPE;
+  if (max_tokens > INT32_MAX - 4096) return DFLASH2_ERR_SHAPE;  // (a block walks them 2048 at a time, in 32 bits)
   if (path && (rows < 2 || rows > 32)) return DFLASH2_ERR_BLOCK_SIZE;
   if ((int64_t)batch * rows > 1 && out_stride < vocab) return DFLASH2_ERR_SHAPE;
   if (!out || (uintptr_t)out % (dtype == DFLASH2_F32 ? 4 : 2)) return DFLASH2_ERR_INVALID_ARG;

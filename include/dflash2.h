@@ -693,7 +693,7 @@ int dflash2_attend(const dflash2_cache *cache, const int32_t *block_table, int m
  * computed in fp32 and rounded once.
  *   dtype, vocab, logits, stride   as above; `rows` rows per sequence
  *   tokens      [batch, max_tokens] int32, n_tokens [batch] of them used
- *               (both nullable with max_tokens = 0)
+ *               (both nullable with max_tokens = 0; below 2^31 - 4096)
  *   prompt_len  nullable [batch]: tokens before it are seen but not counted
  *               (null: 0)
  *   path        nullable [batch, rows - 1] int32: the drafts (2 to 32 rows);
