@@ -25,8 +25,9 @@
 // with V, so that its rounding (2^-17) does not add to the output's.  8-bit:
 // the codes are multiplied as they are, no byte of the cache is converted.
 // q is split into two e4m3 codes (its 8 bits are 4 + 4: exact but for values
-// below 2^-17 of the row's largest) and P, times the key's value scale, into
-// three e5m2 codes (3 + 3 + 3 bits, 2^-9 of each weight over 2^30 of range).
+// below 2^-17 of the row's largest) and P, times the key's value scale, an f16,
+// into three e5m2 codes, which hold its 11 bits (2^-11 of each weight, or
+// 2^-27 of the row's largest).
 // The scales of keys multiply the scores; those of values the weights.
 //
 // Warps: 0-3 and 4-7 softmax of stream 0 and 1 (thread = query row); 8 loads
@@ -344,11 +345,16 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // Two f16 as three e5m2 each, in the upper bytes of the halves: an f16's
-// upper byte is an e5m2, so cut, subtract, cut, subtract, round.
+// upper byte is an e5m2, so round, subtract, round, subtract.  Rounding, and
+// not cutting, makes three enough for the eleven bits: at most 2^7 units of
+// the last place are left of the first code, 2^3 of the second, and three bits
+// hold every such number.  That is exact from 2^-6 on; below, what is left may
+// lie under an e5m2's smallest step, and rounding the last code too leaves out
+// 2^-17 at most, 2^-27 of a row's largest weight.
 __device__ __forceinline__ void split3(__half2 u, uint32_t (&h)[3]) {
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const uint32_t top = *reinterpret_cast<const uint32_t*>(&u) & 0xff00ff00u;
+    const uint32_t top = (*reinterpret_cast<const uint32_t*>(&u) + 0x00800080u) & 0xff00ff00u;
     h[q] = top;
     u = __hsub2(u, *reinterpret_cast<const __half2*>(&top));
   }
