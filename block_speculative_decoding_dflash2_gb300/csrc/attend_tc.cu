@@ -24,8 +24,9 @@
 // Precision.  bfloat16: P goes in as bf16 high and low parts, two products
 // with V, so that its rounding (2^-17) does not add to the output's.  8-bit:
 // the codes are multiplied as they are, no byte of the cache is converted.
-// q is split into two e4m3 codes (its 8 bits are 4 + 4: exact but for values
-// below 2^-17 of the row's largest) and P, times the key's value scale, an f16,
+// q is split into an e4m3 and an e5m2 code (its 8 bits are 4 + 4, and what
+// rounding to 4 leaves is one of 0 .. 8 units, which 3 bits hold: exact down
+// to 2^-13 of the row's largest, within 2^-21 of the largest below) and P, times the key's value scale, an f16,
 // into three e5m2 codes, which hold its 11 bits (2^-11 of each weight, or
 // 2^-27 of the row's largest).
 // The scales of keys multiply the scores; those of values the weights.
@@ -426,8 +427,9 @@ __device__ __noinline__ void rescale(uint32_t o, int pieces, uint32_t w, int chu
 
 // Rows [r0, r1) of a segment (r0 and r1 - r0 of one place of 128), by a warp,
 // into the place at `dst`: K-major with the 128-byte swizzle.  bfloat16: two
-// halves of 64 dims, 16 KB apart.  8-bit: the high codes and, 16 KB behind,
-// the low ones; a row's largest magnitude becomes 2^7 .. 2^8, and
+// halves of 64 dims, 16 KB apart.  8-bit: the high codes (e4m3) and, 16 KB
+// behind, the low ones (e5m2, whose smallest step is 2^7 times finer: small
+// channels beside large ones keep their bits); a row's largest magnitude becomes 2^7 .. 2^8, and
 // qscale[row] the factor that its scores take.
 template <bool E4M3>
 __device__ __forceinline__ void load_rows(const Plan& p, const SegInfo& g, int r0, int r1, uint8_t* dst, float* qscale) {
@@ -500,7 +502,7 @@ __device__ __forceinline__ void load_rows(const Plan& p, const SegInfo& g, int r
         const __half2 x = __floats2half2_rn(__uint_as_float(w8[i] << 16) * up, __uint_as_float(w8[i] & 0xffff0000u) * up);
         const uint32_t h2 = __nv_cvt_halfraw2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
         const __half2 back(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h2, __NV_E4M3));
-        const uint32_t l2 = __nv_cvt_halfraw2_to_fp8x2(__hsub2(x, back), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t l2 = __nv_cvt_halfraw2_to_fp8x2(__hsub2(x, back), __NV_SATFINITE, __NV_E5M2);
         hi[i >> 1] = (i & 1) ? hi[i >> 1] | (h2 << 16) : h2;
         lo[i >> 1] = (i & 1) ? lo[i >> 1] | (l2 << 16) : l2;
       }
@@ -859,7 +861,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
           ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
       constexpr uint64_t kMnMajor =
           ((uint64_t)(16384 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-      // A K-major, B = K rows K-major; B = V rows MN-major; 8-bit weights are e5m2
+      // A K-major, B = K rows K-major; B = V rows MN-major; 8-bit weights are
+      // e5m2, and so are the low codes of q
       constexpr uint32_t id_s =
           E4M3 ? (1u << 4) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24) : idesc_bf16_f32(kTile, kTile);
       constexpr uint32_t id_o =
@@ -921,7 +924,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
 #pragma unroll
             for (int x = 0; x < 8; ++x)  // 16 dims each; 8 bits: 32 dims each, with the high, then the low codes of q
               mma_ss<E4M3>(pc, kKMajor | (qd + (x >> 2) * 1024 + (x & 3) * 2),
-                           kKMajor | (kd + (E4M3 ? 0 : (x >> 2) * 1024) + (x & 3) * 2), id_s, x > 0 ? 1u : 0u);
+                           kKMajor | (kd + (E4M3 ? 0 : (x >> 2) * 1024) + (x & 3) * 2),
+                           E4M3 && x >= 4 ? id_s | (1u << 7) : id_s, x > 0 ? 1u : 0u);
             umma_commit(s_full + j);
             if (release) {
               umma_commit(empty + k.slot);

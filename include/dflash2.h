@@ -668,7 +668,9 @@ int dflash2_cache_read(const dflash2_cache *cache, const int32_t *block_table, i
  * and weights with head_dim 64, with pages other than 16, 32, 64, ... keys, and
  * for little work.  Otherwise the tensor cores take a weight to 2^-16 of itself
  * with DFLASH2_BF16; with DFLASH2_E4M3 a weight times its value's scale to
- * 2^-11 of itself, or to 2^-27 of the row's largest.  Keys that a token does not see have no part in its result, whatever
+ * 2^-11 of itself, or to 2^-27 of the row's largest, and a query head's values
+ * exactly down to 2^-13 of its largest, below that to 2^-21 of the largest.
+ * Keys that a token does not see have no part in its result, whatever
  * they hold; of a token that sees a value which is not finite, the whole head's
  * result may be NaN.  Keys past the block table (DFLASH2_DEV_BAD_LENGTH) or on a page
  * outside [0, n_pages) (DFLASH2_DEV_BAD_PAGE) are left out.
