@@ -69,6 +69,11 @@ constexpr int kSegs = 3;  // segments that warp 11 may be ahead (its query rows 
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kMaxCtas = kMaxSM;
 constexpr float kNone = -INFINITY;
+// Least log2 of a value's scale that the reference of 8-bit weights follows:
+// weights then stay below 2^(15 + 80), and their sums, of fewer than 2^31 keys,
+// in a float's range.  Smaller values go into smaller codes: below 2^-84 the
+// smallest of them are lost, below 2^-105 or so all.
+constexpr int kLeastScale = -80;
 
 // TMEM columns: scores (then weights) and accumulators of the two streams
 __device__ constexpr uint32_t s_col(int j) { return 128u * j; }
@@ -76,7 +81,7 @@ __device__ constexpr uint32_t o_col(int j) { return 256u + 128u * j; }
 
 struct TileInfo {
   float ks[kTile], vs[kTile];  // scales 2^(byte - 127) of keys and values
-  float lv[kTile];             // log2 of the values' scales (at least -60)
+  float lv[kTile];             // log2 of the values' scales (at least kLeastScale)
   uint32_t bad[4];             // keys whose values were not finite and are zeros now
   uint32_t groups;             // bit i: 16-key group i exists
   float vmax;                  // the largest of lv
@@ -1002,11 +1007,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
             const uint32_t kb = min(x & 0xffffu, 254u), vb = min(x >> 16, 254u);
             info->ks[32 * i + lane] = __uint_as_float(kb << 23);
             info->vs[32 * i + lane] = __uint_as_float(vb << 23);
-            info->lv[32 * i + lane] = (float)max((int)vb - 127, -60);
+            info->lv[32 * i + lane] = (float)max((int)vb - 127, kLeastScale);
             top = max(top, vb);
           }
           top = __reduce_max_sync(0xffffffffu, top);
-          if (lane == 0) info->vmax = (float)max((int)top - 127, -60);
+          if (lane == 0) info->vmax = (float)max((int)top - 127, kLeastScale);
         }
         if (lane < 4) info->bad[lane] = 0;
         if (lane == 0) {

@@ -669,7 +669,8 @@ int dflash2_cache_read(const dflash2_cache *cache, const int32_t *block_table, i
  * for little work.  Otherwise the tensor cores take a weight to 2^-16 of itself
  * with DFLASH2_BF16; with DFLASH2_E4M3 a weight times its value's scale to
  * 2^-11 of itself, or to 2^-27 of the row's largest, and a query head's values
- * exactly down to 2^-13 of its largest, below that to 2^-21 of the largest.
+ * exactly down to 2^-13 of its largest, below that to 2^-21 of the largest
+ * (value scales below 2^-84 lose bits, those below 2^-105 or so vanish).
  * Keys that a token does not see have no part in its result, whatever
  * they hold; of a token that sees a value which is not finite, the whole head's
  * result may be NaN.  Keys past the block table (DFLASH2_DEV_BAD_LENGTH) or on a page

@@ -95,6 +95,25 @@ def test_channels_far_above_the_others(B, force, high, nq, nkv, n_tok, lens):
         assert (np.abs(got[s, :n] - want[s, :n]) <= tol).all(), s
 
 
+@pytest.mark.parametrize("mode", [1, 2])
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("power", [-75, -60, 60, 100])
+@pytest.mark.parametrize("nq,n_tok,lens", [(4, 3, [3, 140, 700]), (4, 64, [200])])
+def test_values_of_any_size(B, force, cache, mode, power, nq, n_tok, lens):
+    """All values of a head by the same power of two larger or smaller: so is the result.  (2^-75 is a scale of 2^-83 of
+    8-bit rows.  The tensor cores then lose 2^-27 * 2^3 of the largest weight in each of up to 700 keys, less than 2^-12
+    of the sum of weight times |value|, beside the 2^-11 of each weight.)"""
+    force(mode)
+    c = Case(B, cache, 128, 16, nq, 1, n_tok, lens, seed=63, spread=1.0)
+    v = c.pool["v"].float()
+    c.pool["v"] = (torch.sign(v) * torch.clamp(v.abs(), 0.5, 1.0) * 2.0 ** power).to(torch.bfloat16)
+    c.quantise()
+    got = c.run()
+    want, mag = c.reference(128 ** -0.5, True, 0)
+    wide = 2.0 ** -9 + 2.0 ** -16 if cache == "e4m3" and mode == 2 else 2.0 ** -14
+    assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + wide * mag).all()
+
+
 @pytest.mark.parametrize("spread", [0, 12])
 def test_weights_that_cancel(B, force, spread):
     """A few keys with values of +1 and -1 (or by powers of two smaller): what their weights' codes leave out shows.  Ten
