@@ -592,7 +592,8 @@ int dflash2_linear_w4(const uint8_t *codes, const void *scale, int group, int ou
  * smallest byte with max|x| <= 448 * 2^(b - 127) over the finite x, and c the
  * nearest e4m3 value of x * 2^(127 - b), ties to even, NaN where x is not
  * finite.  What is stored is a bfloat16 value exactly (below 2^-126 up to its
- * subnormals' step), so rows read back as they are.
+ * subnormals' step; a magnitude that rounds up to 2^128 reads back as an
+ * infinity), so rows read back as they are.
  *   block_table   [batch, max_pages] int32 as above; max_pages * page_size
  *                 below 2^31 - 4096
  *   batch         at most 65535
@@ -661,8 +662,8 @@ int dflash2_cache_read(const dflash2_cache *cache, const int32_t *block_table, i
  *   shared_len  the first shared_len positions are the same in every
  *               sequence (a common prompt): they are read through row 0 of the
  *               block table, which has their pages whatever kv_len[0] is, and
- *               computed once for the whole batch.  0: none.  A sequence may
- *               have fewer keys than that.
+ *               on the tensor cores (below) once for the whole batch.  0:
+ *               none.  A sequence may have fewer keys than that.
  * out = softmax(scale * q k) v over the keys that a token sees, zeros where
  * there is none; sums are fp32 and the result is rounded once.  So are scores
  * and weights with head_dim 64, with pages other than 16, 32, 64, ... keys, and
@@ -673,8 +674,11 @@ int dflash2_cache_read(const dflash2_cache *cache, const int32_t *block_table, i
  * (value scales below 2^-84 lose bits, those below 2^-105 or so vanish).
  * Keys that a token does not see have no part in its result, whatever
  * they hold; of a token that sees a value which is not finite, the whole head's
- * result may be NaN.  Keys past the block table (DFLASH2_DEV_BAD_LENGTH) or on a page
- * outside [0, n_pages) (DFLASH2_DEV_BAD_PAGE) are left out.
+ * result may be NaN.  Weights times values are summed before the division, so
+ * with DFLASH2_BF16 |value| times keys has to stay below 2^111.  A kv_len below
+ * 0 counts as 0, one past the block table as all that the table holds
+ * (DFLASH2_DEV_BAD_LENGTH, both); keys on a page outside [0, n_pages)
+ * (DFLASH2_DEV_BAD_PAGE) are left out.
  * The workspace needs dflash2_attend_workspace bytes (0 for bad sizes; host
  * only), 16-byte aligned, its first 256 bytes zeroed once before the first
  * use; it serves one call at a time, of any sizes that fit.
