@@ -22,7 +22,7 @@
 // memory serves twice as many).
 //
 // Precision.  bfloat16: P goes in as bf16 high and low parts, two products
-// with V, so that its rounding (2^-17) does not add to the output's.  8-bit:
+// with V, so that its rounding (2^-16) does not add to the output's.  8-bit:
 // the codes are multiplied as they are, no byte of the cache is converted.
 // q is split into an e4m3 and an e5m2 code (its 8 bits are 4 + 4, and what
 // rounding to 4 leaves is one of 0 .. 8 units, which 3 bits hold: exact down
@@ -41,12 +41,12 @@
 // instruction cache, and unrolled it took most of the time to fetch.
 //
 // Measured.  32 x 8 tokens at contexts of 512 to 4096, 4 heads a kv head,
-// bfloat16: 68 us, 4.5 TB/s of the cache; 256 x 7 at 8192, 8-bit: 575 us, 3.8
+// bfloat16: 68 us, 4.5 TB/s of the cache; 256 x 7 at 8192, 8-bit: 592 us, 3.6
 // TB/s.  Few rows are bound by a tile's chain of scores, softmax and weighted
 // sums, of which a CTA has two under way (its values come late in the chain,
 // so their bytes wait in shared memory).  Behind a shared prefix: 64 x 16
-// tokens, 5 heads a kv head, 16384 keys, 8-bit: 0.5 ms; 32 x 8, 8192 keys,
-// bfloat16: 75 us; bound by the softmax's instructions, about 2000 cycles a
+// tokens, 5 heads a kv head, 16384 keys, 8-bit: 0.54 ms (0.52 with weights of
+// nine bits); 32 x 8, 8192 keys, bfloat16: 75 us; bound by the softmax's instructions, about 2000 cycles a
 // tile of 256 rows with bfloat16 and 4200 with 8-bit weights, beside products
 // of 1280 to 1540.  (Two softmax warps for every 32 rows, 16 in all, were
 // slower everywhere: 73, 593, 593 and 87 us.)
