@@ -37,6 +37,7 @@ constexpr int kMaxDrafts = 31;
 constexpr int kAhead = 8;              // tokens of the history that a thread has in flight
 constexpr uint32_t kSeen = 0x80000000u;
 constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr int kStaticBytes = 1024;     // more than the kernel's static shared memory (path, barrier, counters)
 
 // -inf where `keep` has no bit: 4 floats or 8 bfloat16.
 __device__ __forceinline__ void blank(uint4& x, uint32_t keep, float) {
@@ -274,10 +275,11 @@ int launch_adjust(const AdjustArgs& a, const Ctx& c) {
   const size_t smem = (size_t)slice * (group * size + 6) + slice / 8 + (a.mask ? (size_t)group * slice / 8 : 0) +
                       (a.n_bias > 0 ? (size_t)slice * 2 : 0);
   const dim3 grid((a.vocab + slice - 1) / slice, a.batch);
-  // (an attribute of the kernel on the current device, so on every call; and
-  // whatever smem is: the limit without it counts the kernel's static bytes too)
+  // (an attribute of the kernel on the current device, so on every call that
+  // needs it; without it 48 KB hold the kernel's static bytes as well)
   const void* kernel = a.bf16_logits ? (const void*)adjust_kernel<bf16> : (const void*)adjust_kernel<float>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024) != cudaSuccess)
+  if (smem + kStaticBytes > 48 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024) != cudaSuccess)
     return DFLASH2_ERR_CUDA;
   return a.bf16_logits ? launch_k(adjust_kernel<bf16>, grid, dim3(kThreads), smem, c, a, slice)
                        : launch_k(adjust_kernel<float>, grid, dim3(kThreads), smem, c, a, slice);
