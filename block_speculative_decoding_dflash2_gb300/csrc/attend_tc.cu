@@ -26,10 +26,10 @@
 // the codes are multiplied as they are, no byte of the cache is converted.
 // q is split into an e4m3 and an e5m2 code (its 8 bits are 4 + 4, and what
 // rounding to 4 leaves is one of 0 .. 8 units, which 3 bits hold: exact down
-// to 2^-13 of the row's largest, within 2^-21 of the largest below) and P, times the key's value scale, an f16,
-// into three e5m2 codes, which hold its 11 bits (2^-11 of each weight, or
-// 2^-27 of the row's largest).
-// The scales of keys multiply the scores; those of values the weights.
+// to 2^-13 of the row's largest, within 2^-21 of the largest below) and P,
+// times the key's value scale, an f16, into three e5m2 codes, which hold its
+// 11 bits (2^-11 of each weight, or 2^-27 of the row's largest).  The scales of
+// keys multiply the scores; those of values the weights.
 //
 // Warps: 0-3 and 4-7 softmax of stream 0 and 1 (thread = query row); 8 loads
 // keys and values by TMA; 9 TMEM and MMA issue; 10 what a tile needs beside
@@ -46,10 +46,11 @@
 // sums, of which a CTA has two under way (its values come late in the chain,
 // so their bytes wait in shared memory).  Behind a shared prefix: 64 x 16
 // tokens, 5 heads a kv head, 16384 keys, 8-bit: 0.54 ms (0.52 with weights of
-// nine bits); 32 x 8, 8192 keys, bfloat16: 75 us; bound by the softmax's instructions, about 2000 cycles a
-// tile of 256 rows with bfloat16 and 4200 with 8-bit weights, beside products
-// of 1280 to 1540.  (Two softmax warps for every 32 rows, 16 in all, were
-// slower everywhere: 73, 593, 593 and 87 us.)
+// nine bits); 32 x 8, 8192 keys, bfloat16: 75 us; bound by the softmax's
+// instructions, about 2000 cycles a tile of 256 rows with bfloat16 and 4500
+// with 8-bit weights, beside products of 1280 to 1540.  (Two softmax warps for
+// every 32 rows, 16 in all, were slower everywhere: 73, 593, 593 and 87 us,
+// with weights of nine bits, where eight took 66, 565, 498 and 79.)
 #include <algorithm>
 #include <cstring>
 
@@ -434,8 +435,8 @@ __device__ __noinline__ void rescale(uint32_t o, int pieces, uint32_t w, int chu
 // into the place at `dst`: K-major with the 128-byte swizzle.  bfloat16: two
 // halves of 64 dims, 16 KB apart.  8-bit: the high codes (e4m3) and, 16 KB
 // behind, the low ones (e5m2, whose smallest step is 2^7 times finer: small
-// channels beside large ones keep their bits); a row's largest magnitude becomes 2^7 .. 2^8, and
-// qscale[row] the factor that its scores take.
+// channels beside large ones keep their bits); a row's largest magnitude
+// becomes 2^7 .. 2^8, and qscale[row] the factor that its scores take.
 template <bool E4M3>
 __device__ __forceinline__ void load_rows(const Plan& p, const SegInfo& g, int r0, int r1, uint8_t* dst, float* qscale) {
   const AttendArgs& a = p.a;

@@ -671,14 +671,15 @@ int dflash2_cache_read(const dflash2_cache *cache, const int32_t *block_table, i
  * with DFLASH2_BF16; with DFLASH2_E4M3 a weight times its value's scale to
  * 2^-11 of itself, or to 2^-27 of the row's largest, and a query head's values
  * exactly down to 2^-13 of its largest, below that to 2^-21 of the largest
- * (value scales below 2^-84 lose bits, those below 2^-105 or so vanish).
- * Keys that a token does not see have no part in its result, whatever
- * they hold; of a token that sees a value which is not finite, the whole head's
- * result may be NaN.  Weights times values are summed before the division, so
- * with DFLASH2_BF16 |value| times keys has to stay below 2^111.  A kv_len below
- * 0 counts as 0, one past the block table as all that the table holds
- * (DFLASH2_DEV_BAD_LENGTH, both); keys on a page outside [0, n_pages)
- * (DFLASH2_DEV_BAD_PAGE) are left out.
+ * (value scales below 2^-84 lose bits, those below 2^-105 or so vanish; beside
+ * scales above 2^100 weights below 2^-17 of the largest may be lost).  Keys
+ * that a token does not see have no part in its result, whatever they hold; of
+ * a token that sees a value which is not finite, the whole head's result may
+ * be NaN.  Weights times values are summed before the division, so |value|
+ * times keys has to stay below 2^111 with DFLASH2_BF16, 2^127 with
+ * DFLASH2_E4M3.  A kv_len below 0 counts as 0, one past the block table as all
+ * that the table holds (DFLASH2_DEV_BAD_LENGTH, both); keys on a page outside
+ * [0, n_pages) (DFLASH2_DEV_BAD_PAGE) are left out.
  * The workspace needs dflash2_attend_workspace bytes (0 for bad sizes; host
  * only), 16-byte aligned, its first 256 bytes zeroed once before the first
  * use; it serves one call at a time, of any sizes that fit.
